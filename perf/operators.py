@@ -222,6 +222,8 @@ def prepare(case, seed):
         st["pos"] = torch.where(padded, -1, pos).to(torch.int32)
         st["inv_freq"] = _inv_freq(case)
         st["wq"], st["wk"] = _weights(g, case)
+        if own:
+            st["ws"] = torch.zeros(256, dtype=torch.uint8, device="cuda")
         return st
     st["scale"] = D ** -0.5
     st["q"] = _randn(g, (S, B, H, D), bf)
@@ -250,6 +252,16 @@ def prepare(case, seed):
     st["q_pos"] = q_pos.to(torch.int32)
     if op == "attn_train":
         st["go"] = _randn(g, (S, B, H, D), bf)
+    if own:
+        # the workspaces that a program keeps from step to step
+        import dsa_sparse_attention_fwd_gb300 as dsa
+        shape = (S, B, H, Hk, D, nblk * case["block"], case["block"],
+                 case["topk"], case["local"])
+        sizes = {"ws": dsa.dsa_block_attn_workspace_size(*shape)}
+        if op == "attn_train":
+            sizes["ws_bwd"] = dsa.dsa_block_attn_bwd_workspace_size(*shape)
+        for name, size in sizes.items():
+            st[name] = torch.zeros(size, dtype=torch.uint8, device="cuda")
     return st
 
 
@@ -461,21 +473,23 @@ def _own(st):
         q, _ = dsa.dsa_paged_append(
             st["k"], st["v"], st["k_cache"], st["v_cache"], st["table"],
             st["pos"], inv_freq=st["inv_freq"], wk=st["wk"], q=st["q"],
-            wq=st["wq"], **rope)
+            wq=st["wq"], workspace=st["ws"], **rope)
         return {"q": q, "k_cache": st["k_cache"], "v_cache": st["v_cache"]}
     args = dict(block_size=case["block"], scale=st["scale"],
                 q_pos=st["q_pos"], local_blocks=case["local"])
     if op == "attn_paged":
         o, lse, _ = dsa.dsa_block_attn_paged_fwd(
             st["q"], st["k_cache"], st["v_cache"], st["table"], st["blocks"],
-            **args)
+            workspace=st["ws"], **args)
         return {"o": o, "lse": lse}
     o, lse, _ = dsa.dsa_block_attn_fwd(st["q"], st["k"], st["v"],
-                                       st["blocks"], **args)
+                                       st["blocks"], workspace=st["ws"],
+                                       **args)
     out = {"o": o, "lse": lse}
     if op == "attn_train":
         gq, gk, gv, _ = dsa.dsa_block_attn_bwd(
-            st["q"], st["k"], st["v"], o, lse, st["go"], st["blocks"], **args)
+            st["q"], st["k"], st["v"], o, lse, st["go"], st["blocks"],
+            workspace=st["ws_bwd"], **args)
         out.update(gq=gq, gk=gk, gv=gv)
     return out
 
