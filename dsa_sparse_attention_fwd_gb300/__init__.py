@@ -16,6 +16,7 @@ returns (scores [B, S, topk] fp32, indices [B, S, topk] int32).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -35,6 +36,10 @@ __all__ = [
     "dsa_kpool_compress", "dsa_expand_selection",
     "dsa_indexer_pooled_workspace_size", "dsa_indexer_fwd_pooled",
     "dsa_sparse_mla_fwd", "dsa_sparse_mla_workspace_size", "STATUS",
+    "rope_inv_freq", "dsa_norm_rope_fwd", "dsa_norm_rope_bwd",
+    "dsa_norm_rope_bwd_workspace_size", "dsa_paged_append",
+    "dsa_block_attn_fwd", "dsa_block_attn_paged_fwd", "dsa_block_attn_bwd",
+    "dsa_block_attn_workspace_size", "dsa_block_attn_bwd_workspace_size",
 ]
 
 STATUS = {
@@ -127,6 +132,35 @@ def load_library(path: str | None = None):
         lib.dsa_sparse_mla_fwd.restype = I
         lib.dsa_sparse_mla_fwd.argtypes = [P, P, P, I, I, I, I, I, I,
                                            ctypes.c_float, P, P, P, Z, P]
+        F = ctypes.c_float
+        lib.dsa_norm_rope_fwd.restype = I
+        lib.dsa_norm_rope_fwd.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P,
+                                          F, P, P, I, I, I, F, P, P, P]
+        lib.dsa_norm_rope_bwd_workspace_size.restype = Z
+        lib.dsa_norm_rope_bwd_workspace_size.argtypes = [I]
+        lib.dsa_norm_rope_bwd.restype = I
+        lib.dsa_norm_rope_bwd.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I,
+                                          P, P, F, P, P, I, I, I, F, P, P, P,
+                                          P, P, Z, P]
+        lib.dsa_paged_append.restype = I
+        lib.dsa_paged_append.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P,
+                                         P, P, I, I, P, I, P, P, P, F, P, I,
+                                         I, I, F, P, P, Z, P]
+        for name in ("dsa_block_attn_workspace_size",
+                     "dsa_block_attn_bwd_workspace_size"):
+            getattr(lib, name).restype = Z
+            getattr(lib, name).argtypes = [I] * 9
+        lib.dsa_block_attn_fwd.restype = I
+        lib.dsa_block_attn_fwd.argtypes = [P, P, P, P, I, I, I, I, I, I, P, I,
+                                           I, I, I, P, F, P, P, P, Z, P]
+        lib.dsa_block_attn_paged_fwd.restype = I
+        lib.dsa_block_attn_paged_fwd.argtypes = [
+            P, P, P, P, I, I, P, I, I, I, I, I, I, P, I, I, I, I, P, F, P, P,
+            P, Z, P]
+        lib.dsa_block_attn_bwd.restype = I
+        lib.dsa_block_attn_bwd.argtypes = [
+            P, P, P, P, P, P, P, I, I, I, I, I, I, P, I, I, I, I, P, F, P, P,
+            P, P, Z, P]
         _lib = lib
         return lib
 
@@ -444,6 +478,415 @@ def dsa_sparse_mla_fwd(q, c, idx, scale, out_o=None, out_lse=None,
     if rc != 0:
         raise DsaError(rc, "dsa_sparse_mla_fwd")
     return out_o, out_lse, workspace
+
+
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def rope_inv_freq(rot_dim, base=10000.0, scaling=None, device=None):
+    """Rotation frequencies [rot_dim / 2] fp64 (radians a position) of
+    base^(-2i / rot_dim), and the factor on cos and sin (rot_scale).
+
+    scaling: None, or a dict with "type" and "factor" (> 1) that stretches
+    the positions for contexts longer than those trained on:
+      "linear"  every frequency divided by factor (position interpolation);
+      "ntk"     the base raised so that the lowest frequency is divided by
+                factor and the highest stays;
+      "yarn"    frequencies that turn more than "beta_fast" (32) times within
+                "original_max_position" stay, those that turn less than
+                "beta_slow" (1) times are divided by factor, a linear ramp
+                over the index between; cos and sin are multiplied by
+                0.1 ln(factor) + 1 (or "attention_factor").
+    Returns (inv_freq, rot_scale)."""
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be positive and even")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    rot_scale = 1.0
+    if scaling is None:
+        inv = base ** (-2.0 * i / rot_dim)
+    else:
+        kind, factor = scaling["type"], float(scaling["factor"])
+        if not factor >= 1.0:
+            raise ValueError("the scaling factor must be at least 1")
+        if kind == "linear":
+            inv = base ** (-2.0 * i / rot_dim) / factor
+        elif kind == "ntk":
+            if rot_dim > 2:
+                base = base * factor ** (rot_dim / (rot_dim - 2))
+            inv = base ** (-2.0 * i / rot_dim)
+        elif kind == "yarn":
+            inv = base ** (-2.0 * i / rot_dim)
+            length = float(scaling["original_max_position"])
+            fast = float(scaling.get("beta_fast", 32))
+            slow = float(scaling.get("beta_slow", 1))
+
+            def index_of(turns):  # the index that turns this often
+                return (rot_dim * math.log(length / (turns * 2 * math.pi))
+                        / (2 * math.log(base)))
+            lo = max(math.floor(index_of(fast)), 0)
+            hi = min(math.ceil(index_of(slow)), rot_dim - 1)
+            ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            inv = inv * (1 - ramp) + inv / factor * ramp
+            rot_scale = float(scaling.get("attention_factor",
+                                          0.1 * math.log(factor) + 1.0))
+        else:
+            raise ValueError(f"unknown scaling type {kind!r}")
+    return inv.to(device) if device is not None else inv, rot_scale
+
+
+def _strides(*tensors, lead=3):
+    """Host array of the leading element strides of each tensor; the last
+    dimension must be contiguous (dimensions of one element have any)."""
+    out = []
+    for t in tensors:
+        for n, st in zip(t.shape[:lead], t.stride()[:lead]):
+            out.append(st if n > 1 else 0)
+    return (ctypes.c_int64 * len(out))(*out)
+
+
+def _last_contiguous(name, t, dt, shape):
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    if any(st < 0 for st in t.stride()):
+        raise ValueError(f"{name} has negative strides")
+
+
+def _dense(name, t, dt, shape):
+    if t.dtype != dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rope_inputs(q, k, inv_freq, positions, wq, wk, dt):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q [S, B, H, D] and k [S, B, Hk, D] expected")
+    S, B, H, D = q.shape
+    Hk = 0 if k is None else k.shape[2]
+    _last_contiguous("q", q, dt, (S, B, H, D))
+    if k is not None:
+        _last_contiguous("k", k, dt, (S, B, Hk, D))
+    if inv_freq is not None and (inv_freq.dtype != torch.float64
+                                 or inv_freq.dim() != 1
+                                 or not inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be contiguous fp64 [rot_dim / 2]")
+    if positions is not None:
+        _dense("positions", positions, torch.int32, (S, B))
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _dense(name, w, torch.float32, (D,))
+    return S, B, H, Hk, D, 0 if inv_freq is None else 2 * inv_freq.numel()
+
+
+def dsa_norm_rope_fwd(q, k, inv_freq, positions=None, wq=None, wk=None,
+                      eps=1e-6, rot_start=0, interleaved=False,
+                      rot_scale=1.0, out_q=None, out_k=None, stream=None):
+    """Per-head RMS norm (where a weight is given) and rotation of q
+    [S, B, H, D] and k [S, B, Hk, D] (or None) on device tensors, bf16, fp16
+    or fp32 with any strides over a contiguous last dimension.  inv_freq
+    [rot_dim / 2] fp64 (rope_inv_freq; None: no rotation), positions [S, B]
+    int32 (None: row s at s).  Returns (out_q, out_k), dense."""
+    lib = load_library()
+    _require_cuda("dsa_norm_rope_fwd", q=q, k=k, inv_freq=inv_freq,
+                  positions=positions, wq=wq, wk=wk, out_q=out_q, out_k=out_k)
+    dt = q.dtype
+    if dt not in _ROPE_DTYPES:
+        raise TypeError(f"q must be bf16, fp16 or fp32, got {dt}")
+    S, B, H, Hk, D, R = _rope_inputs(q, k, inv_freq, positions, wq, wk, dt)
+    if out_q is None:
+        out_q = torch.empty((S, B, H, D), dtype=dt, device=q.device)
+    _dense("out_q", out_q, dt, (S, B, H, D))
+    if k is not None:
+        if out_k is None:
+            out_k = torch.empty((S, B, Hk, D), dtype=dt, device=q.device)
+        _dense("out_k", out_k, dt, (S, B, Hk, D))
+    rc = lib.dsa_norm_rope_fwd(
+        _ptr(q), _strides(q), _ptr(k), None if k is None else _strides(k),
+        _ROPE_DTYPES[dt], S, B, H, Hk, D, _ptr(wq), _ptr(wk), float(eps),
+        _ptr(positions), _ptr(inv_freq), int(rot_start), R,
+        int(bool(interleaved)), float(rot_scale), _ptr(out_q), _ptr(out_k),
+        _stream(stream))
+    if rc != 0:
+        raise DsaError(rc, "dsa_norm_rope_fwd")
+    return out_q, out_k
+
+
+def dsa_norm_rope_bwd_workspace_size(D) -> int:
+    return int(load_library().dsa_norm_rope_bwd_workspace_size(int(D)))
+
+
+def dsa_norm_rope_bwd(q, k, grad_out_q, grad_out_k, inv_freq, positions=None,
+                      wq=None, wk=None, eps=1e-6, rot_start=0,
+                      interleaved=False, rot_scale=1.0, workspace=None,
+                      stream=None):
+    """Backward of dsa_norm_rope_fwd from its inputs and the gradients of its
+    outputs (dense).  Returns (grad_q, grad_k, grad_wq, grad_wk, workspace);
+    the weights' gradients are fp32 [D], None without the weight."""
+    lib = load_library()
+    _require_cuda("dsa_norm_rope_bwd", q=q, k=k, grad_out_q=grad_out_q,
+                  grad_out_k=grad_out_k, inv_freq=inv_freq,
+                  positions=positions, wq=wq, wk=wk, workspace=workspace)
+    dt, dev = q.dtype, q.device
+    if dt not in _ROPE_DTYPES:
+        raise TypeError(f"q must be bf16, fp16 or fp32, got {dt}")
+    S, B, H, Hk, D, R = _rope_inputs(q, k, inv_freq, positions, wq, wk, dt)
+    _dense("grad_out_q", grad_out_q, dt, (S, B, H, D))
+    gk = gwq = gwk = None
+    gq = torch.empty((S, B, H, D), dtype=dt, device=dev)
+    if k is not None:
+        if grad_out_k is None:
+            raise ValueError("grad_out_k is needed with k")
+        _dense("grad_out_k", grad_out_k, dt, (S, B, Hk, D))
+        gk = torch.empty((S, B, Hk, D), dtype=dt, device=dev)
+    if wq is not None:
+        gwq = torch.empty(D, dtype=torch.float32, device=dev)
+    if wk is not None and k is not None:
+        gwk = torch.empty(D, dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(max(dsa_norm_rope_bwd_workspace_size(D), 256),
+                                dtype=torch.uint8, device=dev)
+    rc = lib.dsa_norm_rope_bwd(
+        _ptr(q), _strides(q), _ptr(k), None if k is None else _strides(k),
+        _ptr(grad_out_q), None if k is None else _ptr(grad_out_k),
+        _ROPE_DTYPES[dt], S, B, H, Hk, D, _ptr(wq), _ptr(wk), float(eps),
+        _ptr(positions), _ptr(inv_freq), int(rot_start), R,
+        int(bool(interleaved)), float(rot_scale), _ptr(gq), _ptr(gk),
+        _ptr(gwq), _ptr(gwk), _ptr(workspace), workspace.numel(),
+        _stream(stream))
+    if rc != 0:
+        raise DsaError(rc, "dsa_norm_rope_bwd")
+    return gq, gk, gwq, gwk, workspace
+
+
+def _paged_cache(k_cache, v_cache, page_table, B):
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, Hk, D]")
+    shape = tuple(k_cache.shape)
+    _last_contiguous("k_cache", k_cache, torch.bfloat16, shape)
+    _last_contiguous("v_cache", v_cache, torch.bfloat16, shape)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _dense("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+    return shape
+
+
+def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
+                     inv_freq=None, wk=None, eps=1e-6, rot_start=0,
+                     interleaved=False, rot_scale=1.0, q=None, wq=None,
+                     out_q=None, workspace=None, stream=None):
+    """Append k and v [S, B, Hk, D] bf16 (any strides over a contiguous last
+    dimension) at positions [S, B] int32 (< 0: skipped) to the paged caches
+    [pages, page_size, Hk, D] through page_table [B, max_pages] int32, the
+    keys normed and rotated as by dsa_norm_rope_fwd; q [S, B, H, D] given
+    with them is normed and rotated into out_q in the same launch.  Returns
+    (out_q, workspace).  The call only sets bits in the workspace's status
+    word (256 zeroed bytes to begin with; dsa_indexer_check reads it)."""
+    lib = load_library()
+    _require_cuda("dsa_paged_append", k=k, v=v, k_cache=k_cache,
+                  v_cache=v_cache, page_table=page_table,
+                  positions=positions, inv_freq=inv_freq, wk=wk, q=q, wq=wq,
+                  out_q=out_q, workspace=workspace)
+    bf = torch.bfloat16
+    S, B, Hk, _, D, R = _rope_inputs(k, None, inv_freq, positions, wk, None,
+                                     bf)
+    _last_contiguous("v", v, bf, (S, B, Hk, D))
+    pages, page_size, *_ = _paged_cache(k_cache, v_cache, page_table, B)
+    if tuple(k_cache.shape[2:]) != (Hk, D):
+        raise ValueError("the cache's heads or head size differ from k's")
+    H = 0
+    if q is not None:
+        H = q.shape[2]
+        _rope_inputs(q, None, None, positions, wq, None, bf)
+        if tuple(q.shape) != (S, B, H, D):
+            raise ValueError("q must be [S, B, H, D] with k's S, B and D")
+        if out_q is None:
+            out_q = torch.empty((S, B, H, D), dtype=bf, device=q.device)
+        _dense("out_q", out_q, bf, (S, B, H, D))
+    if workspace is None:
+        workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
+    rc = lib.dsa_paged_append(
+        _ptr(k), _strides(k), _ptr(v), _strides(v), _ptr(q),
+        None if q is None else _strides(q), S, B, H, Hk, D, _ptr(k_cache),
+        _ptr(v_cache), _strides(k_cache, v_cache), pages, page_size,
+        _ptr(page_table), page_table.shape[1], _ptr(positions), _ptr(wq),
+        _ptr(wk), float(eps), _ptr(inv_freq), int(rot_start), R,
+        int(bool(interleaved)), float(rot_scale),
+        None if q is None else _ptr(out_q), _ptr(workspace),
+        workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise DsaError(rc, "dsa_paged_append")
+    return out_q, workspace
+
+
+def dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
+                                  local_blocks=0) -> int:
+    """Workspace bytes of dsa_block_attn_fwd and, with T = max_pages *
+    page_size, of dsa_block_attn_paged_fwd (0: invalid sizes)."""
+    return int(load_library().dsa_block_attn_workspace_size(
+        S, B, H, Hk, D, T, block_size, topk, local_blocks))
+
+
+def dsa_block_attn_bwd_workspace_size(S, B, H, Hk, D, T, block_size, topk,
+                                      local_blocks=0) -> int:
+    return int(load_library().dsa_block_attn_bwd_workspace_size(
+        S, B, H, Hk, D, T, block_size, topk, local_blocks))
+
+
+def _selection(blocks, B, S, Hk, q_pos):
+    """(sel_heads, topk) of blocks [B, S, topk] or [B, S, Hk, topk]."""
+    if q_pos is not None:
+        _dense("q_pos", q_pos, torch.int32, (B,))
+    if blocks is None:
+        return 1, 0
+    if blocks.dim() == 3:
+        shape = (B, S, blocks.shape[-1])
+    else:
+        shape = (B, S, Hk, blocks.shape[-1])
+    _dense("blocks", blocks, torch.int32, shape)
+    return (1 if blocks.dim() == 3 else Hk), blocks.shape[-1]
+
+
+def _block_attn_out(q, size, out_o, out_lse, workspace):
+    S, B, H, D = q.shape
+    if out_o is None:
+        out_o = torch.empty_like(q)
+    _dense("out_o", out_o, torch.bfloat16, (S, B, H, D))
+    if out_lse is None:
+        out_lse = torch.empty((S, B, H), dtype=torch.float32, device=q.device)
+    _dense("out_lse", out_lse, torch.float32, (S, B, H))
+    if workspace is None:
+        if size == 0:
+            raise DsaError(1, "dsa_block_attn_workspace_size")
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        workspace[:256].zero_()
+    return out_o, out_lse, workspace
+
+
+def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
+                       local_blocks=0, out_o=None, out_lse=None,
+                       workspace=None, stream=None):
+    """Attention over selected blocks on device tensors: q [S, B, H, D] bf16,
+    k and v [T, B, Hk, D] bf16 (any strides over a contiguous last
+    dimension), blocks [B, S, topk] or [B, S, Hk, topk] int32 block ids (-1:
+    empty; None: local blocks only), q_pos [B] int32 (row s at q_pos[b] + s;
+    None: at s), local_blocks trailing blocks always attended to.  Returns
+    (o [S, B, H, D] bf16, lse [S, B, H] fp32, workspace); a workspace of the
+    caller's has its first 256 bytes zeroed once, before its first use."""
+    lib = load_library()
+    _require_cuda("dsa_block_attn_fwd", q=q, k=k, v=v, blocks=blocks,
+                  q_pos=q_pos, out_o=out_o, out_lse=out_lse,
+                  workspace=workspace)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [S, B, H, D] and k [T, B, Hk, D] expected")
+    S, B, H, D = q.shape
+    T, _, Hk, _ = k.shape
+    _dense("q", q, torch.bfloat16, (S, B, H, D))
+    _last_contiguous("k", k, torch.bfloat16, (T, B, Hk, D))
+    _last_contiguous("v", v, torch.bfloat16, (T, B, Hk, D))
+    sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
+    out_o, out_lse, workspace = _block_attn_out(
+        q, dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
+                                         local_blocks),
+        out_o, out_lse, workspace)
+    rc = lib.dsa_block_attn_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _strides(k, v), S, B, H, Hk, D, T,
+        _ptr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
+        _ptr(q_pos), float(scale), _ptr(out_o), _ptr(out_lse),
+        _ptr(workspace), workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise DsaError(rc, "dsa_block_attn_fwd")
+    return out_o, out_lse, workspace
+
+
+def dsa_block_attn_paged_fwd(q, k_cache, v_cache, page_table, blocks,
+                             block_size, scale, q_pos=None, local_blocks=0,
+                             out_o=None, out_lse=None, workspace=None,
+                             stream=None):
+    """dsa_block_attn_fwd over paged caches [pages, page_size, Hk, D] bf16
+    through page_table [B, max_pages] int32 (S = 1: one token of each
+    sequence at q_pos[b])."""
+    lib = load_library()
+    _require_cuda("dsa_block_attn_paged_fwd", q=q, k_cache=k_cache,
+                  v_cache=v_cache, page_table=page_table, blocks=blocks,
+                  q_pos=q_pos, out_o=out_o, out_lse=out_lse,
+                  workspace=workspace)
+    if q.dim() != 4:
+        raise ValueError("q [S, B, H, D] expected")
+    S, B, H, D = q.shape
+    _dense("q", q, torch.bfloat16, (S, B, H, D))
+    pages, page_size, Hk, Dk = _paged_cache(k_cache, v_cache, page_table, B)
+    if Dk != D:
+        raise ValueError(f"the cache's head size {Dk} differs from q's {D}")
+    max_pages = page_table.shape[1]
+    sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
+    out_o, out_lse, workspace = _block_attn_out(
+        q, dsa_block_attn_workspace_size(S, B, H, Hk, D,
+                                         max_pages * page_size, block_size,
+                                         topk, local_blocks),
+        out_o, out_lse, workspace)
+    rc = lib.dsa_block_attn_paged_fwd(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _strides(k_cache, v_cache),
+        pages, page_size, _ptr(page_table), max_pages, S, B, H, Hk, D,
+        _ptr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
+        _ptr(q_pos), float(scale), _ptr(out_o), _ptr(out_lse),
+        _ptr(workspace), workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise DsaError(rc, "dsa_block_attn_paged_fwd")
+    return out_o, out_lse, workspace
+
+
+def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
+                       q_pos=None, local_blocks=0, grad_q=None, grad_k=None,
+                       grad_v=None, workspace=None, stream=None):
+    """Backward of dsa_block_attn_fwd from its inputs, its outputs o and lse,
+    and grad_o [S, B, H, D] bf16.  Returns (grad_q [S, B, H, D], grad_k and
+    grad_v [T, B, Hk, D], dense bf16, workspace)."""
+    lib = load_library()
+    _require_cuda("dsa_block_attn_bwd", q=q, k=k, v=v, o=o, lse=lse,
+                  grad_o=grad_o, blocks=blocks, q_pos=q_pos, grad_q=grad_q,
+                  grad_k=grad_k, grad_v=grad_v, workspace=workspace)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q [S, B, H, D] and k [T, B, Hk, D] expected")
+    S, B, H, D = q.shape
+    T, _, Hk, _ = k.shape
+    bf = torch.bfloat16
+    for name, t in (("q", q), ("o", o), ("grad_o", grad_o)):
+        _dense(name, t, bf, (S, B, H, D))
+    _dense("lse", lse, torch.float32, (S, B, H))
+    _last_contiguous("k", k, bf, (T, B, Hk, D))
+    _last_contiguous("v", v, bf, (T, B, Hk, D))
+    sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
+    if grad_q is None:
+        grad_q = torch.empty_like(q)
+    if grad_k is None:
+        grad_k = torch.empty((T, B, Hk, D), dtype=bf, device=q.device)
+    if grad_v is None:
+        grad_v = torch.empty((T, B, Hk, D), dtype=bf, device=q.device)
+    _dense("grad_q", grad_q, bf, (S, B, H, D))
+    _dense("grad_k", grad_k, bf, (T, B, Hk, D))
+    _dense("grad_v", grad_v, bf, (T, B, Hk, D))
+    if workspace is None:
+        n = dsa_block_attn_bwd_workspace_size(S, B, H, Hk, D, T, block_size,
+                                              topk, local_blocks)
+        if n == 0:
+            raise DsaError(1, "dsa_block_attn_bwd_workspace_size")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace[:256].zero_()
+    rc = lib.dsa_block_attn_bwd(
+        _ptr(q), _ptr(k), _ptr(v), _strides(k, v), _ptr(o), _ptr(lse),
+        _ptr(grad_o), S, B, H, Hk, D, T, _ptr(blocks), sel_heads, topk,
+        int(block_size), int(local_blocks), _ptr(q_pos), float(scale),
+        _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(workspace),
+        workspace.numel(), _stream(stream))
+    if rc != 0:
+        raise DsaError(rc, "dsa_block_attn_bwd")
+    return grad_q, grad_k, grad_v, workspace
 
 
 def dsa_indexer_logits(q, k, w, compress_ratio, q_pos=None, logits=None,

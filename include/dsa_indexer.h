@@ -506,6 +506,177 @@ DSA_API int dsa_sparse_mla_fwd(const void *q, const void *c,
                                float *out_o, float *out_lse, void *workspace,
                                size_t workspace_bytes, void *cuda_stream);
 
+/*
+ * Attention over selected blocks with per-head keys and values, and what
+ * prepares its inputs.
+ *
+ * Element strides are HOST arrays of int64 read during the call (NULL: the
+ * dense layout); the last dimension is contiguous.
+ *
+ * Status word: dsa_paged_append(), dsa_block_attn_fwd(),
+ * dsa_block_attn_paged_fwd() and dsa_block_attn_bwd() only set bits in the
+ * status word at the start of their workspace (one launch less than clearing
+ * it).  Zero a new workspace's first 256 bytes once; dsa_indexer_check()
+ * reads and clears the word.
+ */
+
+/* Element types of dsa_norm_rope_fwd() and _bwd(). */
+#define DSA_BF16 0
+#define DSA_FP16 1
+#define DSA_FP32 2
+
+/*
+ * RMS norm of each head of the queries and keys, then the rotation of
+ * positions, one launch.  A row x is one head of one token (D values):
+ *     n = x * rsqrt(mean(x^2) + eps) * w     (n = x where the weight is NULL)
+ * and within [rot_start, rot_start + rot_dim), t = position * inv_freq[i],
+ *     (a, b) -> rot_scale * (a cos t - b sin t, a sin t + b cos t)
+ * for the pairs (2i, 2i + 1) (interleaved != 0) or (i, i + rot_dim / 2),
+ * counted from rot_start.  The rest of the row is n.  Statistics, weights
+ * and rotation in fp32 from an angle that is exact in the position; one
+ * rounding at the end.
+ *   q [S, B, H, D], k [S, B, Hk, D] (nullable) of `dtype`; q_strides,
+ *   k_strides: element strides (s, b, head) or NULL.
+ *   wq, wk [D] fp32 or NULL; positions [S, B] int32 or NULL (row s at s);
+ *   inv_freq [rot_dim / 2] fp64, radians a position.
+ *   out_q [S, B, H, D], out_k [S, B, Hk, D] of `dtype`, dense.
+ * Envelope: D <= 256, rot_dim even, rot_start + rot_dim <= D, else
+ * DSA_ERR_UNSUPPORTED (D) or DSA_ERR_INVALID_ARG.  Pointers need their
+ * element's alignment only; 16-byte aligned rows are faster.
+ */
+DSA_API int dsa_norm_rope_fwd(const void *q, const int64_t *q_strides,
+                              const void *k, const int64_t *k_strides,
+                              int dtype, int S, int B, int H, int Hk, int D,
+                              const float *wq, const float *wk, float eps,
+                              const int32_t *positions,
+                              const double *inv_freq, int rot_start,
+                              int rot_dim, int interleaved, float rot_scale,
+                              void *out_q, void *out_k, void *cuda_stream);
+
+/*
+ * Its backward: from the outputs' gradients (dense, of `dtype`) the inputs'
+ * (dense, of `dtype`) and the weights' (fp32 [D], summed over all rows in a
+ * fixed order; not written where the weight is NULL).
+ *   workspace: dsa_norm_rope_bwd_workspace_size(D) bytes, 256-byte aligned
+ *   (no status word: nothing here can fail on the device).
+ */
+DSA_API size_t dsa_norm_rope_bwd_workspace_size(int D);
+DSA_API int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides,
+                              const void *k, const int64_t *k_strides,
+                              const void *grad_out_q, const void *grad_out_k,
+                              int dtype, int S, int B, int H, int Hk, int D,
+                              const float *wq, const float *wk, float eps,
+                              const int32_t *positions,
+                              const double *inv_freq, int rot_start,
+                              int rot_dim, int interleaved, float rot_scale,
+                              void *grad_q, void *grad_k, float *grad_wq,
+                              float *grad_wk, void *workspace,
+                              size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Appends keys and values to a paged cache, the keys normed and rotated on
+ * the way (arithmetic of dsa_norm_rope_fwd()), the values copied; queries
+ * given with them are normed and rotated into out_q in the same launch.
+ * Token (s, b) at position p = positions[s, b] goes to slot p % page_size of
+ * page page_table[b, p / page_size]; p < 0 appends nothing (padding; its
+ * query row is still written).  A position past the table, or a page id
+ * outside [0, num_pages), appends nothing and sets DSA_ERR_INDEX_RANGE.
+ * Two tokens with one slot leave either of them there.
+ *   k, v [S, B, Hk, D], q [S, B, H, D] (nullable) bf16 with element strides
+ *   (s, b, head) or NULL; k_cache, v_cache bf16, cache_strides: element
+ *   strides (page, slot, head) of k_cache, then of v_cache, or NULL for
+ *   [num_pages, page_size, Hk, D]; page_table [B, max_pages] int32;
+ *   positions [S, B] int32; out_q [S, B, H, D] bf16 dense.
+ *   workspace: 256 bytes, 256-byte aligned (the status word).
+ */
+DSA_API int dsa_paged_append(
+    const void *k, const int64_t *k_strides, const void *v,
+    const int64_t *v_strides, const void *q, const int64_t *q_strides, int S,
+    int B, int H, int Hk, int D, void *k_cache, void *v_cache,
+    const int64_t *cache_strides, int num_pages, int page_size,
+    const int32_t *page_table, int max_pages, const int32_t *positions,
+    const float *wq, const float *wk, float eps, const double *inv_freq,
+    int rot_start, int rot_dim, int interleaved, float rot_scale, void *out_q,
+    void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Attention over selected blocks of keys.  Blocks are runs of block_size
+ * keys; row (s, b), at position p = q_pos[b] + s (q_pos NULL: p = s), attends
+ * to the keys j <= p, j < T, of
+ *   - the blocks that blocks[b, s, :] names: a set, so a repeated id counts
+ *     once; -1 is an empty entry, an id past the row's own block names no
+ *     key, an id outside [-1, ceil(T / block_size)) is skipped and sets
+ *     DSA_ERR_INDEX_RANGE;
+ *   - the local_blocks blocks that end with the one p lies in.
+ * With head h reading key head h / (H / Hk),
+ *     x_j = scale q.k_j,  o = sum_j softmax(x)_j v_j,  lse = ln sum_j exp x_j
+ * and o = 0, lse = -inf for a row without keys.  dsa_indexer_fwd() over keys
+ * compressed by block_size gives such ids (its top-k over whole blocks).
+ *   q [S, B, H, D] bf16 dense; k, v [T, B, Hk, D] bf16, kv_strides: element
+ *   strides (token, sequence, head) of k, then of v, or NULL for dense;
+ *   blocks [B, S, topk] (sel_heads = 1: one selection for all heads) or
+ *   [B, S, Hk, topk] (sel_heads = Hk) int32, NULL with topk = 0.
+ *   out_o [S, B, H, D] bf16, out_lse [S, B, H] fp32.
+ * Envelope: D in {64, 128}; block_size in {16, 32, 64, 128}; H / Hk <= 64;
+ * at most 16384 blocks; scale > 0; q, k, v, out_o 16-byte aligned and the
+ * strides multiples of 8.  Scores, statistics and sums in fp32; the softmax
+ * weights enter the output product as bf16.  What a masked key's v holds
+ * (infinities and NaN too) does not reach a row.
+ *   workspace: dsa_block_attn_workspace_size() bytes, 256-byte aligned
+ *   (0 for invalid sizes).
+ */
+#define DSA_BLOCK_ATTN_MAX_GROUP 64
+#define DSA_BLOCK_ATTN_MAX_BLOCKS 16384
+DSA_API size_t dsa_block_attn_workspace_size(int S, int B, int H, int Hk,
+                                             int D, int T, int block_size,
+                                             int topk, int local_blocks);
+DSA_API int dsa_block_attn_fwd(const void *q, const void *k, const void *v,
+                               const int64_t *kv_strides, int S, int B, int H,
+                               int Hk, int D, int T, const int32_t *blocks,
+                               int sel_heads, int topk, int block_size,
+                               int local_blocks, const int32_t *q_pos,
+                               float scale, void *out_o, float *out_lse,
+                               void *workspace, size_t workspace_bytes,
+                               void *cuda_stream);
+
+/*
+ * The same over a paged cache (one token a sequence, several, or a chunk of
+ * a prompt): T = max_pages * page_size, block n of sequence b lies in page
+ * page_table[b, n * block_size / page_size]; page_size is a multiple of
+ * block_size.  cache_strides as for dsa_paged_append().  A block whose page
+ * id is outside [0, num_pages) is skipped and sets DSA_ERR_INDEX_RANGE; the
+ * table is read only for blocks that a row attends to.
+ */
+DSA_API int dsa_block_attn_paged_fwd(
+    const void *q, const void *k_cache, const void *v_cache,
+    const int64_t *cache_strides, int num_pages, int page_size,
+    const int32_t *page_table, int max_pages, int S, int B, int H, int Hk,
+    int D, const int32_t *blocks, int sel_heads, int topk, int block_size,
+    int local_blocks, const int32_t *q_pos, float scale, void *out_o,
+    float *out_lse, void *workspace, size_t workspace_bytes,
+    void *cuda_stream);
+
+/*
+ * Backward of dsa_block_attn_fwd(): o and lse are its outputs, grad_o
+ * [S, B, H, D] bf16 the gradient of o (lse gets none).  Outputs, dense bf16:
+ * grad_q [S, B, H, D], grad_k and grad_v [T, B, Hk, D] (sums over the group's
+ * heads; every element written, in an order that does not change from run to
+ * run).  The probabilities and dS enter the products as bf16, the sums are
+ * fp32.  Finite inputs only: a NaN or an infinity in q, k, v or grad_o may
+ * reach gradients of neighbouring rows.
+ *   workspace: dsa_block_attn_bwd_workspace_size() bytes, 256-byte aligned.
+ */
+DSA_API size_t dsa_block_attn_bwd_workspace_size(int S, int B, int H, int Hk,
+                                                 int D, int T, int block_size,
+                                                 int topk, int local_blocks);
+DSA_API int dsa_block_attn_bwd(
+    const void *q, const void *k, const void *v, const int64_t *kv_strides,
+    const void *o, const float *lse, const void *grad_o, int S, int B, int H,
+    int Hk, int D, int T, const int32_t *blocks, int sel_heads, int topk,
+    int block_size, int local_blocks, const int32_t *q_pos, float scale,
+    void *grad_q, void *grad_k, void *grad_v, void *workspace,
+    size_t workspace_bytes, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
