@@ -152,6 +152,32 @@ int encode_q_heads(CUtensorMap *m, const Problem &p, int queries, int heads) {
   return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_UNSUPPORTED;
 }
 
+// Keys or values bf16 viewed as (d, token, head, sequence or page), element
+// strides st, sh, sx; one box is 64 d x `rows` tokens.  A dimension of one
+// element, or one that repeats the same element (stride 0: the caller passes
+// extent 1), may have any stride.
+int encode_kv(CUtensorMap *m, const void *base, int D, int rows,
+              long long tokens, long long st, long long heads, long long sh,
+              long long outer, long long sx) {
+  auto fn = encode_fn();
+  if (!fn) return DSA_ERR_CUDA;
+  auto bytes = [&](long long n, long long s) {
+    return (cuuint64_t)(n > 1 ? s * 2 : (long long)D * 2);
+  };
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)tokens,
+                              (cuuint64_t)heads, (cuuint64_t)outer};
+  const cuuint64_t strides[3] = {bytes(tokens, st), bytes(heads, sh),
+                                 bytes(outer, sx)};
+  const cuuint32_t box[4] = {(cuuint32_t)dsa::kChunk, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_UNSUPPORTED;
+}
+
 // Multiprocessor count of the current device (DSA_ERR_UNSUPPORTED unless
 // it is an sm_103 device).
 int device_num_sms(int *num_sms) {

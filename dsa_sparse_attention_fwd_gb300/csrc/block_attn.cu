@@ -3,46 +3,544 @@
 // p = q_pos[b] + s attends to the keys j <= p of its blocks: the topk given
 // ids (each once) and the `local` blocks that end with its own.
 //     x_j = scale q.k_j,  o = softmax(x) v,  lse = ln sum exp x
+//
+// A CTA takes one query tile: up to 32 consecutive queries with the G heads
+// that share a key head, 128 MMA rows.  It walks the union of its queries'
+// blocks, 128 keys a step; a row's own choice is a bit in the block's mask.
+// Neighbouring queries ask for much the same blocks, so the union is little
+// longer than one query's list and the keys are read once for all of them;
+// where they do not, an MMA over 128 rows still takes no longer than one over
+// 16, so a query alone costs what it would cost in a tile of its own.
+//   S = Q K^T on the tensor cores (128 x 128, fp32 in tensor memory); each
+// softmax thread owns a row: maximum, moved only when a step exceeds it by
+// more than 2^8 (then O is rescaled), P = exp2(S c - m) rounded to bf16 into
+// the columns of S it has read; O += P V with P from tensor memory.
+//   One stage of K and V (96 KB with Q at D = 128) and 256 tensor-memory
+// columns let two CTAs share an SM: one's products run under the other's
+// softmax, and its next K arrives while its own softmax and second product
+// run.  Few rows (single tokens) are split over their blocks, and a second
+// kernel joins the parts.
+//
+// Masked keys: their scores are replaced before use; a V row that no row of
+// the tile sees is zeroed in shared memory (a page's unwritten end may hold
+// anything).  A V row that some rows see meets a zero weight in the others,
+// which a NaN or an infinity survives: rows with a result that is not finite
+// are computed again on their own (block_attn_row.cuh).
+//
+// Warps: 0 .. 3 softmax (warp w reads tensor-memory lanes 32 w .. + 31), 4
+// TMA producer, 5 MMA issuer and tensor-memory allocator.
 #include "block_attn.cuh"
 #include "block_attn_host.cuh"
 #include "block_attn_row.cuh"
 #include "dsa_indexer.h"
+#include "ptx.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kRows = 128;  // MMA rows of a query tile
+constexpr int kKeys = 128;  // keys of a step
+constexpr int kFwdThreads = 192;
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
+constexpr uint32_t kTmS = 0, kTmO = 128;  // tensor-memory columns; P is in S
+constexpr float kSlack = 8.f;
 
-// One warp per (row, head).
-__global__ void __launch_bounds__(kRowWarps * 32)
-    block_attn_rows_kernel(const BlockAttn p, __nv_bfloat16 *out_o,
-                           float *out_lse) {
-  __shared__ float qs_all[kRowWarps][128];
+// What a launch adds to the problem.
+struct FwdPlan {
+  int qt;      // queries of a tile
+  int tiles;   // query tiles of a sequence
+  int splits;  // CTAs that share a tile's blocks
+  int cap;     // entries of the block list
+  __nv_bfloat16 *o;
+  float *lse;
+  // splits > 1: [item][split][qt * G] rows of D and of log-sums (base 2)
+  float *part_o, *part_l;
+};
+
+template <int D>
+struct FwdSmem {
+  static constexpr int kCh = D / 64;
+  static constexpr int kTile = kCh * kRows * 128;  // 128 rows of D bf16
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kTile;
+  static constexpr int kOffV = 2 * kTile;
+  static constexpr int kOffBar = 3 * kTile;
+  // q_full k_full k_empty v_full v_empty s_full p_full o_full
+  static constexpr int kOffMisc = kOffBar + 8 * 8;
+  static constexpr int kOffWords = kOffMisc + 32;
+  static int bytes(int nblk, int cap) {
+    return kOffWords + nblk * 4 + ((cap * 2 + 15) & ~15) + 1024;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kFwdThreads, 2)
+    block_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ KvMaps maps,
+                          const BlockAttn p, const FwdPlan pl) {
+  using L = FwdSmem<D>;
+  constexpr int CH = L::kCh;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys);
+  constexpr uint32_t kIdescO = idesc_bf16_f32_mn(kRows, D, false, true);
+  const float neg_inf = -__int_as_float(0x7f800000);
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw_addr);
+  const uint32_t sQ = base + L::kOffQ, sK = base + L::kOffK,
+                 sV = base + L::kOffV;
+  const uint32_t bars = base + L::kOffBar;
+  const uint32_t q_full = bars, k_full = bars + 8, k_empty = bars + 16,
+                 v_full = bars + 24, v_empty = bars + 32, s_full = bars + 40,
+                 p_full = bars + 48, o_full = bars + 56;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+  volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
+  int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
+  uint32_t *words = reinterpret_cast<uint32_t *>(smem + L::kOffWords);
+  uint16_t *list = reinterpret_cast<uint16_t *>(words + p.nblk);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // later tiles have more keys: they go first
+  int it = blockIdx.x;
+  const int split = it % pl.splits;
+  it /= pl.splits;
+  const int hk = it % p.Hk;
+  it /= p.Hk;
+  const int b = it % p.B;
+  const int tile = pl.tiles - 1 - it / p.B;
+  const int s0 = tile * pl.qt;
+  const int nq = min(pl.qt, p.S - s0);
+
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) mbar_init(bars + 8 * i, i == 6 ? 4 : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_holder), 256);
+    tmem_relinquish();
+  }
+  for (int n = tid; n < p.nblk; n += kFwdThreads) words[n] = 0u;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  mark_blocks(p, b, s0, nq, hk, words, tid, kFwdThreads);
+  __syncthreads();
+  if (warp == 0) {
+    const int n = list_blocks(words, p.nblk, list, lane);
+    if (lane == 0) *sCount = n;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_holder;
+  const int bpt = kKeys / p.blk;  // blocks of a step
+  const int all = (*sCount + bpt - 1) / bpt;
+  const int t0 = (int)((long long)all * split / pl.splits);
+  const int t1 = (int)((long long)all * (split + 1) / pl.splits);
+  const int count = *sCount;
+  if (t1 - t0 == 1 && count < t1 * bpt) {
+    // a single, ragged step: the rows past its blocks are read by the second
+    // product (times zero) and must be numbers
+    for (int i = tid; i < L::kTile / 16; i += kFwdThreads) {
+      const uint32_t z[4] = {0u, 0u, 0u, 0u};
+      st_shared_v4(sV + i * 16, z);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+
+  if (warp == kTmaWarp) {
+    // ---------------- TMA producer ----------------
+    if (t1 > t0 && lane == 0) {
+      mbar_arrive_expect_tx(q_full, CH * pl.qt * p.G * 128);
+      for (int c = 0; c < CH; ++c)
+        tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk,
+                    hk * p.G, b, s0);
+    }
+    for (int t = t0; t < t1; ++t) {
+      const uint32_t ph = (t - t0) & 1u;
+      const int nb = min(bpt, count - t * bpt);
+      // lane (block, chunk) of the step
+      const int bi = lane / CH, c = lane % CH;
+      const bool mine = bi < nb;
+      int tok = 0, outer = 0;
+      if (mine) {
+        const int n = list[t * bpt + bi];
+        if (p.table) {
+          bool bad = false;
+          outer = block_page(p, b, n, bad);
+          tok = (int)((long long)n * p.blk % p.page_size);
+        } else {
+          outer = b;
+          tok = n * p.blk;
+        }
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t full = kv ? v_full : k_full;
+        if (!__all_sync(0xffffffffu,
+                        wait_bar_inl(kv ? v_empty : k_empty, ph ^ 1u,
+                                     abort_flag, p.status)))
+          goto done;
+        if (lane == 0) mbar_arrive_expect_tx(full, nb * p.blk * CH * 128);
+        __syncwarp();
+        if (mine)
+          tma_load_4d((kv ? sV : sK) + c * (kRows * 128) + bi * p.blk * 128,
+                      kv ? &maps.v : &maps.k, full, c * kChunk, tok,
+                      hk * (kv ? maps.bc_vh : maps.bc_kh),
+                      outer * (kv ? maps.bc_vs : maps.bc_ks));
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- MMA issuer ----------------
+    const uint32_t lead = lane == 0;
+    auto wall = [&](uint32_t bar, uint32_t ph) -> bool {
+      return __all_sync(0xffffffffu,
+                        wait_bar_inl(bar, ph, abort_flag, p.status));
+    };
+    const uint64_t qd = sdesc_k_sw128(sQ), kd = sdesc_k_sw128(sK);
+    const uint64_t vd = sdesc_mn_sw128(sV, kRows * 128, 1024);
+    if (t1 > t0 && !wall(q_full, 0)) goto done;
+    for (int t = t0; t < t1; ++t) {
+      const uint32_t ph = (t - t0) & 1u;
+      if (!wall(k_full, ph)) goto done;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t o = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+        mma_bf16_by(tmem + kTmS, qd + o, kd + o, kIdescS, ks != 0, lead);
+      }
+      mma_commit_by(k_empty, lead);
+      mma_commit_by(s_full, lead);
+      if (!wall(v_full, ph) || !wall(p_full, ph)) goto done;
+      tc_fence_after();
+#pragma unroll
+      for (int ks = 0; ks < kKeys / 16; ++ks)
+        mma_bf16_ta_by(tmem + kTmO, tmem + kTmS + ks * 8,
+                       vd + ((ks * 2048) >> 4), kIdescO,
+                       (t > t0 || ks != 0) ? 1u : 0u, lead);
+      mma_commit_by(v_empty, lead);
+      if (t + 1 == t1) mma_commit_by(o_full, lead);
+    }
+  } else {
+    // ---------------- softmax: one row a thread ----------------
+    const int row = tid;
+    const int qi = row / p.G;
+    const bool live = qi < nq;
+    const int s = s0 + (live ? qi : 0), h = hk * p.G + row % p.G;
+    const long long pos = live ? min(row_pos(p.q_pos, b, s),
+                                     (long long)p.T - 1)
+                               : -1;
+    // the last key that any row of the tile sees, and its block
+    const long long pos_hi =
+        min(row_pos(p.q_pos, b, s0 + nq - 1), (long long)p.T - 1);
+    const float c2 = p.scale * 1.4426950408889634f;
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tS = tmem + kTmS + lane_off, tO = tmem + kTmO + lane_off;
+    float m = neg_inf, l = 0.f;
+    for (int t = t0; t < t1; ++t) {
+      const uint32_t ph = (t - t0) & 1u;
+      uint32_t mask[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        mask[c] = live ? tile_mask(words, list, t * bpt, count, p.blk, c, qi,
+                                   pos)
+                       : 0u;
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_inl(s_full, ph, abort_flag, p.status)))
+        goto done;
+      tc_fence_after();
+      float mx = neg_inf;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (__all_sync(0xffffffffu, mask[c] == 0u)) continue;
+        uint32_t u[32];
+        __syncwarp();
+        tmem_ld32(tS + c * 32, u);
+        tmem_ld_wait();
+        reg_fence32(u);
+        if (__all_sync(0xffffffffu, mask[c] == 0xffffffffu)) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(u[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            mx = fmaxf(mx, mask[c] >> i & 1u ? __uint_as_float(u[i])
+                                             : neg_inf);
+        }
+      }
+      mx *= c2;
+      // a row without a key so far keeps m = -inf and weights of zero
+      const bool move = mx > m + kSlack;
+      if (__any_sync(0xffffffffu, move && t > t0)) {
+        const float f = move ? ex2(m - mx) : 1.f;
+        l *= f;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t u[32];
+          __syncwarp();
+          tmem_ld32(tO + c * 32, u);
+          tmem_ld_wait();
+          reg_fence32(u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+          tmem_st32(tO + c * 32, u);
+        }
+      }
+      if (move) m = mx;
+      const float mu = m > neg_inf ? m : 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+        if (__all_sync(0xffffffffu, mask[c] == 0u)) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+        } else {
+          uint32_t u[32];
+          __syncwarp();
+          tmem_ld32(tS + c * 32, u);
+          tmem_ld_wait();
+          reg_fence32(u);
+          const bool full = __all_sync(0xffffffffu, mask[c] == 0xffffffffu);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float e0 = ex2(fmaf(__uint_as_float(u[i]), c2, -mu));
+            float e1 = ex2(fmaf(__uint_as_float(u[i + 1]), c2, -mu));
+            if (!full) {
+              e0 = mask[c] >> i & 1u ? e0 : 0.f;
+              e1 = mask[c] >> (i + 1) & 1u ? e1 : 0.f;
+            }
+            l += e0 + e1;
+            pk[i >> 1] = pack_bf16x2(e0, e1);
+          }
+        }
+        __syncwarp();
+        tmem_st16(tS + c * 16, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      // V rows of this step that no row sees
+      {
+        const int i = t * bpt + row / p.blk;
+        const bool over =
+            i < count && (long long)list[i] * p.blk + row % p.blk > pos_hi;
+        if (__any_sync(0xffffffffu, over)) {
+          if (!__all_sync(0xffffffffu,
+                          wait_bar_inl(v_full, ph, abort_flag, p.status)))
+            goto done;
+          const uint32_t z[4] = {0u, 0u, 0u, 0u};
+          if (over)
+            for (int c = 0; c < CH * 8; ++c)
+              st_shared_v4(sV + (c >> 3) * (kRows * 128) + row * 128 +
+                               (c & 7) * 16,
+                           z);
+          fence_proxy_async_smem();
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    // ---------------- o = O / l ----------------
+    if (t1 > t0) {
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_inl(o_full, 0, abort_flag, p.status)))
+        goto done;
+      tc_fence_after();
+    }
+    const bool some = l > 0.f || l != l;
+    const float inv = some ? 1.f / l : 0.f;
+    bool odd = l != l || l > 3e38f;  // not finite: computed again below
+    const size_t at = ((size_t)s * p.B + b) * p.H + h;
+    const size_t part =
+        ((size_t)(blockIdx.x / pl.splits) * pl.splits + split) *
+            (pl.qt * p.G) +
+        row;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t u[32];
+      if (t1 > t0) {
+        __syncwarp();
+        tmem_ld32(tO + c * 32, u);
+        tmem_ld_wait();
+        reg_fence32(u);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float v = some ? __uint_as_float(u[i]) * inv : 0.f;
+        odd |= !(fabsf(v) < 3e38f);
+        u[i] = __float_as_uint(v);
+      }
+      if (!live) {
+      } else if (pl.splits > 1) {
+        float4 *dst = reinterpret_cast<float4 *>(pl.part_o + part * D + c * 32);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          dst[i] = make_float4(
+              __uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+              __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
+      } else {
+        uint4 *dst = reinterpret_cast<uint4 *>(pl.o + at * D + c * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(u[8 * i + 2 * e]),
+                               __uint_as_float(u[8 * i + 2 * e + 1]));
+          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+    odd &= live;
+    if (live) {
+      const float lse2 = some ? m + log2f(l) : neg_inf;
+      if (pl.splits > 1)
+        // a NaN tells the joining kernel to compute the row again
+        pl.part_l[part] = odd ? __int_as_float(0x7fffffff) : lse2;
+      else
+        pl.lse[at] = some ? lse2 * 0.69314718055994531f : neg_inf;
+    }
+    unsigned todo = __ballot_sync(0xffffffffu, odd);
+    if (pl.splits == 1) {
+      // K's space is free: the last product is done
+      float *qs = reinterpret_cast<float *>(smem + L::kOffK) + warp * 128;
+      for (; todo; todo &= todo - 1) {
+        const int r = warp * 32 + __ffs(todo) - 1;
+        const int sr = s0 + r / p.G, hr = hk * p.G + r % p.G;
+        const size_t ar = ((size_t)sr * p.B + b) * p.H + hr;
+        __syncwarp();
+        for (int d = lane; d < D; d += 32)
+          qs[d] = __bfloat162float(p.q[ar * D + d]);
+        __syncwarp();
+        bool bad = false;
+        float acc[4], ls;
+        attn_row(p, b, sr, hk, qs, lane, bad, acc, ls);
+        for (int i = 0; i * 32 < D; ++i)
+          pl.o[ar * D + lane + 32 * i] = __float2bfloat16(acc[i]);
+        if (lane == 0) pl.lse[ar] = ls;
+      }
+    }
+  }
+done:
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// Joins the parts of a split tile: o = sum_i w_i o_i / sum_i w_i with
+// w_i = 2^(l_i - max).  One warp a row.
+__global__ void __launch_bounds__(256)
+    block_attn_join_kernel(const BlockAttn p, const FwdPlan pl) {
+  __shared__ float qs_all[8][128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long it = (long long)blockIdx.x * kRowWarps + warp;
-  if (it >= (long long)p.S * p.B * p.H) return;
-  const int h = (int)(it % p.H);
-  const int b = (int)(it / p.H % p.B), s = (int)(it / p.H / p.B);
-  float *qs = qs_all[warp];
-  for (int d = lane; d < p.D; d += 32)
-    qs[d] = __bfloat162float(p.q[it * p.D + d]);
-  __syncwarp();
-  bool bad = false;
-  float acc[4], lse;
-  attn_row(p, b, s, h / p.G, qs, lane, bad, acc, lse);
-  for (int i = 0; i * 32 < p.D; ++i)
-    out_o[it * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
-  if (lane == 0) out_lse[it] = lse;
-  if (__any_sync(0xffffffffu, bad) && lane == 0)
-    atomicOr(p.status, kStatusIndexRange);
+  const long long r = (long long)blockIdx.x * 8 + warp;
+  if (r >= (long long)p.S * p.B * p.H) return;
+  const float neg_inf = -__int_as_float(0x7f800000);
+  const int h = (int)(r % p.H);
+  const int b = (int)(r / p.H % p.B), s = (int)(r / p.H / p.B);
+  const int hk = h / p.G, tile = s / pl.qt;
+  const int rows = pl.qt * p.G;
+  const size_t item = ((size_t)(pl.tiles - 1 - tile) * p.B + b) * p.Hk + hk;
+  const size_t part =
+      item * pl.splits * rows + (s - tile * pl.qt) * p.G + h % p.G;
+  float mx = neg_inf;
+  bool odd = false;
+  for (int i = lane; i < pl.splits; i += 32) {
+    const float l = pl.part_l[part + (size_t)i * rows];
+    odd |= l != l;
+    mx = fmaxf(mx, l);
+  }
+  for (int x = 16; x; x >>= 1)
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  float acc[4] = {}, ls = neg_inf;
+  if (__any_sync(0xffffffffu, odd)) {
+    float *qs = qs_all[warp];
+    for (int d = lane; d < p.D; d += 32)
+      qs[d] = __bfloat162float(p.q[r * p.D + d]);
+    __syncwarp();
+    bool bad = false;
+    attn_row(p, b, s, hk, qs, lane, bad, acc, ls);
+  } else if (mx > neg_inf) {
+    float sum = 0.f;
+    for (int i = 0; i < pl.splits; ++i) {
+      const float w = ex2(pl.part_l[part + (size_t)i * rows] - mx);
+      sum += w;
+      const float *src = pl.part_o + (part + (size_t)i * rows) * p.D + lane;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        if (d * 32 < p.D) acc[d] = fmaf(w, src[32 * d], acc[d]);
+    }
+    for (int d = 0; d < 4; ++d) acc[d] /= sum;
+    ls = (mx + log2f(sum)) * 0.69314718055994531f;
+  }
+  for (int d = 0; d * 32 < p.D; ++d)
+    pl.o[r * p.D + lane + 32 * d] = __float2bfloat16(acc[d]);
+  if (lane == 0) pl.lse[r] = ls;
+}
+
+// Room for two CTAs an SM on the largest device: a split launch has no more.
+constexpr int kSplitItems = 320;
+
+template <int D>
+int launch_fwd(const CUtensorMap &tm_q, const KvMaps &maps,
+               const BlockAttn &p, const FwdPlan &pl, cudaStream_t st) {
+  auto kern = block_attn_fwd_kernel<D>;
+  const int smem = FwdSmem<D>::bytes(p.nblk, pl.cap);
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const long long grid = (long long)pl.tiles * p.B * p.Hk * pl.splits;
+  if (grid > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
+  kern<<<(unsigned)grid, kFwdThreads, smem, st>>>(tm_q, maps, p, pl);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
-            cudaStream_t st) {
+            int num_sms, cudaStream_t st) {
+  FwdPlan pl{};
+  pl.qt = tile_queries(p.G, kRows);
+  if (pl.qt > p.S) pl.qt = p.S;
+  pl.tiles = (p.S + pl.qt - 1) / pl.qt;
+  const long long most = (long long)pl.qt * (p.topk + p.local);
+  pl.cap = (int)(most < p.nblk ? most : p.nblk);
+  pl.o = static_cast<__nv_bfloat16 *>(out_o);
+  pl.lse = out_lse;
+  // Few tiles: share each among CTAs until two an SM are busy, with a step
+  // each at least.
+  const long long items = (long long)pl.tiles * p.B * p.Hk;
+  const int bpt = kKeys / p.blk;
+  long long slots = 2ll * num_sms;
+  if (slots > kSplitItems) slots = kSplitItems;
+  pl.splits = 1;
+  if (items * 2 <= slots) {
+    long long n = slots / items;
+    const long long steps = (pl.cap + bpt - 1) / bpt;
+    if (n > steps) n = steps;
+    pl.splits = (int)n;
+  }
+  if (pl.splits > 1) {
+    pl.part_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    const size_t rows = (size_t)items * pl.splits * pl.qt * p.G;
+    pl.part_o = pl.part_l + ((rows + 63) & ~(size_t)63);
+  }
+  CUtensorMap tm_q;
+  KvMaps maps;
+  Problem qp{p.q, nullptr, nullptr, nullptr, p.S, p.B, p.H, p.D, 1, 1};
+  int rc = encode_q_heads(&tm_q, qp, pl.qt, p.G);
+  if (rc != DSA_OK) return rc;
+  rc = encode_kv_maps(p, p.blk, &maps);
+  if (rc != DSA_OK) return rc;
+  rc = p.D == 64 ? launch_fwd<64>(tm_q, maps, p, pl, st)
+                 : launch_fwd<128>(tm_q, maps, p, pl, st);
+  if (rc != DSA_OK || pl.splits == 1) return rc;
   const long long rows = (long long)p.S * p.B * p.H;
-  block_attn_rows_kernel<<<(unsigned)((rows + kRowWarps - 1) / kRowWarps),
-                           kRowWarps * 32, 0, st>>>(
-      p, static_cast<__nv_bfloat16 *>(out_o), out_lse);
+  block_attn_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
@@ -61,7 +559,7 @@ int fwd_common(BlockAttn &p, void *out_o, float *out_lse, void *workspace,
   int num_sms = 0;
   const int rd = device_num_sms(&num_sms);
   if (rd != DSA_OK) return rd;
-  return run_fwd(p, out_o, out_lse, workspace,
+  return run_fwd(p, out_o, out_lse, workspace, num_sms,
                  static_cast<cudaStream_t>(cuda_stream));
 }
 
@@ -95,6 +593,9 @@ int check_block_attn(BlockAttn &p) {
   if (!aligned_to(p.q, 16) || !aligned_to(p.k, 16) || !aligned_to(p.v, 16) ||
       !aligned_to(p.blocks, 4) || !aligned_to(p.q_pos, 4))
     return DSA_ERR_INVALID_ARG;
+  // tokens of one tensor may not share their memory
+  if ((p.table ? p.page_size : p.T) > 1 && (p.k_st == 0 || p.v_st == 0))
+    return DSA_ERR_INVALID_ARG;
   for (long long s : {p.k_st, p.k_sb, p.k_sh, p.v_st, p.v_sb, p.v_sh})
     if (s % 8 != 0 || s < 0 || s >= (1ll << 38)) return DSA_ERR_INVALID_ARG;
   return DSA_OK;
@@ -123,7 +624,15 @@ size_t dsa_block_attn_workspace_size(int S, int B, int H, int Hk, int D,
   if (S <= 0 || B <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || D <= 0 ||
       T <= 0 || block_size <= 0 || topk < 0 || local_blocks < 0)
     return 0;
-  return 256;
+  // the status word, then the parts of tiles shared among CTAs
+  const int G = H / Hk;
+  if (G > DSA_BLOCK_ATTN_MAX_GROUP) return 256;
+  long long qt = dsa::tile_queries(G, dsa::kRows);
+  if (qt > S) qt = S;
+  const long long items = ((S + qt - 1) / qt) * B * Hk;
+  if (items * 2 > dsa::kSplitItems) return 256;
+  const size_t rows = (size_t)dsa::kSplitItems * qt * G;
+  return 256 + (rows + 64) * 4 + rows * D * 4;
 }
 
 int dsa_block_attn_fwd(const void *q, const void *k, const void *v,

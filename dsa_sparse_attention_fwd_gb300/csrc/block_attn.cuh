@@ -60,4 +60,92 @@ __device__ __forceinline__ int block_page(const BlockAttn &p, int b, int n,
   return -1;
 }
 
+// Query tiles: `qt` consecutive queries of one sequence with the G heads of
+// one key head are qt * G <= `rows` MMA rows (row = query * G + head); at
+// most 32 queries, one bit each in a block's mask.
+__host__ __device__ __forceinline__ int tile_queries(int G, int rows) {
+  const int n = rows / G;
+  return n > 32 ? 32 : n;
+}
+
+// The blocks that the queries s0 .. s0 + nq - 1 of sequence b attend to
+// under key head hk: words[n] gets bit i where query s0 + i holds block n.
+// Every thread of the CTA takes part; the caller has zeroed words[0 .. nblk)
+// and synchronises before and after.
+__device__ __forceinline__ void mark_blocks(const BlockAttn &p, int b, int s0,
+                                            int nq, int hk, uint32_t *words,
+                                            int tid, int nthreads) {
+  const int n_cand = p.topk + p.local;
+  const long long pos0 = row_pos(p.q_pos, b, s0);
+  bool bad = false;
+  for (int x = tid; x < nq * n_cand; x += nthreads) {
+    const int i = x / n_cand;
+    const int n = candidate(p, row_ids(p, b, s0 + i, hk), pos0 + i,
+                            x - i * n_cand, bad);
+    if (n < 0) continue;
+    if (p.table && block_page(p, b, n, bad) < 0) continue;
+    atomicOr(words + n, 1u << i);
+  }
+  if (bad) atomicOr(p.status, kStatusIndexRange);
+}
+
+// The marked blocks in ascending order; one warp.  Returns their number.
+__device__ __forceinline__ int list_blocks(const uint32_t *words, int nblk,
+                                           uint16_t *list, int lane) {
+  int count = 0;
+  for (int n0 = 0; n0 < nblk; n0 += 128) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int n = n0 + u * 32 + lane;
+      const bool any = n < nblk && words[n] != 0;
+      const unsigned m = __ballot_sync(0xffffffffu, any);
+      if (any) list[count + __popc(m & ((1u << lane) - 1))] = (uint16_t)n;
+      count += __popc(m);
+    }
+  }
+  return count;
+}
+
+// The keys j0 .. j0 + width - 1 that a row at `pos` sees, as a mask.
+__device__ __forceinline__ uint32_t run_mask(long long pos, long long j0,
+                                             int width) {
+  const long long n = pos - j0 + 1;
+  if (n <= 0) return 0u;
+  if (n >= width) return width >= 32 ? 0xffffffffu : (1u << width) - 1u;
+  return (1u << (int)n) - 1u;
+}
+
+// Mask of the 32 keys `c` (0 ..) of a tile whose blocks are list[l0 ..],
+// l0 + i < count, for the row of query bit qi at position pos.
+__device__ __forceinline__ uint32_t tile_mask(const uint32_t *words,
+                                              const uint16_t *list, int l0,
+                                              int count, int blk, int c,
+                                              int qi, long long pos) {
+  if (blk >= 32) {
+    const int i = l0 + c * 32 / blk;
+    if (i >= count) return 0u;
+    const int n = list[i];
+    if (!(words[n] >> qi & 1u)) return 0u;
+    return run_mask(pos, (long long)n * blk + c * 32 % blk, 32);
+  }
+  uint32_t m = 0u;  // blocks of 16
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = l0 + c * 2 + u;
+    if (i >= count) continue;
+    const int n = list[i];
+    if (words[n] >> qi & 1u)
+      m |= run_mask(pos, (long long)n * 16, 16) << (16 * u);
+  }
+  return m;
+}
+
+// TMA coordinates of block n of sequence b, for a map made with
+// encode_kv_maps(): token (or slot) and sequence (or page).  A broadcast
+// sequence or head has extent 1 and coordinate 0 (bc_*).
+struct KvMaps {
+  CUtensorMap k, v;
+  int bc_ks, bc_kh, bc_vs, bc_vh;  // 0 where broadcast, else 1
+};
+
 }  // namespace dsa

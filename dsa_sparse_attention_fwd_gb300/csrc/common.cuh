@@ -152,6 +152,12 @@ cudaError_t launch_index_topk(const Problem &p, const CUtensorMap &tm_q,
 int encode_q(CUtensorMap *m, const Problem &p, int queries);
 int encode_q_heads(CUtensorMap *m, const Problem &p, int queries, int heads);
 
+// TMA map of keys or values [..] bf16 as (d, token, head, sequence or page)
+// with a box of 64 d x `rows` tokens (returns a dsa_status code).
+int encode_kv(CUtensorMap *m, const void *base, int D, int rows,
+              long long tokens, long long st, long long heads, long long sh,
+              long long outer, long long sx);
+
 // Multiprocessor count of the current device (a dsa_status code).
 int device_num_sms(int *num_sms);
 

@@ -309,6 +309,22 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc,
       : "memory");
 }
 
+// As mma_bf16_by with A in tensor memory: lane = row, each 32-bit column two
+// consecutive K values, so one MMA's K = 16 takes 8 columns.
+__device__ __forceinline__ void mma_bf16_ta_by(uint32_t d_tmem,
+                                               uint32_t a_tmem,
+                                               uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate,
+                                               uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
+}
+
 // mma_bf16 executed by the whole (converged) warp and issued by the lanes
 // whose `issue` is non-zero (one lane): no branch around the instruction.
 __device__ __forceinline__ void mma_bf16_by(uint32_t d_tmem, uint64_t adesc,
@@ -404,6 +420,26 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr,
       "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
       "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+// Store 16 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr,
+                                          const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 2^x by the special-function unit (results below 2^-126 become zero).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ void tmem_st_wait() {
