@@ -1,78 +1,999 @@
 // Backward of the block attention.  With P = exp(x - lse) from the saved
-// log-sums:  dv_j += P do,  dP = do.v_j,  dS = P (dP - do.o) scale,
-// dq += dS k_j,  dk_j += dS q; dk and dv are sums over the heads of a group.
+// log-sums and delta = do.o (a sum over D):
+//     dv_j = sum P do,   dP = do.v_j,   dS = P (dP - delta),
+//     dq = scale sum dS k_j,   dk_j = scale sum dS q;
+// dk and dv are sums over the heads of a group and over the rows that hold
+// the key's block.
+//
+// Two passes, each with its sums in tensor memory, so nothing is added
+// atomically and the results do not change from run to run:
+//   dq: a CTA takes a query tile (128 rows of queries x heads, as in the
+// forward) and walks the union of its blocks, 64 keys a step: S = Q K^T, dP =
+// dO V^T, dS in bf16 back into tensor memory, dQ += dS K.
+//   dk, dv: a CTA takes 128 consecutive keys and walks the query tiles (64
+// rows) that hold one of their blocks: S^T = K Q^T, dP^T = V dO^T, dV += P^T
+// dO, dK += dS^T Q.  The list of these query tiles is the transpose of the
+// selection: bwd_mark_kernel lists each query tile's blocks and sets a bit
+// for each of its key tiles, bwd_scan_kernel turns the counts into offsets
+// and cuts long lists (blocks that every query holds) into chunks of a
+// quarter of an SM's share, bwd_fill_kernel writes them.  Chunks of one key
+// tile leave their sums in fp32 and bwd_join_kernel adds them in order.
+//   Both run one CTA an SM with the scores of two steps in tensor memory: one
+// warpgroup works on one step while the tensor cores run the other's
+// products.
 #include "block_attn.cuh"
 #include "block_attn_host.cuh"
-#include "block_attn_row.cuh"
 #include "dsa_indexer.h"
 #include "ptx.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kBwdThreads = 320;  // 8 compute warps, TMA warp, MMA warp
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kKeyTile = 128;  // keys of a dk, dv item
+constexpr int kRowTile = 64;   // rows of its query tiles
+constexpr int kKvStages = 3;
+constexpr int kMinChunk = 16;     // query tiles of a chunk at least
+constexpr int kChunkUnits = 640;  // 4 chunks on each of 160 SMs
 
-// One warp per (row, head); dk and dv by fp32 atomics.
-__global__ void __launch_bounds__(kRowWarps * 32)
-    block_attn_bwd_rows_kernel(const BlockAttn p, const __nv_bfloat16 *o,
-                               const float *lse, const __nv_bfloat16 *go,
-                               __nv_bfloat16 *gq, float *gk, float *gv) {
-  __shared__ float qs_all[kRowWarps][128], gs_all[kRowWarps][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long it = (long long)blockIdx.x * kRowWarps + warp;
-  if (it >= (long long)p.S * p.B * p.H) return;
-  const int h = (int)(it % p.H);
-  const int b = (int)(it / p.H % p.B), s = (int)(it / p.H / p.B);
-  const int hk = h / p.G;
-  float *qs = qs_all[warp], *gs = gs_all[warp];
-  float delta = 0.f;
-  for (int d = lane; d < p.D; d += 32) {
-    qs[d] = __bfloat162float(p.q[it * p.D + d]);
-    gs[d] = __bfloat162float(go[it * p.D + d]);
-    delta = fmaf(gs[d], __bfloat162float(o[it * p.D + d]), delta);
-  }
-  for (int x = 16; x; x >>= 1) delta += __shfl_xor_sync(0xffffffffu, delta, x);
-  __syncwarp();
-  const float ls = lse[it];
-  bool bad = false;
-  float acc[4] = {};
-  row_keys(p, b, s, hk, qs, lane, bad,
-           [&](int j, float x, bool has, long long ko, long long vo) {
-             float pr = 0.f, ds = 0.f;
-             if (has) {
-               float dp = 0.f;
-               for (int d = 0; d < p.D; ++d)
-                 dp = fmaf(gs[d], __bfloat162float(p.v[vo + d]), dp);
-               pr = expf(x - ls);
-               ds = pr * (dp - delta) * p.scale;
-             }
-             const unsigned any = __ballot_sync(0xffffffffu, has);
-             for (int t = 0; t < 32; ++t) {
-               const long long at = __shfl_sync(0xffffffffu, ko, t);
-               const float w = __shfl_sync(0xffffffffu, ds, t);
-               const float pw = __shfl_sync(0xffffffffu, pr, t);
-               const int jt = __shfl_sync(0xffffffffu, j, t);
-               if (!(any >> t & 1u)) continue;
-               const size_t g0 =
-                   (((size_t)jt * p.B + b) * p.Hk + hk) * p.D + lane;
-               for (int i = 0; i * 32 < p.D; ++i) {
-                 const int d = lane + 32 * i;
-                 acc[i] = fmaf(w, __bfloat162float(p.k[at + d]), acc[i]);
-                 atomicAdd(gk + g0 + 32 * i, w * qs[d]);
-                 atomicAdd(gv + g0 + 32 * i, pw * gs[d]);
-               }
-             }
-           });
-  for (int i = 0; i * 32 < p.D; ++i)
-    gq[it * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
-  if (__any_sync(0xffffffffu, bad) && lane == 0)
-    atomicOr(p.status, kStatusIndexRange);
+// The transposed selection and the other buffers in the workspace.
+struct BwdPlan {
+  int qt, nqt;      // queries of a 64-row tile, such tiles of a sequence
+  int nkt, nqw;     // key tiles of a sequence, words of a bit row over nqt
+  int bpt;          // blocks of a key tile
+  int cap;          // blocks that a query tile can hold
+  int rep;          // key heads that share a selection
+  long long entries;  // of all lists, at most
+  int items, slots;   // at most
+  float2 *stat;       // [S, B, H] (lse log2 e, delta); no keys: (+inf, 0)
+  uint32_t *counts;   // [B Hs nkt] entries of each key tile
+  uint32_t *bits;     // [B Hs nkt][nqw]
+  uint32_t *head;     // number of items
+  uint32_t *lens;     // [B Hs nqt] blocks of each query tile
+  uint32_t *lmask;    // [B Hs nqt][cap] query masks of its blocks
+  uint16_t *lblk;     // [B Hs nqt][cap] the blocks, ascending
+  uint32_t *offs;     // [B Hs nkt] first entry
+  uint32_t *slot0;    // [B Hs nkt] first partial slot (chunks > 1)
+  uint32_t *chunks;   // [B Hs nkt]
+  uint2 *item;        // (key tile of all, chunk)
+  uint32_t *chunk_len;
+  uint32_t *eq;       // [entries] query tile
+  uint32_t *em;       // [entries][bpt] query masks of the tile's blocks
+  float *part;        // [slots][rep][2][128][D]
+  size_t bytes;       // of the workspace
+  size_t zero_bytes;  // from counts on: cleared by the call
+};
+
+int make_plan(const BlockAttn &p, char *ws, BwdPlan *pl) {
+  pl->qt = tile_queries(p.G, kRowTile);
+  if (pl->qt > p.S) pl->qt = p.S;
+  pl->nqt = (p.S + pl->qt - 1) / pl->qt;
+  pl->nkt = (int)(((long long)p.T + kKeyTile - 1) / kKeyTile);
+  pl->nqw = (pl->nqt + 31) / 32;
+  pl->bpt = kKeyTile / p.blk;
+  const long long most = (long long)pl->qt * (p.topk + p.local);
+  pl->cap = (int)(most < p.nblk ? most : p.nblk);
+  pl->rep = p.Hk / p.sel_heads;
+  const long long bh = (long long)p.B * p.sel_heads;
+  const long long kts = bh * pl->nkt, qts = bh * pl->nqt;
+  pl->entries = qts * (pl->nkt < pl->cap ? pl->nkt : pl->cap);
+  if (pl->entries >= (1ll << 31) || kts >= (1ll << 28) ||
+      qts * pl->cap >= (1ll << 40))
+    return DSA_ERR_UNSUPPORTED;
+  pl->items = (int)(kts + kChunkUnits / pl->rep + 1);
+  // only lists longer than a chunk have slots: at most twice entries / chunk
+  long long slots = 2 * (kChunkUnits / pl->rep) + 2;
+  if (slots > pl->entries / (kMinChunk / 2) + 1)
+    slots = pl->entries / (kMinChunk / 2) + 1;
+  pl->slots = (int)slots;
+  size_t at = 256;
+  auto take = [&](size_t n) {
+    char *r = ws + at;
+    at = (at + n + 255) & ~(size_t)255;
+    return r;
+  };
+  const size_t z0 = at;
+  pl->counts = reinterpret_cast<uint32_t *>(take(kts * 4));
+  pl->bits = reinterpret_cast<uint32_t *>(take(kts * pl->nqw * 4));
+  pl->zero_bytes = at - z0;
+  pl->head = reinterpret_cast<uint32_t *>(take(4));
+  pl->chunk_len = reinterpret_cast<uint32_t *>(take(4));
+  pl->stat = reinterpret_cast<float2 *>(take((size_t)p.S * p.B * p.H * 8));
+  pl->lens = reinterpret_cast<uint32_t *>(take(qts * 4));
+  pl->lmask = reinterpret_cast<uint32_t *>(take((size_t)qts * pl->cap * 4));
+  pl->lblk = reinterpret_cast<uint16_t *>(take((size_t)qts * pl->cap * 2));
+  pl->offs = reinterpret_cast<uint32_t *>(take(kts * 4));
+  pl->slot0 = reinterpret_cast<uint32_t *>(take(kts * 4));
+  pl->chunks = reinterpret_cast<uint32_t *>(take(kts * 4));
+  pl->item = reinterpret_cast<uint2 *>(take((size_t)pl->items * 8));
+  pl->eq = reinterpret_cast<uint32_t *>(take((size_t)pl->entries * 4));
+  pl->em = reinterpret_cast<uint32_t *>(
+      take((size_t)pl->entries * pl->bpt * 4));
+  pl->part = reinterpret_cast<float *>(
+      take((size_t)pl->slots * pl->rep * 2 * kKeyTile * p.D * 4));
+  pl->bytes = at;
+  return DSA_OK;
 }
 
-__global__ void round_kernel(const float *x, __nv_bfloat16 *y, size_t n) {
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (size_t)gridDim.x * blockDim.x)
-    y[i] = __float2bfloat16(x[i]);
+// ---- delta --------------------------------------------------------------------
+
+// stat = (lse log2 e, do.o); one warp a row.  A row without keys gets +inf,
+// so its weights exp2(x - inf) are zero.
+template <int D>
+__global__ void __launch_bounds__(256)
+    bwd_delta_kernel(const __nv_bfloat16 *o, const __nv_bfloat16 *go,
+                     const float *lse, long long rows, float2 *stat) {
+  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= rows) return;
+  float t = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const size_t at = (size_t)r * D + i * 64 + lane * 2;
+    const float2 a = __bfloat1622float2(
+        *reinterpret_cast<const __nv_bfloat162 *>(o + at));
+    const float2 g = __bfloat1622float2(
+        *reinterpret_cast<const __nv_bfloat162 *>(go + at));
+    t = fmaf(a.x, g.x, t);
+    t = fmaf(a.y, g.y, t);
+  }
+  for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
+  if (lane == 0) {
+    const float inf = __int_as_float(0x7f800000);
+    const float l = lse[r];
+    stat[r] = l == -inf ? make_float2(inf, 0.f)
+                        : make_float2(l * 1.4426950408889634f, t);
+  }
+}
+
+// ---- the transposed selection ---------------------------------------------------
+
+// A CTA lists the blocks of one query tile and marks its key tiles.
+__global__ void __launch_bounds__(128)
+    bwd_mark_kernel(const BlockAttn p, const BwdPlan pl) {
+  extern __shared__ uint32_t words[];
+  uint16_t *list = reinterpret_cast<uint16_t *>(words + p.nblk);
+  __shared__ int sCount;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const long long it = blockIdx.x;
+  const int tile = (int)(it % pl.nqt);
+  const long long bh = it / pl.nqt;
+  const int b = (int)(bh / p.sel_heads), hs = (int)(bh % p.sel_heads);
+  const int s0 = tile * pl.qt, nq = min(pl.qt, p.S - s0);
+  for (int n = tid; n < p.nblk; n += 128) words[n] = 0u;
+  __syncthreads();
+  mark_blocks(p, b, s0, nq, hs, words, tid, 128);
+  __syncthreads();
+  if (tid < 32) {
+    const int n = list_blocks(words, p.nblk, list, lane);
+    if (lane == 0) sCount = n;
+  }
+  __syncthreads();
+  const int count = sCount;
+  if (tid == 0) pl.lens[it] = (uint32_t)count;
+  for (int i = tid; i < count; i += 128) {
+    const int n = list[i];
+    pl.lblk[(size_t)it * pl.cap + i] = (uint16_t)n;
+    pl.lmask[(size_t)it * pl.cap + i] = words[n];
+    const int kt = n / pl.bpt;
+    if (i == 0 || list[i - 1] / pl.bpt != kt) {
+      const long long k = bh * pl.nkt + kt;
+      atomicOr(pl.bits + k * pl.nqw + (tile >> 5), 1u << (tile & 31));
+      atomicAdd(pl.counts + k, 1u);
+    }
+  }
+}
+
+// Exclusive sum of x over the 1024 threads of the CTA, and the total.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *sums,
+                                               uint32_t &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t inc = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) sums[warp] = inc;
+  __syncthreads();
+  uint32_t before = 0;
+  total = 0;
+  for (int w = 0; w < 32; ++w) {
+    const uint32_t v = sums[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  return before + inc - x;
+}
+
+// Offsets of the lists, and the items: chunks of each list (a list without
+// entries is one chunk, which writes zeros).  One CTA.
+__global__ void __launch_bounds__(1024)
+    bwd_scan_kernel(const BwdPlan pl, int kts) {
+  __shared__ uint32_t sums[32];
+  const int per = (kts + 1023) / 1024;
+  const int k0 = min(kts, (int)threadIdx.x * per), k1 = min(kts, k0 + per);
+  uint32_t n = 0, total;
+  for (int k = k0; k < k1; ++k) n += pl.counts[k];
+  uint32_t off = block_scan(n, sums, total);
+  const unsigned long long share =
+      ((unsigned long long)total * pl.rep + kChunkUnits - 1) / kChunkUnits;
+  const uint32_t len = share > kMinChunk ? (uint32_t)share : kMinChunk;
+  uint32_t items = 0, slots = 0, unused;
+  for (int k = k0; k < k1; ++k) {
+    const uint32_t c = pl.counts[k];
+    const uint32_t ch = c == 0 ? 1u : (c + len - 1) / len;
+    items += ch;
+    slots += ch > 1 ? ch : 0u;
+  }
+  uint32_t item = block_scan(items, sums, total);
+  if (threadIdx.x == 0) {
+    *pl.head = total;
+    *pl.chunk_len = len;
+  }
+  uint32_t slot = block_scan(slots, sums, unused);
+  for (int k = k0; k < k1; ++k) {
+    const uint32_t c = pl.counts[k];
+    const uint32_t ch = c == 0 ? 1u : (c + len - 1) / len;
+    pl.offs[k] = off;
+    pl.chunks[k] = ch;
+    pl.slot0[k] = slot;
+    for (uint32_t i = 0; i < ch; ++i) pl.item[item + i] = make_uint2(k, i);
+    off += c;
+    item += ch;
+    slot += ch > 1 ? ch : 0u;
+  }
+}
+
+// The entries of one key tile, in the order of the query tiles.
+__global__ void __launch_bounds__(1024)
+    bwd_fill_kernel(const BlockAttn p, const BwdPlan pl) {
+  __shared__ uint32_t sums[32];
+  const long long k = blockIdx.x;
+  const int kt = (int)(k % pl.nkt);
+  const long long bh = k / pl.nkt;
+  const uint32_t off = pl.offs[k], count = pl.counts[k];
+  if (count == 0) return;
+  uint32_t done = 0;
+  for (int w0 = 0; w0 < pl.nqw; w0 += 1024) {
+    const int w = w0 + threadIdx.x;
+    uint32_t m = w < pl.nqw ? pl.bits[k * pl.nqw + w] : 0u;
+    uint32_t total;
+    uint32_t at = off + done + block_scan(__popc(m), sums, total);
+    for (; m; m &= m - 1) pl.eq[at++] = w * 32 + __ffs(m) - 1;
+    done += total;
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < count; i += 1024) {
+    const size_t it = (size_t)bh * pl.nqt + pl.eq[off + i];
+    const uint16_t *blk = pl.lblk + it * pl.cap;
+    // first of the tile's blocks that is in this key tile
+    int lo = 0, hi = (int)pl.lens[it];
+    const int first = kt * pl.bpt, last = first + pl.bpt, n = hi;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (blk[mid] < first) lo = mid + 1;
+      else hi = mid;
+    }
+    uint32_t *em = pl.em + (size_t)(off + i) * pl.bpt;
+    for (int x = 0; x < pl.bpt; ++x) em[x] = 0u;
+    for (; lo < n && blk[lo] < last; ++lo)
+      em[blk[lo] - first] = pl.lmask[it * pl.cap + lo];
+  }
+}
+
+// ---- dk, dv ---------------------------------------------------------------------
+
+template <int D>
+struct KvSmem {
+  static constexpr int kCh = D / 64;
+  static constexpr int kTile = kCh * kKeyTile * 128;  // K or V
+  static constexpr int kRow = kCh * kRowTile * 128;   // Q or dO of a stage
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kTile;
+  static constexpr int kOffS = 2 * kTile;  // stages: Q, dO
+  static constexpr int kOffStat = kOffS + kKvStages * 2 * kRow;
+  static constexpr int kOffMask = kOffStat + kKvStages * kRowTile * 8;
+  static constexpr int kOffBar = kOffMask + kKvStages * 32;
+  // kv_full st_full[3] st_empty[3] sdp_full[2] ds_full[2] acc_full
+  static constexpr int kOffMisc = kOffBar + 12 * 8;
+  static constexpr int kBytes = kOffMisc + 32 + 1024;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    block_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_go,
+                          const __grid_constant__ KvMaps maps,
+                          const BlockAttn p, const BwdPlan pl,
+                          __nv_bfloat16 *gk, __nv_bfloat16 *gv) {
+  using L = KvSmem<D>;
+  constexpr int CH = L::kCh;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kKeyTile, kRowTile);
+  constexpr uint32_t kIdescA = idesc_bf16_f32_mn(kKeyTile, D, false, true);
+  constexpr uint32_t kTmK = 0, kTmV = 128, kTmBuf = 256;  // + 128 a step
+
+  if (blockIdx.x / pl.rep >= *pl.head) return;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw_addr);
+  const uint32_t sK = base + L::kOffK, sV = base + L::kOffV;
+  auto sQ = [&](int st) { return base + L::kOffS + st * 2 * L::kRow; };
+  auto sG = [&](int st) { return sQ(st) + L::kRow; };
+  float2 *stat = reinterpret_cast<float2 *>(smem + L::kOffStat);
+  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::kOffMask);
+  const uint32_t bars = base + L::kOffBar;
+  const uint32_t kv_full = bars, acc_full = bars + 88;
+  auto st_full = [&](int i) { return bars + 8 + 8 * i; };
+  auto st_empty = [&](int i) { return bars + 32 + 8 * i; };
+  auto sdp_full = [&](int i) { return bars + 56 + 8 * i; };
+  auto ds_full = [&](int i) { return bars + 72 + 8 * i; };
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+  volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint2 item = pl.item[blockIdx.x / pl.rep];
+  const int k = (int)item.x;
+  const int kt = k % pl.nkt, bh = k / pl.nkt;
+  const int b = bh / p.sel_heads;
+  const int hk = bh % p.sel_heads * pl.rep + blockIdx.x % pl.rep;
+  const uint32_t count = pl.counts[k], len = *pl.chunk_len;
+  const uint32_t e0 = pl.offs[k] + item.y * len;
+  const int n = (int)min(len, count - item.y * len);  // entries of this item
+
+  if (tid == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(acc_full, 1);
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(st_full(i), 33);
+      mbar_init(st_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sdp_full(i), 1);
+      mbar_init(ds_full(i), 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_go);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  // rows past the query tile's are never loaded, but read as operands (times
+  // zero): they must be numbers
+  if (pl.qt * p.G < kRowTile) {
+    for (int i = tid; i < kKvStages * 2 * L::kRow / 16; i += kBwdThreads) {
+      const uint32_t z[4] = {0u, 0u, 0u, 0u};
+      st_shared_v4(base + L::kOffS + i * 16, z);
+    }
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == kTmaWarp) {
+    if (n > 0 && lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * L::kTile);
+      for (int c = 0; c < CH; ++c) {
+        tma_load_4d(sK + c * (kKeyTile * 128), &maps.k, kv_full, c * kChunk,
+                    kt * kKeyTile, hk * maps.bc_kh, b * maps.bc_ks);
+        tma_load_4d(sV + c * (kKeyTile * 128), &maps.v, kv_full, c * kChunk,
+                    kt * kKeyTile, hk * maps.bc_vh, b * maps.bc_vs);
+      }
+    }
+    const float inf = __int_as_float(0x7f800000);
+    for (int i = 0; i < n; ++i) {
+      const int st = i % kKvStages;
+      const uint32_t ph = (i / kKvStages) & 1u;
+      const int s0 = (int)pl.eq[e0 + i] * pl.qt;
+      const int rows = min(pl.qt, p.S - s0) * p.G;
+      float2 v[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = lane + 32 * u;
+        v[u] = make_float2(inf, 0.f);
+        if (r < rows)
+          v[u] = pl.stat[((size_t)(s0 + r / p.G) * p.B + b) * p.H + hk * p.G +
+                         r % p.G];
+      }
+      // the keys' blocks, without the queries before the key itself
+      const uint32_t m =
+          lane < pl.bpt ? pl.em[(size_t)(e0 + i) * pl.bpt + lane] : 0u;
+      if (!__all_sync(0xffffffffu, wait_bar_inl(st_empty(st), ph ^ 1u,
+                                                abort_flag, p.status)))
+        goto done;
+      stat[st * kRowTile + lane] = v[0];
+      stat[st * kRowTile + lane + 32] = v[1];
+      if (lane < 8) masks[st * 8 + lane] = m;
+      mbar_arrive(st_full(st));
+      if (lane == 0) {
+        mbar_arrive_expect_tx(st_full(st), 2 * CH * pl.qt * p.G * 128);
+        for (int c = 0; c < CH; ++c) {
+          tma_load_4d(sQ(st) + c * (kRowTile * 128), &tm_q, st_full(st),
+                      c * kChunk, hk * p.G, b, s0);
+          tma_load_4d(sG(st) + c * (kRowTile * 128), &tm_go, st_full(st),
+                      c * kChunk, hk * p.G, b, s0);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == kMmaWarp) {
+    const uint32_t lead = lane == 0;
+    auto wall = [&](uint32_t bar, uint32_t ph) -> bool {
+      return __all_sync(0xffffffffu,
+                        wait_bar_inl(bar, ph, abort_flag, p.status));
+    };
+    if (n > 0 && !wall(kv_full, 0)) goto done;
+    const uint64_t kd = sdesc_k_sw128(sK), vd = sdesc_k_sw128(sV);
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {
+        const int st = i % kKvStages;
+        if (!wall(st_full(st), (i / kKvStages) & 1u)) goto done;
+        tc_fence_after();
+        const uint64_t qd = sdesc_k_sw128(sQ(st)), gd = sdesc_k_sw128(sG(st));
+        const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t ao = ((ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32) >> 4;
+          const uint32_t bo = ((ks >> 2) * (kRowTile * 128) + (ks & 3) * 32) >> 4;
+          mma_bf16_by(d, kd + ao, qd + bo, kIdescS, ks != 0, lead);
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t ao = ((ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32) >> 4;
+          const uint32_t bo = ((ks >> 2) * (kRowTile * 128) + (ks & 3) * 32) >> 4;
+          mma_bf16_by(d + 64, vd + ao, gd + bo, kIdescS, ks != 0, lead);
+        }
+        mma_commit_by(sdp_full(i & 1), lead);
+      }
+      if (i > 0) {
+        const int j = i - 1, st = j % kKvStages;
+        if (!wall(ds_full(j & 1), (j >> 1) & 1u)) goto done;
+        tc_fence_after();
+        const uint64_t qm = sdesc_mn_sw128(sQ(st), kRowTile * 128, 1024);
+        const uint64_t gm = sdesc_mn_sw128(sG(st), kRowTile * 128, 1024);
+        const uint32_t a = tmem + kTmBuf + (j & 1) * 128;
+#pragma unroll
+        for (int ks = 0; ks < kRowTile / 16; ++ks)
+          mma_bf16_ta_by(tmem + kTmV, a + ks * 8, gm + ((ks * 2048) >> 4),
+                         kIdescA, (j > 0 || ks != 0) ? 1u : 0u, lead);
+#pragma unroll
+        for (int ks = 0; ks < kRowTile / 16; ++ks)
+          mma_bf16_ta_by(tmem + kTmK, a + 64 + ks * 8, qm + ((ks * 2048) >> 4),
+                         kIdescA, (j > 0 || ks != 0) ? 1u : 0u, lead);
+        mma_commit_by(st_empty(st), lead);
+        if (i == n) mma_commit_by(acc_full, lead);
+      }
+    }
+  } else {
+    // ---------------- one key a thread; steps alternate ----------------
+    const int wg = warp >> 2;
+    const int key = (warp & 3) * 32 + lane;
+    const long long j = (long long)kt * kKeyTile + key;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const float c2 = p.scale * 1.4426950408889634f;
+    const uint32_t every = pl.qt >= 32 ? 0xffffffffu : (1u << pl.qt) - 1u;
+    const unsigned long long gmask =
+        p.G >= 64 ? ~0ull : (1ull << p.G) - 1ull;
+    const long long q0 = row_pos(p.q_pos, b, 0);
+    for (int i = wg; i < n; i += 2) {
+      const int st = i % kKvStages;
+      const long long pos0 = q0 + (long long)pl.eq[e0 + i] * pl.qt;
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_inl(sdp_full(wg), (i >> 1) & 1u, abort_flag,
+                                   p.status) &&
+                          wait_bar_inl(st_full(st), (i / kKvStages) & 1u,
+                                       abort_flag, p.status)))
+        goto done;
+      tc_fence_after();
+      // queries that hold this key's block and are not before it
+      uint32_t qm = masks[st * 8 + key / p.blk];
+      const long long late = j - pos0;
+      if (late > 0) qm = late >= 32 ? 0u : qm & (~0u << (int)late);
+      if (j >= p.T) qm = 0u;
+      const bool full = __all_sync(0xffffffffu, qm == every);
+      unsigned long long rm = ~0ull;
+      if (!full) {
+        rm = 0ull;
+        for (int q = 0; q < pl.qt; ++q)
+          if (qm >> q & 1u) rm |= gmask << (q * p.G);
+      }
+      const float4 *sp =
+          reinterpret_cast<const float4 *>(stat + st * kRowTile);
+      const uint32_t ts = tmem + kTmBuf + wg * 128 + lane_off;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t u[32], g[32];
+        __syncwarp();
+        tmem_ld32(ts + c * 32, u);
+        tmem_ld32(ts + 64 + c * 32, g);
+        tmem_ld_wait();
+        reg_fence32(u);
+        reg_fence32(g);
+        uint32_t pk[16], dk[16];
+        const uint32_t half = (uint32_t)(rm >> (32 * c));
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float4 sd = sp[(c * 32 + x) >> 1];
+          float p0 = ex2(fmaf(__uint_as_float(u[x]), c2, -sd.x));
+          float p1 = ex2(fmaf(__uint_as_float(u[x + 1]), c2, -sd.z));
+          if (!full) {
+            p0 = half >> x & 1u ? p0 : 0.f;
+            p1 = half >> (x + 1) & 1u ? p1 : 0.f;
+          }
+          pk[x >> 1] = pack_bf16x2(p0, p1);
+          dk[x >> 1] = pack_bf16x2(p0 * (__uint_as_float(g[x]) - sd.y),
+                                   p1 * (__uint_as_float(g[x + 1]) - sd.w));
+        }
+        __syncwarp();
+        tmem_st16(ts + c * 16, pk);
+        tmem_st16(ts + 64 + c * 16, dk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full(wg));
+    }
+    // ---------------- dK (warpgroup 0), dV (1) ----------------
+    if (n > 0) {
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_inl(acc_full, 0, abort_flag, p.status)))
+        goto done;
+      tc_fence_after();
+    }
+    const float f = wg == 0 ? p.scale : 1.f;
+    const bool direct = pl.chunks[k] == 1;
+    float *part =
+        pl.part + ((((size_t)pl.slot0[k] + item.y) * pl.rep +
+                    blockIdx.x % pl.rep) * 2 + wg) * kKeyTile * D +
+        (size_t)key * D;
+    __nv_bfloat16 *out =
+        (wg == 0 ? gk : gv) + (((size_t)j * p.B + b) * p.Hk + hk) * D;
+#pragma unroll 1
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t u[32];
+      if (n > 0) {
+        __syncwarp();
+        tmem_ld32(tmem + (wg == 0 ? kTmK : kTmV) + lane_off + c * 32, u);
+        tmem_ld_wait();
+        reg_fence32(u);
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        u[x] = n > 0 ? __float_as_uint(__uint_as_float(u[x]) * f) : 0u;
+      if (!direct) {
+        uint4 *dst = reinterpret_cast<uint4 *>(part + c * 32);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          dst[x] = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2],
+                              u[4 * x + 3]);
+      } else if (j < p.T) {
+        uint4 *dst = reinterpret_cast<uint4 *>(out + c * 32);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(u[8 * x + 2 * e]),
+                               __uint_as_float(u[8 * x + 2 * e + 1]));
+          dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+done:
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Adds the chunks of the key tiles that have several.
+template <int D>
+__global__ void __launch_bounds__(256)
+    bwd_join_kernel(const BlockAttn p, const BwdPlan pl, __nv_bfloat16 *gk,
+                    __nv_bfloat16 *gv) {
+  const int k = blockIdx.x / pl.rep, r = blockIdx.x % pl.rep;
+  const uint32_t ch = pl.chunks[k];
+  if (ch <= 1) return;
+  const int kt = k % pl.nkt, bh = k / pl.nkt;
+  const int b = bh / p.sel_heads, hk = bh % p.sel_heads * pl.rep + r;
+  const size_t stride = (size_t)pl.rep * 2 * kKeyTile * D;
+  const float *part = pl.part + ((size_t)pl.slot0[k] * pl.rep + r) * 2 *
+                                    kKeyTile * D;
+  for (int x = threadIdx.x; x < 2 * kKeyTile * D / 4; x += 256) {
+    const int e = x * 4;
+    const int which = e / (kKeyTile * D), key = e / D % kKeyTile, d = e % D;
+    const long long j = (long long)kt * kKeyTile + key;
+    if (j >= p.T) continue;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t c = 0; c < ch; ++c) {
+      const float4 v =
+          *reinterpret_cast<const float4 *>(part + c * stride + e);
+      t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+    }
+    uint2 o = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+    *reinterpret_cast<uint2 *>((which ? gv : gk) +
+                               (((size_t)j * p.B + b) * p.Hk + hk) * D + d) =
+        o;
+  }
+}
+
+// ---- dq ---------------------------------------------------------------------------
+
+constexpr int kDqRows = 128, kDqKeys = 64;
+
+template <int D>
+struct DqSmem {
+  static constexpr int kCh = D / 64;
+  static constexpr int kTile = kCh * kDqRows * 128;  // Q or dO
+  static constexpr int kKey = kCh * kDqKeys * 128;   // K or V of a stage
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffG = kTile;
+  static constexpr int kOffBar = 2 * kTile;
+  // q_full kv_full[3] kv_empty[3] sdp_full[2] ds_full[2] acc_full
+  static constexpr int kOffMisc = kOffBar + 12 * 8;
+  static constexpr int kOffS = 2 * kTile + 1024;  // stages: K, V
+  static int bytes(int stages, int nblk, int cap) {
+    return kOffS + stages * 2 * kKey + nblk * 4 + ((cap * 2 + 15) & ~15) +
+           1024;
+  }
+};
+
+struct DqPlan {
+  int qt, tiles, cap, stages;
+  const float2 *stat;
+  __nv_bfloat16 *gq;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    block_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
+                         const __grid_constant__ CUtensorMap tm_go,
+                         const __grid_constant__ KvMaps maps,
+                         const BlockAttn p, const DqPlan pl) {
+  using L = DqSmem<D>;
+  constexpr int CH = L::kCh;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(kDqRows, kDqKeys);
+  constexpr uint32_t kIdescA = idesc_bf16_f32_mn(kDqRows, D, false, true);
+  constexpr uint32_t kTmQ = 0, kTmBuf = 128;  // + 128 a step
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t *smem = smem_raw + (base - raw_addr);
+  const uint32_t sQ = base + L::kOffQ, sG = base + L::kOffG;
+  auto sK = [&](int st) { return base + L::kOffS + st * 2 * L::kKey; };
+  auto sV = [&](int st) { return sK(st) + L::kKey; };
+  const uint32_t bars = base + L::kOffBar;
+  const uint32_t q_full = bars, acc_full = bars + 88;
+  auto kv_full = [&](int i) { return bars + 8 + 8 * i; };
+  auto kv_empty = [&](int i) { return bars + 32 + 8 * i; };
+  auto sdp_full = [&](int i) { return bars + 56 + 8 * i; };
+  auto ds_full = [&](int i) { return bars + 72 + 8 * i; };
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
+  volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
+  int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
+  uint32_t *words = reinterpret_cast<uint32_t *>(smem + L::kOffS +
+                                                 pl.stages * 2 * L::kKey);
+  uint16_t *list = reinterpret_cast<uint16_t *>(words + p.nblk);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int it = blockIdx.x;
+  const int hk = it % p.Hk;
+  it /= p.Hk;
+  const int b = it % p.B;
+  const int tile = pl.tiles - 1 - it / p.B;
+  const int s0 = tile * pl.qt;
+  const int nq = min(pl.qt, p.S - s0);
+
+  if (tid == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(acc_full, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(kv_full(i), 1);
+      mbar_init(kv_empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sdp_full(i), 1);
+      mbar_init(ds_full(i), 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_go);
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  for (int n = tid; n < p.nblk; n += kBwdThreads) words[n] = 0u;
+  // keys past a ragged step's blocks are read as an operand (times zero)
+  for (int i = tid; i < pl.stages * 2 * L::kKey / 16; i += kBwdThreads) {
+    const uint32_t z[4] = {0u, 0u, 0u, 0u};
+    st_shared_v4(base + L::kOffS + i * 16, z);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  mark_blocks(p, b, s0, nq, hk, words, tid, kBwdThreads);
+  __syncthreads();
+  if (warp == 0) {
+    const int n = list_blocks(words, p.nblk, list, lane);
+    if (lane == 0) *sCount = n;
+  }
+  __syncthreads();
+  const uint32_t tmem = *tmem_holder;
+  // a step takes units of up to 64 keys: whole blocks, or halves of 128
+  const int count = *sCount;
+  const int unit = min(p.blk, kDqKeys), per = p.blk / unit;
+  const int upt = kDqKeys / unit;
+  const int n = (count * per + upt - 1) / upt;
+
+  if (warp == kTmaWarp) {
+    if (n > 0 && lane == 0) {
+      mbar_arrive_expect_tx(q_full, 2 * CH * pl.qt * p.G * 128);
+      for (int c = 0; c < CH; ++c) {
+        tma_load_4d(sQ + c * (kDqRows * 128), &tm_q, q_full, c * kChunk,
+                    hk * p.G, b, s0);
+        tma_load_4d(sG + c * (kDqRows * 128), &tm_go, q_full, c * kChunk,
+                    hk * p.G, b, s0);
+      }
+    }
+    for (int i = 0; i < n; ++i) {
+      const int st = i % pl.stages;
+      const uint32_t ph = (i / pl.stages) & 1u;
+      const int nu = min(upt, count * per - i * upt);
+      const int ui = lane / CH, c = lane % CH;  // unit and chunk of this lane
+      if (!__all_sync(0xffffffffu, wait_bar_inl(kv_empty(st), ph ^ 1u,
+                                                abort_flag, p.status)))
+        goto done;
+      if (lane == 0)
+        mbar_arrive_expect_tx(kv_full(st), 2 * nu * unit * CH * 128);
+      __syncwarp();
+      if (ui < nu) {
+        const int x = i * upt + ui;
+        const int tok = list[x / per] * p.blk + x % per * unit;
+        const uint32_t at = c * (kDqKeys * 128) + ui * unit * 128;
+        tma_load_4d(sK(st) + at, &maps.k, kv_full(st), c * kChunk, tok,
+                    hk * maps.bc_kh, b * maps.bc_ks);
+        tma_load_4d(sV(st) + at, &maps.v, kv_full(st), c * kChunk, tok,
+                    hk * maps.bc_vh, b * maps.bc_vs);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    const uint32_t lead = lane == 0;
+    auto wall = [&](uint32_t bar, uint32_t ph) -> bool {
+      return __all_sync(0xffffffffu,
+                        wait_bar_inl(bar, ph, abort_flag, p.status));
+    };
+    if (n > 0 && !wall(q_full, 0)) goto done;
+    const uint64_t qd = sdesc_k_sw128(sQ), gd = sdesc_k_sw128(sG);
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {
+        const int st = i % pl.stages;
+        if (!wall(kv_full(st), (i / pl.stages) & 1u)) goto done;
+        tc_fence_after();
+        const uint64_t kd = sdesc_k_sw128(sK(st)), vd = sdesc_k_sw128(sV(st));
+        const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t ao = ((ks >> 2) * (kDqRows * 128) + (ks & 3) * 32) >> 4;
+          const uint32_t bo = ((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
+          mma_bf16_by(d, qd + ao, kd + bo, kIdescS, ks != 0, lead);
+        }
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t ao = ((ks >> 2) * (kDqRows * 128) + (ks & 3) * 32) >> 4;
+          const uint32_t bo = ((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
+          mma_bf16_by(d + 64, gd + ao, vd + bo, kIdescS, ks != 0, lead);
+        }
+        mma_commit_by(sdp_full(i & 1), lead);
+      }
+      if (i > 0) {
+        const int j = i - 1, st = j % pl.stages;
+        if (!wall(ds_full(j & 1), (j >> 1) & 1u)) goto done;
+        tc_fence_after();
+        const uint64_t km = sdesc_mn_sw128(sK(st), kDqKeys * 128, 1024);
+        const uint32_t a = tmem + kTmBuf + (j & 1) * 128;
+#pragma unroll
+        for (int ks = 0; ks < kDqKeys / 16; ++ks)
+          mma_bf16_ta_by(tmem + kTmQ, a + ks * 8, km + ((ks * 2048) >> 4),
+                         kIdescA, (j > 0 || ks != 0) ? 1u : 0u, lead);
+        mma_commit_by(kv_empty(st), lead);
+        if (i == n) mma_commit_by(acc_full, lead);
+      }
+    }
+  } else {
+    // ---------------- one row a thread; steps alternate ----------------
+    const int wg = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int qi = row / p.G;
+    const bool live = qi < nq;
+    const int s = s0 + (live ? qi : 0);
+    const long long pos =
+        live ? min(row_pos(p.q_pos, b, s), (long long)p.T - 1) : -1;
+    const size_t at = ((size_t)s * p.B + b) * p.H + hk * p.G + row % p.G;
+    const float2 sd = live ? pl.stat[at]
+                           : make_float2(__int_as_float(0x7f800000), 0.f);
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const float c2 = p.scale * 1.4426950408889634f;
+    for (int i = wg; i < n; i += 2) {
+      uint32_t mask[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        mask[c] = 0u;
+        if (!live) continue;
+        if (unit < p.blk) {  // halves of a block
+          const int bn = list[i >> 1];
+          if (words[bn] >> qi & 1u)
+            mask[c] = run_mask(pos, (long long)bn * p.blk + (i & 1) * 64 +
+                                        c * 32, 32);
+        } else {
+          mask[c] = tile_mask(words, list, i * upt, count, p.blk, c, qi, pos);
+        }
+      }
+      if (!__all_sync(0xffffffffu, wait_bar_inl(sdp_full(wg), (i >> 1) & 1u,
+                                                abort_flag, p.status)))
+        goto done;
+      tc_fence_after();
+      const uint32_t ts = tmem + kTmBuf + wg * 128 + lane_off;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t dk[16];
+        if (__all_sync(0xffffffffu, mask[c] == 0u)) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) dk[x] = 0u;
+        } else {
+          const bool full = __all_sync(0xffffffffu, mask[c] == 0xffffffffu);
+          uint32_t u[32], g[32];
+          __syncwarp();
+          tmem_ld32(ts + c * 32, u);
+          tmem_ld32(ts + 64 + c * 32, g);
+          tmem_ld_wait();
+          reg_fence32(u);
+          reg_fence32(g);
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float p0 = ex2(fmaf(__uint_as_float(u[x]), c2, -sd.x));
+            float p1 = ex2(fmaf(__uint_as_float(u[x + 1]), c2, -sd.x));
+            if (!full) {
+              p0 = mask[c] >> x & 1u ? p0 : 0.f;
+              p1 = mask[c] >> (x + 1) & 1u ? p1 : 0.f;
+            }
+            dk[x >> 1] = pack_bf16x2(p0 * (__uint_as_float(g[x]) - sd.y),
+                                     p1 * (__uint_as_float(g[x + 1]) - sd.y));
+          }
+        }
+        __syncwarp();
+        tmem_st16(ts + c * 16, dk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full(wg));
+    }
+    if (n > 0) {
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_inl(acc_full, 0, abort_flag, p.status)))
+        goto done;
+      tc_fence_after();
+    }
+    // each warpgroup writes half of the columns
+#pragma unroll 1
+    for (int c = wg * (D / 64); c < (wg + 1) * (D / 64); ++c) {
+      uint32_t u[32];
+      if (n > 0) {
+        __syncwarp();
+        tmem_ld32(tmem + kTmQ + lane_off + c * 32, u);
+        tmem_ld_wait();
+        reg_fence32(u);
+      }
+#pragma unroll
+      for (int x = 0; x < 32; ++x)
+        u[x] = n > 0 ? __float_as_uint(__uint_as_float(u[x]) * p.scale) : 0u;
+      if (live) {
+        uint4 *dst = reinterpret_cast<uint4 *>(pl.gq + at * D + c * 32);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(u[8 * x + 2 * e]),
+                               __uint_as_float(u[8 * x + 2 * e + 1]));
+          dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+done:
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr int kMaxSmem = 232448;  // 227 KB opt-in per block
+
+template <int D>
+int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
+               const float *lse, const void *go, void *gq, void *gk, void *gv,
+               cudaStream_t st) {
+  auto ok = [](cudaError_t e) { return e == cudaSuccess; };
+  const long long rows = (long long)p.S * p.B * p.H;
+  const int kts = p.B * p.sel_heads * pl.nkt;
+  const long long qts = (long long)p.B * p.sel_heads * pl.nqt;
+  auto bf = [](void *x) { return static_cast<__nv_bfloat16 *>(x); };
+  if (!ok(cudaMemsetAsync(pl.counts, 0, pl.zero_bytes, st)))
+    return DSA_ERR_CUDA;
+  bwd_delta_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
+      static_cast<const __nv_bfloat16 *>(o),
+      static_cast<const __nv_bfloat16 *>(go), lse, rows, pl.stat);
+  const int mark_smem = p.nblk * 4 + pl.cap * 2;
+  if (!ok(cudaFuncSetAttribute(bwd_mark_kernel,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               mark_smem)))
+    return DSA_ERR_CUDA;
+  bwd_mark_kernel<<<(unsigned)qts, 128, mark_smem, st>>>(p, pl);
+  bwd_scan_kernel<<<1, 1024, 0, st>>>(pl, kts);
+  bwd_fill_kernel<<<kts, 1024, 0, st>>>(p, pl);
+  if (!ok(cudaGetLastError())) return DSA_ERR_CUDA;
+
+  CUtensorMap tm_q, tm_go;
+  KvMaps maps;
+  const Problem qp{p.q, nullptr, nullptr, nullptr, p.S, p.B, p.H, p.D, 1, 1};
+  const Problem gp{go, nullptr, nullptr, nullptr, p.S, p.B, p.H, p.D, 1, 1};
+  int rc = encode_q_heads(&tm_q, qp, pl.qt, p.G);
+  if (rc == DSA_OK) rc = encode_q_heads(&tm_go, gp, pl.qt, p.G);
+  if (rc == DSA_OK) rc = encode_kv_maps(p, kKeyTile, &maps);
+  if (rc != DSA_OK) return rc;
+  auto dkv = block_attn_dkv_kernel<D>;
+  if (!ok(cudaFuncSetAttribute(dkv,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               KvSmem<D>::kBytes)))
+    return DSA_ERR_CUDA;
+  dkv<<<(unsigned)pl.items * pl.rep, kBwdThreads, KvSmem<D>::kBytes, st>>>(
+      tm_q, tm_go, maps, p, pl, bf(gk), bf(gv));
+  bwd_join_kernel<D><<<(unsigned)kts * pl.rep, 256, 0, st>>>(p, pl, bf(gk),
+                                                             bf(gv));
+  if (!ok(cudaGetLastError())) return DSA_ERR_CUDA;
+
+  DqPlan dp{};
+  dp.qt = tile_queries(p.G, kDqRows);
+  if (dp.qt > p.S) dp.qt = p.S;
+  dp.tiles = (p.S + dp.qt - 1) / dp.qt;
+  const long long most = (long long)dp.qt * (p.topk + p.local);
+  dp.cap = (int)(most < p.nblk ? most : p.nblk);
+  dp.stat = pl.stat;
+  dp.gq = bf(gq);
+  // three stages unless a very long context's block words need the room
+  dp.stages = DqSmem<D>::bytes(3, p.nblk, dp.cap) <= kMaxSmem ? 3 : 2;
+  const int smem = DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap);
+  rc = encode_q_heads(&tm_q, qp, dp.qt, p.G);
+  if (rc == DSA_OK) rc = encode_q_heads(&tm_go, gp, dp.qt, p.G);
+  if (rc == DSA_OK) rc = encode_kv_maps(p, p.blk < kDqKeys ? p.blk : kDqKeys,
+                                        &maps);
+  if (rc != DSA_OK) return rc;
+  auto dq = block_attn_dq_kernel<D>;
+  if (!ok(cudaFuncSetAttribute(
+          dq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
+    return DSA_ERR_CUDA;
+  const long long grid = (long long)dp.tiles * p.B * p.Hk;
+  dq<<<(unsigned)grid, kBwdThreads, smem, st>>>(tm_q, tm_go, maps, p, dp);
+  return ok(cudaGetLastError()) ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -86,7 +1007,23 @@ size_t dsa_block_attn_bwd_workspace_size(int S, int B, int H, int Hk, int D,
   if (dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
                                     local_blocks) == 0)
     return 0;
-  return 256 + (size_t)T * B * Hk * D * 8;
+  // the larger of the two ways to select: shared by all heads, or not
+  size_t most = 0;
+  for (int heads : {1, Hk}) {
+    dsa::BlockAttn p{};
+    p.S = S, p.B = B, p.H = H, p.Hk = Hk, p.G = H / Hk, p.D = D, p.T = T;
+    p.sel_heads = heads, p.topk = topk, p.blk = block_size;
+    p.local = local_blocks;
+    p.nblk = (int)(((long long)T + block_size - 1) / block_size);
+    if (p.G > DSA_BLOCK_ATTN_MAX_GROUP || topk + local_blocks <= 0 ||
+        (block_size != 16 && block_size != 32 && block_size != 64 &&
+         block_size != 128))
+      return 0;
+    dsa::BwdPlan pl;
+    if (dsa::make_plan(p, nullptr, &pl) != DSA_OK) return 0;
+    if (pl.bytes > most) most = pl.bytes;
+  }
+  return most;
 }
 
 int dsa_block_attn_bwd(const void *q, const void *k, const void *v,
@@ -116,29 +1053,21 @@ int dsa_block_attn_bwd(const void *q, const void *k, const void *v,
     return DSA_ERR_INVALID_ARG;
   const size_t need = dsa_block_attn_bwd_workspace_size(
       S, B, H, Hk, D, T, block_size, topk, local_blocks);
+  if (need == 0) return DSA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need) return DSA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return DSA_ERR_INVALID_ARG;
   p.status = static_cast<int *>(workspace);
   int num_sms = 0;
   rc = dsa::device_num_sms(&num_sms);
   if (rc != DSA_OK) return rc;
+  dsa::BwdPlan pl;
+  rc = dsa::make_plan(p, static_cast<char *>(workspace), &pl);
+  if (rc != DSA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const size_t n = (size_t)T * B * Hk * D;
-  float *gk = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
-  float *gv = gk + n;
-  if (cudaMemsetAsync(gk, 0, n * 8, st) != cudaSuccess) return DSA_ERR_CUDA;
-  const long long rows = (long long)S * B * H;
-  dsa::block_attn_bwd_rows_kernel<<<
-      (unsigned)((rows + dsa::kRowWarps - 1) / dsa::kRowWarps),
-      dsa::kRowWarps * 32, 0, st>>>(
-      p, static_cast<const __nv_bfloat16 *>(o), lse,
-      static_cast<const __nv_bfloat16 *>(grad_o),
-      static_cast<__nv_bfloat16 *>(grad_q), gk, gv);
-  dsa::round_kernel<<<1024, 256, 0, st>>>(
-      gk, static_cast<__nv_bfloat16 *>(grad_k), n);
-  dsa::round_kernel<<<1024, 256, 0, st>>>(
-      gv, static_cast<__nv_bfloat16 *>(grad_v), n);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return D == 64 ? dsa::launch_bwd<64>(p, pl, o, lse, grad_o, grad_q, grad_k,
+                                       grad_v, st)
+                 : dsa::launch_bwd<128>(p, pl, o, lse, grad_o, grad_q, grad_k,
+                                        grad_v, st);
 }
 
 }  // extern "C"
