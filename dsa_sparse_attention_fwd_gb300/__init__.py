@@ -534,31 +534,59 @@ def rope_inv_freq(rot_dim, base=10000.0, scaling=None, device=None):
     return inv.to(device) if device is not None else inv, rot_scale
 
 
-def _strides(*tensors, lead=3):
-    """Host array of the leading element strides of each tensor; the last
-    dimension must be contiguous (dimensions of one element have any)."""
-    out = []
-    for t in tensors:
-        for n, st in zip(t.shape[:lead], t.stride()[:lead]):
-            out.append(st if n > 1 else 0)
-    return (ctypes.c_int64 * len(out))(*out)
+# The calls below run once a layer for a single token, where the host's time
+# is the call's: their checks touch each tensor a few times only.
+_I3, _I6 = ctypes.c_int64 * 3, ctypes.c_int64 * 6
+
+
+def _on_gpu(where, **tensors):
+    """_require_cuda() in its own words, without building device objects
+    while all is well."""
+    dev = -1
+    for t in tensors.values():
+        if t is not None:
+            if dev < 0 and t.is_cuda:
+                dev = t.get_device()
+            elif not t.is_cuda or t.get_device() != dev:
+                break
+    else:
+        return dev
+    _require_cuda(where, **tensors)
+
+
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _strides(t):
+    """Host array of the three leading element strides (None: dense)."""
+    return None if t.is_contiguous() else _I3(*t.stride()[:3])
+
+
+def _strides2(a, b):
+    return (None if a.is_contiguous() and b.is_contiguous()
+            else _I6(*a.stride()[:3], *b.stride()[:3]))
 
 
 def _last_contiguous(name, t, dt, shape):
     if t.dtype != dt:
         raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    if any(st < 0 for st in t.stride()):
-        raise ValueError(f"{name} has negative strides")
 
 
 def _dense(name, t, dt, shape):
     if t.dtype != dt:
         raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -593,7 +621,7 @@ def dsa_norm_rope_fwd(q, k, inv_freq, positions=None, wq=None, wk=None,
     [rot_dim / 2] fp64 (rope_inv_freq; None: no rotation), positions [S, B]
     int32 (None: row s at s).  Returns (out_q, out_k), dense."""
     lib = load_library()
-    _require_cuda("dsa_norm_rope_fwd", q=q, k=k, inv_freq=inv_freq,
+    dev = _on_gpu("dsa_norm_rope_fwd", q=q, k=k, inv_freq=inv_freq,
                   positions=positions, wq=wq, wk=wk, out_q=out_q, out_k=out_k)
     dt = q.dtype
     if dt not in _ROPE_DTYPES:
@@ -607,11 +635,11 @@ def dsa_norm_rope_fwd(q, k, inv_freq, positions=None, wq=None, wk=None,
             out_k = torch.empty((S, B, Hk, D), dtype=dt, device=q.device)
         _dense("out_k", out_k, dt, (S, B, Hk, D))
     rc = lib.dsa_norm_rope_fwd(
-        _ptr(q), _strides(q), _ptr(k), None if k is None else _strides(k),
-        _ROPE_DTYPES[dt], S, B, H, Hk, D, _ptr(wq), _ptr(wk), float(eps),
-        _ptr(positions), _ptr(inv_freq), int(rot_start), R,
-        int(bool(interleaved)), float(rot_scale), _ptr(out_q), _ptr(out_k),
-        _stream(stream))
+        _addr(q), _strides(q), _addr(k), None if k is None else _strides(k),
+        _ROPE_DTYPES[dt], S, B, H, Hk, D, _addr(wq), _addr(wk), float(eps),
+        _addr(positions), _addr(inv_freq), int(rot_start), R,
+        int(bool(interleaved)), float(rot_scale), _addr(out_q), _addr(out_k),
+        _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_norm_rope_fwd")
     return out_q, out_k
@@ -629,36 +657,36 @@ def dsa_norm_rope_bwd(q, k, grad_out_q, grad_out_k, inv_freq, positions=None,
     outputs (dense).  Returns (grad_q, grad_k, grad_wq, grad_wk, workspace);
     the weights' gradients are fp32 [D], None without the weight."""
     lib = load_library()
-    _require_cuda("dsa_norm_rope_bwd", q=q, k=k, grad_out_q=grad_out_q,
+    dev = _on_gpu("dsa_norm_rope_bwd", q=q, k=k, grad_out_q=grad_out_q,
                   grad_out_k=grad_out_k, inv_freq=inv_freq,
                   positions=positions, wq=wq, wk=wk, workspace=workspace)
-    dt, dev = q.dtype, q.device
+    dt = q.dtype
     if dt not in _ROPE_DTYPES:
         raise TypeError(f"q must be bf16, fp16 or fp32, got {dt}")
     S, B, H, Hk, D, R = _rope_inputs(q, k, inv_freq, positions, wq, wk, dt)
     _dense("grad_out_q", grad_out_q, dt, (S, B, H, D))
     gk = gwq = gwk = None
-    gq = torch.empty((S, B, H, D), dtype=dt, device=dev)
+    gq = torch.empty((S, B, H, D), dtype=dt, device=q.device)
     if k is not None:
         if grad_out_k is None:
             raise ValueError("grad_out_k is needed with k")
         _dense("grad_out_k", grad_out_k, dt, (S, B, Hk, D))
-        gk = torch.empty((S, B, Hk, D), dtype=dt, device=dev)
+        gk = torch.empty((S, B, Hk, D), dtype=dt, device=q.device)
     if wq is not None:
-        gwq = torch.empty(D, dtype=torch.float32, device=dev)
+        gwq = torch.empty(D, dtype=torch.float32, device=q.device)
     if wk is not None and k is not None:
-        gwk = torch.empty(D, dtype=torch.float32, device=dev)
+        gwk = torch.empty(D, dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = torch.empty(max(dsa_norm_rope_bwd_workspace_size(D), 256),
-                                dtype=torch.uint8, device=dev)
+                                dtype=torch.uint8, device=q.device)
     rc = lib.dsa_norm_rope_bwd(
-        _ptr(q), _strides(q), _ptr(k), None if k is None else _strides(k),
-        _ptr(grad_out_q), None if k is None else _ptr(grad_out_k),
-        _ROPE_DTYPES[dt], S, B, H, Hk, D, _ptr(wq), _ptr(wk), float(eps),
-        _ptr(positions), _ptr(inv_freq), int(rot_start), R,
-        int(bool(interleaved)), float(rot_scale), _ptr(gq), _ptr(gk),
-        _ptr(gwq), _ptr(gwk), _ptr(workspace), workspace.numel(),
-        _stream(stream))
+        _addr(q), _strides(q), _addr(k), None if k is None else _strides(k),
+        _addr(grad_out_q), None if k is None else _addr(grad_out_k),
+        _ROPE_DTYPES[dt], S, B, H, Hk, D, _addr(wq), _addr(wk), float(eps),
+        _addr(positions), _addr(inv_freq), int(rot_start), R,
+        int(bool(interleaved)), float(rot_scale), _addr(gq), _addr(gk),
+        _addr(gwq), _addr(gwk), _addr(workspace), workspace.numel(),
+        _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_norm_rope_bwd")
     return gq, gk, gwq, gwk, workspace
@@ -688,7 +716,7 @@ def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
     (out_q, workspace).  The call only sets bits in the workspace's status
     word (256 zeroed bytes to begin with; dsa_indexer_check reads it)."""
     lib = load_library()
-    _require_cuda("dsa_paged_append", k=k, v=v, k_cache=k_cache,
+    dev = _on_gpu("dsa_paged_append", k=k, v=v, k_cache=k_cache,
                   v_cache=v_cache, page_table=page_table,
                   positions=positions, inv_freq=inv_freq, wk=wk, q=q, wq=wq,
                   out_q=out_q, workspace=workspace)
@@ -711,14 +739,14 @@ def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
     if workspace is None:
         workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
     rc = lib.dsa_paged_append(
-        _ptr(k), _strides(k), _ptr(v), _strides(v), _ptr(q),
-        None if q is None else _strides(q), S, B, H, Hk, D, _ptr(k_cache),
-        _ptr(v_cache), _strides(k_cache, v_cache), pages, page_size,
-        _ptr(page_table), page_table.shape[1], _ptr(positions), _ptr(wq),
-        _ptr(wk), float(eps), _ptr(inv_freq), int(rot_start), R,
+        _addr(k), _strides(k), _addr(v), _strides(v), _addr(q),
+        None if q is None else _strides(q), S, B, H, Hk, D, _addr(k_cache),
+        _addr(v_cache), _strides2(k_cache, v_cache), pages, page_size,
+        _addr(page_table), page_table.shape[1], _addr(positions), _addr(wq),
+        _addr(wk), float(eps), _addr(inv_freq), int(rot_start), R,
         int(bool(interleaved)), float(rot_scale),
-        None if q is None else _ptr(out_q), _ptr(workspace),
-        workspace.numel(), _stream(stream))
+        None if q is None else _addr(out_q), _addr(workspace),
+        workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_paged_append")
     return out_q, workspace
@@ -779,7 +807,7 @@ def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
     (o [S, B, H, D] bf16, lse [S, B, H] fp32, workspace); a workspace of the
     caller's has its first 256 bytes zeroed once, before its first use."""
     lib = load_library()
-    _require_cuda("dsa_block_attn_fwd", q=q, k=k, v=v, blocks=blocks,
+    dev = _on_gpu("dsa_block_attn_fwd", q=q, k=k, v=v, blocks=blocks,
                   q_pos=q_pos, out_o=out_o, out_lse=out_lse,
                   workspace=workspace)
     if q.dim() != 4 or k.dim() != 4:
@@ -795,10 +823,10 @@ def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
                                          local_blocks),
         out_o, out_lse, workspace)
     rc = lib.dsa_block_attn_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _strides(k, v), S, B, H, Hk, D, T,
-        _ptr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
-        _ptr(q_pos), float(scale), _ptr(out_o), _ptr(out_lse),
-        _ptr(workspace), workspace.numel(), _stream(stream))
+        _addr(q), _addr(k), _addr(v), _strides2(k, v), S, B, H, Hk, D, T,
+        _addr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
+        _addr(q_pos), float(scale), _addr(out_o), _addr(out_lse),
+        _addr(workspace), workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_block_attn_fwd")
     return out_o, out_lse, workspace
@@ -812,7 +840,7 @@ def dsa_block_attn_paged_fwd(q, k_cache, v_cache, page_table, blocks,
     through page_table [B, max_pages] int32 (S = 1: one token of each
     sequence at q_pos[b])."""
     lib = load_library()
-    _require_cuda("dsa_block_attn_paged_fwd", q=q, k_cache=k_cache,
+    dev = _on_gpu("dsa_block_attn_paged_fwd", q=q, k_cache=k_cache,
                   v_cache=v_cache, page_table=page_table, blocks=blocks,
                   q_pos=q_pos, out_o=out_o, out_lse=out_lse,
                   workspace=workspace)
@@ -831,11 +859,11 @@ def dsa_block_attn_paged_fwd(q, k_cache, v_cache, page_table, blocks,
                                          topk, local_blocks),
         out_o, out_lse, workspace)
     rc = lib.dsa_block_attn_paged_fwd(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _strides(k_cache, v_cache),
-        pages, page_size, _ptr(page_table), max_pages, S, B, H, Hk, D,
-        _ptr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
-        _ptr(q_pos), float(scale), _ptr(out_o), _ptr(out_lse),
-        _ptr(workspace), workspace.numel(), _stream(stream))
+        _addr(q), _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
+        pages, page_size, _addr(page_table), max_pages, S, B, H, Hk, D,
+        _addr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
+        _addr(q_pos), float(scale), _addr(out_o), _addr(out_lse),
+        _addr(workspace), workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_block_attn_paged_fwd")
     return out_o, out_lse, workspace
@@ -848,7 +876,7 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     and grad_o [S, B, H, D] bf16.  Returns (grad_q [S, B, H, D], grad_k and
     grad_v [T, B, Hk, D], dense bf16, workspace)."""
     lib = load_library()
-    _require_cuda("dsa_block_attn_bwd", q=q, k=k, v=v, o=o, lse=lse,
+    dev = _on_gpu("dsa_block_attn_bwd", q=q, k=k, v=v, o=o, lse=lse,
                   grad_o=grad_o, blocks=blocks, q_pos=q_pos, grad_q=grad_q,
                   grad_k=grad_k, grad_v=grad_v, workspace=workspace)
     if q.dim() != 4 or k.dim() != 4:
@@ -879,11 +907,11 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
         workspace[:256].zero_()
     rc = lib.dsa_block_attn_bwd(
-        _ptr(q), _ptr(k), _ptr(v), _strides(k, v), _ptr(o), _ptr(lse),
-        _ptr(grad_o), S, B, H, Hk, D, T, _ptr(blocks), sel_heads, topk,
-        int(block_size), int(local_blocks), _ptr(q_pos), float(scale),
-        _ptr(grad_q), _ptr(grad_k), _ptr(grad_v), _ptr(workspace),
-        workspace.numel(), _stream(stream))
+        _addr(q), _addr(k), _addr(v), _strides2(k, v), _addr(o), _addr(lse),
+        _addr(grad_o), S, B, H, Hk, D, T, _addr(blocks), sel_heads, topk,
+        int(block_size), int(local_blocks), _addr(q_pos), float(scale),
+        _addr(grad_q), _addr(grad_k), _addr(grad_v), _addr(workspace),
+        workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_block_attn_bwd")
     return grad_q, grad_k, grad_v, workspace

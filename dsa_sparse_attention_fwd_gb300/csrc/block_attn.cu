@@ -593,11 +593,17 @@ int check_block_attn(BlockAttn &p) {
   if (!aligned_to(p.q, 16) || !aligned_to(p.k, 16) || !aligned_to(p.v, 16) ||
       !aligned_to(p.blocks, 4) || !aligned_to(p.q_pos, 4))
     return DSA_ERR_INVALID_ARG;
+  for (long long s : {p.k_st, p.k_sb, p.k_sh, p.v_st, p.v_sb, p.v_sh})
+    if (s < 0 || s >= (1ll << 38)) return DSA_ERR_INVALID_ARG;
+  // a dimension of one element may have any other stride
+  if ((p.table ? p.page_size : p.T) == 1) p.k_st = p.v_st = 0;
+  if ((p.table ? p.num_pages : p.B) == 1) p.k_sb = p.v_sb = 0;
+  if (p.Hk == 1) p.k_sh = p.v_sh = 0;
   // tokens of one tensor may not share their memory
   if ((p.table ? p.page_size : p.T) > 1 && (p.k_st == 0 || p.v_st == 0))
     return DSA_ERR_INVALID_ARG;
   for (long long s : {p.k_st, p.k_sb, p.k_sh, p.v_st, p.v_sb, p.v_sh})
-    if (s % 8 != 0 || s < 0 || s >= (1ll << 38)) return DSA_ERR_INVALID_ARG;
+    if (s % 8 != 0) return DSA_ERR_INVALID_ARG;
   return DSA_OK;
 }
 

@@ -18,12 +18,18 @@
 //
 // Bounded by memory: each row is read once and written once, and the
 // statistics stay in registers.  Lanes own 8 consecutive values (16 bytes in
-// 16-bit types), so D = 128 puts two rows in a warp.  Rows that cannot be
-// read in 16-byte pieces (odd sizes, strides or pointers) take the same code
-// with element loads and the partner exchanged through shared memory.
+// 16-bit types), so D = 128 puts two rows in a warp.  CTAs are persistent: the
+// conversion of the frequencies (64-bit arithmetic, slow on this part) runs
+// once a CTA into shared memory, sines and cosines once a token and warp (each
+// lane R / 64 pairs, exchanged through shared memory), and a warp has the
+// loads of kBatch row groups in flight.  Rows that cannot be read in 16-byte
+// pieces (odd sizes, strides or pointers) take the same code with element
+// loads and the partner exchanged through shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "dsa_indexer.h"
@@ -32,10 +38,14 @@
 namespace dsa {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeMaxD = 256;
-constexpr int kRopeBwdMaxCtas = 1216;  // partial sums of the weight gradients
+// CTAs an SM holds (the launch bounds); a grid has no more, so that all run
+// at once and each takes its share of the rows.
+constexpr int rope_ctas(int el, bool vec) { return el == 2 && vec ? 6 : 3; }
+constexpr int kRopeBwdCtas = 4;
+constexpr int kRopeMaxCtas = 6 * 160;
 
 // One of the row sets (queries, keys or values) of a call.
 struct RopeRows {
@@ -102,13 +112,31 @@ struct Chunk {
         raw[i] = e0 + i < D ? p[e0 + i] : Cvt<T>::from(0.f);
     }
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+  __device__ __forceinline__ void get(float2 (&x)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = Cvt<T>::to(raw[i]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = make_float2(raw[2 * i], raw[2 * i + 1]);
+      } else {
+        const uint32_t w = reinterpret_cast<const uint32_t *>(raw)[i];
+        if constexpr (std::is_same<T, __half>::value)
+          x[i] = __half22float2(reinterpret_cast<const __half2 &>(w));
+        else
+          x[i] = make_float2(__uint_as_float(w << 16),
+                             __uint_as_float(w & 0xffff0000u));
+      }
+    }
   }
-  __device__ __forceinline__ void set(const float (&x)[8]) {
+  __device__ __forceinline__ void set(const float2 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) raw[i] = Cvt<T>::from(x[i]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(T) == 4)
+        raw[2 * i] = x[i].x, raw[2 * i + 1] = x[i].y;
+      else if constexpr (std::is_same<T, __half>::value)
+        reinterpret_cast<__half2 *>(raw)[i] = __float22half2_rn(x[i]);
+      else
+        reinterpret_cast<uint32_t *>(raw)[i] = pack_bf16x2(x[i].x, x[i].y);
+    }
   }
   __device__ __forceinline__ void store(T *p, int e0, int D) const {
     if constexpr (VEC) {
@@ -126,91 +154,131 @@ struct Chunk {
   }
 };
 
-// The rotation's coefficients of a lane's 8 elements at one token:
-// y_e = n_e c + n_partner s.
-template <bool VEC>
-struct Turn {
-  float c[8], s[8];
-  int src_lane;  // lane of the partners (halves layout, 16-byte pieces)
+// Frequencies as turns a position, 64-bit fixed point.
+__device__ __forceinline__ void load_freqs(const RopeArgs &a,
+                                           unsigned long long *fr) {
+  for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) {
+    double t = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+    t -= floor(t);
+    fr[i] = __double2ull_rn(t * 18446744073709551616.0);
+  }
+}
 
-  __device__ __forceinline__ void setup(const RopeArgs &a, int e0, int lane) {
-    src_lane = lane;
-    const int rel0 = e0 - a.r0;
-    if (VEC && !a.interleaved && rel0 >= 0 && rel0 < a.R)
-      src_lane = rel0 < a.R / 2 ? lane + a.R / 16 : lane - a.R / 16;
+// cos and sin (times m) of a token's angles into `cs`, by one warp.
+__device__ __forceinline__ void token_turns(const RopeArgs &a, int pos,
+                                            int lane,
+                                            const unsigned long long *fr,
+                                            float2 *cs) {
+  __syncwarp();
+  for (int i = lane; i < a.R / 2; i += 32) {
+    const unsigned long long ph = (unsigned long long)(long long)pos * fr[i];
+    // the top half as a signed fraction of half a turn
+    const float x = (float)(int)(unsigned)(ph >> 32) * 4.656612873077393e-10f;
+    float sn, co;
+    sincospif(x, &sn, &co);
+    cs[i] = make_float2(a.mscale * co, a.mscale * sn);
   }
-  // Element e's pair index, or -1 outside the rotated part.
-  static __device__ __forceinline__ int pair(const RopeArgs &a, int e) {
-    const int rel = e - a.r0;
-    if (rel < 0 || rel >= a.R) return -1;
-    if (a.interleaved) return rel >> 1;
-    return rel < a.R / 2 ? rel : rel - a.R / 2;
-  }
+  __syncwarp();
+}
+
+// The rotation's coefficients of a lane's 8 elements, with the weights where
+// given: y_e = x_e c + x_partner s (times the row's rstd).  An element outside
+// the rotated part is its own partner with half its coefficient in each, so
+// that an infinity there stays one.  Arithmetic on pairs (two fp32 a
+// register pair and instruction).
+template <typename T, bool VEC>
+struct Turn {
+  float2 c[4], s[4];
+  int src_lane;      // lane of the partners (halves layout, 16-byte pieces)
+  unsigned rotated;  // a bit for each element with a partner
+
   static __device__ __forceinline__ int partner(const RopeArgs &a, int e) {
     const int rel = e - a.r0;
     if (rel < 0 || rel >= a.R) return e;
     if (a.interleaved) return a.r0 + (rel ^ 1);
     return rel < a.R / 2 ? e + a.R / 2 : e - a.R / 2;
   }
-  static __device__ __forceinline__ bool first(const RopeArgs &a, int e) {
-    const int rel = e - a.r0;
-    return a.interleaved ? (rel & 1) == 0 : rel < a.R / 2;
-  }
-  __device__ __forceinline__ void at(const RopeArgs &a, int e0, int pos,
-                                     bool back) {
+  // `back` turns the other way (without weights).
+  __device__ __forceinline__ void set(const RopeArgs &a, int e0, int lane,
+                                      const float2 *cs, const float *w,
+                                      bool back) {
+    const int rel0 = e0 - a.r0;
+    src_lane = lane;
+    if (VEC && !a.interleaved && rel0 >= 0 && rel0 < a.R)
+      src_lane = rel0 < a.R / 2 ? lane + a.R / 16 : lane - a.R / 16;
+    rotated = 0u;
+    float cc[8], ss[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int pi = pair(a, e0 + i);
-      if (pi < 0) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-        continue;
+      const int rel = rel0 + i;
+      cc[i] = ss[i] = 0.5f;
+      if (e0 + i >= a.D) continue;
+      if (rel >= 0 && rel < a.R) {
+        const int pi =
+            a.interleaved ? rel >> 1 : rel < a.R / 2 ? rel : rel - a.R / 2;
+        const bool first = a.interleaved ? (rel & 1) == 0 : rel < a.R / 2;
+        const float2 v = cs[pi];
+        cc[i] = v.x;
+        ss[i] = first != back ? -v.y : v.y;
+        rotated |= 1u << i;
       }
-      if (VEC && a.interleaved && (i & 1)) {  // the neighbour's angle
-        c[i] = c[i - 1];
-        s[i] = -s[i - 1];
-        continue;
+      if (w) {
+        cc[i] *= __ldg(w + e0 + i);
+        ss[i] *= __ldg(w + partner(a, e0 + i));
       }
-      double t = __ldg(a.inv_freq + pi) * 0.15915494309189535;  // 1 / (2 pi)
-      t -= floor(t);
-      const unsigned long long f = __double2ull_rn(t * 18446744073709551616.0);
-      const unsigned long long ph = (unsigned long long)(long long)pos * f;
-      const float x = (float)(int)(unsigned)(ph >> 32) * 4.656612873077393e-10f;
-      float sn, cs;
-      sincospif(x, &sn, &cs);
-      c[i] = a.mscale * cs;
-      sn = a.mscale * sn;
-      s[i] = first(a, e0 + i) != back ? -sn : sn;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = make_float2(cc[2 * i], cc[2 * i + 1]);
+      s[i] = make_float2(ss[2 * i], ss[2 * i + 1]);
     }
   }
-  // y = rotation of n.  `buf`: the row's LPR * 8 floats of shared memory.
-  __device__ __forceinline__ void apply(const RopeArgs &a, const float (&n)[8],
-                                        float (&y)[8], int e0,
-                                        float *buf) const {
-    if constexpr (VEC) {
+  // y = x turned.  `buf`: the row's LPR * 8 floats of shared memory.
+  __device__ __forceinline__ void apply(const RopeArgs &a,
+                                        const Chunk<T, VEC> &ch,
+                                        const float2 (&x)[4], float2 (&y)[4],
+                                        int e0, float *buf) const {
+    float2 o[4];
+    if constexpr (VEC) {  // a chunk is turned whole or not at all
       if (a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = fmaf(n[i], c[i], n[i ^ 1] * s[i]);
+        for (int i = 0; i < 4; ++i)
+          o[i] = rotated ? make_float2(x[i].y, x[i].x) : x[i];
       } else {
+        Chunk<T, VEC> from;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_sync(0xffffffffu, n[i], src_lane);
-          y[i] = fmaf(n[i], c[i], o * s[i]);
-        }
+        for (int i = 0; i < (int)sizeof(ch.raw) / 4; ++i)
+          reinterpret_cast<uint32_t *>(from.raw)[i] = __shfl_sync(
+              0xffffffffu, reinterpret_cast<const uint32_t *>(ch.raw)[i],
+              src_lane);
+        from.get(o);
       }
     } else {
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) buf[e0 + i] = n[i];
+      for (int i = 0; i < 4; ++i)
+        buf[e0 + 2 * i] = x[i].x, buf[e0 + 2 * i + 1] = x[i].y;
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = e0 + i < a.D ? buf[partner(a, e0 + i)] : 0.f;
-        y[i] = fmaf(n[i], c[i], o * s[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + 2 * i;  // past D: the lane's own (zero)
+        o[i].x = e < a.D ? buf[partner(a, e)] : 0.f;
+        o[i].y = e + 1 < a.D ? buf[partner(a, e + 1)] : 0.f;
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      y[i] = __ffma2_rn(x[i], c[i], __fmul2_rn(o[i], s[i]));
   }
 };
+
+// Sum of squares of a lane's elements.
+__device__ __forceinline__ float squares(const float2 (&x)[4]) {
+  float2 t = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) t = __ffma2_rn(x[i], x[i], t);
+  return t.x + t.y;
+}
 
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
@@ -220,162 +288,231 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// A lane's 8 weights (ones without).
 __device__ __forceinline__ void load_w(const float *w, int e0, int D,
-                                       float (&x)[8]) {
+                                       float2 (&x)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = e0 + i < D ? __ldg(w + e0 + i) : 0.f;
+  for (int i = 0; i < 4; ++i) {
+    x[i] = make_float2(1.f, 1.f);
+    if (w && e0 + 2 * i < D) x[i].x = __ldg(w + e0 + 2 * i);
+    if (w && e0 + 2 * i + 1 < D) x[i].y = __ldg(w + e0 + 2 * i + 1);
+  }
+}
+
+// Row groups whose loads a warp has in flight.
+constexpr int kBatch = 4;
+
+// A warp's share of one token: heads [h0, h1) of the row set `r`.
+// KIND 0: queries, 1: keys, 2: values (copied).  `dst0`: the token's first
+// head in the output, heads `dh` elements apart; nullptr: not written.
+template <typename T, bool VEC, int LPR, int KIND>
+__device__ __forceinline__ void rope_heads(const RopeArgs &a,
+                                           const RopeRows &r, const T *src0,
+                                           T *dst0, long long dh, int h0,
+                                           int h1, int lane, int sub, int e0,
+                                           const float2 *cs, float *buf) {
+  constexpr int RPW = 32 / LPR;
+  if (h0 >= h1) return;
+  const bool norm = KIND < 2 && r.w != nullptr;
+  Turn<T, VEC> turn;
+  if (KIND < 2) turn.set(a, e0, lane, cs, r.w, false);
+  const float over_d = 1.f / a.D;
+  for (int hb = h0; hb < h1; hb += kBatch * RPW) {
+    Chunk<T, VEC> x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = hb + u * RPW + sub;
+      x[u].load(src0 + h * r.sh, e0, h < h1 ? a.D : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int h = hb + u * RPW + sub;
+      if (hb + u * RPW >= h1) break;
+      if constexpr (KIND < 2) {
+        float2 n[4], y[4];
+        x[u].get(n);
+        turn.apply(a, x[u], n, y, e0, buf);
+        if (norm) {
+          const float r2 =
+              rsqrtf(row_sum<LPR>(squares(n)) * over_d + a.eps);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            y[i] = __fmul2_rn(y[i], make_float2(r2, r2));
+        }
+        x[u].set(y);
+      }
+      if (h < h1 && dst0) x[u].store(dst0 + h * dh, e0, a.D);
+    }
+  }
 }
 
 // PAGED: k and v rows go to the cache; without it there is no v.
 template <typename T, bool VEC, int LPR, bool PAGED>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
     norm_rope_kernel(const RopeArgs a) {
   constexpr int RPW = 32 / LPR;
-  __shared__ float xch[VEC ? 1 : kRopeWarps * RPW * LPR * 8];
+  __shared__ __align__(16) float xch[VEC ? 1 : kRopeWarps * RPW * LPR * 8];
+  __shared__ unsigned long long fr[kRopeMaxD / 2];
+  __shared__ float2 cs[kRopeWarps][kRopeMaxD / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, e0 = (lane % LPR) * 8;
   float *buf = VEC ? xch : xch + (warp * RPW + sub) * LPR * 8;
-  const long long item = (long long)blockIdx.x * kRopeWarps + warp;
-  const long long tok = item / a.chunks;
-  if (tok >= (long long)a.S * a.B) return;
-  const int s = (int)(tok / a.B), b = (int)(tok % a.B);
-  const int heads = a.q.heads + a.k.heads + a.v.heads;
-  const int h0 = (int)(item % a.chunks) * a.heads_per_item;
-  const int h1 = min(heads, h0 + a.heads_per_item);
-  const int pos = a.pos ? __ldg(a.pos + tok) : s;
-  long long slot_k = 0, slot_v = 0;
-  bool keep = true;
-  if constexpr (PAGED) {
-    keep = pos >= 0;
-    if (keep) {
-      const int pg = pos / a.page_size;
-      const int page =
-          pg < a.max_pages ? __ldg(a.table + (long long)b * a.max_pages + pg)
-                           : -1;
-      if (page < 0 || page >= a.num_pages) {
-        keep = false;
-        if (lane == 0) atomicOr(a.status, kStatusIndexRange);
-      } else {
-        const long long off = pos - pg * a.page_size;
-        slot_k = page * a.k.ps + off * a.k.ts;
-        slot_v = page * a.v.ps + off * a.v.ts;
+  // below 2^31: only few tokens are cut into chunks
+  const unsigned items = (unsigned)a.S * a.B * a.chunks;
+  const int nq = a.q.heads, nk = a.k.heads, nv = a.v.heads;
+  load_freqs(a, fr);
+  __syncthreads();
+  for (unsigned item = blockIdx.x * kRopeWarps + warp; item < items;
+       item += gridDim.x * kRopeWarps) {
+    const unsigned tk = item / (unsigned)a.chunks;
+    const long long tok = tk;
+    const int s = (int)(tk / (unsigned)a.B), b = (int)(tk % (unsigned)a.B);
+    const int h0 = (int)(item % (unsigned)a.chunks) * a.heads_per_item;
+    const int h1 = h0 + a.heads_per_item;
+    const int pos = a.pos ? __ldg(a.pos + tok) : s;
+    T *k_dst = nullptr, *v_dst = nullptr;
+    if constexpr (PAGED) {
+      if (pos >= 0) {
+        const int pg = pos / a.page_size;
+        const int page =
+            pg < a.max_pages ? __ldg(a.table + (long long)b * a.max_pages + pg)
+                             : -1;
+        if (page < 0 || page >= a.num_pages) {
+          if (lane == 0) atomicOr(a.status, kStatusIndexRange);
+        } else {
+          const long long off = pos - pg * a.page_size;
+          k_dst = static_cast<T *>(a.k.out) + page * a.k.ps + off * a.k.ts;
+          v_dst = static_cast<T *>(a.v.out) + page * a.v.ps + off * a.v.ts;
+        }
       }
+    } else {
+      k_dst = static_cast<T *>(a.k.out) + tok * nk * (long long)a.D;
     }
-  }
-  Turn<VEC> turn;
-  turn.setup(a, e0, lane);
-  turn.at(a, e0, pos, false);
-  for (int h = h0; h < h1; h += RPW) {
-    const int hh = h + sub;
-    const bool live = hh < h1;
-    const int kind = hh < a.q.heads ? 0 : hh < a.q.heads + a.k.heads ? 1 : 2;
-    const RopeRows &r = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const int hr = kind == 0   ? hh
-                   : kind == 1 ? hh - a.q.heads
-                               : hh - a.q.heads - a.k.heads;
-    Chunk<T, VEC> x;
-    const T *src =
-        static_cast<const T *>(r.in) + s * r.ss + b * r.sb + hr * r.sh;
-    x.load(src, e0, live ? a.D : 0);
-    float n[8], y[8];
-    x.get(n);
-    float ms = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ms = fmaf(n[i], n[i], ms);
-    ms = row_sum<LPR>(ms);
-    if (r.w) {
-      float w[8];
-      load_w(r.w, e0, a.D, w);
-      const float rstd = rsqrtf(ms / a.D + a.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) n[i] *= rstd * w[i];
+    token_turns(a, pos, lane, fr, cs[warp]);
+    auto src = [&](const RopeRows &r) {
+      return static_cast<const T *>(r.in) + s * r.ss + b * r.sb;
+    };
+    rope_heads<T, VEC, LPR, 0>(
+        a, a.q, src(a.q), static_cast<T *>(a.q.out) + tok * nq * (long long)a.D,
+        a.D, min(h0, nq), min(h1, nq), lane, sub, e0, cs[warp], buf);
+    const int k0 = max(h0 - nq, 0), k1 = min(h1 - nq, nk);
+    if (!PAGED || k_dst)
+      rope_heads<T, VEC, LPR, 1>(a, a.k, src(a.k), k_dst, PAGED ? a.k.hs : a.D,
+                                 k0, k1, lane, sub, e0, cs[warp], buf);
+    if constexpr (PAGED) {
+      if (v_dst)
+        rope_heads<T, VEC, LPR, 2>(a, a.v, src(a.v), v_dst, a.v.hs,
+                                   max(h0 - nq - nk, 0),
+                                   min(h1 - nq - nk, nv), lane, sub, e0, cs[warp], buf);
     }
-    turn.apply(a, n, y, e0, buf);
-    if (kind < 2) x.set(y);
-    T *dst;
-    if (PAGED && kind > 0)
-      dst = static_cast<T *>(r.out) + (kind == 1 ? slot_k : slot_v) +
-            hr * r.hs;
-    else
-      dst = static_cast<T *>(r.out) +
-            (tok * r.heads + hr) * (long long)a.D;
-    if (live && (keep || kind == 0)) x.store(dst, e0, a.D);
   }
 }
 
 // Backward.  With u = the output's gradient rotated back (times m), xh = x
-// rstd:  dw += u xh;  g = u w;  dx = rstd (g - xh mean(g xh)).
+// rstd:  dw += u xh;  g = u w;  dx = rstd (g - xh mean(g xh)); without a
+// weight there is no norm either: dx = u.
 template <typename T, bool VEC, int LPR>
-__global__ void __launch_bounds__(kRopeThreads)
+__device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
+                                               const RopeRows &r,
+                                               const T *src0, long long at0,
+                                               int h0, int h1, int lane,
+                                               int sub, int e0,
+                                               const float2 *cs, float *buf,
+                                               float2 (&dw)[4]) {
+  constexpr int RPW = 32 / LPR, U = kBatch / 2;
+  if (h0 >= h1) return;
+  const bool norm = r.w != nullptr;
+  const T *gin = static_cast<const T *>(r.gin) + at0;
+  T *out = static_cast<T *>(r.out) + at0;
+  float2 w[4];
+  load_w(r.w, e0, a.D, w);
+  Turn<T, VEC> turn;
+  turn.set(a, e0, lane, cs, nullptr, true);
+  const float over_d = 1.f / a.D;
+  for (int hb = h0; hb < h1; hb += U * RPW) {
+    Chunk<T, VEC> x[U], g[U];
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const int h = hb + v * RPW + sub;
+      g[v].load(gin + (long long)h * a.D, e0, h < h1 ? a.D : 0);
+      x[v].load(src0 + h * r.sh, e0, norm && h < h1 ? a.D : 0);
+    }
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const int h = hb + v * RPW + sub;
+      if (hb + v * RPW >= h1) break;
+      float2 u[4], y[4];
+      g[v].get(y);
+      turn.apply(a, g[v], y, u, e0, buf);
+      if (norm) {
+        float2 xh[4], gw[4];
+        x[v].get(xh);
+        float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          gw[i] = __fmul2_rn(u[i], w[i]);
+          dot = __ffma2_rn(gw[i], xh[i], dot);
+        }
+        const float rstd =
+            rsqrtf(row_sum<LPR>(squares(xh)) * over_d + a.eps);
+        // mean(g xh)
+        const float back = row_sum<LPR>(dot.x + dot.y) * rstd * over_d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          xh[i] = __fmul2_rn(xh[i], make_float2(rstd, rstd));
+          dw[i] = __ffma2_rn(u[i], xh[i], dw[i]);
+          u[i] = __fmul2_rn(
+              make_float2(rstd, rstd),
+              __ffma2_rn(xh[i], make_float2(-back, -back), gw[i]));
+        }
+      }
+      g[v].set(u);
+      if (h < h1) g[v].store(out + (long long)h * a.D, e0, a.D);
+    }
+  }
+}
+
+template <typename T, bool VEC, int LPR>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
     norm_rope_bwd_kernel(const RopeArgs a) {
   constexpr int RPW = 32 / LPR;
-  __shared__ float xch[kRopeWarps * RPW * LPR * 8];
+  __shared__ __align__(16) float xch[kRopeWarps * RPW * LPR * 8];
+  __shared__ unsigned long long fr[kRopeMaxD / 2];
+  __shared__ float2 cs[kRopeWarps][kRopeMaxD / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, e0 = (lane % LPR) * 8;
   float *buf = xch + (warp * RPW + sub) * LPR * 8;
-  const long long items = (long long)a.S * a.B * a.chunks;
-  const int heads = a.q.heads + a.k.heads;
-  float dw[2][8] = {};
-  Turn<VEC> turn;
-  turn.setup(a, e0, lane);
-  for (long long item = (long long)blockIdx.x * kRopeWarps + warp;
-       item < items; item += (long long)gridDim.x * kRopeWarps) {
-    const long long tok = item / a.chunks;
-    const int s = (int)(tok / a.B), b = (int)(tok % a.B);
-    const int h0 = (int)(item % a.chunks) * a.heads_per_item;
-    const int h1 = min(heads, h0 + a.heads_per_item);
-    turn.at(a, e0, a.pos ? __ldg(a.pos + tok) : s, true);
-    for (int h = h0; h < h1; h += RPW) {
-      const int hh = h + sub;
-      const bool live = hh < h1;
-      const int kind = hh < a.q.heads ? 0 : 1;
-      const RopeRows &r = kind == 0 ? a.q : a.k;
-      const int hr = kind == 0 ? hh : hh - a.q.heads;
-      Chunk<T, VEC> g;
-      const long long at = (tok * r.heads + hr) * (long long)a.D;
-      g.load(static_cast<const T *>(r.gin) + at, e0, live ? a.D : 0);
-      float u[8], y[8];
-      g.get(y);
-      turn.apply(a, y, u, e0, buf);
-      // without a weight there is no norm either: dx = u.  The sums run in
-      // every lane, as neighbouring rows of a warp may be of both kinds.
-      const bool norm = r.w != nullptr;
-      Chunk<T, VEC> x;
-      x.load(static_cast<const T *>(r.in) + s * r.ss + b * r.sb + hr * r.sh,
-             e0, live && norm ? a.D : 0);
-      float xh[8], w[8] = {};
-      x.get(xh);
-      if (norm) load_w(r.w, e0, a.D, w);
-      float ms = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        ms = fmaf(xh[i], xh[i], ms);
-        dot = fmaf(u[i] * w[i], xh[i], dot);
-      }
-      ms = row_sum<LPR>(ms);
-      dot = row_sum<LPR>(dot);
-      if (norm) {
-        const float rstd = rsqrtf(ms / a.D + a.eps);
-        const float back = dot * rstd / a.D;  // mean(g xh)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xh[i] *= rstd;
-          const float d = u[i] * xh[i];
-          dw[0][i] += kind == 0 ? d : 0.f;
-          dw[1][i] += kind == 0 ? 0.f : d;
-          u[i] = rstd * fmaf(-xh[i], back, u[i] * w[i]);
-        }
-      }
-      g.set(u);
-      if (live) g.store(static_cast<T *>(r.out) + at, e0, a.D);
-    }
+  // below 2^31: only few tokens are cut into chunks
+  const unsigned items = (unsigned)a.S * a.B * a.chunks;
+  const int nq = a.q.heads, nk = a.k.heads;
+  load_freqs(a, fr);
+  __syncthreads();
+  float2 dw[2][4] = {};
+  for (unsigned item = blockIdx.x * kRopeWarps + warp; item < items;
+       item += gridDim.x * kRopeWarps) {
+    const unsigned tk = item / (unsigned)a.chunks;
+    const long long tok = tk;
+    const int s = (int)(tk / (unsigned)a.B), b = (int)(tk % (unsigned)a.B);
+    const int h0 = (int)(item % (unsigned)a.chunks) * a.heads_per_item;
+    const int h1 = h0 + a.heads_per_item;
+    token_turns(a, a.pos ? __ldg(a.pos + tok) : s, lane, fr, cs[warp]);
+    auto src = [&](const RopeRows &r) {
+      return static_cast<const T *>(r.in) + s * r.ss + b * r.sb;
+    };
+    rope_heads_bwd<T, VEC, LPR>(a, a.q, src(a.q), tok * nq * (long long)a.D,
+                                min(h0, nq), min(h1, nq), lane, sub, e0, cs[warp], buf,
+                                dw[0]);
+    rope_heads_bwd<T, VEC, LPR>(a, a.k, src(a.k), tok * nk * (long long)a.D,
+                                max(h0 - nq, 0), min(h1 - nq, nk), lane, sub,
+                                e0, cs[warp], buf, dw[1]);
   }
   // this CTA's weight gradients, summed over its rows in a fixed order
   for (int kind = 0; kind < 2; ++kind) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      xch[(warp * RPW + sub) * LPR * 8 + e0 + i] = dw[kind][i];
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<float2 *>(xch)[((warp * RPW + sub) * LPR * 8 + e0) / 2 +
+                                      i] = dw[kind][i];
     __syncthreads();
     for (int e = threadIdx.x; e < a.D; e += kRopeThreads) {
       float t = 0.f;
@@ -385,21 +522,26 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
 }
 
-// Sums the CTAs' partial weight gradients; one warp per 32 columns.
-__global__ void rope_dw_kernel(const float *partial, int ctas, int D,
-                               float *gwq, float *gwk) {
-  __shared__ float part[8][32];
-  const int e = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
-  const int kind = blockIdx.y;
+// Sums the CTAs' partial weight gradients: a CTA takes 32 columns, each warp
+// every 32nd part.
+__global__ void __launch_bounds__(1024)
+    rope_dw_kernel(const float *partial, int ctas, int D, float *gwq,
+                   float *gwk) {
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane, kind = blockIdx.y;
   float *out = kind == 0 ? gwq : gwk;
   float t = 0.f;
-  if (e < D)
-    for (int c = g; c < ctas; c += 8)
+  if (e < D) {
+#pragma unroll 4
+    for (int c = g; c < ctas; c += 32)
       t += partial[((size_t)c * 2 + kind) * D + e];
-  part[g][threadIdx.x & 31] = t;
+  }
+  part[g][lane] = t;
   __syncthreads();
   if (g == 0 && e < D && out) {
-    for (int i = 1; i < 8; ++i) t += part[i][threadIdx.x & 31];
+    t = 0.f;
+    for (int i = 0; i < 32; ++i) t += part[i][lane];
     out[e] = t;
   }
 }
@@ -437,18 +579,19 @@ cudaError_t launch_lpr(RopeArgs &a, int mode, int num_sms, int *ctas,
   a.chunks = (heads + per - 1) / per;
   const long long items = toks * a.chunks;
   const long long grid = (items + kRopeWarps - 1) / kRopeWarps;
-  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  long long most = (long long)num_sms *
+                   (mode == kModeBwd ? kRopeBwdCtas : rope_ctas(sizeof(T), VEC));
+  if (most > kRopeMaxCtas) most = kRopeMaxCtas;
+  *ctas = (int)(grid < most ? grid : most);
   if (mode == kModeBwd) {
-    const long long most = 8ll * num_sms < kRopeBwdMaxCtas ? 8ll * num_sms
-                                                           : kRopeBwdMaxCtas;
-    *ctas = (int)(grid < most ? grid : most);
     norm_rope_bwd_kernel<T, VEC, LPR><<<*ctas, kRopeThreads, 0, st>>>(a);
   } else if (mode == kModeAppend) {
-    norm_rope_kernel<T, VEC, LPR, true>
-        <<<(int)grid, kRopeThreads, 0, st>>>(a);
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      norm_rope_kernel<T, VEC, LPR, true>
+          <<<*ctas, kRopeThreads, 0, st>>>(a);
   } else {
     norm_rope_kernel<T, VEC, LPR, false>
-        <<<(int)grid, kRopeThreads, 0, st>>>(a);
+        <<<*ctas, kRopeThreads, 0, st>>>(a);
   }
   return cudaGetLastError();
 }
@@ -464,7 +607,6 @@ cudaError_t launch_rope(RopeArgs &a, int mode, int num_sms, int *ctas,
                    vec_rows(a.v, el, paged);
   const int ch = (a.D + 7) / 8;
   if (vec) {
-    if (ch <= 4) return launch_lpr<T, true, 4>(a, mode, num_sms, ctas, st);
     if (ch <= 8) return launch_lpr<T, true, 8>(a, mode, num_sms, ctas, st);
     if (ch <= 16) return launch_lpr<T, true, 16>(a, mode, num_sms, ctas, st);
     return launch_lpr<T, true, 32>(a, mode, num_sms, ctas, st);
@@ -509,14 +651,18 @@ int check_rope(const RopeArgs &a, int dtype) {
   return DSA_OK;
 }
 
-// strides: 3 element strides (s, b, head), or nullptr for dense.
-void set_in(RopeRows &r, const void *in, const int64_t *strides, int B,
+// strides: 3 element strides (s, b, head), or nullptr for dense; that of a
+// dimension of one element counts for nothing.
+void set_in(RopeRows &r, const void *in, const int64_t *strides, int S, int B,
             int heads, int D) {
   r.in = in;
   r.heads = in ? heads : 0;
   r.ss = strides ? strides[0] : (long long)B * heads * D;
   r.sb = strides ? strides[1] : (long long)heads * D;
   r.sh = strides ? strides[2] : D;
+  if (S == 1) r.ss = 0;
+  if (B == 1) r.sb = 0;
+  if (heads == 1) r.sh = 0;
 }
 
 }  // namespace
@@ -534,8 +680,8 @@ int dsa_norm_rope_fwd(const void *q, const int64_t *q_strides, const void *k,
   if (!q || !out_q || H <= 0) return DSA_ERR_INVALID_ARG;
   if (k && (!out_k || Hk <= 0)) return DSA_ERR_INVALID_ARG;
   dsa::RopeArgs a{};
-  dsa::set_in(a.q, q, q_strides, B, H, D);
-  dsa::set_in(a.k, k, k_strides, B, Hk, D);
+  dsa::set_in(a.q, q, q_strides, S, B, H, D);
+  dsa::set_in(a.k, k, k_strides, S, B, Hk, D);
   a.q.out = out_q;
   a.k.out = out_k;
   a.q.w = wq;
@@ -557,7 +703,7 @@ int dsa_norm_rope_fwd(const void *q, const int64_t *q_strides, const void *k,
 
 size_t dsa_norm_rope_bwd_workspace_size(int D) {
   if (D <= 0 || D > dsa::kRopeMaxD) return 0;
-  return (size_t)dsa::kRopeBwdMaxCtas * 2 * D * sizeof(float);
+  return (size_t)dsa::kRopeMaxCtas * 2 * D * sizeof(float);
 }
 
 int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides, const void *k,
@@ -574,8 +720,8 @@ int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides, const void *k,
   if (k && (!grad_out_k || !grad_k || Hk <= 0)) return DSA_ERR_INVALID_ARG;
   if ((wq && !grad_wq) || (k && wk && !grad_wk)) return DSA_ERR_INVALID_ARG;
   dsa::RopeArgs a{};
-  dsa::set_in(a.q, q, q_strides, B, H, D);
-  dsa::set_in(a.k, k, k_strides, B, Hk, D);
+  dsa::set_in(a.q, q, q_strides, S, B, H, D);
+  dsa::set_in(a.k, k, k_strides, S, B, Hk, D);
   a.q.gin = grad_out_q;
   a.k.gin = grad_out_k;
   a.q.out = grad_q;
@@ -601,7 +747,7 @@ int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides, const void *k,
       cudaSuccess)
     return DSA_ERR_CUDA;
   if (a.q.w || a.k.w) {
-    dsa::rope_dw_kernel<<<dim3((D + 31) / 32, 2), 256, 0, st>>>(
+    dsa::rope_dw_kernel<<<dim3((D + 31) / 32, 2), 1024, 0, st>>>(
         a.partial, ctas, D, a.q.w ? grad_wq : nullptr,
         a.k.w ? grad_wk : nullptr);
     if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
@@ -627,9 +773,9 @@ int dsa_paged_append(const void *k, const int64_t *k_strides, const void *v,
   if (num_pages <= 0 || page_size <= 0 || max_pages <= 0)
     return DSA_ERR_INVALID_ARG;
   dsa::RopeArgs a{};
-  dsa::set_in(a.q, q, q_strides, B, H, D);
-  dsa::set_in(a.k, k, k_strides, B, Hk, D);
-  dsa::set_in(a.v, v, v_strides, B, Hk, D);
+  dsa::set_in(a.q, q, q_strides, S, B, H, D);
+  dsa::set_in(a.k, k, k_strides, S, B, Hk, D);
+  dsa::set_in(a.v, v, v_strides, S, B, Hk, D);
   a.q.out = out_q;
   a.k.out = k_cache;
   a.v.out = v_cache;
@@ -639,6 +785,9 @@ int dsa_paged_append(const void *k, const int64_t *k_strides, const void *v,
     r.ps = cs ? cs[0] : (long long)page_size * Hk * D;
     r.ts = cs ? cs[1] : (long long)Hk * D;
     r.hs = cs ? cs[2] : D;
+    if (num_pages == 1) r.ps = 0;
+    if (page_size == 1) r.ts = 0;
+    if (Hk == 1) r.hs = 0;
   }
   a.q.w = wq;
   a.k.w = wk;
