@@ -14,18 +14,22 @@
 //   S = Q K^T on the tensor cores (128 x 128, fp32 in tensor memory); each
 // softmax thread owns a row: maximum, moved only when a step exceeds it by
 // more than 2^8 (then O is rescaled), P = exp2(S c - m) rounded to bf16 into
-// the columns of S it has read; O += P V with P from tensor memory.
+// columns of S that are done; O += P V with P from tensor memory.  A row holds
+// 16 neighbouring keys or none of them, so its mask is a choice of m or +inf
+// for each 16; only steps with keys after some row's position look at single
+// keys.
 //   One stage of K and V (96 KB with Q at D = 128) and 256 tensor-memory
 // columns let two CTAs share an SM: one's products run under the other's
 // softmax, and its next K arrives while its own softmax and second product
 // run.  Few rows (single tokens) are split over their blocks, and a second
 // kernel joins the parts.
 //
-// Masked keys: their scores are replaced before use; a V row that no row of
+// Masked keys: a score that is not finite in a key that only other rows hold
+// spoils the row's sum, see below; a V row that no row of
 // the tile sees is zeroed in shared memory (a page's unwritten end may hold
 // anything).  A V row that some rows see meets a zero weight in the others,
-// which a NaN or an infinity survives: rows with a result that is not finite
-// are computed again on their own (block_attn_row.cuh).
+// which a NaN or an infinity survives: rows with a sum or a result that is not
+// finite are computed again on their own (block_attn_row.cuh).
 //
 // Warps: 0 .. 3 softmax (warp w reads tensor-memory lanes 32 w .. + 31), 4
 // TMA producer, 5 MMA issuer and tensor-memory allocator.
@@ -42,7 +46,7 @@ constexpr int kRows = 128;  // MMA rows of a query tile
 constexpr int kKeys = 128;  // keys of a step
 constexpr int kFwdThreads = 192;
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
-constexpr uint32_t kTmS = 0, kTmO = 128;  // tensor-memory columns; P is in S
+constexpr uint32_t kTmS = 0, kTmO = 128;  // tensor-memory columns; P: 64
 constexpr float kSlack = 8.f;
 
 // What a launch adds to the problem.
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     if (lane == 0) *sCount = n;
   }
   __syncthreads();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   const int bpt = kKeys / p.blk;  // blocks of a step
   const int all = (*sCount + bpt - 1) / bpt;
   const int t0 = (int)((long long)all * split / pl.splits);
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t full = kv ? v_full : k_full;
         if (!__all_sync(0xffffffffu,
-                        wait_bar_inl(kv ? v_empty : k_empty, ph ^ 1u,
+                        wait_bar_spin(kv ? v_empty : k_empty, ph ^ 1u,
                                      abort_flag, p.status)))
           goto done;
         if (lane == 0) mbar_arrive_expect_tx(full, nb * p.blk * CH * 128);
@@ -195,36 +199,38 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       }
     }
   } else if (warp == kMmaWarp) {
-    // ---------------- MMA issuer ----------------
-    const uint32_t lead = lane == 0;
-    auto wall = [&](uint32_t bar, uint32_t ph) -> bool {
-      return __all_sync(0xffffffffu,
-                        wait_bar_inl(bar, ph, abort_flag, p.status));
-    };
-    const uint64_t qd = sdesc_k_sw128(sQ), kd = sdesc_k_sw128(sK);
-    const uint64_t vd = sdesc_mn_sw128(sV, kRows * 128, 1024);
-    if (t1 > t0 && !wall(q_full, 0)) goto done;
-    for (int t = t0; t < t1; ++t) {
-      const uint32_t ph = (t - t0) & 1u;
-      if (!wall(k_full, ph)) goto done;
-      tc_fence_after();
+    // ---------------- MMA issuer: one thread ----------------
+    if (elect_one()) {
+      auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
+        return wait_bar_spin(bar, ph, abort_flag, p.status);
+      };
+      const uint64_t qd = sdesc_k_sw128(sQ), kd = sdesc_k_sw128(sK);
+      const uint64_t vd = sdesc_mn_sw128(sV, kRows * 128, 1024);
+      bool ok = t1 <= t0 || wait(q_full, 0);
+      uint32_t ph = 0, acc = 0;
+      for (int t = t0; ok && t < t1; ++t) {
+        if (!(ok = wait(k_full, ph))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t o = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
-        mma_bf16_by(tmem + kTmS, qd + o, kd + o, kIdescS, ks != 0, lead);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t o = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+          mma_bf16(tmem + kTmS, qd + o, kd + o, kIdescS, ks != 0);
+        }
+        mma_commit(k_empty);
+        mma_commit(s_full);
+        if (!(ok = wait(v_full, ph) && wait(p_full, ph))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_bf16_ta(tmem + kTmO, tmem + kTmS + 64 + ks * 8,
+                      vd + ((ks * 2048) >> 4), kIdescO, ks == 0 ? acc : 1u);
+        mma_commit(v_empty);
+        if (t + 1 == t1) mma_commit(o_full);
+        acc = 1;
+        ph ^= 1;
       }
-      mma_commit_by(k_empty, lead);
-      mma_commit_by(s_full, lead);
-      if (!wall(v_full, ph) || !wall(p_full, ph)) goto done;
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks)
-        mma_bf16_ta_by(tmem + kTmO, tmem + kTmS + ks * 8,
-                       vd + ((ks * 2048) >> 4), kIdescO,
-                       (t > t0 || ks != 0) ? 1u : 0u, lead);
-      mma_commit_by(v_empty, lead);
-      if (t + 1 == t1) mma_commit_by(o_full, lead);
     }
+    __syncwarp();
   } else {
     // ---------------- softmax: one row a thread ----------------
     const int row = tid;
@@ -237,39 +243,72 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // the last key that any row of the tile sees, and its block
     const long long pos_hi =
         min(row_pos(p.q_pos, b, s0 + nq - 1), (long long)p.T - 1);
+    const long long pos_lo =
+        min(row_pos(p.q_pos, b, s0), (long long)p.T - 1);
     const float c2 = p.scale * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + kTmS + lane_off, tO = tmem + kTmO + lane_off;
-    float m = neg_inf, l = 0.f;
+    float m = neg_inf;
+    float2 l2[2] = {};
     for (int t = t0; t < t1; ++t) {
       const uint32_t ph = (t - t0) & 1u;
-      uint32_t mask[4];
+      uint32_t mask[4], held = 0u;
+      bool diag[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c) {
         mask[c] = live ? tile_mask(words, list, t * bpt, count, p.blk, c, qi,
                                    pos)
                        : 0u;
+        diag[c] = tile_end(list, t * bpt, count, p.blk, c) > pos_lo;
+        if (__any_sync(0xffffffffu, mask[c] != 0u)) held |= 1u << c;
+      }
       if (!__all_sync(0xffffffffu,
-                      wait_bar_inl(s_full, ph, abort_flag, p.status)))
+                      wait_bar_spin(s_full, ph, abort_flag, p.status)))
         goto done;
       tc_fence_after();
+      // Pass 1: the row's maximum, two chunks of 32 keys at a time; the
+      // second two stay in registers.
+      uint32_t u[2][32];
       float mx = neg_inf;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (__all_sync(0xffffffffu, mask[c] == 0u)) continue;
-        uint32_t u[32];
+      auto fetch = [&](int c, uint32_t(&x)[32]) {
         __syncwarp();
-        tmem_ld32(tS + c * 32, u);
-        tmem_ld_wait();
-        reg_fence32(u);
-        if (__all_sync(0xffffffffu, mask[c] == 0xffffffffu)) {
+        tmem_ld32(tS + c * 32, x);
+      };
+      // keys after some row's position: one by one
+      auto hide = [&](int c, uint32_t(&x)[32]) {
+        if (!diag[c]) return;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(u[i]));
-        } else {
+        for (int i = 0; i < 32; ++i)
+          x[i] = mask[c] >> i & 1u ? x[i] : 0xff800000u;
+      };
+      auto chunk_max = [&](int c, const uint32_t(&x)[32]) {
+        float a[2] = {neg_inf, neg_inf};
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            mx = fmaxf(mx, mask[c] >> i & 1u ? __uint_as_float(u[i])
-                                             : neg_inf);
+        for (int h = 0; h < 2; ++h) {
+          float e = neg_inf;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            a[h] = fmaxf(a[h], fmaxf(__uint_as_float(x[16 * h + i]),
+                                     __uint_as_float(x[16 * h + i + 1])));
+            e = fmaxf(e, fmaxf(__uint_as_float(x[16 * h + i + 2]),
+                               __uint_as_float(x[16 * h + i + 3])));
+          }
+          // a row holds all 16 keys or none, or they are hidden above
+          if (mask[c] & (0xffffu << (16 * h))) mx = fmaxf(mx, fmaxf(a[h], e));
+        }
+      };
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        if (held & (3u << c)) {
+          fetch(c, u[0]);
+          fetch(c + 1, u[1]);
+          tmem_ld_wait();
+          reg_fence32(u[0]);
+          reg_fence32(u[1]);
+          hide(c, u[0]);
+          hide(c + 1, u[1]);
+          chunk_max(c, u[0]);
+          chunk_max(c + 1, u[1]);
         }
       }
       mx *= c2;
@@ -277,50 +316,66 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const bool move = mx > m + kSlack;
       if (__any_sync(0xffffffffu, move && t > t0)) {
         const float f = move ? ex2(m - mx) : 1.f;
-        l *= f;
+        l2[0] = __fmul2_rn(l2[0], make_float2(f, f));
+        l2[1] = __fmul2_rn(l2[1], make_float2(f, f));
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
-          uint32_t u[32];
+          uint32_t w[32];
           __syncwarp();
-          tmem_ld32(tO + c * 32, u);
+          tmem_ld32(tO + c * 32, w);
           tmem_ld_wait();
-          reg_fence32(u);
+          reg_fence32(w);
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
-          tmem_st32(tO + c * 32, u);
+            w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
+          tmem_st32(tO + c * 32, w);
         }
       }
       if (move) m = mx;
       const float mu = m > neg_inf ? m : 0.f;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      // Pass 2: P = exp2(S c2 - mu), chunks 3, 2 from registers, then 1, 0;
+      // P's columns begin at 64, in chunks that are done.
+      auto weights = [&](int c, const uint32_t(&x)[32]) {
         uint32_t pk[16];
-        if (__all_sync(0xffffffffu, mask[c] == 0u)) {
+        if (held >> c & 1u) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            // -inf takes the weights of keys that the row does not hold to 0
+            const float sub = mask[c] & (0xffffu << (16 * h)) ? -mu : neg_inf;
+#pragma unroll
+            for (int i = 16 * h; i < 16 * h + 16; i += 2) {
+              float2 e = __ffma2_rn(
+                  make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
+                  make_float2(c2, c2), make_float2(sub, sub));
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              l2[(i >> 1) & 1] = __fadd2_rn(l2[(i >> 1) & 1], e);
+              pk[i >> 1] = pack_bf16x2(e.x, e.y);
+            }
+          }
+        } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = 0u;
-        } else {
-          uint32_t u[32];
-          __syncwarp();
-          tmem_ld32(tS + c * 32, u);
-          tmem_ld_wait();
-          reg_fence32(u);
-          const bool full = __all_sync(0xffffffffu, mask[c] == 0xffffffffu);
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float e0 = ex2(fmaf(__uint_as_float(u[i]), c2, -mu));
-            float e1 = ex2(fmaf(__uint_as_float(u[i + 1]), c2, -mu));
-            if (!full) {
-              e0 = mask[c] >> i & 1u ? e0 : 0.f;
-              e1 = mask[c] >> (i + 1) & 1u ? e1 : 0.f;
-            }
-            l += e0 + e1;
-            pk[i >> 1] = pack_bf16x2(e0, e1);
-          }
         }
         __syncwarp();
-        tmem_st16(tS + c * 16, pk);
+        tmem_st16(tS + 64 + c * 16, pk);
+      };
+      weights(3, u[1]);
+      if (held & 2u) fetch(1, u[1]);
+      weights(2, u[0]);
+      if (held & 2u) {
+        tmem_ld_wait();
+        reg_fence32(u[1]);
+        hide(1, u[1]);
       }
+      if (held & 1u) fetch(0, u[0]);
+      weights(1, u[1]);
+      if (held & 1u) {
+        tmem_ld_wait();
+        reg_fence32(u[0]);
+        hide(0, u[0]);
+      }
+      weights(0, u[0]);
       tmem_st_wait();
       tc_fence_before();
       // V rows of this step that no row sees
@@ -330,7 +385,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             i < count && (long long)list[i] * p.blk + row % p.blk > pos_hi;
         if (__any_sync(0xffffffffu, over)) {
           if (!__all_sync(0xffffffffu,
-                          wait_bar_inl(v_full, ph, abort_flag, p.status)))
+                          wait_bar_spin(v_full, ph, abort_flag, p.status)))
             goto done;
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
           if (over)
@@ -347,10 +402,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // ---------------- o = O / l ----------------
     if (t1 > t0) {
       if (!__all_sync(0xffffffffu,
-                      wait_bar_inl(o_full, 0, abort_flag, p.status)))
+                      wait_bar_spin(o_full, 0, abort_flag, p.status)))
         goto done;
       tc_fence_after();
     }
+    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const bool some = l > 0.f || l != l;
     const float inv = some ? 1.f / l : 0.f;
     bool odd = l != l || l > 3e38f;  // not finite: computed again below
@@ -428,6 +484,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 done:
   __syncthreads();
   if (warp == kMmaWarp) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }

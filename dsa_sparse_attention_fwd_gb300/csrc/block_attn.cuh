@@ -140,6 +140,17 @@ __device__ __forceinline__ uint32_t tile_mask(const uint32_t *words,
   return m;
 }
 
+// The last key of those 32.
+__device__ __forceinline__ long long tile_end(const uint16_t *list, int l0,
+                                              int count, int blk, int c) {
+  if (blk >= 32) {
+    const int i = l0 + c * 32 / blk;
+    return i < count ? (long long)list[i] * blk + c * 32 % blk + 31 : -1;
+  }
+  const int i = l0 + c * 2, j = i + 1 < count ? i + 1 : i;  // ascending
+  return i < count ? (long long)list[j] * 16 + 15 : -1;
+}
+
 // TMA coordinates of block n of sequence b, for a map made with
 // encode_kv_maps(): token (or slot) and sequence (or page).  A broadcast
 // sequence or head has extent 1 and coordinate 0 (bc_*).

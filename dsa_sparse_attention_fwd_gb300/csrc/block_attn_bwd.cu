@@ -18,9 +18,11 @@
 // and cuts long lists (blocks that every query holds) into chunks of a
 // quarter of an SM's share, bwd_fill_kernel writes them.  Chunks of one key
 // tile leave their sums in fp32 and bwd_join_kernel adds them in order.
-//   Both run one CTA an SM with the scores of two steps in tensor memory: one
-// warpgroup works on one step while the tensor cores run the other's
-// products.
+//   Both run one CTA an SM with the scores of two steps in tensor memory: the
+// compute warps work on one step (each of the two warpgroups on half of its
+// columns) while the tensor cores run the products of its neighbours.
+//   Masks cost no arithmetic away from the diagonal: a (row, block) that is
+// not held has a log-sum of +inf, so its weights are exp2(-inf) = 0.
 #include "block_attn.cuh"
 #include "block_attn_host.cuh"
 #include "dsa_indexer.h"
@@ -294,8 +296,10 @@ struct KvSmem {
   static constexpr int kOffV = kTile;
   static constexpr int kOffS = 2 * kTile;  // stages: Q, dO
   static constexpr int kOffStat = kOffS + kKvStages * 2 * kRow;
-  static constexpr int kOffMask = kOffStat + kKvStages * kRowTile * 8;
-  static constexpr int kOffBar = kOffMask + kKvStages * 32;
+  // a stage's log-sums for each block of the key tile, delta, query masks,
+  // and the first query's position
+  static constexpr int kStat = (8 + 1) * kRowTile * 4 + 64;
+  static constexpr int kOffBar = kOffStat + kKvStages * kStat;
   // kv_full st_full[3] st_empty[3] sdp_full[2] ds_full[2] acc_full
   static constexpr int kOffMisc = kOffBar + 12 * 8;
   static constexpr int kBytes = kOffMisc + 32 + 1024;
@@ -322,8 +326,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t sK = base + L::kOffK, sV = base + L::kOffV;
   auto sQ = [&](int st) { return base + L::kOffS + st * 2 * L::kRow; };
   auto sG = [&](int st) { return sQ(st) + L::kRow; };
-  float2 *stat = reinterpret_cast<float2 *>(smem + L::kOffStat);
-  uint32_t *masks = reinterpret_cast<uint32_t *>(smem + L::kOffMask);
+  // offsets of K step ks in the tiles of keys and of rows
+  auto koff = [](int ks) {
+    return (uint32_t)((ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32) >> 4;
+  };
+  auto roff = [](int ks) {
+    return (uint32_t)((ks >> 2) * (kRowTile * 128) + (ks & 3) * 32) >> 4;
+  };
+  auto stat = [&](int st) {
+    return reinterpret_cast<float *>(smem + L::kOffStat + st * L::kStat);
+  };
   const uint32_t bars = base + L::kOffBar;
   const uint32_t kv_full = bars, acc_full = bars + 88;
   auto st_full = [&](int i) { return bars + 8 + 8 * i; };
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sdp_full(i), 1);
-      mbar_init(ds_full(i), 4);
+      mbar_init(ds_full(i), 8);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -377,7 +389,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
 
   if (warp == kTmaWarp) {
     if (n > 0 && lane == 0) {
@@ -390,29 +402,41 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     const float inf = __int_as_float(0x7f800000);
+    const long long q0 = row_pos(p.q_pos, b, 0);
+    const int qr[2] = {lane / p.G, (lane + 32) / p.G};  // queries of two rows
+    const int hr[2] = {lane % p.G, (lane + 32) % p.G};
     for (int i = 0; i < n; ++i) {
       const int st = i % kKvStages;
       const uint32_t ph = (i / kKvStages) & 1u;
       const int s0 = (int)pl.eq[e0 + i] * pl.qt;
-      const int rows = min(pl.qt, p.S - s0) * p.G;
+      const int nq = min(pl.qt, p.S - s0);
       float2 v[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int r = lane + 32 * u;
         v[u] = make_float2(inf, 0.f);
-        if (r < rows)
-          v[u] = pl.stat[((size_t)(s0 + r / p.G) * p.B + b) * p.H + hk * p.G +
-                         r % p.G];
+        if (qr[u] < nq)
+          v[u] = pl.stat[((size_t)(s0 + qr[u]) * p.B + b) * p.H + hk * p.G +
+                         hr[u]];
       }
-      // the keys' blocks, without the queries before the key itself
       const uint32_t m =
           lane < pl.bpt ? pl.em[(size_t)(e0 + i) * pl.bpt + lane] : 0u;
-      if (!__all_sync(0xffffffffu, wait_bar_inl(st_empty(st), ph ^ 1u,
+      if (!__all_sync(0xffffffffu, wait_bar_spin(st_empty(st), ph ^ 1u,
                                                 abort_flag, p.status)))
         goto done;
-      stat[st * kRowTile + lane] = v[0];
-      stat[st * kRowTile + lane + 32] = v[1];
-      if (lane < 8) masks[st * 8 + lane] = m;
+      float *sst = stat(st);
+      for (int x = 0; x < pl.bpt; ++x) {
+        const uint32_t mx = __shfl_sync(0xffffffffu, m, x);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          sst[x * kRowTile + lane + 32 * u] =
+              qr[u] < nq && (mx >> qr[u] & 1u) ? v[u].x : inf;
+      }
+      sst[8 * kRowTile + lane] = v[0].y;
+      sst[8 * kRowTile + lane + 32] = v[1].y;
+      uint32_t *meta = reinterpret_cast<uint32_t *>(sst + 9 * kRowTile);
+      if (lane < 8) meta[lane] = m;
+      if (lane == 8)
+        *reinterpret_cast<long long *>(meta + 8) = q0 + s0;
       mbar_arrive(st_full(st));
       if (lane == 0) {
         mbar_arrive_expect_tx(st_full(st), 2 * CH * pl.qt * p.G * 128);
@@ -426,126 +450,136 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       __syncwarp();
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t lead = lane == 0;
-    auto wall = [&](uint32_t bar, uint32_t ph) -> bool {
-      return __all_sync(0xffffffffu,
-                        wait_bar_inl(bar, ph, abort_flag, p.status));
-    };
-    if (n > 0 && !wall(kv_full, 0)) goto done;
-    const uint64_t kd = sdesc_k_sw128(sK), vd = sdesc_k_sw128(sV);
-    for (int i = 0; i <= n; ++i) {
-      if (i < n) {
-        const int st = i % kKvStages;
-        if (!wall(st_full(st), (i / kKvStages) & 1u)) goto done;
-        tc_fence_after();
-        const uint64_t qd = sdesc_k_sw128(sQ(st)), gd = sdesc_k_sw128(sG(st));
-        const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
+    if (elect_one()) {
+      auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
+        return wait_bar_spin(bar, ph, abort_flag, p.status);
+      };
+      const uint64_t kd = sdesc_k_sw128(sK), vd = sdesc_k_sw128(sV);
+      bool ok = n <= 0 || wait(kv_full, 0);
+      int st = 0, done = 0;  // stages of the step begun and of the one before
+      uint32_t ph = 0, acc = 0;
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {
+          if (!(ok = wait(st_full(st), ph))) break;
+          tc_fence_after();
+          const uint64_t qd = sdesc_k_sw128(sQ(st)),
+                         gd = sdesc_k_sw128(sG(st));
+          const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t ao = ((ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32) >> 4;
-          const uint32_t bo = ((ks >> 2) * (kRowTile * 128) + (ks & 3) * 32) >> 4;
-          mma_bf16_by(d, kd + ao, qd + bo, kIdescS, ks != 0, lead);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_bf16(d, kd + koff(ks), qd + roff(ks), kIdescS, ks != 0);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_bf16(d + 64, vd + koff(ks), gd + roff(ks), kIdescS, ks != 0);
+          mma_commit(sdp_full(i & 1));
+          if (++st == kKvStages) st = 0, ph ^= 1;
         }
+        if (i > 0) {
+          const int b1 = (i - 1) & 1;
+          if (!(ok = wait(ds_full(b1), ((i - 1) >> 1) & 1u))) break;
+          tc_fence_after();
+          const uint64_t qm = sdesc_mn_sw128(sQ(done), kRowTile * 128, 1024);
+          const uint64_t gm = sdesc_mn_sw128(sG(done), kRowTile * 128, 1024);
+          const uint32_t a = tmem + kTmBuf + b1 * 128;
+          // each warpgroup's 32 rows are 16 columns at its half's start
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t ao = ((ks >> 2) * (kKeyTile * 128) + (ks & 3) * 32) >> 4;
-          const uint32_t bo = ((ks >> 2) * (kRowTile * 128) + (ks & 3) * 32) >> 4;
-          mma_bf16_by(d + 64, vd + ao, gd + bo, kIdescS, ks != 0, lead);
+          for (int ks = 0; ks < kRowTile / 16; ++ks)
+            mma_bf16_ta(tmem + kTmV, a + (ks >> 1) * 32 + (ks & 1) * 8,
+                        gm + ((ks * 2048) >> 4), kIdescA, ks == 0 ? acc : 1u);
+#pragma unroll
+          for (int ks = 0; ks < kRowTile / 16; ++ks)
+            mma_bf16_ta(tmem + kTmK, a + 64 + (ks >> 1) * 32 + (ks & 1) * 8,
+                        qm + ((ks * 2048) >> 4), kIdescA, ks == 0 ? acc : 1u);
+          mma_commit(st_empty(done));
+          if (i == n) mma_commit(acc_full);
+          acc = 1;
+          if (++done == kKvStages) done = 0;
         }
-        mma_commit_by(sdp_full(i & 1), lead);
-      }
-      if (i > 0) {
-        const int j = i - 1, st = j % kKvStages;
-        if (!wall(ds_full(j & 1), (j >> 1) & 1u)) goto done;
-        tc_fence_after();
-        const uint64_t qm = sdesc_mn_sw128(sQ(st), kRowTile * 128, 1024);
-        const uint64_t gm = sdesc_mn_sw128(sG(st), kRowTile * 128, 1024);
-        const uint32_t a = tmem + kTmBuf + (j & 1) * 128;
-#pragma unroll
-        for (int ks = 0; ks < kRowTile / 16; ++ks)
-          mma_bf16_ta_by(tmem + kTmV, a + ks * 8, gm + ((ks * 2048) >> 4),
-                         kIdescA, (j > 0 || ks != 0) ? 1u : 0u, lead);
-#pragma unroll
-        for (int ks = 0; ks < kRowTile / 16; ++ks)
-          mma_bf16_ta_by(tmem + kTmK, a + 64 + ks * 8, qm + ((ks * 2048) >> 4),
-                         kIdescA, (j > 0 || ks != 0) ? 1u : 0u, lead);
-        mma_commit_by(st_empty(st), lead);
-        if (i == n) mma_commit_by(acc_full, lead);
       }
     }
+    __syncwarp();
   } else {
-    // ---------------- one key a thread; steps alternate ----------------
+    // ---------- one key a thread; a warpgroup takes 32 of the rows ----------
     const int wg = warp >> 2;
     const int key = (warp & 3) * 32 + lane;
     const long long j = (long long)kt * kKeyTile + key;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = p.scale * 1.4426950408889634f;
-    const uint32_t every = pl.qt >= 32 ? 0xffffffffu : (1u << pl.qt) - 1u;
-    const unsigned long long gmask =
-        p.G >= 64 ? ~0ull : (1ull << p.G) - 1ull;
-    const long long q0 = row_pos(p.q_pos, b, 0);
-    for (int i = wg; i < n; i += 2) {
+    const int kb = key / p.blk;  // this key's block
+    const long long last = (long long)kt * kKeyTile + kKeyTile - 1;
+    for (int i = 0; i < n; ++i) {
       const int st = i % kKvStages;
-      const long long pos0 = q0 + (long long)pl.eq[e0 + i] * pl.qt;
       if (!__all_sync(0xffffffffu,
-                      wait_bar_inl(sdp_full(wg), (i >> 1) & 1u, abort_flag,
+                      wait_bar_spin(sdp_full(i & 1), (i >> 1) & 1u, abort_flag,
                                    p.status) &&
-                          wait_bar_inl(st_full(st), (i / kKvStages) & 1u,
+                          wait_bar_spin(st_full(st), (i / kKvStages) & 1u,
                                        abort_flag, p.status)))
         goto done;
       tc_fence_after();
-      // queries that hold this key's block and are not before it
-      uint32_t qm = masks[st * 8 + key / p.blk];
-      const long long late = j - pos0;
-      if (late > 0) qm = late >= 32 ? 0u : qm & (~0u << (int)late);
-      if (j >= p.T) qm = 0u;
-      const bool full = __all_sync(0xffffffffu, qm == every);
-      unsigned long long rm = ~0ull;
-      if (!full) {
-        rm = 0ull;
-        for (int q = 0; q < pl.qt; ++q)
-          if (qm >> q & 1u) rm |= gmask << (q * p.G);
-      }
-      const float4 *sp =
-          reinterpret_cast<const float4 *>(stat + st * kRowTile);
-      const uint32_t ts = tmem + kTmBuf + wg * 128 + lane_off;
+      const uint32_t ts = tmem + kTmBuf + (i & 1) * 128 + wg * 32 + lane_off;
+      uint32_t u[32], g[32];
+      __syncwarp();
+      tmem_ld32(ts, u);
+      tmem_ld32(ts + 64, g);
+      const float *sst = stat(st);
+      const float4 *sl = reinterpret_cast<const float4 *>(
+          sst + kb * kRowTile + wg * 32);
+      const float4 *sd = reinterpret_cast<const float4 *>(
+          sst + 8 * kRowTile + wg * 32);
+      const uint32_t *meta =
+          reinterpret_cast<const uint32_t *>(sst + 9 * kRowTile);
+      const long long pos0 = *reinterpret_cast<const long long *>(meta + 8);
+      tmem_ld_wait();
+      reg_fence32(u);
+      reg_fence32(g);
+      if (last > pos0) {  // keys after some query: row by row
+        uint32_t qm = meta[kb];
+        const long long late = j - pos0;
+        if (late > 0) qm = late >= 32 ? 0u : qm & (~0u << (int)late);
+        if (j >= p.T) qm = 0u;
+        int q = wg * 32 / p.G, h = wg * 32 % p.G;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t u[32], g[32];
-        __syncwarp();
-        tmem_ld32(ts + c * 32, u);
-        tmem_ld32(ts + 64 + c * 32, g);
-        tmem_ld_wait();
-        reg_fence32(u);
-        reg_fence32(g);
-        uint32_t pk[16], dk[16];
-        const uint32_t half = (uint32_t)(rm >> (32 * c));
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const float4 sd = sp[(c * 32 + x) >> 1];
-          float p0 = ex2(fmaf(__uint_as_float(u[x]), c2, -sd.x));
-          float p1 = ex2(fmaf(__uint_as_float(u[x + 1]), c2, -sd.z));
-          if (!full) {
-            p0 = half >> x & 1u ? p0 : 0.f;
-            p1 = half >> (x + 1) & 1u ? p1 : 0.f;
-          }
-          pk[x >> 1] = pack_bf16x2(p0, p1);
-          dk[x >> 1] = pack_bf16x2(p0 * (__uint_as_float(g[x]) - sd.y),
-                                   p1 * (__uint_as_float(g[x + 1]) - sd.w));
+        for (int x = 0; x < 32; ++x) {
+          if (q >= 32 || !(qm >> q & 1u)) u[x] = 0xff800000u;
+          if (++h == p.G) h = 0, ++q;
         }
-        __syncwarp();
-        tmem_st16(ts + c * 16, pk);
-        tmem_st16(ts + 64 + c * 16, dk);
       }
+      uint32_t pk[16], dk[16];
+#pragma unroll
+      for (int x = 0; x < 32; x += 4) {
+        const float4 l4 = sl[x >> 2], d4 = sd[x >> 2];
+#pragma unroll
+        for (int y = 0; y < 4; y += 2) {
+          const float2 l = y ? make_float2(l4.z, l4.w)
+                             : make_float2(l4.x, l4.y);
+          const float2 d = y ? make_float2(d4.z, d4.w)
+                             : make_float2(d4.x, d4.y);
+          float2 e = __ffma2_rn(
+              make_float2(__uint_as_float(u[x + y]),
+                          __uint_as_float(u[x + y + 1])),
+              make_float2(c2, c2), make_float2(-l.x, -l.y));
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          pk[(x + y) >> 1] = pack_bf16x2(e.x, e.y);
+          const float2 w = __fmul2_rn(
+              e, __fadd2_rn(make_float2(__uint_as_float(g[x + y]),
+                                        __uint_as_float(g[x + y + 1])),
+                            make_float2(-d.x, -d.y)));
+          dk[(x + y) >> 1] = pack_bf16x2(w.x, w.y);
+        }
+      }
+      __syncwarp();
+      tmem_st16(ts, pk);
+      tmem_st16(ts + 64, dk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full(wg));
+      if (lane == 0) mbar_arrive(ds_full(i & 1));
     }
     // ---------------- dK (warpgroup 0), dV (1) ----------------
     if (n > 0) {
       if (!__all_sync(0xffffffffu,
-                      wait_bar_inl(acc_full, 0, abort_flag, p.status)))
+                      wait_bar_spin(acc_full, 0, abort_flag, p.status)))
         goto done;
       tc_fence_after();
     }
@@ -592,6 +626,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 done:
   __syncthreads();
   if (warp == kMmaWarp) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -674,6 +709,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t sQ = base + L::kOffQ, sG = base + L::kOffG;
   auto sK = [&](int st) { return base + L::kOffS + st * 2 * L::kKey; };
   auto sV = [&](int st) { return sK(st) + L::kKey; };
+  auto roff = [](int ks) {
+    return (uint32_t)((ks >> 2) * (kDqRows * 128) + (ks & 3) * 32) >> 4;
+  };
+  auto koff = [](int ks) {
+    return (uint32_t)((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
+  };
   const uint32_t bars = base + L::kOffBar;
   const uint32_t q_full = bars, acc_full = bars + 88;
   auto kv_full = [&](int i) { return bars + 8 + 8 * i; };
@@ -705,7 +746,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sdp_full(i), 1);
-      mbar_init(ds_full(i), 4);
+      mbar_init(ds_full(i), 8);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -735,7 +776,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (lane == 0) *sCount = n;
   }
   __syncthreads();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   // a step takes units of up to 64 keys: whole blocks, or halves of 128
   const int count = *sCount;
   const int unit = min(p.blk, kDqKeys), per = p.blk / unit;
@@ -752,12 +793,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     hk * p.G, b, s0);
       }
     }
+    int st = 0;
+    uint32_t ph = 0;
     for (int i = 0; i < n; ++i) {
-      const int st = i % pl.stages;
-      const uint32_t ph = (i / pl.stages) & 1u;
       const int nu = min(upt, count * per - i * upt);
       const int ui = lane / CH, c = lane % CH;  // unit and chunk of this lane
-      if (!__all_sync(0xffffffffu, wait_bar_inl(kv_empty(st), ph ^ 1u,
+      if (!__all_sync(0xffffffffu, wait_bar_spin(kv_empty(st), ph ^ 1u,
                                                 abort_flag, p.status)))
         goto done;
       if (lane == 0)
@@ -772,52 +813,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tma_load_4d(sV(st) + at, &maps.v, kv_full(st), c * kChunk, tok,
                     hk * maps.bc_vh, b * maps.bc_vs);
       }
+      if (++st == pl.stages) st = 0, ph ^= 1;
     }
   } else if (warp == kMmaWarp) {
-    const uint32_t lead = lane == 0;
-    auto wall = [&](uint32_t bar, uint32_t ph) -> bool {
-      return __all_sync(0xffffffffu,
-                        wait_bar_inl(bar, ph, abort_flag, p.status));
-    };
-    if (n > 0 && !wall(q_full, 0)) goto done;
-    const uint64_t qd = sdesc_k_sw128(sQ), gd = sdesc_k_sw128(sG);
-    for (int i = 0; i <= n; ++i) {
-      if (i < n) {
-        const int st = i % pl.stages;
-        if (!wall(kv_full(st), (i / pl.stages) & 1u)) goto done;
-        tc_fence_after();
-        const uint64_t kd = sdesc_k_sw128(sK(st)), vd = sdesc_k_sw128(sV(st));
-        const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
+    if (elect_one()) {
+      auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
+        return wait_bar_spin(bar, ph, abort_flag, p.status);
+      };
+      const uint64_t qd = sdesc_k_sw128(sQ), gd = sdesc_k_sw128(sG);
+      bool ok = n <= 0 || wait(q_full, 0);
+      int st = 0, done = 0;
+      uint32_t ph = 0, acc = 0;
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i < n) {
+          if (!(ok = wait(kv_full(st), ph))) break;
+          tc_fence_after();
+          const uint64_t kd = sdesc_k_sw128(sK(st)),
+                         vd = sdesc_k_sw128(sV(st));
+          const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t ao = ((ks >> 2) * (kDqRows * 128) + (ks & 3) * 32) >> 4;
-          const uint32_t bo = ((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
-          mma_bf16_by(d, qd + ao, kd + bo, kIdescS, ks != 0, lead);
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_bf16(d, qd + roff(ks), kd + koff(ks), kIdescS, ks != 0);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks)
+            mma_bf16(d + 64, gd + roff(ks), vd + koff(ks), kIdescS, ks != 0);
+          mma_commit(sdp_full(i & 1));
+          if (++st == pl.stages) st = 0, ph ^= 1;
         }
+        if (i > 0) {
+          const int b1 = (i - 1) & 1;
+          if (!(ok = wait(ds_full(b1), ((i - 1) >> 1) & 1u))) break;
+          tc_fence_after();
+          const uint64_t km = sdesc_mn_sw128(sK(done), kDqKeys * 128, 1024);
+          const uint32_t a = tmem + kTmBuf + b1 * 128;
+          // each warpgroup's 32 keys are 16 columns at its half's start
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t ao = ((ks >> 2) * (kDqRows * 128) + (ks & 3) * 32) >> 4;
-          const uint32_t bo = ((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
-          mma_bf16_by(d + 64, gd + ao, vd + bo, kIdescS, ks != 0, lead);
+          for (int ks = 0; ks < kDqKeys / 16; ++ks)
+            mma_bf16_ta(tmem + kTmQ, a + (ks >> 1) * 32 + (ks & 1) * 8,
+                        km + ((ks * 2048) >> 4), kIdescA, ks == 0 ? acc : 1u);
+          mma_commit(kv_empty(done));
+          if (i == n) mma_commit(acc_full);
+          acc = 1;
+          if (++done == pl.stages) done = 0;
         }
-        mma_commit_by(sdp_full(i & 1), lead);
-      }
-      if (i > 0) {
-        const int j = i - 1, st = j % pl.stages;
-        if (!wall(ds_full(j & 1), (j >> 1) & 1u)) goto done;
-        tc_fence_after();
-        const uint64_t km = sdesc_mn_sw128(sK(st), kDqKeys * 128, 1024);
-        const uint32_t a = tmem + kTmBuf + (j & 1) * 128;
-#pragma unroll
-        for (int ks = 0; ks < kDqKeys / 16; ++ks)
-          mma_bf16_ta_by(tmem + kTmQ, a + ks * 8, km + ((ks * 2048) >> 4),
-                         kIdescA, (j > 0 || ks != 0) ? 1u : 0u, lead);
-        mma_commit_by(kv_empty(st), lead);
-        if (i == n) mma_commit_by(acc_full, lead);
       }
     }
+    __syncwarp();
   } else {
-    // ---------------- one row a thread; steps alternate ----------------
+    // ---------- one row a thread; a warpgroup takes 32 of the keys ----------
     const int wg = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int qi = row / p.G;
@@ -825,69 +868,76 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int s = s0 + (live ? qi : 0);
     const long long pos =
         live ? min(row_pos(p.q_pos, b, s), (long long)p.T - 1) : -1;
+    const long long pos_lo =
+        min(row_pos(p.q_pos, b, s0), (long long)p.T - 1);
     const size_t at = ((size_t)s * p.B + b) * p.H + hk * p.G + row % p.G;
-    const float2 sd = live ? pl.stat[at]
-                           : make_float2(__int_as_float(0x7f800000), 0.f);
+    const float inf = __int_as_float(0x7f800000);
+    const float2 sd = live ? pl.stat[at] : make_float2(inf, 0.f);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = p.scale * 1.4426950408889634f;
-    for (int i = wg; i < n; i += 2) {
-      uint32_t mask[2];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        mask[c] = 0u;
-        if (!live) continue;
-        if (unit < p.blk) {  // halves of a block
-          const int bn = list[i >> 1];
-          if (words[bn] >> qi & 1u)
-            mask[c] = run_mask(pos, (long long)bn * p.blk + (i & 1) * 64 +
-                                        c * 32, 32);
-        } else {
-          mask[c] = tile_mask(words, list, i * upt, count, p.blk, c, qi, pos);
-        }
+    for (int i = 0; i < n; ++i) {
+      uint32_t mask = 0u;
+      long long end;
+      if (unit < p.blk) {  // half of a block
+        const int bn = list[i >> 1];
+        const long long j0 = (long long)bn * p.blk + (i & 1) * 64 + wg * 32;
+        if (live && (words[bn] >> qi & 1u)) mask = run_mask(pos, j0, 32);
+        end = j0 + 31;
+      } else {
+        if (live)
+          mask = tile_mask(words, list, i * upt, count, p.blk, wg, qi, pos);
+        end = tile_end(list, i * upt, count, p.blk, wg);
       }
-      if (!__all_sync(0xffffffffu, wait_bar_inl(sdp_full(wg), (i >> 1) & 1u,
+      const bool any = __any_sync(0xffffffffu, mask != 0u);
+      if (!__all_sync(0xffffffffu, wait_bar_spin(sdp_full(i & 1), (i >> 1) & 1u,
                                                 abort_flag, p.status)))
         goto done;
       tc_fence_after();
-      const uint32_t ts = tmem + kTmBuf + wg * 128 + lane_off;
+      const uint32_t ts = tmem + kTmBuf + (i & 1) * 128 + wg * 32 + lane_off;
+      uint32_t dk[16];
+      if (!any) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t dk[16];
-        if (__all_sync(0xffffffffu, mask[c] == 0u)) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) dk[x] = 0u;
-        } else {
-          const bool full = __all_sync(0xffffffffu, mask[c] == 0xffffffffu);
-          uint32_t u[32], g[32];
-          __syncwarp();
-          tmem_ld32(ts + c * 32, u);
-          tmem_ld32(ts + 64 + c * 32, g);
-          tmem_ld_wait();
-          reg_fence32(u);
-          reg_fence32(g);
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(u[x]), c2, -sd.x));
-            float p1 = ex2(fmaf(__uint_as_float(u[x + 1]), c2, -sd.x));
-            if (!full) {
-              p0 = mask[c] >> x & 1u ? p0 : 0.f;
-              p1 = mask[c] >> (x + 1) & 1u ? p1 : 0.f;
-            }
-            dk[x >> 1] = pack_bf16x2(p0 * (__uint_as_float(g[x]) - sd.y),
-                                     p1 * (__uint_as_float(g[x + 1]) - sd.y));
-          }
-        }
+        for (int x = 0; x < 16; ++x) dk[x] = 0u;
+      } else {
+        uint32_t u[32], g[32];
         __syncwarp();
-        tmem_st16(ts + c * 16, dk);
+        tmem_ld32(ts, u);
+        tmem_ld32(ts + 64, g);
+        tmem_ld_wait();
+        reg_fence32(u);
+        reg_fence32(g);
+        if (end > pos_lo) {  // keys after some row's position: one by one
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            u[x] = mask >> x & 1u ? u[x] : 0xff800000u;
+        }
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          // a row holds 16 neighbouring keys or none, or they are hidden
+          const float sub =
+              mask & (x < 16 ? 0xffffu : 0xffff0000u) ? -sd.x : -inf;
+          float2 e = __ffma2_rn(
+              make_float2(__uint_as_float(u[x]), __uint_as_float(u[x + 1])),
+              make_float2(c2, c2), make_float2(sub, sub));
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          const float2 w = __fmul2_rn(
+              e, __fadd2_rn(make_float2(__uint_as_float(g[x]),
+                                        __uint_as_float(g[x + 1])),
+                            make_float2(-sd.y, -sd.y)));
+          dk[x >> 1] = pack_bf16x2(w.x, w.y);
+        }
       }
+      __syncwarp();
+      tmem_st16(ts, dk);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full(wg));
+      if (lane == 0) mbar_arrive(ds_full(i & 1));
     }
     if (n > 0) {
       if (!__all_sync(0xffffffffu,
-                      wait_bar_inl(acc_full, 0, abort_flag, p.status)))
+                      wait_bar_spin(acc_full, 0, abort_flag, p.status)))
         goto done;
       tc_fence_after();
     }
@@ -921,6 +971,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 done:
   __syncthreads();
   if (warp == kMmaWarp) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
