@@ -237,14 +237,9 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     const int qi = row / p.G;
     const bool live = qi < nq;
     const int s = s0 + (live ? qi : 0), h = hk * p.G + row % p.G;
-    const long long pos = live ? min(row_pos(p.q_pos, b, s),
-                                     (long long)p.T - 1)
-                               : -1;
-    // the last key that any row of the tile sees, and its block
-    const long long pos_hi =
-        min(row_pos(p.q_pos, b, s0 + nq - 1), (long long)p.T - 1);
-    const long long pos_lo =
-        min(row_pos(p.q_pos, b, s0), (long long)p.T - 1);
+    const int pos = live ? key_pos(p, b, s) : -1;
+    // the last key that the first and that any row of the tile sees
+    const int pos_lo = key_pos(p, b, s0), pos_hi = key_pos(p, b, s0 + nq - 1);
     const float c2 = p.scale * 1.4426950408889634f;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t tS = tmem + kTmS + lane_off, tO = tmem + kTmO + lane_off;
@@ -256,10 +251,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       bool diag[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mask[c] = live ? tile_mask(words, list, t * bpt, count, p.blk, c, qi,
-                                   pos)
-                       : 0u;
-        diag[c] = tile_end(list, t * bpt, count, p.blk, c) > pos_lo;
+        int end;
+        mask[c] = step_mask(words, list, t * bpt, count, p.lb, c, qi & 31,
+                            pos, end);
+        diag[c] = end > pos_lo;
         if (__any_sync(0xffffffffu, mask[c] != 0u)) held |= 1u << c;
       }
       if (!__all_sync(0xffffffffu,
@@ -378,11 +373,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       weights(0, u[0]);
       tmem_st_wait();
       tc_fence_before();
-      // V rows of this step that no row sees
-      {
-        const int i = t * bpt + row / p.blk;
+      if (diag[0] || diag[1] || diag[2] || diag[3]) {
+        // V rows of this step that no row sees
+        const int i = t * bpt + (row >> p.lb);
         const bool over =
-            i < count && (long long)list[i] * p.blk + row % p.blk > pos_hi;
+            i < count &&
+            (list[i] << p.lb) + (row & (p.blk - 1)) > pos_hi;
         if (__any_sync(0xffffffffu, over)) {
           if (!__all_sync(0xffffffffu,
                           wait_bar_spin(v_full, ph, abort_flag, p.status)))
@@ -636,6 +632,7 @@ int check_block_attn(BlockAttn &p) {
   if (p.D != 64 && p.D != 128) return DSA_ERR_UNSUPPORTED;
   if (p.blk != 16 && p.blk != 32 && p.blk != 64 && p.blk != 128)
     return DSA_ERR_UNSUPPORTED;
+  p.lb = p.blk == 16 ? 4 : p.blk == 32 ? 5 : p.blk == 64 ? 6 : 7;
   p.G = p.H / p.Hk;
   if (p.G > DSA_BLOCK_ATTN_MAX_GROUP) return DSA_ERR_UNSUPPORTED;
   p.nblk = (int)(((long long)p.T + p.blk - 1) / p.blk);

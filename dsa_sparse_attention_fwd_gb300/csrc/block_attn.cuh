@@ -21,6 +21,7 @@ struct BlockAttn {
   int max_pages, page_size, num_pages;
   int S, B, H, Hk, G, D, T;     // G = H / Hk heads share a key head
   int sel_heads, topk, blk, local, nblk;
+  int lb;  // log2 of blk
   float scale;
   int *status;
 };
@@ -106,49 +107,46 @@ __device__ __forceinline__ int list_blocks(const uint32_t *words, int nblk,
   return count;
 }
 
-// The keys j0 .. j0 + width - 1 that a row at `pos` sees, as a mask.
-__device__ __forceinline__ uint32_t run_mask(long long pos, long long j0,
-                                             int width) {
-  const long long n = pos - j0 + 1;
-  if (n <= 0) return 0u;
-  if (n >= width) return width >= 32 ? 0xffffffffu : (1u << width) - 1u;
-  return (1u << (int)n) - 1u;
+// A row's position as the masks use it: capped to the last key (T is at most
+// 2^21: 16384 blocks of 128), -1 before the first.
+__device__ __forceinline__ int key_pos(const BlockAttn &p, int b, int s) {
+  const long long pos = row_pos(p.q_pos, b, s);
+  return pos < 0 ? -1 : pos < p.T ? (int)pos : p.T - 1;
 }
 
-// Mask of the 32 keys `c` (0 ..) of a tile whose blocks are list[l0 ..],
-// l0 + i < count, for the row of query bit qi at position pos.
-__device__ __forceinline__ uint32_t tile_mask(const uint32_t *words,
+// The first n of `width` keys, n of any size: a mask.
+__device__ __forceinline__ uint32_t first_keys(int n, int width) {
+  n = n < 0 ? 0 : n;
+  return n >= width ? 0xffffffffu >> (32 - width) : (1u << n) - 1u;
+}
+
+// Mask of the 32 keys `c` (0 ..) of a step whose blocks are list[l0 ..] up to
+// count, for the row of query bit qi at `pos`; `end`: the last of the keys
+// (-1: none).  Shifts only, and no branch but one on the block size: it runs
+// for every row and step.
+__device__ __forceinline__ uint32_t step_mask(const uint32_t *words,
                                               const uint16_t *list, int l0,
-                                              int count, int blk, int c,
-                                              int qi, long long pos) {
-  if (blk >= 32) {
-    const int i = l0 + c * 32 / blk;
-    if (i >= count) return 0u;
-    const int n = list[i];
-    if (!(words[n] >> qi & 1u)) return 0u;
-    return run_mask(pos, (long long)n * blk + c * 32 % blk, 32);
+                                              int count, int lb, int c, int qi,
+                                              int pos, int &end) {
+  if (lb >= 5) {
+    const int i = l0 + (c * 32 >> lb);
+    const int n = list[i < count ? i : count - 1];
+    const int j0 = (n << lb) + (c * 32 & ((1 << lb) - 1));
+    const uint32_t held = i < count ? words[n] >> qi & 1u : 0u;
+    end = i < count ? j0 + 31 : -1;
+    return first_keys(held ? pos - j0 + 1 : 0, 32);
   }
   uint32_t m = 0u;  // blocks of 16
+  end = -1;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int i = l0 + c * 2 + u;
-    if (i >= count) continue;
-    const int n = list[i];
-    if (words[n] >> qi & 1u)
-      m |= run_mask(pos, (long long)n * 16, 16) << (16 * u);
+    const int n = list[i < count ? i : count - 1];
+    const uint32_t held = i < count ? words[n] >> qi & 1u : 0u;
+    if (i < count) end = n * 16 + 15;  // ascending: the last one stays
+    m |= first_keys(held ? pos - n * 16 + 1 : 0, 16) << (16 * u);
   }
   return m;
-}
-
-// The last key of those 32.
-__device__ __forceinline__ long long tile_end(const uint16_t *list, int l0,
-                                              int count, int blk, int c) {
-  if (blk >= 32) {
-    const int i = l0 + c * 32 / blk;
-    return i < count ? (long long)list[i] * blk + c * 32 % blk + 31 : -1;
-  }
-  const int i = l0 + c * 2, j = i + 1 < count ? i + 1 : i;  // ascending
-  return i < count ? (long long)list[j] * 16 + 15 : -1;
 }
 
 // TMA coordinates of block n of sequence b, for a map made with

@@ -866,28 +866,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int qi = row / p.G;
     const bool live = qi < nq;
     const int s = s0 + (live ? qi : 0);
-    const long long pos =
-        live ? min(row_pos(p.q_pos, b, s), (long long)p.T - 1) : -1;
-    const long long pos_lo =
-        min(row_pos(p.q_pos, b, s0), (long long)p.T - 1);
+    const int pos = live ? key_pos(p, b, s) : -1;
+    const int pos_lo = key_pos(p, b, s0);
     const size_t at = ((size_t)s * p.B + b) * p.H + hk * p.G + row % p.G;
     const float inf = __int_as_float(0x7f800000);
     const float2 sd = live ? pl.stat[at] : make_float2(inf, 0.f);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = p.scale * 1.4426950408889634f;
     for (int i = 0; i < n; ++i) {
-      uint32_t mask = 0u;
-      long long end;
-      if (unit < p.blk) {  // half of a block
-        const int bn = list[i >> 1];
-        const long long j0 = (long long)bn * p.blk + (i & 1) * 64 + wg * 32;
-        if (live && (words[bn] >> qi & 1u)) mask = run_mask(pos, j0, 32);
-        end = j0 + 31;
-      } else {
-        if (live)
-          mask = tile_mask(words, list, i * upt, count, p.blk, wg, qi, pos);
-        end = tile_end(list, i * upt, count, p.blk, wg);
-      }
+      // (a step of halves of 128 is one half: two steps a block)
+      int end;
+      const uint32_t mask =
+          step_mask(words, list, unit < p.blk ? i >> 1 : i * upt, count, p.lb,
+                    wg + (unit < p.blk ? (i & 1) * 2 : 0), qi & 31, pos, end);
       const bool any = __any_sync(0xffffffffu, mask != 0u);
       if (!__all_sync(0xffffffffu, wait_bar_spin(sdp_full(i & 1), (i >> 1) & 1u,
                                                 abort_flag, p.status)))
