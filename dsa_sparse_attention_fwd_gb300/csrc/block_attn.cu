@@ -132,6 +132,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 32 * kTmaWarp) {  // Q arrives while the blocks are listed
+    mbar_arrive_expect_tx(q_full, CH * pl.qt * p.G * 128);
+    for (int c = 0; c < CH; ++c)
+      tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk,
+                  hk * p.G, b, s0);
+  }
   mark_blocks(p, b, s0, nq, hk, words, tid, kFwdThreads);
   __syncthreads();
   if (warp == 0) {
@@ -158,12 +164,6 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 
   if (warp == kTmaWarp) {
     // ---------------- TMA producer ----------------
-    if (t1 > t0 && lane == 0) {
-      mbar_arrive_expect_tx(q_full, CH * pl.qt * p.G * 128);
-      for (int c = 0; c < CH; ++c)
-        tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk,
-                    hk * p.G, b, s0);
-    }
     for (int t = t0; t < t1; ++t) {
       const uint32_t ph = (t - t0) & 1u;
       const int nb = min(bpt, count - t * bpt);
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       };
       const uint64_t qd = sdesc_k_sw128(sQ), kd = sdesc_k_sw128(sK);
       const uint64_t vd = sdesc_mn_sw128(sV, kRows * 128, 1024);
-      bool ok = t1 <= t0 || wait(q_full, 0);
+      bool ok = wait(q_full, 0);
       uint32_t ph = 0, acc = 0;
       for (int t = t0; ok && t < t1; ++t) {
         if (!(ok = wait(k_full, ph))) break;

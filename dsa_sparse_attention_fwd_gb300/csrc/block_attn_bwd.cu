@@ -35,7 +35,9 @@ constexpr int kBwdThreads = 320;  // 8 compute warps, TMA warp, MMA warp
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
 constexpr int kKeyTile = 128;  // keys of a dk, dv item
 constexpr int kRowTile = 64;   // rows of its query tiles
-constexpr int kKvStages = 3;
+// A stage of 32 KB takes 1900 cycles to arrive from L2 and is held for 2900
+// more, with a step every 1300 to 1500: four stages.
+constexpr int kKvStages = 4;
 constexpr int kMinChunk = 16;     // query tiles of a chunk at least
 constexpr int kChunkUnits = 640;  // 4 chunks on each of 160 SMs
 
@@ -80,7 +82,7 @@ int make_plan(const BlockAttn &p, char *ws, BwdPlan *pl) {
   const long long bh = (long long)p.B * p.sel_heads;
   const long long kts = bh * pl->nkt, qts = bh * pl->nqt;
   pl->entries = qts * (pl->nkt < pl->cap ? pl->nkt : pl->cap);
-  if (pl->entries >= (1ll << 31) || kts >= (1ll << 28) ||
+  if (pl->entries >= (1ll << 31) || kts >= (1ll << 20) ||
       qts * pl->cap >= (1ll << 40))
     return DSA_ERR_UNSUPPORTED;
   pl->items = (int)(kts + kChunkUnits / pl->rep + 1);
@@ -120,32 +122,50 @@ int make_plan(const BlockAttn &p, char *ws, BwdPlan *pl) {
 
 // ---- delta --------------------------------------------------------------------
 
-// stat = (lse log2 e, do.o); one warp a row.  A row without keys gets +inf,
-// so its weights exp2(x - inf) are zero.
+// stat = (lse log2 e, do.o); D / 8 lanes a row, 16 bytes each, kDeltaRows
+// rows in flight.  A row without keys gets +inf, so its weights exp2(x - inf)
+// are zero.
+constexpr int kDeltaRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
     bwd_delta_kernel(const __nv_bfloat16 *o, const __nv_bfloat16 *go,
                      const float *lse, long long rows, float2 *stat) {
-  const long long r = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (r >= rows) return;
-  float t = 0.f;
+  constexpr int L = D / 8, kPer = 256 / L;  // lanes of a row, rows of a pass
+  const int sub = threadIdx.x / L, lane = threadIdx.x % L;
+  const long long r0 = (long long)blockIdx.x * kPer * kDeltaRows + sub;
+  uint4 a[kDeltaRows], g[kDeltaRows];
+  float l[kDeltaRows];
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const size_t at = (size_t)r * D + i * 64 + lane * 2;
-    const float2 a = __bfloat1622float2(
-        *reinterpret_cast<const __nv_bfloat162 *>(o + at));
-    const float2 g = __bfloat1622float2(
-        *reinterpret_cast<const __nv_bfloat162 *>(go + at));
-    t = fmaf(a.x, g.x, t);
-    t = fmaf(a.y, g.y, t);
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const long long r = r0 + i * kPer;
+    a[i] = g[i] = make_uint4(0u, 0u, 0u, 0u);
+    l[i] = 0.f;
+    if (r < rows) {
+      a[i] = __ldg(reinterpret_cast<const uint4 *>(o + r * D) + lane);
+      g[i] = __ldg(reinterpret_cast<const uint4 *>(go + r * D) + lane);
+      if (lane == 0) l[i] = __ldg(lse + r);
+    }
   }
-  for (int x = 16; x; x >>= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-  if (lane == 0) {
-    const float inf = __int_as_float(0x7f800000);
-    const float l = lse[r];
-    stat[r] = l == -inf ? make_float2(inf, 0.f)
-                        : make_float2(l * 1.4426950408889634f, t);
+#pragma unroll
+  for (int i = 0; i < kDeltaRows; ++i) {
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+    const uint32_t y[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+    float t = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      t = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(y[e] << 16), t);
+      t = fmaf(__uint_as_float(x[e] & 0xffff0000u),
+               __uint_as_float(y[e] & 0xffff0000u), t);
+    }
+#pragma unroll
+    for (int m = L / 2; m; m >>= 1) t += __shfl_xor_sync(0xffffffffu, t, m);
+    const long long r = r0 + i * kPer;
+    if (lane == 0 && r < rows) {
+      const float inf = __int_as_float(0x7f800000);
+      stat[r] = l[i] == -inf
+                    ? make_float2(inf, 0.f)
+                    : make_float2(l[i] * 1.4426950408889634f, t);
+    }
   }
 }
 
@@ -222,16 +242,20 @@ __global__ void __launch_bounds__(1024)
   const unsigned long long share =
       ((unsigned long long)total * pl.rep + kChunkUnits - 1) / kChunkUnits;
   const uint32_t len = share > kMinChunk ? (uint32_t)share : kMinChunk;
-  uint32_t items = 0, slots = 0, unused;
+  // whole chunks come first, the lists' ends and the empty lists after them:
+  // CTAs start in this order, and the short ones fill the last round
+  uint32_t whole = 0, rest = 0, slots = 0, unused, wholes, rests;
   for (int k = k0; k < k1; ++k) {
     const uint32_t c = pl.counts[k];
     const uint32_t ch = c == 0 ? 1u : (c + len - 1) / len;
-    items += ch;
+    whole += c / len;
+    rest += ch - c / len;
     slots += ch > 1 ? ch : 0u;
   }
-  uint32_t item = block_scan(items, sums, total);
+  uint32_t item = block_scan(whole, sums, wholes);
+  uint32_t end = block_scan(rest, sums, rests) + wholes;
   if (threadIdx.x == 0) {
-    *pl.head = total;
+    *pl.head = wholes + rests;
     *pl.chunk_len = len;
   }
   uint32_t slot = block_scan(slots, sums, unused);
@@ -241,9 +265,11 @@ __global__ void __launch_bounds__(1024)
     pl.offs[k] = off;
     pl.chunks[k] = ch;
     pl.slot0[k] = slot;
-    for (uint32_t i = 0; i < ch; ++i) pl.item[item + i] = make_uint2(k, i);
+    for (uint32_t i = 0; i < ch; ++i) {
+      uint2 *to = pl.item + (i < c / len ? item++ : end++);
+      *to = make_uint2(k, i);
+    }
     off += c;
-    item += ch;
     slot += ch > 1 ? ch : 0u;
   }
 }
@@ -300,8 +326,8 @@ struct KvSmem {
   // and the first query's position
   static constexpr int kStat = (8 + 1) * kRowTile * 4 + 64;
   static constexpr int kOffBar = kOffStat + kKvStages * kStat;
-  // kv_full st_full[3] st_empty[3] sdp_full[2] ds_full[2] acc_full
-  static constexpr int kOffMisc = kOffBar + 12 * 8;
+  // kv_full acc_full sdp_full[2] ds_full[2] st_full[] st_empty[]
+  static constexpr int kOffMisc = kOffBar + (6 + 2 * kKvStages) * 8;
   static constexpr int kBytes = kOffMisc + 32 + 1024;
 };
 
@@ -337,11 +363,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return reinterpret_cast<float *>(smem + L::kOffStat + st * L::kStat);
   };
   const uint32_t bars = base + L::kOffBar;
-  const uint32_t kv_full = bars, acc_full = bars + 88;
-  auto st_full = [&](int i) { return bars + 8 + 8 * i; };
-  auto st_empty = [&](int i) { return bars + 32 + 8 * i; };
-  auto sdp_full = [&](int i) { return bars + 56 + 8 * i; };
-  auto ds_full = [&](int i) { return bars + 72 + 8 * i; };
+  const uint32_t kv_full = bars, acc_full = bars + 8;
+  auto sdp_full = [&](int i) { return bars + 16 + 8 * i; };
+  auto ds_full = [&](int i) { return bars + 32 + 8 * i; };
+  auto st_full = [&](int i) { return bars + 48 + 8 * i; };
+  auto st_empty = [&](int i) { return bars + 48 + 8 * (kKvStages + i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
 
@@ -632,12 +658,14 @@ done:
   }
 }
 
-// Adds the chunks of the key tiles that have several.
+// Adds the chunks of the key tiles that have several; kJoinParts CTAs a tile.
+constexpr int kJoinParts = 16;
 template <int D>
 __global__ void __launch_bounds__(256)
     bwd_join_kernel(const BlockAttn p, const BwdPlan pl, __nv_bfloat16 *gk,
                     __nv_bfloat16 *gv) {
-  const int k = blockIdx.x / pl.rep, r = blockIdx.x % pl.rep;
+  const int kr = blockIdx.x / kJoinParts;
+  const int k = kr / pl.rep, r = kr % pl.rep;
   const uint32_t ch = pl.chunks[k];
   if (ch <= 1) return;
   const int kt = k % pl.nkt, bh = k / pl.nkt;
@@ -645,12 +673,14 @@ __global__ void __launch_bounds__(256)
   const size_t stride = (size_t)pl.rep * 2 * kKeyTile * D;
   const float *part = pl.part + ((size_t)pl.slot0[k] * pl.rep + r) * 2 *
                                     kKeyTile * D;
-  for (int x = threadIdx.x; x < 2 * kKeyTile * D / 4; x += 256) {
-    const int e = x * 4;
+  constexpr int kPart = 2 * kKeyTile * D / 4 / kJoinParts;
+  for (int x = threadIdx.x; x < kPart; x += 256) {
+    const int e = (blockIdx.x % kJoinParts * kPart + x) * 4;
     const int which = e / (kKeyTile * D), key = e / D % kKeyTile, d = e % D;
     const long long j = (long long)kt * kKeyTile + key;
     if (j >= p.T) continue;
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (uint32_t c = 0; c < ch; ++c) {
       const float4 v =
           *reinterpret_cast<const float4 *>(part + c * stride + e);
@@ -675,8 +705,8 @@ struct DqSmem {
   static constexpr int kOffQ = 0;
   static constexpr int kOffG = kTile;
   static constexpr int kOffBar = 2 * kTile;
-  // q_full kv_full[3] kv_empty[3] sdp_full[2] ds_full[2] acc_full
-  static constexpr int kOffMisc = kOffBar + 12 * 8;
+  // q_full acc_full sdp_full[2] ds_full[2] kv_full[] kv_empty[]
+  static constexpr int kOffMisc = kOffBar + (6 + 2 * kKvStages) * 8;
   static constexpr int kOffS = 2 * kTile + 1024;  // stages: K, V
   static int bytes(int stages, int nblk, int cap) {
     return kOffS + stages * 2 * kKey + nblk * 4 + ((cap * 2 + 15) & ~15) +
@@ -716,11 +746,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return (uint32_t)((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
   };
   const uint32_t bars = base + L::kOffBar;
-  const uint32_t q_full = bars, acc_full = bars + 88;
-  auto kv_full = [&](int i) { return bars + 8 + 8 * i; };
-  auto kv_empty = [&](int i) { return bars + 32 + 8 * i; };
-  auto sdp_full = [&](int i) { return bars + 56 + 8 * i; };
-  auto ds_full = [&](int i) { return bars + 72 + 8 * i; };
+  const uint32_t q_full = bars, acc_full = bars + 8;
+  auto sdp_full = [&](int i) { return bars + 16 + 8 * i; };
+  auto ds_full = [&](int i) { return bars + 32 + 8 * i; };
+  auto kv_full = [&](int i) { return bars + 48 + 8 * i; };
+  auto kv_empty = [&](int i) { return bars + 48 + 8 * (kKvStages + i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -740,7 +770,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(acc_full, 1);
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < kKvStages; ++i) {
       mbar_init(kv_full(i), 1);
       mbar_init(kv_empty(i), 1);
     }
@@ -769,6 +799,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (tid == 32 * kTmaWarp) {
+    mbar_arrive_expect_tx(q_full, 2 * CH * pl.qt * p.G * 128);
+    for (int c = 0; c < CH; ++c) {
+      tma_load_4d(sQ + c * (kDqRows * 128), &tm_q, q_full, c * kChunk,
+                  hk * p.G, b, s0);
+      tma_load_4d(sG + c * (kDqRows * 128), &tm_go, q_full, c * kChunk,
+                  hk * p.G, b, s0);
+    }
+  }
   mark_blocks(p, b, s0, nq, hk, words, tid, kBwdThreads);
   __syncthreads();
   if (warp == 0) {
@@ -784,15 +823,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int n = (count * per + upt - 1) / upt;
 
   if (warp == kTmaWarp) {
-    if (n > 0 && lane == 0) {
-      mbar_arrive_expect_tx(q_full, 2 * CH * pl.qt * p.G * 128);
-      for (int c = 0; c < CH; ++c) {
-        tma_load_4d(sQ + c * (kDqRows * 128), &tm_q, q_full, c * kChunk,
-                    hk * p.G, b, s0);
-        tma_load_4d(sG + c * (kDqRows * 128), &tm_go, q_full, c * kChunk,
-                    hk * p.G, b, s0);
-      }
-    }
     int st = 0;
     uint32_t ph = 0;
     for (int i = 0; i < n; ++i) {
@@ -821,7 +851,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         return wait_bar_spin(bar, ph, abort_flag, p.status);
       };
       const uint64_t qd = sdesc_k_sw128(sQ), gd = sdesc_k_sw128(sG);
-      bool ok = n <= 0 || wait(q_full, 0);
+      bool ok = wait(q_full, 0);
       int st = 0, done = 0;
       uint32_t ph = 0, acc = 0;
       for (int i = 0; ok && i <= n; ++i) {
@@ -981,7 +1011,9 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
   auto bf = [](void *x) { return static_cast<__nv_bfloat16 *>(x); };
   if (!ok(cudaMemsetAsync(pl.counts, 0, pl.zero_bytes, st)))
     return DSA_ERR_CUDA;
-  bwd_delta_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(
+  constexpr int kDelta = 256 / (D / 8) * kDeltaRows;
+  bwd_delta_kernel<D><<<(unsigned)((rows + kDelta - 1) / kDelta), 256, 0,
+                        st>>>(
       static_cast<const __nv_bfloat16 *>(o),
       static_cast<const __nv_bfloat16 *>(go), lse, rows, pl.stat);
   const int mark_smem = p.nblk * 4 + pl.cap * 2;
@@ -1009,8 +1041,8 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
     return DSA_ERR_CUDA;
   dkv<<<(unsigned)pl.items * pl.rep, kBwdThreads, KvSmem<D>::kBytes, st>>>(
       tm_q, tm_go, maps, p, pl, bf(gk), bf(gv));
-  bwd_join_kernel<D><<<(unsigned)kts * pl.rep, 256, 0, st>>>(p, pl, bf(gk),
-                                                             bf(gv));
+  bwd_join_kernel<D><<<(unsigned)kts * pl.rep * kJoinParts, 256, 0, st>>>(
+      p, pl, bf(gk), bf(gv));
   if (!ok(cudaGetLastError())) return DSA_ERR_CUDA;
 
   DqPlan dp{};
@@ -1021,8 +1053,11 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
   dp.cap = (int)(most < p.nblk ? most : p.nblk);
   dp.stat = pl.stat;
   dp.gq = bf(gq);
-  // three stages unless a very long context's block words need the room
-  dp.stages = DqSmem<D>::bytes(3, p.nblk, dp.cap) <= kMaxSmem ? 3 : 2;
+  // fewer stages where a very long context's block words need the room
+  dp.stages = kKvStages;
+  while (dp.stages > 2 &&
+         DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap) > kMaxSmem)
+    --dp.stages;
   const int smem = DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap);
   rc = encode_q_heads(&tm_q, qp, dp.qt, p.G);
   if (rc == DSA_OK) rc = encode_q_heads(&tm_go, gp, dp.qt, p.G);
