@@ -11,8 +11,8 @@
 // longer than one query's list and the keys are read once for all of them;
 // where they do not, an MMA over 128 rows still takes no longer than one over
 // 16, so a query alone costs what it would cost in a tile of its own.
-//   S = Q K^T on the tensor cores (128 x 128, fp32 in tensor memory); each
-// softmax thread owns a row: maximum, moved only when a step exceeds it by
+//   S = Q K^T on the tensor cores (128 x 128, fp32 in tensor memory); a
+// softmax thread has half of a row in registers: maximum, moved only when a step exceeds it by
 // more than 2^8 (then O is rescaled), P = exp2(S c - m) rounded to bf16 into
 // columns of S that are done; O += P V with P from tensor memory.  A row holds
 // 16 neighbouring keys or none of them, so its mask is a choice of m or +inf
@@ -31,8 +31,9 @@
 // which a NaN or an infinity survives: rows with a sum or a result that is not
 // finite are computed again on their own (block_attn_row.cuh).
 //
-// Warps: 0 .. 3 softmax (warp w reads tensor-memory lanes 32 w .. + 31), 4
-// TMA producer, 5 MMA issuer and tensor-memory allocator.
+// Warps: 0 .. 7 softmax (warp w reads tensor-memory lanes 32 (w % 4) .. + 31,
+// 64 keys of a step: the two warps of a row exchange its maximum), 8 TMA
+// producer, 9 MMA issuer and tensor-memory allocator.
 #include "block_attn.cuh"
 #include "block_attn_host.cuh"
 #include "block_attn_row.cuh"
@@ -44,9 +45,11 @@ namespace {
 
 constexpr int kRows = 128;  // MMA rows of a query tile
 constexpr int kKeys = 128;  // keys of a step
-constexpr int kFwdThreads = 192;
-constexpr int kTmaWarp = 4, kMmaWarp = 5;
-constexpr uint32_t kTmS = 0, kTmO = 128;  // tensor-memory columns; P: 64
+constexpr int kSoftWarps = 8;  // two for each 32 rows, 64 keys each
+constexpr int kFwdThreads = 32 * (kSoftWarps + 2);
+constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+// tensor-memory columns; P takes the second half of each 64 of S
+constexpr uint32_t kTmS = 0, kTmO = 128;
 constexpr float kSlack = 8.f;
 
 // What a launch adds to the problem.
@@ -71,17 +74,49 @@ struct FwdSmem {
   static constexpr int kOffBar = 3 * kTile;
   // q_full k_full k_empty v_full v_empty s_full p_full o_full
   static constexpr int kOffMisc = kOffBar + 8 * 8;
-  static constexpr int kOffWords = kOffMisc + 32;
+  static constexpr int kOffRed = kOffMisc + 32;  // [4][128]
+  static constexpr int kOffWords = kOffRed + 4 * kRows * 4;
   static int bytes(int nblk, int cap) {
     return kOffWords + nblk * 4 + ((cap * 2 + 15) & ~15) + 1024;
   }
 };
 
+// One row on its own, by one warp (qs: 128 floats of shared memory).  Out of
+// line: it is rare, and inlined it costs the loop before it registers.
+__device__ __noinline__ void redo_row(const BlockAttn &p, const FwdPlan &pl,
+                                      int b, int s, int h, float *qs,
+                                      int lane) {
+  const size_t at = ((size_t)s * p.B + b) * p.H + h;
+  __syncwarp();
+  for (int d = lane; d < p.D; d += 32)
+    qs[d] = __bfloat162float(p.q[at * p.D + d]);
+  __syncwarp();
+  bool bad = false;
+  float acc[4], lse;
+  attn_row(p, b, s, h / p.G, qs, lane, bad, acc, lse);
+  for (int i = 0; i * 32 < p.D; ++i)
+    pl.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
+  if (lane == 0) pl.lse[at] = lse;
+}
+
+// The barrier of the two warps of 32 rows.  Its number is written out: one
+// that is computed makes the compiler claim all sixteen, and a second CTA no
+// longer fits the SM.
+__device__ __forceinline__ bool pair_bar(int quad, bool pred) {
+  switch (quad) {
+    case 0: return named_bar_or(1, 64, pred);
+    case 1: return named_bar_or(2, 64, pred);
+    case 2: return named_bar_or(3, 64, pred);
+    default: return named_bar_or(4, 64, pred);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     block_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ KvMaps maps,
-                          const BlockAttn p, const FwdPlan pl) {
+                          const __grid_constant__ BlockAttn p,
+                          const __grid_constant__ FwdPlan pl) {
   using L = FwdSmem<D>;
   constexpr int CH = L::kCh;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys);
@@ -117,7 +152,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const int nq = min(pl.qt, p.S - s0);
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(bars + 8 * i, i == 6 ? 4 : 1);
+    for (int i = 0; i < 8; ++i)
+      mbar_init(bars + 8 * i, i == 6 ? kSoftWarps : 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_q);
@@ -222,7 +258,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_bf16_ta(tmem + kTmO, tmem + kTmS + 64 + ks * 8,
+          mma_bf16_ta(tmem + kTmO, tmem + kTmS + (ks >> 2) * 64 + 32 + (ks & 3) * 8,
                       vd + ((ks * 2048) >> 4), kIdescO, ks == 0 ? acc : 1u);
         mma_commit(v_empty);
         if (t + 1 == t1) mma_commit(o_full);
@@ -232,81 +268,74 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     __syncwarp();
   } else {
-    // ---------------- softmax: one row a thread ----------------
-    const int row = tid;
+    // ---------- softmax: a thread takes a row's keys 64 half .. + 63 ----------
+    const int half = warp >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
     const int qi = row / p.G;
     const bool live = qi < nq;
-    const int s = s0 + (live ? qi : 0), h = hk * p.G + row % p.G;
-    const int pos = live ? key_pos(p, b, s) : -1;
+    const int pos = live ? key_pos(p, b, s0 + qi) : -1;
     // the last key that the first and that any row of the tile sees
     const int pos_lo = key_pos(p, b, s0), pos_hi = key_pos(p, b, s0 + nq - 1);
     const float c2 = p.scale * 1.4426950408889634f;
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t tS = tmem + kTmS + lane_off, tO = tmem + kTmO + lane_off;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t tS = tmem + kTmS + lane_off + half * 64,
+                   tO = tmem + kTmO + lane_off + half * (D / 2);
+    float *red = reinterpret_cast<float *>(smem + L::kOffRed);
     float m = neg_inf;
     float2 l2[2] = {};
+    // the two warps of 32 rows meet at a barrier every step: a wait that
+    // gave up is carried to it, so that both leave together
+    bool fail = false;
     for (int t = t0; t < t1; ++t) {
       const uint32_t ph = (t - t0) & 1u;
-      uint32_t mask[4], held = 0u;
-      bool diag[4];
+      uint32_t mask[2];
+      bool held[2], diag[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         int end;
-        mask[c] = step_mask(words, list, t * bpt, count, p.lb, c, qi & 31,
-                            pos, end);
+        mask[c] = step_mask(words, list, t * bpt, count, p.lb, 2 * half + c,
+                            qi & 31, pos, end);
         diag[c] = end > pos_lo;
-        if (__any_sync(0xffffffffu, mask[c] != 0u)) held |= 1u << c;
+        held[c] = __any_sync(0xffffffffu, mask[c] != 0u);
       }
-      if (!__all_sync(0xffffffffu,
-                      wait_bar_spin(s_full, ph, abort_flag, p.status)))
-        goto done;
+      fail |= !__all_sync(0xffffffffu, wait_bar_spin(s_full, ph, abort_flag,
+                                                     p.status));
       tc_fence_after();
-      // Pass 1: the row's maximum, two chunks of 32 keys at a time; the
-      // second two stay in registers.
-      uint32_t u[2][32];
+      // the row's maximum, 32 keys at a time; the second 32 stay
+      uint32_t u[32];
       float mx = neg_inf;
-      auto fetch = [&](int c, uint32_t(&x)[32]) {
+      auto fetch = [&](int c) {
         __syncwarp();
-        tmem_ld32(tS + c * 32, x);
+        tmem_ld32(tS + c * 32, u);
+        tmem_ld_wait();
+        reg_fence32(u);
+        if (diag[c]) {  // keys after some row's position: one by one
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            u[i] = mask[c] >> i & 1u ? u[i] : 0xff800000u;
+        }
       };
-      // keys after some row's position: one by one
-      auto hide = [&](int c, uint32_t(&x)[32]) {
-        if (!diag[c]) return;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = mask[c] >> i & 1u ? x[i] : 0xff800000u;
-      };
-      auto chunk_max = [&](int c, const uint32_t(&x)[32]) {
-        float a[2] = {neg_inf, neg_inf};
+      for (int c = 0; c < 2; ++c) {
+        if (!held[c]) continue;
+        fetch(c);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float e = neg_inf;
+        for (int g = 0; g < 2; ++g) {
+          float a = neg_inf, e = neg_inf;
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            a[h] = fmaxf(a[h], fmaxf(__uint_as_float(x[16 * h + i]),
-                                     __uint_as_float(x[16 * h + i + 1])));
-            e = fmaxf(e, fmaxf(__uint_as_float(x[16 * h + i + 2]),
-                               __uint_as_float(x[16 * h + i + 3])));
+          for (int i = 16 * g; i < 16 * g + 16; i += 4) {
+            a = fmaxf(a, fmaxf(__uint_as_float(u[i]),
+                               __uint_as_float(u[i + 1])));
+            e = fmaxf(e, fmaxf(__uint_as_float(u[i + 2]),
+                               __uint_as_float(u[i + 3])));
           }
           // a row holds all 16 keys or none, or they are hidden above
-          if (mask[c] & (0xffffu << (16 * h))) mx = fmaxf(mx, fmaxf(a[h], e));
-        }
-      };
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        if (held & (3u << c)) {
-          fetch(c, u[0]);
-          fetch(c + 1, u[1]);
-          tmem_ld_wait();
-          reg_fence32(u[0]);
-          reg_fence32(u[1]);
-          hide(c, u[0]);
-          hide(c + 1, u[1]);
-          chunk_max(c, u[0]);
-          chunk_max(c + 1, u[1]);
+          if (mask[c] & (0xffffu << (16 * g))) mx = fmaxf(mx, fmaxf(a, e));
         }
       }
-      mx *= c2;
+      red[half * kRows + row] = mx;
+      if (pair_bar(quad, fail)) goto done;
+      mx = fmaxf(mx, red[(half ^ 1) * kRows + row]) * c2;
       // a row without a key so far keeps m = -inf and weights of zero
       const bool move = mx > m + kSlack;
       if (__any_sync(0xffffffffu, move && t > t0)) {
@@ -314,34 +343,36 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         l2[0] = __fmul2_rn(l2[0], make_float2(f, f));
         l2[1] = __fmul2_rn(l2[1], make_float2(f, f));
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t w[32];
+        for (int c = 0; c < D / 32; ++c) {  // half of O's columns
+          uint32_t w[16];
           __syncwarp();
-          tmem_ld32(tO + c * 32, w);
+          tmem_ld16(tO + c * 16, w);
           tmem_ld_wait();
-          reg_fence32(w);
+          reg_fence16(w);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < 16; ++i)
             w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-          tmem_st32(tO + c * 32, w);
+          tmem_st16(tO + c * 16, w);
         }
       }
       if (move) m = mx;
       const float mu = m > neg_inf ? m : 0.f;
-      // Pass 2: P = exp2(S c2 - mu), chunks 3, 2 from registers, then 1, 0;
-      // P's columns begin at 64, in chunks that are done.
-      auto weights = [&](int c, const uint32_t(&x)[32]) {
+      // P = exp2(S c2 - mu) into the second half of the 64 columns of S
+#pragma unroll
+      for (int c = 1; c >= 0; --c) {
         uint32_t pk[16];
-        if (held >> c & 1u) {
+        if (held[c]) {
+          if (c == 0) fetch(0);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int g = 0; g < 2; ++g) {
             // -inf takes the weights of keys that the row does not hold to 0
-            const float sub = mask[c] & (0xffffu << (16 * h)) ? -mu : neg_inf;
+            const float sub = mask[c] & (0xffffu << (16 * g)) ? -mu : neg_inf;
 #pragma unroll
-            for (int i = 16 * h; i < 16 * h + 16; i += 2) {
-              float2 e = __ffma2_rn(
-                  make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])),
-                  make_float2(c2, c2), make_float2(sub, sub));
+            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(u[i]),
+                                                __uint_as_float(u[i + 1])),
+                                    make_float2(c2, c2),
+                                    make_float2(sub, sub));
               e.x = ex2(e.x);
               e.y = ex2(e.y);
               l2[(i >> 1) & 1] = __fadd2_rn(l2[(i >> 1) & 1], e);
@@ -353,40 +384,23 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           for (int i = 0; i < 16; ++i) pk[i] = 0u;
         }
         __syncwarp();
-        tmem_st16(tS + 64 + c * 16, pk);
-      };
-      weights(3, u[1]);
-      if (held & 2u) fetch(1, u[1]);
-      weights(2, u[0]);
-      if (held & 2u) {
-        tmem_ld_wait();
-        reg_fence32(u[1]);
-        hide(1, u[1]);
+        tmem_st16(tS + 32 + c * 16, pk);
       }
-      if (held & 1u) fetch(0, u[0]);
-      weights(1, u[1]);
-      if (held & 1u) {
-        tmem_ld_wait();
-        reg_fence32(u[0]);
-        hide(0, u[0]);
-      }
-      weights(0, u[0]);
       tmem_st_wait();
       tc_fence_before();
-      if (diag[0] || diag[1] || diag[2] || diag[3]) {
-        // V rows of this step that no row sees
-        const int i = t * bpt + (row >> p.lb);
-        const bool over =
-            i < count &&
-            (list[i] << p.lb) + (row & (p.blk - 1)) > pos_hi;
+      if (diag[0] || diag[1]) {
+        // V rows of this step that no row sees; each half its 64 keys
+        const int kr = half * 64 + (row & 63);
+        const int i = t * bpt + (kr >> p.lb);
+        const bool over = row < 64 && i < count &&
+                          (list[i] << p.lb) + (kr & (p.blk - 1)) > pos_hi;
         if (__any_sync(0xffffffffu, over)) {
-          if (!__all_sync(0xffffffffu,
-                          wait_bar_spin(v_full, ph, abort_flag, p.status)))
-            goto done;
+          fail |= !__all_sync(0xffffffffu, wait_bar_spin(v_full, ph, abort_flag,
+                                                         p.status));
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
-          if (over)
+          if (over && !fail)
             for (int c = 0; c < CH * 8; ++c)
-              st_shared_v4(sV + (c >> 3) * (kRows * 128) + row * 128 +
+              st_shared_v4(sV + (c >> 3) * (kRows * 128) + kr * 128 +
                                (c & 7) * 16,
                            z);
           fence_proxy_async_smem();
@@ -395,24 +409,28 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
     }
+    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+    red[half * kRows + row] = l;
+    if (pair_bar(quad, fail)) goto done;
+    l += red[(half ^ 1) * kRows + row];
     // ---------------- o = O / l ----------------
     if (t1 > t0) {
-      if (!__all_sync(0xffffffffu,
-                      wait_bar_spin(o_full, 0, abort_flag, p.status)))
-        goto done;
+      fail = !__all_sync(0xffffffffu,
+                         wait_bar_spin(o_full, 0, abort_flag, p.status));
       tc_fence_after();
     }
-    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const bool some = l > 0.f || l != l;
     const float inv = some ? 1.f / l : 0.f;
     bool odd = l != l || l > 3e38f;  // not finite: computed again below
-    const size_t at = ((size_t)s * p.B + b) * p.H + h;
+    const size_t at =
+        ((size_t)(s0 + qi) * p.B + b) * p.H + hk * p.G + row % p.G;
     const size_t part =
         ((size_t)(blockIdx.x / pl.splits) * pl.splits + split) *
             (pl.qt * p.G) +
         row;
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
+    for (int c = 0; c < D / 64; ++c) {  // half of the columns
+      const int d0 = half * (D / 2) + c * 32;
       uint32_t u[32];
       if (t1 > t0) {
         __syncwarp();
@@ -428,14 +446,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       }
       if (!live) {
       } else if (pl.splits > 1) {
-        float4 *dst = reinterpret_cast<float4 *>(pl.part_o + part * D + c * 32);
+        float4 *dst = reinterpret_cast<float4 *>(pl.part_o + part * D + d0);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           dst[i] = make_float4(
               __uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
               __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
       } else {
-        uint4 *dst = reinterpret_cast<uint4 *>(pl.o + at * D + c * 32);
+        uint4 *dst = reinterpret_cast<uint4 *>(pl.o + at * D + d0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t w[4];
@@ -447,8 +465,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
       }
     }
-    odd &= live;
-    if (live) {
+    // a row that is not finite in either half
+    red[(2 + half) * kRows + row] = odd && live ? 1.f : 0.f;
+    if (pair_bar(quad, fail)) goto done;
+    odd = live && (odd || red[(3 - half) * kRows + row] != 0.f);
+    if (live && half == 0) {
       const float lse2 = some ? m + log2f(l) : neg_inf;
       if (pl.splits > 1)
         // a NaN tells the joining kernel to compute the row again
@@ -456,24 +477,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       else
         pl.lse[at] = some ? lse2 * 0.69314718055994531f : neg_inf;
     }
-    unsigned todo = __ballot_sync(0xffffffffu, odd);
+    unsigned todo = __ballot_sync(0xffffffffu, odd && half == 0);
     if (pl.splits == 1) {
       // K's space is free: the last product is done
       float *qs = reinterpret_cast<float *>(smem + L::kOffK) + warp * 128;
       for (; todo; todo &= todo - 1) {
-        const int r = warp * 32 + __ffs(todo) - 1;
-        const int sr = s0 + r / p.G, hr = hk * p.G + r % p.G;
-        const size_t ar = ((size_t)sr * p.B + b) * p.H + hr;
-        __syncwarp();
-        for (int d = lane; d < D; d += 32)
-          qs[d] = __bfloat162float(p.q[ar * D + d]);
-        __syncwarp();
-        bool bad = false;
-        float acc[4], ls;
-        attn_row(p, b, sr, hk, qs, lane, bad, acc, ls);
-        for (int i = 0; i * 32 < D; ++i)
-          pl.o[ar * D + lane + 32 * i] = __float2bfloat16(acc[i]);
-        if (lane == 0) pl.lse[ar] = ls;
+        const int r = quad * 32 + __ffs(todo) - 1;
+        redo_row(p, pl, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
       }
     }
   }
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(256)
       qs[d] = __bfloat162float(p.q[r * p.D + d]);
     __syncwarp();
     bool bad = false;
-    attn_row(p, b, s, hk, qs, lane, bad, acc, ls);
+    attn_row(p, b, s, h / p.G, qs, lane, bad, acc, ls);
   } else if (mx > neg_inf) {
     float sum = 0.f;
     for (int i = 0; i < pl.splits; ++i) {

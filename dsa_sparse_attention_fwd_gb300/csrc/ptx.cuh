@@ -109,6 +109,20 @@ __device__ __forceinline__ bool wait_bar_inl(uint32_t bar, uint32_t parity,
   return wait_bar_loop(bar, parity, abort_flag, status);
 }
 
+// As mbar_try_wait, the thread suspended for up to `ns` nanoseconds.
+__device__ __forceinline__ bool mbar_try_wait_ns(uint32_t bar, uint32_t parity,
+                                                 uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // wait_bar_inl() that polls a while before it reads the timer: for chains of
 // short waits (a few microseconds at most), where the read would be part of
 // each link.
@@ -116,8 +130,8 @@ __device__ __forceinline__ bool wait_bar_spin(uint32_t bar, uint32_t parity,
                                               volatile int *abort_flag,
                                               int *status) {
 #pragma unroll 1
-  for (int it = 0; it < 1024; ++it)
-    if (mbar_try_wait(bar, parity)) return true;
+  for (int it = 0; it < 64; ++it)
+    if (mbar_try_wait_ns(bar, parity, 1000000u)) return true;
   return wait_bar_poll(bar, parity, abort_flag, status);
 }
 
