@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const int s0 = tile * pl.qt;
   const int nq = min(pl.qt, p.S - s0);
 
+  const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
   if (tid == 0) {
     for (int i = 0; i < 8; ++i)
       mbar_init(bars + 8 * i, i == 6 ? kSoftWarps : 1);
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk,
                   hk * p.G, b, s0);
   }
-  mark_blocks(p, b, s0, nq, hk, words, tid, kFwdThreads);
+  mark_blocks(p, b, s0, nq, hk, words, tid, kFwdThreads, first);
   __syncthreads();
   if (warp == 0) {
     const int n = list_blocks(words, p.nblk, list, lane);
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t full = kv ? v_full : k_full;
         if (!__all_sync(0xffffffffu,
-                        wait_bar_spin(kv ? v_empty : k_empty, ph ^ 1u,
+                        wait_bar_rest(kv ? v_empty : k_empty, ph ^ 1u,
                                      abort_flag, p.status)))
           goto done;
         if (lane == 0) mbar_arrive_expect_tx(full, nb * p.blk * CH * 128);
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // ---------------- MMA issuer: one thread ----------------
     if (elect_one()) {
       auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
-        return wait_bar_spin(bar, ph, abort_flag, p.status);
+        return wait_bar_rest(bar, ph, abort_flag, p.status);
       };
       const uint64_t qd = sdesc_k_sw128(sQ), kd = sdesc_k_sw128(sK);
       const uint64_t vd = sdesc_mn_sw128(sV, kRows * 128, 1024);
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         diag[c] = end > pos_lo;
         held[c] = __any_sync(0xffffffffu, mask[c] != 0u);
       }
-      fail |= !__all_sync(0xffffffffu, wait_bar_spin(s_full, ph, abort_flag,
+      fail |= !__all_sync(0xffffffffu, wait_bar_rest(s_full, ph, abort_flag,
                                                      p.status));
       tc_fence_after();
       // the row's maximum, 32 keys at a time; the second 32 stay
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         const bool over = row < 64 && i < count &&
                           (list[i] << p.lb) + (kr & (p.blk - 1)) > pos_hi;
         if (__any_sync(0xffffffffu, over)) {
-          fail |= !__all_sync(0xffffffffu, wait_bar_spin(v_full, ph, abort_flag,
+          fail |= !__all_sync(0xffffffffu, wait_bar_rest(v_full, ph, abort_flag,
                                                          p.status));
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
           if (over && !fail)
@@ -416,7 +417,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // ---------------- o = O / l ----------------
     if (t1 > t0) {
       fail = !__all_sync(0xffffffffu,
-                         wait_bar_spin(o_full, 0, abort_flag, p.status));
+                         wait_bar_rest(o_full, 0, abort_flag, p.status));
       tc_fence_after();
     }
     const bool some = l > 0.f || l != l;
@@ -428,8 +429,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         ((size_t)(blockIdx.x / pl.splits) * pl.splits + split) *
             (pl.qt * p.G) +
         row;
-#pragma unroll 1
-    for (int c = 0; c < D / 64; ++c) {  // half of the columns
+    // half of the columns; Q's space is free for the way out
+    const uint32_t out_buf = sQ + warp * (32 * D);
+    constexpr int kOut = D / 4;  // words of this half's bf16 row
+    uint32_t ow[kOut];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
       const int d0 = half * (D / 2) + c * 32;
       uint32_t u[32];
       if (t1 > t0) {
@@ -444,27 +449,24 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         odd |= !(fabsf(v) < 3e38f);
         u[i] = __float_as_uint(v);
       }
-      if (!live) {
-      } else if (pl.splits > 1) {
-        float4 *dst = reinterpret_cast<float4 *>(pl.part_o + part * D + d0);
+      if (pl.splits > 1) {
+        if (live) {
+          float4 *dst = reinterpret_cast<float4 *>(pl.part_o + part * D + d0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(
-              __uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-              __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
-      } else {
-        uint4 *dst = reinterpret_cast<uint4 *>(pl.o + at * D + d0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(u[8 * i + 2 * e]),
-                               __uint_as_float(u[8 * i + 2 * e + 1]));
-          dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(
+                __uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
         }
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        ow[c * 16 + i] = pack_bf16x2(__uint_as_float(u[2 * i]),
+                                     __uint_as_float(u[2 * i + 1]));
     }
+    if (pl.splits == 1)
+      store_rows<kOut>(out_buf, ow,
+                       live ? pl.o + at * D + half * (D / 2) : nullptr, lane);
     // a row that is not finite in either half
     red[(2 + half) * kRows + row] = odd && live ? 1.f : 0.f;
     if (pair_bar(quad, fail)) goto done;

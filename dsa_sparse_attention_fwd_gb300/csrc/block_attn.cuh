@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace dsa {
 
@@ -71,23 +72,43 @@ __host__ __device__ __forceinline__ int tile_queries(int G, int rows) {
 
 // The blocks that the queries s0 .. s0 + nq - 1 of sequence b attend to
 // under key head hk: words[n] gets bit i where query s0 + i holds block n.
-// Every thread of the CTA takes part; the caller has zeroed words[0 .. nblk)
-// and synchronises before and after.
+// Every thread of the CTA takes part.  The first call looks up the thread's
+// first candidate (three loads in a row, that need no shared memory yet), the
+// second, after the words have been cleared, marks it and the others.
+struct FirstMark {
+  int n, i;  // block (-1: none), query
+  bool bad;
+};
+__device__ __forceinline__ int mark_at(const BlockAttn &p, int b, int s0,
+                                       int hk, long long pos0, int i, int c,
+                                       bool &bad) {
+  int n = candidate(p, row_ids(p, b, s0 + i, hk), pos0 + i, c, bad);
+  if (n >= 0 && p.table && block_page(p, b, n, bad) < 0) n = -1;
+  return n;
+}
+__device__ __forceinline__ FirstMark first_mark(const BlockAttn &p, int b,
+                                                int s0, int nq, int hk,
+                                                int tid) {
+  const int n_cand = p.topk + p.local;
+  FirstMark f{-1, tid / n_cand, false};
+  if (tid < nq * n_cand)
+    f.n = mark_at(p, b, s0, hk, row_pos(p.q_pos, b, s0), f.i,
+                  tid - f.i * n_cand, f.bad);
+  return f;
+}
 __device__ __forceinline__ void mark_blocks(const BlockAttn &p, int b, int s0,
                                             int nq, int hk, uint32_t *words,
-                                            int tid, int nthreads) {
+                                            int tid, int nthreads,
+                                            FirstMark f) {
   const int n_cand = p.topk + p.local;
-  const long long pos0 = row_pos(p.q_pos, b, s0);
-  bool bad = false;
-  for (int x = tid; x < nq * n_cand; x += nthreads) {
+  if (f.n >= 0) atomicOr(words + f.n, 1u << f.i);
+  for (int x = tid + nthreads; x < nq * n_cand; x += nthreads) {
     const int i = x / n_cand;
-    const int n = candidate(p, row_ids(p, b, s0 + i, hk), pos0 + i,
-                            x - i * n_cand, bad);
-    if (n < 0) continue;
-    if (p.table && block_page(p, b, n, bad) < 0) continue;
-    atomicOr(words + n, 1u << i);
+    const int n = mark_at(p, b, s0, hk, row_pos(p.q_pos, b, s0), i,
+                          x - i * n_cand, f.bad);
+    if (n >= 0) atomicOr(words + n, 1u << i);
   }
-  if (bad) atomicOr(p.status, kStatusIndexRange);
+  if (f.bad) atomicOr(p.status, kStatusIndexRange);
 }
 
 // The marked blocks in ascending order; one warp.  Returns their number.
@@ -147,6 +168,36 @@ __device__ __forceinline__ uint32_t step_mask(const uint32_t *words,
     m |= first_keys(held ? pos - n * 16 + 1 : 0, 16) << (16 * u);
   }
   return m;
+}
+
+// A warp's 32 rows of NW words to memory, lane = row, `dst` its address
+// (nullptr: not written), through NW * 128 bytes of shared memory, so that a
+// store covers whole rows: written from the lanes' own rows, the output of a
+// forward tile took 6000 cycles.
+template <int NW>
+__device__ __forceinline__ void store_rows(uint32_t buf,
+                                           const uint32_t (&w)[NW], void *dst,
+                                           int lane) {
+  constexpr int NC = NW / 4;  // 16-byte pieces of a row
+  auto at = [&](int r, int c) {
+    const int sw = NC == 8 ? r & 7 : (r >> 1) & 3;
+    return buf + (uint32_t)(r * NC + (c ^ sw)) * 16;
+  };
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const uint32_t v[4] = {w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]};
+    st_shared_v4(at(lane, c), v);
+  }
+  __syncwarp();
+  const unsigned long long d = reinterpret_cast<unsigned long long>(dst);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int r = (i * 32 + lane) / NC, c = lane % NC;
+    const float4 v = ld_shared_v4f(at(r, c));
+    const unsigned long long to = __shfl_sync(0xffffffffu, d, r);
+    if (to) *reinterpret_cast<float4 *>(to + c * 16) = v;
+  }
+  __syncwarp();
 }
 
 // TMA coordinates of block n of sequence b, for a map made with

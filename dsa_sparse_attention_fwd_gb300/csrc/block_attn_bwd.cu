@@ -183,9 +183,10 @@ __global__ void __launch_bounds__(128)
   const long long bh = it / pl.nqt;
   const int b = (int)(bh / p.sel_heads), hs = (int)(bh % p.sel_heads);
   const int s0 = tile * pl.qt, nq = min(pl.qt, p.S - s0);
+  const FirstMark first = first_mark(p, b, s0, nq, hs, tid);
   for (int n = tid; n < p.nblk; n += 128) words[n] = 0u;
   __syncthreads();
-  mark_blocks(p, b, s0, nq, hs, words, tid, 128);
+  mark_blocks(p, b, s0, nq, hs, words, tid, 128, first);
   __syncthreads();
   if (tid < 32) {
     const int n = list_blocks(words, p.nblk, list, lane);
@@ -431,23 +432,37 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const long long q0 = row_pos(p.q_pos, b, 0);
     const int qr[2] = {lane / p.G, (lane + 32) / p.G};  // queries of two rows
     const int hr[2] = {lane % p.G, (lane + 32) % p.G};
-    for (int i = 0; i < n; ++i) {
-      const int st = i % kKvStages;
-      const uint32_t ph = (i / kKvStages) & 1u;
-      const int s0 = (int)pl.eq[e0 + i] * pl.qt;
-      const int nq = min(pl.qt, p.S - s0);
-      float2 v[2];
+    // What a step needs from memory is asked for one step before, and the
+    // query tile's number two before.
+    float2 v[2], v1[2];
+    uint32_t m, m1;
+    auto ask = [&](int i, int tile, float2(&to)[2], uint32_t &tm) {
+      const int s0 = tile * pl.qt, nq = min(pl.qt, p.S - s0);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        v[u] = make_float2(inf, 0.f);
-        if (qr[u] < nq)
-          v[u] = pl.stat[((size_t)(s0 + qr[u]) * p.B + b) * p.H + hk * p.G +
-                         hr[u]];
+        to[u] = make_float2(inf, 0.f);
+        if (i < n && qr[u] < nq)
+          to[u] = __ldg(pl.stat + ((size_t)(s0 + qr[u]) * p.B + b) * p.H +
+                        hk * p.G + hr[u]);
       }
-      const uint32_t m =
-          lane < pl.bpt ? pl.em[(size_t)(e0 + i) * pl.bpt + lane] : 0u;
-      if (!__all_sync(0xffffffffu, wait_bar_spin(st_empty(st), ph ^ 1u,
-                                                abort_flag, p.status)))
+      tm = i < n && lane < pl.bpt
+               ? __ldg(pl.em + (size_t)(e0 + i) * pl.bpt + lane)
+               : 0u;
+    };
+    int tile0 = n > 0 ? (int)__ldg(pl.eq + e0) : 0;
+    int tile1 = n > 1 ? (int)__ldg(pl.eq + e0 + 1) : 0;
+    ask(0, tile0, v1, m1);
+    int st = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n; ++i) {
+      const int s0 = tile0 * pl.qt;
+      const int nq = min(pl.qt, p.S - s0);
+      v[0] = v1[0], v[1] = v1[1], m = m1;
+      ask(i + 1, tile1, v1, m1);
+      tile0 = tile1;
+      tile1 = i + 2 < n ? (int)__ldg(pl.eq + e0 + i + 2) : 0;
+      if (!__all_sync(0xffffffffu, wait_bar_rest(st_empty(st), ph ^ 1u,
+                                                 abort_flag, p.status)))
         goto done;
       float *sst = stat(st);
       for (int x = 0; x < pl.bpt; ++x) {
@@ -474,11 +489,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
       }
       __syncwarp();
+      if (++st == kKvStages) st = 0, ph ^= 1;
     }
   } else if (warp == kMmaWarp) {
     if (elect_one()) {
       auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
-        return wait_bar_spin(bar, ph, abort_flag, p.status);
+        return wait_bar_rest(bar, ph, abort_flag, p.status);
       };
       const uint64_t kd = sdesc_k_sw128(sK), vd = sdesc_k_sw128(sV);
       bool ok = n <= 0 || wait(kv_full, 0);
@@ -536,9 +552,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < n; ++i) {
       const int st = i % kKvStages;
       if (!__all_sync(0xffffffffu,
-                      wait_bar_spin(sdp_full(i & 1), (i >> 1) & 1u, abort_flag,
+                      wait_bar_rest(sdp_full(i & 1), (i >> 1) & 1u, abort_flag,
                                    p.status) &&
-                          wait_bar_spin(st_full(st), (i / kKvStages) & 1u,
+                          wait_bar_rest(st_full(st), (i / kKvStages) & 1u,
                                        abort_flag, p.status)))
         goto done;
       tc_fence_after();
@@ -605,7 +621,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // ---------------- dK (warpgroup 0), dV (1) ----------------
     if (n > 0) {
       if (!__all_sync(0xffffffffu,
-                      wait_bar_spin(acc_full, 0, abort_flag, p.status)))
+                      wait_bar_rest(acc_full, 0, abort_flag, p.status)))
         goto done;
       tc_fence_after();
     }
@@ -617,6 +633,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         (size_t)key * D;
     __nv_bfloat16 *out =
         (wg == 0 ? gk : gv) + (((size_t)j * p.B + b) * p.Hk + hk) * D;
+    // K's and V's space is free for the way out
+    const uint32_t out_buf = (wg == 0 ? sK : sV) + (warp & 3) * 4096;
+    const bool inside = j < p.T;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t u[32];
@@ -630,22 +649,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       for (int x = 0; x < 32; ++x)
         u[x] = n > 0 ? __float_as_uint(__uint_as_float(u[x]) * f) : 0u;
       if (!direct) {
-        uint4 *dst = reinterpret_cast<uint4 *>(part + c * 32);
+        store_rows<32>(out_buf, u, part + c * 32, lane);
+      } else {
+        uint32_t w[16];
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
-          dst[x] = make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2],
-                              u[4 * x + 3]);
-      } else if (j < p.T) {
-        uint4 *dst = reinterpret_cast<uint4 *>(out + c * 32);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(u[8 * x + 2 * e]),
-                               __uint_as_float(u[8 * x + 2 * e + 1]));
-          dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        for (int x = 0; x < 16; ++x)
+          w[x] = pack_bf16x2(__uint_as_float(u[2 * x]),
+                             __uint_as_float(u[2 * x + 1]));
+        store_rows<16>(out_buf, w, inside ? out + c * 32 : nullptr, lane);
       }
     }
   }
@@ -767,6 +778,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int s0 = tile * pl.qt;
   const int nq = min(pl.qt, p.S - s0);
 
+  const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
   if (tid == 0) {
     mbar_init(q_full, 1);
     mbar_init(acc_full, 1);
@@ -808,7 +820,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                   hk * p.G, b, s0);
     }
   }
-  mark_blocks(p, b, s0, nq, hk, words, tid, kBwdThreads);
+  mark_blocks(p, b, s0, nq, hk, words, tid, kBwdThreads, first);
   __syncthreads();
   if (warp == 0) {
     const int n = list_blocks(words, p.nblk, list, lane);
@@ -828,7 +840,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < n; ++i) {
       const int nu = min(upt, count * per - i * upt);
       const int ui = lane / CH, c = lane % CH;  // unit and chunk of this lane
-      if (!__all_sync(0xffffffffu, wait_bar_spin(kv_empty(st), ph ^ 1u,
+      if (!__all_sync(0xffffffffu, wait_bar_rest(kv_empty(st), ph ^ 1u,
                                                 abort_flag, p.status)))
         goto done;
       if (lane == 0)
@@ -848,7 +860,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   } else if (warp == kMmaWarp) {
     if (elect_one()) {
       auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
-        return wait_bar_spin(bar, ph, abort_flag, p.status);
+        return wait_bar_rest(bar, ph, abort_flag, p.status);
       };
       const uint64_t qd = sdesc_k_sw128(sQ), gd = sdesc_k_sw128(sG);
       bool ok = wait(q_full, 0);
@@ -910,7 +922,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           step_mask(words, list, unit < p.blk ? i >> 1 : i * upt, count, p.lb,
                     wg + (unit < p.blk ? (i & 1) * 2 : 0), qi & 31, pos, end);
       const bool any = __any_sync(0xffffffffu, mask != 0u);
-      if (!__all_sync(0xffffffffu, wait_bar_spin(sdp_full(i & 1), (i >> 1) & 1u,
+      if (!__all_sync(0xffffffffu, wait_bar_rest(sdp_full(i & 1), (i >> 1) & 1u,
                                                 abort_flag, p.status)))
         goto done;
       tc_fence_after();
@@ -958,36 +970,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     if (n > 0) {
       if (!__all_sync(0xffffffffu,
-                      wait_bar_spin(acc_full, 0, abort_flag, p.status)))
+                      wait_bar_rest(acc_full, 0, abort_flag, p.status)))
         goto done;
       tc_fence_after();
     }
-    // each warpgroup writes half of the columns
-#pragma unroll 1
-    for (int c = wg * (D / 64); c < (wg + 1) * (D / 64); ++c) {
+    // each warpgroup writes half of the columns; Q's space is free
+    uint32_t ow[D / 4];
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
       uint32_t u[32];
       if (n > 0) {
         __syncwarp();
-        tmem_ld32(tmem + kTmQ + lane_off + c * 32, u);
+        tmem_ld32(tmem + kTmQ + lane_off + wg * (D / 2) + c * 32, u);
         tmem_ld_wait();
         reg_fence32(u);
       }
 #pragma unroll
-      for (int x = 0; x < 32; ++x)
-        u[x] = n > 0 ? __float_as_uint(__uint_as_float(u[x]) * p.scale) : 0u;
-      if (live) {
-        uint4 *dst = reinterpret_cast<uint4 *>(pl.gq + at * D + c * 32);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(u[8 * x + 2 * e]),
-                               __uint_as_float(u[8 * x + 2 * e + 1]));
-          dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      for (int x = 0; x < 16; ++x)
+        ow[c * 16 + x] =
+            n > 0 ? pack_bf16x2(__uint_as_float(u[2 * x]) * p.scale,
+                                __uint_as_float(u[2 * x + 1]) * p.scale)
+                  : 0u;
     }
+    store_rows<D / 4>(sQ + warp * (32 * D), ow,
+                      live ? pl.gq + at * D + wg * (D / 2) : nullptr, lane);
   }
 done:
   __syncthreads();
