@@ -9,7 +9,10 @@
 // atomically and the results do not change from run to run:
 //   dq: a CTA takes a query tile (128 rows of queries x heads, as in the
 // forward) and walks the union of its blocks, 64 keys a step: S = Q K^T, dP =
-// dO V^T, dS in bf16 back into tensor memory, dQ += dS K.
+// dO V^T, dS in bf16 back into tensor memory, dQ += dS K.  Q and dO are operands
+// from tensor memory: with both operands in shared memory, a product with 64
+// columns is bound by reading its 128 rows again for each K step (48 cycles
+// against 32).
 //   dk, dv: a CTA takes 128 consecutive keys and walks the query tiles (64
 // rows) that hold one of their blocks: S^T = K Q^T, dP^T = V dO^T, dV += P^T
 // dO, dK += dS^T Q.  The list of these query tiles is the transpose of the
@@ -708,17 +711,15 @@ __global__ void __launch_bounds__(256)
 
 constexpr int kDqRows = 128, kDqKeys = 64;
 
+constexpr int kDqStages = 6;
 template <int D>
 struct DqSmem {
   static constexpr int kCh = D / 64;
-  static constexpr int kTile = kCh * kDqRows * 128;  // Q or dO
-  static constexpr int kKey = kCh * kDqKeys * 128;   // K or V of a stage
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffG = kTile;
-  static constexpr int kOffBar = 2 * kTile;
-  // q_full acc_full sdp_full[2] ds_full[2] kv_full[] kv_empty[]
-  static constexpr int kOffMisc = kOffBar + (6 + 2 * kKvStages) * 8;
-  static constexpr int kOffS = 2 * kTile + 1024;  // stages: K, V
+  static constexpr int kKey = kCh * kDqKeys * 128;  // K or V of a stage
+  static constexpr int kOffBar = 0;
+  // q_full acc_full sdp_full[2] ds_full[2] kv_full[] kv_empty[] q_here
+  static constexpr int kOffMisc = kOffBar + (7 + 2 * kDqStages) * 8;
+  static constexpr int kOffS = 1024;  // stages: K, V
   static int bytes(int stages, int nblk, int cap) {
     return kOffS + stages * 2 * kKey + nblk * 4 + ((cap * 2 + 15) & ~15) +
            1024;
@@ -741,27 +742,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr int CH = L::kCh;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kDqRows, kDqKeys);
   constexpr uint32_t kIdescA = idesc_bf16_f32_mn(kDqRows, D, false, true);
-  constexpr uint32_t kTmQ = 0, kTmBuf = 128;  // + 128 a step
+  // tensor memory: dQ, two steps' scores, Q and dO (bf16)
+  constexpr uint32_t kTmQ = 0, kTmBuf = 128, kTmA = 384, kTmG = 384 + D / 2;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw_addr);
-  const uint32_t sQ = base + L::kOffQ, sG = base + L::kOffG;
   auto sK = [&](int st) { return base + L::kOffS + st * 2 * L::kKey; };
   auto sV = [&](int st) { return sK(st) + L::kKey; };
-  auto roff = [](int ks) {
-    return (uint32_t)((ks >> 2) * (kDqRows * 128) + (ks & 3) * 32) >> 4;
-  };
   auto koff = [](int ks) {
     return (uint32_t)((ks >> 2) * (kDqKeys * 128) + (ks & 3) * 32) >> 4;
   };
   const uint32_t bars = base + L::kOffBar;
   const uint32_t q_full = bars, acc_full = bars + 8;
+  const uint32_t q_here = bars + 48 + 16 * kDqStages;
   auto sdp_full = [&](int i) { return bars + 16 + 8 * i; };
   auto ds_full = [&](int i) { return bars + 32 + 8 * i; };
   auto kv_full = [&](int i) { return bars + 48 + 8 * i; };
-  auto kv_empty = [&](int i) { return bars + 48 + 8 * (kKvStages + i); };
+  auto kv_empty = [&](int i) { return bars + 48 + 8 * (kDqStages + i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -780,9 +779,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
   const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
   if (tid == 0) {
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 8);
+    mbar_init(q_here, 1);
     mbar_init(acc_full, 1);
-    for (int i = 0; i < kKvStages; ++i) {
+    for (int i = 0; i < kDqStages; ++i) {
       mbar_init(kv_full(i), 1);
       mbar_init(kv_empty(i), 1);
     }
@@ -802,21 +802,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   for (int n = tid; n < p.nblk; n += kBwdThreads) words[n] = 0u;
-  // keys past a ragged step's blocks are read as an operand (times zero)
-  for (int i = tid; i < pl.stages * 2 * L::kKey / 16; i += kBwdThreads) {
-    const uint32_t z[4] = {0u, 0u, 0u, 0u};
-    st_shared_v4(base + L::kOffS + i * 16, z);
-  }
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Q and dO pass through the last two stages on their way to tensor memory
+  const uint32_t sQ = sK(pl.stages - 1), sG = sK(pl.stages - 2);
   if (tid == 32 * kTmaWarp) {
-    mbar_arrive_expect_tx(q_full, 2 * CH * pl.qt * p.G * 128);
+    mbar_arrive_expect_tx(q_here, 2 * CH * pl.qt * p.G * 128);
     for (int c = 0; c < CH; ++c) {
-      tma_load_4d(sQ + c * (kDqRows * 128), &tm_q, q_full, c * kChunk,
+      tma_load_4d(sQ + c * (kDqRows * 128), &tm_q, q_here, c * kChunk,
                   hk * p.G, b, s0);
-      tma_load_4d(sG + c * (kDqRows * 128), &tm_go, q_full, c * kChunk,
+      tma_load_4d(sG + c * (kDqRows * 128), &tm_go, q_here, c * kChunk,
                   hk * p.G, b, s0);
     }
   }
@@ -838,16 +834,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int st = 0;
     uint32_t ph = 0;
     for (int i = 0; i < n; ++i) {
-      const int nu = min(upt, count * per - i * upt);
+      if (i == pl.stages - 2 &&
+          !__all_sync(0xffffffffu,
+                      wait_bar_rest(q_full, 0, abort_flag, p.status)))
+        goto done;
       const int ui = lane / CH, c = lane % CH;  // unit and chunk of this lane
       if (!__all_sync(0xffffffffu, wait_bar_rest(kv_empty(st), ph ^ 1u,
                                                 abort_flag, p.status)))
         goto done;
       if (lane == 0)
-        mbar_arrive_expect_tx(kv_full(st), 2 * nu * unit * CH * 128);
+        mbar_arrive_expect_tx(kv_full(st), 2 * kDqKeys * CH * 128);
       __syncwarp();
-      if (ui < nu) {
-        const int x = i * upt + ui;
+      if (ui < upt) {
+        // a ragged step's end repeats the last unit: masked, but numbers
+        const int x = min(i * upt + ui, count * per - 1);
         const int tok = list[x / per] * p.blk + x % per * unit;
         const uint32_t at = c * (kDqKeys * 128) + ui * unit * 128;
         tma_load_4d(sK(st) + at, &maps.k, kv_full(st), c * kChunk, tok,
@@ -862,8 +862,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
         return wait_bar_rest(bar, ph, abort_flag, p.status);
       };
-      const uint64_t qd = sdesc_k_sw128(sQ), gd = sdesc_k_sw128(sG);
+      const uint32_t ta = tmem + kTmA, tg = tmem + kTmG;
       bool ok = wait(q_full, 0);
+      tc_fence_after();
       int st = 0, done = 0;
       uint32_t ph = 0, acc = 0;
       for (int i = 0; ok && i <= n; ++i) {
@@ -875,10 +876,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_bf16(d, qd + roff(ks), kd + koff(ks), kIdescS, ks != 0);
+            mma_bf16_ta(d, ta + ks * 8, kd + koff(ks), kIdescS, ks != 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            mma_bf16(d + 64, gd + roff(ks), vd + koff(ks), kIdescS, ks != 0);
+            mma_bf16_ta(d + 64, tg + ks * 8, vd + koff(ks), kIdescS, ks != 0);
           mma_commit(sdp_full(i & 1));
           if (++st == pl.stages) st = 0, ph ^= 1;
         }
@@ -915,6 +916,28 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float2 sd = live ? pl.stat[at] : make_float2(inf, 0.f);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const float c2 = p.scale * 1.4426950408889634f;
+    // Q (warpgroup 0) and dO (1) into tensor memory, each thread its row
+    if (!__all_sync(0xffffffffu,
+                    wait_bar_rest(q_here, 0, abort_flag, p.status)))
+      goto done;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint32_t w[32];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float4 v =
+            ld_shared_v4f((wg == 0 ? sQ : sG) + c * (kDqRows * 128) +
+                          row * 128 + ((x ^ (row & 7)) << 4));
+        w[4 * x] = __float_as_uint(v.x), w[4 * x + 1] = __float_as_uint(v.y);
+        w[4 * x + 2] = __float_as_uint(v.z), w[4 * x + 3] = __float_as_uint(v.w);
+      }
+      __syncwarp();
+      tmem_st32(tmem + (wg == 0 ? kTmA : kTmG) + lane_off + c * 32, w);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
     for (int i = 0; i < n; ++i) {
       // (a step of halves of 128 is one half: two steps a block)
       int end;
@@ -974,7 +997,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         goto done;
       tc_fence_after();
     }
-    // each warpgroup writes half of the columns; Q's space is free
+    // each warpgroup writes half of the columns; the first stage is free
     uint32_t ow[D / 4];
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
@@ -992,7 +1015,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 __uint_as_float(u[2 * x + 1]) * p.scale)
                   : 0u;
     }
-    store_rows<D / 4>(sQ + warp * (32 * D), ow,
+    store_rows<D / 4>(sK(0) + warp * (32 * D), ow,
                       live ? pl.gq + at * D + wg * (D / 2) : nullptr, lane);
   }
 done:
@@ -1060,7 +1083,7 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
   dp.stat = pl.stat;
   dp.gq = bf(gq);
   // fewer stages where a very long context's block words need the room
-  dp.stages = kKvStages;
+  dp.stages = kDqStages;
   while (dp.stages > 2 &&
          DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap) > kMaxSmem)
     --dp.stages;
