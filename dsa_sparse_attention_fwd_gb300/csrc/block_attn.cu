@@ -11,18 +11,19 @@
 // longer than one query's list and the keys are read once for all of them;
 // where they do not, an MMA over 128 rows still takes no longer than one over
 // 16, so a query alone costs what it would cost in a tile of its own.
-//   S = Q K^T on the tensor cores (128 x 128, fp32 in tensor memory); a
-// softmax thread has half of a row in registers: maximum, moved only when a step exceeds it by
-// more than 2^8 (then O is rescaled), P = exp2(S c - m) rounded to bf16 into
-// columns of S that are done; O += P V with P from tensor memory.  A row holds
-// 16 neighbouring keys or none of them, so its mask is a choice of m or +inf
-// for each 16; only steps with keys after some row's position look at single
-// keys.
-//   One stage of K and V (96 KB with Q at D = 128) and 256 tensor-memory
-// columns let two CTAs share an SM: one's products run under the other's
-// softmax, and its next K arrives while its own softmax and second product
-// run.  Few rows (single tokens) are split over their blocks, and a second
-// kernel joins the parts.
+//   A step is 64 keys: S = Q K^T on the tensor cores (128 x 64, fp32 in
+// tensor memory), of which each softmax thread holds a row in registers:
+// maximum, moved only when a step exceeds it by more than 2^8 (then O is
+// rescaled), P = exp2(S c - m) rounded to bf16 into columns of S; O += P V
+// with P from tensor memory.  A row holds 16 neighbouring keys or none of
+// them, so its mask is a choice of m or +inf for each 16; only steps with keys
+// after some row's position look at single keys.
+//   The scores have two buffers: the next step's product runs under this
+// step's softmax, and the softmax warps go from step to step without waiting
+// for the second product.  Two stages each of K and V (96 KB with Q at D =
+// 128) and 256 tensor-memory columns let two CTAs share an SM.  Few rows
+// (single tokens) are split over their blocks, and a second kernel joins the
+// parts.
 //
 // Masked keys: a score that is not finite in a key that only other rows hold
 // spoils the row's sum, see below; a V row that no row of
@@ -31,9 +32,8 @@
 // which a NaN or an infinity survives: rows with a sum or a result that is not
 // finite are computed again on their own (block_attn_row.cuh).
 //
-// Warps: 0 .. 7 softmax (warp w reads tensor-memory lanes 32 (w % 4) .. + 31,
-// 64 keys of a step: the two warps of a row exchange its maximum), 8 TMA
-// producer, 9 MMA issuer and tensor-memory allocator.
+// Warps: 0 .. 3 softmax (thread = row = tensor-memory lane), 4 TMA producer,
+// 5 MMA issuer and tensor-memory allocator.
 #include "block_attn.cuh"
 #include "block_attn_host.cuh"
 #include "block_attn_row.cuh"
@@ -44,11 +44,11 @@ namespace dsa {
 namespace {
 
 constexpr int kRows = 128;  // MMA rows of a query tile
-constexpr int kKeys = 128;  // keys of a step
-constexpr int kSoftWarps = 8;  // two for each 32 rows, 64 keys each
-constexpr int kFwdThreads = 32 * (kSoftWarps + 2);
-constexpr int kTmaWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-// tensor-memory columns; P takes the second half of each 64 of S
+constexpr int kKeys = 64;   // keys of a step
+constexpr int kFwdThreads = 192;
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
+// tensor-memory columns: two steps' scores, O; P takes the second half of
+// its scores
 constexpr uint32_t kTmS = 0, kTmO = 128;
 constexpr float kSlack = 8.f;
 
@@ -68,14 +68,14 @@ template <int D>
 struct FwdSmem {
   static constexpr int kCh = D / 64;
   static constexpr int kTile = kCh * kRows * 128;  // 128 rows of D bf16
+  static constexpr int kKey = kCh * kKeys * 128;   // K or V of a step
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kTile;
-  static constexpr int kOffV = 2 * kTile;
-  static constexpr int kOffBar = 3 * kTile;
-  // q_full k_full k_empty v_full v_empty s_full p_full o_full
-  static constexpr int kOffMisc = kOffBar + 8 * 8;
-  static constexpr int kOffRed = kOffMisc + 32;  // [4][128]
-  static constexpr int kOffWords = kOffRed + 4 * kRows * 4;
+  static constexpr int kOffV = kOffK + 2 * kKey;
+  static constexpr int kOffBar = kOffV + 2 * kKey;
+  // q_full o_done; k_full k_empty v_full v_empty s_full p_full, two each
+  static constexpr int kOffMisc = kOffBar + 14 * 8;
+  static constexpr int kOffWords = kOffMisc + 32;
   static int bytes(int nblk, int cap) {
     return kOffWords + nblk * 4 + ((cap * 2 + 15) & ~15) + 1024;
   }
@@ -99,18 +99,6 @@ __device__ __noinline__ void redo_row(const BlockAttn &p, const FwdPlan &pl,
   if (lane == 0) pl.lse[at] = lse;
 }
 
-// The barrier of the two warps of 32 rows.  Its number is written out: one
-// that is computed makes the compiler claim all sixteen, and a second CTA no
-// longer fits the SM.
-__device__ __forceinline__ bool pair_bar(int quad, bool pred) {
-  switch (quad) {
-    case 0: return named_bar_or(1, 64, pred);
-    case 1: return named_bar_or(2, 64, pred);
-    case 2: return named_bar_or(3, 64, pred);
-    default: return named_bar_or(4, 64, pred);
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     block_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -127,12 +115,23 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const uint32_t raw_addr = smem_u32(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t *smem = smem_raw + (base - raw_addr);
-  const uint32_t sQ = base + L::kOffQ, sK = base + L::kOffK,
-                 sV = base + L::kOffV;
+  const uint32_t sQ = base + L::kOffQ;
+  auto sK = [&](int st) { return base + L::kOffK + st * L::kKey; };
+  auto sV = [&](int st) { return base + L::kOffV + st * L::kKey; };
+  auto qoff = [](int ks) {  // K step ks in a tile of 128 rows, and of 64 keys
+    return (uint32_t)((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+  };
+  auto koff = [](int ks) {
+    return (uint32_t)((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4;
+  };
   const uint32_t bars = base + L::kOffBar;
-  const uint32_t q_full = bars, k_full = bars + 8, k_empty = bars + 16,
-                 v_full = bars + 24, v_empty = bars + 32, s_full = bars + 40,
-                 p_full = bars + 48, o_full = bars + 56;
+  const uint32_t q_full = bars, o_done = bars + 8;
+  auto k_full = [&](int i) { return bars + 16 + 8 * i; };
+  auto k_empty = [&](int i) { return bars + 32 + 8 * i; };
+  auto v_full = [&](int i) { return bars + 48 + 8 * i; };
+  auto v_empty = [&](int i) { return bars + 64 + 8 * i; };
+  auto s_full = [&](int i) { return bars + 80 + 8 * i; };
+  auto p_full = [&](int i) { return bars + 96 + 8 * i; };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -151,13 +150,15 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const int s0 = tile * pl.qt;
   const int nq = min(pl.qt, p.S - s0);
 
-  const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i)
-      mbar_init(bars + 8 * i, i == 6 ? kSoftWarps : 1);
+    for (int i = 0; i < 14; ++i) mbar_init(bars + 8 * i, i >= 12 ? 4 : 1);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
+    // Q arrives while the blocks are listed
+    mbar_arrive_expect_tx(q_full, CH * pl.qt * p.G * 128);
+    for (int c = 0; c < CH; ++c)
+      tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk, hk * p.G,
+                  b, s0);
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
@@ -165,16 +166,11 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     tmem_alloc(smem_u32(tmem_holder), 256);
     tmem_relinquish();
   }
+  const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
   for (int n = tid; n < p.nblk; n += kFwdThreads) words[n] = 0u;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (tid == 32 * kTmaWarp) {  // Q arrives while the blocks are listed
-    mbar_arrive_expect_tx(q_full, CH * pl.qt * p.G * 128);
-    for (int c = 0; c < CH; ++c)
-      tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk,
-                  hk * p.G, b, s0);
-  }
   mark_blocks(p, b, s0, nq, hk, words, tid, kFwdThreads, first);
   __syncthreads();
   if (warp == 0) {
@@ -183,17 +179,20 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   }
   __syncthreads();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
-  const int bpt = kKeys / p.blk;  // blocks of a step
-  const int all = (*sCount + bpt - 1) / bpt;
+  // a step takes units of up to 64 keys: whole blocks, or halves of 128
+  const int count = *sCount;
+  const int unit = min(p.blk, kKeys), per = p.blk / unit;
+  const int upt = kKeys / unit, units = count * per;
+  const int all = (units + upt - 1) / upt;
   const int t0 = (int)((long long)all * split / pl.splits);
   const int t1 = (int)((long long)all * (split + 1) / pl.splits);
-  const int count = *sCount;
-  if (t1 - t0 == 1 && count < t1 * bpt) {
-    // a single, ragged step: the rows past its blocks are read by the second
-    // product (times zero) and must be numbers
-    for (int i = tid; i < L::kTile / 16; i += kFwdThreads) {
+  const int n = t1 - t0;
+  if (n > 0 && n <= 2 && units < t1 * upt) {
+    // the first pass of a stage is ragged: the rows past its blocks are read
+    // by the second product (times zero) and must be numbers
+    for (int i = tid; i < 2 * L::kKey / 16; i += kFwdThreads) {
       const uint32_t z[4] = {0u, 0u, 0u, 0u};
-      st_shared_v4(sV + i * 16, z);
+      st_shared_v4(sV(0) + i * 16, z);
     }
     fence_proxy_async_smem();
     __syncthreads();
@@ -201,35 +200,35 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 
   if (warp == kTmaWarp) {
     // ---------------- TMA producer ----------------
-    for (int t = t0; t < t1; ++t) {
-      const uint32_t ph = (t - t0) & 1u;
-      const int nb = min(bpt, count - t * bpt);
-      // lane (block, chunk) of the step
-      const int bi = lane / CH, c = lane % CH;
-      const bool mine = bi < nb;
+    const int ui = lane / CH, c = lane % CH;  // unit and chunk of this lane
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (i >> 1) & 1u;
+      const int nu = min(upt, units - (t0 + i) * upt);
       int tok = 0, outer = 0;
-      if (mine) {
-        const int n = list[t * bpt + bi];
+      if (ui < nu) {
+        const int x = (t0 + i) * upt + ui;
+        const int bn = list[x / per];
+        tok = bn * p.blk + x % per * unit;
+        outer = b;
         if (p.table) {
           bool bad = false;
-          outer = block_page(p, b, n, bad);
-          tok = (int)((long long)n * p.blk % p.page_size);
-        } else {
-          outer = b;
-          tok = n * p.blk;
+          outer = block_page(p, b, bn, bad);
+          tok %= p.page_size;
         }
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
-        const uint32_t full = kv ? v_full : k_full;
+        const uint32_t full = kv ? v_full(st) : k_full(st);
         if (!__all_sync(0xffffffffu,
-                        wait_bar_rest(kv ? v_empty : k_empty, ph ^ 1u,
-                                     abort_flag, p.status)))
+                        wait_bar_rest(kv ? v_empty(st) : k_empty(st), ph ^ 1u,
+                                      abort_flag, p.status)))
           goto done;
-        if (lane == 0) mbar_arrive_expect_tx(full, nb * p.blk * CH * 128);
+        if (lane == 0) mbar_arrive_expect_tx(full, nu * unit * CH * 128);
         __syncwarp();
-        if (mine)
-          tma_load_4d((kv ? sV : sK) + c * (kRows * 128) + bi * p.blk * 128,
+        if (ui < nu)
+          tma_load_4d((kv ? sV(st) : sK(st)) + c * (kKeys * 128) +
+                          ui * unit * 128,
                       kv ? &maps.v : &maps.k, full, c * kChunk, tok,
                       hk * (kv ? maps.bc_vh : maps.bc_kh),
                       outer * (kv ? maps.bc_vs : maps.bc_ks));
@@ -241,148 +240,160 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       auto wait = [&](uint32_t bar, uint32_t ph) -> bool {
         return wait_bar_rest(bar, ph, abort_flag, p.status);
       };
-      const uint64_t qd = sdesc_k_sw128(sQ), kd = sdesc_k_sw128(sK);
-      const uint64_t vd = sdesc_mn_sw128(sV, kRows * 128, 1024);
+      const uint64_t qd = sdesc_k_sw128(sQ);
       bool ok = wait(q_full, 0);
-      uint32_t ph = 0, acc = 0;
-      for (int t = t0; ok && t < t1; ++t) {
-        if (!(ok = wait(k_full, ph))) break;
+      auto scores = [&](int i) -> bool {
+        const int st = i & 1;
+        if (!wait(k_full(st), (i >> 1) & 1u)) return false;
         tc_fence_after();
+        const uint64_t kd = sdesc_k_sw128(sK(st));
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
-          mma_bf16(tmem + kTmS, qd + o, kd + o, kIdescS, ks != 0);
-        }
-        mma_commit(k_empty);
-        mma_commit(s_full);
-        if (!(ok = wait(v_full, ph) && wait(p_full, ph))) break;
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_bf16(tmem + kTmS + st * 64, qd + qoff(ks), kd + koff(ks),
+                   kIdescS, ks != 0);
+        mma_commit(k_empty(st));
+        mma_commit(s_full(st));
+        return true;
+      };
+      if (ok && n > 0) ok = scores(0);
+      uint32_t acc = 0;
+      for (int i = 0; ok && i < n; ++i) {
+        if (i + 1 < n && !(ok = scores(i + 1))) break;
+        const int st = i & 1;
+        const uint32_t ph = (i >> 1) & 1u;
+        if (!(ok = wait(v_full(st), ph) && wait(p_full(st), ph))) break;
         tc_fence_after();
+        const uint64_t vd = sdesc_mn_sw128(sV(st), kKeys * 128, 1024);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_bf16_ta(tmem + kTmO, tmem + kTmS + (ks >> 2) * 64 + 32 + (ks & 3) * 8,
+          mma_bf16_ta(tmem + kTmO, tmem + kTmS + st * 64 + 32 + ks * 8,
                       vd + ((ks * 2048) >> 4), kIdescO, ks == 0 ? acc : 1u);
-        mma_commit(v_empty);
-        if (t + 1 == t1) mma_commit(o_full);
+        mma_commit(v_empty(st));
+        mma_commit(o_done);
         acc = 1;
-        ph ^= 1;
       }
     }
     __syncwarp();
   } else {
-    // ---------- softmax: a thread takes a row's keys 64 half .. + 63 ----------
-    const int half = warp >> 2, quad = warp & 3;
-    const int row = quad * 32 + lane;
+    // ---------------- softmax: one row a thread ----------------
+    const int row = tid;
     const int qi = row / p.G;
     const bool live = qi < nq;
     const int pos = live ? key_pos(p, b, s0 + qi) : -1;
     // the last key that the first and that any row of the tile sees
     const int pos_lo = key_pos(p, b, s0), pos_hi = key_pos(p, b, s0 + nq - 1);
     const float c2 = p.scale * 1.4426950408889634f;
-    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const uint32_t tS = tmem + kTmS + lane_off + half * 64,
-                   tO = tmem + kTmO + lane_off + half * (D / 2);
-    float *red = reinterpret_cast<float *>(smem + L::kOffRed);
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t tO = tmem + kTmO + lane_off;
     float m = neg_inf;
     float2 l2[2] = {};
-    // the two warps of 32 rows meet at a barrier every step: a wait that
-    // gave up is carried to it, so that both leave together
-    bool fail = false;
-    for (int t = t0; t < t1; ++t) {
-      const uint32_t ph = (t - t0) & 1u;
-      uint32_t mask[2];
-      bool held[2], diag[2];
+    uint32_t next[2] = {};
+    bool next_diag[2] = {};
+    if (n > 0)
+      step_masks(words, list, t0, count, p.lb, qi & 31, pos, pos_lo, next,
+                 next_diag);
+    for (int i = 0; i < n; ++i) {
+      const int st = i & 1;
+      const uint32_t ph = (i >> 1) & 1u;
+      const uint32_t tS = tmem + kTmS + st * 64 + lane_off;
+      const int t = t0 + i;
+      const uint32_t mask[2] = {next[0], next[1]};
+      const bool diag[2] = {next_diag[0], next_diag[1]};
+      bool held[2];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        int end;
-        mask[c] = step_mask(words, list, t * bpt, count, p.lb, 2 * half + c,
-                            qi & 31, pos, end);
-        diag[c] = end > pos_lo;
+      for (int c = 0; c < 2; ++c)
         held[c] = __any_sync(0xffffffffu, mask[c] != 0u);
-      }
-      fail |= !__all_sync(0xffffffffu, wait_bar_rest(s_full, ph, abort_flag,
-                                                     p.status));
+      if (!__all_sync(0xffffffffu, wait_bar_rest(s_full(st), ph, abort_flag,
+                                                 p.status)))
+        goto done;
       tc_fence_after();
-      // the row's maximum, 32 keys at a time; the second 32 stay
-      uint32_t u[32];
+      uint32_t u[2][32];
       float mx = neg_inf;
-      auto fetch = [&](int c) {
+      if (held[0] || held[1]) {
         __syncwarp();
-        tmem_ld32(tS + c * 32, u);
+        tmem_ld32(tS, u[0]);
+        tmem_ld32(tS + 32, u[1]);
         tmem_ld_wait();
-        reg_fence32(u);
-        if (diag[c]) {  // keys after some row's position: one by one
+        reg_fence32(u[0]);
+        reg_fence32(u[1]);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            u[i] = mask[c] >> i & 1u ? u[i] : 0xff800000u;
-        }
-      };
+        for (int c = 0; c < 2; ++c) {
+          if (diag[c]) {  // keys after some row's position: one by one
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (!held[c]) continue;
-        fetch(c);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float a = neg_inf, e = neg_inf;
-#pragma unroll
-          for (int i = 16 * g; i < 16 * g + 16; i += 4) {
-            a = fmaxf(a, fmaxf(__uint_as_float(u[i]),
-                               __uint_as_float(u[i + 1])));
-            e = fmaxf(e, fmaxf(__uint_as_float(u[i + 2]),
-                               __uint_as_float(u[i + 3])));
+            for (int x = 0; x < 32; ++x)
+              u[c][x] = mask[c] >> x & 1u ? u[c][x] : 0xff800000u;
           }
-          // a row holds all 16 keys or none, or they are hidden above
-          if (mask[c] & (0xffffu << (16 * g))) mx = fmaxf(mx, fmaxf(a, e));
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float a = neg_inf, e = neg_inf;
+#pragma unroll
+            for (int x = 16 * g; x < 16 * g + 16; x += 4) {
+              a = fmaxf(a, fmaxf(__uint_as_float(u[c][x]),
+                                 __uint_as_float(u[c][x + 1])));
+              e = fmaxf(e, fmaxf(__uint_as_float(u[c][x + 2]),
+                                 __uint_as_float(u[c][x + 3])));
+            }
+            // a row holds all 16 keys or none, or they are hidden above
+            if (mask[c] & (0xffffu << (16 * g))) mx = fmaxf(mx, fmaxf(a, e));
+          }
         }
+        mx *= c2;
       }
-      red[half * kRows + row] = mx;
-      if (pair_bar(quad, fail)) goto done;
-      mx = fmaxf(mx, red[(half ^ 1) * kRows + row]) * c2;
       // a row without a key so far keeps m = -inf and weights of zero
       const bool move = mx > m + kSlack;
-      if (__any_sync(0xffffffffu, move && t > t0)) {
+      if (i > 0 && __any_sync(0xffffffffu, move)) {
+        // O is at rest once the last step's second product is done
+        if (!__all_sync(0xffffffffu,
+                        wait_bar_rest(o_done, (i - 1) & 1u, abort_flag,
+                                      p.status)))
+          goto done;
+        tc_fence_after();
         const float f = move ? ex2(m - mx) : 1.f;
         l2[0] = __fmul2_rn(l2[0], make_float2(f, f));
         l2[1] = __fmul2_rn(l2[1], make_float2(f, f));
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {  // half of O's columns
-          uint32_t w[16];
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[32];
           __syncwarp();
-          tmem_ld16(tO + c * 16, w);
+          tmem_ld32(tO + c * 32, w);
           tmem_ld_wait();
-          reg_fence16(w);
+          reg_fence32(w);
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            w[i] = __float_as_uint(__uint_as_float(w[i]) * f);
-          tmem_st16(tO + c * 16, w);
+          for (int x = 0; x < 32; ++x)
+            w[x] = __float_as_uint(__uint_as_float(w[x]) * f);
+          tmem_st32(tO + c * 32, w);
         }
       }
       if (move) m = mx;
       const float mu = m > neg_inf ? m : 0.f;
-      // P = exp2(S c2 - mu) into the second half of the 64 columns of S
+      // the next step's masks, among the exponentials
+      if (i + 1 < n)
+        step_masks(words, list, t + 1, count, p.lb, qi & 31, pos, pos_lo,
+                   next, next_diag);
+      // P = exp2(S c2 - mu)
 #pragma unroll
-      for (int c = 1; c >= 0; --c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t pk[16];
         if (held[c]) {
-          if (c == 0) fetch(0);
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             // -inf takes the weights of keys that the row does not hold to 0
             const float sub = mask[c] & (0xffffu << (16 * g)) ? -mu : neg_inf;
 #pragma unroll
-            for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-              float2 e = __ffma2_rn(make_float2(__uint_as_float(u[i]),
-                                                __uint_as_float(u[i + 1])),
+            for (int x = 16 * g; x < 16 * g + 16; x += 2) {
+              float2 e = __ffma2_rn(make_float2(__uint_as_float(u[c][x]),
+                                                __uint_as_float(u[c][x + 1])),
                                     make_float2(c2, c2),
                                     make_float2(sub, sub));
               e.x = ex2(e.x);
               e.y = ex2(e.y);
-              l2[(i >> 1) & 1] = __fadd2_rn(l2[(i >> 1) & 1], e);
-              pk[i >> 1] = pack_bf16x2(e.x, e.y);
+              l2[(x >> 1) & 1] = __fadd2_rn(l2[(x >> 1) & 1], e);
+              pk[x >> 1] = pack_bf16x2(e.x, e.y);
             }
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = 0u;
+          for (int x = 0; x < 16; ++x) pk[x] = 0u;
         }
         __syncwarp();
         tmem_st16(tS + 32 + c * 16, pk);
@@ -390,36 +401,37 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       tmem_st_wait();
       tc_fence_before();
       if (diag[0] || diag[1]) {
-        // V rows of this step that no row sees; each half its 64 keys
-        const int kr = half * 64 + (row & 63);
-        const int i = t * bpt + (kr >> p.lb);
-        const bool over = row < 64 && i < count &&
-                          (list[i] << p.lb) + (kr & (p.blk - 1)) > pos_hi;
+        // V rows of this step that no row sees
+        const int x = t * upt + row / unit;
+        const bool over =
+            row < kKeys && x < units &&
+            list[x / per] * p.blk + x % per * unit + row % unit > pos_hi;
         if (__any_sync(0xffffffffu, over)) {
-          fail |= !__all_sync(0xffffffffu, wait_bar_rest(v_full, ph, abort_flag,
-                                                         p.status));
+          if (!__all_sync(0xffffffffu,
+                          wait_bar_rest(v_full(st), ph, abort_flag,
+                                        p.status)))
+            goto done;
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
-          if (over && !fail)
+          if (over)
             for (int c = 0; c < CH * 8; ++c)
-              st_shared_v4(sV + (c >> 3) * (kRows * 128) + kr * 128 +
+              st_shared_v4(sV(st) + (c >> 3) * (kKeys * 128) + row * 128 +
                                (c & 7) * 16,
                            z);
           fence_proxy_async_smem();
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(p_full(st));
     }
-    float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
-    red[half * kRows + row] = l;
-    if (pair_bar(quad, fail)) goto done;
-    l += red[(half ^ 1) * kRows + row];
     // ---------------- o = O / l ----------------
-    if (t1 > t0) {
-      fail = !__all_sync(0xffffffffu,
-                         wait_bar_rest(o_full, 0, abort_flag, p.status));
+    if (n > 0) {
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_rest(o_done, (n - 1) & 1u, abort_flag,
+                                    p.status)))
+        goto done;
       tc_fence_after();
     }
+    const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const bool some = l > 0.f || l != l;
     const float inv = some ? 1.f / l : 0.f;
     bool odd = l != l || l > 3e38f;  // not finite: computed again below
@@ -429,49 +441,43 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         ((size_t)(blockIdx.x / pl.splits) * pl.splits + split) *
             (pl.qt * p.G) +
         row;
-    // half of the columns; Q's space is free for the way out
-    const uint32_t out_buf = sQ + warp * (32 * D);
-    constexpr int kOut = D / 4;  // words of this half's bf16 row
-    uint32_t ow[kOut];
-#pragma unroll
+    const uint32_t out_buf = sQ + warp * 4096;  // Q's space is free
+#pragma unroll 1
     for (int c = 0; c < D / 64; ++c) {
-      const int d0 = half * (D / 2) + c * 32;
-      uint32_t u[32];
-      if (t1 > t0) {
+      uint32_t u[2][32];
+      if (n > 0) {
         __syncwarp();
-        tmem_ld32(tO + c * 32, u);
+        tmem_ld32(tO + c * 64, u[0]);
+        tmem_ld32(tO + c * 64 + 32, u[1]);
         tmem_ld_wait();
-        reg_fence32(u);
+        reg_fence32(u[0]);
+        reg_fence32(u[1]);
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float v = some ? __uint_as_float(u[i]) * inv : 0.f;
+      for (int x = 0; x < 64; ++x) {
+        const float v = some ? __uint_as_float(u[x >> 5][x & 31]) * inv : 0.f;
         odd |= !(fabsf(v) < 3e38f);
-        u[i] = __float_as_uint(v);
+        u[x >> 5][x & 31] = __float_as_uint(v);
       }
       if (pl.splits > 1) {
-        if (live) {
-          float4 *dst = reinterpret_cast<float4 *>(pl.part_o + part * D + d0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(
-                __uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
-                __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
-        }
+        for (int h = 0; h < 2; ++h)
+          store_rows<32>(out_buf, u[h],
+                         live ? pl.part_o + part * D + c * 64 + h * 32
+                              : nullptr,
+                         lane);
+      } else {
+        uint32_t w[32];
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          w[x] = pack_bf16x2(__uint_as_float(u[x >> 4][2 * x & 31]),
+                             __uint_as_float(u[x >> 4][(2 * x & 31) + 1]));
+        store_rows<32>(out_buf, w, live ? pl.o + at * D + c * 64 : nullptr,
+                       lane);
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        ow[c * 16 + i] = pack_bf16x2(__uint_as_float(u[2 * i]),
-                                     __uint_as_float(u[2 * i + 1]));
     }
-    if (pl.splits == 1)
-      store_rows<kOut>(out_buf, ow,
-                       live ? pl.o + at * D + half * (D / 2) : nullptr, lane);
-    // a row that is not finite in either half
-    red[(2 + half) * kRows + row] = odd && live ? 1.f : 0.f;
-    if (pair_bar(quad, fail)) goto done;
-    odd = live && (odd || red[(3 - half) * kRows + row] != 0.f);
-    if (live && half == 0) {
+    odd &= live;
+    if (live) {
       const float lse2 = some ? m + log2f(l) : neg_inf;
       if (pl.splits > 1)
         // a NaN tells the joining kernel to compute the row again
@@ -479,12 +485,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       else
         pl.lse[at] = some ? lse2 * 0.69314718055994531f : neg_inf;
     }
-    unsigned todo = __ballot_sync(0xffffffffu, odd && half == 0);
+    unsigned todo = __ballot_sync(0xffffffffu, odd);
     if (pl.splits == 1) {
-      // K's space is free: the last product is done
-      float *qs = reinterpret_cast<float *>(smem + L::kOffK) + warp * 128;
+      // (store_rows is done with this warp's part of the space)
+      float *qs = reinterpret_cast<float *>(smem + L::kOffQ) + warp * 1024;
       for (; todo; todo &= todo - 1) {
-        const int r = quad * 32 + __ffs(todo) - 1;
+        const int r = warp * 32 + __ffs(todo) - 1;
         redo_row(p, pl, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
       }
     }
@@ -579,13 +585,12 @@ int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
   // Few tiles: share each among CTAs until two an SM are busy, with a step
   // each at least.
   const long long items = (long long)pl.tiles * p.B * p.Hk;
-  const int bpt = kKeys / p.blk;
   long long slots = 2ll * num_sms;
   if (slots > kSplitItems) slots = kSplitItems;
   pl.splits = 1;
   if (items * 2 <= slots) {
     long long n = slots / items;
-    const long long steps = (pl.cap + bpt - 1) / bpt;
+    const long long steps = ((long long)pl.cap * p.blk + kKeys - 1) / kKeys;
     if (n > steps) n = steps;
     pl.splits = (int)n;
   }
@@ -599,7 +604,7 @@ int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
   Problem qp{p.q, nullptr, nullptr, nullptr, p.S, p.B, p.H, p.D, 1, 1};
   int rc = encode_q_heads(&tm_q, qp, pl.qt, p.G);
   if (rc != DSA_OK) return rc;
-  rc = encode_kv_maps(p, p.blk, &maps);
+  rc = encode_kv_maps(p, p.blk < kKeys ? p.blk : kKeys, &maps);
   if (rc != DSA_OK) return rc;
   rc = p.D == 64 ? launch_fwd<64>(tm_q, maps, p, pl, st)
                  : launch_fwd<128>(tm_q, maps, p, pl, st);

@@ -33,14 +33,14 @@ struct BlockAttn {
 __device__ __forceinline__ int candidate(const BlockAttn &p,
                                          const int32_t *ids, long long pos,
                                          int i, bool &bad) {
-  if (pos < 0) return -1;
-  const long long own = pos / p.blk;
   if (i < p.topk) {
-    const int n = __ldg(ids + i);
+    const int n = __ldg(ids + i);  // (does not wait for the position)
     if (n < -1 || n >= p.nblk) bad = true;
-    return n < 0 || n >= p.nblk || n > own - p.local ? -1 : n;
+    if (pos < 0) return -1;
+    return n < 0 || n >= p.nblk || n > (pos >> p.lb) - p.local ? -1 : n;
   }
-  const long long n = own - (i - p.topk);
+  if (pos < 0) return -1;
+  const long long n = (pos >> p.lb) - (i - p.topk);
   return n >= 0 && n < p.nblk ? (int)n : -1;
 }
 
@@ -111,19 +111,32 @@ __device__ __forceinline__ void mark_blocks(const BlockAttn &p, int b, int s0,
   if (f.bad) atomicOr(p.status, kStatusIndexRange);
 }
 
-// The marked blocks in ascending order; one warp.  Returns their number.
-__device__ __forceinline__ int list_blocks(const uint32_t *words, int nblk,
+// The marked blocks in ascending order, and their masks moved to the front of
+// words in the same order; one warp.  Returns their number.
+__device__ __forceinline__ int list_blocks(uint32_t *words, int nblk,
                                            uint16_t *list, int lane) {
   int count = 0;
   for (int n0 = 0; n0 < nblk; n0 += 128) {
+    uint32_t w[4];
+    unsigned m[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int n = n0 + u * 32 + lane;
-      const bool any = n < nblk && words[n] != 0;
-      const unsigned m = __ballot_sync(0xffffffffu, any);
-      if (any) list[count + __popc(m & ((1u << lane) - 1))] = (uint16_t)n;
-      count += __popc(m);
+      w[u] = n < nblk ? words[n] : 0u;
     }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) m[u] = __ballot_sync(0xffffffffu, w[u] != 0u);
+    // (an entry never moves up, and these 128 have been read)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = count + __popc(m[u] & ((1u << lane) - 1));
+      if (w[u]) {
+        words[at] = w[u];
+        list[at] = (uint16_t)(n0 + u * 32 + lane);
+      }
+      count += __popc(m[u]);
+    }
+    __syncwarp();
   }
   return count;
 }
@@ -141,33 +154,56 @@ __device__ __forceinline__ uint32_t first_keys(int n, int width) {
   return n >= width ? 0xffffffffu >> (32 - width) : (1u << n) - 1u;
 }
 
-// Mask of the 32 keys `c` (0 ..) of a step whose blocks are list[l0 ..] up to
-// count, for the row of query bit qi at `pos`; `end`: the last of the keys
-// (-1: none).  Shifts only, and no branch but one on the block size: it runs
-// for every row and step.
-__device__ __forceinline__ uint32_t step_mask(const uint32_t *words,
-                                              const uint16_t *list, int l0,
-                                              int count, int lb, int c, int qi,
-                                              int pos, int &end) {
-  if (lb >= 5) {
-    const int i = l0 + (c * 32 >> lb);
-    const int n = list[i < count ? i : count - 1];
-    const int j0 = (n << lb) + (c * 32 & ((1 << lb) - 1));
-    const uint32_t held = i < count ? words[n] >> qi & 1u : 0u;
-    end = i < count ? j0 + 31 : -1;
-    return first_keys(held ? pos - j0 + 1 : 0, 32);
+// The masks of the 64 keys of step t for the row of query bit qi at `pos`:
+// its units of 16, 32 or 64 keys are list[t * 4 ..], list[t * 2 ..], list[t],
+// or half of list[t / 2].  `diag`: some of the keys (each 32) come after
+// pos_lo.  The masks of held blocks are made key by key only then; it runs for
+// every row and step.
+__device__ __forceinline__ void step_masks(const uint32_t *words,
+                                           const uint16_t *list, int t,
+                                           int count, int lb, int qi, int pos,
+                                           int pos_lo, uint32_t (&mask)[2],
+                                           bool (&diag)[2]) {
+  if (lb >= 6) {
+    const int i = lb == 6 ? t : t >> 1;
+    const uint32_t held = words[i] >> qi & 1u;
+    const int j0 = ((int)list[i] << lb) + (lb == 6 ? 0 : (t & 1) * 64);
+    mask[0] = mask[1] = 0u - held;
+    diag[0] = j0 + 31 > pos_lo;
+    diag[1] = j0 + 63 > pos_lo;
+    if (diag[1]) {
+      mask[0] &= first_keys(pos - j0 + 1, 32);
+      mask[1] &= first_keys(pos - j0 - 31, 32);
+    }
+    return;
   }
-  uint32_t m = 0u;  // blocks of 16
-  end = -1;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = l0 + c * 2 + u;
-    const int n = list[i < count ? i : count - 1];
-    const uint32_t held = i < count ? words[n] >> qi & 1u : 0u;
-    if (i < count) end = n * 16 + 15;  // ascending: the last one stays
-    m |= first_keys(held ? pos - n * 16 + 1 : 0, 16) << (16 * u);
+  for (int c = 0; c < 2; ++c) {
+    mask[c] = 0u;
+    int end = -1;
+    if (lb == 5) {
+      const int i = 2 * t + c, x = min(i, count - 1);
+      const int j0 = (int)list[x] * 32;
+      if (i < count) {
+        end = j0 + 31;
+        mask[c] = 0u - (words[x] >> qi & 1u);
+        if (end > pos_lo) mask[c] &= first_keys(pos - j0 + 1, 32);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int i = 4 * t + 2 * c + u, x = min(i, count - 1);
+        const int j0 = (int)list[x] * 16;
+        if (i < count) {
+          end = j0 + 15;  // ascending: the last one stays
+          uint32_t h = 0u - (words[x] >> qi & 1u);
+          if (end > pos_lo) h &= first_keys(pos - j0 + 1, 16);
+          mask[c] |= (h & 0xffffu) << (16 * u);
+        }
+      }
+    }
+    diag[c] = end > pos_lo;
   }
-  return m;
 }
 
 // A warp's 32 rows of NW words to memory, lane = row, `dst` its address

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(128)
   for (int i = tid; i < count; i += 128) {
     const int n = list[i];
     pl.lblk[(size_t)it * pl.cap + i] = (uint16_t)n;
-    pl.lmask[(size_t)it * pl.cap + i] = words[n];
+    pl.lmask[(size_t)it * pl.cap + i] = words[i];
     const int kt = n / pl.bpt;
     if (i == 0 || list[i - 1] / pl.bpt != kt) {
       const long long k = bh * pl.nkt + kt;
@@ -777,7 +777,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int s0 = tile * pl.qt;
   const int nq = min(pl.qt, p.S - s0);
 
-  const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
+  // Q and dO pass through the last two stages on their way to tensor memory
+  const uint32_t sQ = sK(pl.stages - 1), sG = sK(pl.stages - 2);
   if (tid == 0) {
     mbar_init(q_full, 8);
     mbar_init(q_here, 1);
@@ -792,22 +793,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_go);
-    tma_prefetch_desc(&maps.k);
-    tma_prefetch_desc(&maps.v);
-  }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(tmem_holder), 512);
-    tmem_relinquish();
-  }
-  for (int n = tid; n < p.nblk; n += kBwdThreads) words[n] = 0u;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  // Q and dO pass through the last two stages on their way to tensor memory
-  const uint32_t sQ = sK(pl.stages - 1), sG = sK(pl.stages - 2);
-  if (tid == 32 * kTmaWarp) {
     mbar_arrive_expect_tx(q_here, 2 * CH * pl.qt * p.G * 128);
     for (int c = 0; c < CH; ++c) {
       tma_load_4d(sQ + c * (kDqRows * 128), &tm_q, q_here, c * kChunk,
@@ -815,7 +800,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tma_load_4d(sG + c * (kDqRows * 128), &tm_go, q_here, c * kChunk,
                   hk * p.G, b, s0);
     }
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_relinquish();
+  }
+  const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
+  for (int n = tid; n < p.nblk; n += kBwdThreads) words[n] = 0u;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   mark_blocks(p, b, s0, nq, hk, words, tid, kBwdThreads, first);
   __syncthreads();
   if (warp == 0) {
@@ -939,11 +935,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
     for (int i = 0; i < n; ++i) {
-      // (a step of halves of 128 is one half: two steps a block)
-      int end;
-      const uint32_t mask =
-          step_mask(words, list, unit < p.blk ? i >> 1 : i * upt, count, p.lb,
-                    wg + (unit < p.blk ? (i & 1) * 2 : 0), qi & 31, pos, end);
+      uint32_t masks[2];
+      bool diag[2];
+      step_masks(words, list, i, count, p.lb, qi & 31, pos, pos_lo, masks,
+                 diag);
+      const uint32_t mask = wg ? masks[1] : masks[0];
+      const bool late = wg ? diag[1] : diag[0];
       const bool any = __any_sync(0xffffffffu, mask != 0u);
       if (!__all_sync(0xffffffffu, wait_bar_rest(sdp_full(i & 1), (i >> 1) & 1u,
                                                 abort_flag, p.status)))
@@ -962,7 +959,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tmem_ld_wait();
         reg_fence32(u);
         reg_fence32(g);
-        if (end > pos_lo) {  // keys after some row's position: one by one
+        if (late) {  // keys after some row's position: one by one
 #pragma unroll
           for (int x = 0; x < 32; ++x)
             u[x] = mask >> x & 1u ? u[x] : 0xff800000u;
