@@ -442,40 +442,36 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             (pl.qt * p.G) +
         row;
     const uint32_t out_buf = sQ + warp * 4096;  // Q's space is free
+    // (a short loop: this runs once a CTA, and instructions that are fetched
+    // to run once take longer than they save)
+    float2 chk = make_float2(0.f, 0.f);  // not a number where O is not finite
 #pragma unroll 1
-    for (int c = 0; c < D / 64; ++c) {
-      uint32_t u[2][32];
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t u[32], w[16];
       if (n > 0) {
         __syncwarp();
-        tmem_ld32(tO + c * 64, u[0]);
-        tmem_ld32(tO + c * 64 + 32, u[1]);
+        tmem_ld32(tO + c * 32, u);
         tmem_ld_wait();
-        reg_fence32(u[0]);
-        reg_fence32(u[1]);
+        reg_fence32(u);
       }
 #pragma unroll
-      for (int x = 0; x < 64; ++x) {
-        const float v = some ? __uint_as_float(u[x >> 5][x & 31]) * inv : 0.f;
-        odd |= !(fabsf(v) < 3e38f);
-        u[x >> 5][x & 31] = __float_as_uint(v);
+      for (int x = 0; x < 16; ++x) {
+        float2 v = __fmul2_rn(make_float2(__uint_as_float(u[2 * x]),
+                                          __uint_as_float(u[2 * x + 1])),
+                              make_float2(inv, inv));
+        chk = __ffma2_rn(v, make_float2(0.f, 0.f), chk);
+        u[2 * x] = some ? __float_as_uint(v.x) : 0u;
+        u[2 * x + 1] = some ? __float_as_uint(v.y) : 0u;
+        w[x] = some ? pack_bf16x2(v.x, v.y) : 0u;
       }
-      if (pl.splits > 1) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          store_rows<32>(out_buf, u[h],
-                         live ? pl.part_o + part * D + c * 64 + h * 32
-                              : nullptr,
-                         lane);
-      } else {
-        uint32_t w[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x)
-          w[x] = pack_bf16x2(__uint_as_float(u[x >> 4][2 * x & 31]),
-                             __uint_as_float(u[x >> 4][(2 * x & 31) + 1]));
-        store_rows<32>(out_buf, w, live ? pl.o + at * D + c * 64 : nullptr,
+      if (pl.splits > 1)
+        store_rows<32>(out_buf, u,
+                       live ? pl.part_o + part * D + c * 32 : nullptr, lane);
+      else
+        store_rows<16>(out_buf, w, live ? pl.o + at * D + c * 32 : nullptr,
                        lane);
-      }
     }
+    odd |= some && !(chk.x + chk.y == 0.f);
     odd &= live;
     if (live) {
       const float lse2 = some ? m + log2f(l) : neg_inf;
