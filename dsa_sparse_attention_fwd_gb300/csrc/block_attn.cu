@@ -22,8 +22,8 @@
 // step's softmax, and the softmax warps go from step to step without waiting
 // for the second product.  Two stages each of K and V (96 KB with Q at D =
 // 128) and 256 tensor-memory columns let two CTAs share an SM.  Few rows
-// (single tokens) are split over their blocks, and a second kernel joins the
-// parts.
+// (single tokens) are split over their blocks; the CTA that ends last joins
+// the parts.
 //
 // Masked keys: a score that is not finite in a key that only other rows hold
 // spoils the row's sum, see below; a V row that no row of
@@ -62,6 +62,7 @@ struct FwdPlan {
   float *lse;
   // splits > 1: [item][split][qt * G] rows of D and of log-sums (base 2)
   float *part_o, *part_l;
+  uint32_t *done;  // [item] parts that are written; zero between calls
 };
 
 template <int D>
@@ -97,6 +98,79 @@ __device__ __noinline__ void redo_row(const BlockAttn &p, const FwdPlan &pl,
   for (int i = 0; i * 32 < p.D; ++i)
     pl.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
   if (lane == 0) pl.lse[at] = lse;
+}
+
+// Joins the parts of a split tile, o = sum_i w_i o_i / sum_i w_i with w_i =
+// 2^(l_i - max), in the order of the splits; the CTA that finished last.  A
+// thread takes four columns of a row and has kJoin parts in flight: the join
+// is a chain of loads from L2.  qs: 128 floats of shared memory a warp.
+constexpr int kJoin = 8;
+template <int D>
+__device__ __noinline__ void join_parts(const BlockAttn &p, const FwdPlan &pl,
+                                        size_t part0, int b, int s0, int nq,
+                                        int hk, float *qs, int tid) {
+  constexpr int kLanes = D / 4;  // threads of a row: half a warp or a warp
+  const float neg_inf = -__int_as_float(0x7f800000);
+  const int rows = pl.qt * p.G, lane = tid & 31, c = tid % kLanes;
+  const int todo = nq * p.G;
+  // (whole warps stay in the loop: they vote)
+  for (int r0 = tid / 32 * (32 / kLanes); r0 < todo;
+       r0 += kFwdThreads / kLanes) {
+    const int r = r0 + lane / kLanes;
+    const bool mine = r < todo;
+    const size_t part = part0 + (mine ? r : 0);
+    float m = neg_inf, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool odd = false;
+    for (int i0 = 0; i0 < pl.splits; i0 += kJoin) {
+      float l[kJoin];
+      float4 v[kJoin];
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const size_t at = part + (size_t)min(i0 + u, pl.splits - 1) * rows;
+        l[u] = __ldcg(pl.part_l + at);
+        v[u] = __ldcg(reinterpret_cast<const float4 *>(pl.part_o + at * D) + c);
+        if (i0 + u >= pl.splits) l[u] = neg_inf;
+      }
+      float mx = m;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        odd |= l[u] != l[u];
+        mx = fmaxf(mx, l[u]);
+      }
+      const float ref = mx > neg_inf ? mx : 0.f;
+      const float f = ex2(m - ref);
+      sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const float w = ex2(l[u] - ref);
+        sum += w;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+      m = mx;
+    }
+    const int s = s0 + r / p.G, h = hk * p.G + r % p.G;
+    if (mine) {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const size_t at = ((size_t)s * p.B + b) * p.H + h;
+      reinterpret_cast<uint2 *>(pl.o + at * D)[c] =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                     pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (c == 0)
+        pl.lse[at] =
+            sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : neg_inf;
+    }
+    // rows with a part that is not finite
+    unsigned again = __ballot_sync(0xffffffffu, mine && odd && c == 0);
+    for (; again; again &= again - 1) {
+      const int ra = r0 + (__ffs(again) - 1) / kLanes;
+      redo_row(p, pl, b, s0 + ra / p.G, hk * p.G + ra % p.G,
+               qs + tid / 32 * 128, lane);
+    }
+  }
 }
 
 template <int D>
@@ -424,13 +498,13 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (lane == 0) mbar_arrive(p_full(st));
     }
     // ---------------- o = O / l ----------------
-    if (n > 0) {
-      if (!__all_sync(0xffffffffu,
-                      wait_bar_rest(o_done, (n - 1) & 1u, abort_flag,
-                                    p.status)))
+    // The last score product came before the second products of the last two
+    // steps: both may be open, and a parity names one phase of two.
+    for (int i = max(n - 2, 0); i < n; ++i)
+      if (!__all_sync(0xffffffffu, wait_bar_rest(o_done, i & 1u, abort_flag,
+                                                 p.status)))
         goto done;
-      tc_fence_after();
-    }
+    tc_fence_after();
     const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
     const bool some = l > 0.f || l != l;
     const float inv = some ? 1.f / l : 0.f;
@@ -476,7 +550,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     if (live) {
       const float lse2 = some ? m + log2f(l) : neg_inf;
       if (pl.splits > 1)
-        // a NaN tells the joining kernel to compute the row again
+        // a NaN tells the joining CTA to compute the row again
         pl.part_l[part] = odd ? __int_as_float(0x7fffffff) : lse2;
       else
         pl.lse[at] = some ? lse2 * 0.69314718055994531f : neg_inf;
@@ -492,7 +566,24 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
   }
 done:
+  if (pl.splits > 1) __threadfence();  // this CTA's parts, before the count
   __syncthreads();
+  if (pl.splits > 1) {
+    // (also after a wait that gave up: the counts stay whole)
+    const int item = blockIdx.x / pl.splits;
+    if (tid == 0) {
+      const uint32_t before = atomicAdd(pl.done + item, 1u);
+      const bool last = before + 1 == (uint32_t)pl.splits;
+      if (last) pl.done[item] = 0u;  // for the next call
+      __threadfence();
+      *sCount = last;
+    }
+    __syncthreads();
+    if (*sCount)
+      join_parts<D>(p, pl, (size_t)item * pl.splits * (pl.qt * p.G), b, s0, nq,
+                    hk, reinterpret_cast<float *>(smem), tid);
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
@@ -500,59 +591,12 @@ done:
   }
 }
 
-// Joins the parts of a split tile: o = sum_i w_i o_i / sum_i w_i with
-// w_i = 2^(l_i - max).  One warp a row.
-__global__ void __launch_bounds__(256)
-    block_attn_join_kernel(const BlockAttn p, const FwdPlan pl) {
-  __shared__ float qs_all[8][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long r = (long long)blockIdx.x * 8 + warp;
-  if (r >= (long long)p.S * p.B * p.H) return;
-  const float neg_inf = -__int_as_float(0x7f800000);
-  const int h = (int)(r % p.H);
-  const int b = (int)(r / p.H % p.B), s = (int)(r / p.H / p.B);
-  const int hk = h / p.G, tile = s / pl.qt;
-  const int rows = pl.qt * p.G;
-  const size_t item = ((size_t)(pl.tiles - 1 - tile) * p.B + b) * p.Hk + hk;
-  const size_t part =
-      item * pl.splits * rows + (s - tile * pl.qt) * p.G + h % p.G;
-  float mx = neg_inf;
-  bool odd = false;
-  for (int i = lane; i < pl.splits; i += 32) {
-    const float l = pl.part_l[part + (size_t)i * rows];
-    odd |= l != l;
-    mx = fmaxf(mx, l);
-  }
-  for (int x = 16; x; x >>= 1)
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  float acc[4] = {}, ls = neg_inf;
-  if (__any_sync(0xffffffffu, odd)) {
-    float *qs = qs_all[warp];
-    for (int d = lane; d < p.D; d += 32)
-      qs[d] = __bfloat162float(p.q[r * p.D + d]);
-    __syncwarp();
-    bool bad = false;
-    attn_row(p, b, s, h / p.G, qs, lane, bad, acc, ls);
-  } else if (mx > neg_inf) {
-    float sum = 0.f;
-    for (int i = 0; i < pl.splits; ++i) {
-      const float w = ex2(pl.part_l[part + (size_t)i * rows] - mx);
-      sum += w;
-      const float *src = pl.part_o + (part + (size_t)i * rows) * p.D + lane;
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        if (d * 32 < p.D) acc[d] = fmaf(w, src[32 * d], acc[d]);
-    }
-    for (int d = 0; d < 4; ++d) acc[d] /= sum;
-    ls = (mx + log2f(sum)) * 0.69314718055994531f;
-  }
-  for (int d = 0; d * 32 < p.D; ++d)
-    pl.o[r * p.D + lane + 32 * d] = __float2bfloat16(acc[d]);
-  if (lane == 0) pl.lse[r] = ls;
-}
-
 // Room for two CTAs an SM on the largest device: a split launch has no more.
 constexpr int kSplitItems = 320;
+// A CTA takes some 5 us to start and end, a step 0.6 us.
+constexpr int kMinSteps = 2;
+static_assert(256 + kSplitItems / 2 * 4 <= DSA_BLOCK_ATTN_HEADER,
+              "a count for each item that is split");
 
 template <int D>
 int launch_fwd(const CUtensorMap &tm_q, const KvMaps &maps,
@@ -578,20 +622,23 @@ int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
   pl.cap = (int)(most < p.nblk ? most : p.nblk);
   pl.o = static_cast<__nv_bfloat16 *>(out_o);
   pl.lse = out_lse;
-  // Few tiles: share each among CTAs until two an SM are busy, with a step
-  // each at least.
+  // Few tiles: share each among CTAs until two an SM are busy, with
+  // kMinSteps steps each at least.
   const long long items = (long long)pl.tiles * p.B * p.Hk;
   long long slots = 2ll * num_sms;
   if (slots > kSplitItems) slots = kSplitItems;
   pl.splits = 1;
   if (items * 2 <= slots) {
     long long n = slots / items;
-    const long long steps = ((long long)pl.cap * p.blk + kKeys - 1) / kKeys;
+    long long steps = ((long long)pl.cap * p.blk + kKeys - 1) / kKeys;
+    steps = (steps + kMinSteps - 1) / kMinSteps;
     if (n > steps) n = steps;
     pl.splits = (int)n;
   }
   if (pl.splits > 1) {
-    pl.part_l = reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
+    char *ws = static_cast<char *>(workspace);
+    pl.done = reinterpret_cast<uint32_t *>(ws + 256);
+    pl.part_l = reinterpret_cast<float *>(ws + DSA_BLOCK_ATTN_HEADER);
     const size_t rows = (size_t)items * pl.splits * pl.qt * p.G;
     pl.part_o = pl.part_l + ((rows + 63) & ~(size_t)63);
   }
@@ -604,10 +651,7 @@ int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
   if (rc != DSA_OK) return rc;
   rc = p.D == 64 ? launch_fwd<64>(tm_q, maps, p, pl, st)
                  : launch_fwd<128>(tm_q, maps, p, pl, st);
-  if (rc != DSA_OK || pl.splits == 1) return rc;
-  const long long rows = (long long)p.S * p.B * p.H;
-  block_attn_join_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return rc;
 }
 
 int fwd_common(BlockAttn &p, void *out_o, float *out_lse, void *workspace,
@@ -699,13 +743,13 @@ size_t dsa_block_attn_workspace_size(int S, int B, int H, int Hk, int D,
     return 0;
   // the status word, then the parts of tiles shared among CTAs
   const int G = H / Hk;
-  if (G > DSA_BLOCK_ATTN_MAX_GROUP) return 256;
+  if (G > DSA_BLOCK_ATTN_MAX_GROUP) return DSA_BLOCK_ATTN_HEADER;
   long long qt = dsa::tile_queries(G, dsa::kRows);
   if (qt > S) qt = S;
   const long long items = ((S + qt - 1) / qt) * B * Hk;
-  if (items * 2 > dsa::kSplitItems) return 256;
+  if (items * 2 > dsa::kSplitItems) return DSA_BLOCK_ATTN_HEADER;
   const size_t rows = (size_t)dsa::kSplitItems * qt * G;
-  return 256 + (rows + 64) * 4 + rows * D * 4;
+  return DSA_BLOCK_ATTN_HEADER + (rows + 64) * 4 + rows * D * 4;
 }
 
 int dsa_block_attn_fwd(const void *q, const void *k, const void *v,
