@@ -629,11 +629,13 @@ def dsa_norm_rope_fwd(q, k, inv_freq, positions=None, wq=None, wk=None,
     S, B, H, Hk, D, R = _rope_inputs(q, k, inv_freq, positions, wq, wk, dt)
     if out_q is None:
         out_q = torch.empty((S, B, H, D), dtype=dt, device=q.device)
-    _dense("out_q", out_q, dt, (S, B, H, D))
+    else:
+        _dense("out_q", out_q, dt, (S, B, H, D))
     if k is not None:
         if out_k is None:
             out_k = torch.empty((S, B, Hk, D), dtype=dt, device=q.device)
-        _dense("out_k", out_k, dt, (S, B, Hk, D))
+        else:
+            _dense("out_k", out_k, dt, (S, B, Hk, D))
     rc = lib.dsa_norm_rope_fwd(
         _addr(q), _strides(q), _addr(k), None if k is None else _strides(k),
         _ROPE_DTYPES[dt], S, B, H, Hk, D, _addr(wq), _addr(wk), float(eps),
@@ -735,7 +737,8 @@ def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
             raise ValueError("q must be [S, B, H, D] with k's S, B and D")
         if out_q is None:
             out_q = torch.empty((S, B, H, D), dtype=bf, device=q.device)
-        _dense("out_q", out_q, bf, (S, B, H, D))
+        else:
+            _dense("out_q", out_q, bf, (S, B, H, D))
     if workspace is None:
         workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
     rc = lib.dsa_paged_append(
@@ -780,15 +783,19 @@ def _selection(blocks, B, S, Hk, q_pos):
     return (1 if blocks.dim() == 3 else Hk), blocks.shape[-1]
 
 
-def _block_attn_out(q, size, out_o, out_lse, workspace):
+def _block_attn_out(q, shape, out_o, out_lse, workspace):
+    """The outputs and the workspace of a forward, made where not given."""
     S, B, H, D = q.shape
     if out_o is None:
         out_o = torch.empty_like(q)
-    _dense("out_o", out_o, torch.bfloat16, (S, B, H, D))
+    else:
+        _dense("out_o", out_o, torch.bfloat16, (S, B, H, D))
     if out_lse is None:
         out_lse = torch.empty((S, B, H), dtype=torch.float32, device=q.device)
-    _dense("out_lse", out_lse, torch.float32, (S, B, H))
+    else:
+        _dense("out_lse", out_lse, torch.float32, (S, B, H))
     if workspace is None:
+        size = dsa_block_attn_workspace_size(*shape)
         if size == 0:
             raise DsaError(1, "dsa_block_attn_workspace_size")
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
@@ -819,9 +826,8 @@ def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
     _last_contiguous("v", v, torch.bfloat16, (T, B, Hk, D))
     sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
     out_o, out_lse, workspace = _block_attn_out(
-        q, dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
-                                         local_blocks),
-        out_o, out_lse, workspace)
+        q, (S, B, H, Hk, D, T, block_size, topk, local_blocks), out_o,
+        out_lse, workspace)
     rc = lib.dsa_block_attn_fwd(
         _addr(q), _addr(k), _addr(v), _strides2(k, v), S, B, H, Hk, D, T,
         _addr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
@@ -854,10 +860,8 @@ def dsa_block_attn_paged_fwd(q, k_cache, v_cache, page_table, blocks,
     max_pages = page_table.shape[1]
     sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
     out_o, out_lse, workspace = _block_attn_out(
-        q, dsa_block_attn_workspace_size(S, B, H, Hk, D,
-                                         max_pages * page_size, block_size,
-                                         topk, local_blocks),
-        out_o, out_lse, workspace)
+        q, (S, B, H, Hk, D, max_pages * page_size, block_size, topk,
+            local_blocks), out_o, out_lse, workspace)
     rc = lib.dsa_block_attn_paged_fwd(
         _addr(q), _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
         pages, page_size, _addr(page_table), max_pages, S, B, H, Hk, D,
@@ -892,13 +896,16 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
     if grad_q is None:
         grad_q = torch.empty_like(q)
+    else:
+        _dense("grad_q", grad_q, bf, (S, B, H, D))
     if grad_k is None:
         grad_k = torch.empty((T, B, Hk, D), dtype=bf, device=q.device)
+    else:
+        _dense("grad_k", grad_k, bf, (T, B, Hk, D))
     if grad_v is None:
         grad_v = torch.empty((T, B, Hk, D), dtype=bf, device=q.device)
-    _dense("grad_q", grad_q, bf, (S, B, H, D))
-    _dense("grad_k", grad_k, bf, (T, B, Hk, D))
-    _dense("grad_v", grad_v, bf, (T, B, Hk, D))
+    else:
+        _dense("grad_v", grad_v, bf, (T, B, Hk, D))
     if workspace is None:
         n = dsa_block_attn_bwd_workspace_size(S, B, H, Hk, D, T, block_size,
                                               topk, local_blocks)

@@ -182,15 +182,18 @@ __device__ __forceinline__ void token_turns(const RopeArgs &a, int pos,
 }
 
 // The rotation's coefficients of a lane's 8 elements, with the weights where
-// given: y_e = x_e c + x_partner s (times the row's rstd).  An element outside
-// the rotated part is its own partner with half its coefficient in each, so
-// that an infinity there stays one.  Arithmetic on pairs (two fp32 a
-// register pair and instruction).
+// given: y_e = x_e c + x_partner s (times the row's rstd); s = 0 outside the
+// rotated part.  There x_partner is left out where it may not be finite (an
+// infinity stays one): `plain` says that the lane's elements all are.
+// Arithmetic on pairs (two fp32 a register pair and instruction).
 template <typename T, bool VEC>
 struct Turn {
   float2 c[4], s[4];
   int src_lane;      // lane of the partners (halves layout, 16-byte pieces)
   unsigned rotated;  // a bit for each element with a partner
+
+  int p0;            // VEC: first pair of the lane's chunk
+  float sign;        // VEC, halves: of s
 
   static __device__ __forceinline__ int partner(const RopeArgs &a, int e) {
     const int rel = e - a.r0;
@@ -198,52 +201,110 @@ struct Turn {
     if (a.interleaved) return a.r0 + (rel ^ 1);
     return rel < a.R / 2 ? e + a.R / 2 : e - a.R / 2;
   }
-  // `back` turns the other way (without weights).
-  __device__ __forceinline__ void set(const RopeArgs &a, int e0, int lane,
-                                      const float2 *cs, const float *w,
-                                      bool back) {
+  // What stays the same from token to token; `back` turns the other way.
+  __device__ __forceinline__ void init(const RopeArgs &a, int e0, int lane,
+                                       bool back) {
     const int rel0 = e0 - a.r0;
+    const bool first = a.interleaved || rel0 < a.R / 2;
     src_lane = lane;
-    if (VEC && !a.interleaved && rel0 >= 0 && rel0 < a.R)
-      src_lane = rel0 < a.R / 2 ? lane + a.R / 16 : lane - a.R / 16;
     rotated = 0u;
-    float cc[8], ss[8];
+    p0 = 0;
+    sign = first != back ? -1.f : 1.f;
+    if (VEC) {
+      if (rel0 >= 0 && rel0 < a.R) {
+        rotated = 0xffu;
+        p0 = a.interleaved ? rel0 / 2 : first ? rel0 : rel0 - a.R / 2;
+        if (!a.interleaved)
+          src_lane = first ? lane + a.R / 16 : lane - a.R / 16;
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int rel = rel0 + i;
-      cc[i] = ss[i] = 0.5f;
-      if (e0 + i >= a.D) continue;
-      if (rel >= 0 && rel < a.R) {
-        const int pi =
-            a.interleaved ? rel >> 1 : rel < a.R / 2 ? rel : rel - a.R / 2;
-        const bool first = a.interleaved ? (rel & 1) == 0 : rel < a.R / 2;
-        const float2 v = cs[pi];
-        cc[i] = v.x;
-        ss[i] = first != back ? -v.y : v.y;
-        rotated |= 1u << i;
+      for (int i = 0; i < 8; ++i)
+        if (rel0 + i >= 0 && rel0 + i < a.R && e0 + i < a.D)
+          rotated |= 1u << i;
+    }
+  }
+  // The token's coefficients.  `w`: the weights in shared memory (zeros past
+  // D), or nullptr.
+  __device__ __forceinline__ void set(const RopeArgs &a, int e0, bool back,
+                                      const float2 *cs, const float *w) {
+    if constexpr (VEC) {
+      const float4 *q = reinterpret_cast<const float4 *>(cs + p0);
+      const float one = rotated ? 0.f : 1.f, turn = rotated ? 1.f : 0.f;
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // two pairs
+          const float4 v = q[i];
+          c[2 * i] = make_float2(fmaf(v.x, turn, one), fmaf(v.x, turn, one));
+          c[2 * i + 1] = make_float2(fmaf(v.z, turn, one),
+                                     fmaf(v.z, turn, one));
+          s[2 * i] = make_float2(v.y * turn * sign, -v.y * turn * sign);
+          s[2 * i + 1] = make_float2(v.w * turn * sign, -v.w * turn * sign);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 v = q[i];
+          c[i] = make_float2(fmaf(v.x, turn, one), fmaf(v.z, turn, one));
+          s[i] = make_float2(v.y * turn * sign, v.w * turn * sign);
+        }
       }
       if (w) {
-        cc[i] *= __ldg(w + e0 + i);
-        ss[i] *= __ldg(w + partner(a, e0 + i));
-      }
-    }
+        // the partners' weights: the halves' other chunk, or the neighbours
+        const int eo = a.interleaved || !rotated ? e0
+                       : e0 - a.r0 < a.R / 2     ? e0 + a.R / 2
+                                                 : e0 - a.R / 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = make_float2(cc[2 * i], cc[2 * i + 1]);
-      s[i] = make_float2(ss[2 * i], ss[2 * i + 1]);
+        for (int i = 0; i < 2; ++i) {
+          const float4 m = *reinterpret_cast<const float4 *>(w + e0 + 4 * i);
+          const float4 o = *reinterpret_cast<const float4 *>(w + eo + 4 * i);
+          c[2 * i] = __fmul2_rn(c[2 * i], make_float2(m.x, m.y));
+          c[2 * i + 1] = __fmul2_rn(c[2 * i + 1], make_float2(m.z, m.w));
+          s[2 * i] = __fmul2_rn(s[2 * i], a.interleaved
+                                              ? make_float2(o.y, o.x)
+                                              : make_float2(o.x, o.y));
+          s[2 * i + 1] = __fmul2_rn(s[2 * i + 1], a.interleaved
+                                                      ? make_float2(o.w, o.z)
+                                                      : make_float2(o.z, o.w));
+        }
+      }
+    } else {
+      float cc[8], ss[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int rel = e0 + i - a.r0;
+        cc[i] = 1.f;
+        ss[i] = 0.f;
+        if (rotated >> i & 1u) {
+          const int pi =
+              a.interleaved ? rel >> 1 : rel < a.R / 2 ? rel : rel - a.R / 2;
+          const bool first = a.interleaved ? (rel & 1) == 0 : rel < a.R / 2;
+          const float2 v = cs[pi];
+          cc[i] = v.x;
+          ss[i] = first != back ? -v.y : v.y;
+        }
+        if (w && e0 + i < a.D) {
+          cc[i] *= w[e0 + i];
+          ss[i] *= w[partner(a, e0 + i)];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = make_float2(cc[2 * i], cc[2 * i + 1]);
+        s[i] = make_float2(ss[2 * i], ss[2 * i + 1]);
+      }
     }
   }
   // y = x turned.  `buf`: the row's LPR * 8 floats of shared memory.
   __device__ __forceinline__ void apply(const RopeArgs &a,
                                         const Chunk<T, VEC> &ch,
                                         const float2 (&x)[4], float2 (&y)[4],
-                                        int e0, float *buf) const {
+                                        int e0, float *buf, bool plain) const {
     float2 o[4];
     if constexpr (VEC) {  // a chunk is turned whole or not at all
       if (a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          o[i] = rotated ? make_float2(x[i].y, x[i].x) : x[i];
+        for (int i = 0; i < 4; ++i) o[i] = make_float2(x[i].y, x[i].x);
       } else {
         Chunk<T, VEC> from;
 #pragma unroll
@@ -261,9 +322,16 @@ struct Turn {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int e = e0 + 2 * i;  // past D: the lane's own (zero)
+        const int e = e0 + 2 * i;  // past D: zero
         o[i].x = e < a.D ? buf[partner(a, e)] : 0.f;
         o[i].y = e + 1 < a.D ? buf[partner(a, e + 1)] : 0.f;
+      }
+    }
+    if (!plain) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!(rotated >> (2 * i) & 1u)) o[i].x = 0.f;
+        if (!(rotated >> (2 * i + 1) & 1u)) o[i].y = 0.f;
       }
     }
 #pragma unroll
@@ -288,14 +356,13 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// A lane's 8 weights (ones without).
-__device__ __forceinline__ void load_w(const float *w, int e0, int D,
-                                       float2 (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = make_float2(1.f, 1.f);
-    if (w && e0 + 2 * i < D) x[i].x = __ldg(w + e0 + 2 * i);
-    if (w && e0 + 2 * i + 1 < D) x[i].y = __ldg(w + e0 + 2 * i + 1);
+// Both sets' weights into shared memory, zeros past D.
+__device__ __forceinline__ void load_weights(const RopeArgs &a,
+                                             float (&sw)[2][kRopeMaxD]) {
+  for (int i = threadIdx.x; i < 2 * kRopeMaxD; i += kRopeThreads) {
+    const float *w = i < kRopeMaxD ? a.q.w : a.k.w;
+    const int e = i % kRopeMaxD;
+    sw[i / kRopeMaxD][e] = w && e < a.D ? __ldg(w + e) : 0.f;
   }
 }
 
@@ -309,21 +376,25 @@ template <typename T, bool VEC, int LPR, int KIND>
 __device__ __forceinline__ void rope_heads(const RopeArgs &a,
                                            const RopeRows &r, const T *src0,
                                            T *dst0, long long dh, int h0,
-                                           int h1, int lane, int sub, int e0,
-                                           const float2 *cs, float *buf) {
+                                           int h1, int sub, int e0,
+                                           Turn<T, VEC> &turn,
+                                           const float2 *cs, const float *w,
+                                           float *buf) {
   constexpr int RPW = 32 / LPR;
   if (h0 >= h1) return;
   const bool norm = KIND < 2 && r.w != nullptr;
-  Turn<T, VEC> turn;
-  if (KIND < 2) turn.set(a, e0, lane, cs, r.w, false);
-  const float over_d = 1.f / a.D;
-  for (int hb = h0; hb < h1; hb += kBatch * RPW) {
-    Chunk<T, VEC> x[kBatch];
+  Chunk<T, VEC> x[kBatch];
+  auto fetch = [&](int hb) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int h = hb + u * RPW + sub;
       x[u].load(src0 + h * r.sh, e0, h < h1 ? a.D : 0);
     }
+  };
+  fetch(h0);  // on the way while the coefficients are made
+  if (KIND < 2) turn.set(a, e0, false, cs, norm ? w : nullptr);
+  const float over_d = 1.f / a.D;
+  for (int hb = h0;;) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int h = hb + u * RPW + sub;
@@ -331,10 +402,10 @@ __device__ __forceinline__ void rope_heads(const RopeArgs &a,
       if constexpr (KIND < 2) {
         float2 n[4], y[4];
         x[u].get(n);
-        turn.apply(a, x[u], n, y, e0, buf);
+        const float sq = squares(n);
+        turn.apply(a, x[u], n, y, e0, buf, sq < 3e38f);
         if (norm) {
-          const float r2 =
-              rsqrtf(row_sum<LPR>(squares(n)) * over_d + a.eps);
+          const float r2 = rsqrtf(row_sum<LPR>(sq) * over_d + a.eps);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             y[i] = __fmul2_rn(y[i], make_float2(r2, r2));
@@ -343,6 +414,9 @@ __device__ __forceinline__ void rope_heads(const RopeArgs &a,
       }
       if (h < h1 && dst0) x[u].store(dst0 + h * dh, e0, a.D);
     }
+    hb += kBatch * RPW;
+    if (hb >= h1) break;
+    fetch(hb);
   }
 }
 
@@ -353,40 +427,46 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
   constexpr int RPW = 32 / LPR;
   __shared__ __align__(16) float xch[VEC ? 1 : kRopeWarps * RPW * LPR * 8];
   __shared__ unsigned long long fr[kRopeMaxD / 2];
-  __shared__ float2 cs[kRopeWarps][kRopeMaxD / 2];
+  __shared__ __align__(16) float2 cs[kRopeWarps][kRopeMaxD / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, e0 = (lane % LPR) * 8;
   float *buf = VEC ? xch : xch + (warp * RPW + sub) * LPR * 8;
   // below 2^31: only few tokens are cut into chunks
   const unsigned items = (unsigned)a.S * a.B * a.chunks;
   const int nq = a.q.heads, nk = a.k.heads, nv = a.v.heads;
+  __shared__ __align__(16) float sw[2][kRopeMaxD];
+  load_weights(a, sw);
   load_freqs(a, fr);
   __syncthreads();
-  for (unsigned item = blockIdx.x * kRopeWarps + warp; item < items;
-       item += gridDim.x * kRopeWarps) {
+  Turn<T, VEC> turn;
+  turn.init(a, e0, lane, false);
+  const unsigned stride = gridDim.x * kRopeWarps;
+  const unsigned item0 = blockIdx.x * kRopeWarps + warp;
+  // (a position is asked for one item ahead)
+  auto position = [&](unsigned item) {
+    const unsigned tk = item / (unsigned)a.chunks;
+    return item >= items ? 0
+           : a.pos       ? __ldg(a.pos + tk)
+                         : (int)(tk / (unsigned)a.B);
+  };
+  int next_pos = position(item0);
+  for (unsigned item = item0; item < items; item += stride) {
     const unsigned tk = item / (unsigned)a.chunks;
     const long long tok = tk;
     const int s = (int)(tk / (unsigned)a.B), b = (int)(tk % (unsigned)a.B);
     const int h0 = (int)(item % (unsigned)a.chunks) * a.heads_per_item;
     const int h1 = h0 + a.heads_per_item;
-    const int pos = a.pos ? __ldg(a.pos + tok) : s;
-    T *k_dst = nullptr, *v_dst = nullptr;
+    const int pos = next_pos;
+    next_pos = position(item + stride);
+    const int k0 = max(h0 - nq, 0), k1 = min(h1 - nq, nk);
+    const int v0 = max(h0 - nq - nk, 0), v1 = min(h1 - nq - nk, nv);
+    int page = -1;
     if constexpr (PAGED) {
-      if (pos >= 0) {
+      if (pos >= 0 && h1 > nq) {
         const int pg = pos / a.page_size;
-        const int page =
-            pg < a.max_pages ? __ldg(a.table + (long long)b * a.max_pages + pg)
-                             : -1;
-        if (page < 0 || page >= a.num_pages) {
-          if (lane == 0) atomicOr(a.status, kStatusIndexRange);
-        } else {
-          const long long off = pos - pg * a.page_size;
-          k_dst = static_cast<T *>(a.k.out) + page * a.k.ps + off * a.k.ts;
-          v_dst = static_cast<T *>(a.v.out) + page * a.v.ps + off * a.v.ts;
-        }
+        if (pg < a.max_pages)
+          page = __ldg(a.table + (long long)b * a.max_pages + pg);
       }
-    } else {
-      k_dst = static_cast<T *>(a.k.out) + tok * nk * (long long)a.D;
     }
     token_turns(a, pos, lane, fr, cs[warp]);
     auto src = [&](const RopeRows &r) {
@@ -394,16 +474,27 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
     };
     rope_heads<T, VEC, LPR, 0>(
         a, a.q, src(a.q), static_cast<T *>(a.q.out) + tok * nq * (long long)a.D,
-        a.D, min(h0, nq), min(h1, nq), lane, sub, e0, cs[warp], buf);
-    const int k0 = max(h0 - nq, 0), k1 = min(h1 - nq, nk);
-    if (!PAGED || k_dst)
-      rope_heads<T, VEC, LPR, 1>(a, a.k, src(a.k), k_dst, PAGED ? a.k.hs : a.D,
-                                 k0, k1, lane, sub, e0, cs[warp], buf);
+        a.D, min(h0, nq), min(h1, nq), sub, e0, turn, cs[warp], sw[0], buf);
     if constexpr (PAGED) {
-      if (v_dst)
-        rope_heads<T, VEC, LPR, 2>(a, a.v, src(a.v), v_dst, a.v.hs,
-                                   max(h0 - nq - nk, 0),
-                                   min(h1 - nq - nk, nv), lane, sub, e0, cs[warp], buf);
+      if (pos < 0 || h1 <= nq) continue;
+      if (page < 0 || page >= a.num_pages) {
+        if (lane == 0) atomicOr(a.status, kStatusIndexRange);
+        continue;
+      }
+      const long long off = pos % a.page_size;
+      rope_heads<T, VEC, LPR, 1>(
+          a, a.k, src(a.k),
+          static_cast<T *>(a.k.out) + page * a.k.ps + off * a.k.ts, a.k.hs, k0,
+          k1, sub, e0, turn, cs[warp], sw[1], buf);
+      rope_heads<T, VEC, LPR, 2>(
+          a, a.v, src(a.v),
+          static_cast<T *>(a.v.out) + page * a.v.ps + off * a.v.ts, a.v.hs, v0,
+          v1, sub, e0, turn, cs[warp], sw[1], buf);
+    } else {
+      rope_heads<T, VEC, LPR, 1>(
+          a, a.k, src(a.k),
+          static_cast<T *>(a.k.out) + tok * nk * (long long)a.D, a.D, k0, k1,
+          sub, e0, turn, cs[warp], sw[1], buf);
     }
   }
 }
@@ -415,19 +506,19 @@ template <typename T, bool VEC, int LPR>
 __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
                                                const RopeRows &r,
                                                const T *src0, long long at0,
-                                               int h0, int h1, int lane,
-                                               int sub, int e0,
-                                               const float2 *cs, float *buf,
+                                               int h0, int h1, int sub,
+                                               int e0, Turn<T, VEC> &turn,
+                                               const float *sw, float *buf,
                                                float2 (&dw)[4]) {
-  constexpr int RPW = 32 / LPR, U = kBatch / 2;
+  constexpr int RPW = 32 / LPR, U = kBatch;
   if (h0 >= h1) return;
   const bool norm = r.w != nullptr;
   const T *gin = static_cast<const T *>(r.gin) + at0;
   T *out = static_cast<T *>(r.out) + at0;
   float2 w[4];
-  load_w(r.w, e0, a.D, w);
-  Turn<T, VEC> turn;
-  turn.set(a, e0, lane, cs, nullptr, true);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = *reinterpret_cast<const float2 *>(sw + e0 + 2 * i);
   const float over_d = 1.f / a.D;
   for (int hb = h0; hb < h1; hb += U * RPW) {
     Chunk<T, VEC> x[U], g[U];
@@ -443,7 +534,7 @@ __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
       if (hb + v * RPW >= h1) break;
       float2 u[4], y[4];
       g[v].get(y);
-      turn.apply(a, g[v], y, u, e0, buf);
+      turn.apply(a, g[v], y, u, e0, buf, squares(y) < 3e38f);
       if (norm) {
         float2 xh[4], gw[4];
         x[v].get(xh);
@@ -478,16 +569,20 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
   constexpr int RPW = 32 / LPR;
   __shared__ __align__(16) float xch[kRopeWarps * RPW * LPR * 8];
   __shared__ unsigned long long fr[kRopeMaxD / 2];
-  __shared__ float2 cs[kRopeWarps][kRopeMaxD / 2];
+  __shared__ __align__(16) float2 cs[kRopeWarps][kRopeMaxD / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, e0 = (lane % LPR) * 8;
   float *buf = xch + (warp * RPW + sub) * LPR * 8;
   // below 2^31: only few tokens are cut into chunks
   const unsigned items = (unsigned)a.S * a.B * a.chunks;
   const int nq = a.q.heads, nk = a.k.heads;
+  __shared__ __align__(16) float sw[2][kRopeMaxD];
+  load_weights(a, sw);
   load_freqs(a, fr);
   __syncthreads();
   float2 dw[2][4] = {};
+  Turn<T, VEC> turn;
+  turn.init(a, e0, lane, true);
   for (unsigned item = blockIdx.x * kRopeWarps + warp; item < items;
        item += gridDim.x * kRopeWarps) {
     const unsigned tk = item / (unsigned)a.chunks;
@@ -496,15 +591,16 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
     const int h0 = (int)(item % (unsigned)a.chunks) * a.heads_per_item;
     const int h1 = h0 + a.heads_per_item;
     token_turns(a, a.pos ? __ldg(a.pos + tok) : s, lane, fr, cs[warp]);
+    turn.set(a, e0, true, cs[warp], nullptr);
     auto src = [&](const RopeRows &r) {
       return static_cast<const T *>(r.in) + s * r.ss + b * r.sb;
     };
     rope_heads_bwd<T, VEC, LPR>(a, a.q, src(a.q), tok * nq * (long long)a.D,
-                                min(h0, nq), min(h1, nq), lane, sub, e0, cs[warp], buf,
-                                dw[0]);
+                                min(h0, nq), min(h1, nq), sub, e0, turn, sw[0],
+                                buf, dw[0]);
     rope_heads_bwd<T, VEC, LPR>(a, a.k, src(a.k), tok * nk * (long long)a.D,
-                                max(h0 - nq, 0), min(h1 - nq, nk), lane, sub,
-                                e0, cs[warp], buf, dw[1]);
+                                max(h0 - nq, 0), min(h1 - nq, nk), sub, e0,
+                                turn, sw[1], buf, dw[1]);
   }
   // this CTA's weight gradients, summed over its rows in a fixed order
   for (int kind = 0; kind < 2; ++kind) {
@@ -570,8 +666,8 @@ cudaError_t launch_lpr(RopeArgs &a, int mode, int num_sms, int *ctas,
   const int heads = a.q.heads + a.k.heads + a.v.heads;
   const long long toks = (long long)a.S * a.B;
   // Heads per warp: all heads of a token share the coefficients, but a few
-  // tokens have to be spread over the GPU: halve until there are 32 warps
-  // an SM or one row set a warp is left.
+  // tokens have to be spread over the GPU: halve until there are 32 warps an
+  // SM or one row group a warp is left.
   int per = (heads + RPW - 1) / RPW * RPW;
   while (per > RPW && toks * ((heads + per - 1) / per) < 32ll * num_sms)
     per = ((per / 2) + RPW - 1) / RPW * RPW;
