@@ -21,9 +21,11 @@
 // and cuts long lists (blocks that every query holds) into chunks of a
 // quarter of an SM's share, bwd_fill_kernel writes them.  Chunks of one key
 // tile leave their sums in fp32 and bwd_join_kernel adds them in order.
-//   Both run one CTA an SM with the scores of two steps in tensor memory: the
-// compute warps work on one step (each of the two warpgroups on half of its
-// columns) while the tensor cores run the products of its neighbours.
+//   At D = 128 both run one CTA an SM with the scores of two steps in tensor
+// memory: the compute warps work on one step (each of the two warpgroups on
+// half of its columns) while the tensor cores run the products of its
+// neighbours.  At D = 64, where the products are short, the sums and one step
+// take half of tensor memory, and two CTAs share an SM.
 //   Masks cost no arithmetic away from the diagonal: a (row, block) that is
 // not held has a log-sum of +inf, so its weights are exp2(-inf) = 0.
 #include "block_attn.cuh"
@@ -315,6 +317,10 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
+// Steps in tensor memory, and CTAs an SM.
+constexpr int bwd_bufs(int D) { return D == 64 ? 1 : 2; }
+constexpr int bwd_ctas(int D) { return D == 64 ? 2 : 1; }
+
 // ---- dk, dv ---------------------------------------------------------------------
 
 template <int D>
@@ -336,7 +342,7 @@ struct KvSmem {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
     block_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_go,
                           const __grid_constant__ KvMaps maps,
@@ -346,7 +352,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr int CH = L::kCh;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kKeyTile, kRowTile);
   constexpr uint32_t kIdescA = idesc_bf16_f32_mn(kKeyTile, D, false, true);
-  constexpr uint32_t kTmK = 0, kTmV = 128, kTmBuf = 256;  // + 128 a step
+  constexpr int NB = bwd_bufs(D);
+  constexpr uint32_t kTmK = 0, kTmV = D, kTmBuf = 2 * D;  // + 128 a step
+  constexpr uint32_t kTmCols = 2 * D + NB * 128;
 
   if (blockIdx.x / pl.rep >= *pl.head) return;
   extern __shared__ uint8_t smem_raw[];
@@ -404,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tma_prefetch_desc(&maps.v);
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_alloc(smem_u32(tmem_holder), kTmCols);
     tmem_relinquish();
   }
   // rows past the query tile's are never loaded, but read as operands (times
@@ -503,25 +511,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       bool ok = n <= 0 || wait(kv_full, 0);
       int st = 0, done = 0;  // stages of the step begun and of the one before
       uint32_t ph = 0, acc = 0;
-      for (int i = 0; ok && i <= n; ++i) {
+      for (int i = 0; ok && i < n + NB - 1; ++i) {
         if (i < n) {
           if (!(ok = wait(st_full(st), ph))) break;
           tc_fence_after();
           const uint64_t qd = sdesc_k_sw128(sQ(st)),
                          gd = sdesc_k_sw128(sG(st));
-          const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
+          const uint32_t d = tmem + kTmBuf + i % NB * 128;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             mma_bf16(d, kd + koff(ks), qd + roff(ks), kIdescS, ks != 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             mma_bf16(d + 64, vd + koff(ks), gd + roff(ks), kIdescS, ks != 0);
-          mma_commit(sdp_full(i & 1));
+          mma_commit(sdp_full(i % NB));
           if (++st == kKvStages) st = 0, ph ^= 1;
         }
-        if (i > 0) {
-          const int b1 = (i - 1) & 1;
-          if (!(ok = wait(ds_full(b1), ((i - 1) >> 1) & 1u))) break;
+        if (i >= NB - 1) {
+          const int j = i - (NB - 1), b1 = j % NB;
+          if (!(ok = wait(ds_full(b1), j / NB & 1u))) break;
           tc_fence_after();
           const uint64_t qm = sdesc_mn_sw128(sQ(done), kRowTile * 128, 1024);
           const uint64_t gm = sdesc_mn_sw128(sG(done), kRowTile * 128, 1024);
@@ -536,7 +544,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mma_bf16_ta(tmem + kTmK, a + 64 + (ks >> 1) * 32 + (ks & 1) * 8,
                         qm + ((ks * 2048) >> 4), kIdescA, ks == 0 ? acc : 1u);
           mma_commit(st_empty(done));
-          if (i == n) mma_commit(acc_full);
+          if (j + 1 == n) mma_commit(acc_full);
           acc = 1;
           if (++done == kKvStages) done = 0;
         }
@@ -555,13 +563,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     for (int i = 0; i < n; ++i) {
       const int st = i % kKvStages;
       if (!__all_sync(0xffffffffu,
-                      wait_bar_rest(sdp_full(i & 1), (i >> 1) & 1u, abort_flag,
+                      wait_bar_rest(sdp_full(i % NB), i / NB & 1u, abort_flag,
                                    p.status) &&
                           wait_bar_rest(st_full(st), (i / kKvStages) & 1u,
                                        abort_flag, p.status)))
         goto done;
       tc_fence_after();
-      const uint32_t ts = tmem + kTmBuf + (i & 1) * 128 + wg * 32 + lane_off;
+      const uint32_t ts = tmem + kTmBuf + i % NB * 128 + wg * 32 + lane_off;
       uint32_t u[32], g[32];
       __syncwarp();
       tmem_ld32(ts, u);
@@ -619,7 +627,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full(i & 1));
+      if (lane == 0) mbar_arrive(ds_full(i % NB));
     }
     // ---------------- dK (warpgroup 0), dV (1) ----------------
     if (n > 0) {
@@ -668,7 +676,7 @@ done:
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, kTmCols);
   }
 }
 
@@ -733,7 +741,7 @@ struct DqPlan {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
     block_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_go,
                          const __grid_constant__ KvMaps maps,
@@ -743,7 +751,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr uint32_t kIdescS = idesc_bf16_f32(kDqRows, kDqKeys);
   constexpr uint32_t kIdescA = idesc_bf16_f32_mn(kDqRows, D, false, true);
   // tensor memory: dQ, two steps' scores, Q and dO (bf16)
-  constexpr uint32_t kTmQ = 0, kTmBuf = 128, kTmA = 384, kTmG = 384 + D / 2;
+  constexpr int NB = bwd_bufs(D);
+  constexpr uint32_t kTmQ = 0, kTmBuf = D, kTmA = D + NB * 128,
+                     kTmG = kTmA + D / 2, kTmCols = kTmG + D / 2;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -804,7 +814,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tma_prefetch_desc(&maps.v);
   }
   if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(tmem_holder), 512);
+    tmem_alloc(smem_u32(tmem_holder), kTmCols);
     tmem_relinquish();
   }
   const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
@@ -863,25 +873,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_after();
       int st = 0, done = 0;
       uint32_t ph = 0, acc = 0;
-      for (int i = 0; ok && i <= n; ++i) {
+      for (int i = 0; ok && i < n + NB - 1; ++i) {
         if (i < n) {
           if (!(ok = wait(kv_full(st), ph))) break;
           tc_fence_after();
           const uint64_t kd = sdesc_k_sw128(sK(st)),
                          vd = sdesc_k_sw128(sV(st));
-          const uint32_t d = tmem + kTmBuf + (i & 1) * 128;
+          const uint32_t d = tmem + kTmBuf + i % NB * 128;
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             mma_bf16_ta(d, ta + ks * 8, kd + koff(ks), kIdescS, ks != 0);
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
             mma_bf16_ta(d + 64, tg + ks * 8, vd + koff(ks), kIdescS, ks != 0);
-          mma_commit(sdp_full(i & 1));
+          mma_commit(sdp_full(i % NB));
           if (++st == pl.stages) st = 0, ph ^= 1;
         }
-        if (i > 0) {
-          const int b1 = (i - 1) & 1;
-          if (!(ok = wait(ds_full(b1), ((i - 1) >> 1) & 1u))) break;
+        if (i >= NB - 1) {
+          const int j = i - (NB - 1), b1 = j % NB;
+          if (!(ok = wait(ds_full(b1), j / NB & 1u))) break;
           tc_fence_after();
           const uint64_t km = sdesc_mn_sw128(sK(done), kDqKeys * 128, 1024);
           const uint32_t a = tmem + kTmBuf + b1 * 128;
@@ -891,7 +901,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mma_bf16_ta(tmem + kTmQ, a + (ks >> 1) * 32 + (ks & 1) * 8,
                         km + ((ks * 2048) >> 4), kIdescA, ks == 0 ? acc : 1u);
           mma_commit(kv_empty(done));
-          if (i == n) mma_commit(acc_full);
+          if (j + 1 == n) mma_commit(acc_full);
           acc = 1;
           if (++done == pl.stages) done = 0;
         }
@@ -942,11 +952,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const uint32_t mask = wg ? masks[1] : masks[0];
       const bool late = wg ? diag[1] : diag[0];
       const bool any = __any_sync(0xffffffffu, mask != 0u);
-      if (!__all_sync(0xffffffffu, wait_bar_rest(sdp_full(i & 1), (i >> 1) & 1u,
+      if (!__all_sync(0xffffffffu, wait_bar_rest(sdp_full(i % NB), i / NB & 1u,
                                                 abort_flag, p.status)))
         goto done;
       tc_fence_after();
-      const uint32_t ts = tmem + kTmBuf + (i & 1) * 128 + wg * 32 + lane_off;
+      const uint32_t ts = tmem + kTmBuf + i % NB * 128 + wg * 32 + lane_off;
       uint32_t dk[16];
       if (!any) {
 #pragma unroll
@@ -986,7 +996,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full(i & 1));
+      if (lane == 0) mbar_arrive(ds_full(i % NB));
     }
     if (n > 0) {
       if (!__all_sync(0xffffffffu,
@@ -1020,7 +1030,7 @@ done:
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, kTmCols);
   }
 }
 
@@ -1081,8 +1091,8 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
   dp.gq = bf(gq);
   // fewer stages where a very long context's block words need the room
   dp.stages = kDqStages;
-  while (dp.stages > 2 &&
-         DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap) > kMaxSmem)
+  while (dp.stages > 2 && DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap) >
+                              kMaxSmem / bwd_ctas(D) - 1024)
     --dp.stages;
   const int smem = DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap);
   rc = encode_q_heads(&tm_q, qp, dp.qt, p.G);
