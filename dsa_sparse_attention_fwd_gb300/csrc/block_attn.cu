@@ -50,6 +50,9 @@ constexpr int kTmaWarp = 4, kMmaWarp = 5;
 // tensor-memory columns: two steps' scores, O; P takes the second half of
 // its scores
 constexpr uint32_t kTmS = 0, kTmO = 128;
+// Stages of K and of V: what two CTAs an SM have room for (16 KB each at D =
+// 128, 8 KB at D = 64).
+constexpr int fwd_stages(int D) { return D == 64 ? 4 : 2; }
 constexpr float kSlack = 8.f;
 
 // What a launch adds to the problem.
@@ -72,10 +75,12 @@ struct FwdSmem {
   static constexpr int kKey = kCh * kKeys * 128;   // K or V of a step
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kTile;
-  static constexpr int kOffV = kOffK + 2 * kKey;
-  static constexpr int kOffBar = kOffV + 2 * kKey;
-  // q_full o_done; k_full k_empty v_full v_empty s_full p_full, two each
-  static constexpr int kOffMisc = kOffBar + 14 * 8;
+  static constexpr int kStages = fwd_stages(D);
+  static constexpr int kOffV = kOffK + kStages * kKey;
+  static constexpr int kOffBar = kOffV + kStages * kKey;
+  // q_full o_done; s_full p_full, two each; k_full k_empty v_full v_empty
+  static constexpr int kBars = 6 + 4 * kStages;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffWords = kOffMisc + 32;
   static int bytes(int nblk, int cap) {
     return kOffWords + nblk * 4 + ((cap * 2 + 15) & ~15) + 1024;
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                           const __grid_constant__ BlockAttn p,
                           const __grid_constant__ FwdPlan pl) {
   using L = FwdSmem<D>;
-  constexpr int CH = L::kCh;
+  constexpr int CH = L::kCh, NS = L::kStages;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys);
   constexpr uint32_t kIdescO = idesc_bf16_f32_mn(kRows, D, false, true);
   const float neg_inf = -__int_as_float(0x7f800000);
@@ -200,12 +205,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   };
   const uint32_t bars = base + L::kOffBar;
   const uint32_t q_full = bars, o_done = bars + 8;
-  auto k_full = [&](int i) { return bars + 16 + 8 * i; };
-  auto k_empty = [&](int i) { return bars + 32 + 8 * i; };
-  auto v_full = [&](int i) { return bars + 48 + 8 * i; };
-  auto v_empty = [&](int i) { return bars + 64 + 8 * i; };
-  auto s_full = [&](int i) { return bars + 80 + 8 * i; };
-  auto p_full = [&](int i) { return bars + 96 + 8 * i; };
+  auto s_full = [&](int i) { return bars + 16 + 8 * i; };
+  auto p_full = [&](int i) { return bars + 32 + 8 * i; };
+  auto k_full = [&](int i) { return bars + 48 + 8 * i; };
+  auto k_empty = [&](int i) { return bars + 48 + 8 * (NS + i); };
+  auto v_full = [&](int i) { return bars + 48 + 8 * (2 * NS + i); };
+  auto v_empty = [&](int i) { return bars + 48 + 8 * (3 * NS + i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -225,7 +230,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const int nq = min(pl.qt, p.S - s0);
 
   if (tid == 0) {
-    for (int i = 0; i < 14; ++i) mbar_init(bars + 8 * i, i >= 12 ? 4 : 1);
+    for (int i = 0; i < L::kBars; ++i)
+      mbar_init(bars + 8 * i, i == 4 || i == 5 ? 4 : 1);  // p_full: 4 warps
     *abort_flag = 0;
     fence_mbar_init();
     // Q arrives while the blocks are listed
@@ -261,12 +267,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const int t0 = (int)((long long)all * split / pl.splits);
   const int t1 = (int)((long long)all * (split + 1) / pl.splits);
   const int n = t1 - t0;
-  if (n > 0 && n <= 2 && units < t1 * upt) {
+  if (n > 0 && n <= NS && units < t1 * upt) {
     // the first pass of a stage is ragged: the rows past its blocks are read
     // by the second product (times zero) and must be numbers
-    for (int i = tid; i < 2 * L::kKey / 16; i += kFwdThreads) {
+    for (int i = tid; i < L::kKey / 16; i += kFwdThreads) {
       const uint32_t z[4] = {0u, 0u, 0u, 0u};
-      st_shared_v4(sV(0) + i * 16, z);
+      st_shared_v4(sV((n - 1) % NS) + i * 16, z);
     }
     fence_proxy_async_smem();
     __syncthreads();
@@ -276,8 +282,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // ---------------- TMA producer ----------------
     const int ui = lane / CH, c = lane % CH;  // unit and chunk of this lane
     for (int i = 0; i < n; ++i) {
-      const int st = i & 1;
-      const uint32_t ph = (i >> 1) & 1u;
+      const int st = i % NS;
+      const uint32_t ph = i / NS & 1u;
       const int nu = min(upt, units - (t0 + i) * upt);
       int tok = 0, outer = 0;
       if (ui < nu) {
@@ -317,30 +323,31 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const uint64_t qd = sdesc_k_sw128(sQ);
       bool ok = wait(q_full, 0);
       auto scores = [&](int i) -> bool {
-        const int st = i & 1;
-        if (!wait(k_full(st), (i >> 1) & 1u)) return false;
+        const int st = i % NS;
+        if (!wait(k_full(st), i / NS & 1u)) return false;
         tc_fence_after();
         const uint64_t kd = sdesc_k_sw128(sK(st));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          mma_bf16(tmem + kTmS + st * 64, qd + qoff(ks), kd + koff(ks),
+          mma_bf16(tmem + kTmS + (i & 1) * 64, qd + qoff(ks), kd + koff(ks),
                    kIdescS, ks != 0);
         mma_commit(k_empty(st));
-        mma_commit(s_full(st));
+        mma_commit(s_full(i & 1));
         return true;
       };
       if (ok && n > 0) ok = scores(0);
       uint32_t acc = 0;
       for (int i = 0; ok && i < n; ++i) {
         if (i + 1 < n && !(ok = scores(i + 1))) break;
-        const int st = i & 1;
-        const uint32_t ph = (i >> 1) & 1u;
-        if (!(ok = wait(v_full(st), ph) && wait(p_full(st), ph))) break;
+        const int st = i % NS;
+        if (!(ok = wait(v_full(st), i / NS & 1u) &&
+                   wait(p_full(i & 1), (i >> 1) & 1u)))
+          break;
         tc_fence_after();
         const uint64_t vd = sdesc_mn_sw128(sV(st), kKeys * 128, 1024);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_bf16_ta(tmem + kTmO, tmem + kTmS + st * 64 + 32 + ks * 8,
+          mma_bf16_ta(tmem + kTmO, tmem + kTmS + (i & 1) * 64 + 32 + ks * 8,
                       vd + ((ks * 2048) >> 4), kIdescO, ks == 0 ? acc : 1u);
         mma_commit(v_empty(st));
         mma_commit(o_done);
@@ -367,9 +374,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       step_masks(words, list, t0, count, p.lb, qi & 31, pos, pos_lo, next,
                  next_diag);
     for (int i = 0; i < n; ++i) {
-      const int st = i & 1;
-      const uint32_t ph = (i >> 1) & 1u;
-      const uint32_t tS = tmem + kTmS + st * 64 + lane_off;
+      const int st = i % NS;
+      const uint32_t tS = tmem + kTmS + (i & 1) * 64 + lane_off;
       const int t = t0 + i;
       const uint32_t mask[2] = {next[0], next[1]};
       const bool diag[2] = {next_diag[0], next_diag[1]};
@@ -377,8 +383,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         held[c] = __any_sync(0xffffffffu, mask[c] != 0u);
-      if (!__all_sync(0xffffffffu, wait_bar_rest(s_full(st), ph, abort_flag,
-                                                 p.status)))
+      if (!__all_sync(0xffffffffu, wait_bar_rest(s_full(i & 1), (i >> 1) & 1u,
+                                                 abort_flag, p.status)))
         goto done;
       tc_fence_after();
       uint32_t u[2][32];
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
             list[x / per] * p.blk + x % per * unit + row % unit > pos_hi;
         if (__any_sync(0xffffffffu, over)) {
           if (!__all_sync(0xffffffffu,
-                          wait_bar_rest(v_full(st), ph, abort_flag,
+                          wait_bar_rest(v_full(st), i / NS & 1u, abort_flag,
                                         p.status)))
             goto done;
           const uint32_t z[4] = {0u, 0u, 0u, 0u};
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(st));
+      if (lane == 0) mbar_arrive(p_full(i & 1));
     }
     // ---------------- o = O / l ----------------
     // The last score product came before the second products of the last two

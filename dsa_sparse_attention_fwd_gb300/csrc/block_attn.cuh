@@ -100,13 +100,30 @@ __device__ __forceinline__ void mark_blocks(const BlockAttn &p, int b, int s0,
                                             int nq, int hk, uint32_t *words,
                                             int tid, int nthreads,
                                             FirstMark f) {
-  const int n_cand = p.topk + p.local;
+  constexpr int U = 4;  // candidates of a thread on the way together
+  const int n_cand = p.topk + p.local, all = nq * n_cand;
   if (f.n >= 0) atomicOr(words + f.n, 1u << f.i);
-  for (int x = tid + nthreads; x < nq * n_cand; x += nthreads) {
-    const int i = x / n_cand;
-    const int n = mark_at(p, b, s0, hk, row_pos(p.q_pos, b, s0), i,
-                          x - i * n_cand, f.bad);
-    if (n >= 0) atomicOr(words + n, 1u << i);
+  if (all > nthreads) {
+    const long long pos0 = row_pos(p.q_pos, b, s0);
+    for (int x0 = tid + nthreads; x0 < all; x0 += U * nthreads) {
+      int n[U], i[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = x0 + u * nthreads;
+        i[u] = x / n_cand;
+        n[u] = x < all ? candidate(p, row_ids(p, b, s0 + i[u], hk),
+                                   pos0 + i[u], x - i[u] * n_cand, f.bad)
+                       : -1;
+      }
+      if (p.table) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (n[u] >= 0 && block_page(p, b, n[u], f.bad) < 0) n[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (n[u] >= 0) atomicOr(words + n[u], 1u << i[u]);
+    }
   }
   if (f.bad) atomicOr(p.status, kStatusIndexRange);
 }
