@@ -50,9 +50,15 @@ constexpr int kTmaWarp = 4, kMmaWarp = 5;
 // tensor-memory columns: two steps' scores, O; P takes the second half of
 // its scores
 constexpr uint32_t kTmS = 0, kTmO = 128;
+// Rows of Q in shared memory: tiles of up to 32 rows (single tokens) are held
+// in 32, and the products read what follows as the other rows, whose results
+// no one uses.  The room goes to the stages: such launches wait for memory.
+constexpr int q_rows(bool few) { return few ? 32 : kRows; }
 // Stages of K and of V: what two CTAs an SM have room for (16 KB each at D =
 // 128, 8 KB at D = 64).
-constexpr int fwd_stages(int D) { return D == 64 ? 4 : 2; }
+constexpr int fwd_stages(int D, bool few) {
+  return D == 64 ? (few ? 5 : 4) : (few ? 3 : 2);
+}
 constexpr float kSlack = 8.f;
 
 // What a launch adds to the problem.
@@ -68,14 +74,14 @@ struct FwdPlan {
   uint32_t *done;  // [item] parts that are written; zero between calls
 };
 
-template <int D>
+template <int D, bool FEW>
 struct FwdSmem {
   static constexpr int kCh = D / 64;
-  static constexpr int kTile = kCh * kRows * 128;  // 128 rows of D bf16
+  static constexpr int kTile = kCh * q_rows(FEW) * 128;
   static constexpr int kKey = kCh * kKeys * 128;   // K or V of a step
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kTile;
-  static constexpr int kStages = fwd_stages(D);
+  static constexpr int kStages = fwd_stages(D, FEW);
   static constexpr int kOffV = kOffK + kStages * kKey;
   static constexpr int kOffBar = kOffV + kStages * kKey;
   // q_full o_done; s_full p_full, two each; k_full k_empty v_full v_empty
@@ -178,13 +184,13 @@ __device__ __noinline__ void join_parts(const BlockAttn &p, const FwdPlan &pl,
   }
 }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(kFwdThreads, 2)
     block_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ KvMaps maps,
                           const __grid_constant__ BlockAttn p,
                           const __grid_constant__ FwdPlan pl) {
-  using L = FwdSmem<D>;
+  using L = FwdSmem<D, FEW>;
   constexpr int CH = L::kCh, NS = L::kStages;
   constexpr uint32_t kIdescS = idesc_bf16_f32(kRows, kKeys);
   constexpr uint32_t kIdescO = idesc_bf16_f32_mn(kRows, D, false, true);
@@ -197,8 +203,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
   const uint32_t sQ = base + L::kOffQ;
   auto sK = [&](int st) { return base + L::kOffK + st * L::kKey; };
   auto sV = [&](int st) { return base + L::kOffV + st * L::kKey; };
-  auto qoff = [](int ks) {  // K step ks in a tile of 128 rows, and of 64 keys
-    return (uint32_t)((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4;
+  auto qoff = [](int ks) {  // K step ks in Q's rows, and in 64 keys
+    return (uint32_t)((ks >> 2) * (q_rows(FEW) * 128) + (ks & 3) * 32) >> 4;
   };
   auto koff = [](int ks) {
     return (uint32_t)((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4;
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     // Q arrives while the blocks are listed
     mbar_arrive_expect_tx(q_full, CH * pl.qt * p.G * 128);
     for (int c = 0; c < CH; ++c)
-      tma_load_4d(sQ + c * (kRows * 128), &tm_q, q_full, c * kChunk, hk * p.G,
+      tma_load_4d(sQ + c * (q_rows(FEW) * 128), &tm_q, q_full, c * kChunk, hk * p.G,
                   b, s0);
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
         ((size_t)(blockIdx.x / pl.splits) * pl.splits + split) *
             (pl.qt * p.G) +
         row;
-    const uint32_t out_buf = sQ + warp * 4096;  // Q's space is free
+    const uint32_t out_buf = sK(0) + warp * 4096;  // K's space is free
     // (a short loop: this runs once a CTA, and instructions that are fetched
     // to run once take longer than they save)
     float2 chk = make_float2(0.f, 0.f);  // not a number where O is not finite
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     unsigned todo = __ballot_sync(0xffffffffu, odd);
     if (pl.splits == 1) {
       // (store_rows is done with this warp's part of the space)
-      float *qs = reinterpret_cast<float *>(smem + L::kOffQ) + warp * 1024;
+      float *qs = reinterpret_cast<float *>(smem + L::kOffK) + warp * 1024;
       for (; todo; todo &= todo - 1) {
         const int r = warp * 32 + __ffs(todo) - 1;
         redo_row(p, pl, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
@@ -587,7 +593,7 @@ done:
     __syncthreads();
     if (*sCount)
       join_parts<D>(p, pl, (size_t)item * pl.splits * (pl.qt * p.G), b, s0, nq,
-                    hk, reinterpret_cast<float *>(smem), tid);
+                    hk, reinterpret_cast<float *>(smem + L::kOffK), tid);
     __syncthreads();
   }
   if (warp == kMmaWarp) {
@@ -604,11 +610,11 @@ constexpr int kMinSteps = 2;
 static_assert(256 + kSplitItems / 2 * 4 <= DSA_BLOCK_ATTN_HEADER,
               "a count for each item that is split");
 
-template <int D>
+template <int D, bool FEW>
 int launch_fwd(const CUtensorMap &tm_q, const KvMaps &maps,
                const BlockAttn &p, const FwdPlan &pl, cudaStream_t st) {
-  auto kern = block_attn_fwd_kernel<D>;
-  const int smem = FwdSmem<D>::bytes(p.nblk, pl.cap);
+  auto kern = block_attn_fwd_kernel<D, FEW>;
+  const int smem = FwdSmem<D, FEW>::bytes(p.nblk, pl.cap);
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem) != cudaSuccess)
     return DSA_ERR_CUDA;
@@ -655,8 +661,13 @@ int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
   if (rc != DSA_OK) return rc;
   rc = encode_kv_maps(p, p.blk < kKeys ? p.blk : kKeys, &maps);
   if (rc != DSA_OK) return rc;
-  rc = p.D == 64 ? launch_fwd<64>(tm_q, maps, p, pl, st)
-                 : launch_fwd<128>(tm_q, maps, p, pl, st);
+  const bool few = pl.qt * p.G <= q_rows(true);
+  if (p.D == 64)
+    rc = few ? launch_fwd<64, true>(tm_q, maps, p, pl, st)
+             : launch_fwd<64, false>(tm_q, maps, p, pl, st);
+  else
+    rc = few ? launch_fwd<128, true>(tm_q, maps, p, pl, st)
+             : launch_fwd<128, false>(tm_q, maps, p, pl, st);
   return rc;
 }
 
