@@ -799,7 +799,7 @@ def _block_attn_out(q, shape, out_o, out_lse, workspace):
         if size == 0:
             raise DsaError(1, "dsa_block_attn_workspace_size")
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        workspace[:1024].zero_()
+        workspace[:256].zero_()
     return out_o, out_lse, workspace
 
 
@@ -812,7 +812,7 @@ def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
     empty; None: local blocks only), q_pos [B] int32 (row s at q_pos[b] + s;
     None: at s), local_blocks trailing blocks always attended to.  Returns
     (o [S, B, H, D] bf16, lse [S, B, H] fp32, workspace); a workspace of the
-    caller's has its first 1024 bytes zeroed once, before its first use."""
+    caller's has its first 256 bytes zeroed once, before its first use."""
     lib = load_library()
     dev = _on_gpu("dsa_block_attn_fwd", q=q, k=k, v=v, blocks=blocks,
                   q_pos=q_pos, out_o=out_o, out_lse=out_lse,

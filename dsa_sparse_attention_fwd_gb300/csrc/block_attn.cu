@@ -71,7 +71,7 @@ struct FwdPlan {
   float *lse;
   // splits > 1: [item][split][qt * G] rows of D and of log-sums (base 2)
   float *part_o, *part_l;
-  uint32_t *done;  // [item] parts that are written; zero between calls
+  uint32_t *done;  // a byte an item: parts written; zero between calls
 };
 
 template <int D, bool FEW>
@@ -584,9 +584,11 @@ done:
     // (also after a wait that gave up: the counts stay whole)
     const int item = blockIdx.x / pl.splits;
     if (tid == 0) {
-      const uint32_t before = atomicAdd(pl.done + item, 1u);
+      const int sh = 8 * (item & 3);
+      uint32_t *word = pl.done + (item >> 2);
+      const uint32_t before = atomicAdd(word, 1u << sh) >> sh & 0xffu;
       const bool last = before + 1 == (uint32_t)pl.splits;
-      if (last) pl.done[item] = 0u;  // for the next call
+      if (last) atomicAnd(word, ~(0xffu << sh));  // for the next call
       __threadfence();
       *sCount = last;
     }
@@ -607,8 +609,11 @@ done:
 constexpr int kSplitItems = 320;
 // A CTA takes some 5 us to start and end, a step 0.6 us.
 constexpr int kMinSteps = 2;
-static_assert(256 + kSplitItems / 2 * 4 <= DSA_BLOCK_ATTN_HEADER,
-              "a count for each item that is split");
+// The counts of written parts, in the 256 bytes that every entry point leaves
+// to the status word: no other use of a workspace touches them.
+constexpr int kDoneOffset = 64;
+static_assert(kDoneOffset + kSplitItems / 2 <= 256,
+              "a byte for each item that is split");
 
 template <int D, bool FEW>
 int launch_fwd(const CUtensorMap &tm_q, const KvMaps &maps,
@@ -645,12 +650,13 @@ int run_fwd(const BlockAttn &p, void *out_o, float *out_lse, void *workspace,
     long long steps = ((long long)pl.cap * p.blk + kKeys - 1) / kKeys;
     steps = (steps + kMinSteps - 1) / kMinSteps;
     if (n > steps) n = steps;
+    if (n > 255) n = 255;  // counted in a byte
     pl.splits = (int)n;
   }
   if (pl.splits > 1) {
     char *ws = static_cast<char *>(workspace);
-    pl.done = reinterpret_cast<uint32_t *>(ws + 256);
-    pl.part_l = reinterpret_cast<float *>(ws + DSA_BLOCK_ATTN_HEADER);
+    pl.done = reinterpret_cast<uint32_t *>(ws + kDoneOffset);
+    pl.part_l = reinterpret_cast<float *>(ws + 256);
     const size_t rows = (size_t)items * pl.splits * pl.qt * p.G;
     pl.part_o = pl.part_l + ((rows + 63) & ~(size_t)63);
   }
@@ -760,13 +766,13 @@ size_t dsa_block_attn_workspace_size(int S, int B, int H, int Hk, int D,
     return 0;
   // the status word, then the parts of tiles shared among CTAs
   const int G = H / Hk;
-  if (G > DSA_BLOCK_ATTN_MAX_GROUP) return DSA_BLOCK_ATTN_HEADER;
+  if (G > DSA_BLOCK_ATTN_MAX_GROUP) return 256;
   long long qt = dsa::tile_queries(G, dsa::kRows);
   if (qt > S) qt = S;
   const long long items = ((S + qt - 1) / qt) * B * Hk;
-  if (items * 2 > dsa::kSplitItems) return DSA_BLOCK_ATTN_HEADER;
+  if (items * 2 > dsa::kSplitItems) return 256;
   const size_t rows = (size_t)dsa::kSplitItems * qt * G;
-  return DSA_BLOCK_ATTN_HEADER + (rows + 64) * 4 + rows * D * 4;
+  return 256 + (rows + 64) * 4 + rows * D * 4;
 }
 
 int dsa_block_attn_fwd(const void *q, const void *k, const void *v,

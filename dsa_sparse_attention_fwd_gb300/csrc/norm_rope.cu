@@ -799,7 +799,8 @@ int dsa_norm_rope_fwd(const void *q, const int64_t *q_strides, const void *k,
 
 size_t dsa_norm_rope_bwd_workspace_size(int D) {
   if (D <= 0 || D > dsa::kRopeMaxD) return 0;
-  return (size_t)dsa::kRopeMaxCtas * 2 * D * sizeof(float);
+  // (the first 256 bytes stay as they are: a workspace may be shared)
+  return 256 + (size_t)dsa::kRopeMaxCtas * 2 * D * sizeof(float);
 }
 
 int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides, const void *k,
@@ -834,7 +835,8 @@ int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides, const void *k,
   if (!workspace || workspace_bytes < dsa_norm_rope_bwd_workspace_size(D))
     return DSA_ERR_WORKSPACE;
   if (!dsa::aligned(workspace, 256)) return DSA_ERR_INVALID_ARG;
-  a.partial = static_cast<float *>(workspace);
+  a.partial =
+      reinterpret_cast<float *>(static_cast<char *>(workspace) + 256);
   int num_sms = 0, ctas = 0;
   rc = dsa::device_num_sms(&num_sms);
   if (rc != DSA_OK) return rc;

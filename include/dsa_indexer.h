@@ -516,10 +516,11 @@ DSA_API int dsa_sparse_mla_fwd(const void *q, const void *c,
  * Status word: dsa_paged_append(), dsa_block_attn_fwd(),
  * dsa_block_attn_paged_fwd() and dsa_block_attn_bwd() only set bits in the
  * status word at the start of their workspace (one launch less than clearing
- * it).  Zero a new workspace's first DSA_BLOCK_ATTN_HEADER bytes once (the
- * append's 256 bytes); dsa_indexer_check() reads and clears the word.
+ * it).  Zero a new workspace's first 256 bytes once; dsa_indexer_check()
+ * reads and clears the word.  The block attention keeps counts in these 256
+ * bytes that are zero between calls; every entry point of this library leaves
+ * them so, and calls of all kinds may share a workspace in stream order.
  */
-#define DSA_BLOCK_ATTN_HEADER 1024
 
 /* Element types of dsa_norm_rope_fwd() and _bwd(). */
 #define DSA_BF16 0

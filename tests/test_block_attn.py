@@ -308,6 +308,72 @@ def test_paged_past_32_bit_offsets(dsa):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_the_longest_context(dsa, D):
+    """16384 blocks: the block words take most of the shared memory, and the
+    ids that are 16 bits wide on the way reach their end."""
+    S, H, Hk, block, T = 5, 12, 1, 16, 16384 * 16
+    g = torch.Generator().manual_seed(101)
+    q = torch.randn((S, 1, H, D), generator=g).to(BF)
+    go = torch.randn((S, 1, H, D), generator=g).to(BF)
+    k = torch.randn((T, 1, Hk, D), generator=g).to(BF)
+    v = torch.randn((T, 1, Hk, D), generator=g).to(BF)
+    blocks = torch.randint(0, 16384, (1, S, 9), generator=g, dtype=torch.int32)
+    blocks[0, :, 0] = 16383
+    blocks[0, :, 1] = 0
+    qp = torch.tensor([T - 3], dtype=torch.int32)     # rows past the last key
+    dq, dk, dv, dgo, dbl, dqp = cu(q, k, v, go, blocks, qp)
+    kw = dict(q_pos=dqp, local_blocks=2)
+    o, lse, ws = dsa.dsa_block_attn_fwd(dq, dk, dv, dbl, block, 0.125, **kw)
+    assert dsa.dsa_indexer_check(ws) == 0
+    r = block_attn_ref(q, k, v, blocks, block, 2, 0.125, qp, go)
+    check_attn(r, o, lse)
+    grads = dsa.dsa_block_attn_bwd(dq, dk, dv, o, lse, dgo, dbl, block, 0.125,
+                                   **kw)
+    assert dsa.dsa_indexer_check(grads[3]) == 0
+    check_grads(r, *grads[:3])
+
+
+@gpu
+def test_one_workspace_for_many_calls(dsa):
+    """A workspace that is zeroed once serves calls of other shapes, split and
+    not, forward and backward, and a call that reports an error."""
+    ws = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    for rnd in range(2):
+        for case in (CASES[11], CASES[1], CASES[2], CASES[8]):
+            S, B, H, Hk, D, T, block, topk, local, shared, q_pos = case
+            q, k, v, go, blocks = cu(*problem(S, B, H, Hk, D, T, block, topk,
+                                              shared, 111))
+            qp = None
+            if q_pos is not None:
+                qp = torch.tensor(q_pos, dtype=torch.int32).cuda()
+            kw = dict(q_pos=qp, local_blocks=local)
+            o, lse, _ = dsa.dsa_block_attn_fwd(q, k, v, blocks, block, 0.1, **kw)
+            o2, lse2, _ = dsa.dsa_block_attn_fwd(q, k, v, blocks, block, 0.1,
+                                                 workspace=ws, **kw)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+            g = dsa.dsa_block_attn_bwd(q, k, v, o, lse, go, blocks, block, 0.1,
+                                       **kw)
+            g2 = dsa.dsa_block_attn_bwd(q, k, v, o, lse, go, blocks, block,
+                                        0.1, workspace=ws, **kw)
+            assert all(torch.equal(a, b) for a, b in zip(g[:3], g2[:3]))
+            assert dsa.dsa_indexer_check(ws) == 0
+        # other entry points write the rest of it
+        x = torch.ones((64, 2, 4, 128), device="cuda")
+        w1 = torch.ones(128, device="cuda")
+        dsa.dsa_norm_rope_bwd(x, None, x, None, None, wq=w1, workspace=ws)
+        qi = torch.ones((40, 1, 4, 64), dtype=BF, device="cuda")
+        dsa.dsa_indexer_fwd(qi, qi[:, :, 0].contiguous(),
+                            torch.ones((40, 1, 4), device="cuda"), 1, 8,
+                            workspace=ws)
+        q, k, v, _, blocks = problem(1, 1, 4, 1, 64, 2048, 16, 16, True, 5)
+        blocks[0, 0, 3] = 5000
+        dsa.dsa_block_attn_fwd(*cu(q, k, v, blocks), 16, 0.1, workspace=ws,
+                               q_pos=torch.tensor([2047]).int().cuda())
+        assert dsa.dsa_indexer_check(ws) == 6
+
+
+@gpu
 def test_agrees_with_the_indexers_selection(dsa):
     """The indexer's top-k over keys compressed by the block size names the
     blocks: together they are attention over the best whole blocks and the
