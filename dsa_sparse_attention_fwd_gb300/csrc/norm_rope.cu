@@ -170,6 +170,9 @@ __device__ __forceinline__ void token_turns(const RopeArgs &a, int pos,
                                             const unsigned long long *fr,
                                             float2 *cs) {
   __syncwarp();
+  // Lanes outside the rotated part multiply the first eight by zero; without
+  // one nothing else writes them, and what is there may not be finite.
+  if (a.R == 0 && lane < 8) cs[lane] = make_float2(0.f, 0.f);
   for (int i = lane; i < a.R / 2; i += 32) {
     const unsigned long long ph = (unsigned long long)(long long)pos * fr[i];
     // the top half as a signed fraction of half a turn

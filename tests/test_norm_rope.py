@@ -432,3 +432,21 @@ def test_append_refuses(dsa, over, code):
              st=None)
     a.update(over)
     assert dsa.load_library().dsa_paged_append(*a.values()) == code
+
+
+@gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_no_rotation_whatever_shared_memory_holds(dsa, dt):
+    """Without a rotation no angles are written; NaN that an earlier kernel
+    left in shared memory stays out of the rows."""
+    k = torch.full((640, 1, 1, 128), float("nan"), dtype=torch.bfloat16,
+                   device="cuda")
+    qa = torch.ones((640, 1, 64, 128), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn((512, 3, 8, 128), dtype=torch.float32).to(dt).cuda()
+    for _ in range(3):
+        dsa.dsa_block_attn_fwd(qa, k, k, None, 64, 0.1, local_blocks=1)
+        y, _ = dsa.dsa_norm_rope_fwd(x, None, None)
+        assert torch.equal(y, x)
+        dsa.dsa_block_attn_fwd(qa, k, k, None, 64, 0.1, local_blocks=1)
+        g = dsa.dsa_norm_rope_bwd(x, None, x, None, None)[0]
+        assert torch.equal(g, x)
