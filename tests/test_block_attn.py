@@ -8,7 +8,8 @@ import math
 import pytest
 import torch
 
-from tests.block_ref import block_attn_ref, check_attn, check_grads
+from tests.block_ref import (block_attn_ref, check_attn, check_grads,
+                             row_keys)
 
 gpu = pytest.mark.gpu
 BF = torch.bfloat16
@@ -371,6 +372,46 @@ def test_one_workspace_for_many_calls(dsa):
         dsa.dsa_block_attn_fwd(*cu(q, k, v, blocks), 16, 0.1, workspace=ws,
                                q_pos=torch.tensor([2047]).int().cuda())
         assert dsa.dsa_indexer_check(ws) == 6
+
+
+@gpu
+@pytest.mark.parametrize("D,G,block", [(64, 1, 16), (128, 4, 64)])
+@pytest.mark.parametrize("first", [None, -2])
+def test_gradients_of_rows_with_few_keys(dsa, D, G, block, first):
+    """At a sequence's first positions the weights are one-sided and dS is a
+    small difference: the rounding of o does not enter it.  Errors: dS's
+    rounding, 2^-8 of it; a score of magnitude X is a chain of up to nine fp32
+    sums, 9 2^-23 X off, and so is the log-sum: P is 2^-18 (1 + X) off with
+    the exponential's 2^-21, and so is what dS is made of; then the result's
+    rounding."""
+    S, B, Hk = 40, 2, 2
+    q, k, v, go, blocks = problem(S, B, Hk * G, Hk, D, S, block, 3, False, 17)
+    qp = None if first is None else torch.tensor([first, 0], dtype=torch.int32)
+    kw = dict(q_pos=None if qp is None else qp.cuda(), local_blocks=1)
+    dq, dk, dv, dgo, dbl = cu(q, k, v, go, blocks)
+    o, lse, _ = dsa.dsa_block_attn_fwd(dq, dk, dv, dbl, block, 0.2, **kw)
+    gq = dsa.dsa_block_attn_bwd(dq, dk, dv, o, lse, dgo, dbl, block, 0.2,
+                                **kw)[0].double().cpu()
+    r = block_attn_ref(q, k, v, blocks, block, 1, 0.2, qp, go)
+    for b in range(B):
+        p0 = 0 if qp is None else int(qp[b])
+        for s in range(max(0, -p0), 32 - p0):
+            for h in range(Hk * G):
+                hk = h // G
+                js = row_keys(blocks, b, s, hk, p0 + s, block, 1, S)
+                kk, vv = k[js, b, hk].double(), v[js, b, hk].double()
+                g = go[s, b, h].double()
+                p = torch.softmax(0.2 * kk @ q[s, b, h].double(), 0)
+                dp = vv @ g
+                ds = 0.2 * p * (dp - p @ dp)
+                mag = vv.abs() @ g.abs()
+                off = 2.0 ** -18 * (1 + float(r["X"][s, b, h]))
+                e = 2.0 ** -8 * ds.abs() + 0.2 * p * off * (mag + p @ mag)
+                tol = e @ kk.abs()
+                want = r["gq"][s, b, h]
+                tol = tol + 2.0 ** -8 * (want.abs() + tol) + 1e-30
+                err = (gq[s, b, h] - want).abs()
+                assert bool((err <= tol).all()), (b, s, h, (err / tol).max())
 
 
 @gpu
