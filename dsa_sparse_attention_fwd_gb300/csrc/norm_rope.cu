@@ -25,6 +25,11 @@
 // loads of kBatch row groups in flight.  Rows that cannot be read in 16-byte
 // pieces (odd sizes, strides or pointers) take the same code with element
 // loads and the partner exchanged through shared memory.
+//
+// Measured on one GB300 (copies 6776 GB/s): 32768 tokens of 72 heads of 128 in
+// bf16, 1.2 GB: 206 us, 5.9 TB/s (a library copy of the same bytes 181 us, 6.7);
+// without the rotation 187, without the norm 196.  It waits for loads: six
+// CTAs of four warps hold what 80 registers a thread let them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -424,6 +429,9 @@ __device__ __forceinline__ void rope_heads(const RopeArgs &a,
 }
 
 // PAGED: k and v rows go to the cache; without it there is no v.
+// Append, measured: 8192 tokens of 40 + 2 x 8 rows of 64: 33 us, 3.5 TB/s of
+// 114 MB: a warp has two or three tokens, and for each a chain of the position,
+// its page and five batches of rows.  One token of 64 sequences: 5 us.
 template <typename T, bool VEC, int LPR, bool PAGED>
 __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
     norm_rope_kernel(const RopeArgs a) {
@@ -505,6 +513,10 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
 // Backward.  With u = the output's gradient rotated back (times m), xh = x
 // rstd:  dw += u xh;  g = u w;  dx = rstd (g - xh mean(g xh)); without a
 // weight there is no norm either: dx = u.
+// Measured: 8192 tokens of 40 heads of 128 in bf16, 252 MB: 62 us, 4.1 TB/s,
+// and 8 more for the sum of the weights' parts.  Two inputs and the
+// coefficients take 128 registers a thread, so 16 warps an SM have loads in
+// flight instead of 24.
 template <typename T, bool VEC, int LPR>
 __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
                                                const RopeRows &r,
