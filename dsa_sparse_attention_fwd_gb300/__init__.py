@@ -64,6 +64,8 @@ class DsaError(RuntimeError):
 def load_library(path: str | None = None):
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -539,19 +541,19 @@ def rope_inv_freq(rot_dim, base=10000.0, scaling=None, device=None):
 _I3, _I6 = ctypes.c_int64 * 3, ctypes.c_int64 * 6
 
 
-def _on_gpu(where, **tensors):
-    """_require_cuda() in its own words, without building device objects
-    while all is well."""
+def _on_gpu(where, names, *tensors):
+    """_require_cuda() of the tensors by these names, without building device
+    objects or a dict while all is well: the device's index."""
     dev = -1
-    for t in tensors.values():
+    for t in tensors:
         if t is not None:
-            if dev < 0 and t.is_cuda:
-                dev = t.get_device()
-            elif not t.is_cuda or t.get_device() != dev:
+            d = t.get_device()  # -1: not on a GPU
+            if d < 0 or d != dev >= 0:
                 break
+            dev = d
     else:
         return dev
-    _require_cuda(where, **tensors)
+    _require_cuda(where, **dict(zip(names.split(), tensors)))
 
 
 def _raw_stream(stream, dev):
@@ -592,23 +594,25 @@ def _dense(name, t, dt, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _rope_inputs(q, k, inv_freq, positions, wq, wk, dt):
+def _rope_inputs(q, k, inv_freq, positions, wq, wk, dt, q_name="q",
+                 k_name="k"):
     if q.dim() != 4 or (k is not None and k.dim() != 4):
         raise ValueError("q [S, B, H, D] and k [S, B, Hk, D] expected")
     S, B, H, D = q.shape
     Hk = 0 if k is None else k.shape[2]
-    _last_contiguous("q", q, dt, (S, B, H, D))
+    _last_contiguous(q_name, q, dt, (S, B, H, D))
     if k is not None:
-        _last_contiguous("k", k, dt, (S, B, Hk, D))
+        _last_contiguous(k_name, k, dt, (S, B, Hk, D))
     if inv_freq is not None and (inv_freq.dtype != torch.float64
                                  or inv_freq.dim() != 1
                                  or not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be contiguous fp64 [rot_dim / 2]")
     if positions is not None:
         _dense("positions", positions, torch.int32, (S, B))
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _dense(name, w, torch.float32, (D,))
+    if wq is not None:
+        _dense("w" + q_name, wq, torch.float32, (D,))
+    if wk is not None:
+        _dense("w" + k_name, wk, torch.float32, (D,))
     return S, B, H, Hk, D, 0 if inv_freq is None else 2 * inv_freq.numel()
 
 
@@ -621,8 +625,9 @@ def dsa_norm_rope_fwd(q, k, inv_freq, positions=None, wq=None, wk=None,
     [rot_dim / 2] fp64 (rope_inv_freq; None: no rotation), positions [S, B]
     int32 (None: row s at s).  Returns (out_q, out_k), dense."""
     lib = load_library()
-    dev = _on_gpu("dsa_norm_rope_fwd", q=q, k=k, inv_freq=inv_freq,
-                  positions=positions, wq=wq, wk=wk, out_q=out_q, out_k=out_k)
+    dev = _on_gpu("dsa_norm_rope_fwd",
+                  "q k inv_freq positions wq wk out_q out_k",
+                  q, k, inv_freq, positions, wq, wk, out_q, out_k)
     dt = q.dtype
     if dt not in _ROPE_DTYPES:
         raise TypeError(f"q must be bf16, fp16 or fp32, got {dt}")
@@ -659,9 +664,11 @@ def dsa_norm_rope_bwd(q, k, grad_out_q, grad_out_k, inv_freq, positions=None,
     outputs (dense).  Returns (grad_q, grad_k, grad_wq, grad_wk, workspace);
     the weights' gradients are fp32 [D], None without the weight."""
     lib = load_library()
-    dev = _on_gpu("dsa_norm_rope_bwd", q=q, k=k, grad_out_q=grad_out_q,
-                  grad_out_k=grad_out_k, inv_freq=inv_freq,
-                  positions=positions, wq=wq, wk=wk, workspace=workspace)
+    dev = _on_gpu("dsa_norm_rope_bwd",
+                  "q k grad_out_q grad_out_k inv_freq positions wq wk "
+                  "workspace",
+                  q, k, grad_out_q, grad_out_k, inv_freq, positions, wq, wk,
+                  workspace)
     dt = q.dtype
     if dt not in _ROPE_DTYPES:
         raise TypeError(f"q must be bf16, fp16 or fp32, got {dt}")
@@ -718,23 +725,20 @@ def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
     (out_q, workspace).  The call only sets bits in the workspace's status
     word (256 zeroed bytes to begin with; dsa_indexer_check reads it)."""
     lib = load_library()
-    dev = _on_gpu("dsa_paged_append", k=k, v=v, k_cache=k_cache,
-                  v_cache=v_cache, page_table=page_table,
-                  positions=positions, inv_freq=inv_freq, wk=wk, q=q, wq=wq,
-                  out_q=out_q, workspace=workspace)
+    dev = _on_gpu("dsa_paged_append",
+                  "k v k_cache v_cache page_table positions inv_freq wk q "
+                  "wq out_q workspace",
+                  k, v, k_cache, v_cache, page_table, positions, inv_freq, wk,
+                  q, wq, out_q, workspace)
     bf = torch.bfloat16
-    S, B, Hk, _, D, R = _rope_inputs(k, None, inv_freq, positions, wk, None,
-                                     bf)
+    S, B, Hk, H, D, R = _rope_inputs(k, q, inv_freq, positions, wk,
+                                     None if q is None else wq, bf, "k", "q")
     _last_contiguous("v", v, bf, (S, B, Hk, D))
-    pages, page_size, *_ = _paged_cache(k_cache, v_cache, page_table, B)
-    if tuple(k_cache.shape[2:]) != (Hk, D):
+    pages, page_size, cache_heads, cache_dim = _paged_cache(
+        k_cache, v_cache, page_table, B)
+    if cache_heads != Hk or cache_dim != D:
         raise ValueError("the cache's heads or head size differ from k's")
-    H = 0
     if q is not None:
-        H = q.shape[2]
-        _rope_inputs(q, None, None, positions, wq, None, bf)
-        if tuple(q.shape) != (S, B, H, D):
-            raise ValueError("q must be [S, B, H, D] with k's S, B and D")
         if out_q is None:
             out_q = torch.empty((S, B, H, D), dtype=bf, device=q.device)
         else:
@@ -814,9 +818,9 @@ def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
     (o [S, B, H, D] bf16, lse [S, B, H] fp32, workspace); a workspace of the
     caller's has its first 256 bytes zeroed once, before its first use."""
     lib = load_library()
-    dev = _on_gpu("dsa_block_attn_fwd", q=q, k=k, v=v, blocks=blocks,
-                  q_pos=q_pos, out_o=out_o, out_lse=out_lse,
-                  workspace=workspace)
+    dev = _on_gpu("dsa_block_attn_fwd",
+                  "q k v blocks q_pos out_o out_lse workspace",
+                  q, k, v, blocks, q_pos, out_o, out_lse, workspace)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q [S, B, H, D] and k [T, B, Hk, D] expected")
     S, B, H, D = q.shape
@@ -846,10 +850,11 @@ def dsa_block_attn_paged_fwd(q, k_cache, v_cache, page_table, blocks,
     through page_table [B, max_pages] int32 (S = 1: one token of each
     sequence at q_pos[b])."""
     lib = load_library()
-    dev = _on_gpu("dsa_block_attn_paged_fwd", q=q, k_cache=k_cache,
-                  v_cache=v_cache, page_table=page_table, blocks=blocks,
-                  q_pos=q_pos, out_o=out_o, out_lse=out_lse,
-                  workspace=workspace)
+    dev = _on_gpu("dsa_block_attn_paged_fwd",
+                  "q k_cache v_cache page_table blocks q_pos out_o out_lse "
+                  "workspace",
+                  q, k_cache, v_cache, page_table, blocks, q_pos, out_o,
+                  out_lse, workspace)
     if q.dim() != 4:
         raise ValueError("q [S, B, H, D] expected")
     S, B, H, D = q.shape
@@ -880,9 +885,11 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     and grad_o [S, B, H, D] bf16.  Returns (grad_q [S, B, H, D], grad_k and
     grad_v [T, B, Hk, D], dense bf16, workspace)."""
     lib = load_library()
-    dev = _on_gpu("dsa_block_attn_bwd", q=q, k=k, v=v, o=o, lse=lse,
-                  grad_o=grad_o, blocks=blocks, q_pos=q_pos, grad_q=grad_q,
-                  grad_k=grad_k, grad_v=grad_v, workspace=workspace)
+    dev = _on_gpu("dsa_block_attn_bwd",
+                  "q k v o lse grad_o blocks q_pos grad_q grad_k grad_v "
+                  "workspace",
+                  q, k, v, o, lse, grad_o, blocks, q_pos, grad_q, grad_k,
+                  grad_v, workspace)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q [S, B, H, D] and k [T, B, Hk, D] expected")
     S, B, H, D = q.shape
