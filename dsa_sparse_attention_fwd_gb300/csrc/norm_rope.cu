@@ -159,9 +159,14 @@ struct Chunk {
   }
 };
 
-// Frequencies as turns a position, 64-bit fixed point.
-__device__ __forceinline__ void load_freqs(const RopeArgs &a,
-                                           unsigned long long *fr) {
+// Frequencies as turns a position, 64-bit fixed point.  Lanes outside the
+// rotated part multiply the first eight coefficients of `cs` by zero; without a
+// rotation nothing else writes them, and what is there may not be finite.
+__device__ __forceinline__ void load_freqs(
+    const RopeArgs &a, unsigned long long *fr,
+    float2 (&cs)[kRopeWarps][kRopeMaxD / 2]) {
+  if (a.R == 0 && threadIdx.x < kRopeWarps * 8)
+    cs[threadIdx.x / 8][threadIdx.x % 8] = make_float2(0.f, 0.f);
   for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) {
     double t = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
     t -= floor(t);
@@ -175,9 +180,6 @@ __device__ __forceinline__ void token_turns(const RopeArgs &a, int pos,
                                             const unsigned long long *fr,
                                             float2 *cs) {
   __syncwarp();
-  // Lanes outside the rotated part multiply the first eight by zero; without
-  // one nothing else writes them, and what is there may not be finite.
-  if (a.R == 0 && lane < 8) cs[lane] = make_float2(0.f, 0.f);
   for (int i = lane; i < a.R / 2; i += 32) {
     const unsigned long long ph = (unsigned long long)(long long)pos * fr[i];
     // the top half as a signed fraction of half a turn
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
   const int nq = a.q.heads, nk = a.k.heads, nv = a.v.heads;
   __shared__ __align__(16) float sw[2][kRopeMaxD];
   load_weights(a, sw);
-  load_freqs(a, fr);
+  load_freqs(a, fr, cs);
   __syncthreads();
   Turn<T, VEC> turn;
   turn.init(a, e0, lane, false);
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBwdCtas)
   const int nq = a.q.heads, nk = a.k.heads;
   __shared__ __align__(16) float sw[2][kRopeMaxD];
   load_weights(a, sw);
-  load_freqs(a, fr);
+  load_freqs(a, fr, cs);
   __syncthreads();
   float2 dw[2][4] = {};
   Turn<T, VEC> turn;
