@@ -27,7 +27,7 @@
 // loads and the partner exchanged through shared memory.
 //
 // Measured on one GB300 (copies 6776 GB/s): 32768 tokens of 72 heads of 128 in
-// bf16, 1.2 GB: 206 us, 5.9 TB/s (a library copy of the same bytes 181 us, 6.7);
+// bf16, 1.2 GB: 205 us, 5.9 TB/s (a library copy of the same bytes 181 us, 6.7);
 // without the rotation 187, without the norm 196.  It waits for loads: six
 // CTAs of four warps hold what 80 registers a thread let them.
 #include <cuda_bf16.h>
@@ -515,10 +515,11 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(T), VEC))
 // Backward.  With u = the output's gradient rotated back (times m), xh = x
 // rstd:  dw += u xh;  g = u w;  dx = rstd (g - xh mean(g xh)); without a
 // weight there is no norm either: dx = u.
-// Measured: 8192 tokens of 40 heads of 128 in bf16, 252 MB: 62 us, 4.1 TB/s,
+// Measured: 8192 tokens of 40 heads of 128 in bf16, 252 MB: 60 us, 4.2 TB/s,
 // and 8 more for the sum of the weights' parts.  Two inputs and the
 // coefficients take 128 registers a thread, so 16 warps an SM have loads in
-// flight instead of 24.
+// flight instead of 24; each has the next two row groups on the way while it
+// works on two (one batch of four after the other: 2.4 us more).
 template <typename T, bool VEC, int LPR>
 __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
                                                const RopeRows &r,
@@ -527,7 +528,7 @@ __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
                                                int e0, Turn<T, VEC> &turn,
                                                const float *sw, float *buf,
                                                float2 (&dw)[4]) {
-  constexpr int RPW = 32 / LPR, U = kBatch;
+  constexpr int RPW = 32 / LPR, U = 2;
   if (h0 >= h1) return;
   const bool norm = r.w != nullptr;
   const T *gin = static_cast<const T *>(r.gin) + at0;
@@ -537,14 +538,15 @@ __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
   for (int i = 0; i < 4; ++i)
     w[i] = *reinterpret_cast<const float2 *>(sw + e0 + 2 * i);
   const float over_d = 1.f / a.D;
-  for (int hb = h0; hb < h1; hb += U * RPW) {
-    Chunk<T, VEC> x[U], g[U];
+  auto fetch = [&](Chunk<T, VEC> (&x)[U], Chunk<T, VEC> (&g)[U], int hb) {
 #pragma unroll
     for (int v = 0; v < U; ++v) {
       const int h = hb + v * RPW + sub;
       g[v].load(gin + (long long)h * a.D, e0, h < h1 ? a.D : 0);
       x[v].load(src0 + h * r.sh, e0, norm && h < h1 ? a.D : 0);
     }
+  };
+  auto work = [&](Chunk<T, VEC> (&x)[U], Chunk<T, VEC> (&g)[U], int hb) {
 #pragma unroll
     for (int v = 0; v < U; ++v) {
       const int h = hb + v * RPW + sub;
@@ -577,6 +579,14 @@ __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
       g[v].set(u);
       if (h < h1) g[v].store(out + (long long)h * a.D, e0, a.D);
     }
+  };
+  Chunk<T, VEC> xa[U], ga[U], xb[U], gb[U];
+  fetch(xa, ga, h0);
+  for (int hb = h0; hb < h1; hb += 2 * U * RPW) {
+    fetch(xb, gb, hb + U * RPW);
+    work(xa, ga, hb);
+    fetch(xa, ga, hb + 2 * U * RPW);
+    work(xb, gb, hb + U * RPW);
   }
 }
 
