@@ -563,8 +563,10 @@ __device__ __forceinline__ void rope_heads_bwd(const RopeArgs &a,
           gw[i] = __fmul2_rn(u[i], w[i]);
           dot = __ffma2_rn(gw[i], xh[i], dot);
         }
-        const float rstd =
-            rsqrtf(row_sum<LPR>(squares(xh)) * over_d + a.eps);
+        // padding of a last group (h >= h1) is a row of zeros, whose root may
+        // be infinite (eps = 0): it adds nothing to dw
+        const float ms = row_sum<LPR>(squares(xh)) * over_d + a.eps;
+        const float rstd = h < h1 ? rsqrtf(ms) : 0.f;
         // mean(g xh)
         const float back = row_sum<LPR>(dot.x + dot.y) * rstd * over_d;
 #pragma unroll

@@ -450,3 +450,26 @@ def test_no_rotation_whatever_shared_memory_holds(dsa, dt):
         dsa.dsa_block_attn_fwd(qa, k, k, None, 64, 0.1, local_blocks=1)
         g = dsa.dsa_norm_rope_bwd(x, None, x, None, None)[0]
         assert torch.equal(g, x)
+
+
+@gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D,H,Hk", [
+    (64, 6, 2), (64, 4, 1), (128, 3, 1), (50, 5, 3), (256, 3, 1), (128, 4, 2)])
+def test_backward_without_eps(dsa, dt, D, H, Hk):
+    """eps = 0 is allowed, and heads that fill a warp's last group of rows in
+    part leave nothing in the weights' gradients."""
+    S, B = 3, 2
+    q, k = make(S, B, H, D, dt, 1, False), make(S, B, Hk, D, dt, 2, False)
+    gq, gk = make(S, B, H, D, dt, 5, False), make(S, B, Hk, D, dt, 6, False)
+    wq, wk = weights(D, 3)
+    pos, f = positions(S, B, 4), inv(D)
+    got = dsa.dsa_norm_rope_bwd(
+        q.cuda(), k.cuda(), gq.cuda(), gk.cuda(), f.cuda(),
+        positions=pos.cuda(), wq=wq.cuda(), wk=wk.cuda(), eps=0.0)
+    for name, x, w, g, dx, dw in (("q", q, wq, gq, got[0], got[2]),
+                                  ("k", k, wk, gk, got[1], got[3])):
+        rx, mx, rw, mw = norm_rope_bwd_ref(x, w, g, pos, f, 0, False, 0.0)
+        assert_close("d" + name, dx, rx, mx, dt, 2.0 ** -17)
+        err = (dw.double().cpu() - rw).abs()
+        assert bool((err <= 2.0 ** -14 * mw + 1e-30).all()), "d weight " + name
