@@ -303,8 +303,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       const uint32_t ph = i / NS & 1u;
       const int nu = min(upt, units - (t0 + i) * upt);
       int tok = 0, outer = 0;
-      if (ui < nu) {
-        const int x = (t0 + i) * upt + ui;
+      if (ui < upt) {
+        // a ragged step's end repeats the last unit's keys: their scores are
+        // masked, but have to be numbers (V's rows there are zeros, see above)
+        const int x = min((t0 + i) * upt + ui, units - 1);
         const int bn = list[x / per];
         tok = bn * p.blk + x % per * unit;
         outer = b;
@@ -317,13 +319,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const uint32_t full = kv ? v_full(st) : k_full(st);
+        const int n_in = kv ? nu : upt;
         if (!__all_sync(0xffffffffu,
                         wait_bar_rest(kv ? v_empty(st) : k_empty(st), ph ^ 1u,
                                       abort_flag, p.status)))
           goto done;
-        if (lane == 0) mbar_arrive_expect_tx(full, nu * unit * CH * 128);
+        if (lane == 0) mbar_arrive_expect_tx(full, n_in * unit * CH * 128);
         __syncwarp();
-        if (ui < nu)
+        if (ui < n_in)
           tma_load_4d((kv ? sV(st) : sK(st)) + c * (kKeys * 128) +
                           ui * unit * 128,
                       kv ? &maps.v : &maps.k, full, c * kChunk, tok,

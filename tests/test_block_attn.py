@@ -540,3 +540,42 @@ def test_backward_refuses(dsa, over, code):
 def test_workspace_size_of_invalid_shapes(dsa, args):
     assert dsa.dsa_block_attn_workspace_size(*args) == 0
     assert dsa.dsa_block_attn_bwd_workspace_size(*args) == 0
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("S,G", [(1, 4), (1, 1), (20, 16)])
+@pytest.mark.parametrize("n", [1, 3, 5])
+def test_ragged_blocks_whatever_shared_memory_holds(dsa, D, S, G, n):
+    """Blocks of 16 in a step of 64: the rows of keys that the last step does
+    not load are numbers, so NaN that an earlier kernel left in shared memory
+    changes no bit.  No key comes after a row's position here: those would be
+    hidden one by one."""
+    B, Hk, T, block = 300, 1, 160, 16
+    q, k, v, _, _ = problem(S, B, Hk * G, Hk, D, T, block, 0, True, 121)
+    blocks = torch.arange(n, dtype=torch.int32).expand(B, S, n).contiguous()
+    qp = torch.full((B,), 100, dtype=torch.int32)
+    dq, dk, dv, dbl, dqp = cu(q, k, v, blocks, qp)
+    # at least 304 tiles of three blocks: every SM's shared memory, and keys in
+    # the stages where this call's go
+    if G * S <= 32:
+        shape, rows, first = (1, 640, 32, D), 192, 191
+    else:
+        shape, rows, first = (640, 1, 64, D), 640, 0
+    fq = torch.ones(shape, dtype=BF, device="cuda")
+    fp = torch.full((shape[1],), first, dtype=torch.int32, device="cuda")
+    fill = {name: torch.full((rows, shape[1], 1, D), x, dtype=BF, device="cuda")
+            for name, x in (("zero", 0.0), ("nan", math.nan))}
+    run = lambda: dsa.dsa_block_attn_fwd(dq, dk, dv, dbl, block, 0.125,
+                                         q_pos=dqp)[:2]
+    got = {}
+    for name, x in fill.items():
+        dsa.dsa_block_attn_fwd(fq, x, x, None, 64, 0.1, q_pos=fp,
+                               local_blocks=3)
+        got[name] = run()
+    assert torch.equal(got["zero"][0], got["nan"][0])
+    assert torch.equal(got["zero"][1], got["nan"][1])
+    sub = slice(0, 2)
+    r = block_attn_ref(q[:, sub], k[:, sub], v[:, sub], blocks[sub], block, 0,
+                       0.125, qp)
+    check_attn(r, got["nan"][0][:, sub], got["nan"][1][:, sub])
