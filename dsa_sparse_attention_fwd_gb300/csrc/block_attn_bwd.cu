@@ -1,10 +1,20 @@
 // Backward of the block attention.  With P = exp(x - lse) from the saved
 // log-sums and delta = do.o (a sum over D):
 //     dv_j = sum P do,   dP = do.v_j,   dS = P (dP - delta),
-//     dq = scale sum dS k_j,   dk_j = scale sum dS q
-// (delta as sum P dP where a row has few keys, see few_keys_delta);
+//     dq = scale sum dS k_j,   dk_j = scale sum dS q;
 // dk and dv are sums over the heads of a group and over the rows that hold
 // the key's block.
+//   delta is read from the rounded o, e off, and every dS with it by P e.  Where
+// a key d has nearly all of a row's weight, dS_d is a small difference of which
+// e may be most (a sink that holds 0.99 of the weights: dq 7.5% off, 39% in
+// those rows).  sum dS = 0 by definition, so the sum that the dq pass finds is
+// e: it corrects delta for dk and dv, and in dq it comes off dS_d where d has
+// more than half of the weight.  What stays there is (1 - P_d) e, as small
+// against the true dS as e is against dP; dS_d's own rounding, which the sum
+// does not see, comes off with it.  dq and dk are then 0.23 to 0.25% off at any
+// weight of the sink (one rounding of the exact ones: 0.17%), for 11 us of the
+// training step below.  Rows without such a key at a sequence's first positions
+// get delta from their keys (few_keys_delta).
 //
 // Two passes, each with its sums in tensor memory, so nothing is added
 // atomically and the results do not change from run to run:
@@ -137,8 +147,8 @@ int make_plan(const BlockAttn &p, char *ws, BwdPlan *pl) {
 // ---- delta --------------------------------------------------------------------
 
 // stat = (lse log2 e, do.o); D / 8 lanes a row, 16 bytes each, kDeltaRows
-// rows in flight.  Bound by memory: 6.5 TB/s at 4096 x 64 rows of 128 (21 us).  A row without keys gets +inf, so its weights exp2(x - inf)
-// are zero.
+// rows in flight.  Bound by memory: 6.5 TB/s at 4096 x 64 rows of 128 (21 us).
+// A row without keys gets +inf, so its weights exp2(x - inf) are zero.
 constexpr int kDeltaRows = 4;
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -184,12 +194,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // delta of a row at one of a sequence's first kFewKeys positions, by one warp,
-// as sum P dP instead of do.o: o has been rounded, and where a row's weight is
-// all on one key, dS = P (dP - delta) is a small difference of what the
-// rounding is 2^-9 of (dq and dk of sequences below 8 tokens: 0.52% off at
-// worst, 0.28% so, for 4 us in the launch of bwd_mark_kernel).  Rows with more
-// keys are seldom so one-sided, and the sum over their keys is what the two
-// passes take their time for.
+// as sum P dP instead of do.o, whose o has been rounded.  Rows of two or three
+// keys have a dS that is small against dP more often than others do: dq of
+// sequences below 8 tokens is 0.32% off at worst without, 0.24% with it, for
+// 4 us in the launch of bwd_mark_kernel.  The rule is the position, which needs
+// no look at the selection; later rows with as few keys stay at 0.32%.
 constexpr int kFewKeys = 32;
 __device__ __forceinline__ void few_keys_delta(const BlockAttn &p,
                                                const __nv_bfloat16 *go,
@@ -826,9 +835,14 @@ struct DqSmem {
   static constexpr int kCh = D / 64;
   static constexpr int kKey = kCh * kDqKeys * 128;  // K or V of a stage
   static constexpr int kOffBar = 0;
-  // q_full acc_full sdp_full[2] ds_full[2] kv_full[] kv_empty[] q_here
-  static constexpr int kOffMisc = kOffBar + (7 + 2 * kDqStages) * 8;
-  static constexpr int kOffS = 1024;  // stages: K, V
+  // q_full acc_full sdp_full[2] ds_full[2] kv_full[] kv_empty[] q_here met
+  static constexpr int kOffMisc = kOffBar + (8 + 2 * kDqStages) * 8;
+  // a row's sum of dS by each warpgroup, its key with most weight and that
+  // key's rounding
+  static constexpr int kOffLeft = 512;
+  static constexpr int kOffTop = kOffLeft + 2 * kDqRows * 4;
+  static constexpr int kOffS = 3072;  // stages: K, V
+  static_assert(kOffMisc + 32 <= kOffLeft && kOffTop + kDqRows * 8 <= kOffS);
   static int bytes(int stages, int nblk, int cap) {
     return kOffS + stages * 2 * kKey + nblk * 4 + ((cap * 2 + 15) & ~15) +
            1024;
@@ -837,9 +851,37 @@ struct DqSmem {
 
 struct DqPlan {
   int qt, tiles, cap, stages;
-  const float2 *stat;
+  float2 *stat;
   __nv_bfloat16 *gq;
 };
+
+// The one of a thread's 32 keys that has more than half of its row's weight (its
+// column, or -1), and what rounding this key's dS to bf16 adds to it.  Out of
+// line: a row has one such key at most.
+__device__ __noinline__ int top_key(uint32_t ts, uint32_t mask, float c2,
+                                    float2 sd, float &fix) {
+  uint32_t u[32];
+  __syncwarp();
+  tmem_ld32(ts, u);
+  tmem_ld_wait();
+  reg_fence32(u);
+  int at = -1;
+  float top = 0.f;
+#pragma unroll
+  for (int x = 0; x < 32; ++x) {
+    const float e = ex2(fmaf(__uint_as_float(u[x]), c2, -sd.x));
+    if ((mask >> x & 1u) && e > 0.5f) at = x, top = e;
+  }
+  tmem_ld32(ts + 64, u);
+  tmem_ld_wait();
+  reg_fence32(u);
+  float dp = 0.f;
+#pragma unroll
+  for (int x = 0; x < 32; ++x) dp = x == at ? __uint_as_float(u[x]) : dp;
+  const float w = top * (dp - sd.y);
+  fix = __bfloat162float(__float2bfloat16(w)) - w;
+  return at;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
@@ -867,7 +909,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
   };
   const uint32_t bars = base + L::kOffBar;
   const uint32_t q_full = bars, acc_full = bars + 8;
-  const uint32_t q_here = bars + 48 + 16 * kDqStages;
+  const uint32_t q_here = bars + 48 + 16 * kDqStages, met = q_here + 8;
   auto sdp_full = [&](int i) { return bars + 16 + 8 * i; };
   auto ds_full = [&](int i) { return bars + 32 + 8 * i; };
   auto kv_full = [&](int i) { return bars + 48 + 8 * i; };
@@ -875,6 +917,8 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
+  float *lefts = reinterpret_cast<float *>(smem + L::kOffLeft);
+  int2 *tops = reinterpret_cast<int2 *>(smem + L::kOffTop);
   uint32_t *words = reinterpret_cast<uint32_t *>(smem + L::kOffS +
                                                  pl.stages * 2 * L::kKey);
   uint16_t *list = reinterpret_cast<uint16_t *>(words + p.nblk);
@@ -893,6 +937,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
   if (tid == 0) {
     mbar_init(q_full, 8);
     mbar_init(q_here, 1);
+    mbar_init(met, 8);
     mbar_init(acc_full, 1);
     for (int i = 0; i < kDqStages; ++i) {
       mbar_init(kv_full(i), 1);
@@ -919,6 +964,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
     tmem_relinquish();
   }
   const FirstMark first = first_mark(p, b, s0, nq, hk, tid);
+  if (tid < kDqRows) tops[tid] = make_int2(-1, 0);
   for (int n = tid; n < p.nblk; n += kBwdThreads) words[n] = 0u;
   tc_fence_before();
   __syncthreads();
@@ -1045,6 +1091,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
+    float2 left = make_float2(0.f, 0.f);  // this thread's sum of dS
     for (int i = 0; i < n; ++i) {
       uint32_t masks[2];
       bool diag[2];
@@ -1075,6 +1122,7 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
           for (int x = 0; x < 32; ++x)
             u[x] = mask >> x & 1u ? u[x] : 0xff800000u;
         }
+        float2 weight = make_float2(0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           // a row holds 16 neighbouring keys or none, or they are hidden
@@ -1090,6 +1138,18 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
                                         __uint_as_float(g[x + 1])),
                             make_float2(-sd.y, -sd.y)));
           dk[x >> 1] = pack_bf16x2(w.x, w.y);
+          weight = __fadd2_rn(weight, e);
+          left = __fadd2_rn(left, w);
+        }
+        if (__any_sync(0xffffffffu, weight.x + weight.y > 0.5f)) {
+          float fix;
+          const int x = top_key(ts, mask, c2, sd, fix);
+          if (x >= 0) {
+            const int col = wg * 32 + x, ux = i * upt + col / unit;
+            tops[row] = make_int2(
+                list[ux / per] * p.blk + ux % per * unit + col % unit,
+                __float_as_int(fix));
+          }
         }
       }
       __syncwarp();
@@ -1099,12 +1159,24 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
       __syncwarp();
       if (lane == 0) mbar_arrive(ds_full(i % NB));
     }
-    if (n > 0) {
-      if (!__all_sync(0xffffffffu,
-                      wait_bar_rest(acc_full, 0, abort_flag, p.status)))
-        goto done;
-      tc_fence_after();
-    }
+    // The sum of a row's dS is what delta is off by: delta is put right for the
+    // dk, dv pass, and here the key with most of the weight takes it.
+    lefts[wg * kDqRows + row] = left.x + left.y;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(met);
+    if (!__all_sync(0xffffffffu,
+                    (n == 0 || wait_bar_rest(acc_full, 0, abort_flag,
+                                             p.status)) &&
+                        wait_bar_rest(met, 0, abort_flag, p.status)))
+      goto done;
+    tc_fence_after();
+    const float off = lefts[row] + lefts[kDqRows + row];
+    const int2 top = tops[row];
+    const float back = off + __int_as_float(top.y);
+    if (wg == 0 && live)
+      reinterpret_cast<float *>(pl.stat + at)[1] = sd.y + off;
+    const uint4 *kt = reinterpret_cast<const uint4 *>(
+        p.k + b * p.k_sb + max(top.x, 0) * p.k_st + hk * p.k_sh + wg * (D / 2));
     // each warpgroup writes half of the columns; the first stage is free
     uint32_t ow[D / 4];
 #pragma unroll
@@ -1115,6 +1187,20 @@ __global__ void __launch_bounds__(kBwdThreads, bwd_ctas(D))
         tmem_ld32(tmem + kTmQ + lane_off + wg * (D / 2) + c * 32, u);
         tmem_ld_wait();
         reg_fence32(u);
+      }
+      if (top.x >= 0) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
+          const uint4 v = __ldg(kt + (c * 32 + x) / 8);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            u[x + y] = __float_as_uint(
+                fmaf(-back,
+                     __uint_as_float(y & 1 ? w[y >> 1] & 0xffff0000u
+                                           : w[y >> 1] << 16),
+                     __uint_as_float(u[x + y])));
+        }
       }
 #pragma unroll
       for (int x = 0; x < 16; ++x)
@@ -1169,21 +1255,7 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
   KvMaps maps;
   const Problem qp{p.q, nullptr, nullptr, nullptr, p.S, p.B, p.H, p.D, 1, 1};
   const Problem gp{go, nullptr, nullptr, nullptr, p.S, p.B, p.H, p.D, 1, 1};
-  int rc = encode_q_heads(&tm_q, qp, pl.qt, p.G);
-  if (rc == DSA_OK) rc = encode_q_heads(&tm_go, gp, pl.qt, p.G);
-  if (rc == DSA_OK) rc = encode_kv_maps(p, kKeyTile, &maps);
-  if (rc != DSA_OK) return rc;
-  auto dkv = block_attn_dkv_kernel<D>;
-  if (!ok(cudaFuncSetAttribute(dkv,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               KvSmem<D>::kBytes)))
-    return DSA_ERR_CUDA;
-  dkv<<<(unsigned)pl.items * pl.rep, kBwdThreads, KvSmem<D>::kBytes, st>>>(
-      tm_q, tm_go, maps, p, pl, bf(gk), bf(gv));
-  bwd_join_kernel<D><<<(unsigned)kts * pl.rep * kJoinParts, 256, 0, st>>>(
-      p, pl, bf(gk), bf(gv));
-  if (!ok(cudaGetLastError())) return DSA_ERR_CUDA;
-
+  // dq first: it puts delta right for dk, dv
   DqPlan dp{};
   dp.qt = tile_queries(p.G, kDqRows);
   if (dp.qt > p.S) dp.qt = p.S;
@@ -1198,7 +1270,7 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
                               kMaxSmem / bwd_ctas(D) - 1024)
     --dp.stages;
   const int smem = DqSmem<D>::bytes(dp.stages, p.nblk, dp.cap);
-  rc = encode_q_heads(&tm_q, qp, dp.qt, p.G);
+  int rc = encode_q_heads(&tm_q, qp, dp.qt, p.G);
   if (rc == DSA_OK) rc = encode_q_heads(&tm_go, gp, dp.qt, p.G);
   if (rc == DSA_OK) rc = encode_kv_maps(p, p.blk < kDqKeys ? p.blk : kDqKeys,
                                         &maps);
@@ -1209,6 +1281,21 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
     return DSA_ERR_CUDA;
   const long long grid = (long long)dp.tiles * p.B * p.Hk;
   dq<<<(unsigned)grid, kBwdThreads, smem, st>>>(tm_q, tm_go, maps, p, dp);
+  if (!ok(cudaGetLastError())) return DSA_ERR_CUDA;
+
+  rc = encode_q_heads(&tm_q, qp, pl.qt, p.G);
+  if (rc == DSA_OK) rc = encode_q_heads(&tm_go, gp, pl.qt, p.G);
+  if (rc == DSA_OK) rc = encode_kv_maps(p, kKeyTile, &maps);
+  if (rc != DSA_OK) return rc;
+  auto dkv = block_attn_dkv_kernel<D>;
+  if (!ok(cudaFuncSetAttribute(dkv,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               KvSmem<D>::kBytes)))
+    return DSA_ERR_CUDA;
+  dkv<<<(unsigned)pl.items * pl.rep, kBwdThreads, KvSmem<D>::kBytes, st>>>(
+      tm_q, tm_go, maps, p, pl, bf(gk), bf(gv));
+  bwd_join_kernel<D><<<(unsigned)kts * pl.rep * kJoinParts, 256, 0, st>>>(
+      p, pl, bf(gk), bf(gv));
   return ok(cudaGetLastError()) ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -579,3 +579,64 @@ def test_ragged_blocks_whatever_shared_memory_holds(dsa, D, S, G, n):
     r = block_attn_ref(q[:, sub], k[:, sub], v[:, sub], blocks[sub], block, 0,
                        0.125, qp)
     check_attn(r, got["nan"][0][:, sub], got["nan"][1][:, sub])
+
+
+@gpu
+@pytest.mark.parametrize("D,G,block", [(64, 1, 16), (64, 4, 64), (128, 4, 16),
+                                       (128, 12, 32)])
+def test_gradients_of_one_sided_rows(dsa, D, G, block):
+    """A sink key that every row holds, with most of the weight of many: dS is
+    a small difference there, and the rounding of o in delta does not enter it
+    as a whole.  With d the key of more than half of the weight (if any) and
+    delta0 = do.o from the rounded o, off by e0 <= 2^-8 sum |do o|:
+      dS_j: its rounding, 2^-8 of it; P is off by a factor 1 + 2^-18 (1 + X)
+    (the exponential, and a score's and the log-sum's chains of nine fp32
+    sums), which also reaches delta = sum P (dP - delta0) + delta0; dP and
+    delta0 by 2^-20 of their magnitudes;
+      dq, where d exists: dS_d is minus the others' sum, so e0 reaches the
+    others only, P_j e0 (|k_j| + |k_d|); else P_j e0 |k_j|;
+      the results' rounding."""
+    S, B, Hk, T, first = 96, 1, 2, 140, 44
+    q, k, v, go, blocks = problem(S, B, Hk * G, Hk, D, T, block, 3, False, 131)
+    g = torch.Generator().manual_seed(132)
+    u = torch.randn(D, generator=g)
+    u *= 9 ** 0.5 * D ** 0.25 / u.norm()
+    q = (q.float() + u).to(BF)
+    k[3] = (k[3].float() + u).to(BF)
+    blocks[..., 0] = 0
+    qp = torch.tensor([first], dtype=torch.int32)
+    scale = D ** -0.5
+    kw = dict(q_pos=qp.cuda(), local_blocks=1)
+    dq, dk, dv, dgo, dbl = cu(q, k, v, go, blocks)
+    o, lse, _ = dsa.dsa_block_attn_fwd(dq, dk, dv, dbl, block, scale, **kw)
+    grads = dsa.dsa_block_attn_bwd(dq, dk, dv, o, lse, dgo, dbl, block, scale,
+                                   **kw)[:3]
+    r = block_attn_ref(q, k, v, blocks, block, 1, scale, qp, go)
+    tq, tk = torch.zeros_like(r["tq"]), torch.zeros_like(r["tk"])
+    sided = 0
+    for s in range(S):
+        for h in range(Hk * G):
+            hk = h // G
+            js = row_keys(blocks, 0, s, hk, first + s, block, 1, T)
+            kk, vv = k[js, 0, hk].double(), v[js, 0, hk].double()
+            qq, gg = q[s, 0, h].double(), go[s, 0, h].double()
+            p = torch.softmax(scale * kk @ qq, 0)
+            dp = vv @ gg
+            gap = (dp - p @ dp).abs()
+            e0 = 2.0 ** -8 * float(gg.abs() @ (p @ vv).abs())
+            mag = vv.abs() @ gg.abs()
+            off = 2.0 ** -18 * (1 + float(r["X"][s, 0, h]))
+            e = scale * p * ((2.0 ** -8 + off) * gap + off * (p @ gap + e0)
+                             + 2.0 ** -20 * (mag + p @ mag))
+            tk[js, 0, hk] += e[:, None] * qq.abs()
+            top = int(p.argmax())
+            few = e + scale * p * e0                # e0 in every key
+            t = few @ kk.abs()
+            if p[top] > 0.5 - 2.0 ** -10:
+                few[top] = 2.0 ** -18 * scale * e0  # what cancels, in fp32
+                both = few @ (kk.abs() + kk[top].abs())
+                t = both if p[top] > 0.5 + 2.0 ** -10 else torch.maximum(t, both)
+            tq[s, 0, h] = t
+            sided += int(p[top] > 0.95)
+    assert sided > 0.2 * S * Hk * G
+    check_grads(dict(r, tq=tq, tk=tk), *grads)
