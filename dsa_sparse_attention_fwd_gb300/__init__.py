@@ -177,6 +177,30 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(stream, shape, dt, device):
+    """torch.empty() in the memory of the stream that a call runs on (the
+    current one where none is given): memory that was freed by work on the
+    current stream may still be in use by what is queued there.  A result used
+    on another stream afterwards follows torch's rules for that
+    (record_stream)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dt, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dt, device=device)
+
+
+def _zeroed_workspace(stream, size, device):
+    """A workspace whose first 256 bytes are cleared in the stream's order."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _zeroed_workspace(None, size, device)
+    if size <= 256:
+        return torch.zeros(size, dtype=torch.uint8, device=device)
+    workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    workspace[:256].zero_()
+    return workspace
+
+
 def dsa_status_string(code: int) -> str:
     return load_library().dsa_status_string(int(code)).decode()
 
@@ -266,14 +290,13 @@ def dsa_indexer_fwd(q, k, w, compress_ratio, topk, q_pos=None, in_idx=None,
     if in_idx is not None and tuple(in_idx.shape) != (B, S, topk):
         raise ValueError("topk_indices must be [B, S, topk]")
     if out_idx is None:
-        out_idx = torch.empty((B, S, topk), dtype=torch.int32, device=dev)
+        out_idx = _empty(stream, (B, S, topk), torch.int32, dev)
     if out_scores is None:
-        out_scores = torch.empty((B, S, topk), dtype=torch.float32,
-                                 device=dev)
+        out_scores = _empty(stream, (B, S, topk), torch.float32, dev)
     ws = dsa_indexer_workspace_size(S, B, H, D, S_kv, compress_ratio, topk,
                                     in_idx is not None)
     if workspace is None:
-        workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, max(ws, 256), torch.uint8, dev)
     if stage_events:
         evs = (ctypes.c_void_p * len(stage_events))(
             *[ctypes.c_void_p(e.cuda_event) for e in stage_events])
@@ -316,16 +339,15 @@ def dsa_indexer_bwd(q, k, w, compress_ratio, idx, grad_scores, q_pos=None,
             or tuple(grad_scores.shape) != (B, S, topk)):
         raise ValueError("grad_scores must be contiguous fp32 [B, S, topk]")
     dev = q.device
-    f32 = dict(dtype=torch.float32, device=dev)
     if grad_q is None:
-        grad_q = torch.empty((S, B, H, D), **f32)
+        grad_q = _empty(stream, (S, B, H, D), torch.float32, dev)
     if grad_k is None:
-        grad_k = torch.empty((S_kv, B, D), **f32)
+        grad_k = _empty(stream, (S_kv, B, D), torch.float32, dev)
     if grad_w is None:
-        grad_w = torch.empty((S, B, H), **f32)
+        grad_w = _empty(stream, (S, B, H), torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(dsa_indexer_bwd_workspace_size(),
-                                dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, dsa_indexer_bwd_workspace_size(),
+                           torch.uint8, dev)
     rc = lib.dsa_indexer_bwd(
         _ptr(q), _ptr(k), _ptr(w), S, B, H, D, S_kv, int(compress_ratio),
         int(topk), _ptr(q_pos), _ptr(idx), _ptr(grad_scores), _ptr(grad_q),
@@ -362,9 +384,8 @@ def dsa_kpool_compress(k, gate, ape, kpool, first_key=0, valid=None,
                   valid=valid)
     T, B, D = _pool_inputs(k, gate, ape, valid, kpool)
     P = max(0, (T - first_key) // kpool)
-    keys = torch.empty((max(P, 1), B, D), dtype=torch.bfloat16,
-                       device=k.device)
-    pv = torch.empty((max(P, 1), B), dtype=torch.uint8, device=k.device)
+    keys = _empty(stream, (max(P, 1), B, D), torch.bfloat16, k.device)
+    pv = _empty(stream, (max(P, 1), B), torch.uint8, k.device)
     rc = lib.dsa_kpool_compress(_ptr(k), _ptr(gate), _ptr(ape), _ptr(valid),
                                 T, B, D, int(kpool), int(first_key),
                                 _ptr(keys), _ptr(pv), _stream(stream))
@@ -381,8 +402,8 @@ def dsa_expand_selection(pools, kpool, first_key=0, out=None, stream=None):
         raise ValueError("pools must be contiguous int32")
     select_k = pools.shape[-1]
     if out is None:
-        out = torch.empty(tuple(pools.shape[:-1]) + (select_k * kpool,),
-                          dtype=torch.int32, device=pools.device)
+        out = _empty(stream, tuple(pools.shape[:-1]) + (select_k * kpool,),
+                     torch.int32, pools.device)
     rows = pools.numel() // select_k
     rc = lib.dsa_expand_selection(_ptr(pools), rows, select_k, int(kpool),
                                   int(first_key), _ptr(out), _stream(stream))
@@ -422,18 +443,17 @@ def dsa_indexer_fwd_pooled(q, k, gate, ape, w, kpool, first_key, index_topk,
     sk = index_topk // kpool
     dev = q.device
     if out_tokens is None:
-        out_tokens = torch.empty((B, S, index_topk), dtype=torch.int32,
-                                 device=dev)
+        out_tokens = _empty(stream, (B, S, index_topk), torch.int32, dev)
     if out_pools is None:
-        out_pools = torch.empty((B, S, sk), dtype=torch.int32, device=dev)
+        out_pools = _empty(stream, (B, S, sk), torch.int32, dev)
     if out_scores is None:
-        out_scores = torch.empty((B, S, sk), dtype=torch.float32, device=dev)
+        out_scores = _empty(stream, (B, S, sk), torch.float32, dev)
     if workspace is None:
         n = dsa_indexer_pooled_workspace_size(S, B, H, D, T, kpool,
                                               first_key, index_topk)
         if n == 0:
             raise DsaError(2, "dsa_indexer_pooled_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, n, torch.uint8, dev)
     rc = lib.dsa_indexer_fwd_pooled(
         _ptr(q), _ptr(k), _ptr(gate), _ptr(ape), _ptr(valid), _ptr(w), S, B,
         H, D, T, int(kpool), int(first_key), int(index_topk), _ptr(q_pos),
@@ -467,12 +487,12 @@ def dsa_sparse_mla_fwd(q, c, idx, scale, out_o=None, out_lse=None,
     topk = idx.shape[-1]
     dev = q.device
     if out_o is None:
-        out_o = torch.empty((S, B, H, Dc), dtype=torch.float32, device=dev)
+        out_o = _empty(stream, (S, B, H, Dc), torch.float32, dev)
     if out_lse is None:
-        out_lse = torch.empty((S, B, H), dtype=torch.float32, device=dev)
+        out_lse = _empty(stream, (S, B, H), torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(dsa_sparse_mla_workspace_size(),
-                                dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, dsa_sparse_mla_workspace_size(),
+                           torch.uint8, dev)
     rc = lib.dsa_sparse_mla_fwd(_ptr(q), _ptr(c), _ptr(idx), S, B, H, Dc, T,
                                 topk, float(scale), _ptr(out_o),
                                 _ptr(out_lse), _ptr(workspace),
@@ -633,12 +653,12 @@ def dsa_norm_rope_fwd(q, k, inv_freq, positions=None, wq=None, wk=None,
         raise TypeError(f"q must be bf16, fp16 or fp32, got {dt}")
     S, B, H, Hk, D, R = _rope_inputs(q, k, inv_freq, positions, wq, wk, dt)
     if out_q is None:
-        out_q = torch.empty((S, B, H, D), dtype=dt, device=q.device)
+        out_q = _empty(stream, (S, B, H, D), dt, q.device)
     else:
         _dense("out_q", out_q, dt, (S, B, H, D))
     if k is not None:
         if out_k is None:
-            out_k = torch.empty((S, B, Hk, D), dtype=dt, device=q.device)
+            out_k = _empty(stream, (S, B, Hk, D), dt, q.device)
         else:
             _dense("out_k", out_k, dt, (S, B, Hk, D))
     rc = lib.dsa_norm_rope_fwd(
@@ -675,19 +695,20 @@ def dsa_norm_rope_bwd(q, k, grad_out_q, grad_out_k, inv_freq, positions=None,
     S, B, H, Hk, D, R = _rope_inputs(q, k, inv_freq, positions, wq, wk, dt)
     _dense("grad_out_q", grad_out_q, dt, (S, B, H, D))
     gk = gwq = gwk = None
-    gq = torch.empty((S, B, H, D), dtype=dt, device=q.device)
+    gq = _empty(stream, (S, B, H, D), dt, q.device)
     if k is not None:
         if grad_out_k is None:
             raise ValueError("grad_out_k is needed with k")
         _dense("grad_out_k", grad_out_k, dt, (S, B, Hk, D))
-        gk = torch.empty((S, B, Hk, D), dtype=dt, device=q.device)
+        gk = _empty(stream, (S, B, Hk, D), dt, q.device)
     if wq is not None:
-        gwq = torch.empty(D, dtype=torch.float32, device=q.device)
+        gwq = _empty(stream, D, torch.float32, q.device)
     if wk is not None and k is not None:
-        gwk = torch.empty(D, dtype=torch.float32, device=q.device)
+        gwk = _empty(stream, D, torch.float32, q.device)
     if workspace is None:
-        workspace = torch.empty(max(dsa_norm_rope_bwd_workspace_size(D), 256),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream,
+                           max(dsa_norm_rope_bwd_workspace_size(D), 256),
+                           torch.uint8, q.device)
     rc = lib.dsa_norm_rope_bwd(
         _addr(q), _strides(q), _addr(k), None if k is None else _strides(k),
         _addr(grad_out_q), None if k is None else _addr(grad_out_k),
@@ -740,11 +761,11 @@ def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
         raise ValueError("the cache's heads or head size differ from k's")
     if q is not None:
         if out_q is None:
-            out_q = torch.empty((S, B, H, D), dtype=bf, device=q.device)
+            out_q = _empty(stream, (S, B, H, D), bf, q.device)
         else:
             _dense("out_q", out_q, bf, (S, B, H, D))
     if workspace is None:
-        workspace = torch.zeros(256, dtype=torch.uint8, device=k.device)
+        workspace = _zeroed_workspace(stream, 256, k.device)
     rc = lib.dsa_paged_append(
         _addr(k), _strides(k), _addr(v), _strides(v), _addr(q),
         None if q is None else _strides(q), S, B, H, Hk, D, _addr(k_cache),
@@ -787,23 +808,22 @@ def _selection(blocks, B, S, Hk, q_pos):
     return (1 if blocks.dim() == 3 else Hk), blocks.shape[-1]
 
 
-def _block_attn_out(q, shape, out_o, out_lse, workspace):
+def _block_attn_out(q, shape, out_o, out_lse, workspace, stream):
     """The outputs and the workspace of a forward, made where not given."""
     S, B, H, D = q.shape
     if out_o is None:
-        out_o = torch.empty_like(q)
+        out_o = _empty(stream, (S, B, H, D), q.dtype, q.device)
     else:
         _dense("out_o", out_o, torch.bfloat16, (S, B, H, D))
     if out_lse is None:
-        out_lse = torch.empty((S, B, H), dtype=torch.float32, device=q.device)
+        out_lse = _empty(stream, (S, B, H), torch.float32, q.device)
     else:
         _dense("out_lse", out_lse, torch.float32, (S, B, H))
     if workspace is None:
         size = dsa_block_attn_workspace_size(*shape)
         if size == 0:
             raise DsaError(1, "dsa_block_attn_workspace_size")
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        workspace[:256].zero_()
+        workspace = _zeroed_workspace(stream, size, q.device)
     return out_o, out_lse, workspace
 
 
@@ -831,7 +851,7 @@ def dsa_block_attn_fwd(q, k, v, blocks, block_size, scale, q_pos=None,
     sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
     out_o, out_lse, workspace = _block_attn_out(
         q, (S, B, H, Hk, D, T, block_size, topk, local_blocks), out_o,
-        out_lse, workspace)
+        out_lse, workspace, stream)
     rc = lib.dsa_block_attn_fwd(
         _addr(q), _addr(k), _addr(v), _strides2(k, v), S, B, H, Hk, D, T,
         _addr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
@@ -866,7 +886,7 @@ def dsa_block_attn_paged_fwd(q, k_cache, v_cache, page_table, blocks,
     sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
     out_o, out_lse, workspace = _block_attn_out(
         q, (S, B, H, Hk, D, max_pages * page_size, block_size, topk,
-            local_blocks), out_o, out_lse, workspace)
+            local_blocks), out_o, out_lse, workspace, stream)
     rc = lib.dsa_block_attn_paged_fwd(
         _addr(q), _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
         pages, page_size, _addr(page_table), max_pages, S, B, H, Hk, D,
@@ -902,15 +922,15 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     _last_contiguous("v", v, bf, (T, B, Hk, D))
     sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
     if grad_q is None:
-        grad_q = torch.empty_like(q)
+        grad_q = _empty(stream, (S, B, H, D), bf, q.device)
     else:
         _dense("grad_q", grad_q, bf, (S, B, H, D))
     if grad_k is None:
-        grad_k = torch.empty((T, B, Hk, D), dtype=bf, device=q.device)
+        grad_k = _empty(stream, (T, B, Hk, D), bf, q.device)
     else:
         _dense("grad_k", grad_k, bf, (T, B, Hk, D))
     if grad_v is None:
-        grad_v = torch.empty((T, B, Hk, D), dtype=bf, device=q.device)
+        grad_v = _empty(stream, (T, B, Hk, D), bf, q.device)
     else:
         _dense("grad_v", grad_v, bf, (T, B, Hk, D))
     if workspace is None:
@@ -918,8 +938,7 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
                                               topk, local_blocks)
         if n == 0:
             raise DsaError(1, "dsa_block_attn_bwd_workspace_size")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        workspace[:256].zero_()
+        workspace = _zeroed_workspace(stream, n, q.device)
     rc = lib.dsa_block_attn_bwd(
         _addr(q), _addr(k), _addr(v), _strides2(k, v), _addr(o), _addr(lse),
         _addr(grad_o), S, B, H, Hk, D, T, _addr(blocks), sel_heads, topk,
@@ -941,10 +960,11 @@ def dsa_indexer_logits(q, k, w, compress_ratio, q_pos=None, logits=None,
     S, B, H, D, S_kv = _check_inputs(q, k, w, q_pos, None)
     dev = q.device
     if logits is None:
-        logits = torch.empty((B, S, S_kv), dtype=torch.float32, device=dev)
+        logits = _empty(stream, (B, S, S_kv), torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(int(lib.dsa_indexer_logits_workspace_size()),
-                                dtype=torch.uint8, device=dev)
+        workspace = _empty(stream,
+                           int(lib.dsa_indexer_logits_workspace_size()),
+                           torch.uint8, dev)
     rc = lib.dsa_indexer_logits(
         _ptr(q), _ptr(k), _ptr(w), S, B, H, D, S_kv, int(compress_ratio),
         _ptr(q_pos), _ptr(logits), _ptr(workspace), workspace.numel(),
@@ -1020,16 +1040,16 @@ def dsa_indexer_fwd_varlen(q, k, w, cu_seqlens_q, cu_seqlens_k,
         raise ValueError("in_idx must be contiguous int32 [T, topk]")
     dev = q.device
     if out_idx is None:
-        out_idx = torch.empty((T, topk), dtype=torch.int32, device=dev)
+        out_idx = _empty(stream, (T, topk), torch.int32, dev)
     if out_scores is None:
-        out_scores = torch.empty((T, topk), dtype=torch.float32, device=dev)
+        out_scores = _empty(stream, (T, topk), torch.float32, dev)
     if workspace is None:
         need = dsa_indexer_varlen_workspace_size(cq, ck, H, D,
                                                  compress_ratio, topk,
                                                  in_idx is not None)
         if need == 0:
             raise DsaError(2, "dsa_indexer_varlen_workspace_size")
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _empty(stream, need, torch.uint8, dev)
     rc = lib.dsa_indexer_fwd_varlen(
         _ptr(q), _ptr(k), _ptr(w), N, _ptr(cq), _ptr(ck), H, D,
         int(compress_ratio), int(topk), _ptr(q_pos), _ptr(in_idx),
@@ -1098,9 +1118,8 @@ def dsa_indexer_fwd_host(q, k, w, compress_ratio, topk, q_pos=None,
     if need == 0:
         raise DsaError(2, "dsa_indexer_host_buffer_size")
     if device_buf is None:
-        device_buf = torch.empty(need, dtype=torch.uint8,
-                                 device=torch.device(
-                                     "cuda", torch.cuda.current_device()))
+        device_buf = _empty(stream, need, torch.uint8,
+                            torch.device("cuda", torch.cuda.current_device()))
     rc = lib.dsa_indexer_fwd_host(
         _ptr(q), _ptr(k), _ptr(w), S, B, H, D, S_kv, int(compress_ratio),
         int(topk), _ptr(q_pos), _ptr(in_idx), _ptr(out_idx),
