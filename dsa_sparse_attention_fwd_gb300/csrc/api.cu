@@ -29,9 +29,28 @@ struct DeviceInfo {
 std::mutex g_dev_mu;
 DeviceInfo g_dev[64];
 
+// Tensor maps are encoded by the driver, which wants a current context.  A
+// thread that has made no CUDA call has none: it gets its device's.
+bool bind_context(int dev) {
+  static PFN_cuCtxGetCurrent_v4000 fn = []() {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &p, 4000,
+                                         cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
+  }();
+  CUcontext ctx = nullptr;
+  if (!fn || fn(&ctx) != CUDA_SUCCESS) return false;
+  return ctx || cudaSetDevice(dev) == cudaSuccess;
+}
+
 int current_device_info(DeviceInfo *out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSA_ERR_CUDA;
+  if (!bind_context(dev)) return DSA_ERR_CUDA;
   if (dev < 0 || dev >= 64) return DSA_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DeviceInfo &d = g_dev[dev];
