@@ -99,7 +99,7 @@ struct FwdSmem {
   static constexpr int kBars = 6 + 4 * kStages;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffWords = kOffMisc + 32;
-  static int bytes(int nblk, int cap) {
+  static constexpr int bytes(int nblk, int cap) {
     return kOffWords + nblk * 4 + ((cap * 2 + 15) & ~15) + 1024;
   }
 };
@@ -634,9 +634,10 @@ int launch_fwd(const CUtensorMap &tm_q, const KvMaps &maps,
                const BlockAttn &p, const FwdPlan &pl, cudaStream_t st) {
   auto kern = block_attn_fwd_kernel<D, FEW>;
   const int smem = FwdSmem<D, FEW>::bytes(p.nblk, pl.cap);
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           smem) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  constexpr int kMost = FwdSmem<D, FEW>::bytes(DSA_BLOCK_ATTN_MAX_BLOCKS,
+                                               DSA_BLOCK_ATTN_MAX_BLOCKS);
+  static_assert(kMost <= kMaxSmem);
+  if (allow_smem(kern, kMost) != cudaSuccess) return DSA_ERR_CUDA;
   const long long grid = (long long)pl.tiles * p.B * p.Hk * pl.splits;
   if (grid > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
   kern<<<(unsigned)grid, kFwdThreads, smem, st>>>(tm_q, maps, p, pl);

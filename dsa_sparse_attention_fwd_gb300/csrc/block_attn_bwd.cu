@@ -1221,8 +1221,6 @@ done:
   }
 }
 
-constexpr int kMaxSmem = 232448;  // 227 KB opt-in per block
-
 template <int D>
 int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
                const float *lse, const void *go, void *gq, void *gk, void *gv,
@@ -1241,9 +1239,7 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
       static_cast<const __nv_bfloat16 *>(go), lse, rows, pl.stat);
   const unsigned few = p.B * p.H * (kFewKeys / 4);
   const int mark_smem = p.nblk * 4 + pl.cap * 2;
-  if (!ok(cudaFuncSetAttribute(bwd_mark_kernel,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               mark_smem)))
+  if (!ok(allow_smem(bwd_mark_kernel, DSA_BLOCK_ATTN_MAX_BLOCKS * 6)))
     return DSA_ERR_CUDA;
   bwd_mark_kernel<<<few + (unsigned)qts, 128, mark_smem, st>>>(
       p, static_cast<const __nv_bfloat16 *>(go), pl, few);
@@ -1276,9 +1272,7 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
                                         &maps);
   if (rc != DSA_OK) return rc;
   auto dq = block_attn_dq_kernel<D>;
-  if (!ok(cudaFuncSetAttribute(
-          dq, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)))
-    return DSA_ERR_CUDA;
+  if (!ok(allow_smem(dq, kMaxSmem))) return DSA_ERR_CUDA;
   const long long grid = (long long)dp.tiles * p.B * p.Hk;
   dq<<<(unsigned)grid, kBwdThreads, smem, st>>>(tm_q, tm_go, maps, p, dp);
   if (!ok(cudaGetLastError())) return DSA_ERR_CUDA;
@@ -1288,10 +1282,7 @@ int launch_bwd(const BlockAttn &p, const BwdPlan &pl, const void *o,
   if (rc == DSA_OK) rc = encode_kv_maps(p, kKeyTile, &maps);
   if (rc != DSA_OK) return rc;
   auto dkv = block_attn_dkv_kernel<D>;
-  if (!ok(cudaFuncSetAttribute(dkv,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               KvSmem<D>::kBytes)))
-    return DSA_ERR_CUDA;
+  if (!ok(allow_smem(dkv, KvSmem<D>::kBytes))) return DSA_ERR_CUDA;
   dkv<<<(unsigned)pl.items * pl.rep, kBwdThreads, KvSmem<D>::kBytes, st>>>(
       tm_q, tm_go, maps, p, pl, bf(gk), bf(gv));
   bwd_join_kernel<D><<<(unsigned)kts * pl.rep * kJoinParts, 256, 0, st>>>(

@@ -77,6 +77,8 @@ __device__ __forceinline__ float2 relu2x2(float a, float b) {
   return __fadd2_rn(make_float2(a, b), make_float2(fabsf(a), fabsf(b)));
 }
 
+constexpr int kMaxSmem = 232448;  // 227 KB opt-in per block
+
 // Scoring kernel tile geometry.
 constexpr int kTileKeys = 128;      // MMA M: compressed keys per tile
 constexpr int kTileCols = 256;      // MMA N: (query, head) columns per tile
@@ -135,7 +137,7 @@ cudaError_t launch_fill_masked(float *logits, size_t n, cudaStream_t st);
 // for at most kIndexTopkMaxCtas CTAs) instead of [B, S, S_kv] logits.
 constexpr int kIndexTopkMaxCtas = 160;
 constexpr int kIndexTopkMaxTopk = 2048;
-constexpr size_t kIndexTopkMaxSmem = 232448;  // 227 KB opt-in per block
+constexpr size_t kIndexTopkMaxSmem = kMaxSmem;
 bool index_topk_supported(int S, int H, int D, int S_kv, int topk);
 size_t index_topk_smem_bytes(int H, int D, int topk);
 size_t index_topk_scratch_bytes(int H, int S_kv);
@@ -160,6 +162,16 @@ int encode_kv(CUtensorMap *m, const void *base, int D, int rows,
 
 // Multiprocessor count of the current device (a dsa_status code).
 int device_num_sms(int *num_sms);
+
+// Lets a kernel's launches use `bytes` of dynamic shared memory: the most that
+// any of its launches may need, never this launch's own need.  The limit belongs
+// to the kernel, so a smaller value would fail a larger launch that another
+// thread is about to make.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  return cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 
 // The forward behind the C entry points (arguments and return codes of
 // dsa_indexer_fwd_profiled); clear_status = false keeps the workspace's

@@ -991,8 +991,7 @@ cudaError_t launch_hk(const Problem &p, const CUtensorMap &tm_q,
   constexpr int TQ = kTileCols / H;
   auto kern = index_topk_kernel<H, KC, KV>;
   const size_t smem = FusedSmem<H, KC>::bytes(topk);
-  cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = allow_smem(kern, kMaxSmem);
   if (e != cudaSuccess) return e;
   const long long n_items = (long long)((p.S + TQ - 1) / TQ) * p.B;
   long long grid = n_items < num_sms ? n_items : num_sms;

@@ -1042,8 +1042,9 @@ cudaError_t launch_sel(const Problem &p, const float *logits, int topk,
                        int s0, int Sc) {
   const SelLayout l = sel_layout(p.S_kv, topk, unstaged_rows(p, Sc), NT);
   auto kern = topk_select_kernel<EPT, NT>;
-  cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.dyn);
+  // (callers leave 4 KB of a block's room beside the static SelShared)
+  static_assert(sizeof(SelShared) <= 4096);
+  cudaError_t e = allow_smem(kern, kMaxSmem - 4096);
   if (e != cudaSuccess) return e;
   const long long rows = (long long)p.B * Sc;
   // launched with programmatic stream serialization: the CTAs are queued

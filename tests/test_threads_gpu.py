@@ -8,6 +8,7 @@ import torch
 
 gpu = pytest.mark.gpu
 BF = torch.bfloat16
+CALLS = 3000
 
 
 @pytest.fixture(scope="module")
@@ -108,3 +109,40 @@ def test_a_threads_first_cuda_call(dsa, name):
     torch.cuda.synchronize()
     assert codes == [0]
     assert torch.equal(tensors[0], want)
+
+
+PAIRS = {
+    "block forward": lambda d, a, b: (block_forward(d, 64, a),
+                                      block_forward(d, 16 * 16384, b)),
+    "block backward": lambda d, a, b: (block_backward(d, 64, a),
+                                       block_backward(d, 16 * 8192, b)),
+    # the selection's rows, and the one-kernel forward's candidates
+    "selection": lambda d, a, b: (indexer(d, 1, 64, 64, 8, a),
+                                  indexer(d, 1, 64, 16384, 8, b)),
+    "one kernel": lambda d, a, b: (indexer(d, 8, 64, 8192, 8, a),
+                                   indexer(d, 8, 64, 8192, 2048, b)),
+}
+
+
+@gpu
+@pytest.mark.parametrize("pair", PAIRS)
+def test_two_threads_with_contexts_of_different_lengths(dsa, pair):
+    """Longer contexts need more shared memory, whose limit is the kernel's:
+    one thread's call must not lower it before the other's launch."""
+    lib = dsa.load_library()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls = PAIRS[pair](dsa, *streams)
+    torch.cuda.synchronize()
+    codes = [set(), set()]
+
+    def work(i):
+        for _ in range(CALLS):
+            codes[i].add(calls[i][0](lib))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}, {0}]
