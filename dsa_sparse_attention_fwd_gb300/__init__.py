@@ -246,6 +246,18 @@ def _require_cuda(where: str, **tensors):
         elif t.device != dev:
             raise ValueError(f"{where}: {name} is on {t.device}, the other "
                              f"tensors on {dev}")
+    if dev is not None:
+        _require_current(where, dev.index)
+
+
+def _require_current(where: str, index: int):
+    """Kernels run on the current device: tensors of another one are refused
+    before it reads their pointers."""
+    if index is not None and index != torch.cuda.current_device():
+        raise ValueError(f"{where}: the tensors are on cuda:{index}, the "
+                         f"current device is cuda:"
+                         f"{torch.cuda.current_device()} (call within "
+                         f"torch.cuda.device({index}))")
 
 
 def _check_inputs(q, k, w, q_pos, in_idx):
@@ -572,6 +584,8 @@ def _on_gpu(where, names, *tensors):
                 break
             dev = d
     else:
+        if dev != torch._C._cuda_getDevice():
+            _require_current(where, dev)
         return dev
     _require_cuda(where, **dict(zip(names.split(), tensors)))
 

@@ -79,3 +79,35 @@ def test_host_call_refuses_a_host_device_buffer(dsa):
     with pytest.raises(ValueError, match="CUDA tensor"):
         dsa.dsa_indexer_fwd_host(q, k, w, 1, 4,
                                  device_buf=torch.zeros(16, dtype=torch.uint8))
+
+
+class OnDevice:
+    """Stands for a CUDA tensor of the given device, as far as the device
+    checks look at one."""
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+
+@pytest.mark.parametrize("call", [
+    lambda m, t: m._require_cuda("call", q=t, k=None, w=t),
+    lambda m, t: m._on_gpu("call", "q k w", t, None, t),
+])
+def test_tensors_of_another_device_than_the_current_one(dsa, monkeypatch,
+                                                        call):
+    """Kernels are launched on the current device; tensors of another would be
+    read there."""
+    now = [0]
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0],
+                        raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    call(dsa, OnDevice(0))
+    with pytest.raises(ValueError, match="cuda:1.*current device is cuda:0"):
+        call(dsa, OnDevice(1))
+    now[0] = 1
+    call(dsa, OnDevice(1))
+    with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
+        call(dsa, OnDevice(0))
