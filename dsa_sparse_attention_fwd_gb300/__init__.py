@@ -950,9 +950,8 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     if workspace is None:
         n = dsa_block_attn_bwd_workspace_size(S, B, H, Hk, D, T, block_size,
                                               topk, local_blocks)
-        if n == 0:
-            raise DsaError(1, "dsa_block_attn_bwd_workspace_size")
-        workspace = _zeroed_workspace(stream, n, q.device)
+        # (0: invalid or not supported, and the call below says which)
+        workspace = _zeroed_workspace(stream, max(n, 256), q.device)
     rc = lib.dsa_block_attn_bwd(
         _addr(q), _addr(k), _addr(v), _strides2(k, v), _addr(o), _addr(lse),
         _addr(grad_o), S, B, H, Hk, D, T, _addr(blocks), sel_heads, topk,

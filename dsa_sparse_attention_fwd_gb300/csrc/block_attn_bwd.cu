@@ -64,6 +64,8 @@ constexpr int kRowTile = 64;   // rows of its query tiles
 constexpr int kKvStages = 4;
 constexpr int kMinChunk = 16;     // query tiles of a chunk at least
 constexpr int kChunkUnits = 640;  // 4 chunks on each of 160 SMs
+constexpr int kJoinParts = 16;    // CTAs that join a key tile's chunks
+constexpr int kFewKeys = 32;      // see few_keys_delta
 
 // The transposed selection and the other buffers in the workspace.
 struct BwdPlan {
@@ -106,8 +108,11 @@ int make_plan(const BlockAttn &p, char *ws, BwdPlan *pl) {
   const long long bh = (long long)p.B * p.sel_heads;
   const long long kts = bh * pl->nkt, qts = bh * pl->nqt;
   pl->entries = qts * (pl->nkt < pl->cap ? pl->nkt : pl->cap);
+  // (the last two: grids of the marking, the dk, dv pass and its join)
   if (pl->entries >= (1ll << 31) || kts >= (1ll << 20) ||
-      qts * pl->cap >= (1ll << 40))
+      qts * pl->cap >= (1ll << 40) ||
+      (long long)p.B * p.H * (kFewKeys / 4) + qts >= (1ll << 31) ||
+      (kts + kChunkUnits) * pl->rep * kJoinParts >= (1ll << 31))
     return DSA_ERR_UNSUPPORTED;
   pl->items = (int)(kts + kChunkUnits / pl->rep + 1);
   // only lists longer than a chunk have slots: at most twice entries / chunk
@@ -199,7 +204,6 @@ __global__ void __launch_bounds__(256)
 // sequences below 8 tokens is 0.32% off at worst without, 0.24% with it, for
 // 4 us in the launch of bwd_mark_kernel.  The rule is the position, which needs
 // no look at the selection; later rows with as few keys stay at 0.32%.
-constexpr int kFewKeys = 32;
 __device__ __forceinline__ void few_keys_delta(const BlockAttn &p,
                                                const __nv_bfloat16 *go,
                                                float2 *stat, int b, int h,
@@ -791,7 +795,6 @@ done:
 // Adds the chunks of the key tiles that have several; kJoinParts CTAs a tile.
 // Bound by memory and, where one tile has most of the chunks (a block that
 // every query holds), by that tile's CTAs: 20 us for 90 MB.
-constexpr int kJoinParts = 16;
 template <int D>
 __global__ void __launch_bounds__(256)
     bwd_join_kernel(const BlockAttn p, const BwdPlan pl, __nv_bfloat16 *gk,
@@ -1301,7 +1304,12 @@ size_t dsa_block_attn_bwd_workspace_size(int S, int B, int H, int Hk, int D,
   if (dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
                                     local_blocks) == 0)
     return 0;
-  // the larger of the two ways to select: shared by all heads, or not
+  if (H / Hk > DSA_BLOCK_ATTN_MAX_GROUP || topk + local_blocks <= 0 ||
+      (block_size != 16 && block_size != 32 && block_size != 64 &&
+       block_size != 128))
+    return 0;
+  // the larger of the two ways to select, shared by all heads or not, that are
+  // supported
   size_t most = 0;
   for (int heads : {1, Hk}) {
     dsa::BlockAttn p{};
@@ -1309,13 +1317,9 @@ size_t dsa_block_attn_bwd_workspace_size(int S, int B, int H, int Hk, int D,
     p.sel_heads = heads, p.topk = topk, p.blk = block_size;
     p.local = local_blocks;
     p.nblk = (int)(((long long)T + block_size - 1) / block_size);
-    if (p.G > DSA_BLOCK_ATTN_MAX_GROUP || topk + local_blocks <= 0 ||
-        (block_size != 16 && block_size != 32 && block_size != 64 &&
-         block_size != 128))
-      return 0;
     dsa::BwdPlan pl;
-    if (dsa::make_plan(p, nullptr, &pl) != DSA_OK) return 0;
-    if (pl.bytes > most) most = pl.bytes;
+    if (dsa::make_plan(p, nullptr, &pl) == DSA_OK && pl.bytes > most)
+      most = pl.bytes;
   }
   return most;
 }
@@ -1345,17 +1349,17 @@ int dsa_block_attn_bwd(const void *q, const void *k, const void *v,
       !aligned_to(grad_q, 16) || !aligned_to(grad_k, 16) ||
       !aligned_to(grad_v, 16))
     return DSA_ERR_INVALID_ARG;
+  // this selection's limits, then the room that any may take
+  dsa::BwdPlan pl;
+  rc = dsa::make_plan(p, static_cast<char *>(workspace), &pl);
+  if (rc != DSA_OK) return rc;
   const size_t need = dsa_block_attn_bwd_workspace_size(
       S, B, H, Hk, D, T, block_size, topk, local_blocks);
-  if (need == 0) return DSA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < need) return DSA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return DSA_ERR_INVALID_ARG;
   p.status = static_cast<int *>(workspace);
   int num_sms = 0;
   rc = dsa::device_num_sms(&num_sms);
-  if (rc != DSA_OK) return rc;
-  dsa::BwdPlan pl;
-  rc = dsa::make_plan(p, static_cast<char *>(workspace), &pl);
   if (rc != DSA_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   return D == 64 ? dsa::launch_bwd<64>(p, pl, o, lse, grad_o, grad_q, grad_k,

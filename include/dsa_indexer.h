@@ -666,7 +666,14 @@ DSA_API int dsa_block_attn_paged_fwd(
  * run).  The probabilities and dS enter the products as bf16, the sums are
  * fp32.  Finite inputs only: a NaN or an infinity in q, k, v or grad_o may
  * reach gradients of neighbouring rows.
- *   workspace: dsa_block_attn_bwd_workspace_size() bytes, 256-byte aligned.
+ * Envelope: the forward's, and with n = B * sel_heads, Q = ceil(S / min(32,
+ * 64 / (H / Hk))) query tiles and K = ceil(T / 128) key tiles of a sequence:
+ * n * K < 2^20, (n * K + 640) * Hk / sel_heads < 2^27, n * Q * min(K, blocks
+ * that a query tile can hold) < 2^31, 8 * B * H + n * Q < 2^31; else
+ * DSA_ERR_UNSUPPORTED.
+ *   workspace: dsa_block_attn_bwd_workspace_size() bytes, 256-byte aligned:
+ *   enough for either kind of selection that these sizes support; 0 for
+ *   invalid sizes and where neither is supported.
  */
 DSA_API size_t dsa_block_attn_bwd_workspace_size(int S, int B, int H, int Hk,
                                                  int D, int T, int block_size,

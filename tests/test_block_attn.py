@@ -640,3 +640,39 @@ def test_gradients_of_one_sided_rows(dsa, D, G, block):
             sided += int(p[top] > 0.95)
     assert sided > 0.2 * S * Hk * G
     check_grads(dict(r, tq=tq, tk=tk), *grads)
+
+
+def test_backward_limits(dsa):
+    """The backward's own limits are those of the selection at hand, and
+    reported as what they are."""
+    lib = dsa.load_library()
+    a = dict(q=FAKE, k=FAKE, v=FAKE, strides=None, o=FAKE, lse=FAKE, go=FAKE,
+             S=4, B=64, H=8, Hk=8, D=64, T=1 << 18, blocks=FAKE, sel=1, topk=2,
+             blk=64, local=1, qp=None, scale=0.1, gq=FAKE, gk=FAKE, gv=FAKE,
+             ws=FAKE, wsb=16, st=None)
+    call = lambda **over: lib.dsa_block_attn_bwd(*dict(a, **over).values())
+    # 2^17 lists of key tiles where the heads share a selection, 2^20 where not:
+    # (a small workspace, so that what is supported is refused for that)
+    assert call() == 3
+    assert call(sel=8) == 2
+    size = dsa.dsa_block_attn_bwd_workspace_size
+    assert size(4, 64, 8, 8, 64, 1 << 18, 64, 2, 1) > 0
+    assert size(4, 1024, 8, 8, 64, 1 << 18, 64, 2, 1) == 0
+    assert call(B=1024) == 2
+    # launches of more than 2^31 CTAs
+    assert call(S=1, B=1 << 19, H=1024, Hk=64, T=128, topk=1) == 2
+    assert call(S=1, B=1 << 17, H=1024, Hk=1024, T=128, topk=1) == 2
+
+
+def test_backward_reports_unsupported_shapes(dsa, monkeypatch):
+    """A valid shape past the limits is unsupported, not invalid; refused
+    before its (host) tensors are read."""
+    monkeypatch.setattr(dsa, "_on_gpu", lambda *a: 0)
+    monkeypatch.setattr(dsa, "_raw_stream", lambda *a: None)
+    S, B, Hk, D = 1, 1 << 17, 8, 64
+    x = torch.empty((S, B, Hk, D), dtype=BF)
+    lse = torch.empty((S, B, Hk))
+    blocks = torch.empty((B, S, Hk, 1), dtype=torch.int32)
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.dsa_block_attn_bwd(x, x, x, x, lse, x, blocks, 16, 0.1)
+    assert e.value.code == 2
