@@ -758,7 +758,10 @@ def dsa_paged_append(k, v, k_cache, v_cache, page_table, positions,
     keys normed and rotated as by dsa_norm_rope_fwd; q [S, B, H, D] given
     with them is normed and rotated into out_q in the same launch.  Returns
     (out_q, workspace).  The call only sets bits in the workspace's status
-    word (256 zeroed bytes to begin with; dsa_indexer_check reads it)."""
+    word (256 zeroed bytes to begin with; dsa_indexer_check reads it); an
+    indexer call in the same workspace clears it, so an error that has not been
+    read by then is lost: give the append, or it and the block attention, a
+    workspace of their own."""
     lib = load_library()
     dev = _on_gpu("dsa_paged_append",
                   "k v k_cache v_cache page_table positions inv_freq wk q "

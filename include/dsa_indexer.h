@@ -517,9 +517,14 @@ DSA_API int dsa_sparse_mla_fwd(const void *q, const void *c,
  * dsa_block_attn_paged_fwd() and dsa_block_attn_bwd() only set bits in the
  * status word at the start of their workspace (one launch less than clearing
  * it).  Zero a new workspace's first 256 bytes once; dsa_indexer_check()
- * reads and clears the word.  The block attention keeps counts in these 256
- * bytes that are zero between calls; every entry point of this library leaves
- * them so, and calls of all kinds may share a workspace in stream order.
+ * reads and clears the word.  A bit stays through further calls of these four,
+ * so one check at the end of a step sees them all.  The calls of the sections
+ * above clear the word when they begin: in a workspace that they share with
+ * these, a bit set before them is LOST unless it has been read.  Give these
+ * calls a workspace of their own, or check before such a call.
+ * The block attention keeps counts in these 256 bytes that are zero between
+ * calls; every entry point of this library leaves them so.  That apart, calls
+ * of all kinds may share a workspace in stream order.
  */
 
 /* Element types of dsa_norm_rope_fwd() and _bwd(). */

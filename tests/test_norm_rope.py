@@ -473,3 +473,34 @@ def test_backward_without_eps(dsa, dt, D, H, Hk):
         assert_close("d" + name, dx, rx, mx, dt, 2.0 ** -17)
         err = (dw.double().cpu() - rw).abs()
         assert bool((err <= 2.0 ** -14 * mw + 1e-30).all()), "d weight " + name
+
+
+@gpu
+def test_errors_stay_in_a_workspace_of_their_own(dsa):
+    """A bad page that the append reports outlives further appends and block
+    attention in its workspace, and indexer calls in theirs; an indexer call in
+    the same workspace begins with clearing the word, as the header says."""
+    bf = torch.bfloat16
+    k = torch.ones((1, 2, 2, 64), dtype=bf, device="cuda")
+    kc = torch.zeros((4, 16, 2, 64), dtype=bf, device="cuda")
+    good = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    bad = torch.tensor([[0, 1], [4, 3]], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([[3, 5]], dtype=torch.int32, device="cuda")
+    size = dsa.dsa_block_attn_workspace_size(1, 2, 2, 2, 64, 32, 16, 0, 1)
+    ws = torch.zeros(max(size, 1 << 20), dtype=torch.uint8, device="cuda")
+    index = lambda w: dsa.dsa_indexer_fwd(
+        k, k[:, :, 0].contiguous(), torch.ones((1, 2, 2), device="cuda"), 1, 1,
+        workspace=w)
+
+    def step(index_ws):
+        dsa.dsa_paged_append(k, k, kc, kc, bad, pos, workspace=ws)
+        index(index_ws)
+        dsa.dsa_paged_append(k, k, kc, kc, good, pos, workspace=ws)
+        dsa.dsa_block_attn_paged_fwd(k, kc, kc, good, None, 16, 0.1,
+                                     q_pos=pos[0], local_blocks=1,
+                                     workspace=ws)
+    step(torch.empty_like(ws))
+    assert dsa.dsa_indexer_check(ws) == 6
+    assert dsa.dsa_indexer_check(ws) == 0
+    step(ws)
+    assert dsa.dsa_indexer_check(ws) == 0
