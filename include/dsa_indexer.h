@@ -588,7 +588,8 @@ DSA_API int dsa_norm_rope_bwd(const void *q, const int64_t *q_strides,
  * page page_table[b, p / page_size]; p < 0 appends nothing (padding; its
  * query row is still written).  A position past the table, or a page id
  * outside [0, num_pages), appends nothing and sets DSA_ERR_INDEX_RANGE.
- * Two tokens with one slot leave either of them there.
+ * Where two tokens of a call have one slot, it may be left with a mix of them:
+ * heads, keys and values of either.
  *   k, v [S, B, Hk, D], q [S, B, H, D] (nullable) bf16 with element strides
  *   (s, b, head) or NULL; k_cache, v_cache bf16, cache_strides: element
  *   strides (page, slot, head) of k_cache, then of v_cache, or NULL for
