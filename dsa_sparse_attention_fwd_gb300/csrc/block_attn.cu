@@ -26,15 +26,18 @@
 // joins the parts.
 //
 // Measured on one GB300 (bf16 peak 1909 TFLOP/s, copies 6776 GB/s):
-//   16384 tokens, 64 / 8 heads of 128, 18 blocks of 64: 877 us, 1170 TFLOP/s
-// of the unions' products (1.7 times a row's own).  The tensor pipe is busy
-// 48% of the time and issue slots 45%: a step alternates between a product
-// and a softmax of 64 columns, and two CTAs fill each other's gaps only in
-// part.
-//   3 x 777 tokens, 40 / 8 heads of 64 from pages: 300 us; unions of three
-// times a row's list, and a softmax twice as long beside a product.
-//   One token of 64 sequences, 34 blocks of 64, 4 heads of 128: 52 us, 5.4
+//   16384 tokens, 64 / 8 heads of 128, 18 blocks of 64: 877 to 895 us, 1160
+// TFLOP/s of the unions' products (1.7 times a row's own).  The tensor pipe is
+// busy 48% of the time and issue slots 45%: a step alternates between a
+// product and a softmax of 64 columns, and two CTAs fill each other's gaps only
+// in part.
+//   3 x 777 tokens, 40 / 8 heads of 64 from pages: 289 to 300 us; unions of
+// three times a row's list, and a softmax twice as long beside a product.
+//   One token of 64 sequences, 34 blocks of 64, 4 heads of 128: 53 us, 5.4
 // TB/s; of one sequence: 12 us, of which two steps are 3.
+//   A tile has 32 queries at most (a block's mask is one word), so heads with
+// keys of their own (G = 1) fill 32 of the 128 MMA rows: 4096 tokens of 16 such
+// heads take 115 us, of 64 heads in groups of four 118.
 //
 // Masked keys: a score that is not finite in a key that only other rows hold
 // spoils the row's sum, see below; a V row that no row of

@@ -4,9 +4,9 @@
 //     dq = scale sum dS k_j,   dk_j = scale sum dS q;
 // dk and dv are sums over the heads of a group and over the rows that hold
 // the key's block.
-//   delta is read from the rounded o, e off, and every dS with it by P e.  Where
-// a key d has nearly all of a row's weight, dS_d is a small difference of which
-// e may be most (a sink that holds 0.99 of the weights: dq 7.5% off, 39% in
+//   delta is read from the rounded o, e off, and every dS with it by P e.
+// Where a key d has nearly all of a row's weight, dS_d is a small difference of
+// which e may be most (a sink that holds 0.99 of the weights: dq 7.5% off, 39% in
 // those rows).  sum dS = 0 by definition, so the sum that the dq pass finds is
 // e: it corrects delta for dk and dv, and in dq it comes off dS_d where d has
 // more than half of the weight.  What stays there is (1 - P_d) e, as small
@@ -41,9 +41,9 @@
 // not held has a log-sum of +inf, so its weights are exp2(-inf) = 0.
 //
 // Measured on one GB300 (bf16 peak 1909 TFLOP/s) at 4096 tokens, 64 / 4 heads
-// of 128, 17 blocks of 64: dk, dv 322 us, 1330 TFLOP/s of the lists' products;
-// dq 187 us, 1285; delta 21, join 20, the transposed selection 33.  The tensor
-// pipe is busy 55% of the time in both: dk, dv is bound by shared memory (its
+// of 128, 17 blocks of 64: dk, dv 323 us, 1330 TFLOP/s of the lists' products;
+// dq 202 us, 1190; delta 23, join 22, the transposed selection 33.  The tensor
+// pipe is busy 55% and 50% of the time: dk, dv is bound by shared memory (its
 // products with 64 columns read 6 KB in 48 cycles, for 32 of arithmetic; 1375
 // cycles a step of 64 rows by that, 1600 to 1750 measured), dq by its chain of
 // score product, exponentials and dS a step with one CTA an SM.
@@ -276,8 +276,9 @@ __device__ __forceinline__ void few_keys_delta(const BlockAttn &p,
 // ---- the transposed selection ---------------------------------------------------
 
 // Three short launches (15, 7 and 11 us at 4096 tokens of 64 heads): the
-// order of a list must not depend on who comes first, so they cannot be one
-// without a barrier over the grid.
+// order of a list must not depend on who comes first, so the filling waits for
+// all counts.  (The scan needs the counts only and could be the work of the
+// marking's last CTA; that has not been tried.)
 // A CTA lists the blocks of one query tile and marks its key tiles.  The first
 // `few` CTAs take four positions of one head each (few_keys_delta) instead.
 __global__ void __launch_bounds__(128)
