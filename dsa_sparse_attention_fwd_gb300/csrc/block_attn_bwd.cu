@@ -845,8 +845,9 @@ struct DqSmem {
   // key's rounding
   static constexpr int kOffLeft = 512;
   static constexpr int kOffTop = kOffLeft + 2 * kDqRows * 4;
-  static constexpr int kOffS = 3072;  // stages: K, V
-  static_assert(kOffMisc + 32 <= kOffLeft && kOffTop + kDqRows * 8 <= kOffS);
+  // stages: K, V
+  static constexpr int kOffS = (kOffTop + kDqRows * 8 + 1023) / 1024 * 1024;
+  static_assert(kOffMisc + 32 <= kOffLeft);
   static int bytes(int stages, int nblk, int cap) {
     return kOffS + stages * 2 * kKey + nblk * 4 + ((cap * 2 + 15) & ~15) +
            1024;
