@@ -40,6 +40,8 @@ __all__ = [
     "dsa_norm_rope_bwd_workspace_size", "dsa_paged_append",
     "dsa_block_attn_fwd", "dsa_block_attn_paged_fwd", "dsa_block_attn_bwd",
     "dsa_block_attn_workspace_size", "dsa_block_attn_bwd_workspace_size",
+    "dsa_paged_append_q8", "dsa_paged_read_q8", "dsa_block_attn_paged_q8_fwd",
+    "dsa_block_attn_q8_workspace_size",
 ]
 
 STATUS = {
@@ -149,7 +151,8 @@ def load_library(path: str | None = None):
                                          P, P, I, I, P, I, P, P, P, F, P, I,
                                          I, I, F, P, P, Z, P]
         for name in ("dsa_block_attn_workspace_size",
-                     "dsa_block_attn_bwd_workspace_size"):
+                     "dsa_block_attn_bwd_workspace_size",
+                     "dsa_block_attn_q8_workspace_size"):
             getattr(lib, name).restype = Z
             getattr(lib, name).argtypes = [I] * 9
         lib.dsa_block_attn_fwd.restype = I
@@ -163,6 +166,17 @@ def load_library(path: str | None = None):
         lib.dsa_block_attn_bwd.argtypes = [
             P, P, P, P, P, P, P, I, I, I, I, I, I, P, I, I, I, I, P, F, P, P,
             P, P, Z, P]
+        lib.dsa_paged_append_q8.restype = I
+        lib.dsa_paged_append_q8.argtypes = [
+            P, P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, I, I, I, P, I, P,
+            P, P, P, F, P, I, I, I, F, P, P, Z, P]
+        lib.dsa_paged_read_q8.restype = I
+        lib.dsa_paged_read_q8.argtypes = [
+            P, P, P, P, P, I, I, I, P, I, I, I, I, I, P, P, P, P, P, Z, P]
+        lib.dsa_block_attn_paged_q8_fwd.restype = I
+        lib.dsa_block_attn_paged_q8_fwd.argtypes = [
+            P, P, P, P, P, P, I, I, I, P, I, I, I, I, I, I, P, I, I, I, I, P,
+            F, P, P, P, Z, P]
         _lib = lib
         return lib
 
@@ -825,7 +839,8 @@ def _selection(blocks, B, S, Hk, q_pos):
     return (1 if blocks.dim() == 3 else Hk), blocks.shape[-1]
 
 
-def _block_attn_out(q, shape, out_o, out_lse, workspace, stream):
+def _block_attn_out(q, shape, out_o, out_lse, workspace, stream,
+                    workspace_size=dsa_block_attn_workspace_size):
     """The outputs and the workspace of a forward, made where not given."""
     S, B, H, D = q.shape
     if out_o is None:
@@ -837,9 +852,9 @@ def _block_attn_out(q, shape, out_o, out_lse, workspace, stream):
     else:
         _dense("out_lse", out_lse, torch.float32, (S, B, H))
     if workspace is None:
-        size = dsa_block_attn_workspace_size(*shape)
+        size = workspace_size(*shape)
         if size == 0:
-            raise DsaError(1, "dsa_block_attn_workspace_size")
+            raise DsaError(1, workspace_size.__name__)
         workspace = _zeroed_workspace(stream, size, q.device)
     return out_o, out_lse, workspace
 
@@ -964,6 +979,170 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     if rc != 0:
         raise DsaError(rc, "dsa_block_attn_bwd")
     return grad_q, grad_k, grad_v, workspace
+
+
+def _paged_cache_q8(k_cache, v_cache, k_scale, v_scale, page_table, B):
+    """(pages, page_size, Hk, D, group) of an 8-bit cache."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, Hk, D]")
+    shape = k_cache.shape
+    _last_contiguous("k_cache", k_cache, torch.float8_e4m3fn, shape)
+    _last_contiguous("v_cache", v_cache, torch.float8_e4m3fn, shape)
+    pages, page_size, Hk, D = shape
+    if k_scale.dim() != 3:
+        raise ValueError("k_scale must be [pages, page_size / group, Hk]")
+    n = k_scale.shape[1]
+    if n <= 0 or page_size % n:
+        raise ValueError(f"k_scale: {n} scales do not divide a page of "
+                         f"{page_size} tokens")
+    _dense("k_scale", k_scale, torch.float32, (pages, n, Hk))
+    _dense("v_scale", v_scale, torch.float32, (pages, n, Hk))
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _dense("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+    return pages, page_size, Hk, D, page_size // n
+
+
+def dsa_paged_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table,
+                        start, count=None, inv_freq=None, wk=None, eps=1e-6,
+                        rot_start=0, interleaved=False, rot_scale=1.0, q=None,
+                        wq=None, out_q=None, workspace=None, stream=None):
+    """Append rows s < count[b] of k and v [S, B, Hk, D] bf16 (any strides
+    over a contiguous last dimension; count [B] int32, None: all rows) at
+    positions start[b] + s (start [B] int32; < 0: nothing is appended) to
+    paged caches held in 8 bits: k_cache, v_cache [pages, page_size, Hk, D]
+    float8_e4m3fn, k_scale, v_scale [pages, page_size / group, Hk] fp32, a
+    power of two for each group of tokens and head.  The keys are normed and
+    rotated as by dsa_norm_rope_fwd; q [S, B, H, D] given with them is normed
+    and rotated into out_q in the same launch.  An append ends its sequence: a
+    group's scale may grow with it, which rounds the group's earlier tokens
+    again.  Returns (out_q, workspace); the status word is that of
+    dsa_paged_append."""
+    lib = load_library()
+    dev = _on_gpu("dsa_paged_append_q8",
+                  "k v k_cache v_cache k_scale v_scale page_table start count "
+                  "inv_freq wk q wq out_q workspace",
+                  k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
+                  count, inv_freq, wk, q, wq, out_q, workspace)
+    bf = torch.bfloat16
+    S, B, Hk, H, D, R = _rope_inputs(k, q, inv_freq, None, wk,
+                                     None if q is None else wq, bf, "k", "q")
+    _last_contiguous("v", v, bf, (S, B, Hk, D))
+    pages, page_size, cache_heads, cache_dim, group = _paged_cache_q8(
+        k_cache, v_cache, k_scale, v_scale, page_table, B)
+    if cache_heads != Hk or cache_dim != D:
+        raise ValueError("the cache's heads or head size differ from k's")
+    _dense("start", start, torch.int32, (B,))
+    if count is not None:
+        _dense("count", count, torch.int32, (B,))
+    if q is not None:
+        if out_q is None:
+            out_q = _empty(stream, (S, B, H, D), bf, q.device)
+        else:
+            _dense("out_q", out_q, bf, (S, B, H, D))
+    if workspace is None:
+        workspace = _zeroed_workspace(stream, 256, k.device)
+    rc = lib.dsa_paged_append_q8(
+        _addr(k), _strides(k), _addr(v), _strides(v), _addr(q),
+        None if q is None else _strides(q), S, B, H, Hk, D, _addr(k_cache),
+        _addr(v_cache), _strides2(k_cache, v_cache), _addr(k_scale),
+        _addr(v_scale), group, pages, page_size, _addr(page_table),
+        page_table.shape[1], _addr(start), _addr(count), _addr(wq), _addr(wk),
+        float(eps), _addr(inv_freq), int(rot_start), R,
+        int(bool(interleaved)), float(rot_scale),
+        None if q is None else _addr(out_q), _addr(workspace),
+        workspace.numel(), _raw_stream(stream, dev))
+    if rc != 0:
+        raise DsaError(rc, "dsa_paged_append_q8")
+    return out_q, workspace
+
+
+def dsa_paged_read_q8(k_cache, v_cache, k_scale, v_scale, page_table, T,
+                      first=None, length=None, out_k=None, out_v=None,
+                      workspace=None, stream=None):
+    """Read a cache held in 8 bits back: (k, v, workspace), k and v [T, B, Hk,
+    D] bf16 with row t of sequence b token first[b] + t (first [B] int32,
+    None: t) where t < length[b] (None: T), zeros behind.  For caches as
+    dsa_paged_append_q8 writes them."""
+    lib = load_library()
+    dev = _on_gpu("dsa_paged_read_q8",
+                  "k_cache v_cache k_scale v_scale page_table first length "
+                  "out_k out_v workspace",
+                  k_cache, v_cache, k_scale, v_scale, page_table, first,
+                  length, out_k, out_v, workspace)
+    B = page_table.shape[0]
+    pages, page_size, Hk, D, group = _paged_cache_q8(
+        k_cache, v_cache, k_scale, v_scale, page_table, B)
+    for name, t in (("first", first), ("length", length)):
+        if t is not None:
+            _dense(name, t, torch.int32, (B,))
+    bf, shape = torch.bfloat16, (T, B, Hk, D)
+    if out_k is None:
+        out_k = _empty(stream, shape, bf, k_cache.device)
+    else:
+        _dense("out_k", out_k, bf, shape)
+    if out_v is None:
+        out_v = _empty(stream, shape, bf, k_cache.device)
+    else:
+        _dense("out_v", out_v, bf, shape)
+    if workspace is None:
+        workspace = _zeroed_workspace(stream, 256, k_cache.device)
+    rc = lib.dsa_paged_read_q8(
+        _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
+        _addr(k_scale), _addr(v_scale), group, pages, page_size,
+        _addr(page_table), page_table.shape[1], int(T), B, Hk, D,
+        _addr(first), _addr(length), _addr(out_k), _addr(out_v),
+        _addr(workspace), workspace.numel(), _raw_stream(stream, dev))
+    if rc != 0:
+        raise DsaError(rc, "dsa_paged_read_q8")
+    return out_k, out_v, workspace
+
+
+def dsa_block_attn_q8_workspace_size(S, B, H, Hk, D, T, block_size, topk,
+                                     local_blocks=0) -> int:
+    """Workspace bytes of dsa_block_attn_paged_q8_fwd, T = max_pages *
+    page_size (0: invalid sizes)."""
+    return int(load_library().dsa_block_attn_q8_workspace_size(
+        S, B, H, Hk, D, T, block_size, topk, local_blocks))
+
+
+def dsa_block_attn_paged_q8_fwd(q, k_cache, v_cache, k_scale, v_scale,
+                                page_table, blocks, block_size, scale,
+                                q_pos=None, local_blocks=0, out_o=None,
+                                out_lse=None, workspace=None, stream=None):
+    """dsa_block_attn_paged_fwd over caches held in 8 bits, as
+    dsa_paged_append_q8 writes them.  blocks None with local_blocks =
+    max_pages * page_size / block_size: all keys up to each row's position."""
+    lib = load_library()
+    dev = _on_gpu("dsa_block_attn_paged_q8_fwd",
+                  "q k_cache v_cache k_scale v_scale page_table blocks q_pos "
+                  "out_o out_lse workspace",
+                  q, k_cache, v_cache, k_scale, v_scale, page_table, blocks,
+                  q_pos, out_o, out_lse, workspace)
+    if q.dim() != 4:
+        raise ValueError("q [S, B, H, D] expected")
+    S, B, H, D = q.shape
+    _dense("q", q, torch.bfloat16, (S, B, H, D))
+    pages, page_size, Hk, Dk, group = _paged_cache_q8(
+        k_cache, v_cache, k_scale, v_scale, page_table, B)
+    if Dk != D:
+        raise ValueError(f"the cache's head size {Dk} differs from q's {D}")
+    max_pages = page_table.shape[1]
+    sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
+    out_o, out_lse, workspace = _block_attn_out(
+        q, (S, B, H, Hk, D, max_pages * page_size, block_size, topk,
+            local_blocks), out_o, out_lse, workspace, stream,
+        dsa_block_attn_q8_workspace_size)
+    rc = lib.dsa_block_attn_paged_q8_fwd(
+        _addr(q), _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
+        _addr(k_scale), _addr(v_scale), group, pages, page_size,
+        _addr(page_table), max_pages, S, B, H, Hk, D, _addr(blocks),
+        sel_heads, topk, int(block_size), int(local_blocks), _addr(q_pos),
+        float(scale), _addr(out_o), _addr(out_lse), _addr(workspace),
+        workspace.numel(), _raw_stream(stream, dev))
+    if rc != 0:
+        raise DsaError(rc, "dsa_block_attn_paged_q8_fwd")
+    return out_o, out_lse, workspace
 
 
 def dsa_indexer_logits(q, k, w, compress_ratio, q_pos=None, logits=None,

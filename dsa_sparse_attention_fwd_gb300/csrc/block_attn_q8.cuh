@@ -1,0 +1,95 @@
+// Attention over a paged cache held in 8 bits: the problem as the kernels of
+// block_attn_q8*.cu see it, and one row from the formulas.
+#pragma once
+
+#include "block_attn.cuh"
+#include "cache_q8.cuh"
+
+namespace dsa {
+
+struct BlockAttnQ8 : BlockAttn {  // k, v and their strides: unused
+  Q8Cache c;
+  __nv_bfloat16 *o;
+  float *lse;
+};
+
+// One row by one warp in fp32 on the CUDA cores: a running maximum and sum
+// over its keys, 32 at a time, lane l holding one.  Rows whose fast result is
+// not finite are computed again by it: a key that only other rows of a tile
+// see may hold anything.  qs: the query as fp32 in shared memory, this
+// warp's own copy; lane l returns o[l + 32 i] in acc[i].
+static __device__ __noinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
+                                                int s, int hk, const float *qs,
+                                                int lane, bool &bad,
+                                                float (&acc)[4], float &lse) {
+  const float neg_inf = -__int_as_float(0x7f800000);
+  const long long pos = row_pos(p.q_pos, b, s);
+  const int32_t *ids = row_ids(p, b, s, hk);
+  const int n_cand = p.topk + p.local;
+  float m = neg_inf, l = 0.f;
+  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
+  for (int i = 0; i < n_cand; ++i) {
+    if (i >= p.topk && pos < (long long)(i - p.topk) << p.lb) break;
+    const int n = candidate(p, ids, pos, i, bad);
+    if (n < 0) continue;
+    bool again = false;  // a block given twice counts once
+    for (int t = lane; t < i && i < p.topk; t += 32)
+      again |= __ldg(ids + t) == n;
+    if (__any_sync(0xffffffffu, again)) continue;
+    const int page = block_page(p, b, n, bad);
+    if (page < 0) continue;
+    const int off0 = (int)((long long)n * p.blk % p.page_size);
+    for (int c = 0; c < p.blk; c += 32) {
+      const int jj = c + lane;
+      const long long j = (long long)n * p.blk + jj;
+      const bool has = jj < p.blk && j <= pos && j < p.T;
+      const int off = off0 + min(jj, p.blk - 1);
+      const float sk = q8_pow2(q8_exp(__ldg(p.c.ks + q8_scale_at(p.c, page, off, hk))));
+      const float sv = q8_pow2(q8_exp(__ldg(p.c.vs + q8_scale_at(p.c, page, off, hk))));
+      const uint8_t *kr =
+          p.c.k + page * p.c.k_p + off * p.c.k_t + hk * p.c.k_h;
+      const long long vo = page * p.c.v_p + off * p.c.v_t + hk * p.c.v_h;
+      float x = 0.f;
+      if (has) {
+        for (int d = 0; d < p.D; d += 4) {
+          const uint32_t w = *reinterpret_cast<const uint32_t *>(kr + d);
+          const float2 lo = q8_float2(w & 0xffffu), hi = q8_float2(w >> 16);
+          x = fmaf(qs[d], lo.x, x);
+          x = fmaf(qs[d + 1], lo.y, x);
+          x = fmaf(qs[d + 2], hi.x, x);
+          x = fmaf(qs[d + 3], hi.y, x);
+        }
+        x *= sk * p.scale;
+      }
+      float t = has ? x : neg_inf;
+      for (int o = 16; o; o >>= 1)
+        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+      const float mn = fmaxf(m, t);
+      const unsigned any = __ballot_sync(0xffffffffu, has);
+      if (!any) continue;
+      // a finite stand-in while every score so far is -inf
+      const float mu = mn > neg_inf ? mn : 0.f;
+      const float f = m > neg_inf ? expf(m - mu) : 0.f;
+      const float e = has ? expf(x - mu) : 0.f;
+      float es = e;
+      for (int o = 16; o; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
+      l = l * f + es;
+      for (int k = 0; k < 4; ++k) acc[k] *= f;
+      m = mn;
+      for (int t2 = 0; t2 < 32; ++t2) {
+        const long long at = __shfl_sync(0xffffffffu, vo, t2);
+        const float w = __shfl_sync(0xffffffffu, e * sv, t2);
+        if (!(any >> t2 & 1u)) continue;
+        for (int k = 0; k * 32 < p.D; ++k) {
+          const float2 v = q8_float2(p.c.v[at + lane + 32 * k]);
+          acc[k] = fmaf(w, v.x, acc[k]);
+        }
+      }
+    }
+  }
+  const bool some = l > 0.f || l != l;
+  for (int k = 0; k < 4; ++k) acc[k] = some ? acc[k] / l : 0.f;
+  lse = some ? m + logf(l) : neg_inf;
+}
+
+}  // namespace dsa

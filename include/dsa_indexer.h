@@ -692,6 +692,98 @@ DSA_API int dsa_block_attn_bwd(
     void *grad_q, void *grad_k, void *grad_v, void *workspace,
     size_t workspace_bytes, void *cuda_stream);
 
+/*
+ * A paged cache held in 8 bits.  k_cache, v_cache hold e4m3 values (one byte
+ * each) [num_pages, page_size, Hk, D], cache_strides as for
+ * dsa_paged_append(); k_scale, v_scale fp32 [num_pages, page_size / group, Hk],
+ * dense, hold one power of two for each `group` consecutive tokens and head:
+ * a key or value is its e4m3 value times the scale of its group.  Scales lie
+ * in [2^-40, 2^40]; anything else found there is read as the power of two at
+ * or below it, within these limits (a group that was never written has keys
+ * that no row sees).
+ * Envelope of the three entry points: group in {16, 32, 64, 128}, page_size a
+ * multiple of group, D a multiple of 16 up to 256, max_pages * page_size <
+ * 2^31; caches 16-byte aligned and their strides multiples of 16, none of them
+ * zero for a dimension of more than one element.
+ * Status word and workspace: as for dsa_paged_append() and
+ * dsa_block_attn_fwd() above (bits are only set; zero a new workspace's first
+ * 256 bytes once).
+ */
+
+/*
+ * Appends rows s < count[b] (NULL: all S) of sequence b at positions start[b]
+ * + s, the keys normed and rotated on the way (arithmetic of
+ * dsa_norm_rope_fwd(), in fp32 up to the rounding to e4m3), queries given with
+ * them into out_q, all S rows of them, row s at start[b] + s.  count is
+ * capped to [0, S]; a negative start[b] appends nothing.
+ * Scales: a group takes the smallest power of two s with |x| <= 448 s for all
+ * its new values x; where it holds earlier tokens (it begins before start[b])
+ * it keeps its scale if that is larger, and the earlier tokens' codes are
+ * rounded again if it grows.  Values round to nearest even; an infinity or a
+ * value beyond the largest scale becomes +-448, a NaN stays one, and neither
+ * counts for the scale.
+ * An append ends its sequence: tokens behind its last row are left as they are
+ * in memory, but their group's scale may be another afterwards.  Rows in a page
+ * that the table does not name (past it, or an id outside [0, num_pages)) are
+ * not appended and set DSA_ERR_INDEX_RANGE.  Sequences of one call must not
+ * share a group that the call writes to.
+ *   k, v, q, their strides, wq, wk, the rotation and out_q: as for
+ *   dsa_paged_append(); start, count [B] int32 on the device.
+ * Also: D * group <= 16384, else DSA_ERR_UNSUPPORTED.
+ *   workspace: 256 bytes, 256-byte aligned (the status word).
+ */
+DSA_API int dsa_paged_append_q8(
+    const void *k, const int64_t *k_strides, const void *v,
+    const int64_t *v_strides, const void *q, const int64_t *q_strides, int S,
+    int B, int H, int Hk, int D, void *k_cache, void *v_cache,
+    const int64_t *cache_strides, float *k_scale, float *v_scale, int group,
+    int num_pages, int page_size, const int32_t *page_table, int max_pages,
+    const int32_t *start, const int32_t *count, const float *wq,
+    const float *wk, float eps, const double *inv_freq, int rot_start,
+    int rot_dim, int interleaved, float rot_scale, void *out_q,
+    void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Reads it back: row t of out_k and out_v [T, B, Hk, D] bf16 (dense; one of
+ * them may be NULL) is token first[b] + t (first NULL: t) of sequence b where t
+ * < length[b] (NULL: T), exactly; zeros behind.  A token before the first or in
+ * a page that the table does not name gives zeros and sets
+ * DSA_ERR_INDEX_RANGE.
+ *   workspace: 256 bytes, 256-byte aligned (the status word).
+ */
+DSA_API int dsa_paged_read_q8(const void *k_cache, const void *v_cache,
+                              const int64_t *cache_strides,
+                              const float *k_scale, const float *v_scale,
+                              int group, int num_pages, int page_size,
+                              const int32_t *page_table, int max_pages, int T,
+                              int B, int Hk, int D, const int32_t *first,
+                              const int32_t *length, void *out_k, void *out_v,
+                              void *workspace, size_t workspace_bytes,
+                              void *cuda_stream);
+
+/*
+ * dsa_block_attn_paged_fwd() over it: selected blocks and local ones, or, with
+ * topk = 0 and local_blocks = max_pages * page_size / block_size, all keys up
+ * to each row's position.  The cache's values are multiplied as they are (e4m3
+ * to fp16 is exact; the queries enter as fp16 scaled by a power of two a row,
+ * 2^-24 of the row's largest value); scores, statistics and sums in fp32; the
+ * softmax weights, times the values' scale, enter the output product as fp16.
+ * Envelope: that of dsa_block_attn_paged_fwd() and of the cache.
+ *   workspace: dsa_block_attn_q8_workspace_size() bytes (T = max_pages *
+ *   page_size), 256-byte aligned (0 for invalid sizes).
+ */
+DSA_API size_t dsa_block_attn_q8_workspace_size(int S, int B, int H, int Hk,
+                                                int D, int T, int block_size,
+                                                int topk, int local_blocks);
+DSA_API int dsa_block_attn_paged_q8_fwd(
+    const void *q, const void *k_cache, const void *v_cache,
+    const int64_t *cache_strides, const float *k_scale, const float *v_scale,
+    int group, int num_pages, int page_size, const int32_t *page_table,
+    int max_pages, int S, int B, int H, int Hk, int D, const int32_t *blocks,
+    int sel_heads, int topk, int block_size, int local_blocks,
+    const int32_t *q_pos, float scale, void *out_o, float *out_lse,
+    void *workspace, size_t workspace_bytes, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
