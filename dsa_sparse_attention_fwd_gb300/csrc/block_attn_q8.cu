@@ -9,6 +9,9 @@
 namespace dsa {
 namespace {
 
+// Rows of a sequence and key head that take the kernel for few rows.
+bool few_rows(int S, int G) { return (long long)S * G <= 64; }
+
 // One warp a row.
 __global__ void __launch_bounds__(128) attn_q8_rows_kernel(
     const __grid_constant__ BlockAttnQ8 p) {
@@ -44,7 +47,7 @@ size_t dsa_block_attn_q8_workspace_size(int S, int B, int H, int Hk, int D,
   if (S <= 0 || B <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || D <= 0 ||
       T <= 0 || block_size <= 0 || topk < 0 || local_blocks < 0)
     return 0;
-  return 256;
+  return dsa::few_rows(S, H / Hk) ? dsa::attn_q8_step_workspace_bytes(D) : 256;
 }
 
 int dsa_block_attn_paged_q8_fwd(
@@ -87,6 +90,9 @@ int dsa_block_attn_paged_q8_fwd(
   int num_sms = 0;
   rc = dsa::device_num_sms(&num_sms);
   if (rc != DSA_OK) return rc;
+  if (dsa::few_rows(S, p.G))
+    return dsa::run_attn_q8_step(p, workspace, num_sms,
+                                 static_cast<cudaStream_t>(cuda_stream));
   const long long grid = ((long long)S * B * H + 3) / 4;
   const long long most = 16ll * num_sms;
   dsa::attn_q8_rows_kernel<<<(unsigned)(grid < most ? grid : most), 128, 0,

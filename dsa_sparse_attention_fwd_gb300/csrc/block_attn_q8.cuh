@@ -13,6 +13,11 @@ struct BlockAttnQ8 : BlockAttn {  // k, v and their strides: unused
   float *lse;
 };
 
+// Few rows (block_attn_q8_step.cu).
+size_t attn_q8_step_workspace_bytes(int D);
+int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
+                     cudaStream_t st);
+
 // One row by one warp in fp32 on the CUDA cores: a running maximum and sum
 // over its keys, 32 at a time, lane l holding one.  Rows whose fast result is
 // not finite are computed again by it: a key that only other rows of a tile

@@ -1,0 +1,952 @@
+// Attention over a paged cache held in 8 bits for few rows: single tokens and
+// drafts, over selected blocks or all keys.
+//
+// Bounded by memory: every key and value is one byte an element and is read
+// once for the G heads (and, where all keys are attended to, the queries) that
+// share it.  An item is up to 16 or 32 rows of one sequence and key head; all
+// items' steps of 32 keys laid end to end are cut into equal slices, one a
+// CTA, so that sequences of any lengths load the GPU evenly.  An item that
+// spans CTAs leaves its parts in the workspace, joined by the CTA that
+// finishes last in the order of the slices.
+//
+// A producer warp walks the slice (block lists, pages, scales) and fills a
+// ring of shared memory by TMA, each of eight warps having its own stages: a
+// step of 32 keys goes to one warp, which keeps its own running maximum, sum
+// and output for the item; the warps meet only at an item's end, while the
+// ring fills with the next.  The products are mma.sync m16n8k16: a tile of a
+// few rows cannot fill a tcgen05 tile, whose operands would have to be
+// written to shared memory again as 16-bit values (three times the bytes that
+// came); here they go from the 8-bit tile to registers, two elements a
+// conversion (e4m3 to fp16 is exact).
+//     t_j = c q.k_j 2^ek + ev,   P_j = 2^(t_j - m),   O += P_j v_j,
+//     l += P_j 2^-ev
+// with 2^ek, 2^ev the group's scales: the values' scale is part of the
+// exponent, so the largest P is 2^6 to 2^14 whatever the scales are, and fp16
+// holds P to 2^-11 (more than bf16), down to 2^-31 of the largest.  The query
+// enters as fp16 after a power of two brings its largest value to 2^14.
+//
+// The order of the elements in the products is free as long as both sides
+// agree, and chosen for whole 16-byte loads without bank conflicts: thread (g,
+// t) reads 16 neighbours of a key, and for the output product 16 neighbours of
+// the keys 2t and (2t + 1) ^ 4.
+//
+// Values that are not finite: masked scores are replaced before use, value
+// rows that no row of the tile sees are zeroed in registers, and rows whose
+// result is not finite are computed again on their own (block_attn_q8.cuh).
+#include "block_attn_host.cuh"
+#include "block_attn_q8.cuh"
+#include "ptx.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kWarps = 8;                      // that multiply
+constexpr int kThreads = kWarps * 32 + 32;     // and the producer
+constexpr int kKeys = 32;                      // of a step
+constexpr int kPitch = 36;                     // floats of a row in the join
+// A CTA's slice has at least so many steps: one a warp.
+constexpr int kMinSteps = kWarps;
+// The counts of written parts: a byte for each CTA, in the 256 bytes that
+// every entry point leaves to the status word.
+constexpr int kDoneOffset = 64;
+constexpr int kMaxCtas = 256 - kDoneOffset;
+
+struct StepPlan {
+  bool all;     // no selection: all keys of the local blocks
+  int rows;     // rows of an item's whole (b, hk) or (b, s, hk)
+  int tiles;    // items that these are cut into
+  int items_b;  // items of a sequence
+  int box;      // tokens of a TMA box: 16 or 32
+  int stages;   // of a warp's ring
+  int cap;      // entries of the block list
+  float *part_o, *part_l;  // [CTA][2][32] rows of D, and their log-sums
+  uint32_t *done;
+};
+
+struct Maps8 {
+  CUtensorMap k, v;
+};
+
+// What the producer says of an item's part.
+struct Entry {
+  int n, g0;           // its steps, and the CTA's steps before it
+  int b, hk, s, tile;  // s: the query (selection); rows of a tile otherwise
+  int c0, c1;          // CTAs that share it
+  int slot;            // where this one's part goes: 0, 1 or -1 (whole)
+  int pad[3];
+};
+
+// Of 16 keys of a step: exponents of the scales, the first key, and how many
+// of them some row of the tile sees.
+struct Sub {
+  int ek, ev, j0, seen;
+};
+
+template <int D, int MT>
+struct StepSmem {
+  static constexpr int kStage = 2 * kKeys * D;  // K, then V
+  static constexpr int kJoin = kWarps * 16 * kPitch * 4;
+  static constexpr int kQ = MT > 1 ? MT * 16 * D * 2 : 0;
+  static int bytes(int stages, int nblk, int cap) {
+    return stages * kWarps * (kStage + 2 * (int)sizeof(Sub) + 16) + kJoin +
+           kQ + 2 * (int)sizeof(Entry) + 3 * kWarps * 32 * 4 + 256 +
+           (cap ? (nblk + 31) / 32 * 4 + (cap * 2 + 15) / 16 * 16 : 0) + 1024;
+  }
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4],
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// First row position, last key that a row of the queries [s0, s1] sees, and
+// the first key that one may see (local blocks only).
+struct Span {
+  int lo, hi;  // keys lo .. hi (hi < lo: none)
+};
+__device__ __forceinline__ Span span_of(const BlockAttnQ8 &p, int b, int s0,
+                                        int s1) {
+  const long long first = row_pos(p.q_pos, b, s0);
+  const long long last = row_pos(p.q_pos, b, s1);
+  Span r;
+  r.hi = last < 0 ? -1 : (int)min(last, (long long)p.T - 1);
+  const long long blk = ((max(first, 0ll) >> p.lb) - p.local + 1) << p.lb;
+  r.lo = (int)min(max(blk, 0ll), (long long)p.T);
+  return r;
+}
+
+// Steps that an item of sequence b may take: what slices are cut by.
+__device__ __forceinline__ long long steps_bound(const BlockAttnQ8 &p,
+                                                 const StepPlan &pl, int b) {
+  const Span r = span_of(p, b, 0, p.S - 1);
+  long long keys = (long long)r.hi + 1 - (pl.all ? r.lo : 0);
+  if (!pl.all) keys = min(keys, (long long)(p.topk + p.local) << p.lb);
+  return max(1ll, (keys + kKeys - 1) / kKeys);
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_q8_step_kernel(const __grid_constant__ Maps8 maps,
+                        const __grid_constant__ BlockAttnQ8 p,
+                        const __grid_constant__ StepPlan pl) {
+  using L = StepSmem<D, MT>;
+  constexpr int kRows = 16 * MT;
+  const float neg_inf = -__int_as_float(0x7f800000);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const int NS = pl.stages;
+  uint8_t *at = smem + NS * kWarps * L::kStage;
+  float *join = reinterpret_cast<float *>(at);
+  at += L::kJoin;
+  uint4 *qf = reinterpret_cast<uint4 *>(at);  // MT > 1: Q as MMA operands
+  at += L::kQ;
+  Sub *subs = reinterpret_cast<Sub *>(at);
+  at += NS * kWarps * 2 * sizeof(Sub);
+  Entry *entries = reinterpret_cast<Entry *>(at);
+  at += 2 * sizeof(Entry);
+  float *row_m = reinterpret_cast<float *>(at);  // [warp][32]
+  float *row_l = row_m + kWarps * 32;
+  float *row_f = row_l + kWarps * 32;
+  at += 3 * kWarps * 32 * 4;
+  const uint32_t bars = smem_u32(at);
+  at += NS * kWarps * 16;
+  volatile int *abort_flag = reinterpret_cast<int *>(at);
+  unsigned *odd_rows = reinterpret_cast<unsigned *>(at + 4);
+  int *joined = reinterpret_cast<int *>(at + 8);
+  float *row_lse = reinterpret_cast<float *>(at + 64);  // [32]
+  const uint32_t item_bars = smem_u32(at + 16);
+  at += 64 + 32 * 4 + 64;
+  uint32_t *bitmap = reinterpret_cast<uint32_t *>(at);
+  uint16_t *list = reinterpret_cast<uint16_t *>(bitmap + (p.nblk + 31) / 32);
+  auto full = [&](int w, int st) { return bars + (w * NS + st) * 16; };
+  auto empty = [&](int w, int st) { return bars + (w * NS + st) * 16 + 8; };
+  auto item_full = [&](int e) { return item_bars + e * 16; };
+  auto item_empty = [&](int e) { return item_bars + e * 16 + 8; };
+  auto stage = [&](int w, int st) {
+    return smem_u32(smem) + (w * NS + st) * L::kStage;
+  };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NS * kWarps; ++i) {
+      mbar_init(bars + i * 16, 1);
+      mbar_init(bars + i * 16 + 8, 1);
+    }
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(item_full(e), 1);
+      mbar_init(item_empty(e), kWarps);
+    }
+    *abort_flag = 0;
+    *odd_rows = 0;
+    joined[1] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    // ---------------- producer ----------------
+    // the sequences' steps, and this CTA's slice of them all
+    const int per = (p.B + 31) / 32;
+    long long mine = 0;
+    for (int b = lane * per; b < min(p.B, lane * per + per); ++b)
+      mine += steps_bound(p, pl, b) * pl.items_b;
+    long long before = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    const long long all = __shfl_sync(0xffffffffu, before, 31);
+    before -= mine;
+    const long long ctas =
+        min((long long)gridDim.x, (all + kMinSteps - 1) / kMinSteps);
+    const long long cta = blockIdx.x;
+    const long long u0 = cta < ctas ? all * cta / ctas : all;
+    const long long u1 = cta < ctas ? all * (cta + 1) / ctas : all;
+    // the CTA that holds step u of them all
+    auto holder = [&](long long u) {
+      long long c = (u * ctas + ctas - 1) / all;
+      while (c > 0 && all * c / ctas > u) --c;
+      while (c + 1 < ctas && all * (c + 1) / ctas <= u) ++c;
+      return (int)c;
+    };
+    int b = 0;
+    long long w = u0, w_b = 0;  // position, and where sequence b begins
+    if (u0 < u1) {
+      const unsigned here = __ballot_sync(
+          0xffffffffu, before <= u0 && u0 < before + mine);
+      const int src = __ffs(here) - 1;
+      b = src * per;
+      w_b = __shfl_sync(0xffffffffu, before, src);
+    }
+    int entry = 0, g = 0;
+    bool bad = false, ok = true;
+    while (ok && w < u1) {
+      const long long U = steps_bound(p, pl, b);
+      if (w - w_b >= U * pl.items_b) {
+        w_b += U * pl.items_b;
+        ++b;
+        continue;
+      }
+      const int idx = (int)((w - w_b) / U);
+      const long long w_i = w_b + idx * U;
+      const long long x0 = w - w_i, x1 = min(U, x0 + (u1 - w));
+      w += x1 - x0;
+      const int tile = idx % pl.tiles;
+      const int s = pl.all ? 0 : idx / pl.tiles % p.S;
+      const int hk = pl.all ? idx / pl.tiles : idx / pl.tiles / p.S;
+      // the item's keys: units of `box` keys
+      Span sp;
+      int units;
+      if (pl.all) {
+        sp = span_of(p, b, tile * kRows / p.G,
+                     (min(pl.rows, (tile + 1) * kRows) - 1) / p.G);
+        units = max(0, sp.hi - sp.lo + pl.box) / pl.box;
+      } else {
+        sp = span_of(p, b, s, s);
+        const long long pos = row_pos(p.q_pos, b, s);
+        const int32_t *ids = row_ids(p, b, s, hk);
+        const int words = (p.nblk + 31) / 32, n_cand = p.topk + p.local;
+        for (int i = lane; i < words; i += 32) bitmap[i] = 0u;
+        __syncwarp();
+        for (int i0 = lane; i0 < n_cand; i0 += 128) {
+          int n[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            n[u] = i0 + u * 32 < n_cand
+                       ? candidate(p, ids, pos, i0 + u * 32, bad)
+                       : -1;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (n[u] >= 0) atomicOr(bitmap + (n[u] >> 5), 1u << (n[u] & 31));
+        }
+        __syncwarp();
+        int count = 0;
+        for (int i0 = 0; i0 < words; i0 += 32) {
+          uint32_t m = i0 + lane < words ? bitmap[i0 + lane] : 0u;
+          const int mn = __popc(m);
+          int to = mn;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, to, o);
+            if (lane >= o) to += x;
+          }
+          const int sum = __shfl_sync(0xffffffffu, to, 31);
+          to += count - mn;
+          for (; m; m &= m - 1)
+            list[to++] = (uint16_t)((i0 + lane) * 32 + __ffs(m) - 1);
+          count += sum;
+        }
+        __syncwarp();
+        units = count << (p.lb - (pl.box == 32 ? 5 : 4));
+      }
+      const int per_step = kKeys / pl.box;
+      const int steps = (units + per_step - 1) / per_step;
+      const int t0 = (int)(steps * x0 / U), t1 = (int)(steps * x1 / U);
+      // tell the others
+      if (!__all_sync(0xffffffffu, wait_bar(item_empty(entry & 1),
+                                            (entry >> 1 & 1) ^ 1, abort_flag,
+                                            p.status))) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        Entry &e = entries[entry & 1];
+        e.n = t1 - t0;
+        e.g0 = g;
+        e.b = b, e.hk = hk, e.s = s, e.tile = tile;
+        e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
+        e.c0 = e.c1 = (int)cta;
+        if (e.slot >= 0) {
+          e.c0 = x0 == 0 ? (int)cta : holder(w_i);
+          e.c1 = x1 == U ? (int)cta : holder(w_i + U - 1);
+        }
+        mbar_arrive(item_full(entry & 1));
+      }
+      __syncwarp();
+      ++entry;
+      // 16 steps at a time: lane 2 i + j holds the 16 keys j of step i
+      struct Look {
+        int page, off, j0, seen;
+        float ks, vs;
+      };
+      auto look = [&](int t) {
+        Look r{-1, 0, 0, 0, 1.f, 1.f};
+        const int step = t + (lane >> 1), sub = lane & 1;
+        if (step >= t1) return r;
+        const int unit = pl.box == 32 ? step : 2 * step + sub;
+        if (unit >= units) return r;
+        if (pl.all) {
+          r.j0 = sp.lo + step * kKeys + sub * 16;
+        } else {
+          const int sh = p.lb - (pl.box == 32 ? 5 : 4);
+          r.j0 = ((int)list[unit >> sh] << p.lb) +
+                 (unit & ((1 << sh) - 1)) * pl.box +
+                 (pl.box == 32 ? sub * 16 : 0);
+        }
+        r.seen = min(max(sp.hi - r.j0 + 1, 0), 16);
+        if (r.seen == 0) return r;
+        const int pg = r.j0 / p.page_size;
+        r.off = r.j0 - pg * p.page_size;
+        r.page = __ldg(p.table + (long long)b * p.max_pages + pg);
+        if (r.page < 0 || r.page >= p.num_pages) {
+          bad = true;
+          r.seen = 0;
+          r.page = -1;
+        } else {
+          const long long sa = q8_scale_at(p.c, r.page, r.off, hk);
+          r.ks = __ldg(p.c.ks + sa);
+          r.vs = __ldg(p.c.vs + sa);
+        }
+        return r;
+      };
+      Look next = look(t0);
+      for (int t = t0; ok && t < t1; t += 16) {
+        const Look cur = next;
+        if (t + 16 < t1) next = look(t + 16);
+        const Sub mine_s{q8_exp(cur.ks), q8_exp(cur.vs), cur.j0, cur.seen};
+        for (int i = 0; i < 16 && t + i < t1; ++i, ++g) {
+          const int wp = g % kWarps, turn = g / kWarps;
+          const int st = turn % NS;
+          if (!__all_sync(0xffffffffu,
+                          wait_bar(empty(wp, st), (turn / NS & 1) ^ 1,
+                                   abort_flag, p.status))) {
+            ok = false;
+            break;
+          }
+          // lanes 2 i and 2 i + 1 hold this step's keys
+          const int page0 = __shfl_sync(0xffffffffu, cur.page, 2 * i);
+          const int page1 = __shfl_sync(0xffffffffu, cur.page, 2 * i + 1);
+          if ((lane >> 1) == i) subs[(wp * NS + st) * 2 + (lane & 1)] = mine_s;
+          const int n_box = pl.box == 32 ? (page0 >= 0) * 2
+                                         : (page0 >= 0) + (page1 >= 0);
+          __syncwarp();
+          if (lane == 2 * i)
+            mbar_arrive_expect_tx(full(wp, st), n_box * 2 * 16 * D);
+          __syncwarp();
+          if ((lane >> 1) == i && cur.page >= 0 &&
+              (pl.box == 16 || lane == 2 * i)) {
+            const uint32_t dst = stage(wp, st) + (lane & 1) * 16 * D;
+            tma_load_4d(dst, &maps.k, full(wp, st), 0, cur.off, hk, cur.page);
+            tma_load_4d(dst + kKeys * D, &maps.v, full(wp, st), 0, cur.off, hk,
+                        cur.page);
+          }
+        }
+      }
+    }
+    if (bad) atomicOr(p.status, kStatusIndexRange);
+    // no more
+    if (ok && __all_sync(0xffffffffu,
+                         wait_bar(item_empty(entry & 1), (entry >> 1 & 1) ^ 1,
+                                  abort_flag, p.status))) {
+      if (lane == 0) {
+        entries[entry & 1].n = -1;
+        mbar_arrive(item_full(entry & 1));
+      }
+    }
+  } else {
+    // ---------------- the eight warps that multiply ----------------
+    const int gq = lane >> 2, tq = lane & 3;
+    const float c2 = p.scale * 1.4426950408889634f;
+    for (int entry = 0;; ++entry) {
+      const bool got = __all_sync(
+          0xffffffffu, wait_bar(item_full(entry & 1), entry >> 1 & 1,
+                                abort_flag, p.status));
+      // (all stop together; and the item before has left shared memory)
+      if (named_bar_or(1, kWarps * 32, !got)) break;
+      const Entry e = entries[entry & 1];
+      if (e.n < 0) break;
+      // this thread's rows: gq and gq + 8 of each 16
+      int pos[MT][2], lo[MT][2];
+      long long out_row[MT][2];  // -1: none
+      float cr[MT][2];           // c 2^(the query's power of two)
+      uint32_t qr[MT == 1 ? D / 16 : 1][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float qv[2][D / 4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int rr = e.tile * kRows + mt * 16 + gq + 8 * i;
+          const bool live = rr < pl.rows;
+          const int s = pl.all ? rr / p.G : e.s;
+          const int h = e.hk * p.G + (pl.all ? rr % p.G : rr);
+          out_row[mt][i] =
+              live ? ((long long)s * p.B + e.b) * p.H + h : -1;
+          const long long ps = live ? row_pos(p.q_pos, e.b, s) : -1;
+          pos[mt][i] = ps < 0 ? -1 : (int)min(ps, (long long)p.T - 1);
+          lo[mt][i] =
+              pl.all && live
+                  ? (int)min(max(((ps >> p.lb) - p.local + 1) << p.lb, 0ll),
+                             (long long)p.T)
+                  : 0;
+          float top = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            uint4 x[2] = {};
+            if (live) {
+              const uint4 *src = reinterpret_cast<const uint4 *>(
+                  p.q + out_row[mt][i] * D + 64 * c + 16 * tq);
+              x[0] = __ldg(src);
+              x[1] = __ldg(src + 1);
+            }
+            const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w,
+                                   x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              qv[i][c * 16 + 2 * k] = __uint_as_float(u[k] << 16);
+              qv[i][c * 16 + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < D / 4; ++k) top = fmaxf(top, fabsf(qv[i][k]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // the largest value to [2^14, 2^15)
+          int eq = (__float_as_int(top) >> 23) - 127 - 14;
+          eq = min(max(eq, -100), 100);
+          const float f = q8_pow2(-eq);
+#pragma unroll
+          for (int k = 0; k < D / 4; ++k) qv[i][k] *= f;
+          cr[mt][i] = c2 * q8_pow2(eq);
+        }
+        // operand k of step ks: elements 64 (ks / 4) + 16 tq + 4 (ks % 4) ..
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int k = (ks >> 2) * 16 + (ks & 3) * 4;
+          const uint32_t a[4] = {pack_half2(qv[0][k], qv[0][k + 1]),
+                                 pack_half2(qv[1][k], qv[1][k + 1]),
+                                 pack_half2(qv[0][k + 2], qv[0][k + 3]),
+                                 pack_half2(qv[1][k + 2], qv[1][k + 3])};
+          if constexpr (MT == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qr[ks][j] = a[j];
+          } else if (ks % kWarps == warp) {
+            qf[(ks * MT + mt) * 32 + lane] =
+                make_uint4(a[0], a[1], a[2], a[3]);
+          }
+        }
+      }
+      if constexpr (MT > 1) named_bar_sync(1, kWarps * 32);
+      // the tile's rows see the same keys but where a step holds keys after
+      // the first row's position or before the last row's first block
+      int pos_lo = 0x7fffffff, lo_hi = 0;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (out_row[mt][i] >= 0) pos_lo = min(pos_lo, pos[mt][i]);
+          lo_hi = max(lo_hi, lo[mt][i]);
+        }
+      pos_lo = __reduce_min_sync(0xffffffffu, pos_lo);
+      lo_hi = __reduce_max_sync(0xffffffffu, lo_hi);
+
+      float o[MT][D / 8][4] = {};
+      float m[MT][2], l[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        m[mt][0] = m[mt][1] = neg_inf, l[mt][0] = l[mt][1] = 0.f;
+      const int g1 = e.g0 + e.n;
+      int g = e.g0 + (warp - e.g0 % kWarps + kWarps) % kWarps;
+      bool ok = true;
+      for (; ok && g < g1; g += kWarps) {
+        const int turn = g / kWarps, st = turn % NS;
+        if (!__all_sync(0xffffffffu, wait_bar(full(warp, st), turn / NS & 1,
+                                              abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        const uint32_t sk = stage(warp, st), sv = sk + kKeys * D;
+        const Sub sub[2] = {subs[(warp * NS + st) * 2],
+                            subs[(warp * NS + st) * 2 + 1]};
+        // ---- scores: four tiles of 8 keys ----
+        float x[MT][4][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[mt][n][j] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 kw[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const int r = 8 * n + (gq ^ ((gq & 1) << 2));
+            const int ch = c * 4 + tq;
+            kw[n] = lds128(sk + r * D +
+                           ((D == 128 ? ch ^ (r & 7) : ch ^ (r >> 1 & 3)) << 4));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if constexpr (MT == 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[mt][i] = qr[c * 4 + j][i];
+              } else {
+                const uint4 v = qf[((c * 4 + j) * MT + mt) * 32 + lane];
+                a[mt][0] = v.x, a[mt][1] = v.y, a[mt][2] = v.z, a[mt][3] = v.w;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const uint32_t wd = j == 0   ? kw[n].x
+                                  : j == 1 ? kw[n].y
+                                  : j == 2 ? kw[n].z
+                                           : kw[n].w;
+              const uint32_t b0 = q8_half2(wd & 0xffffu);
+              const uint32_t b1 = q8_half2(wd >> 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mma_f16(x[mt][n], a[mt], b0, b1);
+            }
+          }
+        }
+        // ---- softmax ----
+        uint32_t pa[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float mx[2] = {neg_inf, neg_inf};
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float sc = q8_pow2(sub[u].ek), ev = (float)sub[u].ev;
+            const float a0 = cr[mt][0] * sc, a1 = cr[mt][1] * sc;
+            const bool some = sub[u].seen < 16 || sub[u].j0 + 15 > pos_lo ||
+                              sub[u].j0 < lo_hi;
+#pragma unroll
+            for (int n = 2 * u; n < 2 * u + 2; ++n) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[mt][n][j] = fmaf(x[mt][n][j], j < 2 ? a0 : a1, ev);
+              if (some) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int key = 8 * (n & 1) + ((2 * tq + (j & 1)) ^
+                                                 ((j & 1) << 2));
+                  const int jj = sub[u].j0 + key;
+                  const bool sees = key < sub[u].seen &&
+                                    jj <= pos[mt][j >> 1] &&
+                                    jj >= lo[mt][j >> 1];
+                  x[mt][n][j] = sees ? x[mt][n][j] : neg_inf;
+                }
+              }
+              mx[0] = fmaxf(mx[0], fmaxf(x[mt][n][0], x[mt][n][1]));
+              mx[1] = fmaxf(mx[1], fmaxf(x[mt][n][2], x[mt][n][3]));
+            }
+          }
+          bool move = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            move |= mx[i] > m[mt][i] + 14.f;
+          }
+          if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool mv = mx[i] > m[mt][i] + 14.f;
+              const float to = mx[i] - 6.f;
+              const float f = mv ? ex2(m[mt][i] - to) : 1.f;
+              if (mv) m[mt][i] = to;
+              l[mt][i] *= f;
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                o[mt][n][2 * i] *= f;
+                o[mt][n][2 * i + 1] *= f;
+              }
+            }
+          }
+          const float mu0 = m[mt][0] > neg_inf ? m[mt][0] : 0.f;
+          const float mu1 = m[mt][1] > neg_inf ? m[mt][1] : 0.f;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              float *v = x[mt][2 * u + n];
+              v[0] = ex2(v[0] - mu0), v[1] = ex2(v[1] - mu0);
+              v[2] = ex2(v[2] - mu1), v[3] = ex2(v[3] - mu1);
+              s0 += v[0] + v[1];
+              s1 += v[2] + v[3];
+              pa[mt][u][2 * n] = pack_half2(v[0], v[1]);
+              pa[mt][u][2 * n + 1] = pack_half2(v[2], v[3]);
+            }
+            const float un = q8_pow2(-sub[u].ev);
+            l[mt][0] = fmaf(s0, un, l[mt][0]);
+            l[mt][1] = fmaf(s1, un, l[mt][1]);
+          }
+        }
+        // ---- O += P V, 16 keys at a time ----
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          constexpr int W = D / 32;  // 32-bit words of a key that a thread has
+          uint32_t vw[4][W];
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const int key = 8 * (r4 >> 1) + ((2 * tq + (r4 & 1)) ^
+                                             ((r4 & 1) << 2));
+            const int r = 16 * u + key;
+            if constexpr (D == 128) {
+              const uint4 v = lds128(sv + r * D + ((gq ^ (r & 7)) << 4));
+              vw[r4][0] = v.x, vw[r4][1] = v.y;
+              vw[r4][2] = v.z, vw[r4][3] = v.w;
+            } else {
+              const uint2 v = lds64(sv + r * D +
+                                    ((gq >> 1 ^ (r >> 1 & 3)) << 4) +
+                                    (gq & 1) * 8);
+              vw[r4][0] = v.x, vw[r4][1] = v.y;
+            }
+            if (sub[u].seen < 16 && key >= sub[u].seen) {
+#pragma unroll
+              for (int i = 0; i < W; ++i) vw[r4][i] = 0u;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              // elements 2 h and 2 h + 1 of word i: keys' bytes side by side
+              const uint32_t sel = h ? 0x7362u : 0x5140u;
+              const uint32_t w0 = __byte_perm(vw[0][i], vw[1][i], sel);
+              const uint32_t w1 = __byte_perm(vw[2][i], vw[3][i], sel);
+              const uint32_t b00 = q8_half2(w0 & 0xffffu);
+              const uint32_t b01 = q8_half2(w1 & 0xffffu);
+              const uint32_t b10 = q8_half2(w0 >> 16);
+              const uint32_t b11 = q8_half2(w1 >> 16);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma_f16(o[mt][i * 4 + 2 * h], pa[mt][u], b00, b01);
+                mma_f16(o[mt][i * 4 + 2 * h + 1], pa[mt][u], b10, b11);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty(warp, st));
+      }
+      // ---------------- the item's end ----------------
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float s = l[mt][i];
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          if (tq == 0) {
+            row_m[warp * 32 + mt * 16 + gq + 8 * i] = m[mt][i];
+            row_l[warp * 32 + mt * 16 + gq + 8 * i] = s;
+          }
+        }
+      named_bar_sync(1, kWarps * 32);
+      const int first = e.tile * kRows;
+      const int live = min(pl.rows - first, kRows);
+      auto row_at = [&](int r) {
+        const int rr = first + r;
+        const int s = pl.all ? rr / p.G : e.s;
+        return ((long long)s * p.B + e.b) * p.H + e.hk * p.G +
+               (pl.all ? rr % p.G : rr);
+      };
+      const size_t part =
+          ((size_t)blockIdx.x * 2 + (e.slot > 0 ? 1 : 0)) * 32;
+      if (tid < kRows) {
+        float M = neg_inf, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, row_m[i * 32 + tid]);
+        const float mu = M > neg_inf ? M : 0.f;
+        float f[kWarps];
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          f[i] = ex2(row_m[i * 32 + tid] - mu);
+          sum = fmaf(row_l[i * 32 + tid], f[i], sum);
+        }
+        const bool some = sum > 0.f || sum != sum;
+        const float inv = some ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) row_f[i * 32 + tid] = f[i] * inv;
+        row_lse[tid] = some ? M + log2f(sum) : neg_inf;
+        if ((sum != sum || sum > 3e38f) && tid < live)
+          atomicOr(odd_rows, 1u << tid);
+      }
+      named_bar_sync(1, kWarps * 32);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float f0 = row_f[warp * 32 + mt * 16 + gq];
+        const float f1 = row_f[warp * 32 + mt * 16 + gq + 8];
+        // columns 2 tq and 2 tq + 1 of tile n are elements (2 tq) D / 8 + n
+        // and the next D / 8: eight tiles and one column a round
+#pragma unroll
+        for (int rd = 0; rd < D / 32; ++rd) {
+          const int cc = rd & 1, nh = rd >> 1;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float4 v[2];
+            float *vv = reinterpret_cast<float *>(v);
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+              vv[n] = o[mt][nh * 8 + n][2 * i + cc] * (i ? f1 : f0);
+            float4 *dst = reinterpret_cast<float4 *>(
+                join + (warp * 16 + gq + 8 * i) * kPitch + tq * 8);
+            dst[0] = v[0];
+            dst[1] = v[1];
+          }
+          named_bar_sync(1, kWarps * 32);
+          {
+            const int r = tid >> 4, c = (tid & 15) * 2;
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+              const float2 v = *reinterpret_cast<const float2 *>(
+                  join + (i * 16 + r) * kPitch + c);
+              sum.x += v.x, sum.y += v.y;
+            }
+            const int d = (2 * (c >> 3) + cc) * (D / 8) + nh * 8 + (c & 7);
+            const int row = mt * 16 + r;
+            if (row < live) {
+              if (!(fabsf(sum.x) <= 3e38f && fabsf(sum.y) <= 3e38f))
+                atomicOr(odd_rows, 1u << row);
+              if (e.slot < 0)
+                *reinterpret_cast<uint32_t *>(p.o + row_at(row) * D + d) =
+                    pack_bf16x2(sum.x, sum.y);
+              else
+                *reinterpret_cast<float2 *>(
+                    pl.part_o + (part + row) * D + d) = sum;
+            }
+          }
+          named_bar_sync(1, kWarps * 32);
+        }
+      }
+      unsigned odd = *odd_rows;
+      if (tid < live) {
+        if (e.slot < 0)
+          p.lse[row_at(tid)] = row_lse[tid] * 0.69314718055994531f;
+        else  // a NaN tells the joining CTA to compute the row again
+          pl.part_l[part + tid] =
+              odd >> tid & 1u ? __int_as_float(0x7fffffff) : row_lse[tid];
+      }
+      if (e.slot >= 0) {
+        __threadfence();
+        named_bar_sync(1, kWarps * 32);
+        if (tid == 0) {
+          const int sh = 8 * (e.c0 & 3);
+          uint32_t *word = pl.done + (e.c0 >> 2);
+          const uint32_t was = atomicAdd(word, 1u << sh) >> sh & 0xffu;
+          const bool last = was == (uint32_t)(e.c1 - e.c0);
+          if (last) atomicAnd(word, ~(0xffu << sh));  // for the next call
+          __threadfence();
+          *joined = last;
+        }
+        named_bar_sync(1, kWarps * 32);
+        odd = 0;
+        if (*joined) {
+          // o = sum_i w_i o_i / sum_i w_i, w_i = 2^(l_i - max)
+          const int parts = e.c1 - e.c0 + 1;
+          constexpr int kLanes = D / 4;  // threads of a row
+          for (int r = tid / kLanes; r < kRows;
+               r += kWarps * 32 / kLanes) {
+            const int c = tid % kLanes;
+            if (r >= live) continue;
+            float M = neg_inf, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            bool again = false;
+            for (int i0 = 0; i0 < parts; i0 += 8) {
+              float ls[8];
+              float4 v[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const int i = min(i0 + u, parts - 1);
+                const size_t a =
+                    ((size_t)(e.c0 + i) * 2 + (i == 0 ? 1 : 0)) * 32 + r;
+                ls[u] = __ldcg(pl.part_l + a);
+                v[u] = __ldcg(
+                    reinterpret_cast<const float4 *>(pl.part_o + a * D) + c);
+                if (i0 + u >= parts) ls[u] = neg_inf;
+              }
+              float mx = M;
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                again |= ls[u] != ls[u];
+                mx = fmaxf(mx, ls[u]);
+              }
+              const float ref = mx > neg_inf ? mx : 0.f;
+              const float f = ex2(M - ref);
+              sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const float wt = ex2(ls[u] - ref);
+                sum += wt;
+                acc.x = fmaf(wt, v[u].x, acc.x);
+                acc.y = fmaf(wt, v[u].y, acc.y);
+                acc.z = fmaf(wt, v[u].z, acc.z);
+                acc.w = fmaf(wt, v[u].w, acc.w);
+              }
+              M = mx;
+            }
+            const float inv = sum > 0.f ? 1.f / sum : 0.f;
+            const long long to = row_at(r);
+            reinterpret_cast<uint2 *>(p.o + to * D)[c] =
+                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                           pack_bf16x2(acc.z * inv, acc.w * inv));
+            if (c == 0) {
+              p.lse[to] = sum > 0.f
+                              ? (M + log2f(sum)) * 0.69314718055994531f
+                              : neg_inf;
+              if (again) atomicOr(joined + 1, 1 << r);
+            }
+          }
+          named_bar_sync(1, kWarps * 32);
+          odd = joined[1];
+        }
+      }
+      if (odd) {  // (the same value in all threads)
+        // rows on their own, a warp each
+        float *qs = join + warp * 128;
+        int k = 0;
+        for (unsigned left = odd; left; left &= left - 1, ++k) {
+          if (k % kWarps != warp) continue;
+          const long long to = row_at(__ffs(left) - 1);
+          const int rr = first + __ffs(left) - 1;
+          __syncwarp();
+          for (int d = lane; d < D; d += 32)
+            qs[d] = __bfloat162float(p.q[to * D + d]);
+          __syncwarp();
+          float acc[4], lse;
+          bool bad = false;
+          attn_row_q8(p, e.b, pl.all ? rr / p.G : e.s, e.hk, qs, lane, bad,
+                      acc, lse);
+          for (int i = 0; i * 32 < D; ++i)
+            p.o[to * D + lane + 32 * i] = __float2bfloat16(acc[i]);
+          if (lane == 0) p.lse[to] = lse;
+        }
+      }
+      named_bar_sync(1, kWarps * 32);
+      if (tid == 0) *odd_rows = 0, joined[1] = 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(item_empty(entry & 1));
+    }
+  }
+}
+
+template <int D, int MT>
+int launch(const BlockAttnQ8 &p, StepPlan &pl, const Maps8 &maps, int ctas,
+           cudaStream_t st) {
+  using L = StepSmem<D, MT>;
+  auto kern = attn_q8_step_kernel<D, MT>;
+  // as many stages as there is room for beside the block list
+  for (pl.stages = D == 64 ? 5 : 3;; --pl.stages) {
+    if (L::bytes(pl.stages, p.nblk, pl.cap) <= kMaxSmem) break;
+    if (pl.stages == 1) return DSA_ERR_UNSUPPORTED;
+  }
+  if (allow_smem(kern, kMaxSmem) != cudaSuccess) return DSA_ERR_CUDA;
+  kern<<<ctas, kThreads, L::bytes(pl.stages, p.nblk, pl.cap), st>>>(maps, p,
+                                                                    pl);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t attn_q8_step_workspace_bytes(int D) {
+  return 256 + (size_t)kMaxCtas * 2 * 32 * (D + 1) * sizeof(float);
+}
+
+int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
+                     cudaStream_t st) {
+  StepPlan pl{};
+  pl.all = p.topk == 0;
+  pl.rows = pl.all ? p.S * p.G : p.G;
+  const int mt = pl.rows > 16 ? 2 : 1;
+  pl.tiles = (pl.rows + 16 * mt - 1) / (16 * mt);
+  const long long items = (long long)pl.tiles * p.Hk * (pl.all ? 1 : p.S);
+  if (items * p.B >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
+  pl.items_b = (int)items;
+  pl.box = p.blk >= 32 ? 32 : 16;
+  if (!pl.all) {
+    const long long most = (long long)p.topk + p.local;
+    pl.cap = (int)(most < p.nblk ? most : p.nblk);
+  }
+  char *ws = static_cast<char *>(workspace);
+  pl.done = reinterpret_cast<uint32_t *>(ws + kDoneOffset);
+  pl.part_l = reinterpret_cast<float *>(ws + 256);
+  pl.part_o = pl.part_l + kMaxCtas * 2 * 32;
+  Maps8 maps;
+  const Q8Cache &c = p.c;
+  int rc = encode_kv8(&maps.k, c.k, p.D, pl.box, c.page_size, c.k_t, p.Hk,
+                      c.k_h, c.num_pages, c.k_p);
+  if (rc != DSA_OK) return rc;
+  rc = encode_kv8(&maps.v, c.v, p.D, pl.box, c.page_size, c.v_t, p.Hk, c.v_h,
+                  c.num_pages, c.v_p);
+  if (rc != DSA_OK) return rc;
+  const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+  if (p.D == 64)
+    return mt == 1 ? launch<64, 1>(p, pl, maps, ctas, st)
+                   : launch<64, 2>(p, pl, maps, ctas, st);
+  return mt == 1 ? launch<128, 1>(p, pl, maps, ctas, st)
+                 : launch<128, 2>(p, pl, maps, ctas, st);
+}
+
+}  // namespace dsa
