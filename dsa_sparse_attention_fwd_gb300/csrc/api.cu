@@ -199,6 +199,8 @@ int encode_kv(CUtensorMap *m, const void *base, int D, int rows,
 
 // TMA map of e4m3 keys or values as (d, token, head, page) with a box of D x
 // `rows` tokens, a row of shared memory D = 128 or 64 bytes, swizzled over it.
+// (No more than a row is brought into L2: its neighbour in memory is another
+// head's, which another CTA reads at another time.)
 int encode_kv8(CUtensorMap *m, const void *base, int D, int rows,
                long long tokens, long long st, long long heads, long long sh,
                long long outer, long long sx) {
@@ -218,7 +220,8 @@ int encode_kv8(CUtensorMap *m, const void *base, int D, int rows,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                            : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  D == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                           : CU_TENSOR_MAP_L2_PROMOTION_NONE,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? DSA_OK : DSA_ERR_UNSUPPORTED;
 }

@@ -41,7 +41,8 @@ namespace dsa {
 namespace {
 
 constexpr int kWarps = 8;                      // that multiply
-constexpr int kThreads = kWarps * 32 + 32;     // and the producer
+constexpr int kFeeders = 4;                    // warps that load for them
+constexpr int kThreads = (kWarps + kFeeders) * 32;
 constexpr int kKeys = 32;                      // of a step
 constexpr int kPitch = 36;                     // floats of a row in the join
 // A CTA's slice has at least so many steps: one a warp.
@@ -211,8 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
 
-  if (warp == kWarps) {
-    // ---------------- producer ----------------
+  if (warp >= kWarps) {
+    // ---------------- the warps that load ----------------
+    // Each serves two of the eight; all walk the slice together.
+    constexpr int kServe = kWarps / kFeeders;
+    const int fw = warp - kWarps, ft = tid - kWarps * 32;
     // the sequences' steps, and this CTA's slice of them all
     const int per = (p.B + 31) / 32;
     long long mine = 0;
@@ -246,9 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       b = src * per;
       w_b = __shfl_sync(0xffffffffu, before, src);
     }
-    int entry = 0, g = 0;
+    int entry = 0, g0 = 0;  // items, and steps before this item's
     bool bad = false, ok = true;
-    while (ok && w < u1) {
+    while (w < u1) {
       const long long U = steps_bound(p, pl, b);
       if (w - w_b >= U * pl.items_b) {
         w_b += U * pl.items_b;
@@ -270,24 +274,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                      (min(pl.rows, (tile + 1) * kRows) - 1) / p.G);
         units = max(0, sp.hi - sp.lo + pl.box) / pl.box;
       } else {
+        // (the list of the item before has been read by all)
+        if (named_bar_or(2, kFeeders * 32, !ok)) break;
         sp = span_of(p, b, s, s);
         const long long pos = row_pos(p.q_pos, b, s);
         const int32_t *ids = row_ids(p, b, s, hk);
         const int words = (p.nblk + 31) / 32, n_cand = p.topk + p.local;
-        for (int i = lane; i < words; i += 32) bitmap[i] = 0u;
-        __syncwarp();
-        for (int i0 = lane; i0 < n_cand; i0 += 128) {
-          int n[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            n[u] = i0 + u * 32 < n_cand
-                       ? candidate(p, ids, pos, i0 + u * 32, bad)
-                       : -1;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (n[u] >= 0) atomicOr(bitmap + (n[u] >> 5), 1u << (n[u] & 31));
+        for (int i = ft; i < words; i += kFeeders * 32) bitmap[i] = 0u;
+        named_bar_sync(2, kFeeders * 32);
+        for (int i = ft; i < n_cand; i += kFeeders * 32) {
+          const int n = candidate(p, ids, pos, i, bad);
+          if (n >= 0) atomicOr(bitmap + (n >> 5), 1u << (n & 31));
         }
-        __syncwarp();
+        named_bar_sync(2, kFeeders * 32);
+        // ascending; every warp counts, the first one writes
         int count = 0;
         for (int i0 = 0; i0 < words; i0 += 32) {
           uint32_t m = i0 + lane < words ? bitmap[i0 + lane] : 0u;
@@ -299,47 +299,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const int sum = __shfl_sync(0xffffffffu, to, 31);
           to += count - mn;
-          for (; m; m &= m - 1)
-            list[to++] = (uint16_t)((i0 + lane) * 32 + __ffs(m) - 1);
+          if (fw == 0)
+            for (; m; m &= m - 1)
+              list[to++] = (uint16_t)((i0 + lane) * 32 + __ffs(m) - 1);
           count += sum;
         }
-        __syncwarp();
+        named_bar_sync(2, kFeeders * 32);
         units = count << (p.lb - (pl.box == 32 ? 5 : 4));
       }
       const int per_step = kKeys / pl.box;
       const int steps = (units + per_step - 1) / per_step;
       const int t0 = (int)(steps * x0 / U), t1 = (int)(steps * x1 / U);
-      // tell the others
-      if (!__all_sync(0xffffffffu, wait_bar(item_empty(entry & 1),
-                                            (entry >> 1 & 1) ^ 1, abort_flag,
-                                            p.status))) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        Entry &e = entries[entry & 1];
-        e.n = t1 - t0;
-        e.g0 = g;
-        e.b = b, e.hk = hk, e.s = s, e.tile = tile;
-        e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
-        e.c0 = e.c1 = (int)cta;
-        if (e.slot >= 0) {
-          e.c0 = x0 == 0 ? (int)cta : holder(w_i);
-          e.c1 = x1 == U ? (int)cta : holder(w_i + U - 1);
+      const int g1 = g0 + t1 - t0;
+      if (fw == 0) {  // tell the others
+        ok = __all_sync(0xffffffffu,
+                        ok && wait_bar(item_empty(entry & 1),
+                                       (entry >> 1 & 1) ^ 1, abort_flag,
+                                       p.status));
+        if (ok && lane == 0) {
+          Entry &e = entries[entry & 1];
+          e.n = t1 - t0;
+          e.g0 = g0;
+          e.b = b, e.hk = hk, e.s = s, e.tile = tile;
+          e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
+          e.c0 = e.c1 = (int)cta;
+          if (e.slot >= 0) {
+            e.c0 = x0 == 0 ? (int)cta : holder(w_i);
+            e.c1 = x1 == U ? (int)cta : holder(w_i + U - 1);
+          }
+          mbar_arrive(item_full(entry & 1));
         }
-        mbar_arrive(item_full(entry & 1));
+        __syncwarp();
       }
-      __syncwarp();
       ++entry;
-      // 16 steps at a time: lane 2 i + j holds the 16 keys j of step i
+      // 16 steps of this warp's at a time: lane 2 i + j holds the 16 keys j of
+      // the i-th; those of steps are g = 8 n + kServe fw + 0, 1
+      auto step_of = [&](int k) {
+        return (k / kServe) * kWarps + fw * kServe + k % kServe;
+      };
       struct Look {
         int page, off, j0, seen;
         float ks, vs;
       };
-      auto look = [&](int t) {
+      const int k0 = g0 / kWarps * kServe;
+      const int k1 = (g1 + kWarps - 1) / kWarps * kServe;
+      auto look = [&](int k) {
         Look r{-1, 0, 0, 0, 1.f, 1.f};
-        const int step = t + (lane >> 1), sub = lane & 1;
-        if (step >= t1) return r;
+        const int g = step_of(k + (lane >> 1)), sub = lane & 1;
+        if (g < g0 || g >= g1) return r;
+        const int step = t0 + g - g0;
         const int unit = pl.box == 32 ? step : 2 * step + sub;
         if (unit >= units) return r;
         if (pl.all) {
@@ -366,12 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return r;
       };
-      Look next = look(t0);
-      for (int t = t0; ok && t < t1; t += 16) {
+      Look next = look(k0);
+      for (int k = k0; ok && k < k1; k += 16) {
         const Look cur = next;
-        if (t + 16 < t1) next = look(t + 16);
-        const Sub mine_s{q8_exp(cur.ks), q8_exp(cur.vs), cur.j0, cur.seen};
-        for (int i = 0; i < 16 && t + i < t1; ++i, ++g) {
+        if (k + 16 < k1) next = look(k + 16);
+        const Sub sub_s{q8_exp(cur.ks), q8_exp(cur.vs), cur.j0, cur.seen};
+        for (int i = 0; i < 16; ++i) {
+          const int g = step_of(k + i);
+          if (g < g0) continue;
+          if (g >= g1) break;
           const int wp = g % kWarps, turn = g / kWarps;
           const int st = turn % NS;
           if (!__all_sync(0xffffffffu,
@@ -381,17 +392,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           // lanes 2 i and 2 i + 1 hold this step's keys
-          const int page0 = __shfl_sync(0xffffffffu, cur.page, 2 * i);
-          const int page1 = __shfl_sync(0xffffffffu, cur.page, 2 * i + 1);
-          if ((lane >> 1) == i) subs[(wp * NS + st) * 2 + (lane & 1)] = mine_s;
-          const int n_box = pl.box == 32 ? (page0 >= 0) * 2
-                                         : (page0 >= 0) + (page1 >= 0);
+          const unsigned there = __ballot_sync(0xffffffffu, cur.page >= 0);
+          const bool here = (lane >> 1) == i;
+          if (here) subs[(wp * NS + st) * 2 + (lane & 1)] = sub_s;
+          const unsigned two = there >> (2 * i) & 3u;
+          const int n_box = pl.box == 32 ? (two & 1u) * 2 : __popc(two);
           __syncwarp();
           if (lane == 2 * i)
             mbar_arrive_expect_tx(full(wp, st), n_box * 2 * 16 * D);
           __syncwarp();
-          if ((lane >> 1) == i && cur.page >= 0 &&
-              (pl.box == 16 || lane == 2 * i)) {
+          if (here && cur.page >= 0 && (pl.box == 16 || lane == 2 * i)) {
             const uint32_t dst = stage(wp, st) + (lane & 1) * 16 * D;
             tma_load_4d(dst, &maps.k, full(wp, st), 0, cur.off, hk, cur.page);
             tma_load_4d(dst + kKeys * D, &maps.v, full(wp, st), 0, cur.off, hk,
@@ -399,12 +409,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      g0 = g1;
+      if (pl.all && !ok) break;
     }
     if (bad) atomicOr(p.status, kStatusIndexRange);
     // no more
-    if (ok && __all_sync(0xffffffffu,
-                         wait_bar(item_empty(entry & 1), (entry >> 1 & 1) ^ 1,
-                                  abort_flag, p.status))) {
+    if (fw == 0 && ok &&
+        __all_sync(0xffffffffu,
+                   wait_bar(item_empty(entry & 1), (entry >> 1 & 1) ^ 1,
+                            abort_flag, p.status))) {
       if (lane == 0) {
         entries[entry & 1].n = -1;
         mbar_arrive(item_full(entry & 1));
