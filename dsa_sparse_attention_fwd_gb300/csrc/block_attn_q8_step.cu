@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   : j == 1 ? kw[n].y
                                   : j == 2 ? kw[n].z
                                            : kw[n].w;
-              const uint32_t b0 = q8_half2(wd & 0xffffu);
-              const uint32_t b1 = q8_half2(wd >> 16);
+              uint32_t b0, b1;
+              q8_half4(wd, b0, b1);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) mma_f16(x[mt][n], a[mt], b0, b1);
             }
@@ -688,10 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t sel = h ? 0x7362u : 0x5140u;
               const uint32_t w0 = __byte_perm(vw[0][i], vw[1][i], sel);
               const uint32_t w1 = __byte_perm(vw[2][i], vw[3][i], sel);
-              const uint32_t b00 = q8_half2(w0 & 0xffffu);
-              const uint32_t b01 = q8_half2(w1 & 0xffffu);
-              const uint32_t b10 = q8_half2(w0 >> 16);
-              const uint32_t b11 = q8_half2(w1 >> 16);
+              uint32_t b00, b01, b10, b11;
+              q8_half4(w0, b00, b10);
+              q8_half4(w1, b01, b11);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
                 mma_f16(o[mt][i * 4 + 2 * h], pa[mt][u], b00, b01);

@@ -82,6 +82,14 @@ __device__ __forceinline__ uint32_t q8_half2(uint32_t w) {
       : "r"(w));
   return r;
 }
+// Four e4m3 as two pairs of fp16.
+__device__ __forceinline__ void q8_half4(uint32_t w, uint32_t &lo,
+                                         uint32_t &hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 __device__ __forceinline__ float2 q8_float2(uint32_t w) {
   const uint32_t h = q8_half2(w);
   float2 r;
