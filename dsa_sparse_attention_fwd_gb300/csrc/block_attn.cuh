@@ -55,7 +55,8 @@ __device__ __forceinline__ const int32_t *row_ids(const BlockAttn &p, int b,
 // table names none (`bad`).
 __device__ __forceinline__ int block_page(const BlockAttn &p, int b, int n,
                                           bool &bad) {
-  const int pg = (int)((long long)n * p.blk / p.page_size);
+  // (below 2^31: the table names fewer tokens)
+  const int pg = (int)((unsigned)n * (unsigned)p.blk / (unsigned)p.page_size);
   const int page = __ldg(p.table + (long long)b * p.max_pages + pg);
   if (page >= 0 && page < p.num_pages) return page;
   bad = true;

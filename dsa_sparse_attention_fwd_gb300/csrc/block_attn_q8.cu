@@ -12,30 +12,6 @@ namespace {
 // Rows of a sequence and key head that take the kernel for few rows.
 bool few_rows(int S, int G) { return (long long)S * G <= 64; }
 
-// One warp a row.
-__global__ void __launch_bounds__(128) attn_q8_rows_kernel(
-    const __grid_constant__ BlockAttnQ8 p) {
-  __shared__ float qs[4][128];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long rows = (long long)p.S * p.B * p.H;
-  for (long long r = (long long)blockIdx.x * 4 + warp; r < rows;
-       r += (long long)gridDim.x * 4) {
-    const int h = (int)(r % p.H), b = (int)(r / p.H % p.B);
-    const int s = (int)(r / p.H / p.B);
-    __syncwarp();
-    for (int d = lane; d < p.D; d += 32)
-      qs[warp][d] = __bfloat162float(p.q[r * p.D + d]);
-    __syncwarp();
-    float acc[4], lse;
-    bool bad = false;
-    attn_row_q8(p, b, s, h / p.G, qs[warp], lane, bad, acc, lse);
-    if (bad) atomicOr(p.status, kStatusIndexRange);
-    for (int i = 0; i * 32 < p.D; ++i)
-      p.o[r * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
-    if (lane == 0) p.lse[r] = lse;
-  }
-}
-
 }  // namespace
 }  // namespace dsa
 
@@ -47,7 +23,9 @@ size_t dsa_block_attn_q8_workspace_size(int S, int B, int H, int Hk, int D,
   if (S <= 0 || B <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || D <= 0 ||
       T <= 0 || block_size <= 0 || topk < 0 || local_blocks < 0)
     return 0;
-  return dsa::few_rows(S, H / Hk) ? dsa::attn_q8_step_workspace_bytes(D) : 256;
+  if (dsa::few_rows(S, H / Hk)) return dsa::attn_q8_step_workspace_bytes(D);
+  return dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
+                                       local_blocks);
 }
 
 int dsa_block_attn_paged_q8_fwd(
@@ -93,11 +71,8 @@ int dsa_block_attn_paged_q8_fwd(
   if (dsa::few_rows(S, p.G))
     return dsa::run_attn_q8_step(p, workspace, num_sms,
                                  static_cast<cudaStream_t>(cuda_stream));
-  const long long grid = ((long long)S * B * H + 3) / 4;
-  const long long most = 16ll * num_sms;
-  dsa::attn_q8_rows_kernel<<<(unsigned)(grid < most ? grid : most), 128, 0,
-                             static_cast<cudaStream_t>(cuda_stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return dsa::run_attn_q8_tile(p, workspace, num_sms,
+                               static_cast<cudaStream_t>(cuda_stream));
 }
 
 }  // extern "C"

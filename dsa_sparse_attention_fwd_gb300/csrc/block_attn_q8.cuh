@@ -18,12 +18,16 @@ size_t attn_q8_step_workspace_bytes(int D);
 int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
                      cudaStream_t st);
 
+// Many (block_attn_q8_tile.cu); workspace as for dsa_block_attn_fwd().
+int run_attn_q8_tile(const BlockAttnQ8 &p, void *workspace, int num_sms,
+                     cudaStream_t st);
+
 // One row by one warp in fp32 on the CUDA cores: a running maximum and sum
 // over its keys, 32 at a time, lane l holding one.  Rows whose fast result is
 // not finite are computed again by it: a key that only other rows of a tile
 // see may hold anything.  qs: the query as fp32 in shared memory, this
 // warp's own copy; lane l returns o[l + 32 i] in acc[i].
-static __device__ __noinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
+__device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
                                                 int s, int hk, const float *qs,
                                                 int lane, bool &bad,
                                                 float (&acc)[4], float &lse) {
@@ -43,7 +47,8 @@ static __device__ __noinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
     if (__any_sync(0xffffffffu, again)) continue;
     const int page = block_page(p, b, n, bad);
     if (page < 0) continue;
-    const int off0 = (int)((long long)n * p.blk % p.page_size);
+    const int off0 =
+        (int)((unsigned)n * (unsigned)p.blk % (unsigned)p.page_size);
     for (int c = 0; c < p.blk; c += 32) {
       const int jj = c + lane;
       const long long j = (long long)n * p.blk + jj;

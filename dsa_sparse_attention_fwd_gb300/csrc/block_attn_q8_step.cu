@@ -150,6 +150,22 @@ __device__ __forceinline__ long long steps_bound(const BlockAttnQ8 &p,
   return max(1ll, (keys + kKeys - 1) / kKeys);
 }
 
+// Out of line: it is rare.
+__device__ __noinline__ void redo_row(const BlockAttnQ8 &p, int b, int s,
+                                      int hk, long long at, float *qs,
+                                      int lane) {
+  __syncwarp();
+  for (int d = lane; d < p.D; d += 32)
+    qs[d] = __bfloat162float(p.q[at * p.D + d]);
+  __syncwarp();
+  float acc[4], lse;
+  bool bad = false;
+  attn_row_q8(p, b, s, hk, qs, lane, bad, acc, lse);
+  for (int i = 0; i * 32 < p.D; ++i)
+    p.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
+  if (lane == 0) p.lse[at] = lse;
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_q8_step_kernel(const __grid_constant__ Maps8 maps,
@@ -883,17 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k % kWarps != warp) continue;
           const long long to = row_at(__ffs(left) - 1);
           const int rr = first + __ffs(left) - 1;
-          __syncwarp();
-          for (int d = lane; d < D; d += 32)
-            qs[d] = __bfloat162float(p.q[to * D + d]);
-          __syncwarp();
-          float acc[4], lse;
-          bool bad = false;
-          attn_row_q8(p, e.b, pl.all ? rr / p.G : e.s, e.hk, qs, lane, bad,
-                      acc, lse);
-          for (int i = 0; i * 32 < D; ++i)
-            p.o[to * D + lane + 32 * i] = __float2bfloat16(acc[i]);
-          if (lane == 0) p.lse[to] = lse;
+          redo_row(p, e.b, pl.all ? rr / p.G : e.s, e.hk, to, qs, lane);
         }
       }
       named_bar_sync(1, kWarps * 32);
