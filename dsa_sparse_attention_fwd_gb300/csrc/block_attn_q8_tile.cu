@@ -227,16 +227,18 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
   // a step takes units of up to 64 keys: whole blocks, or halves of 128
   const int count = *sCount;
-  const int unit = min(p.blk, kKeys), per = p.blk / unit;
-  const int upt = kKeys / unit, units = count * per;
-  const int all = (units + upt - 1) / upt;
+  const int lu = min(p.lb, 6), lper = p.lb - lu;  // logarithms of a unit's
+  const int lupt = 6 - lu;                        // keys, a block's and a
+  const int units = count << lper;                // step's units
+  const int all = (units + (1 << lupt) - 1) >> lupt;
   const int t0 = (int)((long long)all * split / pl.splits);
   const int t1 = (int)((long long)all * (split + 1) / pl.splits);
   const int n = t1 - t0;
-  // first key of key x (of 64) of step t's unit; -1 behind the last one
+  // key x (of 64) of step t's units, the last one instead of those behind it
   auto key_at = [&](int t, int x) {
-    const int u = t * upt + x / unit;
-    return u < units ? list[u / per] * p.blk + u % per * unit + x % unit : -1;
+    const int u = min((t << lupt) + (x >> lu), units - 1);
+    return ((int)list[u >> lper] << p.lb) + ((u & ((1 << lper) - 1)) << lu) +
+           (x & ((1 << lu) - 1));
   };
   // the last key that any row of the tile sees
   const int pos_hi = key_pos(p, b, s0 + nq - 1);
@@ -256,8 +258,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         if (lane >= 4 || i >= n) return r;
         // a ragged step's end repeats the last unit's keys: their scores are
         // masked, but have to be numbers (its values become zeros)
-        const int x = min((t0 + i) * upt + lane * 16 / unit, units - 1);
-        const int j = list[x / per] * p.blk + x % per * unit + lane * 16 % unit;
+        const int j = key_at(t0 + i, lane * 16);
         const int pg = j / p.page_size;
         r.off = j - pg * p.page_size;
         // (blocks without a page are not listed)
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       for (int i = 0; i < n; ++i) {
         const Look cur = next;
         next = look(i + 1);
-        const bool loads = lane < 4 && lane * 16 % unit == 0;
+        const bool loads = lane < 4 && (lane * 16 & ((1 << lu) - 1)) == 0;
         if (lane < 4)
           meta[(i % kMeta) * 4 + lane] = make_int2(q8_exp(cur.ks), q8_exp(cur.vs));
         __syncwarp();
@@ -346,8 +347,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     for (int i = 0; i < n; ++i) {
       const int st = i % NV;
       const uint32_t ph = i / NV & 1u;
-      const int j = key_at(t0 + i, row);
-      const bool zero = j < 0 || j > pos_hi;  // values that no row sees
+      // values that no row sees
+      const bool zero = ((t0 + i) << lupt) + (row >> lu) >= units ||
+                        key_at(t0 + i, row) > pos_hi;
       if (!__all_sync(0xffffffffu, wait_bar_rest_inl(v8_full(st), ph, abort_flag,
                                                  p.status)))
         goto done;
