@@ -18,6 +18,10 @@ struct AppendQ8 {
   Q8Cache c;
   const int32_t *start, *count;  // [B]; count nullptr: all S rows
   int groups;                    // groups that a sequence's rows can reach
+  unsigned kv;                   // CTAs that take keys and values
+  bool by_warp;                  // a warp an item, else a CTA
+  int heads;                     // of a CTA's item
+  int angles;                    // angles of a warp's, in shared memory
 };
 
 // The rows of a sequence that are appended: [0, n).
@@ -26,133 +30,302 @@ __device__ __forceinline__ int rows_of(const AppendQ8 &p, int b, int start) {
   return start < 0 ? 0 : min(max(n, 0), p.a.S);
 }
 
-// A row's values, normed and rotated, into y[0 .. D) of shared memory; one
-// warp.
-__device__ __forceinline__ void turned_row(const RopeArgs &a, const RopeRows &r,
-                                           const __nv_bfloat16 *x, bool turn,
-                                           long long pos, float *n, float *y,
-                                           int lane) {
-  float sq = 0.f;
-  for (int e = lane; e < a.D; e += 32) {
-    n[e] = __bfloat162float(x[e]);
-    sq = fmaf(n[e], n[e], sq);
-  }
-  if (turn && r.w) {
-    for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    const float rstd = rsqrtf(sq / a.D + a.eps);
-    for (int e = lane; e < a.D; e += 32) n[e] = n[e] * rstd * __ldg(r.w + e);
-  }
-  __syncwarp();
-  for (int e = lane; e < a.D; e += 32) {
-    const int rel = e - a.r0;
-    float v = n[e];
-    if (turn && rel >= 0 && rel < a.R) {
-      const bool first = a.interleaved ? (rel & 1) == 0 : rel < a.R / 2;
-      const int i = a.interleaved ? rel >> 1 : rel % (a.R / 2);
-      const int o = a.r0 + (a.interleaved ? rel ^ 1
-                            : first       ? rel + a.R / 2
-                                          : rel - a.R / 2);
-      double t = a.inv_freq[i] * 0.15915494309189535;
-      t -= floor(t);
-      const unsigned long long ph =
-          (unsigned long long)pos * __double2ull_rn(t * 18446744073709551616.0);
-      float sn, co;
-      sincospif((float)(int)(unsigned)(ph >> 32) * 4.656612873077393e-10f, &sn,
-                &co);
-      v = a.mscale * (first ? v * co - n[o] * sn : n[o] * sn + v * co);
-    }
-    y[e] = v;
-  }
-  __syncwarp();
+// cos and sin (times m) of an angle of pos * fr turns: the top 32 bits of the
+// fraction, rounded to fp32, and what that rounds off as a first-order term.
+// A code of the cache may be a whole step off where its value falls on the
+// border between two: the fewer, the closer the angle.
+__device__ __forceinline__ float2 turn_of(const RopeArgs &a, long long pos,
+                                          unsigned long long fr) {
+  const int t = (int)(((unsigned long long)pos * fr) >> 32);
+  const float x = (float)t;
+  const float d = (float)(t - (int)x) * 1.4629180792671596e-9f;  // pi 2^-31
+  float sn, co;
+  sincospif(x * 4.656612873077393e-10f, &sn, &co);
+  return make_float2(a.mscale * fmaf(-sn, d, co), a.mscale * fmaf(co, d, sn));
 }
 
-// One warp an item: a query row, or a (group, head) of keys or values.
-__global__ void __launch_bounds__(128) append_q8_kernel(const AppendQ8 p) {
-  __shared__ float sn[4][256], sy[4][256];
+// Keys or values of one group and head by `nw` warps (one, or the CTA's four):
+// rows s0 .. s0 + n - 1 of the sequence go to the group's tokens from `to` on,
+// `early` tokens before them are there already.  A thread holds 8 neighbouring
+// values of up to RW rows as they came, and works them out twice, for the
+// scale and for the codes: that costs less than fp32 registers for them.
+template <bool VEC, int LPR, int RW, bool KEYS>
+__device__ __forceinline__ void store_group(
+    const AppendQ8 &p, const RopeRows &r, int nw, const __nv_bfloat16 *src,
+    int n, int early, uint8_t *group_at, long long st, float *scale, int e0, int sub,
+    int unit, Turn<__nv_bfloat16, VEC> &turn, const float2 *cs, const float *w,
+    float *buf, float *red) {
+  constexpr int RPW = 32 / LPR;
+  const RopeArgs &a = p.a;
+  const bool norm = KEYS && r.w != nullptr;
+  const int half = a.R / 2;
+  Chunk<__nv_bfloat16, VEC> x[RW];
+#pragma unroll
+  for (int u = 0; u < RW; ++u) {
+    const int row = (u * nw + unit) * RPW + sub;
+    if (u * nw * RPW >= n) break;  // (the same for all warps)
+    x[u].load(src + row * r.ss, e0, row < n ? a.D : 0);
+  }
+  auto values = [&](int u, float2 (&y)[4]) {
+    asm volatile("" ::: "memory");  // one row's coefficients at a time
+    const int row = (u * nw + unit) * RPW + sub;
+    if constexpr (KEYS) {
+      float2 v[4];
+      x[u].get(v);
+      const float sq = squares(v);
+      turn.set(a, e0, false, cs + (row < n ? row : 0) * half,
+               norm ? w : nullptr);
+      turn.apply(a, x[u], v, y, e0, buf, sq < 3e38f);
+      if (norm) {
+        const float r2 = rsqrtf(row_sum<LPR>(sq) * (1.f / a.D) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          y[i] = __fmul2_rn(y[i], make_float2(r2, r2));
+      }
+    } else {
+      x[u].get(y);
+    }
+  };
+  const float had = early > 0 ? *scale : 0.f;
+  float top = 0.f;
+#pragma unroll
+  for (int u = 0; u < RW; ++u) {
+    if (u * nw * RPW >= n) break;
+    const int row = (u * nw + unit) * RPW + sub;
+    float2 y[4];
+    values(u, y);
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      t = fmaxf(t, fmaxf(q8_mag(y[i].x), q8_mag(y[i].y)));
+    // (padding of the last rows may hold what eps = 0 makes of zeros)
+    if (row < n && e0 < a.D) top = fmaxf(top, t);
+  }
+  // non-negative floats compare as integers
+  top = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(top)));
+  if (nw > 1) {
+    if ((threadIdx.x & 31) == 0) red[unit] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kRopeWarps; ++i) top = fmaxf(top, red[i]);
+  }
+  __syncwarp();
+  int e = q8_exp_for(top);
+  if (early > 0) {
+    const int e_old = q8_exp(had);
+    if (e > e_old && e0 < a.D) {
+      const float f = q8_pow2(e_old - e);
+      for (int t = unit * RPW + sub; t < early; t += nw * RPW) {
+        uint2 *at = reinterpret_cast<uint2 *>(group_at + t * st + e0);
+        const uint2 c = *at;
+        const float2 v0 = q8_float2(c.x & 0xffffu), v1 = q8_float2(c.x >> 16);
+        const float2 v2 = q8_float2(c.y & 0xffffu), v3 = q8_float2(c.y >> 16);
+        *at = make_uint2(q8_pack4(v0.x * f, v0.y * f, v1.x * f, v1.y * f),
+                         q8_pack4(v2.x * f, v2.y * f, v3.x * f, v3.y * f));
+      }
+    }
+    e = max(e, e_old);
+  }
+  if (unit == 0 && (threadIdx.x & 31) == 0) *scale = q8_pow2(e);
+  const float inv = q8_pow2(-e);
+#pragma unroll
+  for (int u = 0; u < RW; ++u) {
+    if (u * nw * RPW >= n) break;
+    const int row = (u * nw + unit) * RPW + sub;
+    float2 y[4];
+    values(u, y);
+    if (row < n && e0 < a.D)
+      *reinterpret_cast<uint2 *>(group_at + (early + row) * st + e0) =
+          make_uint2(q8_pack4(y[0].x * inv, y[0].y * inv, y[1].x * inv,
+                              y[1].y * inv),
+                     q8_pack4(y[2].x * inv, y[2].y * inv, y[3].x * inv,
+                              y[3].y * inv));
+  }
+}
+
+// CTAs 0 .. kv - 1 take keys and values, the others queries as
+// norm_rope_kernel() does.  Keys and values: an item is a group that a
+// sequence's rows can reach and one head (by a warp, where a group gets few new
+// rows) or several (by a CTA, the angles of the group's tokens in shared
+// memory for all of them).
+template <bool VEC, int LPR, int RW>
+__global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
+    append_q8_kernel(const __grid_constant__ AppendQ8 p) {
+  constexpr int RPW = 32 / LPR;
+  using T = __nv_bfloat16;
+  __shared__ __align__(16) float xch[VEC ? 1 : kRopeWarps * RPW * LPR * 8];
+  __shared__ unsigned long long fr[kRopeMaxD / 2];
+  __shared__ __align__(16) float sw[2][kRopeMaxD];
+  __shared__ float red[2][kRopeWarps];
+  extern __shared__ __align__(16) float2 angles[];
   const RopeArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float *n = sn[warp], *y = sy[warp];
-  const long long qrows = (long long)a.S * a.B * a.q.heads;
-  const long long kv = (long long)p.groups * a.B * a.k.heads * 2;
-  for (long long it = (long long)blockIdx.x * 4 + warp; it < qrows + kv;
-       it += (long long)gridDim.x * 4) {
-    if (it < qrows) {
-      const int h = (int)(it % a.q.heads);
-      const long long tok = it / a.q.heads;
-      const int s = (int)(tok / a.B), b = (int)(tok % a.B);
-      const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.q.in) +
-                               s * a.q.ss + b * a.q.sb + h * a.q.sh;
-      turned_row(a, a.q, x, true, (long long)__ldg(p.start + b) + s, n, y,
-                 lane);
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.q.out) + it * a.D;
-      for (int e = lane; e < a.D; e += 32) out[e] = __float2bfloat16(y[e]);
-      __syncwarp();
-      continue;
-    }
-    long long r = it - qrows;
-    const bool is_v = r & 1;
-    r >>= 1;
-    const int h = (int)(r % a.k.heads);
-    r /= a.k.heads;
-    const int b = (int)(r % a.B), gi = (int)(r / a.B);
-    const int start = __ldg(p.start + b);
-    const int rows = rows_of(p, b, start);
-    const long long g0 = ((long long)(start >> p.c.lg) + gi) << p.c.lg;
-    const int s0 = (int)max(g0 - start, 0ll);
-    const int s1 = (int)min(g0 + p.c.group - start, (long long)rows);
-    if (s0 >= s1) continue;
-    bool bad = false;
-    const int page = q8_page(p.c, b, g0, bad);
-    if (bad) {
-      if (lane == 0) atomicOr(a.status, kStatusIndexRange);
-      continue;
-    }
-    const int off = (int)(g0 % p.c.page_size);
-    const RopeRows &in = is_v ? a.v : a.k;
-    const __nv_bfloat16 *src =
-        static_cast<const __nv_bfloat16 *>(in.in) + b * in.sb + h * in.sh;
-    uint8_t *dst = (is_v ? p.c.v + page * p.c.v_p + h * p.c.v_h
-                         : p.c.k + page * p.c.k_p + h * p.c.k_h);
-    const long long st = is_v ? p.c.v_t : p.c.k_t;
-    float *scale = (is_v ? p.c.vs : p.c.ks) + q8_scale_at(p.c, page, off, h);
-    float top = 0.f;
-    for (int s = s0; s < s1; ++s) {
-      turned_row(a, in, src + s * in.ss, !is_v, (long long)start + s, n, y,
-                 lane);
-      for (int e = lane; e < a.D; e += 32) top = fmaxf(top, q8_mag(y[e]));
-      __syncwarp();
-    }
-    for (int o = 16; o; o >>= 1)
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    int e = q8_exp_for(top);
-    const int early = (int)max((long long)start - g0, 0ll);
-    if (early > 0) {
-      const int e0 = q8_exp(*scale);
-      if (e > e0) {
-        const float f = q8_pow2(e0 - e);
-        for (int t = 0; t < early; ++t)
-          for (int d = lane * 2; d < a.D; d += 64) {
-            uint16_t *at =
-                reinterpret_cast<uint16_t *>(dst + (off + t) * st + d);
-            const float2 v = q8_float2(*at);
-            *at = (uint16_t)q8_pack2(v.x * f, v.y * f);
-          }
-      }
-      e = max(e, e0);
-    }
-    __syncwarp();
-    if (lane == 0) *scale = q8_pow2(e);
-    const float inv = q8_pow2(-e);
-    for (int s = s0; s < s1; ++s) {
-      turned_row(a, in, src + s * in.ss, !is_v, (long long)start + s, n, y,
-                 lane);
-      uint8_t *row = dst + (off + (start + s - g0)) * st;
-      for (int d = lane * 2; d < a.D; d += 64)
-        *reinterpret_cast<uint16_t *>(row + d) =
-            (uint16_t)q8_pack2(y[d] * inv, y[d + 1] * inv);
-      __syncwarp();
-    }
+  const int sub = lane / LPR, e0 = (lane % LPR) * 8;
+  float *buf = VEC ? xch : xch + (warp * RPW + sub) * LPR * 8;
+  load_weights(a, sw);
+  for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) {
+    double t = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+    t -= floor(t);
+    fr[i] = __double2ull_rn(t * 18446744073709551616.0);
   }
+  const int half = a.R / 2;
+  // lanes outside the rotated part multiply the first coefficients by zero
+  float2 *cs = angles + (blockIdx.x < p.kv && !p.by_warp
+                             ? 0
+                             : warp * p.angles);
+  if (half == 0 && threadIdx.x < kRopeWarps * 8)
+    angles[(threadIdx.x / 8) * p.angles + threadIdx.x % 8] =
+        make_float2(0.f, 0.f);
+  __syncthreads();
+  Turn<T, VEC> turn;
+  turn.init(a, e0, lane, false);
+
+  if (blockIdx.x >= p.kv) {
+    // ---------------- queries ----------------
+    const unsigned items = (unsigned)a.S * a.B * a.chunks;
+    const unsigned stride = (gridDim.x - p.kv) * kRopeWarps;
+    const int nq = a.q.heads;
+    for (unsigned item = (blockIdx.x - p.kv) * kRopeWarps + warp; item < items;
+         item += stride) {
+      const unsigned tk = item / (unsigned)a.chunks;
+      const int s = (int)(tk / (unsigned)a.B), b = (int)(tk % (unsigned)a.B);
+      const int h0 = (int)(item % (unsigned)a.chunks) * a.heads_per_item;
+      const long long pos = (long long)__ldg(p.start + b) + s;
+      __syncwarp();
+      for (int i = lane; i < half; i += 32) cs[i] = turn_of(a, pos, fr[i]);
+      __syncwarp();
+      rope_heads<T, VEC, LPR, 0>(
+          a, a.q, static_cast<const T *>(a.q.in) + s * a.q.ss + b * a.q.sb,
+          static_cast<T *>(a.q.out) + tk * (long long)nq * a.D, a.D, h0,
+          min(h0 + a.heads_per_item, nq), sub, e0, turn, cs, sw[0], buf);
+    }
+    return;
+  }
+  // ---------------- keys and values ----------------
+  const int hc = p.by_warp ? 1 : p.heads;  // heads of an item
+  const int nh = (a.k.heads + hc - 1) / hc;
+  long long it = p.by_warp ? (long long)blockIdx.x * kRopeWarps + warp
+                           : (long long)blockIdx.x;
+  if (it >= (long long)p.groups * a.B * 2 * nh) return;
+  const bool is_v = it & 1;
+  it >>= 1;
+  const int h0 = (int)(it % nh) * hc;
+  it /= nh;
+  const int b = (int)(it % a.B), gi = (int)(it / a.B);
+  const int start = __ldg(p.start + b);
+  const int rows = rows_of(p, b, start);
+  const long long g0 = ((long long)(start >> p.c.lg) + gi) << p.c.lg;
+  const int s0 = (int)max(g0 - start, 0ll);
+  const int s1 = (int)min(g0 + p.c.group - start, (long long)rows);
+  if (s0 >= s1) return;
+  bool bad = false;
+  const int page = q8_page(p.c, b, g0, bad);
+  if (bad) {
+    if (lane == 0) atomicOr(a.status, kStatusIndexRange);
+    return;
+  }
+  const int n = s1 - s0, early = (int)max((long long)start - g0, 0ll);
+  const int off = (int)(g0 % p.c.page_size);
+  if (!is_v && half > 0) {
+    const int nt = p.by_warp ? 32 : kRopeThreads;
+    for (int i = p.by_warp ? lane : threadIdx.x; i < n * half; i += nt) {
+      const int t = i / half;
+      cs[i] = turn_of(a, (long long)start + s0 + t, fr[i - t * half]);
+    }
+    if (p.by_warp)
+      __syncwarp();
+    else
+      __syncthreads();
+  }
+  const RopeRows &in = is_v ? a.v : a.k;
+  const long long st = is_v ? p.c.v_t : p.c.k_t;
+  const int nw = p.by_warp ? 1 : kRopeWarps, unit = p.by_warp ? 0 : warp;
+  for (int h = h0; h < min(h0 + hc, a.k.heads); ++h) {
+    const T *src = static_cast<const T *>(in.in) + b * in.sb + h * in.sh +
+                   s0 * in.ss;
+    uint8_t *at = (is_v ? p.c.v + page * p.c.v_p + h * p.c.v_h
+                        : p.c.k + page * p.c.k_p + h * p.c.k_h) +
+                  off * st;
+    float *scale = (is_v ? p.c.vs : p.c.ks) + q8_scale_at(p.c, page, off, h);
+    float *rd = red[(h - h0) & 1];
+    if (is_v)
+      store_group<VEC, LPR, RW, false>(p, in, nw, src, n, early, at, st, scale,
+                                       e0, sub, unit, turn, cs, sw[1], buf, rd);
+    else
+      store_group<VEC, LPR, RW, true>(p, in, nw, src, n, early, at, st, scale,
+                                      e0, sub, unit, turn, cs, sw[1], buf, rd);
+  }
+}
+
+template <bool VEC, int LPR, int RW>
+int launch_append(AppendQ8 &p, int num_sms, cudaStream_t st) {
+  constexpr int RPW = 32 / LPR;
+  RopeArgs &a = p.a;
+  auto kern = append_q8_kernel<VEC, LPR, RW>;
+  // new rows that a group can get
+  const int most = a.S < p.c.group ? a.S : p.c.group;
+  // by warps where those are two passes of one: single tokens and drafts
+  p.by_warp = most <= 2 * RPW;
+  // angles of the tokens of a group (a warp's, or a CTA's), and of a token of
+  // queries for each warp
+  const int half = a.R / 2 < 8 ? 8 : a.R / 2;
+  p.angles = (p.by_warp ? most : 1) * half;
+  int angles = kRopeWarps * p.angles;
+  if (!p.by_warp && most * half > angles) angles = most * half;
+  const long long groups = 2ll * p.groups * a.B;
+  long long kv;
+  if (p.by_warp) {
+    kv = (groups * a.k.heads + kRopeWarps - 1) / kRopeWarps;
+  } else {
+    // all heads of a group share its angles; fewer where that leaves SMs idle
+    p.heads = a.k.heads;
+    while (p.heads > 1 &&
+           groups * ((a.k.heads + p.heads - 1) / p.heads) < 3ll * num_sms)
+      p.heads = (p.heads + 1) / 2;
+    kv = groups * ((a.k.heads + p.heads - 1) / p.heads);
+  }
+  if (kv >= (1ll << 30)) return DSA_ERR_UNSUPPORTED;
+  p.kv = (unsigned)kv;
+  // queries: as launch_lpr() of norm_rope.cu shares them
+  long long q_ctas = 0;
+  if (a.q.heads > 0) {
+    const long long toks = (long long)a.S * a.B;
+    int per = (a.q.heads + RPW - 1) / RPW * RPW;
+    while (per > RPW &&
+           toks * ((a.q.heads + per - 1) / per) < 32ll * num_sms)
+      per = ((per / 2) + RPW - 1) / RPW * RPW;
+    a.heads_per_item = per;
+    a.chunks = (a.q.heads + per - 1) / per;
+    q_ctas = (toks * a.chunks + kRopeWarps - 1) / kRopeWarps;
+    const long long cap = (RW <= 8 ? 5ll : 3ll) * num_sms;
+    if (q_ctas > cap) q_ctas = cap;
+  }
+  const int smem = angles * (int)sizeof(float2);
+  // (D * group <= 16384, R <= D: 64 KB at most)
+  if (allow_smem(kern, 16384 / 2 * (int)sizeof(float2) + 4096) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  kern<<<(unsigned)(kv + q_ctas), kRopeThreads, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+// RW: rows of a thread that a whole group takes, at most 8 or 16.
+template <bool VEC, int LPR>
+int launch_append_rows(AppendQ8 &p, int num_sms, cudaStream_t st) {
+  constexpr int RPW = 32 / LPR;
+  if (p.c.group <= 8 * kRopeWarps * RPW)
+    return launch_append<VEC, LPR, 8>(p, num_sms, st);
+  return launch_append<VEC, LPR, 16>(p, num_sms, st);
+}
+
+int run_append(AppendQ8 &p, int num_sms, cudaStream_t st) {
+  const RopeArgs &a = p.a;
+  const bool vec = a.r0 % 8 == 0 && a.R % (a.interleaved ? 8 : 16) == 0 &&
+                   vec_rows(a.q, 2, false) && vec_rows(a.k, 2, false) &&
+                   vec_rows(a.v, 2, false);
+  if (!vec) return launch_append_rows<false, 32>(p, num_sms, st);
+  if (a.D <= 64) return launch_append_rows<true, 8>(p, num_sms, st);
+  if (a.D <= 128) return launch_append_rows<true, 16>(p, num_sms, st);
+  return launch_append_rows<true, 32>(p, num_sms, st);
 }
 
 struct ReadQ8 {
@@ -163,50 +336,82 @@ struct ReadQ8 {
   int *status;
 };
 
-// A thread takes 16 values of a row.
-__global__ void __launch_bounds__(256) read_q8_kernel(const ReadQ8 p) {
-  const int ch = p.c.D / 16;
-  const long long per = (long long)p.T * p.B * p.c.Hk * ch;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-       i < 2 * per; i += (long long)gridDim.x * blockDim.x) {
-    const bool is_v = i >= per;
-    __nv_bfloat16 *out = is_v ? p.v : p.k;
-    if (!out) continue;
-    const long long at = is_v ? i - per : i;
-    const int c = (int)(at % ch);
-    const int h = (int)(at / ch % p.c.Hk);
-    const long long row = at / ch / p.c.Hk;
-    const int b = (int)(row % p.B), t = (int)(row / p.B);
-    uint32_t w[8] = {};
-    const int n = p.length ? __ldg(p.length + b) : p.T;
-    if (t < n) {
-      const long long j = (p.first ? (long long)__ldg(p.first + b) : 0) + t;
-      bool bad = false;
-      const int page = q8_page(p.c, b, j, bad);
-      if (bad) {
-        atomicOr(p.status, kStatusIndexRange);
-      } else {
-        const int off = (int)(j % p.c.page_size);
-        const uint8_t *src =
-            is_v ? p.c.v + page * p.c.v_p + off * p.c.v_t + h * p.c.v_h
-                 : p.c.k + page * p.c.k_p + off * p.c.k_t + h * p.c.k_h;
-        const float s = q8_pow2(
-            q8_exp(__ldg((is_v ? p.c.vs : p.c.ks) +
-                         q8_scale_at(p.c, page, off, h))));
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-        const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+// A warp takes kReadRows consecutive tokens of a sequence: their pages are
+// looked up once, and a lane has the loads of all of them in flight, 16 values
+// of one head each.
+constexpr int kReadRows = 8, kReadThreads = 256;
+__global__ void __launch_bounds__(kReadThreads) read_q8_kernel(
+    const __grid_constant__ ReadQ8 p) {
+  const int lane = threadIdx.x & 31;
+  const int ch = p.c.D / 16, pieces = p.c.Hk * ch;
+  const unsigned tiles = (unsigned)((p.T + kReadRows - 1) / kReadRows);
+  const unsigned items = tiles * p.B;
+  const unsigned stride = gridDim.x * (kReadThreads / 32);
+  for (unsigned it = blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5);
+       it < items; it += stride) {
+    const int b = (int)(it / tiles), t0 = (int)(it % tiles) * kReadRows;
+    // lane u: token t0 + u
+    int page = -1, off = 0;
+    {
+      const int t = t0 + lane;
+      const int n = p.length ? __ldg(p.length + b) : p.T;
+      if (lane < kReadRows && t < min(n, p.T)) {
+        const long long j = (p.first ? (long long)__ldg(p.first + b) : 0) + t;
+        bool bad = false;
+        page = q8_page(p.c, b, j, bad);
+        if (bad) atomicOr(p.status, kStatusIndexRange);
+        if (page >= 0) off = (int)((unsigned)j % (unsigned)p.c.page_size);
+      }
+    }
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv) {
+      __nv_bfloat16 *out = kv ? p.v : p.k;
+      if (!out) continue;
+      const uint8_t *in = kv ? p.c.v : p.c.k;
+      const float *scales = kv ? p.c.vs : p.c.ks;
+      const long long sp = kv ? p.c.v_p : p.c.k_p, st = kv ? p.c.v_t : p.c.k_t;
+      const long long sh = kv ? p.c.v_h : p.c.k_h;
+#pragma unroll 1
+      for (int c = lane; c - lane < pieces; c += 32) {
+        const bool mine = c < pieces;  // (whole warps: they exchange pages)
+        const int h = mine ? c / ch : 0, piece = c - h * ch;
+        uint4 x[kReadRows];
+        float s[kReadRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 lo = q8_float2(u[k] & 0xffffu);
-          const float2 hi = q8_float2(u[k] >> 16);
-          w[2 * k] = pack_bf16x2(lo.x * s, lo.y * s);
-          w[2 * k + 1] = pack_bf16x2(hi.x * s, hi.y * s);
+        for (int u = 0; u < kReadRows; ++u) {
+          const int pg = __shfl_sync(0xffffffffu, page, u);
+          const int of = __shfl_sync(0xffffffffu, off, u);
+          x[u] = make_uint4(0u, 0u, 0u, 0u);
+          s[u] = 0.f;
+          if (pg >= 0 && mine) {
+            x[u] = __ldg(reinterpret_cast<const uint4 *>(
+                             in + pg * sp + of * st + h * sh) +
+                         piece);
+            s[u] = __ldg(scales + q8_scale_at(p.c, pg, of, h));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kReadRows; ++u) {
+          if (t0 + u >= p.T || !mine) break;
+          const float f = q8_pow2(q8_exp(s[u]));
+          const uint32_t q[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 lo = q8_float2(q[k] & 0xffffu);
+            const float2 hi = q8_float2(q[k] >> 16);
+            w[2 * k] = pack_bf16x2(lo.x * f, lo.y * f);
+            w[2 * k + 1] = pack_bf16x2(hi.x * f, hi.y * f);
+          }
+          uint4 *to = reinterpret_cast<uint4 *>(
+              out + ((((long long)(t0 + u) * p.B + b) * p.c.Hk + h) * ch +
+                     piece) *
+                        16);
+          __stcs(to, make_uint4(w[0], w[1], w[2], w[3]));
+          __stcs(to + 1, make_uint4(w[4], w[5], w[6], w[7]));
         }
       }
     }
-    uint4 *to = reinterpret_cast<uint4 *>(out + at * 16);
-    to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    to[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
@@ -257,13 +462,7 @@ int dsa_paged_append_q8(
   int num_sms = 0;
   rc = dsa::device_num_sms(&num_sms);
   if (rc != DSA_OK) return rc;
-  const long long items =
-      (long long)S * B * a.q.heads + 2ll * p.groups * B * Hk;
-  const long long grid = (items + 3) / 4;
-  const long long most = 16ll * num_sms;
-  dsa::append_q8_kernel<<<(unsigned)(grid < most ? grid : most), 128, 0,
-                          static_cast<cudaStream_t>(cuda_stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return dsa::run_append(p, num_sms, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int dsa_paged_read_q8(const void *k_cache, const void *v_cache,
@@ -295,9 +494,13 @@ int dsa_paged_read_q8(const void *k_cache, const void *v_cache,
   int num_sms = 0;
   rc = dsa::device_num_sms(&num_sms);
   if (rc != DSA_OK) return rc;
-  const long long grid = ((long long)T * B * Hk * (D / 16) * 2 + 255) / 256;
+  constexpr int kWarps = dsa::kReadThreads / 32;
+  const long long items =
+      (long long)((T + dsa::kReadRows - 1) / dsa::kReadRows) * B;
+  const long long grid = (items + kWarps - 1) / kWarps;
   const long long most = 8ll * num_sms;
-  dsa::read_q8_kernel<<<(unsigned)(grid < most ? grid : most), 256, 0,
+  dsa::read_q8_kernel<<<(unsigned)(grid < most ? grid : most),
+                        dsa::kReadThreads, 0,
                         static_cast<cudaStream_t>(cuda_stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -42,60 +42,6 @@ constexpr int rope_ctas(int el, bool vec) { return el == 2 && vec ? 6 : 3; }
 constexpr int kRopeBwdCtas = 4;
 constexpr int kRopeMaxCtas = 6 * 160;
 
-// Row groups whose loads a warp has in flight.
-constexpr int kBatch = 4;
-
-// A warp's share of one token: heads [h0, h1) of the row set `r`.
-// KIND 0: queries, 1: keys, 2: values (copied).  `dst0`: the token's first
-// head in the output, heads `dh` elements apart; nullptr: not written.
-template <typename T, bool VEC, int LPR, int KIND>
-__device__ __forceinline__ void rope_heads(const RopeArgs &a,
-                                           const RopeRows &r, const T *src0,
-                                           T *dst0, long long dh, int h0,
-                                           int h1, int sub, int e0,
-                                           Turn<T, VEC> &turn,
-                                           const float2 *cs, const float *w,
-                                           float *buf) {
-  constexpr int RPW = 32 / LPR;
-  if (h0 >= h1) return;
-  const bool norm = KIND < 2 && r.w != nullptr;
-  Chunk<T, VEC> x[kBatch];
-  auto fetch = [&](int hb) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = hb + u * RPW + sub;
-      x[u].load(src0 + h * r.sh, e0, h < h1 ? a.D : 0);
-    }
-  };
-  fetch(h0);  // on the way while the coefficients are made
-  if (KIND < 2) turn.set(a, e0, false, cs, norm ? w : nullptr);
-  const float over_d = 1.f / a.D;
-  for (int hb = h0;;) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = hb + u * RPW + sub;
-      if (hb + u * RPW >= h1) break;
-      if constexpr (KIND < 2) {
-        float2 n[4], y[4];
-        x[u].get(n);
-        const float sq = squares(n);
-        turn.apply(a, x[u], n, y, e0, buf, sq < 3e38f);
-        if (norm) {
-          const float r2 = rsqrtf(row_sum<LPR>(sq) * over_d + a.eps);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = __fmul2_rn(y[i], make_float2(r2, r2));
-        }
-        x[u].set(y);
-      }
-      if (h < h1 && dst0) x[u].store(dst0 + h * dh, e0, a.D);
-    }
-    hb += kBatch * RPW;
-    if (hb >= h1) break;
-    fetch(hb);
-  }
-}
-
 // PAGED: k and v rows go to the cache; without it there is no v.
 // Append, measured: 8192 tokens of 40 + 2 x 8 rows of 64: 33 us, 3.5 TB/s of
 // 114 MB: a warp has two or three tokens, and for each a chain of the position,
