@@ -257,64 +257,370 @@ __global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
   }
 }
 
-template <bool VEC, int LPR, int RW>
-int launch_append(AppendQ8 &p, int num_sms, cudaStream_t st) {
+// What is the same for all rows of a thread: the weights of its 8 elements and
+// of their partners, the latter with the rotation's sign; where its angles lie
+// in a token's, or behind them (cosine 1, sine 0) outside the rotated part.
+struct Fixed {
+  float2 w[4], wp[4];
+  int src_lane, at;
+  bool rotated;
+};
+
+// x of 8 elements, normed and rotated: (x w c + x' w' s) rstd.
+template <int LPR>
+__device__ __forceinline__ void turned(const RopeArgs &a, const Fixed &f,
+                                       const Chunk<__nv_bfloat16, true> &raw,
+                                       const float2 *cs, const float2 *none,
+                                       bool norm, float2 (&y)[4]) {
+  Chunk<__nv_bfloat16, true> from;
+  const uint32_t *x = reinterpret_cast<const uint32_t *>(raw.raw);
+  uint32_t *o = reinterpret_cast<uint32_t *>(from.raw);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // neighbours swap places in their word, halves come from another lane;
+    // (an infinity of an element that is its own partner stays out)
+    const uint32_t v = a.interleaved
+                           ? __byte_perm(x[i], x[i], 0x1032)
+                           : __shfl_sync(0xffffffffu, x[i], f.src_lane);
+    o[i] = f.rotated ? v : 0u;
+  }
+  float2 v[4], p[4];
+  raw.get(v);
+  from.get(p);
+  const float4 *q =
+      reinterpret_cast<const float4 *>(f.rotated ? cs + f.at : none);
+  float sq = 0.f;
+  if (norm) sq = row_sum<LPR>(squares(v));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 c, s;
+    if (a.interleaved) {  // one angle for both
+      const float2 t = reinterpret_cast<const float2 *>(q)[i];
+      c = make_float2(t.x, t.x), s = make_float2(t.y, t.y);
+    } else {
+      const float4 t = q[i];
+      c = make_float2(t.x, t.z), s = make_float2(t.y, t.w);
+    }
+    y[i] = __ffma2_rn(__fmul2_rn(v[i], f.w[i]), c,
+                      __fmul2_rn(__fmul2_rn(p[i], f.wp[i]), s));
+  }
+  if (norm) {
+    const float r = rsqrtf(sq * (1.f / a.D) + a.eps);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __fmul2_rn(y[i], make_float2(r, r));
+  }
+}
+
+// Rows in 16-byte pieces.  CTAs 0 .. kv - 1 take keys and values, the others
+// queries as norm_rope_kernel() does.  Keys and values: an item is a group that
+// a sequence's rows can reach, of the keys or the values, and one head (WARP: by
+// a warp, where a group gets few new rows) or some (by a CTA; the angles of the
+// group's tokens are in shared memory for all of them).  A thread holds 8
+// elements of RW rows of a head as fp32 until the group's scale is known, and
+// has the next head's rows on the way.
+constexpr int kVecThreads = 256, kVecWarps = kVecThreads / 32;
+constexpr int vec_ctas(int rw) { return rw <= 4 ? 3 : 2; }  // an SM
+
+template <int LPR, int RW, bool WARP>
+__global__ void __launch_bounds__(kVecThreads, vec_ctas(RW))
+    append_q8_vec_kernel(const __grid_constant__ AppendQ8 p) {
+  constexpr int RPW = 32 / LPR;
+  using T = __nv_bfloat16;
+  __shared__ unsigned long long fr[kRopeMaxD / 2];
+  __shared__ __align__(16) float sw[2][kRopeMaxD];
+  __shared__ float red[2][kVecWarps];
+  __shared__ __align__(16) float2 none[8];  // of elements that do not turn
+  extern __shared__ __align__(16) float2 angles[];
+  const RopeArgs &a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane / LPR, e0 = (lane % LPR) * 8;
+  const int half = a.R / 2;
+  auto frequencies = [&] {
+    for (int i = threadIdx.x; i < half; i += kVecThreads) {
+      double t = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
+      t -= floor(t);
+      fr[i] = __double2ull_rn(t * 18446744073709551616.0);
+    }
+  };
+
+  if (blockIdx.x >= p.kv) {
+    // ---------------- queries ----------------
+    float *buf = nullptr;
+    for (int i = threadIdx.x; i < kRopeMaxD; i += kVecThreads)
+      sw[0][i] = a.q.w && i < a.D ? __ldg(a.q.w + i) : 0.f;
+    frequencies();
+    float2 *cs = angles + warp * p.angles;
+    if (half == 0 && lane < 8) cs[lane] = make_float2(0.f, 0.f);
+    __syncthreads();
+    Turn<T, true> turn;
+    turn.init(a, e0, lane, false);
+    const unsigned items = (unsigned)a.S * a.B * a.chunks;
+    const unsigned stride = (gridDim.x - p.kv) * kVecWarps;
+    const int nq = a.q.heads;
+    for (unsigned item = (blockIdx.x - p.kv) * kVecWarps + warp; item < items;
+         item += stride) {
+      const unsigned tk = item / (unsigned)a.chunks;
+      const int s = (int)(tk / (unsigned)a.B), b = (int)(tk % (unsigned)a.B);
+      const int h0 = (int)(item % (unsigned)a.chunks) * a.heads_per_item;
+      const long long pos = (long long)__ldg(p.start + b) + s;
+      __syncwarp();
+      for (int i = lane; i < half; i += 32) cs[i] = turn_of(a, pos, fr[i]);
+      __syncwarp();
+      rope_heads<T, true, LPR, 0>(
+          a, a.q, static_cast<const T *>(a.q.in) + s * a.q.ss + b * a.q.sb,
+          static_cast<T *>(a.q.out) + tk * (long long)nq * a.D, a.D, h0,
+          min(h0 + a.heads_per_item, nq), sub, e0, turn, cs, sw[0], buf);
+    }
+    return;
+  }
+  // ---------------- keys and values ----------------
+  constexpr int nw = WARP ? 1 : kVecWarps;  // warps of an item
+  const int unit = WARP ? 0 : warp;
+  const int hc = WARP ? 1 : p.heads, nh = (a.k.heads + hc - 1) / hc;
+  long long it = WARP ? (long long)blockIdx.x * kVecWarps + warp
+                      : (long long)blockIdx.x;
+  const bool some = it < (long long)p.groups * a.B * 2 * nh;
+  const bool is_v = it & 1;
+  it >>= 1;
+  const int h0 = (int)(it % nh) * hc;
+  it /= nh;
+  const int b = some ? (int)(it % a.B) : 0, gi = some ? (int)(it / a.B) : 0;
+  const int start = __ldg(p.start + b);
+  const int rows = rows_of(p, b, start);
+  const long long g0 = ((long long)(start >> p.c.lg) + gi) << p.c.lg;
+  const int s0 = (int)max(g0 - start, 0ll);
+  const int s1 = (int)min(g0 + p.c.group - start, (long long)rows);
+  const int n = some ? s1 - s0 : 0;
+  if (!WARP && n <= 0) return;
+  const RopeRows &in = is_v ? a.v : a.k;
+  const T *src0 = static_cast<const T *>(in.in) + b * in.sb + s0 * in.ss;
+  Chunk<T, true> x[RW];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+      const int row = (u * nw + unit) * RPW + sub;
+      if (u * nw * RPW < n)  // (the same for all)
+        x[u].load(src0 + h * in.sh + row * in.ss, e0, row < n ? a.D : 0);
+    }
+  };
+  if (n > 0) fetch(h0);
+  bool bad = false;
+  int page = -1;
+  if (n > 0) {
+    page = q8_page(p.c, b, g0, bad);
+    if (bad && lane == 0) atomicOr(a.status, kStatusIndexRange);
+  }
+  if (!WARP && page < 0) return;
+  const bool norm = a.k.w != nullptr;
+  Fixed f;
+  if (WARP || !is_v) {
+    // (WARP: some of the CTA's items may be keys)
+    frequencies();
+    if (threadIdx.x < 8) none[threadIdx.x] = make_float2(1.f, 0.f);
+    const int rel = e0 - a.r0;
+    const bool first = a.interleaved || rel < half;
+    f.rotated = rel >= 0 && rel < a.R;
+    f.src_lane = lane;
+    f.at = 0;
+    if (f.rotated) {
+      f.at = a.interleaved ? rel / 2 : first ? rel : rel - half;
+      if (!a.interleaved) f.src_lane = first ? lane + a.R / 16 : lane - a.R / 16;
+    }
+    const int ep = a.interleaved || !f.rotated ? e0 : first ? e0 + half : e0 - half;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 w = make_float2(1.f, 1.f), o = w;
+      if (norm && e0 < a.D) {
+        w = make_float2(__ldg(a.k.w + e0 + 2 * i), __ldg(a.k.w + e0 + 2 * i + 1));
+        o = make_float2(__ldg(a.k.w + ep + 2 * i), __ldg(a.k.w + ep + 2 * i + 1));
+      }
+      // (first: a cos - b sin; the other: a sin + b cos)
+      f.w[i] = w;
+      f.wp[i] = a.interleaved ? make_float2(-o.y, o.x)
+                : first       ? make_float2(-o.x, -o.y)
+                              : o;
+    }
+    __syncthreads();
+  }
+  if (WARP && page < 0) return;
+  float2 *cs = angles + (WARP ? warp * p.angles : 0);
+  if (!is_v && half > 0) {
+    for (int i = WARP ? lane : threadIdx.x; i < n * half;
+         i += WARP ? 32 : kVecThreads) {
+      const int t = i / half;
+      cs[i] = turn_of(a, (long long)start + s0 + t, fr[i - t * half]);
+    }
+    if (WARP)
+      __syncwarp();
+    else
+      __syncthreads();
+  }
+  const int early = (int)max((long long)start - g0, 0ll);
+  const int off = (int)(g0 % p.c.page_size);
+  const long long st = is_v ? p.c.v_t : p.c.k_t;
+  const int h1 = min(h0 + hc, a.k.heads);
+  for (int h = h0; h < h1; ++h) {
+    uint8_t *at = (is_v ? p.c.v + page * p.c.v_p + h * p.c.v_h
+                        : p.c.k + page * p.c.k_p + h * p.c.k_h) +
+                  off * st + e0;
+    float *scale = (is_v ? p.c.vs : p.c.ks) + q8_scale_at(p.c, page, off, h);
+    const float had = early > 0 ? *scale : 0.f;
+    float2 y[RW][4];
+    float top = 0.f;
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+      if (u * nw * RPW < n) {
+        const int row = (u * nw + unit) * RPW + sub;
+        if (is_v)
+          x[u].get(y[u]);
+        else
+          turned<LPR>(a, f, x[u], cs + (row < n ? row : 0) * half, none, norm,
+                      y[u]);
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          t = fmaxf(t, fmaxf(q8_mag(y[u][i].x), q8_mag(y[u][i].y)));
+        // (padding of the last rows may hold what eps = 0 makes of zeros)
+        if (row < n && e0 < a.D) top = fmaxf(top, t);
+      }
+    }
+    if (h + 1 < h1) fetch(h + 1);
+    // non-negative floats compare as integers
+    top = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(top)));
+    if constexpr (!WARP) {
+      float *rd = red[(h - h0) & 1];
+      if (lane == 0) rd[unit] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kVecWarps; ++i) top = fmaxf(top, rd[i]);
+    }
+    __syncwarp();
+    int e = q8_exp_for(top);
+    if (early > 0) {
+      const int e_old = q8_exp(had);
+      if (e > e_old && e0 < a.D) {
+        const float fc = q8_pow2(e_old - e);
+        for (int t = unit * RPW + sub; t < early; t += nw * RPW) {
+          uint2 *to = reinterpret_cast<uint2 *>(at + t * st);
+          const uint2 c = *to;
+          const float2 v0 = q8_float2(c.x & 0xffffu), v1 = q8_float2(c.x >> 16);
+          const float2 v2 = q8_float2(c.y & 0xffffu), v3 = q8_float2(c.y >> 16);
+          *to = make_uint2(
+              q8_pack4(v0.x * fc, v0.y * fc, v1.x * fc, v1.y * fc),
+              q8_pack4(v2.x * fc, v2.y * fc, v3.x * fc, v3.y * fc));
+        }
+      }
+      e = max(e, e_old);
+    }
+    if (unit == 0 && lane == 0) *scale = q8_pow2(e);
+    const float inv = q8_pow2(-e);
+#pragma unroll
+    for (int u = 0; u < RW; ++u) {
+      const int row = (u * nw + unit) * RPW + sub;
+      if (row < n && e0 < a.D)
+        *reinterpret_cast<uint2 *>(at + (early + row) * st) = make_uint2(
+            q8_pack4(y[u][0].x * inv, y[u][0].y * inv, y[u][1].x * inv,
+                     y[u][1].y * inv),
+            q8_pack4(y[u][2].x * inv, y[u][2].y * inv, y[u][3].x * inv,
+                     y[u][3].y * inv));
+    }
+  }
+}
+
+// Heads of a CTA's item of keys or values: all share the angles, but fewer
+// where that leaves SMs idle.
+int heads_of_item(long long groups, int heads, int num_sms) {
+  int n = heads;
+  while (n > 1 && groups * ((heads + n - 1) / n) < 3ll * num_sms)
+    n = (n + 1) / 2;
+  return n;
+}
+
+// Queries: warps' items as launch_lpr() of norm_rope.cu cuts them; the CTAs.
+long long query_ctas(RopeArgs &a, int rpw, int warps, long long cap,
+                     int num_sms) {
+  if (a.q.heads == 0) return 0;
+  const long long toks = (long long)a.S * a.B;
+  int per = (a.q.heads + rpw - 1) / rpw * rpw;
+  while (per > rpw && toks * ((a.q.heads + per - 1) / per) < 32ll * num_sms)
+    per = ((per / 2) + rpw - 1) / rpw * rpw;
+  a.heads_per_item = per;
+  a.chunks = (a.q.heads + per - 1) / per;
+  const long long n = (toks * a.chunks + warps - 1) / warps;
+  return n < cap ? n : cap;
+}
+
+template <int LPR, int RW, bool WARP>
+int launch_vec(AppendQ8 &p, int num_sms, cudaStream_t st) {
   constexpr int RPW = 32 / LPR;
   RopeArgs &a = p.a;
-  auto kern = append_q8_kernel<VEC, LPR, RW>;
+  auto kern = append_q8_vec_kernel<LPR, RW, WARP>;
   // new rows that a group can get
   const int most = a.S < p.c.group ? a.S : p.c.group;
-  // by warps where those are two passes of one: single tokens and drafts
-  p.by_warp = most <= 2 * RPW;
   // angles of the tokens of a group (a warp's, or a CTA's), and of a token of
   // queries for each warp
+  const int half = a.R / 2 < 8 ? 8 : a.R / 2;
+  p.angles = (WARP ? most : 1) * half;
+  int angles = kVecWarps * p.angles;
+  if (!WARP && most * half > angles) angles = most * half;
+  const long long groups = 2ll * p.groups * a.B;
+  p.heads = WARP ? 1 : heads_of_item(groups, a.k.heads, num_sms);
+  long long kv = groups * ((a.k.heads + p.heads - 1) / p.heads);
+  if (WARP) kv = (kv + kVecWarps - 1) / kVecWarps;
+  if (kv >= (1ll << 30)) return DSA_ERR_UNSUPPORTED;
+  p.kv = (unsigned)kv;
+  // two rounds of CTAs: the first ones wait for keys and values to finish
+  const long long q_ctas = query_ctas(a, RPW, kVecWarps,
+                                      2ll * vec_ctas(RW) * num_sms, num_sms);
+  // (D * group <= 16384 and R <= D: 64 KB at most)
+  constexpr int kMost = 16384 / 2 * (int)sizeof(float2) + 8192;
+  const int smem = angles * (int)sizeof(float2);
+  if (smem > kMost) return DSA_ERR_UNSUPPORTED;
+  if (allow_smem(kern, kMost) != cudaSuccess) return DSA_ERR_CUDA;
+  kern<<<(unsigned)(kv + q_ctas), kVecThreads, smem, st>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+// RW: rows of a thread that a group takes.  A warp takes an item of its own
+// where those are two passes of one: single tokens and drafts.
+template <int LPR>
+int launch_vec_rows(AppendQ8 &p, int num_sms, cudaStream_t st) {
+  constexpr int RPW = 32 / LPR;
+  const int most = p.a.S < p.c.group ? p.a.S : p.c.group;
+  if (most <= RPW) return launch_vec<LPR, 1, true>(p, num_sms, st);
+  if (most <= 2 * RPW) return launch_vec<LPR, 2, true>(p, num_sms, st);
+  if (p.c.group <= 2 * kVecWarps * RPW)
+    return launch_vec<LPR, 2, false>(p, num_sms, st);
+  if (p.c.group <= 4 * kVecWarps * RPW)
+    return launch_vec<LPR, 4, false>(p, num_sms, st);
+  return launch_vec<LPR, 8, false>(p, num_sms, st);
+}
+
+// Rows without 16-byte pieces: RW rows of a thread, at most 8 or 16.
+template <int RW>
+int launch_any(AppendQ8 &p, int num_sms, cudaStream_t st) {
+  RopeArgs &a = p.a;
+  auto kern = append_q8_kernel<false, 32, RW>;
+  const int most = a.S < p.c.group ? a.S : p.c.group;
+  p.by_warp = most <= 2;
   const int half = a.R / 2 < 8 ? 8 : a.R / 2;
   p.angles = (p.by_warp ? most : 1) * half;
   int angles = kRopeWarps * p.angles;
   if (!p.by_warp && most * half > angles) angles = most * half;
   const long long groups = 2ll * p.groups * a.B;
-  long long kv;
-  if (p.by_warp) {
-    kv = (groups * a.k.heads + kRopeWarps - 1) / kRopeWarps;
-  } else {
-    // all heads of a group share its angles; fewer where that leaves SMs idle
-    p.heads = a.k.heads;
-    while (p.heads > 1 &&
-           groups * ((a.k.heads + p.heads - 1) / p.heads) < 3ll * num_sms)
-      p.heads = (p.heads + 1) / 2;
-    kv = groups * ((a.k.heads + p.heads - 1) / p.heads);
-  }
+  p.heads = p.by_warp ? 1 : heads_of_item(groups, a.k.heads, num_sms);
+  long long kv = groups * ((a.k.heads + p.heads - 1) / p.heads);
+  if (p.by_warp) kv = (kv + kRopeWarps - 1) / kRopeWarps;
   if (kv >= (1ll << 30)) return DSA_ERR_UNSUPPORTED;
   p.kv = (unsigned)kv;
-  // queries: as launch_lpr() of norm_rope.cu shares them
-  long long q_ctas = 0;
-  if (a.q.heads > 0) {
-    const long long toks = (long long)a.S * a.B;
-    int per = (a.q.heads + RPW - 1) / RPW * RPW;
-    while (per > RPW &&
-           toks * ((a.q.heads + per - 1) / per) < 32ll * num_sms)
-      per = ((per / 2) + RPW - 1) / RPW * RPW;
-    a.heads_per_item = per;
-    a.chunks = (a.q.heads + per - 1) / per;
-    q_ctas = (toks * a.chunks + kRopeWarps - 1) / kRopeWarps;
-    const long long cap = (RW <= 8 ? 5ll : 3ll) * num_sms;
-    if (q_ctas > cap) q_ctas = cap;
-  }
+  const long long q_ctas =
+      query_ctas(a, 1, kRopeWarps, 3ll * num_sms, num_sms);
+  constexpr int kMost = 16384 / 2 * (int)sizeof(float2) + 8192;
   const int smem = angles * (int)sizeof(float2);
-  // (D * group <= 16384, R <= D: 64 KB at most)
-  if (allow_smem(kern, 16384 / 2 * (int)sizeof(float2) + 4096) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  if (smem > kMost) return DSA_ERR_UNSUPPORTED;
+  if (allow_smem(kern, kMost) != cudaSuccess) return DSA_ERR_CUDA;
   kern<<<(unsigned)(kv + q_ctas), kRopeThreads, smem, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-}
-
-// RW: rows of a thread that a whole group takes, at most 8 or 16.
-template <bool VEC, int LPR>
-int launch_append_rows(AppendQ8 &p, int num_sms, cudaStream_t st) {
-  constexpr int RPW = 32 / LPR;
-  if (p.c.group <= 8 * kRopeWarps * RPW)
-    return launch_append<VEC, LPR, 8>(p, num_sms, st);
-  return launch_append<VEC, LPR, 16>(p, num_sms, st);
 }
 
 int run_append(AppendQ8 &p, int num_sms, cudaStream_t st) {
@@ -322,10 +628,12 @@ int run_append(AppendQ8 &p, int num_sms, cudaStream_t st) {
   const bool vec = a.r0 % 8 == 0 && a.R % (a.interleaved ? 8 : 16) == 0 &&
                    vec_rows(a.q, 2, false) && vec_rows(a.k, 2, false) &&
                    vec_rows(a.v, 2, false);
-  if (!vec) return launch_append_rows<false, 32>(p, num_sms, st);
-  if (a.D <= 64) return launch_append_rows<true, 8>(p, num_sms, st);
-  if (a.D <= 128) return launch_append_rows<true, 16>(p, num_sms, st);
-  return launch_append_rows<true, 32>(p, num_sms, st);
+  if (!vec)
+    return p.c.group <= 8 * kRopeWarps ? launch_any<8>(p, num_sms, st)
+                                       : launch_any<16>(p, num_sms, st);
+  if (a.D <= 64) return launch_vec_rows<8>(p, num_sms, st);
+  if (a.D <= 128) return launch_vec_rows<16>(p, num_sms, st);
+  return launch_vec_rows<32>(p, num_sms, st);
 }
 
 struct ReadQ8 {
@@ -339,8 +647,8 @@ struct ReadQ8 {
 // A warp takes kReadRows consecutive tokens of a sequence: their pages are
 // looked up once, and a lane has the loads of all of them in flight, 16 values
 // of one head each.
-constexpr int kReadRows = 8, kReadThreads = 256;
-__global__ void __launch_bounds__(kReadThreads) read_q8_kernel(
+constexpr int kReadRows = 4, kReadThreads = 256;
+__global__ void __launch_bounds__(kReadThreads, 4) read_q8_kernel(
     const __grid_constant__ ReadQ8 p) {
   const int lane = threadIdx.x & 31;
   const int ch = p.c.D / 16, pieces = p.c.Hk * ch;
