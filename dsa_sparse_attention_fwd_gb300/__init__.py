@@ -844,7 +844,8 @@ def _block_attn_out(q, shape, out_o, out_lse, workspace, stream,
     """The outputs and the workspace of a forward, made where not given."""
     S, B, H, D = q.shape
     if out_o is None:
-        out_o = _empty(stream, (S, B, H, D), q.dtype, q.device)
+        out_o = (torch.empty_like(q) if stream is None  # (q is dense)
+                 else _empty(stream, (S, B, H, D), q.dtype, q.device))
     else:
         _dense("out_o", out_o, torch.bfloat16, (S, B, H, D))
     if out_lse is None:
@@ -981,26 +982,63 @@ def dsa_block_attn_bwd(q, k, v, o, lse, grad_o, blocks, block_size, scale,
     return grad_q, grad_k, grad_v, workspace
 
 
-def _paged_cache_q8(k_cache, v_cache, k_scale, v_scale, page_table, B):
-    """(pages, page_size, Hk, D, group) of an 8-bit cache."""
+# The three calls below look at each tensor once, all in one expression; where
+# that does not hold, the named checks say what is wrong (or that a layout is
+# fine after all: strided caches).
+_BF, _E4M3 = torch.bfloat16, torch.float8_e4m3fn
+_F32, _I32 = torch.float32, torch.int32
+_I9 = ctypes.c_int64 * 9
+
+
+def _cache_q8_ok(dev, k_cache, v_cache, k_scale, v_scale, page_table):
+    """Whether these are the dense tensors of an 8-bit cache on device dev."""
+    shape = k_cache.shape
+    return (k_cache.dtype is _E4M3 and v_cache.dtype is _E4M3
+            and k_scale.dtype is _F32 and v_scale.dtype is _F32
+            and page_table.dtype is _I32 and v_cache.shape == shape
+            and v_scale.shape == k_scale.shape
+            and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and k_scale.get_device() == dev and v_scale.get_device() == dev
+            and page_table.get_device() == dev and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and page_table.is_contiguous())
+
+
+def _cache_q8_sizes(k_cache, k_scale, page_table):
+    """(pages, page_size, Hk, D, group, B, max_pages)."""
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, Hk, D]")
-    shape = k_cache.shape
-    _last_contiguous("k_cache", k_cache, torch.float8_e4m3fn, shape)
-    _last_contiguous("v_cache", v_cache, torch.float8_e4m3fn, shape)
-    pages, page_size, Hk, D = shape
     if k_scale.dim() != 3:
         raise ValueError("k_scale must be [pages, page_size / group, Hk]")
-    n = k_scale.shape[1]
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    pages, page_size, Hk, D = k_cache.shape
+    pages_s, n, heads_s = k_scale.shape
     if n <= 0 or page_size % n:
         raise ValueError(f"k_scale: {n} scales do not divide a page of "
                          f"{page_size} tokens")
-    _dense("k_scale", k_scale, torch.float32, (pages, n, Hk))
-    _dense("v_scale", v_scale, torch.float32, (pages, n, Hk))
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    _dense("page_table", page_table, torch.int32, (B, page_table.shape[1]))
-    return pages, page_size, Hk, D, page_size // n
+    if pages_s != pages or heads_s != Hk:
+        raise ValueError(f"k_scale shape {tuple(k_scale.shape)} != "
+                         f"{(pages, n, Hk)}")
+    B, max_pages = page_table.shape
+    return pages, page_size, Hk, D, page_size // n, B, max_pages
+
+
+def _check_cache_q8(k_cache, v_cache, k_scale, v_scale, page_table):
+    _last_contiguous("k_cache", k_cache, _E4M3, k_cache.shape)
+    _last_contiguous("v_cache", v_cache, _E4M3, k_cache.shape)
+    _dense("k_scale", k_scale, _F32, k_scale.shape)
+    _dense("v_scale", v_scale, _F32, k_scale.shape)
+    _dense("page_table", page_table, _I32, page_table.shape)
+
+
+def _three_strides(k, v, q):
+    """Host arrays of k's, v's and q's leading strides: addresses in one
+    array, which the caller keeps."""
+    a = _I9(*k.stride()[:3], *v.stride()[:3],
+            *((0, 0, 0) if q is None else q.stride()[:3]))
+    at = ctypes.addressof(a)
+    return a, at, at + 24, None if q is None else at + 48
 
 
 def dsa_paged_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table,
@@ -1018,40 +1056,74 @@ def dsa_paged_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table,
     group's scale may grow with it, which rounds the group's earlier tokens
     again.  Returns (out_q, workspace); the status word is that of
     dsa_paged_append."""
-    lib = load_library()
-    dev = _on_gpu("dsa_paged_append_q8",
-                  "k v k_cache v_cache k_scale v_scale page_table start count "
-                  "inv_freq wk q wq out_q workspace",
-                  k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
-                  count, inv_freq, wk, q, wq, out_q, workspace)
-    bf = torch.bfloat16
-    S, B, Hk, H, D, R = _rope_inputs(k, q, inv_freq, None, wk,
-                                     None if q is None else wq, bf, "k", "q")
-    _last_contiguous("v", v, bf, (S, B, Hk, D))
-    pages, page_size, cache_heads, cache_dim, group = _paged_cache_q8(
-        k_cache, v_cache, k_scale, v_scale, page_table, B)
-    if cache_heads != Hk or cache_dim != D:
-        raise ValueError("the cache's heads or head size differ from k's")
-    _dense("start", start, torch.int32, (B,))
-    if count is not None:
-        _dense("count", count, torch.int32, (B,))
+    lib = _lib or load_library()
+    dev = k.get_device()
+    pages, page_size, Hk, D, group, B, max_pages = _cache_q8_sizes(
+        k_cache, k_scale, page_table)
+    if k.dim() != 4 or (q is not None and q.dim() != 4):
+        raise ValueError("q [S, B, H, D] and k [S, B, Hk, D] expected")
+    S = k.shape[0]
+    shape = (S, B, Hk, D)
+    H, R = 0, 0
+    if q is not None:
+        H = q.shape[2]
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice()
+            and _cache_q8_ok(dev, k_cache, v_cache, k_scale, v_scale,
+                             page_table)
+            and k.dtype is _BF and v.dtype is _BF and k.shape == shape
+            and v.shape == shape and k.stride(3) == 1 and v.stride(3) == 1
+            and v.get_device() == dev
+            and start.dtype is _I32 and start.shape == (B,)
+            and start.is_contiguous() and start.get_device() == dev
+            and (count is None or (
+                count.dtype is _I32 and count.shape == (B,)
+                and count.is_contiguous() and count.get_device() == dev))
+            and (q is None or (
+                q.dtype is _BF and q.shape == (S, B, H, D)
+                and q.stride(3) == 1 and q.get_device() == dev))
+            and (inv_freq is None or (
+                inv_freq.dtype is torch.float64 and inv_freq.dim() == 1
+                and inv_freq.is_contiguous() and inv_freq.get_device() == dev))
+            and (wk is None or (
+                wk.dtype is _F32 and wk.shape == (D,) and wk.is_contiguous()
+                and wk.get_device() == dev))
+            and (wq is None or (
+                wq.dtype is _F32 and wq.shape == (D,) and wq.is_contiguous()
+                and wq.get_device() == dev))
+            and (workspace is None or workspace.get_device() == dev)
+            and (out_q is None or out_q.get_device() == dev)):
+        dev = _on_gpu("dsa_paged_append_q8",
+                      "k v k_cache v_cache k_scale v_scale page_table start "
+                      "count inv_freq wk q wq out_q workspace",
+                      k, v, k_cache, v_cache, k_scale, v_scale, page_table,
+                      start, count, inv_freq, wk, q, wq, out_q, workspace)
+        _rope_inputs(k, q, inv_freq, None, wk, wq, _BF, "k", "q")
+        _last_contiguous("k", k, _BF, shape)
+        _last_contiguous("v", v, _BF, shape)
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+        _dense("start", start, _I32, (B,))
+        if count is not None:
+            _dense("count", count, _I32, (B,))
     if q is not None:
         if out_q is None:
-            out_q = _empty(stream, (S, B, H, D), bf, q.device)
+            out_q = _empty(stream, (S, B, H, D), _BF, q.device)
         else:
-            _dense("out_q", out_q, bf, (S, B, H, D))
+            _dense("out_q", out_q, _BF, (S, B, H, D))
     if workspace is None:
         workspace = _zeroed_workspace(stream, 256, k.device)
+    keep, k_st, v_st, q_st = _three_strides(k, v, q)
     rc = lib.dsa_paged_append_q8(
-        _addr(k), _strides(k), _addr(v), _strides(v), _addr(q),
-        None if q is None else _strides(q), S, B, H, Hk, D, _addr(k_cache),
-        _addr(v_cache), _strides2(k_cache, v_cache), _addr(k_scale),
-        _addr(v_scale), group, pages, page_size, _addr(page_table),
-        page_table.shape[1], _addr(start), _addr(count), _addr(wq), _addr(wk),
-        float(eps), _addr(inv_freq), int(rot_start), R,
-        int(bool(interleaved)), float(rot_scale),
-        None if q is None else _addr(out_q), _addr(workspace),
+        k.data_ptr(), k_st, v.data_ptr(), v_st, _addr(q), q_st, S, B, H, Hk,
+        D, k_cache.data_ptr(), v_cache.data_ptr(), _strides2(k_cache, v_cache),
+        k_scale.data_ptr(), v_scale.data_ptr(), group, pages, page_size,
+        page_table.data_ptr(), max_pages, start.data_ptr(), _addr(count),
+        None if q is None else _addr(wq), _addr(wk), eps, _addr(inv_freq),
+        rot_start, R, 1 if interleaved else 0, rot_scale,
+        None if q is None else out_q.data_ptr(), workspace.data_ptr(),
         workspace.numel(), _raw_stream(stream, dev))
+    del keep
     if rc != 0:
         raise DsaError(rc, "dsa_paged_append_q8")
     return out_q, workspace
@@ -1064,35 +1136,46 @@ def dsa_paged_read_q8(k_cache, v_cache, k_scale, v_scale, page_table, T,
     D] bf16 with row t of sequence b token first[b] + t (first [B] int32,
     None: t) where t < length[b] (None: T), zeros behind.  For caches as
     dsa_paged_append_q8 writes them."""
-    lib = load_library()
-    dev = _on_gpu("dsa_paged_read_q8",
-                  "k_cache v_cache k_scale v_scale page_table first length "
-                  "out_k out_v workspace",
-                  k_cache, v_cache, k_scale, v_scale, page_table, first,
-                  length, out_k, out_v, workspace)
-    B = page_table.shape[0]
-    pages, page_size, Hk, D, group = _paged_cache_q8(
-        k_cache, v_cache, k_scale, v_scale, page_table, B)
-    for name, t in (("first", first), ("length", length)):
-        if t is not None:
-            _dense(name, t, torch.int32, (B,))
-    bf, shape = torch.bfloat16, (T, B, Hk, D)
+    lib = _lib or load_library()
+    dev = k_cache.get_device()
+    pages, page_size, Hk, D, group, B, max_pages = _cache_q8_sizes(
+        k_cache, k_scale, page_table)
+    shape = (T, B, Hk, D)
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice()
+            and _cache_q8_ok(dev, k_cache, v_cache, k_scale, v_scale,
+                             page_table)
+            and (first is None or (
+                first.dtype is _I32 and first.shape == (B,)
+                and first.is_contiguous() and first.get_device() == dev))
+            and (length is None or (
+                length.dtype is _I32 and length.shape == (B,)
+                and length.is_contiguous() and length.get_device() == dev))
+            and (workspace is None or workspace.get_device() == dev)
+            and out_k is None and out_v is None):
+        dev = _on_gpu("dsa_paged_read_q8",
+                      "k_cache v_cache k_scale v_scale page_table first "
+                      "length out_k out_v workspace",
+                      k_cache, v_cache, k_scale, v_scale, page_table, first,
+                      length, out_k, out_v, workspace)
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+        for name, t in (("first", first), ("length", length)):
+            if t is not None:
+                _dense(name, t, _I32, (B,))
+        for name, t in (("out_k", out_k), ("out_v", out_v)):
+            if t is not None:
+                _dense(name, t, _BF, shape)
     if out_k is None:
-        out_k = _empty(stream, shape, bf, k_cache.device)
-    else:
-        _dense("out_k", out_k, bf, shape)
+        out_k = _empty(stream, shape, _BF, k_cache.device)
     if out_v is None:
-        out_v = _empty(stream, shape, bf, k_cache.device)
-    else:
-        _dense("out_v", out_v, bf, shape)
+        out_v = _empty(stream, shape, _BF, k_cache.device)
     if workspace is None:
         workspace = _zeroed_workspace(stream, 256, k_cache.device)
     rc = lib.dsa_paged_read_q8(
-        _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
-        _addr(k_scale), _addr(v_scale), group, pages, page_size,
-        _addr(page_table), page_table.shape[1], int(T), B, Hk, D,
-        _addr(first), _addr(length), _addr(out_k), _addr(out_v),
-        _addr(workspace), workspace.numel(), _raw_stream(stream, dev))
+        k_cache.data_ptr(), v_cache.data_ptr(), _strides2(k_cache, v_cache),
+        k_scale.data_ptr(), v_scale.data_ptr(), group, pages, page_size,
+        page_table.data_ptr(), max_pages, T, B, Hk, D, _addr(first),
+        _addr(length), out_k.data_ptr(), out_v.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_paged_read_q8")
     return out_k, out_v, workspace
@@ -1113,33 +1196,58 @@ def dsa_block_attn_paged_q8_fwd(q, k_cache, v_cache, k_scale, v_scale,
     """dsa_block_attn_paged_fwd over caches held in 8 bits, as
     dsa_paged_append_q8 writes them.  blocks None with local_blocks =
     max_pages * page_size / block_size: all keys up to each row's position."""
-    lib = load_library()
-    dev = _on_gpu("dsa_block_attn_paged_q8_fwd",
-                  "q k_cache v_cache k_scale v_scale page_table blocks q_pos "
-                  "out_o out_lse workspace",
-                  q, k_cache, v_cache, k_scale, v_scale, page_table, blocks,
-                  q_pos, out_o, out_lse, workspace)
+    lib = _lib or load_library()
+    dev = q.get_device()
     if q.dim() != 4:
         raise ValueError("q [S, B, H, D] expected")
+    pages, page_size, Hk, Dk, group, Bt, max_pages = _cache_q8_sizes(
+        k_cache, k_scale, page_table)
     S, B, H, D = q.shape
-    _dense("q", q, torch.bfloat16, (S, B, H, D))
-    pages, page_size, Hk, Dk, group = _paged_cache_q8(
-        k_cache, v_cache, k_scale, v_scale, page_table, B)
-    if Dk != D:
-        raise ValueError(f"the cache's head size {Dk} differs from q's {D}")
-    max_pages = page_table.shape[1]
-    sel_heads, topk = _selection(blocks, B, S, Hk, q_pos)
+    sel_heads, topk = 1, 0
+    ids = None
+    if blocks is not None:
+        topk = blocks.shape[-1]
+        if blocks.dim() == 3:
+            ids = (B, S, topk)
+        else:
+            ids, sel_heads = (B, S, Hk, topk), Hk
+    if not (dev >= 0 and dev == torch._C._cuda_getDevice()
+            and _cache_q8_ok(dev, k_cache, v_cache, k_scale, v_scale,
+                             page_table)
+            and q.dtype is _BF and q.is_contiguous() and Dk == D and Bt == B
+            and (blocks is None or (
+                blocks.dtype is _I32 and blocks.shape == ids
+                and blocks.is_contiguous() and blocks.get_device() == dev))
+            and (q_pos is None or (
+                q_pos.dtype is _I32 and q_pos.shape == (B,)
+                and q_pos.is_contiguous() and q_pos.get_device() == dev))
+            and (workspace is None or workspace.get_device() == dev)
+            and (out_o is None or out_o.get_device() == dev)
+            and (out_lse is None or out_lse.get_device() == dev)):
+        dev = _on_gpu("dsa_block_attn_paged_q8_fwd",
+                      "q k_cache v_cache k_scale v_scale page_table blocks "
+                      "q_pos out_o out_lse workspace",
+                      q, k_cache, v_cache, k_scale, v_scale, page_table,
+                      blocks, q_pos, out_o, out_lse, workspace)
+        _dense("q", q, _BF, q.shape)
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, page_table)
+        if Bt != B:
+            raise ValueError(f"page_table is for {Bt} sequences, q for {B}")
+        if Dk != D:
+            raise ValueError(f"the cache's head size {Dk} differs from q's "
+                             f"{D}")
+        _selection(blocks, B, S, Hk, q_pos)
     out_o, out_lse, workspace = _block_attn_out(
         q, (S, B, H, Hk, D, max_pages * page_size, block_size, topk,
             local_blocks), out_o, out_lse, workspace, stream,
         dsa_block_attn_q8_workspace_size)
     rc = lib.dsa_block_attn_paged_q8_fwd(
-        _addr(q), _addr(k_cache), _addr(v_cache), _strides2(k_cache, v_cache),
-        _addr(k_scale), _addr(v_scale), group, pages, page_size,
-        _addr(page_table), max_pages, S, B, H, Hk, D, _addr(blocks),
-        sel_heads, topk, int(block_size), int(local_blocks), _addr(q_pos),
-        float(scale), _addr(out_o), _addr(out_lse), _addr(workspace),
-        workspace.numel(), _raw_stream(stream, dev))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        _strides2(k_cache, v_cache), k_scale.data_ptr(), v_scale.data_ptr(),
+        group, pages, page_size, page_table.data_ptr(), max_pages, S, B, H, Hk,
+        D, _addr(blocks), sel_heads, topk, block_size, local_blocks,
+        _addr(q_pos), scale, out_o.data_ptr(), out_lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_block_attn_paged_q8_fwd")
     return out_o, out_lse, workspace
