@@ -84,8 +84,8 @@ struct FwdSmem {
   static constexpr int kStages = fwd_stages(D, FEW);
   static constexpr int kOffV = kOffK + kStages * kKey;
   static constexpr int kOffBar = kOffV + kStages * kKey;
-  // q_full o_done; s_full p_full, two each; k_full k_empty v_full v_empty
-  static constexpr int kBars = 6 + 4 * kStages;
+  // q_full; s_full p_full o_done, two each; k_full k_empty v_full v_empty
+  static constexpr int kBars = 7 + 4 * kStages;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffWords = kOffMisc + 32;
   static constexpr int bytes(int nblk, int cap) {
@@ -147,13 +147,14 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     return (uint32_t)((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4;
   };
   const uint32_t bars = base + L::kOffBar;
-  const uint32_t q_full = bars, o_done = bars + 8;
-  auto s_full = [&](int i) { return bars + 16 + 8 * i; };
-  auto p_full = [&](int i) { return bars + 32 + 8 * i; };
-  auto k_full = [&](int i) { return bars + 48 + 8 * i; };
-  auto k_empty = [&](int i) { return bars + 48 + 8 * (NS + i); };
-  auto v_full = [&](int i) { return bars + 48 + 8 * (2 * NS + i); };
-  auto v_empty = [&](int i) { return bars + 48 + 8 * (3 * NS + i); };
+  const uint32_t q_full = bars;
+  auto s_full = [&](int i) { return bars + 8 + 8 * i; };
+  auto p_full = [&](int i) { return bars + 24 + 8 * i; };
+  auto o_done = [&](int i) { return bars + 40 + 8 * i; };
+  auto k_full = [&](int i) { return bars + 56 + 8 * i; };
+  auto k_empty = [&](int i) { return bars + 56 + 8 * (NS + i); };
+  auto v_full = [&](int i) { return bars + 56 + 8 * (2 * NS + i); };
+  auto v_empty = [&](int i) { return bars + 56 + 8 * (3 * NS + i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
 
   if (tid == 0) {
     for (int i = 0; i < L::kBars; ++i)
-      mbar_init(bars + 8 * i, i == 4 || i == 5 ? 4 : 1);  // p_full: 4 warps
+      mbar_init(bars + 8 * i, i == 3 || i == 4 ? 4 : 1);  // p_full: 4 warps
     *abort_flag = 0;
     fence_mbar_init();
     // Q arrives while the blocks are listed
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
           mma_bf16_ta(tmem + kTmO, tmem + kTmS + (i & 1) * 64 + 32 + ks * 8,
                       vd + ((ks * 2048) >> 4), kIdescO, ks == 0 ? acc : 1u);
         mma_commit(v_empty(st));
-        mma_commit(o_done);
+        mma_commit(o_done(i & 1));
         acc = 1;
       }
     }
@@ -370,7 +371,8 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
       if (i > 0 && __any_sync(0xffffffffu, move)) {
         // O is at rest once the last step's second product is done
         if (!__all_sync(0xffffffffu,
-                        wait_bar_rest(o_done, (i - 1) & 1u, abort_flag,
+                        wait_bar_rest(o_done((i - 1) & 1),
+                                      ((i - 1) >> 1) & 1u, abort_flag,
                                       p.status)))
           goto done;
         tc_fence_after();
@@ -451,10 +453,12 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
     }
     // ---------------- o = O / l ----------------
     // The last score product came before the second products of the last two
-    // steps: both may be open, and a parity names one phase of two.
+    // steps: both may be open or done, and a parity names one phase of two, so
+    // each has a barrier of its own.
     for (int i = max(n - 2, 0); i < n; ++i)
-      if (!__all_sync(0xffffffffu, wait_bar_rest(o_done, i & 1u, abort_flag,
-                                                 p.status)))
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_rest(o_done(i & 1), (i >> 1) & 1u, abort_flag,
+                                    p.status)))
         goto done;
     tc_fence_after();
     const float l = (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);

@@ -49,9 +49,9 @@ struct TileSmem {
   static constexpr int kOffV = kOffV8 + kVStages * kKey;
   static constexpr int kOffMeta = kOffV + kVStages * kV16;
   static constexpr int kOffBar = kOffMeta + kMeta * 4 * 8;
-  // q_full o_done, s_full p_full (two each), then k_full k_empty, v8_full
+  // q_full, s_full p_full o_done (two each), then k_full k_empty, v8_full
   // v8_empty, v_full v_empty, meta_full
-  static constexpr int kBars = 6 + 2 * kKStages + 4 * kVStages + kMeta;
+  static constexpr int kBars = 7 + 2 * kKStages + 4 * kVStages + kMeta;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffWords = kOffMisc + 32;
   static constexpr int bytes(int nblk, int cap) {
@@ -159,16 +159,17 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   auto sV8 = [&](int st) { return base + L::kOffV8 + st * L::kKey; };
   auto sV = [&](int st) { return base + L::kOffV + st * L::kV16; };
   const uint32_t bars = base + L::kOffBar;
-  const uint32_t q_full = bars, o_done = bars + 8;
-  auto s_full = [&](int i) { return bars + 16 + 8 * i; };
-  auto p_full = [&](int i) { return bars + 32 + 8 * i; };
-  auto k_full = [&](int i) { return bars + 48 + 8 * i; };
-  auto k_empty = [&](int i) { return bars + 48 + 8 * (NK + i); };
-  auto v8_full = [&](int i) { return bars + 48 + 8 * (2 * NK + i); };
-  auto v8_empty = [&](int i) { return bars + 48 + 8 * (2 * NK + NV + i); };
-  auto v_full = [&](int i) { return bars + 48 + 8 * (2 * NK + 2 * NV + i); };
-  auto v_empty = [&](int i) { return bars + 48 + 8 * (2 * NK + 3 * NV + i); };
-  auto meta_full = [&](int i) { return bars + 48 + 8 * (2 * NK + 4 * NV + i); };
+  const uint32_t q_full = bars;
+  auto s_full = [&](int i) { return bars + 8 + 8 * i; };
+  auto p_full = [&](int i) { return bars + 24 + 8 * i; };
+  auto o_done = [&](int i) { return bars + 40 + 8 * i; };
+  auto k_full = [&](int i) { return bars + 56 + 8 * i; };
+  auto k_empty = [&](int i) { return bars + 56 + 8 * (NK + i); };
+  auto v8_full = [&](int i) { return bars + 56 + 8 * (2 * NK + i); };
+  auto v8_empty = [&](int i) { return bars + 56 + 8 * (2 * NK + NV + i); };
+  auto v_full = [&](int i) { return bars + 56 + 8 * (2 * NK + 2 * NV + i); };
+  auto v_empty = [&](int i) { return bars + 56 + 8 * (2 * NK + 3 * NV + i); };
+  auto meta_full = [&](int i) { return bars + 56 + 8 * (2 * NK + 4 * NV + i); };
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             mma_bf16_ta(tmem + kTmO, tmem + kTmS + (i & 1) * 64 + 32 + ks * 8,
                         vd + ((ks * 2048) >> 4), kIdescO, ks == 0 ? acc : 1u);
           mma_commit(v_empty(st));
-          mma_commit(o_done);
+          mma_commit(o_done(i & 1));
           acc = 1;
         }
       }
@@ -511,7 +512,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       if (i > 0 && __any_sync(0xffffffffu, move)) {
         // O is at rest once the last step's second product is done
         if (!__all_sync(0xffffffffu,
-                        wait_bar_rest_inl(o_done, (i - 1) & 1u, abort_flag,
+                        wait_bar_rest_inl(o_done((i - 1) & 1),
+                                          ((i - 1) >> 1) & 1u, abort_flag,
                                       p.status)))
           goto done;
         tc_fence_after();
@@ -577,8 +579,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     }
     // ---------------- o = O / l ----------------
     for (int i = max(n - 2, 0); i < n; ++i)
-      if (!__all_sync(0xffffffffu, wait_bar_rest_inl(o_done, i & 1u, abort_flag,
-                                                 p.status)))
+      if (!__all_sync(0xffffffffu,
+                      wait_bar_rest_inl(o_done(i & 1), (i >> 1) & 1u,
+                                        abort_flag, p.status)))
         goto done;
     tc_fence_after();
     const bool some = l > 0.f || l != l;
