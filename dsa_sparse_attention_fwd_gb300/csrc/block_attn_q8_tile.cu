@@ -48,7 +48,7 @@ struct TileSmem {
   static constexpr int kOffV8 = kOffK + kKStages * kKey;
   static constexpr int kOffV = kOffV8 + kVStages * kKey;
   static constexpr int kOffMeta = kOffV + kVStages * kV16;
-  static constexpr int kOffBar = kOffMeta + kMeta * 4 * 8;
+  static constexpr int kOffBar = kOffMeta + kMeta * 4 * 16;
   // q_full, s_full p_full o_done (two each), then k_full k_empty, v8_full
   // v8_empty, v_full v_empty, meta_full
   static constexpr int kBars = 7 + 2 * kKStages + 4 * kVStages + kMeta;
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + L::kOffMisc);
   volatile int *abort_flag = reinterpret_cast<int *>(smem + L::kOffMisc + 4);
   int *sCount = reinterpret_cast<int *>(smem + L::kOffMisc + 8);
-  int2 *meta = reinterpret_cast<int2 *>(smem + L::kOffMeta);  // {ek, ev}
+  // of 16 keys: 2^ek, ev, 2^-ev
+  float4 *meta = reinterpret_cast<float4 *>(smem + L::kOffMeta);
   uint32_t *words = reinterpret_cast<uint32_t *>(smem + L::kOffWords);
   uint16_t *list = reinterpret_cast<uint16_t *>(words + p.nblk);
 
@@ -274,8 +275,11 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         const Look cur = next;
         next = look(i + 1);
         const bool loads = lane < 4 && (lane * 16 & ((1 << lu) - 1)) == 0;
-        if (lane < 4)
-          meta[(i % kMeta) * 4 + lane] = make_int2(q8_exp(cur.ks), q8_exp(cur.vs));
+        if (lane < 4) {
+          const int ev = q8_exp(cur.vs);
+          meta[(i % kMeta) * 4 + lane] =
+              make_float4(q8_pow2(q8_exp(cur.ks)), (float)ev, q8_pow2(-ev), 0.f);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(meta_full(i % kMeta));
 #pragma unroll
@@ -345,6 +349,21 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     const int ct = tid - 128;
     constexpr int kPer = D / 32;  // 16-byte pieces of a thread: half a row
     const int row = ct >> 1, half = ct & 1;
+    // pieces of a row's half, the two halves in another order each: no bank
+    // conflicts; a piece of 16 bytes becomes two of 8 fp16, 64 a row of 128
+    // bytes
+    uint32_t from[kPer], to[kPer][2];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) {
+      const int ch = half * kPer + (D == 128 ? c ^ (half << 1) : c ^ half);
+      from[c] = row * D + ((D == 128 ? ch ^ (row & 7) : ch ^ (row >> 1 & 3)) << 4);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int piece = ch * 2 + u;
+        to[c][u] = (piece >> 3) * (kKeys * 128) + row * 128 +
+                   (((piece & 7) ^ (row & 7)) << 4);
+      }
+    }
     for (int i = 0; i < n; ++i) {
       const int st = i % NV;
       const uint32_t ph = i / NV & 1u;
@@ -352,15 +371,12 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       const bool zero = ((t0 + i) << lupt) + (row >> lu) >= units ||
                         key_at(t0 + i, row) > pos_hi;
       if (!__all_sync(0xffffffffu, wait_bar_rest_inl(v8_full(st), ph, abort_flag,
-                                                 p.status)))
+                                                     p.status)))
         goto done;
       uint4 x[kPer];
-      // the halves in another order each: no bank conflicts
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
-        const int ch = half * kPer + (D == 128 ? c ^ (half << 1) : c ^ half);
-        const uint32_t sw = D == 128 ? ch ^ (row & 7) : ch ^ (row >> 1 & 3);
-        const float4 v = ld_shared_v4f(sV8(st) + row * D + sw * 16);
+        const float4 v = ld_shared_v4f(sV8(st) + from[c]);
         x[c] = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y),
                           __float_as_uint(v.z), __float_as_uint(v.w));
         if (zero) x[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -368,21 +384,17 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(v8_empty(st));
       if (!__all_sync(0xffffffffu, wait_bar_rest_inl(v_empty(st), ph ^ 1u,
-                                                 abort_flag, p.status)))
+                                                     abort_flag, p.status)))
         goto done;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
-        const int ch = half * kPer + (D == 128 ? c ^ (half << 1) : c ^ half);
         const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t h[4];
           q8_half4(w[2 * u], h[0], h[1]);
           q8_half4(w[2 * u + 1], h[2], h[3]);
-          const int piece = ch * 2 + u;  // of 8 fp16: 64 a row of 128 bytes
-          st_shared_v4(sV(st) + (piece >> 3) * (kKeys * 128) + row * 128 +
-                           (((piece & 7) ^ (row & 7)) << 4),
-                       h);
+          st_shared_v4(sV(st) + to[c][u], h);
         }
       }
       fence_proxy_async_smem();
@@ -473,7 +485,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                                     p.status)))
         goto done;
       tc_fence_after();
-      const int2 *mt = meta + (i % kMeta) * 4;
+      const float4 *mt = meta + (i % kMeta) * 4;
+      float a16[4], e16[4];  // of 16 keys: c 2^ek, ev
       uint32_t u[2][32];
       float mx = neg_inf;
       if (held[0] || held[1]) {
@@ -501,8 +514,10 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                                  __uint_as_float(u[c][x + 3])));
             }
             // a row holds all 16 keys or none, or they are hidden above
-            const int2 s = mt[2 * c + g];
-            const float top = fmaf(fmaxf(a, e), cr * q8_pow2(s.x), (float)s.y);
+            const float4 s = mt[2 * c + g];
+            a16[2 * c + g] = cr * s.x;
+            e16[2 * c + g] = s.y;
+            const float top = fmaf(fmaxf(a, e), a16[2 * c + g], s.y);
             if (mask[c] & (0xffffu << (16 * g))) mx = fmaxf(mx, top);
           }
         }
@@ -545,11 +560,11 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         if (held[c]) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const int2 s = mt[2 * c + g];
-            const float a = cr * q8_pow2(s.x);
+            const float a = a16[2 * c + g];
             // -inf takes the weights of keys that the row does not hold to 0
             const float sub =
-                mask[c] & (0xffffu << (16 * g)) ? (float)s.y - mu : neg_inf;
+                mask[c] & (0xffffu << (16 * g)) ? e16[2 * c + g] - mu
+                                                : neg_inf;
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int x = 16 * g; x < 16 * g + 16; x += 2) {
@@ -563,7 +578,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                   : "=r"(pk[x >> 1])
                   : "f"(e.y), "f"(e.x));
             }
-            l = fmaf(sum.x + sum.y, q8_pow2(-s.y), l);
+            l = fmaf(sum.x + sum.y, mt[2 * c + g].z, l);
           }
         } else {
 #pragma unroll
