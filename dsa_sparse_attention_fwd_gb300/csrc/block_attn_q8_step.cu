@@ -40,13 +40,19 @@
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;                      // that multiply
-constexpr int kFeeders = 4;                    // warps that load for them
-constexpr int kThreads = (kWarps + kFeeders) * 32;
+constexpr int kFeeders = 4;  // warps that load
+// Warps that multiply, and how many registers of a thread move to them from
+// those that load (setmaxnreg; 384 threads are launched with 168 each).  Twelve
+// warps with 144 registers were 8% slower: the spills cost more than they hide.
+constexpr int kWarps = 8, kThreads = (kWarps + kFeeders) * 32;
+constexpr int kMulRegs = 216, kFeederRegs = 72;
+static_assert(kWarps * kMulRegs + kFeeders * kFeederRegs <=
+                  (kWarps + kFeeders) * 168,
+              "registers move, there are no more of them");
 constexpr int kKeys = 32;                      // of a step
 constexpr int kPitch = 36;                     // floats of a row in the join
-// A CTA's slice has at least so many steps: one a warp.
-constexpr int kMinSteps = kWarps;
+// A CTA's slice has at least so many steps.
+constexpr int kMinSteps = 8;
 // The counts of written parts: a byte for each CTA, in the 256 bytes that
 // every entry point leaves to the status word.
 constexpr int kDoneOffset = 64;
@@ -90,10 +96,19 @@ struct StepSmem {
   static constexpr int kQ = MT > 1 ? MT * 16 * D * 2 : 0;
   static int bytes(int stages, int nblk, int cap) {
     return stages * kWarps * (kStage + 2 * (int)sizeof(Sub) + 16) + kJoin +
-           kQ + 2 * (int)sizeof(Entry) + 3 * kWarps * 32 * 4 + 256 +
+           kQ + 2 * (int)sizeof(Entry) + 3 * kWarps * 16 * MT * 4 + 256 +
            (cap ? (nblk + 31) / 32 * 4 + (cap * 2 + 15) / 16 * 16 : 0) + 1024;
   }
 };
+
+template <int R>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4],
                                         uint32_t b0, uint32_t b1) {
@@ -142,16 +157,18 @@ __device__ __forceinline__ Span span_of(const BlockAttnQ8 &p, int b, int s0,
 }
 
 // Steps that an item of sequence b may take: what slices are cut by.
-__device__ __forceinline__ long long steps_bound(const BlockAttnQ8 &p,
-                                                 const StepPlan &pl, int b) {
+// (2^shift steps count as one.)
+__device__ __forceinline__ unsigned steps_bound(const BlockAttnQ8 &p,
+                                                const StepPlan &pl, int b,
+                                                int shift) {
   const Span r = span_of(p, b, 0, p.S - 1);
-  long long keys = (long long)r.hi + 1 - (pl.all ? r.lo : 0);
-  if (!pl.all) keys = min(keys, (long long)(p.topk + p.local) << p.lb);
-  return max(1ll, (keys + kKeys - 1) / kKeys);
+  int keys = r.hi + 1 - (pl.all ? r.lo : 0);
+  if (!pl.all) keys = min(keys, (p.topk + p.local) << p.lb);
+  return ((unsigned)max(keys - 1, 0) >> (5 + shift)) + 1u;
 }
 
-// Out of line: it is rare.
-__device__ __noinline__ void redo_row(const BlockAttnQ8 &p, int b, int s,
+// (Inlined, rare as it is: kernels with setmaxnreg make no calls.)
+__device__ __forceinline__ void redo_row(const BlockAttnQ8 &p, int b, int s,
                                       int hk, long long at, float *qs,
                                       int lane) {
   __syncwarp();
@@ -187,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   at += NS * kWarps * 2 * sizeof(Sub);
   Entry *entries = reinterpret_cast<Entry *>(at);
   at += 2 * sizeof(Entry);
-  float *row_m = reinterpret_cast<float *>(at);  // [warp][32]
-  float *row_l = row_m + kWarps * 32;
-  float *row_f = row_l + kWarps * 32;
-  at += 3 * kWarps * 32 * 4;
+  float *row_m = reinterpret_cast<float *>(at);  // [warp][kRows]
+  float *row_l = row_m + kWarps * kRows;
+  float *row_f = row_l + kWarps * kRows;
+  at += 3 * kWarps * kRows * 4;
   const uint32_t bars = smem_u32(at);
   at += NS * kWarps * 16;
   volatile int *abort_flag = reinterpret_cast<int *>(at);
@@ -230,38 +247,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= kWarps) {
     // ---------------- the warps that load ----------------
-    // Each serves two of the eight; all walk the slice together.
+    // Each serves some of the others; all walk the slice together.
     constexpr int kServe = kWarps / kFeeders;
     const int fw = warp - kWarps, ft = tid - kWarps * 32;
-    // the sequences' steps, and this CTA's slice of them all
+    regs_fewer<kFeederRegs>();
+    // the sequences' steps, and this CTA's slice of them all: [u0, u1)
     const int per = (p.B + 31) / 32;
-    long long mine = 0;
-    for (int b = lane * per; b < min(p.B, lane * per + per); ++b)
-      mine += steps_bound(p, pl, b) * pl.items_b;
-    long long before = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += x;
+    int shift = 0;
+    unsigned mine, all, before;
+    for (;; ++shift) {  // (sums below 2^31: steps are counted by two, four ..)
+      unsigned long long sum = 0;
+      for (int b = lane * per; b < min(p.B, lane * per + per); ++b)
+        sum += (unsigned long long)steps_bound(p, pl, b, shift) *
+               (unsigned)pl.items_b;
+      unsigned long long upto = sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const unsigned long long t = __shfl_sync(0xffffffffu, upto, 31);
+      mine = (unsigned)sum, before = (unsigned)(upto - sum), all = (unsigned)t;
+      if (t < (1ull << 31) || shift == 16) break;
     }
-    const long long all = __shfl_sync(0xffffffffu, before, 31);
-    before -= mine;
-    const long long ctas =
-        min((long long)gridDim.x, (all + kMinSteps - 1) / kMinSteps);
-    const long long cta = blockIdx.x;
-    const long long u0 = cta < ctas ? all * cta / ctas : all;
-    const long long u1 = cta < ctas ? all * (cta + 1) / ctas : all;
+    const unsigned ctas = min(gridDim.x, max(all / kMinSteps, 1u));
+    const unsigned share = all / ctas, more = all % ctas;
+    // all c / ctas, rounded down.  (The first slices one longer than the rest
+    // would put whole pages between CTAs now and then, all of them at one place
+    // of their pages: 131072 keys of one sequence took 60 us instead of 53.)
+    auto begin_of = [&](unsigned c) { return c * share + c * more / ctas; };
+    const unsigned cta = blockIdx.x;
+    const unsigned u0 = cta < ctas ? begin_of(cta) : all;
+    const unsigned u1 = cta < ctas ? begin_of(cta + 1) : all;
     // the CTA that holds step u of them all
-    auto holder = [&](long long u) {
-      long long c = (u * ctas + ctas - 1) / all;
-      while (c > 0 && all * c / ctas > u) --c;
-      while (c + 1 < ctas && all * (c + 1) / ctas <= u) ++c;
-      return (int)c;
+    auto holder = [&](unsigned u) {
+      int c = (int)((float)u / (float)all * (float)ctas);
+      c = min(c, (int)ctas - 1);
+      while (c > 0 && begin_of(c) > u) --c;
+      while (c + 1 < (int)ctas && begin_of(c + 1) <= u) ++c;
+      return c;
     };
     int b = 0;
-    long long w = u0, w_b = 0;  // position, and where sequence b begins
+    unsigned w = u0, w_b = 0;  // position, and where sequence b begins
     if (u0 < u1) {
-      const unsigned here = __ballot_sync(
-          0xffffffffu, before <= u0 && u0 < before + mine);
+      const unsigned here =
+          __ballot_sync(0xffffffffu, before <= u0 && u0 - before < mine);
       const int src = __ffs(here) - 1;
       b = src * per;
       w_b = __shfl_sync(0xffffffffu, before, src);
@@ -269,15 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     int entry = 0, g0 = 0;  // items, and steps before this item's
     bool bad = false, ok = true;
     while (w < u1) {
-      const long long U = steps_bound(p, pl, b);
+      const unsigned U = steps_bound(p, pl, b, shift);
       if (w - w_b >= U * pl.items_b) {
         w_b += U * pl.items_b;
         ++b;
         continue;
       }
       const int idx = (int)((w - w_b) / U);
-      const long long w_i = w_b + idx * U;
-      const long long x0 = w - w_i, x1 = min(U, x0 + (u1 - w));
+      const unsigned w_i = w_b + idx * U;
+      const unsigned x0 = w - w_i, x1 = min(U, x0 + (u1 - w));
       w += x1 - x0;
       const int tile = idx % pl.tiles;
       const int s = pl.all ? 0 : idx / pl.tiles % p.S;
@@ -324,12 +353,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         units = count << (p.lb - (pl.box == 32 ? 5 : 4));
       }
       const int per_step = kKeys / pl.box;
-      const int steps = (units + per_step - 1) / per_step;
-      const int t0 = (int)(steps * x0 / U), t1 = (int)(steps * x1 / U);
+      const unsigned steps = (units + per_step - 1) / per_step;
+      // (below 2^32: an item has at most 2^16 steps)
+      const int t0 = (int)(steps * x0 / U);
+      const int t1 = (int)(x1 == U ? steps : steps * x1 / U);
       const int g1 = g0 + t1 - t0;
       if (fw == 0) {  // tell the others
         ok = __all_sync(0xffffffffu,
-                        ok && wait_bar(item_empty(entry & 1),
+                        ok && wait_bar_inl(item_empty(entry & 1),
                                        (entry >> 1 & 1) ^ 1, abort_flag,
                                        p.status));
         if (ok && lane == 0) {
@@ -402,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int wp = g % kWarps, turn = g / kWarps;
           const int st = turn % NS;
           if (!__all_sync(0xffffffffu,
-                          wait_bar(empty(wp, st), (turn / NS & 1) ^ 1,
+                          wait_bar_inl(empty(wp, st), (turn / NS & 1) ^ 1,
                                    abort_flag, p.status))) {
             ok = false;
             break;
@@ -432,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no more
     if (fw == 0 && ok &&
         __all_sync(0xffffffffu,
-                   wait_bar(item_empty(entry & 1), (entry >> 1 & 1) ^ 1,
+                   wait_bar_inl(item_empty(entry & 1), (entry >> 1 & 1) ^ 1,
                             abort_flag, p.status))) {
       if (lane == 0) {
         entries[entry & 1].n = -1;
@@ -440,12 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------- the eight warps that multiply ----------------
+    // ---------------- the warps that multiply ----------------
+    regs_more<kMulRegs>();
     const int gq = lane >> 2, tq = lane & 3;
     const float c2 = p.scale * 1.4426950408889634f;
     for (int entry = 0;; ++entry) {
       const bool got = __all_sync(
-          0xffffffffu, wait_bar(item_full(entry & 1), entry >> 1 & 1,
+          0xffffffffu, wait_bar_inl(item_full(entry & 1), entry >> 1 & 1,
                                 abort_flag, p.status));
       // (all stop together; and the item before has left shared memory)
       if (named_bar_or(1, kWarps * 32, !got)) break;
@@ -545,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (; ok && g < g1; g += kWarps) {
         const int turn = g / kWarps, st = turn % NS;
-        if (!__all_sync(0xffffffffu, wait_bar(full(warp, st), turn / NS & 1,
+        if (!__all_sync(0xffffffffu, wait_bar_inl(full(warp, st), turn / NS & 1,
                                               abort_flag, p.status))) {
           ok = false;
           break;
@@ -727,8 +759,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           s += __shfl_xor_sync(0xffffffffu, s, 1);
           s += __shfl_xor_sync(0xffffffffu, s, 2);
           if (tq == 0) {
-            row_m[warp * 32 + mt * 16 + gq + 8 * i] = m[mt][i];
-            row_l[warp * 32 + mt * 16 + gq + 8 * i] = s;
+            row_m[warp * kRows + mt * 16 + gq + 8 * i] = m[mt][i];
+            row_l[warp * kRows + mt * 16 + gq + 8 * i] = s;
           }
         }
       named_bar_sync(1, kWarps * 32);
@@ -745,18 +777,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid < kRows) {
         float M = neg_inf, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, row_m[i * 32 + tid]);
+        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, row_m[i * kRows + tid]);
         const float mu = M > neg_inf ? M : 0.f;
         float f[kWarps];
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-          f[i] = ex2(row_m[i * 32 + tid] - mu);
-          sum = fmaf(row_l[i * 32 + tid], f[i], sum);
+          f[i] = ex2(row_m[i * kRows + tid] - mu);
+          sum = fmaf(row_l[i * kRows + tid], f[i], sum);
         }
         const bool some = sum > 0.f || sum != sum;
         const float inv = some ? 1.f / sum : 0.f;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) row_f[i * 32 + tid] = f[i] * inv;
+        for (int i = 0; i < kWarps; ++i) row_f[i * kRows + tid] = f[i] * inv;
         row_lse[tid] = some ? M + log2f(sum) : neg_inf;
         if ((sum != sum || sum > 3e38f) && tid < live)
           atomicOr(odd_rows, 1u << tid);
@@ -764,20 +796,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_bar_sync(1, kWarps * 32);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const float f0 = row_f[warp * 32 + mt * 16 + gq];
-        const float f1 = row_f[warp * 32 + mt * 16 + gq + 8];
-        // columns 2 tq and 2 tq + 1 of tile n are elements (2 tq) D / 8 + n
-        // and the next D / 8: eight tiles and one column a round
+        const float f0 = row_f[warp * kRows + mt * 16 + gq];
+        const float f1 = row_f[warp * kRows + mt * 16 + gq + 8];
+        // Columns 2 tq and 2 tq + 1 of tile n are elements (2 tq) D / 8 + n
+        // and the next D / 8.  A round takes eight tiles: one of the columns
+        // of 16 rows, or both of 8 where there are no more.
+        const bool few = live - mt * 16 <= 8;
 #pragma unroll
         for (int rd = 0; rd < D / 32; ++rd) {
           const int cc = rd & 1, nh = rd >> 1;
+          if (few && cc) continue;
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             float4 v[2];
             float *vv = reinterpret_cast<float *>(v);
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-              vv[n] = o[mt][nh * 8 + n][2 * i + cc] * (i ? f1 : f0);
+            for (int n = 0; n < 8; ++n) {
+              const float *x = o[mt][nh * 8 + n];
+              vv[n] = few ? x[i] * f0 : x[2 * i + cc] * (i ? f1 : f0);
+            }
             float4 *dst = reinterpret_cast<float4 *>(
                 join + (warp * 16 + gq + 8 * i) * kPitch + tq * 8);
             dst[0] = v[0];
@@ -793,8 +830,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   join + (i * 16 + r) * kPitch + c);
               sum.x += v.x, sum.y += v.y;
             }
-            const int d = (2 * (c >> 3) + cc) * (D / 8) + nh * 8 + (c & 7);
-            const int row = mt * 16 + r;
+            const int col = few ? r >> 3 : cc;
+            const int d = (2 * (c >> 3) + col) * (D / 8) + nh * 8 + (c & 7);
+            const int row = mt * 16 + (few ? r & 7 : r);
             if (row < live) {
               if (!(fabsf(sum.x) <= 3e38f && fabsf(sum.y) <= 3e38f))
                 atomicOr(odd_rows, 1u << row);
@@ -915,8 +953,9 @@ int launch(const BlockAttnQ8 &p, StepPlan &pl, const Maps8 &maps, int ctas,
            cudaStream_t st) {
   using L = StepSmem<D, MT>;
   auto kern = attn_q8_step_kernel<D, MT>;
-  // as many stages as there is room for beside the block list
-  for (pl.stages = D == 64 ? 5 : 3;; --pl.stages) {
+  // as many stages as there is room for beside the block list (two at 128
+  // dimensions hold 128 KB; three are no faster)
+  for (pl.stages = D == 64 ? 4 : 2;; --pl.stages) {
     if (L::bytes(pl.stages, p.nblk, pl.cap) <= kMaxSmem) break;
     if (pl.stages == 1) return DSA_ERR_UNSUPPORTED;
   }
