@@ -45,12 +45,14 @@ constexpr int kFeeders = 4;  // warps that load
 // those that load (setmaxnreg; 384 threads are launched with 168 each).  Twelve
 // warps with 144 registers were 8% slower: the spills cost more than they hide.
 constexpr int kWarps = 8, kThreads = (kWarps + kFeeders) * 32;
-constexpr int kMulRegs = 216, kFeederRegs = 72;
-static_assert(kWarps * kMulRegs + kFeeders * kFeederRegs <=
-                  (kWarps + kFeeders) * 168,
+constexpr int mul_regs(int mt) { return mt == 1 ? 192 : 200; }
+constexpr int feeder_regs(int mt) { return mt == 1 ? 120 : 104; }
+static_assert(kWarps * mul_regs(1) + kFeeders * feeder_regs(1) <=
+                      (kWarps + kFeeders) * 168 &&
+                  kWarps * mul_regs(2) + kFeeders * feeder_regs(2) <=
+                      (kWarps + kFeeders) * 168,
               "registers move, there are no more of them");
-constexpr int kKeys = 32;                      // of a step
-constexpr int kPitch = 36;                     // floats of a row in the join
+constexpr int kKeys = 32;  // of a step
 // A CTA's slice has at least so many steps.
 constexpr int kMinSteps = 8;
 // The counts of written parts: a byte for each CTA, in the 256 bytes that
@@ -89,17 +91,35 @@ struct Sub {
   int ek, ev, j0, seen;
 };
 
+// A tile's rows as the loading warps prepare them: their queries as MMA
+// operands (16-bit, after a power of two), the factor c times that power's
+// inverse, the last and the first key that they see.
+template <int D, int MT>
+struct Rows {
+  uint4 q[D / 16][MT][32];
+  float cr[MT * 16];
+  int pos[MT * 16], lo[MT * 16];
+};
+
 template <int D, int MT>
 struct StepSmem {
   static constexpr int kStage = 2 * kKeys * D;  // K, then V
-  static constexpr int kJoin = kWarps * 16 * kPitch * 4;
-  static constexpr int kQ = MT > 1 ? MT * 16 * D * 2 : 0;
+  // Floats of a row when the warps' outputs are added up: 8 runs of D / 8, each
+  // in an order (run_at) that keeps a warp's 16-byte pieces in different banks.
+  static constexpr int kPitch = D == 128 ? 144 : 72;
+  static constexpr int kSum = kWarps * 16 * kPitch * 4;
   static int bytes(int stages, int nblk, int cap) {
-    return stages * kWarps * (kStage + 2 * (int)sizeof(Sub) + 16) + kJoin +
-           kQ + 2 * (int)sizeof(Entry) + 3 * kWarps * 16 * MT * 4 + 256 +
+    return stages * kWarps * (kStage + 2 * (int)sizeof(Sub) + 16) + kSum +
+           2 * (int)sizeof(Rows<D, MT>) + 4 * (int)sizeof(Entry) +
+           2 * kWarps * 16 * MT * 4 + kWarps * 512 + 128 +
            (cap ? (nblk + 31) / 32 * 4 + (cap * 2 + 15) / 16 * 16 : 0) + 1024;
   }
 };
+// Place of the 16-byte piece k of run q (of 8) of a row.
+template <int D>
+__device__ __forceinline__ int run_at(int q, int k) {
+  return D == 128 ? 4 * q + (k ^ (q >> 1)) : 2 * q + (k ^ (q >> 2));
+}
 
 template <int R>
 __device__ __forceinline__ void regs_more() {
@@ -196,26 +216,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const int NS = pl.stages;
   uint8_t *at = smem + NS * kWarps * L::kStage;
-  float *join = reinterpret_cast<float *>(at);
-  at += L::kJoin;
-  uint4 *qf = reinterpret_cast<uint4 *>(at);  // MT > 1: Q as MMA operands
-  at += L::kQ;
+  float *sums = reinterpret_cast<float *>(at);
+  at += L::kSum;
+  Rows<D, MT> *rows_of_entry = reinterpret_cast<Rows<D, MT> *>(at);  // [2]
+  at += 2 * sizeof(Rows<D, MT>);
   Sub *subs = reinterpret_cast<Sub *>(at);
   at += NS * kWarps * 2 * sizeof(Sub);
-  Entry *entries = reinterpret_cast<Entry *>(at);
-  at += 2 * sizeof(Entry);
+  Entry *entries = reinterpret_cast<Entry *>(at);  // [2]
+  Entry *waiting = entries + 2;                    // [2], see below
+  at += 4 * sizeof(Entry);
   float *row_m = reinterpret_cast<float *>(at);  // [warp][kRows]
   float *row_l = row_m + kWarps * kRows;
-  float *row_f = row_l + kWarps * kRows;
-  at += 3 * kWarps * kRows * 4;
+  at += 2 * kWarps * kRows * 4;
+  float *qs = reinterpret_cast<float *>(at) + (threadIdx.x >> 5) % kWarps * 128;
+  at += kWarps * 512;
   const uint32_t bars = smem_u32(at);
   at += NS * kWarps * 16;
   volatile int *abort_flag = reinterpret_cast<int *>(at);
-  unsigned *odd_rows = reinterpret_cast<unsigned *>(at + 4);
-  int *joined = reinterpret_cast<int *>(at + 8);
-  float *row_lse = reinterpret_cast<float *>(at + 64);  // [32]
+  int *joined = reinterpret_cast<int *>(at + 8);  // [2]
   const uint32_t item_bars = smem_u32(at + 16);
-  at += 64 + 32 * 4 + 64;
+  at += 128;
   uint32_t *bitmap = reinterpret_cast<uint32_t *>(at);
   uint16_t *list = reinterpret_cast<uint16_t *>(bitmap + (p.nblk + 31) / 32);
   auto full = [&](int w, int st) { return bars + (w * NS + st) * 16; };
@@ -233,12 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars + i * 16 + 8, 1);
     }
     for (int e = 0; e < 2; ++e) {
-      mbar_init(item_full(e), 1);
+      mbar_init(item_full(e), kFeeders);
       mbar_init(item_empty(e), kWarps);
     }
     *abort_flag = 0;
-    *odd_rows = 0;
-    joined[1] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
@@ -250,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each serves some of the others; all walk the slice together.
     constexpr int kServe = kWarps / kFeeders;
     const int fw = warp - kWarps, ft = tid - kWarps * 32;
-    regs_fewer<kFeederRegs>();
+    regs_fewer<feeder_regs(MT)>();
     // the sequences' steps, and this CTA's slice of them all: [u0, u1)
     const int per = (p.B + 31) / 32;
     int shift = 0;
@@ -358,27 +376,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t0 = (int)(steps * x0 / U);
       const int t1 = (int)(x1 == U ? steps : steps * x1 / U);
       const int g1 = g0 + t1 - t0;
-      if (fw == 0) {  // tell the others
-        ok = __all_sync(0xffffffffu,
-                        ok && wait_bar_inl(item_empty(entry & 1),
-                                       (entry >> 1 & 1) ^ 1, abort_flag,
-                                       p.status));
-        if (ok && lane == 0) {
-          Entry &e = entries[entry & 1];
-          e.n = t1 - t0;
-          e.g0 = g0;
-          e.b = b, e.hk = hk, e.s = s, e.tile = tile;
-          e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
-          e.c0 = e.c1 = (int)cta;
-          if (e.slot >= 0) {
-            e.c0 = x0 == 0 ? (int)cta : holder(w_i);
-            e.c1 = x1 == U ? (int)cta : holder(w_i + U - 1);
-          }
-          mbar_arrive(item_full(entry & 1));
+      // the queries of the first 16 rows, on the way
+      const int gq = lane >> 2, tq = lane & 3;
+      uint4 raw[2][D / 32];
+      auto row_of = [&](int r, int &rs, int &rh) {
+        const int rr = tile * kRows + r;
+        rs = pl.all ? rr / p.G : s;
+        rh = hk * p.G + (pl.all ? rr - rs * p.G : rr);
+        return rr < pl.rows;
+      };
+      auto fetch = [&](int mt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          int rs, rh;
+          const bool live = row_of(mt * 16 + gq + 8 * i, rs, rh);
+          const uint4 *src = reinterpret_cast<const uint4 *>(
+              p.q + (((long long)rs * p.B + b) * p.H + rh) * D + 16 * tq);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c)  // elements 64 c/2 + 16 tq ..
+            raw[i][c] = live ? __ldg(src + (c >> 1) * 8 + (c & 1))
+                             : make_uint4(0u, 0u, 0u, 0u);
         }
-        __syncwarp();
-      }
-      ++entry;
+      };
+      fetch(0);
+
       // 16 steps of this warp's at a time: lane 2 i + j holds the 16 keys j of
       // the i-th; those of steps are g = 8 n + kServe fw + 0, 1
       auto step_of = [&](int k) {
@@ -422,6 +443,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         return r;
       };
       Look next = look(k0);
+      // tell the others: the item, and its rows
+      ok = __all_sync(0xffffffffu,
+                      ok && wait_bar_inl(item_empty(entry & 1),
+                                         (entry >> 1 & 1) ^ 1, abort_flag,
+                                         p.status));
+      if (ok) {
+        Rows<D, MT> &rw = rows_of_entry[entry & 1];
+        if (fw == 0 && lane == 0) {
+          Entry &e = entries[entry & 1];
+          e.n = t1 - t0;
+          e.g0 = g0;
+          e.b = b, e.hk = hk, e.s = s, e.tile = tile;
+          e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
+          e.c0 = e.c1 = (int)cta;
+          if (e.slot >= 0) {
+            e.c0 = x0 == 0 ? (int)cta : holder(w_i);
+            e.c1 = x1 == U ? (int)cta : holder(w_i + U - 1);
+          }
+        }
+        for (int r = fw * 32 + lane; r < kRows; r += kFeeders * 32) {
+          int rs, rh;
+          const bool live = row_of(r, rs, rh);
+          const long long ps = live ? row_pos(p.q_pos, b, rs) : -1;
+          rw.pos[r] = ps < 0 ? -1 : (int)min(ps, (long long)p.T - 1);
+          rw.lo[r] = pl.all && live
+                         ? (int)min(max(((ps >> p.lb) - p.local + 1) << p.lb,
+                                        0ll),
+                                    (long long)p.T)
+                         : 0;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (mt > 0) fetch(mt);
+          float f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const uint32_t u[4] = {raw[i][c].x, raw[i][c].y, raw[i][c].z,
+                                     raw[i][c].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(u[k] << 16)),
+                                       fabsf(__uint_as_float(u[k] & 0xffff0000u))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the largest value to [2^14, 2^15)
+            int eq = (__float_as_int(top) >> 23) - 127 - 14;
+            eq = min(max(eq, -100), 100);
+            f[i] = q8_pow2(-eq);
+            if (fw == 0 && tq == 0)
+              rw.cr[mt * 16 + gq + 8 * i] =
+                  p.scale * 1.4426950408889634f * q8_pow2(eq);
+          }
+          // operand ks: elements 64 (ks / 4) + 16 tq + 4 (ks % 4) .. + 3; two
+          // words of piece ks / 2
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            if (ks % kFeeders != fw) continue;
+            uint32_t a[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 &v = raw[i][ks >> 1];
+              const uint32_t w0 = ks & 1 ? v.z : v.x, w1 = ks & 1 ? v.w : v.y;
+              a[i] = pack_half2(__uint_as_float(w0 << 16) * f[i],
+                                __uint_as_float(w0 & 0xffff0000u) * f[i]);
+              a[2 + i] = pack_half2(__uint_as_float(w1 << 16) * f[i],
+                                    __uint_as_float(w1 & 0xffff0000u) * f[i]);
+            }
+            rw.q[ks][mt][lane] = make_uint4(a[0], a[1], a[2], a[3]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(item_full(entry & 1));
+      }
+      ++entry;
       for (int k = k0; ok && k < k1; k += 16) {
         const Look cur = next;
         if (k + 16 < k1) next = look(k + 16);
@@ -461,99 +560,142 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (bad) atomicOr(p.status, kStatusIndexRange);
     // no more
-    if (fw == 0 && ok &&
-        __all_sync(0xffffffffu,
-                   wait_bar_inl(item_empty(entry & 1), (entry >> 1 & 1) ^ 1,
-                            abort_flag, p.status))) {
+    if (ok && __all_sync(0xffffffffu,
+                         wait_bar_inl(item_empty(entry & 1),
+                                      (entry >> 1 & 1) ^ 1, abort_flag,
+                                      p.status))) {
       if (lane == 0) {
-        entries[entry & 1].n = -1;
+        if (fw == 0) entries[entry & 1].n = -1;
         mbar_arrive(item_full(entry & 1));
       }
     }
   } else {
     // ---------------- the warps that multiply ----------------
-    regs_more<kMulRegs>();
+    regs_more<mul_regs(MT)>();
     const int gq = lane >> 2, tq = lane & 3;
-    const float c2 = p.scale * 1.4426950408889634f;
+    // Joins the parts of an item that several CTAs share: the one that finished
+    // last, o = sum_i w_i o_i / sum_i w_i with w_i = 2^(l_i - max).
+    auto join_item = [&](const Entry &e) {
+      const int parts = e.c1 - e.c0 + 1;
+      const int first = e.tile * kRows, live = min(pl.rows - first, kRows);
+      constexpr int kLanes = D / 4;  // threads of a row: a warp or half of one
+      const int c = tid % kLanes;
+      // (whole warps stay in the loop: they vote)
+      for (int r0 = tid / 32 * (32 / kLanes); r0 < live;
+           r0 += kWarps * 32 / kLanes) {
+        const int r = r0 + lane / kLanes;
+        const bool mine = r < live;
+        float M = neg_inf, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        bool again = false;
+        for (int i0 = 0; i0 < parts; i0 += 8) {
+          float ls[8];
+          float4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = min(i0 + u, parts - 1);
+            const size_t a = ((size_t)(e.c0 + i) * 2 + (i == 0 ? 1 : 0)) * 32 +
+                             (mine ? r : 0);
+            ls[u] = __ldcg(pl.part_l + a);
+            v[u] = __ldcg(
+                reinterpret_cast<const float4 *>(pl.part_o + a * D) + c);
+            if (i0 + u >= parts) ls[u] = neg_inf;
+          }
+          float mx = M;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            again |= ls[u] != ls[u];
+            mx = fmaxf(mx, ls[u]);
+          }
+          const float ref = mx > neg_inf ? mx : 0.f;
+          const float f = ex2(M - ref);
+          sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const float wt = ex2(ls[u] - ref);
+            sum += wt;
+            acc.x = fmaf(wt, v[u].x, acc.x);
+            acc.y = fmaf(wt, v[u].y, acc.y);
+            acc.z = fmaf(wt, v[u].z, acc.z);
+            acc.w = fmaf(wt, v[u].w, acc.w);
+          }
+          M = mx;
+        }
+        const int rr = first + r;
+        const int s = pl.all ? rr / p.G : e.s;
+        const long long to = ((long long)s * p.B + e.b) * p.H + e.hk * p.G +
+                             (pl.all ? rr - s * p.G : rr);
+        if (mine) {
+          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          reinterpret_cast<uint2 *>(p.o + to * D)[c] =
+              make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                         pack_bf16x2(acc.z * inv, acc.w * inv));
+          if (c == 0)
+            p.lse[to] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994531f
+                                  : neg_inf;
+        }
+        // rows with a part that is not finite
+        unsigned odd = __ballot_sync(0xffffffffu, mine && again && c == 0);
+        for (; odd; odd &= odd - 1) {
+          const int src = __ffs(odd) - 1;
+          redo_row(p, e.b, __shfl_sync(0xffffffffu, s, src), e.hk,
+                   __shfl_sync(0xffffffffu, to, src), qs, lane);
+        }
+      }
+    };
+    // A shared item's part is counted when all have come to the next item, and
+    // joined, if it was the last, at that one's end: its count is on the way
+    // meanwhile.
+    bool shared_item = false;
     for (int entry = 0;; ++entry) {
       const bool got = __all_sync(
           0xffffffffu, wait_bar_inl(item_full(entry & 1), entry >> 1 & 1,
-                                abort_flag, p.status));
+                                    abort_flag, p.status));
       // (all stop together; and the item before has left shared memory)
       if (named_bar_or(1, kWarps * 32, !got)) break;
       const Entry e = entries[entry & 1];
-      if (e.n < 0) break;
+      if (shared_item && warp == (entry & (kWarps - 1))) {
+        if (lane == 0) {
+          const Entry &was = waiting[(entry - 1) & 1];
+          const int sh = 8 * (was.c0 & 3);
+          uint32_t *word = pl.done + (was.c0 >> 2);
+          __threadfence();  // the CTA's parts, before the count
+          const uint32_t had = atomicAdd(word, 1u << sh) >> sh & 0xffu;
+          const bool last = had == (uint32_t)(was.c1 - was.c0);
+          if (last) atomicAnd(word, ~(0xffu << sh));  // for the next call
+          __threadfence();
+          joined[entry & 1] = last;
+        }
+        __syncwarp();
+      }
+      if (e.n < 0) {
+        if (shared_item) {
+          named_bar_sync(1, kWarps * 32);
+          if (joined[entry & 1]) join_item(waiting[(entry - 1) & 1]);
+        }
+        break;
+      }
       // this thread's rows: gq and gq + 8 of each 16
+      const Rows<D, MT> &rw = rows_of_entry[entry & 1];
       int pos[MT][2], lo[MT][2];
-      long long out_row[MT][2];  // -1: none
-      float cr[MT][2];           // c 2^(the query's power of two)
+      float cr[MT][2];
       uint32_t qr[MT == 1 ? D / 16 : 1][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float qv[2][D / 4];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int rr = e.tile * kRows + mt * 16 + gq + 8 * i;
-          const bool live = rr < pl.rows;
-          const int s = pl.all ? rr / p.G : e.s;
-          const int h = e.hk * p.G + (pl.all ? rr % p.G : rr);
-          out_row[mt][i] =
-              live ? ((long long)s * p.B + e.b) * p.H + h : -1;
-          const long long ps = live ? row_pos(p.q_pos, e.b, s) : -1;
-          pos[mt][i] = ps < 0 ? -1 : (int)min(ps, (long long)p.T - 1);
-          lo[mt][i] =
-              pl.all && live
-                  ? (int)min(max(((ps >> p.lb) - p.local + 1) << p.lb, 0ll),
-                             (long long)p.T)
-                  : 0;
-          float top = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            uint4 x[2] = {};
-            if (live) {
-              const uint4 *src = reinterpret_cast<const uint4 *>(
-                  p.q + out_row[mt][i] * D + 64 * c + 16 * tq);
-              x[0] = __ldg(src);
-              x[1] = __ldg(src + 1);
-            }
-            const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w,
-                                   x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              qv[i][c * 16 + 2 * k] = __uint_as_float(u[k] << 16);
-              qv[i][c * 16 + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < D / 4; ++k) top = fmaxf(top, fabsf(qv[i][k]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // the largest value to [2^14, 2^15)
-          int eq = (__float_as_int(top) >> 23) - 127 - 14;
-          eq = min(max(eq, -100), 100);
-          const float f = q8_pow2(-eq);
-#pragma unroll
-          for (int k = 0; k < D / 4; ++k) qv[i][k] *= f;
-          cr[mt][i] = c2 * q8_pow2(eq);
+          const int r = mt * 16 + gq + 8 * i;
+          pos[mt][i] = rw.pos[r], lo[mt][i] = rw.lo[r], cr[mt][i] = rw.cr[r];
         }
-        // operand k of step ks: elements 64 (ks / 4) + 16 tq + 4 (ks % 4) ..
+      if constexpr (MT == 1) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const int k = (ks >> 2) * 16 + (ks & 3) * 4;
-          const uint32_t a[4] = {pack_half2(qv[0][k], qv[0][k + 1]),
-                                 pack_half2(qv[1][k], qv[1][k + 1]),
-                                 pack_half2(qv[0][k + 2], qv[0][k + 3]),
-                                 pack_half2(qv[1][k + 2], qv[1][k + 3])};
-          if constexpr (MT == 1) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) qr[ks][j] = a[j];
-          } else if (ks % kWarps == warp) {
-            qf[(ks * MT + mt) * 32 + lane] =
-                make_uint4(a[0], a[1], a[2], a[3]);
-          }
+          const uint4 v = rw.q[ks][0][lane];
+          qr[ks][0] = v.x, qr[ks][1] = v.y, qr[ks][2] = v.z, qr[ks][3] = v.w;
         }
       }
-      if constexpr (MT > 1) named_bar_sync(1, kWarps * 32);
+      const int first = e.tile * kRows;
+      const int live = min(pl.rows - first, kRows);
       // the tile's rows see the same keys but where a step holds keys after
       // the first row's position or before the last row's first block
       int pos_lo = 0x7fffffff, lo_hi = 0;
@@ -561,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (out_row[mt][i] >= 0) pos_lo = min(pos_lo, pos[mt][i]);
+          if (mt * 16 + gq + 8 * i < live) pos_lo = min(pos_lo, pos[mt][i]);
           lo_hi = max(lo_hi, lo[mt][i]);
         }
       pos_lo = __reduce_min_sync(0xffffffffu, pos_lo);
@@ -612,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[mt][i] = qr[c * 4 + j][i];
               } else {
-                const uint4 v = qf[((c * 4 + j) * MT + mt) * 32 + lane];
+                const uint4 v = rw.q[c * 4 + j][mt][lane];
                 a[mt][0] = v.x, a[mt][1] = v.y, a[mt][2] = v.z, a[mt][3] = v.w;
               }
             }
@@ -751,197 +893,113 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(empty(warp, st));
       }
       // ---------------- the item's end ----------------
+      // the warps' outputs side by side; one barrier, then 16 threads a row
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt) {
+        if (mt > 0) named_bar_sync(1, kWarps * 32);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float s = l[mt][i];
-          s += __shfl_xor_sync(0xffffffffu, s, 1);
-          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          float t = l[mt][i];
+          t += __shfl_xor_sync(0xffffffffu, t, 1);
+          t += __shfl_xor_sync(0xffffffffu, t, 2);
+          const int r = gq + 8 * i;
           if (tq == 0) {
-            row_m[warp * kRows + mt * 16 + gq + 8 * i] = m[mt][i];
-            row_l[warp * kRows + mt * 16 + gq + 8 * i] = s;
+            row_m[warp * kRows + mt * 16 + r] = m[mt][i];
+            row_l[warp * kRows + mt * 16 + r] = t;
+          }
+          // columns 2 tq and 2 tq + 1 of tile n are element n of the runs 2 tq
+          // and 2 tq + 1
+          if (mt * 16 + r < live) {
+            float4 *dst = reinterpret_cast<float4 *>(
+                sums + (warp * 16 + r) * L::kPitch);
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                dst[run_at<D>(2 * tq + cc, k)] = make_float4(
+                    o[mt][4 * k][2 * i + cc], o[mt][4 * k + 1][2 * i + cc],
+                    o[mt][4 * k + 2][2 * i + cc], o[mt][4 * k + 3][2 * i + cc]);
           }
         }
-      named_bar_sync(1, kWarps * 32);
-      const int first = e.tile * kRows;
-      const int live = min(pl.rows - first, kRows);
-      auto row_at = [&](int r) {
-        const int rr = first + r;
-        const int s = pl.all ? rr / p.G : e.s;
-        return ((long long)s * p.B + e.b) * p.H + e.hk * p.G +
-               (pl.all ? rr % p.G : rr);
-      };
-      const size_t part =
-          ((size_t)blockIdx.x * 2 + (e.slot > 0 ? 1 : 0)) * 32;
-      if (tid < kRows) {
-        float M = neg_inf, sum = 0.f;
+        named_bar_sync(1, kWarps * 32);
+        const int r = mt * 16 + (tid >> 4), j = tid & 15;
+        const bool mine = r < live;
+        float M = neg_inf, sum = 0.f, f[kWarps];
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) M = fmaxf(M, row_m[i * kRows + tid]);
+        for (int i = 0; i < kWarps; ++i)
+          M = fmaxf(M, row_m[i * kRows + r]);
         const float mu = M > neg_inf ? M : 0.f;
-        float f[kWarps];
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-          f[i] = ex2(row_m[i * kRows + tid] - mu);
-          sum = fmaf(row_l[i * kRows + tid], f[i], sum);
+          f[i] = ex2(row_m[i * kRows + r] - mu);
+          sum = fmaf(row_l[i * kRows + r], f[i], sum);
         }
         const bool some = sum > 0.f || sum != sum;
         const float inv = some ? 1.f / sum : 0.f;
+        constexpr int kPer = D / 64;  // 16-byte pieces of a thread
+        float4 acc[kPer];
+        bool odd = sum != sum || sum > 3e38f;
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) row_f[i * kRows + tid] = f[i] * inv;
-        row_lse[tid] = some ? M + log2f(sum) : neg_inf;
-        if ((sum != sum || sum > 3e38f) && tid < live)
-          atomicOr(odd_rows, 1u << tid);
-      }
-      named_bar_sync(1, kWarps * 32);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float f0 = row_f[warp * kRows + mt * 16 + gq];
-        const float f1 = row_f[warp * kRows + mt * 16 + gq + 8];
-        // Columns 2 tq and 2 tq + 1 of tile n are elements (2 tq) D / 8 + n
-        // and the next D / 8.  A round takes eight tiles: one of the columns
-        // of 16 rows, or both of 8 where there are no more.
-        const bool few = live - mt * 16 <= 8;
-#pragma unroll
-        for (int rd = 0; rd < D / 32; ++rd) {
-          const int cc = rd & 1, nh = rd >> 1;
-          if (few && cc) continue;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float4 v[2];
-            float *vv = reinterpret_cast<float *>(v);
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const float *x = o[mt][nh * 8 + n];
-              vv[n] = few ? x[i] * f0 : x[2 * i + cc] * (i ? f1 : f0);
-            }
-            float4 *dst = reinterpret_cast<float4 *>(
-                join + (warp * 16 + gq + 8 * i) * kPitch + tq * 8);
-            dst[0] = v[0];
-            dst[1] = v[1];
-          }
-          named_bar_sync(1, kWarps * 32);
-          {
-            const int r = tid >> 4, c = (tid & 15) * 2;
-            float2 sum = make_float2(0.f, 0.f);
+          for (int k = 0; k < kPer; ++k) {
+            acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int piece = j * kPer + k;  // of the row
+            const int at4 = run_at<D>(piece / (D / 32), piece % (D / 32));
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
-              const float2 v = *reinterpret_cast<const float2 *>(
-                  join + (i * 16 + r) * kPitch + c);
-              sum.x += v.x, sum.y += v.y;
+              const float4 v = reinterpret_cast<const float4 *>(
+                  sums + (i * 16 + (tid >> 4)) * L::kPitch)[at4];
+              acc[k].x = fmaf(v.x, f[i], acc[k].x);
+              acc[k].y = fmaf(v.y, f[i], acc[k].y);
+              acc[k].z = fmaf(v.z, f[i], acc[k].z);
+              acc[k].w = fmaf(v.w, f[i], acc[k].w);
             }
-            const int col = few ? r >> 3 : cc;
-            const int d = (2 * (c >> 3) + col) * (D / 8) + nh * 8 + (c & 7);
-            const int row = mt * 16 + (few ? r & 7 : r);
-            if (row < live) {
-              if (!(fabsf(sum.x) <= 3e38f && fabsf(sum.y) <= 3e38f))
-                atomicOr(odd_rows, 1u << row);
-              if (e.slot < 0)
-                *reinterpret_cast<uint32_t *>(p.o + row_at(row) * D + d) =
-                    pack_bf16x2(sum.x, sum.y);
-              else
-                *reinterpret_cast<float2 *>(
-                    pl.part_o + (part + row) * D + d) = sum;
-            }
+            acc[k].x *= inv, acc[k].y *= inv, acc[k].z *= inv, acc[k].w *= inv;
+            const float top = fmaxf(fmaxf(fabsf(acc[k].x), fabsf(acc[k].y)),
+                                    fmaxf(fabsf(acc[k].z), fabsf(acc[k].w)));
+            odd |= !(top <= 3e38f) || acc[k].x != acc[k].x ||
+                   acc[k].y != acc[k].y || acc[k].z != acc[k].z ||
+                   acc[k].w != acc[k].w;
           }
-          named_bar_sync(1, kWarps * 32);
         }
-      }
-      unsigned odd = *odd_rows;
-      if (tid < live) {
-        if (e.slot < 0)
-          p.lse[row_at(tid)] = row_lse[tid] * 0.69314718055994531f;
-        else  // a NaN tells the joining CTA to compute the row again
-          pl.part_l[part + tid] =
-              odd >> tid & 1u ? __int_as_float(0x7fffffff) : row_lse[tid];
-      }
-      if (e.slot >= 0) {
-        __threadfence();
-        named_bar_sync(1, kWarps * 32);
-        if (tid == 0) {
-          const int sh = 8 * (e.c0 & 3);
-          uint32_t *word = pl.done + (e.c0 >> 2);
-          const uint32_t was = atomicAdd(word, 1u << sh) >> sh & 0xffu;
-          const bool last = was == (uint32_t)(e.c1 - e.c0);
-          if (last) atomicAnd(word, ~(0xffu << sh));  // for the next call
-          __threadfence();
-          *joined = last;
+        const unsigned votes = __ballot_sync(0xffffffffu, mine && odd);
+        odd = (votes >> (lane & 16) & 0xffffu) != 0u;  // any of the row's
+        const float lse2 = some ? M + log2f(sum) : neg_inf;
+        const int rr = first + r;
+        const int s = pl.all ? rr / p.G : e.s;
+        const long long to = ((long long)s * p.B + e.b) * p.H + e.hk * p.G +
+                             (pl.all ? rr - s * p.G : rr);
+        if (mine && e.slot < 0) {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            reinterpret_cast<uint2 *>(p.o + to * D)[j * kPer + k] =
+                make_uint2(pack_bf16x2(acc[k].x, acc[k].y),
+                           pack_bf16x2(acc[k].z, acc[k].w));
+          if (j == 0) p.lse[to] = lse2 * 0.69314718055994531f;
+        } else if (mine) {
+          const size_t part =
+              ((size_t)blockIdx.x * 2 + (e.slot > 0 ? 1 : 0)) * 32 + r;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k)
+            reinterpret_cast<float4 *>(pl.part_o + part * D)[j * kPer + k] =
+                acc[k];
+          // a NaN tells the joining CTA to compute the row again
+          if (j == 0)
+            pl.part_l[part] = odd ? __int_as_float(0x7fffffff) : lse2;
         }
-        named_bar_sync(1, kWarps * 32);
-        odd = 0;
-        if (*joined) {
-          // o = sum_i w_i o_i / sum_i w_i, w_i = 2^(l_i - max)
-          const int parts = e.c1 - e.c0 + 1;
-          constexpr int kLanes = D / 4;  // threads of a row
-          for (int r = tid / kLanes; r < kRows;
-               r += kWarps * 32 / kLanes) {
-            const int c = tid % kLanes;
-            if (r >= live) continue;
-            float M = neg_inf, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            bool again = false;
-            for (int i0 = 0; i0 < parts; i0 += 8) {
-              float ls[8];
-              float4 v[8];
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const int i = min(i0 + u, parts - 1);
-                const size_t a =
-                    ((size_t)(e.c0 + i) * 2 + (i == 0 ? 1 : 0)) * 32 + r;
-                ls[u] = __ldcg(pl.part_l + a);
-                v[u] = __ldcg(
-                    reinterpret_cast<const float4 *>(pl.part_o + a * D) + c);
-                if (i0 + u >= parts) ls[u] = neg_inf;
-              }
-              float mx = M;
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                again |= ls[u] != ls[u];
-                mx = fmaxf(mx, ls[u]);
-              }
-              const float ref = mx > neg_inf ? mx : 0.f;
-              const float f = ex2(M - ref);
-              sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const float wt = ex2(ls[u] - ref);
-                sum += wt;
-                acc.x = fmaf(wt, v[u].x, acc.x);
-                acc.y = fmaf(wt, v[u].y, acc.y);
-                acc.z = fmaf(wt, v[u].z, acc.z);
-                acc.w = fmaf(wt, v[u].w, acc.w);
-              }
-              M = mx;
-            }
-            const float inv = sum > 0.f ? 1.f / sum : 0.f;
-            const long long to = row_at(r);
-            reinterpret_cast<uint2 *>(p.o + to * D)[c] =
-                make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
-                           pack_bf16x2(acc.z * inv, acc.w * inv));
-            if (c == 0) {
-              p.lse[to] = sum > 0.f
-                              ? (M + log2f(sum)) * 0.69314718055994531f
-                              : neg_inf;
-              if (again) atomicOr(joined + 1, 1 << r);
-            }
+        if (e.slot < 0) {
+          unsigned again = __ballot_sync(0xffffffffu, mine && odd && j == 0);
+          for (; again; again &= again - 1) {
+            const int src = __ffs(again) - 1;
+            redo_row(p, e.b, __shfl_sync(0xffffffffu, s, src), e.hk,
+                     __shfl_sync(0xffffffffu, to, src), qs, lane);
           }
-          named_bar_sync(1, kWarps * 32);
-          odd = joined[1];
         }
       }
-      if (odd) {  // (the same value in all threads)
-        // rows on their own, a warp each
-        float *qs = join + warp * 128;
-        int k = 0;
-        for (unsigned left = odd; left; left &= left - 1, ++k) {
-          if (k % kWarps != warp) continue;
-          const long long to = row_at(__ffs(left) - 1);
-          const int rr = first + __ffs(left) - 1;
-          redo_row(p, e.b, pl.all ? rr / p.G : e.s, e.hk, to, qs, lane);
-        }
-      }
-      named_bar_sync(1, kWarps * 32);
-      if (tid == 0) *odd_rows = 0, joined[1] = 0;
+      // (its count came before the barrier above)
+      if (shared_item && joined[entry & 1]) join_item(waiting[(entry - 1) & 1]);
+      shared_item = e.slot >= 0;
+      if (tid == 0) waiting[entry & 1] = e;
       __syncwarp();
       if (lane == 0) mbar_arrive(item_empty(entry & 1));
     }
