@@ -19,7 +19,7 @@
 //
 // Warps: 0 .. 3 softmax (thread = row = tensor-memory lane), 4 .. 7 convert the
 // values, 8 TMA producer, 9 MMA issuer and tensor-memory allocator; two CTAs an
-// SM.  Masks, rows that are not finite, split tiles: as in block_attn.cu.
+// SM.  Masks and rows that are not finite: as in block_attn.cu.
 #include "block_attn_host.cuh"
 #include "block_attn_q8.cuh"
 #include "block_attn_split.cuh"
@@ -656,36 +656,93 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     }
   }
 done:
-  if (pl.splits > 1) __threadfence();  // this CTA's parts, before the count
   __syncthreads();
-  if (pl.splits > 1) {
-    // (also after a wait that gave up: the counts stay whole)
-    const int item = blockIdx.x / pl.splits;
-    if (tid == 0) {
-      const int sh = 8 * (item & 3);
-      uint32_t *word = pl.done + (item >> 2);
-      const uint32_t before = atomicAdd(word, 1u << sh) >> sh & 0xffu;
-      const bool last = before + 1 == (uint32_t)pl.splits;
-      if (last) atomicAnd(word, ~(0xffu << sh));  // for the next call
-      __threadfence();
-      *sCount = last;
-    }
-    __syncthreads();
-    // (its registers: those of the warps with the fewest, so the softmax's
-    // warps do it)
-    if (*sCount && warp < 4)
-      join_parts<D, 128>(p, pl, (size_t)item * pl.splits * (pl.qt * p.G), b,
-                         s0, nq, hk,
-                         reinterpret_cast<float *>(smem + L::kOffQ), tid,
-                         [&](int b1, int s1, int h1, float *qs, int l1) {
-                           redo_row8(p, b1, s1, h1, qs, l1);
-                         });
-    __syncthreads();
-  }
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 256);
+  }
+}
+
+// Joins the parts of split tiles, o = sum_i w_i o_i / sum_i w_i with w_i =
+// 2^(l_i - max), in the order of the splits: a warp a row, in a launch of its
+// own.  A tile has 128 rows of up to 255 parts: the CTA that ended last took 190
+// us for 38 of them (one token of 128 heads' rows: 800 us instead of 30).
+template <int D>
+__global__ void __launch_bounds__(256)
+    attn_q8_join_kernel(const __grid_constant__ BlockAttnQ8 p,
+                        const __grid_constant__ FwdPlan pl) {
+  constexpr int kEl = D / 32;  // columns of a lane
+  __shared__ float qs[8][128];
+  const float neg_inf = -__int_as_float(0x7f800000);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rows = pl.qt * p.G;
+  const long long all = (long long)pl.tiles * p.B * p.Hk * rows;
+  for (long long x = (long long)blockIdx.x * 8 + warp; x < all;
+       x += (long long)gridDim.x * 8) {
+    const int row = (int)(x % rows);
+    const long long item = x / rows;
+    int it = (int)item;
+    const int hk = it % p.Hk;
+    it /= p.Hk;
+    const int b = it % p.B;
+    const int s = (pl.tiles - 1 - it / p.B) * pl.qt + row / p.G;
+    if (s >= p.S) continue;
+    float m = neg_inf, sum = 0.f, acc[kEl] = {};
+    bool odd = false;
+    for (int i0 = 0; i0 < pl.splits; i0 += 8) {
+      float l[8], v[8][kEl];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const long long at =
+            (item * pl.splits + min(i0 + u, pl.splits - 1)) * rows + row;
+        l[u] = i0 + u < pl.splits ? __ldcg(pl.part_l + at) : neg_inf;
+        if constexpr (kEl == 4) {
+          const float4 t = __ldcg(
+              reinterpret_cast<const float4 *>(pl.part_o + at * D) + lane);
+          v[u][0] = t.x, v[u][1] = t.y, v[u][2] = t.z, v[u][3] = t.w;
+        } else {
+          const float2 t = __ldcg(
+              reinterpret_cast<const float2 *>(pl.part_o + at * D) + lane);
+          v[u][0] = t.x, v[u][1] = t.y;
+        }
+      }
+      float mx = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        odd |= l[u] != l[u];
+        mx = fmaxf(mx, l[u]);
+      }
+      const float ref = mx > neg_inf ? mx : 0.f;
+      const float f = ex2(m - ref);
+      sum *= f;
+#pragma unroll
+      for (int c = 0; c < kEl; ++c) acc[c] *= f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float w = ex2(l[u] - ref);
+        sum += w;
+#pragma unroll
+        for (int c = 0; c < kEl; ++c) acc[c] = fmaf(w, v[u][c], acc[c]);
+      }
+      m = mx;
+    }
+    const int h = hk * p.G + row % p.G;
+    if (odd) {  // (all lanes of the warp)
+      redo_row8(p, b, s, h, qs[warp], lane);
+      continue;
+    }
+    const size_t at = ((size_t)s * p.B + b) * p.H + h;
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if constexpr (kEl == 4)
+      reinterpret_cast<uint2 *>(p.o + at * D)[lane] =
+          make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                     pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+      reinterpret_cast<uint32_t *>(p.o + at * D)[lane] =
+          pack_bf16x2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0)
+      p.lse[at] = sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : neg_inf;
   }
 }
 
@@ -701,6 +758,10 @@ int launch_tile(const CUtensorMap &tm_k, const CUtensorMap &tm_v,
   const long long grid = (long long)pl.tiles * p.B * p.Hk * pl.splits;
   if (grid > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
   kern<<<(unsigned)grid, kTileThreads, smem, st>>>(tm_k, tm_v, p, pl);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  if (pl.splits == 1) return DSA_OK;
+  const long long rows = (long long)pl.tiles * p.B * p.Hk * pl.qt * p.G;
+  attn_q8_join_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p, pl);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
