@@ -9,8 +9,22 @@
 namespace dsa {
 namespace {
 
-// Rows of a sequence and key head that take the kernel for few rows.
-bool few_rows(int S, int G) { return (long long)S * G <= 64; }
+// Which problems take the kernel for few rows (block_attn_q8_step.cu), by the
+// rows S * G of a sequence and key head that read the same keys; both kernels
+// measured on 4 key heads at 12000 to 16000 keys, or 34 blocks of 64:
+//   all keys, 16 rows: few 18 / 50 / 151 us for 1 / 16 / 64 sequences of 128
+//     dimensions, many 28 / 73 / 264; 32 rows: few 32 / 91 / 278, many 28 / 74 /
+//     266.  At 64 dimensions, 32 rows: few 20 / 51 / 155, many 19 / 72 / 243;
+//     64 rows: few 19 / 84 / 288, many 19 / 79 / 266.
+//   a selection, one token, 16 rows: few 21 / 21 / 21 / 42 us for 1 / 4 / 16 / 64
+//     sequences, many 16 / 18 / 23 / 47: equal near 64 pairs of sequence and key
+//     head.  Several tokens share blocks, which only the other kernel sees: four
+//     of 8 heads 116 and 69 us for 64 sequences.
+bool few_rows(int S, int B, int Hk, int G, int D, int topk) {
+  const long long rows = (long long)S * G;
+  if (topk > 0) return S == 1 && rows <= 16 && (long long)B * Hk >= 64;
+  return rows <= (D == 64 ? 32 : 16);
+}
 
 }  // namespace
 }  // namespace dsa
@@ -23,7 +37,8 @@ size_t dsa_block_attn_q8_workspace_size(int S, int B, int H, int Hk, int D,
   if (S <= 0 || B <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || D <= 0 ||
       T <= 0 || block_size <= 0 || topk < 0 || local_blocks < 0)
     return 0;
-  if (dsa::few_rows(S, H / Hk)) return dsa::attn_q8_step_workspace_bytes(D);
+  if (dsa::few_rows(S, B, Hk, H / Hk, D, topk))
+    return dsa::attn_q8_step_workspace_bytes(D);
   return dsa_block_attn_workspace_size(S, B, H, Hk, D, T, block_size, topk,
                                        local_blocks);
 }
@@ -68,7 +83,7 @@ int dsa_block_attn_paged_q8_fwd(
   int num_sms = 0;
   rc = dsa::device_num_sms(&num_sms);
   if (rc != DSA_OK) return rc;
-  if (dsa::few_rows(S, p.G))
+  if (dsa::few_rows(S, B, Hk, p.G, D, topk))
     return dsa::run_attn_q8_step(p, workspace, num_sms,
                                  static_cast<cudaStream_t>(cuda_stream));
   return dsa::run_attn_q8_tile(p, workspace, num_sms,

@@ -61,8 +61,8 @@ constexpr int kDoneOffset = 64;
 constexpr int kMaxCtas = 256 - kDoneOffset;
 
 struct StepPlan {
-  bool all;     // no selection: all keys of the local blocks
-  int rows;     // rows of an item's whole (b, hk) or (b, s, hk)
+  bool all;     // no selection: all keys of the local blocks (else S = 1)
+  int rows;     // S * G
   int tiles;    // items that these are cut into
   int items_b;  // items of a sequence
   int box;      // tokens of a TMA box: 16 or 32
@@ -79,10 +79,9 @@ struct Maps8 {
 // What the producer says of an item's part.
 struct Entry {
   int n, g0;           // its steps, and the CTA's steps before it
-  int b, hk, s, tile;  // s: the query (selection); rows of a tile otherwise
+  int b, hk, tile;
   int c0, c1;          // CTAs that share it
   int slot;            // where this one's part goes: 0, 1 or -1 (whole)
-  int pad[3];
 };
 
 // Of 16 keys of a step: exponents of the scales, the first key, and how many
@@ -327,8 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned x0 = w - w_i, x1 = min(U, x0 + (u1 - w));
       w += x1 - x0;
       const int tile = idx % pl.tiles;
-      const int s = pl.all ? 0 : idx / pl.tiles % p.S;
-      const int hk = pl.all ? idx / pl.tiles : idx / pl.tiles / p.S;
+      const int hk = idx / pl.tiles;
       // the item's keys: units of `box` keys
       Span sp;
       int units;
@@ -339,9 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // (the list of the item before has been read by all)
         if (named_bar_or(2, kFeeders * 32, !ok)) break;
-        sp = span_of(p, b, s, s);
-        const long long pos = row_pos(p.q_pos, b, s);
-        const int32_t *ids = row_ids(p, b, s, hk);
+        sp = span_of(p, b, 0, 0);
+        const long long pos = row_pos(p.q_pos, b, 0);
+        const int32_t *ids = row_ids(p, b, 0, hk);
         const int words = (p.nblk + 31) / 32, n_cand = p.topk + p.local;
         for (int i = ft; i < words; i += kFeeders * 32) bitmap[i] = 0u;
         named_bar_sync(2, kFeeders * 32);
@@ -381,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 raw[2][D / 32];
       auto row_of = [&](int r, int &rs, int &rh) {
         const int rr = tile * kRows + r;
-        rs = pl.all ? rr / p.G : s;
-        rh = hk * p.G + (pl.all ? rr - rs * p.G : rr);
+        rs = rr / p.G;
+        rh = hk * p.G + rr - rs * p.G;
         return rr < pl.rows;
       };
       auto fetch = [&](int mt) {
@@ -454,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Entry &e = entries[entry & 1];
           e.n = t1 - t0;
           e.g0 = g0;
-          e.b = b, e.hk = hk, e.s = s, e.tile = tile;
+          e.b = b, e.hk = hk, e.tile = tile;
           e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
           e.c0 = e.c1 = (int)cta;
           if (e.slot >= 0) {
@@ -622,9 +620,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           M = mx;
         }
         const int rr = first + r;
-        const int s = pl.all ? rr / p.G : e.s;
-        const long long to = ((long long)s * p.B + e.b) * p.H + e.hk * p.G +
-                             (pl.all ? rr - s * p.G : rr);
+        const int s = rr / p.G;
+        const long long to =
+            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr - s * p.G;
         if (mine) {
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           reinterpret_cast<uint2 *>(p.o + to * D)[c] =
@@ -966,9 +964,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         odd = (votes >> (lane & 16) & 0xffffu) != 0u;  // any of the row's
         const float lse2 = some ? M + log2f(sum) : neg_inf;
         const int rr = first + r;
-        const int s = pl.all ? rr / p.G : e.s;
-        const long long to = ((long long)s * p.B + e.b) * p.H + e.hk * p.G +
-                             (pl.all ? rr - s * p.G : rr);
+        const int s = rr / p.G;
+        const long long to =
+            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr - s * p.G;
         if (mine && e.slot < 0) {
 #pragma unroll
           for (int k = 0; k < kPer; ++k)
@@ -1029,14 +1027,16 @@ size_t attn_q8_step_workspace_bytes(int D) {
   return 256 + (size_t)kMaxCtas * 2 * 32 * (D + 1) * sizeof(float);
 }
 
+// S * G rows of a sequence and key head: all keys for up to 16, or 32 at 64
+// dimensions; a selection of single tokens for up to 16.
 int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
                      cudaStream_t st) {
   StepPlan pl{};
   pl.all = p.topk == 0;
-  pl.rows = pl.all ? p.S * p.G : p.G;
+  pl.rows = p.S * p.G;
   const int mt = pl.rows > 16 ? 2 : 1;
   pl.tiles = (pl.rows + 16 * mt - 1) / (16 * mt);
-  const long long items = (long long)pl.tiles * p.Hk * (pl.all ? 1 : p.S);
+  const long long items = (long long)pl.tiles * p.Hk;
   if (items * p.B >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
   pl.items_b = (int)items;
   pl.box = p.blk >= 32 ? 32 : 16;
@@ -1061,7 +1061,7 @@ int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
     return mt == 1 ? launch<64, 1>(p, pl, maps, ctas, st)
                    : launch<64, 2>(p, pl, maps, ctas, st);
   return mt == 1 ? launch<128, 1>(p, pl, maps, ctas, st)
-                 : launch<128, 2>(p, pl, maps, ctas, st);
+                 : DSA_ERR_UNSUPPORTED;
 }
 
 }  // namespace dsa

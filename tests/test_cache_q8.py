@@ -407,6 +407,14 @@ ATTN = [
     (70, 1, 8, 1, 128, 128, 0, 99, True, 128, 128, 3),
     (40, 2, 4, 4, 128, 32, 4, 1, True, 96, 32, 4),
     (130, 1, 16, 1, 64, 16, 8, 2, False, 64, 16, 5),
+    # single tokens of many sequences
+    (1, 33, 8, 2, 128, 64, 3, 1, False, 64, 64, 4),
+    (1, 16, 32, 4, 64, 32, 5, 1, True, 32, 16, 7),
+    (1, 22, 15, 3, 128, 16, 9, 2, False, 48, 16, 5),
+    (1, 64, 16, 1, 64, 128, 2, 1, False, 128, 128, 3),
+    (1, 70, 4, 1, 128, 64, 0, 99, True, 64, 64, 3),
+    (2, 40, 32, 2, 64, 32, 0, 99, True, 32, 32, 5),
+    (1, 3, 12, 1, 128, 32, 0, 2, True, 64, 32, 4),
 ]
 
 
