@@ -13,6 +13,12 @@ struct BlockAttnQ8 : BlockAttn {  // k, v and their strides: unused
   float *lse;
 };
 
+// TMA map of e4m3 keys or values as (d, token, head, page) with a box of D (64
+// or 128) x `rows` tokens (api.cu).
+int encode_kv8(CUtensorMap *m, const void *base, int D, int rows,
+               long long tokens, long long st, long long heads, long long sh,
+               long long outer, long long sx);
+
 // Few rows (block_attn_q8_step.cu).
 size_t attn_q8_step_workspace_bytes(int D);
 int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,

@@ -92,6 +92,17 @@ __device__ __forceinline__ void regs_fewer() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
+// wait_bar_rest() without the call: kernels that move registers between warps
+// (setmaxnreg) may not make one.
+__device__ __forceinline__ bool wait_bar_rest_inl(uint32_t bar, uint32_t parity,
+                                                  volatile int *abort_flag,
+                                                  int *status) {
+#pragma unroll 1
+  for (int it = 0; it < 64; ++it)
+    if (mbar_try_wait_ns(bar, parity, 1000000u)) return true;
+  return wait_bar_loop(bar, parity, abort_flag, status);
+}
+
 // One row on its own, by one warp (qs: 128 floats of shared memory).
 __device__ __forceinline__ void redo_row8(const BlockAttnQ8 &p, int b, int s,
                                        int h, float *qs, int lane) {

@@ -160,12 +160,6 @@ int encode_kv(CUtensorMap *m, const void *base, int D, int rows,
               long long tokens, long long st, long long heads, long long sh,
               long long outer, long long sx);
 
-// TMA map of e4m3 keys or values as (d, token, head, page) with a box of D (64
-// or 128) x `rows` tokens.
-int encode_kv8(CUtensorMap *m, const void *base, int D, int rows,
-               long long tokens, long long st, long long heads, long long sh,
-               long long outer, long long sx);
-
 // Multiprocessor count of the current device (a dsa_status code).
 int device_num_sms(int *num_sms);
 

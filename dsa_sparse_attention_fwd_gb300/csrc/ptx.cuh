@@ -136,17 +136,6 @@ __device__ __forceinline__ bool wait_bar_rest(uint32_t bar, uint32_t parity,
   return wait_bar_poll(bar, parity, abort_flag, status);
 }
 
-// wait_bar_rest() without the call: kernels that move registers between warps
-// (setmaxnreg) may not make one.
-__device__ __forceinline__ bool wait_bar_rest_inl(uint32_t bar, uint32_t parity,
-                                                  volatile int *abort_flag,
-                                                  int *status) {
-#pragma unroll 1
-  for (int it = 0; it < 64; ++it)
-    if (mbar_try_wait_ns(bar, parity, 1000000u)) return true;
-  return wait_bar_loop(bar, parity, abort_flag, status);
-}
-
 // ---- TMA (tiled tensor loads into shared memory) ----------------------------
 
 __device__ __forceinline__ void tma_prefetch_desc(const void *tmap) {

@@ -9,7 +9,10 @@
 `train_step` returns the loss and the gradient of W; `serve` feeds the same
 tokens through a paged cache, a prompt in one chunk and then one token at a
 time, and returns the layer's outputs, which are those of the training forward
-up to roundings.
+up to roundings.  `serve(.., bits=8)` keeps the cache in 8 bits
+(dsa_paged_append_q8, dsa_paged_read_q8 for the block means,
+dsa_block_attn_paged_q8_fwd): half the memory and, for single tokens, half the
+time; its outputs are those of keys and values rounded to e4m3.
 
     python examples/block_sparse_layer.py
 """
@@ -97,12 +100,18 @@ class Layer:
         gw = x.flatten(0, 1).float().t() @ gy.float()
         return loss, gw, o
 
-    def serve(self, x, prompt):
+    def serve(self, x, prompt, bits=16):
         S, B, _ = x.shape
         pages = -(-S // self.page)
         shape = (B * pages, self.page, self.kv_heads, self.dim)
-        k_cache = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        dtype = torch.bfloat16 if bits == 16 else torch.float8_e4m3fn
+        k_cache = torch.empty(shape, dtype=dtype, device="cuda")
         v_cache = torch.empty_like(k_cache)
+        cache = (k_cache, v_cache)
+        if bits == 8:  # a scale for the tokens of a block and a head
+            scales = (B * pages, self.page // self.block, self.kv_heads)
+            cache += (torch.empty(scales, device="cuda"),
+                      torch.empty(scales, device="cuda"))
         table = torch.randperm(B * pages, device="cuda").to(torch.int32)
         table = table.view(B, pages)
         status = torch.zeros(256, dtype=torch.uint8, device="cuda")
@@ -110,20 +119,31 @@ class Layer:
         steps = [(0, prompt)] + [(s, s + 1) for s in range(prompt, S)]
         for s0, s1 in steps:
             q0, k0, v = self.qkv(x[s0:s1])
-            pos = torch.arange(s0, s1, dtype=torch.int32, device="cuda")
-            q, _ = dsa.dsa_paged_append(
-                k0, v, k_cache, v_cache, table,
-                pos[:, None].expand(-1, B).contiguous(),
-                inv_freq=self.inv_freq, wk=self.wk, q=q0, wq=self.wq,
-                workspace=status, **self.rope())
+            q_pos = torch.full((B,), s0, dtype=torch.int32, device="cuda")
+            turn = dict(inv_freq=self.inv_freq, wk=self.wk, q=q0, wq=self.wq,
+                        workspace=status, **self.rope())
             # (a program would keep the block means; here they are read back)
             done = s1 // self.block * self.block
-            rows = k_cache[table.long()].flatten(1, 2)[:, :done]
-            q_pos = torch.full((B,), s0, dtype=torch.int32, device="cuda")
-            ids = self.select(q, self.index_keys(rows.transpose(0, 1)), q_pos)
-            o, _, ws = dsa.dsa_block_attn_paged_fwd(
-                q, k_cache, v_cache, table, ids, block_size=self.block,
-                scale=self.scale, q_pos=q_pos, local_blocks=self.local)
+            if bits == 16:
+                pos = torch.arange(s0, s1, dtype=torch.int32, device="cuda")
+                q, _ = dsa.dsa_paged_append(
+                    k0, v, *cache, table,
+                    pos[:, None].expand(-1, B).contiguous(), **turn)
+                rows = k_cache[table.long()].flatten(1, 2)[:, :done]
+                rows = rows.transpose(0, 1)
+                attend = dsa.dsa_block_attn_paged_fwd
+            else:
+                q, _ = dsa.dsa_paged_append_q8(k0, v, *cache, table, q_pos,
+                                               **turn)
+                rows = k0[:0]
+                if done:
+                    rows, _, _ = dsa.dsa_paged_read_q8(*cache, table, done,
+                                                       workspace=status)
+                attend = dsa.dsa_block_attn_paged_q8_fwd
+            ids = self.select(q, self.index_keys(rows), q_pos)
+            o, _, ws = attend(q, *cache, table, ids, block_size=self.block,
+                              scale=self.scale, q_pos=q_pos,
+                              local_blocks=self.local)
             outs.append(o)
             workspaces.append(ws)
         for ws in [status] + workspaces:
@@ -153,6 +173,9 @@ def main():
     worst = float((served.float() - o.float()).abs().max())
     print(f"served outputs differ from the training forward's by at most "
           f"{worst:.3g}")
+    served8 = layer.serve(x, prompt=390, bits=8)
+    off = float((served8.float() - o.float()).norm() / o.float().norm())
+    print(f"from a cache held in 8 bits by {off:.3g} of their norm")
     return losses, o, served
 
 

@@ -652,6 +652,203 @@ def test_streams_and_graphs(dsa, case):
     assert dsa.dsa_indexer_check(ws) == 0
 
 
+# ---- together, streams, threads ---------------------------------------------------
+
+@gpu
+def test_a_layer_served(dsa):
+    """A prompt in two chunks and single tokens: append, read back, block means,
+    selection, attention.  Each step's output is the definition's on what the
+    cache holds after it, and the cache is that of one append of all tokens."""
+    S, B, H, Hk, D, block, page = 75, 2, 8, 2, 64, 16, 32
+    pages = 3
+    g = torch.Generator().manual_seed(12)
+    qkv = torch.randn((S, B, H + 2 * Hk, D), generator=g).to(BF).cuda()
+    w = (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    f = inv(D).cuda()
+    table = torch.randperm(B * pages, generator=g).to(torch.int32).view(B, pages)
+    table = table.cuda()
+    cache = [t.cuda() for t in make_cache(B * pages, page, Hk, D, 16, 1)]
+    status = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    steps = [(0, 40), (40, 71)] + [(s, s + 1) for s in range(71, S)]
+    for s0, s1 in steps:
+        x = qkv[s0:s1]
+        start = torch.full((B,), s0, dtype=torch.int32, device="cuda")
+        q, _ = dsa.dsa_paged_append_q8(
+            x[:, :, H:H + Hk], x[:, :, H + Hk:], *cache, table, start,
+            inv_freq=f, wk=w, q=x[:, :, :H], wq=w, workspace=status)
+        k, v, _ = dsa.dsa_paged_read_q8(*cache, table, s1, workspace=status)
+        n = s1 // block
+        means = k[:n * block, :, 0].float().view(n, block, B, D).mean(1).to(BF)
+        wi = torch.full((s1 - s0, B, H), 1.0 / H, device="cuda")
+        _, ids = dsa.v4_lighting_indexer(q, means, wi, block, 2, q_pos=start)
+        o, lse, ws = dsa.dsa_block_attn_paged_q8_fwd(
+            q, *cache, table, ids, block, 0.125, q_pos=start, local_blocks=1)
+        assert dsa.dsa_indexer_check(ws) == 0
+        r = block_attn_ref(q.cpu(), k.cpu(), v.cpu(), ids.cpu(), block, 1,
+                           0.125, q_pos=start.cpu())
+        check_attn(r, o, lse, s1)
+    assert dsa.dsa_indexer_check(status) == 0
+    once = [t.cuda() for t in make_cache(B * pages, page, Hk, D, 16, 1)]
+    zero = torch.zeros(B, dtype=torch.int32, device="cuda")
+    dsa.dsa_paged_append_q8(qkv[:, :, H:H + Hk], qkv[:, :, H + Hk:], *once,
+                            table, zero, inv_freq=f, wk=w)
+    a = dsa.dsa_paged_read_q8(*cache, table, S)
+    b = dsa.dsa_paged_read_q8(*once, table, S)
+    for i in (0, 1):
+        # (codes that were subnormal on the way are a step apart at most)
+        step = cache[2 + i].amax() * 2.0 ** -9
+        assert float((a[i].float() - b[i].float()).abs().max()) <= float(step)
+
+
+@gpu
+def test_example_serves_from_8_bits(dsa):
+    """The example's layer from either cache: the outputs differ by the
+    rounding of keys and values, 2^-4 each at most where one selects the same
+    blocks."""
+    import importlib.util
+    import os
+    import sys
+    path = os.path.join(os.path.dirname(os.path.dirname(
+        os.path.abspath(__file__))), "examples", "block_sparse_layer.py")
+    spec = importlib.util.spec_from_file_location("block_sparse_layer_q8", path)
+    m = importlib.util.module_from_spec(spec)
+    sys.modules["block_sparse_layer_q8"] = m
+    spec.loader.exec_module(m)
+    # every block is local: no selection that a rounding could change
+    layer = m.Layer(hidden=64, local=4, topk=1)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((150, 2, 64), generator=g, device="cuda").to(BF)
+    a = layer.serve(x, prompt=140).float()
+    b = layer.serve(x, prompt=140, bits=8).float()
+    assert bool(torch.isfinite(b).all())
+    # (norms: a softmax's output moves by at most the values' 2^-4 and twice
+    # the scores' 2^-4 |q| |k| scale < 2^-4 * 12 of the values' spread, most of
+    # which averages out; a quarter would be another layer)
+    assert float((a - b).norm() / a.norm()) < 0.25
+
+
+def q8_calls(dsa):
+    """name -> call(stream): what is compared."""
+    a = attn_inputs(ATTN[1], 8)
+    dev = {n: (t.cuda() if isinstance(t, torch.Tensor) else t)
+           for n, t in a.items()}
+    many = {n: (t.cuda() if isinstance(t, torch.Tensor) else t)
+            for n, t in attn_inputs(ATTN[12], 8).items()}
+    k = torch.randn((37, 3, 2, 128), device="cuda").to(BF)
+    start = torch.tensor([0, 70, 300], dtype=torch.int32, device="cuda")
+    bad = torch.full_like(dev["table"], 10 ** 6)
+    f = inv(128).cuda()
+    cache = (dev["kc"], dev["vc"], dev["ks"], dev["vs"])
+    copies = tuple(t.clone() for t in cache)
+    return {
+        "append": lambda st: dsa.dsa_paged_append_q8(
+            k, k, *copies, dev["table"], start, inv_freq=f, q=k,
+            stream=st)[:1],
+        "append, bad page": lambda st: (dsa.dsa_paged_append_q8(
+            k, k, *copies, bad, start, stream=st)[1][:4],),
+        "read": lambda st: dsa.dsa_paged_read_q8(*cache, dev["table"], 99,
+                                                 stream=st)[:2],
+        "one token": lambda st: call(dsa, dev, stream=st)[:2],
+        "chunk": lambda st: call(dsa, many, stream=st)[:2],
+    }
+
+
+@gpu
+def test_given_stream(dsa):
+    """Calls on a stream of their own, while blocks of their outputs' and
+    workspaces' sizes are freed with work queued on the current one."""
+    side = torch.cuda.Stream()
+    for name, fn in q8_calls(dsa).items():
+        want = [t.clone() for t in fn(None)]
+        torch.cuda.synchronize()
+        sizes = [t.numel() * t.element_size() for t in want]
+        held = [torch.empty(n, dtype=torch.uint8, device="cuda")
+                for n in sizes + [256, 1 << 12, 1 << 16, 6 << 20] for _ in "ab"]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(60_000_000)      # some 30 ms
+        for t in held:
+            t.fill_(255)
+        del held, t
+        got = fn(side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            early = [t.clone().cpu() for t in got]
+        torch.cuda.synchronize()
+        for a, b, c in zip(want, got, early):
+            assert torch.equal(a, b), name
+            assert torch.equal(a.cpu(), c), name
+
+
+@gpu
+def test_two_threads(dsa):
+    """Two threads with streams and workspaces of their own at once."""
+    import threading
+    calls = q8_calls(dsa)
+    want = {n: [t.clone() for t in fn(None)] for n, fn in calls.items()
+            if not n.startswith("append")}
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(seed):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(30):
+                    for n in want:
+                        for a, b in zip(calls[n](None), want[n]):
+                            if not torch.equal(a, b):
+                                errors.append(n)
+            st.synchronize()
+        except Exception as e:  # pragma: no cover
+            errors.append(repr(e))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+
+
+@gpu
+def test_wrong_tensors_are_refused(dsa):
+    a = attn_inputs(ATTN[1], 8)
+    dev = {n: (t.cuda() if isinstance(t, torch.Tensor) else t)
+           for n, t in a.items()}
+
+    def refused(err, match, **over):
+        with pytest.raises(err, match=match):
+            call(dsa, dict(dev, **over))
+    refused(TypeError, "q must be", q=dev["q"].float())
+    refused(ValueError, "contiguous", q=dev["q"].transpose(0, 2))
+    refused(TypeError, "k_cache must be", kc=raw(dev["kc"]))
+    refused(ValueError, "v_cache shape", vc=dev["vc"][:-1])
+    refused(ValueError, "k_scale shape", ks=dev["ks"][:-1])
+    refused(TypeError, "v_scale must be", vs=dev["vs"].double())
+    refused(ValueError, "do not divide", ks=dev["ks"].repeat(1, 3, 1))
+    refused(ValueError, "page_table is for", table=dev["table"][:2])
+    refused(ValueError, "blocks shape", ids=dev["ids"][:, :, :1])
+    refused(ValueError, "q_pos shape", q_pos=dev["q_pos"][:2])
+    k = torch.zeros((3, 3, 2, 128), dtype=BF, device="cuda")
+    cache = (dev["kc"], dev["vc"], dev["ks"], dev["vs"], dev["table"])
+    start = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for over, err in ((dict(start=start[:2]), ValueError),
+                      (dict(start=start.long()), TypeError),
+                      (dict(count=start.float()), TypeError),
+                      (dict(k=k[:, :2]), ValueError),
+                      (dict(k=k.float()), TypeError),
+                      (dict(v=k[..., :64]), ValueError),
+                      (dict(wk=start.float()), ValueError),
+                      (dict(q=k.half()), TypeError)):
+        kw = dict(dict(k=k, v=k, start=start), **over)
+        with pytest.raises(err):
+            dsa.dsa_paged_append_q8(
+                kw.pop("k"), kw.pop("v"), *cache, kw.pop("start"), **kw)
+    with pytest.raises(TypeError):
+        dsa.dsa_paged_read_q8(*cache, 5, first=start.long())
+    with pytest.raises(ValueError):
+        dsa.dsa_paged_read_q8(*cache, 5, out_k=k)
+
+
 # ---- references and refusals (no GPU) --------------------------------------------
 
 def test_reference_e4m3_against_torch():
