@@ -1119,8 +1119,9 @@ def dsa_paged_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table,
         D, k_cache.data_ptr(), v_cache.data_ptr(), _strides2(k_cache, v_cache),
         k_scale.data_ptr(), v_scale.data_ptr(), group, pages, page_size,
         page_table.data_ptr(), max_pages, start.data_ptr(), _addr(count),
-        None if q is None else _addr(wq), _addr(wk), eps, _addr(inv_freq),
-        rot_start, R, 1 if interleaved else 0, rot_scale,
+        None if q is None else _addr(wq), _addr(wk), float(eps),
+        _addr(inv_freq), int(rot_start), R, 1 if interleaved else 0,
+        float(rot_scale),
         None if q is None else out_q.data_ptr(), workspace.data_ptr(),
         workspace.numel(), _raw_stream(stream, dev))
     del keep
@@ -1140,6 +1141,7 @@ def dsa_paged_read_q8(k_cache, v_cache, k_scale, v_scale, page_table, T,
     dev = k_cache.get_device()
     pages, page_size, Hk, D, group, B, max_pages = _cache_q8_sizes(
         k_cache, k_scale, page_table)
+    T = int(T)
     shape = (T, B, Hk, D)
     if not (dev >= 0 and dev == torch._C._cuda_getDevice()
             and _cache_q8_ok(dev, k_cache, v_cache, k_scale, v_scale,
@@ -1245,8 +1247,8 @@ def dsa_block_attn_paged_q8_fwd(q, k_cache, v_cache, k_scale, v_scale,
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         _strides2(k_cache, v_cache), k_scale.data_ptr(), v_scale.data_ptr(),
         group, pages, page_size, page_table.data_ptr(), max_pages, S, B, H, Hk,
-        D, _addr(blocks), sel_heads, topk, block_size, local_blocks,
-        _addr(q_pos), scale, out_o.data_ptr(), out_lse.data_ptr(),
+        D, _addr(blocks), sel_heads, topk, int(block_size), int(local_blocks),
+        _addr(q_pos), float(scale), out_o.data_ptr(), out_lse.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc != 0:
         raise DsaError(rc, "dsa_block_attn_paged_q8_fwd")

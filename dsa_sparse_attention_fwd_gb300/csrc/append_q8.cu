@@ -49,17 +49,17 @@ __device__ __forceinline__ float2 turn_of(const RopeArgs &a, long long pos,
 // `early` tokens before them are there already.  A thread holds 8 neighbouring
 // values of up to RW rows as they came, and works them out twice, for the
 // scale and for the codes: that costs less than fp32 registers for them.
-template <bool VEC, int LPR, int RW, bool KEYS>
+template <int LPR, int RW, bool KEYS>
 __device__ __forceinline__ void store_group(
     const AppendQ8 &p, const RopeRows &r, int nw, const __nv_bfloat16 *src,
     int n, int early, uint8_t *group_at, long long st, float *scale, int e0, int sub,
-    int unit, Turn<__nv_bfloat16, VEC> &turn, const float2 *cs, const float *w,
+    int unit, Turn<__nv_bfloat16, false> &turn, const float2 *cs, const float *w,
     float *buf, float *red) {
   constexpr int RPW = 32 / LPR;
   const RopeArgs &a = p.a;
   const bool norm = KEYS && r.w != nullptr;
   const int half = a.R / 2;
-  Chunk<__nv_bfloat16, VEC> x[RW];
+  Chunk<__nv_bfloat16, false> x[RW];
 #pragma unroll
   for (int u = 0; u < RW; ++u) {
     const int row = (u * nw + unit) * RPW + sub;
@@ -143,17 +143,19 @@ __device__ __forceinline__ void store_group(
   }
 }
 
-// CTAs 0 .. kv - 1 take keys and values, the others queries as
+// Rows that cannot be read in 16-byte pieces (odd strides or pointers, halves
+// that do not fall on them): element loads, the partners of the rotation through
+// shared memory.  CTAs 0 .. kv - 1 take keys and values, the others queries as
 // norm_rope_kernel() does.  Keys and values: an item is a group that a
 // sequence's rows can reach and one head (by a warp, where a group gets few new
 // rows) or several (by a CTA, the angles of the group's tokens in shared
 // memory for all of them).
-template <bool VEC, int LPR, int RW>
+template <int LPR, int RW>
 __global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
     append_q8_kernel(const __grid_constant__ AppendQ8 p) {
   constexpr int RPW = 32 / LPR;
   using T = __nv_bfloat16;
-  __shared__ __align__(16) float xch[VEC ? 1 : kRopeWarps * RPW * LPR * 8];
+  __shared__ __align__(16) float xch[kRopeWarps * RPW * LPR * 8];
   __shared__ unsigned long long fr[kRopeMaxD / 2];
   __shared__ __align__(16) float sw[2][kRopeMaxD];
   __shared__ float red[2][kRopeWarps];
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
   const RopeArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPR, e0 = (lane % LPR) * 8;
-  float *buf = VEC ? xch : xch + (warp * RPW + sub) * LPR * 8;
+  float *buf = xch + (warp * RPW + sub) * LPR * 8;
   load_weights(a, sw);
   for (int i = threadIdx.x; i < a.R / 2; i += kRopeThreads) {
     double t = a.inv_freq[i] * 0.15915494309189535;  // 1 / (2 pi)
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
     angles[(threadIdx.x / 8) * p.angles + threadIdx.x % 8] =
         make_float2(0.f, 0.f);
   __syncthreads();
-  Turn<T, VEC> turn;
+  Turn<T, false> turn;
   turn.init(a, e0, lane, false);
 
   if (blockIdx.x >= p.kv) {
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
       __syncwarp();
       for (int i = lane; i < half; i += 32) cs[i] = turn_of(a, pos, fr[i]);
       __syncwarp();
-      rope_heads<T, VEC, LPR, 0>(
+      rope_heads<T, false, LPR, 0>(
           a, a.q, static_cast<const T *>(a.q.in) + s * a.q.ss + b * a.q.sb,
           static_cast<T *>(a.q.out) + tk * (long long)nq * a.D, a.D, h0,
           min(h0 + a.heads_per_item, nq), sub, e0, turn, cs, sw[0], buf);
@@ -249,10 +251,10 @@ __global__ void __launch_bounds__(kRopeThreads, RW <= 8 ? 5 : 3)
     float *scale = (is_v ? p.c.vs : p.c.ks) + q8_scale_at(p.c, page, off, h);
     float *rd = red[(h - h0) & 1];
     if (is_v)
-      store_group<VEC, LPR, RW, false>(p, in, nw, src, n, early, at, st, scale,
+      store_group<LPR, RW, false>(p, in, nw, src, n, early, at, st, scale,
                                        e0, sub, unit, turn, cs, sw[1], buf, rd);
     else
-      store_group<VEC, LPR, RW, true>(p, in, nw, src, n, early, at, st, scale,
+      store_group<LPR, RW, true>(p, in, nw, src, n, early, at, st, scale,
                                       e0, sub, unit, turn, cs, sw[1], buf, rd);
   }
 }
@@ -591,16 +593,17 @@ int launch_vec_rows(AppendQ8 &p, int num_sms, cudaStream_t st) {
   if (most <= 2 * RPW) return launch_vec<LPR, 2, true>(p, num_sms, st);
   if (p.c.group <= 2 * kVecWarps * RPW)
     return launch_vec<LPR, 2, false>(p, num_sms, st);
-  if (p.c.group <= 4 * kVecWarps * RPW)
-    return launch_vec<LPR, 4, false>(p, num_sms, st);
-  return launch_vec<LPR, 8, false>(p, num_sms, st);
+  if constexpr (LPR > 8)  // (64 dimensions have 4 rows at most)
+    if (p.c.group > 4 * kVecWarps * RPW)
+      return launch_vec<LPR, 8, false>(p, num_sms, st);
+  return launch_vec<LPR, 4, false>(p, num_sms, st);
 }
 
-// Rows without 16-byte pieces: RW rows of a thread, at most 8 or 16.
-template <int RW>
+// Rows without 16-byte pieces, RW of a thread.
+template <int LPR, int RW>
 int launch_any(AppendQ8 &p, int num_sms, cudaStream_t st) {
   RopeArgs &a = p.a;
-  auto kern = append_q8_kernel<false, 32, RW>;
+  auto kern = append_q8_kernel<LPR, RW>;
   const int most = a.S < p.c.group ? a.S : p.c.group;
   p.by_warp = most <= 2;
   const int half = a.R / 2 < 8 ? 8 : a.R / 2;
@@ -614,7 +617,7 @@ int launch_any(AppendQ8 &p, int num_sms, cudaStream_t st) {
   if (kv >= (1ll << 30)) return DSA_ERR_UNSUPPORTED;
   p.kv = (unsigned)kv;
   const long long q_ctas =
-      query_ctas(a, 1, kRopeWarps, 3ll * num_sms, num_sms);
+      query_ctas(a, 32 / LPR, kRopeWarps, 3ll * num_sms, num_sms);
   constexpr int kMost = 16384 / 2 * (int)sizeof(float2) + 8192;
   const int smem = angles * (int)sizeof(float2);
   if (smem > kMost) return DSA_ERR_UNSUPPORTED;
@@ -623,14 +626,27 @@ int launch_any(AppendQ8 &p, int num_sms, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
+// A thread holds every row of a group that is its own: 16 at most, as D * group
+// <= 16384.
+template <int LPR>
+int launch_any_rows(AppendQ8 &p, int num_sms, cudaStream_t st) {
+  const int rows = p.c.group / (kRopeWarps * (32 / LPR));
+  if (rows <= 8) return launch_any<LPR, 8>(p, num_sms, st);
+  if constexpr (LPR > 8)  // (64 dimensions have 8 rows at most)
+    if (rows <= 16) return launch_any<LPR, 16>(p, num_sms, st);
+  return DSA_ERR_UNSUPPORTED;
+}
+
 int run_append(AppendQ8 &p, int num_sms, cudaStream_t st) {
   const RopeArgs &a = p.a;
   const bool vec = a.r0 % 8 == 0 && a.R % (a.interleaved ? 8 : 16) == 0 &&
                    vec_rows(a.q, 2, false) && vec_rows(a.k, 2, false) &&
                    vec_rows(a.v, 2, false);
-  if (!vec)
-    return p.c.group <= 8 * kRopeWarps ? launch_any<8>(p, num_sms, st)
-                                       : launch_any<16>(p, num_sms, st);
+  if (!vec) {
+    if (a.D <= 64) return launch_any_rows<8>(p, num_sms, st);
+    if (a.D <= 128) return launch_any_rows<16>(p, num_sms, st);
+    return launch_any_rows<32>(p, num_sms, st);
+  }
   if (a.D <= 64) return launch_vec_rows<8>(p, num_sms, st);
   if (a.D <= 128) return launch_vec_rows<16>(p, num_sms, st);
   return launch_vec_rows<32>(p, num_sms, st);

@@ -162,6 +162,47 @@ def check_append(rows, slack, old_c, old_s, got_c, got_s, table, start, count,
 
 
 @gpu
+@pytest.mark.parametrize("turned", [True, False])
+@pytest.mark.parametrize("S,D,R,group", [
+    (1, 64, 64, 16), (2, 128, 64, 64), (3, 80, 20, 16), (150, 128, 128, 128),
+    (70, 256, 256, 64), (40, 16, 6, 32)])
+def test_append_of_unaligned_rows(dsa, S, D, R, group, turned):
+    """Rows that cannot be read in 16-byte pieces."""
+    B, H, Hk, page, pages = 2, 3, 2, 128, 4
+    g = torch.Generator().manual_seed(9)
+    total = H + 2 * Hk
+    buf = torch.randn((S, B, total * D + 3), generator=g).to(BF)
+    cut = lambda t: t[..., 1:1 + total * D].unflatten(-1, (total, D))
+    part = cut(buf)
+    dev_part = cut(buf.cuda())
+    q, k, v = part[:, :, :H], part[:, :, H:H + Hk], part[:, :, H + Hk:]
+    kc, vc, ks, vs = make_cache(B * pages, page, Hk, D, group, 8)
+    table = torch.randperm(B * pages, generator=g).to(torch.int32).view(B, pages)
+    start = torch.tensor([group * 2 - 1, 70], dtype=torch.int32)
+    wq, wk = weights(D, 3)
+    f, r0 = inv(R), D - R if R < D else 0
+    dev = [t.cuda() for t in (kc, vc, ks, vs)]
+    kw = dict(inv_freq=f.cuda(), wk=wk.cuda(), q=dev_part[:, :, :H],
+              wq=wq.cuda(), rot_start=r0) if turned else {}
+    out_q, ws = dsa.dsa_paged_append_q8(
+        dev_part[:, :, H:H + Hk], dev_part[:, :, H + Hk:], *dev, table.cuda(),
+        start.cuda(), eps=EPS, **kw)
+    assert dsa.dsa_indexer_check(ws) == 0
+    pos = start[None, :] + torch.arange(S)[:, None]
+    if turned:
+        rows, mag = norm_rope_ref(k, wk, pos, f, r0, False, EPS)
+        slack = 2.0 ** -19 * mag
+        want, mag = norm_rope_ref(q, wq, pos, f, r0, False, EPS)
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -19 * mag + 1e-38
+        assert bool(((out_q.double().cpu() - want).abs() <= tol).all())
+    else:
+        rows, slack = k.double(), 0.0
+    for x, sl, i in ((rows, slack, 0), (v.double(), 0.0, 1)):
+        check_append(x, sl, (kc, vc)[i], (ks, vs)[i], dev[i].cpu(),
+                     dev[2 + i].cpu(), table, start.tolist(), [S] * B, group)
+
+
+@gpu
 def test_one_by_one_is_as_in_one_call(dsa):
     """Powers of two: the cache is the same however its tokens are cut into
     calls, but for codes that were subnormal on the way (they may be a step of
@@ -613,6 +654,72 @@ def test_attention_reports_bad_ids_and_pages(dsa):
     a["table"][2, 1] = page
     a["ids"][2, 0, 1, 0] = -1
     r, T = reference(a)
+    check_attn(r, o, lse, T)
+
+
+@gpu
+@pytest.mark.parametrize("case", [ATTN[0], ATTN[6], ATTN[9], ATTN[13], ATTN[16]])
+def test_attention_skips_bad_pages(dsa, case):
+    """A page that the table names wrongly is left out and reported; pages
+    behind a row's position are not looked at."""
+    a = attn_inputs(case, 7)
+    page, S = a["kc"].shape[1], a["q"].shape[0]
+    T = page * a["table"].shape[1]
+    a["q_pos"][:] = T - S - 1 - page // 2
+    a["ids"] = None
+    a["local"] = T // a["block"]
+    if case[7] != 99:                        # the selection's kernel
+        n = -(-T // a["block"])
+        a["ids"] = torch.arange(n).expand(a["q"].shape[1], S, n).contiguous(
+        ).to(torch.int32)
+        a["local"] = 1
+    good = a["table"].clone()
+    a["table"][0, -1] = -7                   # behind the rows
+    o, lse, ws = call(dsa, a)
+    seen = int(a["q_pos"][0]) + S - 1 >= T - page
+    assert dsa.dsa_indexer_check(ws) == (6 if seen else 0)
+    a["table"] = good.clone()
+    a["table"][0, 0] = a["kc"].shape[0]
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) == 6
+    # sequence 0 as if its first page's scores were -inf
+    k, v = (torch.stack(dense(c, s, good, a["group"]), 1)
+            for c, s in ((a["kc"], a["ks"]), (a["vc"], a["vs"])))
+    H, Hk = a["q"].shape[2], a["kc"].shape[2]
+    for s in (0, S - 1):
+        for h in (0, H - 1):
+            hk = h // (H // Hk)
+            js = slice(page, int(a["q_pos"][0]) + s + 1)
+            x = a["scale"] * k[js, 0, hk] @ a["q"][s, 0, h].double()
+            p = torch.softmax(x, 0)
+            want = p @ v[js, 0, hk]
+            tol = (2.0 ** -10 * (p @ v[js, 0, hk].abs())
+                   + 2.0 ** -8 * want.abs() + T * 2.0 ** -27)
+            got = o[s, 0, h].double().cpu()
+            assert bool(((got - want).abs() <= tol).all())
+
+
+@gpu
+@pytest.mark.parametrize("case", [ATTN[1], ATTN[6], ATTN[9], ATTN[12], ATTN[16]])
+def test_attention_of_queries_that_are_not_finite(dsa, case):
+    """A NaN or an infinity in a query stays in its row; queries of zeros and
+    of the smallest and largest sizes are like others."""
+    a = attn_inputs(case, 11)
+    H = a["q"].shape[2]
+    rows = [(0, 0, 0), (a["q"].shape[0] - 1, 0, H - 1)]
+    a["q"][rows[0]][5] = math.nan
+    a["q"][rows[1]][7] = math.inf
+    a["q"][0, -1, 0] = 0
+    a["q"][0, -1, 1 % H] *= 2.0 ** -120
+    o, lse, _ = call(dsa, a)
+    clean = dict(a, q=a["q"].clone())
+    for r in rows:
+        clean["q"][r] = 0
+    r, T = reference(clean)
+    o, lse = o.cpu(), lse.cpu()
+    for x in rows:
+        assert bool(torch.isnan(o[x]).all()) == (float(r["lse"][x]) > -math.inf)
+        o[x], lse[x] = r["o"][x].to(BF), r["lse"][x].float()
     check_attn(r, o, lse, T)
 
 
