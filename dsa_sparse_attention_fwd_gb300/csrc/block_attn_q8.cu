@@ -10,20 +10,23 @@ namespace dsa {
 namespace {
 
 // Which problems take the kernel for few rows (block_attn_q8_step.cu), by the
-// rows S * G of a sequence and key head that read the same keys; both kernels
-// measured on 4 key heads at 12000 to 16000 keys, or 34 blocks of 64:
-//   all keys, 16 rows: few 18 / 50 / 151 us for 1 / 16 / 64 sequences of 128
+// rows that share keys: S * G with all keys, G of a selection, whose queries it
+// takes one by one.  Both kernels measured on 4 key heads at 12000 to 16000
+// keys, or 34 blocks of 64 (us on the device; the other kernel joins split
+// tiles in a second launch, 4 us more of the host's time up to 76 pairs of
+// sequence and key head):
+//   all keys, 16 rows: few 18 / 50 / 151 for 1 / 16 / 64 sequences of 128
 //     dimensions, many 28 / 73 / 264; 32 rows: few 32 / 91 / 278, many 28 / 74 /
 //     266.  At 64 dimensions, 32 rows: few 20 / 51 / 155, many 19 / 72 / 243;
 //     64 rows: few 19 / 84 / 288, many 19 / 79 / 266.
-//   a selection, one token, 16 rows: few 21 / 21 / 21 / 42 us for 1 / 4 / 16 / 64
-//     sequences, many 16 / 18 / 23 / 47: equal near 64 pairs of sequence and key
-//     head.  Several tokens share blocks, which only the other kernel sees: four
-//     of 8 heads 116 and 69 us for 64 sequences.
+//   a selection, one token, 16 rows: few 21 / 21 / 21 / 42 for 1 / 4 / 16 / 64
+//     sequences, many 16 / 18 / 23 / 47 (two launches up to 16).
+//   a selection, four tokens of 8 heads: few 18 / 20 / 37 / 116, many 25 / 20 /
+//     30 / 69, where tokens that share blocks read them once.
 bool few_rows(int S, int B, int Hk, int G, int D, int topk) {
-  const long long rows = (long long)S * G;
-  if (topk > 0) return S == 1 && rows <= 16 && (long long)B * Hk >= 64;
-  return rows <= (D == 64 ? 32 : 16);
+  if (topk > 0)
+    return G <= 16 && (S == 1 || (long long)S * B * Hk <= 128);
+  return (long long)S * G <= (D == 64 ? 32 : 16);
 }
 
 }  // namespace

@@ -61,8 +61,8 @@ constexpr int kDoneOffset = 64;
 constexpr int kMaxCtas = 256 - kDoneOffset;
 
 struct StepPlan {
-  bool all;     // no selection: all keys of the local blocks (else S = 1)
-  int rows;     // S * G
+  bool all;     // no selection: all keys of the local blocks
+  int rows;     // that share keys: S * G, of one query of a selection G
   int tiles;    // items that these are cut into
   int items_b;  // items of a sequence
   int box;      // tokens of a TMA box: 16 or 32
@@ -79,7 +79,7 @@ struct Maps8 {
 // What the producer says of an item's part.
 struct Entry {
   int n, g0;           // its steps, and the CTA's steps before it
-  int b, hk, tile;
+  int b, hk, tile, s;  // s: the query, of a selection
   int c0, c1;          // CTAs that share it
   int slot;            // where this one's part goes: 0, 1 or -1 (whole)
 };
@@ -326,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned x0 = w - w_i, x1 = min(U, x0 + (u1 - w));
       w += x1 - x0;
       const int tile = idx % pl.tiles;
-      const int hk = idx / pl.tiles;
+      const int hk = idx / pl.tiles % p.Hk;
+      const int s = idx / pl.tiles / p.Hk;  // (0 without a selection)
       // the item's keys: units of `box` keys
       Span sp;
       int units;
@@ -337,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // (the list of the item before has been read by all)
         if (named_bar_or(2, kFeeders * 32, !ok)) break;
-        sp = span_of(p, b, 0, 0);
-        const long long pos = row_pos(p.q_pos, b, 0);
-        const int32_t *ids = row_ids(p, b, 0, hk);
+        sp = span_of(p, b, s, s);
+        const long long pos = row_pos(p.q_pos, b, s);
+        const int32_t *ids = row_ids(p, b, s, hk);
         const int words = (p.nblk + 31) / 32, n_cand = p.topk + p.local;
         for (int i = ft; i < words; i += kFeeders * 32) bitmap[i] = 0u;
         named_bar_sync(2, kFeeders * 32);
@@ -379,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint4 raw[2][D / 32];
       auto row_of = [&](int r, int &rs, int &rh) {
         const int rr = tile * kRows + r;
-        rs = rr / p.G;
-        rh = hk * p.G + rr - rs * p.G;
+        rh = hk * p.G + rr % p.G;
+        rs = s + rr / p.G;
         return rr < pl.rows;
       };
       auto fetch = [&](int mt) {
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Entry &e = entries[entry & 1];
           e.n = t1 - t0;
           e.g0 = g0;
-          e.b = b, e.hk = hk, e.tile = tile;
+          e.b = b, e.hk = hk, e.tile = tile, e.s = s;
           e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
           e.c0 = e.c1 = (int)cta;
           if (e.slot >= 0) {
@@ -620,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           M = mx;
         }
         const int rr = first + r;
-        const int s = rr / p.G;
+        const int s = e.s + rr / p.G;
         const long long to =
-            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr - s * p.G;
+            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr % p.G;
         if (mine) {
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           reinterpret_cast<uint2 *>(p.o + to * D)[c] =
@@ -964,9 +965,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         odd = (votes >> (lane & 16) & 0xffffu) != 0u;  // any of the row's
         const float lse2 = some ? M + log2f(sum) : neg_inf;
         const int rr = first + r;
-        const int s = rr / p.G;
+        const int s = e.s + rr / p.G;
         const long long to =
-            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr - s * p.G;
+            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr % p.G;
         if (mine && e.slot < 0) {
 #pragma unroll
           for (int k = 0; k < kPer; ++k)
@@ -1027,16 +1028,15 @@ size_t attn_q8_step_workspace_bytes(int D) {
   return 256 + (size_t)kMaxCtas * 2 * 32 * (D + 1) * sizeof(float);
 }
 
-// S * G rows of a sequence and key head: all keys for up to 16, or 32 at 64
-// dimensions; a selection of single tokens for up to 16.
+// Rows that share keys: up to 16, or 32 of all keys at 64 dimensions.
 int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
                      cudaStream_t st) {
   StepPlan pl{};
   pl.all = p.topk == 0;
-  pl.rows = p.S * p.G;
+  pl.rows = pl.all ? p.S * p.G : p.G;
   const int mt = pl.rows > 16 ? 2 : 1;
   pl.tiles = (pl.rows + 16 * mt - 1) / (16 * mt);
-  const long long items = (long long)pl.tiles * p.Hk;
+  const long long items = (long long)pl.tiles * p.Hk * (pl.all ? 1 : p.S);
   if (items * p.B >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
   pl.items_b = (int)items;
   pl.box = p.blk >= 32 ? 32 : 16;
