@@ -7,6 +7,12 @@
 // where the group holds earlier tokens (it begins before start[b]), s is not
 // smaller than the scale s0 that it has, and their codes c become
 // round(c s0 / s) where it is larger.  New codes are round(x / s).
+//
+// Bounded by loads in flight.  Measured on one GB300 (copies 6767 GB/s), on the
+// device: a ragged chunk of 4 x 2048 tokens of 40 + 2 x 8 heads of 64 27 us (103
+// MB, 15 us; the queries alone take 17.5, keys and values alone 13), one token of
+// 64 sequences of 64 + 2 x 4 heads of 128 5.1 us.  Read back: two prefixes of up
+// to 30000 tokens of 8 heads of 128 62.6 us, 5.6 TB/s, 70% of it writes.
 #include "cache_q8.cuh"
 #include "norm_rope.cuh"
 

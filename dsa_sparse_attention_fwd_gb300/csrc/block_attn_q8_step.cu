@@ -9,9 +9,9 @@
 // spans CTAs leaves its parts in the workspace, joined by the CTA that
 // finishes last in the order of the slices.
 //
-// A producer warp walks the slice (block lists, pages, scales) and fills a
-// ring of shared memory by TMA, each of eight warps having its own stages: a
-// step of 32 keys goes to one warp, which keeps its own running maximum, sum
+// Four warps walk the slice (block lists, pages, scales, queries) and fill a
+// ring of shared memory by TMA, each of the eight others having its own stages:
+// a step of 32 keys goes to one warp, which keeps its own running maximum, sum
 // and output for the item; the warps meet only at an item's end, while the
 // ring fills with the next.  The products are mma.sync m16n8k16: a tile of a
 // few rows cannot fill a tcgen05 tile, whose operands would have to be
@@ -33,6 +33,14 @@
 // Values that are not finite: masked scores are replaced before use, value
 // rows that no row of the tile sees are zeroed in registers, and rows whose
 // result is not finite are computed again on their own (block_attn_q8.cuh).
+//
+// Measured on one GB300 (copies 6767 GB/s), on the device: 64 single tokens over
+// all of 2048 to 32767 keys, 4 heads of 128, 1.09 GB: 186 us, 5.8 TB/s; the loop
+// is 161 of 178 us of a CTA (6.7 TB/s), the start 4, the ends of its 2.7 items 6,
+// the last join 5, and the last CTA ends 15 us after the mean.  One token over
+// 131064 keys: 52.6 us of 39.7.  34 blocks of 64 for 64 tokens: 43 us, of which
+// the loop is 23: items of 68 steps over eight warps end often.  One warp loading
+// for all took 725 cycles a step (358 us); four take less than the memory's 330.
 #include "block_attn_host.cuh"
 #include "block_attn_q8.cuh"
 #include "ptx.cuh"

@@ -764,11 +764,16 @@ DSA_API int dsa_paged_read_q8(const void *k_cache, const void *v_cache,
 /*
  * dsa_block_attn_paged_fwd() over it: selected blocks and local ones, or, with
  * topk = 0 and local_blocks = max_pages * page_size / block_size, all keys up
- * to each row's position.  The cache's values are multiplied as they are (e4m3
- * to fp16 is exact; the queries enter as fp16 scaled by a power of two a row,
- * 2^-24 of the row's largest value); scores, statistics and sums in fp32; the
- * softmax weights, times the values' scale, enter the output product as fp16.
- * Envelope: that of dsa_block_attn_paged_fwd() and of the cache.
+ * to each row's position.  The cache's values are multiplied as they are; the
+ * queries enter as fp16 or as the sum of two e4m3 values, after a power of two a
+ * row (exactly but for elements below 2^-9 of the row's largest: off by 2^-17 of
+ * that at most); scores, statistics and sums in fp32; the softmax
+ * weights, times the values' scale, enter the output product as fp16 (weights
+ * below 2^-31 of the row's largest such product count as nothing in o).
+ * Envelope: that of dsa_block_attn_paged_fwd() and of the cache, D in {64, 128}.
+ * What a masked key's or value's code or scale holds (NaN too) does not reach a
+ * row.  Counts in the workspace's first 256 bytes are zero between calls; after
+ * DSA_ERR_DEVICE_TIMEOUT zero them again.
  *   workspace: dsa_block_attn_q8_workspace_size() bytes (T = max_pages *
  *   page_size), 256-byte aligned (0 for invalid sizes).
  */
