@@ -759,6 +759,84 @@ def test_streams_and_graphs(dsa, case):
     assert dsa.dsa_indexer_check(ws) == 0
 
 
+@gpu
+@pytest.mark.parametrize("case", [
+    # S, B, H, Hk, D, block, topk, local, shared, page, group, pages
+    (40, 42, 8, 4, 64, 16, 2, 1, False, 32, 16, 3),
+    (33, 80, 6, 2, 128, 32, 0, 99, True, 32, 32, 3),
+    (5, 200, 17, 1, 128, 64, 2, 1, True, 64, 64, 2),
+    (7, 170, 33, 1, 64, 128, 0, 99, True, 128, 128, 1),
+])
+def test_attention_of_many_tiles(dsa, case):
+    """Enough tiles that none is cut into parts."""
+    a = attn_inputs(case, 10)
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) == 0
+    r, T = reference(a)
+    check_attn(r, o, lse, T)
+
+
+@gpu
+@pytest.mark.parametrize("case", [
+    # block lists that leave the ring of a single token one stage, and those of
+    # a tile with every block that there may be
+    (1, 2, 4, 1, 128, 16, 9000, 3, True, 1024, 128, 256),
+    (1, 1, 3, 1, 64, 16, 16000, 1, True, 4096, 64, 64),
+    (33, 1, 2, 1, 128, 16, 700, 2, True, 1024, 128, 256),
+    (33, 1, 2, 1, 64, 16, 700, 2, True, 1024, 128, 256),
+])
+def test_attention_of_the_longest_lists(dsa, case):
+    a = attn_inputs(case, 11)
+    a["q_pos"][0] = case[9] * case[11] - case[0]
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) == 0
+    r, T = reference(a)
+    r["w_top"] = w_top(a, T)
+    check_attn(r, o, lse, T)
+
+
+@gpu
+@pytest.mark.parametrize("S,H,D", [(3, 4, 64), (2, 8, 128), (2, 24, 64)])
+def test_attention_of_the_longest_cache(dsa, S, H, D):
+    """All of 2^21 keys: as many steps as an item can have.  (The last case
+    takes the kernel for many rows.)"""
+    page, group, block = 4096, 128, 128
+    T = 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(D + H)
+    kc, vc = ((torch.randn((T // page, page, 1, D), generator=g, device="cuda")
+               * 100).clamp(-448, 448).to(E4M3) for _ in "kv")
+    ks, vs = (2.0 ** torch.randint(-9, -4, (T // page, page // group, 1),
+                                   generator=g, device="cuda").float()
+              for _ in "kv")
+    table = torch.randperm(T // page, generator=g, device="cuda")
+    table = table.to(torch.int32)[None]
+    q = torch.randn((S, 1, H, D), generator=g, device="cuda").to(BF)
+    q_pos = torch.tensor([T - S], dtype=torch.int32, device="cuda")
+    o, lse, ws = dsa.dsa_block_attn_paged_q8_fwd(
+        q, kc, vc, ks, vs, table, None, block, 0.11, q_pos=q_pos,
+        local_blocks=T // block)
+    assert dsa.dsa_indexer_check(ws) == 0
+    order = table[0].long()
+    k, v = ((c.double() * s.double().repeat_interleave(group, 1)[..., None])
+            [order].view(T, D) for c, s in ((kc, ks), (vc, vs)))
+    scale_of = vs.double().repeat_interleave(group, 1)[order].view(T)
+    r = {n: torch.zeros((S, 1, H, D), dtype=torch.float64) for n in ("o", "A_o")}
+    r["lse"], r["X"] = (torch.zeros((S, 1, H), dtype=torch.float64)
+                        for _ in "ab")
+    r["w_top"] = torch.zeros((S, 1, H, 1), dtype=torch.float64)
+    for s in range(S):
+        n = T - S + s + 1
+        x = 0.11 * q[s, 0].double() @ k[:n].T
+        z = torch.logsumexp(x, 1)
+        w = torch.exp(x - z[:, None])
+        r["o"][s, 0], r["lse"][s, 0] = (w @ v[:n]).cpu(), z.cpu()
+        r["A_o"][s, 0] = (w @ v[:n].abs()).cpu()
+        r["X"][s, 0] = (0.11 * q[s, 0].double().abs()
+                        @ k[:n].abs().T).amax(1).cpu()
+        r["w_top"][s, 0, :, 0] = (w * scale_of[:n]).amax(1).cpu()
+    check_attn(r, o, lse, T)
+
+
 # ---- together, streams, threads ---------------------------------------------------
 
 @gpu
@@ -805,6 +883,69 @@ def test_a_layer_served(dsa):
         # (codes that were subnormal on the way are a step apart at most)
         step = cache[2 + i].amax() * 2.0 ** -9
         assert float((a[i].float() - b[i].float()).abs().max()) <= float(step)
+
+
+@gpu
+@pytest.mark.parametrize("S", [1, 20])
+def test_a_step_captured(dsa, S):
+    """Append, attention over all keys and read back in one graph, replayed as
+    the sequences grow; a sequence that is not served keeps its cache."""
+    B, H, Hk, D, page, group, pages = 3, 8, 2, 64, 64, 32, 4
+    g = torch.Generator().manual_seed(S)
+    cache = [t.cuda() for t in make_cache(B * pages, page, Hk, D, group, 4)]
+    eager = [t.clone() for t in cache]
+    table = torch.randperm(B * pages, generator=g).to(torch.int32)
+    table = table.view(B, pages).cuda()
+    f = inv(D).cuda()
+    x = torch.zeros((S, B, H + 2 * Hk, D), dtype=BF, device="cuda")
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    count = torch.zeros(B, dtype=torch.int32, device="cuda")
+    status = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    size = dsa.dsa_block_attn_q8_workspace_size(S, B, H, Hk, D, page * pages,
+                                                16, 0, page * pages // 16)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+
+    def step(c):
+        q, _ = dsa.dsa_paged_append_q8(
+            x[:, :, H:H + Hk], x[:, :, H + Hk:], *c, table, start, count,
+            inv_freq=f, q=x[:, :, :H], workspace=status)
+        o, lse, _ = dsa.dsa_block_attn_paged_q8_fwd(
+            q, *c, table, None, 16, 0.125, q_pos=start,
+            local_blocks=page * pages // 16, workspace=ws)
+        k, v, _ = dsa.dsa_paged_read_q8(*c, table, page * pages, length=count,
+                                        workspace=status)
+        return q, o, lse, k, v
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):        # (appends nothing: counts are zero)
+        step([t.clone() for t in cache])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(cache)
+    at = [0, 37, 100]
+    untouched = [raw(t)[table[1].long()].clone() if t.dtype is E4M3
+                 else t[table[1].long()].clone() for t in cache]
+    for i in range(4):
+        x.copy_(torch.randn(x.shape, generator=g).to(BF))
+        n = [S, 0, S - S // 3]
+        start.copy_(torch.tensor(at, dtype=torch.int32))
+        count.copy_(torch.tensor(n, dtype=torch.int32))
+        graph.replay()
+        want = step(eager)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        for a, b in zip(cache, eager):
+            assert torch.equal(raw(a), raw(b))
+        at = [p + m for p, m in zip(at, n)]
+    for t, was in zip(cache, untouched):
+        now = t[table[1].long()] if t.dtype is not E4M3 else \
+            raw(t)[table[1].long()]
+        assert torch.equal(now, was)
+    assert dsa.dsa_indexer_check(status) == 0
+    assert dsa.dsa_indexer_check(ws) == 0
 
 
 @gpu
