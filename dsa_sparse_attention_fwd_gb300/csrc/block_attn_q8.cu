@@ -16,13 +16,13 @@ namespace {
 // tiles in a second launch, 4 us more of the host's time up to 76 pairs of
 // sequence and key head):
 //   all keys, 16 rows: few 18 / 50 / 151 for 1 / 16 / 64 sequences of 128
-//     dimensions, many 28 / 73 / 264; 32 rows: few 32 / 91 / 278, many 28 / 74 /
-//     266.  At 64 dimensions, 32 rows: few 20 / 51 / 155, many 19 / 72 / 243;
-//     64 rows: few 19 / 84 / 288, many 19 / 79 / 266.
+//     dimensions, many 28 / 69 / 252; 32 rows: few 32 / 91 / 278, many 28 / 69 /
+//     252.  At 64 dimensions, 32 rows: few 20 / 51 / 155, many 18 / 65 / 217;
+//     64 rows: few 19 / 84 / 288, many 19 / 74 / 244.
 //   a selection, one token, 16 rows: few 21 / 21 / 21 / 42 for 1 / 4 / 16 / 64
-//     sequences, many 16 / 18 / 23 / 47 (two launches up to 16).
-//   a selection, four tokens of 8 heads: few 18 / 20 / 37 / 116, many 25 / 20 /
-//     30 / 69, where tokens that share blocks read them once.
+//     sequences, many 16 / 18 / 22 / 46 (two launches up to 16).
+//   a selection, four tokens of 8 heads: few 18 / 20 / 37 / 116, many 24 / 19 /
+//     28 / 67, where tokens that share blocks read them once.
 bool few_rows(int S, int B, int Hk, int G, int D, int topk) {
   if (topk > 0)
     return G <= 16 && (S == 1 || (long long)S * B * Hk <= 128);

@@ -19,13 +19,16 @@
 // largest (see block_attn_q8_step.cu).
 //
 // Measured on one GB300 (bf16 peak 1908 TFLOP/s): 2 x 512 tokens of 32 / 8 heads
-// of 128 over all of 8000 to 15800 keys 244 to 269 us, 836 TFLOP/s; 3 x 777
-// tokens of 40 / 8 heads of 64, 34 blocks of 64, 318 us (the bf16 tiles: 286 to
-// 302).  No unit is busy more than half of the time (tcgen05 41%, issue 50%,
-// exponentials 20%, ALU 38%): a step is a chain of the score product, tensor
+// of 128 over all of 8000 to 15800 keys 227 to 249 us, 900 TFLOP/s; 3 x 777
+// tokens of 40 / 8 heads of 64, 34 blocks of 64, 294 us (the bf16 tiles: 286 to
+// 302).  No unit is busy more than half of the time (tcgen05 45%, issue 51%,
+// exponentials 21%, ALU 40%): a step is a chain of the score product, tensor
 // memory to registers, softmax, and back, which two CTAs an SM overlap twofold.
 // Leaving out one part of it in a copy gave little: the conversion 0 to 3%, the
-// exponentials 8%, half the score product 1 to 3%, the maximum 2 to 4%.
+// exponentials 8%, half the score product 1 to 3%, the maximum 2 to 4%.  Two
+// threads a row were slower (322 -> 378 us: a barrier of two warps a step), and
+// so were tiles cut in parts where there are one to three a CTA slot (268 ->
+// 287): two CTAs at work fill an SM, the parts only add their ends.
 //
 // Warps: 0 .. 3 softmax (thread = row = tensor-memory lane), 4 .. 7 convert the
 // values, 8 TMA producer, 9 MMA issuer and tensor-memory allocator; two CTAs an
@@ -407,9 +410,11 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     for (int i = 0; i < n; ++i) {
       const int st = i % NV;
       const uint32_t ph = i / NV & 1u;
-      // values that no row sees
-      const bool zero = ((t0 + i) << lupt) + (row >> lu) >= units ||
-                        key_at(t0 + i, row) > pos_hi;
+      // values that no row sees: only the last block can hold any (the others
+      // lie before the last row's own), and what fills a ragged step up
+      const bool zero = (t0 + i + 1) << lupt > units - (1 << lper) &&
+                        (((t0 + i) << lupt) + (row >> lu) >= units ||
+                         key_at(t0 + i, row) > pos_hi);
       if (!__all_sync(0xffffffffu, wait_bar_rest_inl(v8_full(st), ph, abort_flag,
                                                      p.status)))
         goto done;
