@@ -65,6 +65,13 @@ struct TileSmem {
   // q_full, s_full p_full o_done (two each), then k_full k_empty, v8_full
   // v8_empty, v_full v_empty, meta_full
   static constexpr int kBars = 7 + 2 * kKStages + 4 * kVStages + kMeta;
+  // Arrivals of a phase of barrier i: one for each warp where four arrive.
+  static constexpr int arrivals(int i) {
+    const int v8_empty = 7 + 2 * kKStages + kVStages;
+    const bool four = i == 0 || i == 3 || i == 4 ||  // q_full, p_full
+                      (i >= v8_empty && i < v8_empty + 2 * kVStages);  // v_full
+    return four ? 4 : 1;
+  }
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kOffWords = kOffMisc + 32;
   static constexpr int bytes(int nblk, int cap) {
@@ -232,13 +239,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const int nq = min(pl.qt, p.S - s0);
 
   if (tid == 0) {
-    for (int i = 0; i < L::kBars; ++i) mbar_init(bars + 8 * i, 1);
-    mbar_init(q_full, 4);
-    for (int i = 0; i < 2; ++i) mbar_init(p_full(i), 4);
-    for (int i = 0; i < NV; ++i) {
-      mbar_init(v8_empty(i), 4);
-      mbar_init(v_full(i), 4);
-    }
+    // (each once: a barrier that is one already may not be initialised again)
+    for (int i = 0; i < L::kBars; ++i)
+      mbar_init(bars + 8 * i, L::arrivals(i));
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_k);
