@@ -498,9 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the largest value to [2^14, 2^15)
+            // the largest value to [2^14, 2^15), whatever finite value it is
             int eq = (__float_as_int(top) >> 23) - 127 - 14;
-            eq = min(max(eq, -100), 100);
+            eq = max(eq, -100);
             f[i] = q8_pow2(-eq);
             if (fw == 0 && tq == 0)
               rw.cr[mt * 16 + gq + 8 * i] =

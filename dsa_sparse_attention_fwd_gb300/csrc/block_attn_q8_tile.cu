@@ -480,7 +480,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
                         ? (__float_as_int(top) >> 23) - 127 - 8 +
                               ((__float_as_int(top) & 0x7fffff) > 0x600000)
                         : 0;
-      const int eq = min(max(e, -100), 100);
+      // (120 at most: no finite query is clamped from above.  Below -100 the
+      // factor c times the scales would leave fp32.)
+      const int eq = max(e, -100);
       const float f = q8_pow2(-eq);
       cr = p.scale * 1.4426950408889634f * q8_pow2(eq);
       if (!(top < __int_as_float(0x7f800000)))
