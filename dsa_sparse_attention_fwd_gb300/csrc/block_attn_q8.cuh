@@ -31,12 +31,12 @@ int run_attn_q8_tile(const BlockAttnQ8 &p, void *workspace, int num_sms,
 // One row by one warp in fp32 on the CUDA cores: a running maximum and sum
 // over its keys, 32 at a time, lane l holding one.  Rows whose fast result is
 // not finite are computed again by it: a key that only other rows of a tile
-// see may hold anything.  qs: the query as fp32 in shared memory, this
-// warp's own copy; lane l returns o[l + 32 i] in acc[i].
+// see may hold anything.  qs: the query times 2^-eq as fp32 in shared memory,
+// this warp's own copy; lane l returns o[l + 32 i] in acc[i].
 __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
-                                                int s, int hk, const float *qs,
-                                                int lane, bool &bad,
-                                                float (&acc)[4], float &lse) {
+                                            int s, int hk, const float *qs,
+                                            int eq, int lane, bool &bad,
+                                            float (&acc)[4], float &lse) {
   const float neg_inf = -__int_as_float(0x7f800000);
   const long long pos = row_pos(p.q_pos, b, s);
   const int32_t *ids = row_ids(p, b, s, hk);
@@ -60,7 +60,7 @@ __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
       const long long j = (long long)n * p.blk + jj;
       const bool has = jj < p.blk && j <= pos && j < p.T;
       const int off = off0 + min(jj, p.blk - 1);
-      const float sk = q8_pow2(q8_exp(__ldg(p.c.ks + q8_scale_at(p.c, page, off, hk))));
+      const int ek = q8_exp(__ldg(p.c.ks + q8_scale_at(p.c, page, off, hk)));
       const float sv = q8_pow2(q8_exp(__ldg(p.c.vs + q8_scale_at(p.c, page, off, hk))));
       const uint8_t *kr =
           p.c.k + page * p.c.k_p + off * p.c.k_t + hk * p.c.k_h;
@@ -75,7 +75,7 @@ __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
           x = fmaf(qs[d + 2], hi.x, x);
           x = fmaf(qs[d + 3], hi.y, x);
         }
-        x *= sk * p.scale;
+        x = scalbnf(x * p.scale, ek + eq);  // (the factor may pass fp32)
       }
       float t = has ? x : neg_inf;
       for (int o = 16; o; o >>= 1)
@@ -106,6 +106,31 @@ __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
   const bool some = l > 0.f || l != l;
   for (int k = 0; k < 4; ++k) acc[k] = some ? acc[k] / l : 0.f;
   lse = some ? m + logf(l) : neg_inf;
+}
+
+// The same, written to o and lse: row s, head h.  qs: 128 floats.  The query
+// is brought to [1, 2) first, so that its products stay within fp32 whatever
+// finite values it has.  (Inlined, rare as it is: kernels with setmaxnreg make
+// no calls.)
+__device__ __forceinline__ void redo_row_q8(const BlockAttnQ8 &p, int b, int s,
+                                            int h, float *qs, int lane) {
+  const size_t at = ((size_t)s * p.B + b) * p.H + h;
+  float top = 0.f;
+  for (int d = lane; d < p.D; d += 32)
+    top = fmaxf(top, fabsf(__bfloat162float(p.q[at * p.D + d])));
+  top = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(top)));
+  const int eq = min(max((__float_as_int(top) >> 23) - 127, -100), 120);
+  const float f = q8_pow2(-eq);
+  __syncwarp();
+  for (int d = lane; d < p.D; d += 32)
+    qs[d] = __bfloat162float(p.q[at * p.D + d]) * f;
+  __syncwarp();
+  bool bad = false;
+  float acc[4], lse;
+  attn_row_q8(p, b, s, h / p.G, qs, eq, lane, bad, acc, lse);
+  for (int i = 0; i * 32 < p.D; ++i)
+    p.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
+  if (lane == 0) p.lse[at] = lse;
 }
 
 }  // namespace dsa

@@ -194,22 +194,6 @@ __device__ __forceinline__ unsigned steps_bound(const BlockAttnQ8 &p,
   return ((unsigned)max(keys - 1, 0) >> (5 + shift)) + 1u;
 }
 
-// (Inlined, rare as it is: kernels with setmaxnreg make no calls.)
-__device__ __forceinline__ void redo_row(const BlockAttnQ8 &p, int b, int s,
-                                      int hk, long long at, float *qs,
-                                      int lane) {
-  __syncwarp();
-  for (int d = lane; d < p.D; d += 32)
-    qs[d] = __bfloat162float(p.q[at * p.D + d]);
-  __syncwarp();
-  float acc[4], lse;
-  bool bad = false;
-  attn_row_q8(p, b, s, hk, qs, lane, bad, acc, lse);
-  for (int i = 0; i * 32 < p.D; ++i)
-    p.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
-  if (lane == 0) p.lse[at] = lse;
-}
-
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_q8_step_kernel(const __grid_constant__ Maps8 maps,
@@ -629,9 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           M = mx;
         }
         const int rr = first + r;
-        const int s = e.s + rr / p.G;
-        const long long to =
-            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr % p.G;
+        const int s = e.s + rr / p.G, h = e.hk * p.G + rr % p.G;
+        const long long to = ((long long)s * p.B + e.b) * p.H + h;
         if (mine) {
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           reinterpret_cast<uint2 *>(p.o + to * D)[c] =
@@ -645,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned odd = __ballot_sync(0xffffffffu, mine && again && c == 0);
         for (; odd; odd &= odd - 1) {
           const int src = __ffs(odd) - 1;
-          redo_row(p, e.b, __shfl_sync(0xffffffffu, s, src), e.hk,
-                   __shfl_sync(0xffffffffu, to, src), qs, lane);
+          redo_row_q8(p, e.b, __shfl_sync(0xffffffffu, s, src),
+                      __shfl_sync(0xffffffffu, h, src), qs, lane);
         }
       }
     };
@@ -973,9 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         odd = (votes >> (lane & 16) & 0xffffu) != 0u;  // any of the row's
         const float lse2 = some ? M + log2f(sum) : neg_inf;
         const int rr = first + r;
-        const int s = e.s + rr / p.G;
-        const long long to =
-            ((long long)s * p.B + e.b) * p.H + e.hk * p.G + rr % p.G;
+        const int s = e.s + rr / p.G, h = e.hk * p.G + rr % p.G;
+        const long long to = ((long long)s * p.B + e.b) * p.H + h;
         if (mine && e.slot < 0) {
 #pragma unroll
           for (int k = 0; k < kPer; ++k)
@@ -998,8 +980,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           unsigned again = __ballot_sync(0xffffffffu, mine && odd && j == 0);
           for (; again; again &= again - 1) {
             const int src = __ffs(again) - 1;
-            redo_row(p, e.b, __shfl_sync(0xffffffffu, s, src), e.hk,
-                     __shfl_sync(0xffffffffu, to, src), qs, lane);
+            redo_row_q8(p, e.b, __shfl_sync(0xffffffffu, s, src),
+                        __shfl_sync(0xffffffffu, h, src), qs, lane);
           }
         }
       }

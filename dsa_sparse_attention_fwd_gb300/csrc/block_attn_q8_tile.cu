@@ -140,22 +140,6 @@ __device__ __forceinline__ bool wait_both(uint32_t bar0, uint32_t parity0,
           wait_bar_rest_inl(bar1, parity1, abort_flag, status));
 }
 
-// One row on its own, by one warp (qs: 128 floats of shared memory).
-__device__ __forceinline__ void redo_row8(const BlockAttnQ8 &p, int b, int s,
-                                       int h, float *qs, int lane) {
-  const size_t at = ((size_t)s * p.B + b) * p.H + h;
-  __syncwarp();
-  for (int d = lane; d < p.D; d += 32)
-    qs[d] = __bfloat162float(p.q[at * p.D + d]);
-  __syncwarp();
-  bool bad = false;
-  float acc[4], lse;
-  attn_row_q8(p, b, s, h / p.G, qs, lane, bad, acc, lse);
-  for (int i = 0; i * 32 < p.D; ++i)
-    p.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
-  if (lane == 0) p.lse[at] = lse;
-}
-
 // words[] of a tile without a selection: the local blocks of each query.
 __device__ __forceinline__ void mark_local(const BlockAttnQ8 &p, int b, int s0,
                                            int nq, uint32_t *words, int tid,
@@ -682,6 +666,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     }
     odd |= some && !(chk.x + chk.y == 0.f);
     odd |= n > 0 && cr != cr;
+    // m is rounded, the multiply-adds that it is taken from are not: above 2^25
+    // they are a whole power of two apart, and a row may lose all its weights
+    odd |= m > neg_inf && fabsf(m) > 33554432.f;
     odd &= live;
     if (live) {
       const float lse2 = some ? m + log2f(l) : neg_inf;
@@ -697,7 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       float *qs = reinterpret_cast<float *>(smem + L::kOffQ) + warp * 1024;
       for (; todo; todo &= todo - 1) {
         const int r = warp * 32 + __ffs(todo) - 1;
-        redo_row8(p, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
+        redo_row_q8(p, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
       }
     }
   }
@@ -775,7 +762,7 @@ __global__ void __launch_bounds__(256)
     }
     const int h = hk * p.G + row % p.G;
     if (odd) {  // (all lanes of the warp)
-      redo_row8(p, b, s, h, qs[warp], lane);
+      redo_row_q8(p, b, s, h, qs[warp], lane);
       continue;
     }
     const size_t at = ((size_t)s * p.B + b) * p.H + h;

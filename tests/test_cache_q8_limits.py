@@ -54,3 +54,35 @@ def test_rows_of_large_queries(dsa, case, power):
     r, T = reference(a)
     assert float(r["lse"][0, 0].abs().min()) > 2.0 ** (power - 20)
     check_attn(r, o, lse, T)
+
+
+@gpu
+@pytest.mark.parametrize("power", [20, 24, 26, 28, 31, 35, 40, 64, 100, 120])
+@pytest.mark.parametrize("case", KERNELS)
+def test_large_scores_of_one_key(dsa, case, power):
+    """Rows of one key, with scores of either sign and any size."""
+    a = attn_inputs(case, 23)
+    a["q_pos"][0] = 0
+    a["q"][0, 0] = (a["q"][0, 0].float() * 2.0 ** power).to(BF)
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) == 0
+    r, T = reference(a)
+    row = r["lse"][0, 0]
+    assert row.numel() < 4 or bool((row < 0).any()) and bool((row > 0).any())
+    check_attn(r, o, lse, T)
+    assert bool((o[0, 0].double().cpu() - r["o"][0, 0]).abs().max() <= 2.0 ** -8
+                * r["o"][0, 0].abs().max())
+
+
+@gpu
+@pytest.mark.parametrize("power", [64, 112, 120])
+@pytest.mark.parametrize("case", [ATTN[5], ATTN[12], ATTN[13]])
+def test_rows_of_large_queries_in_tiles(dsa, case, power):
+    """(As above, of the kernel for many rows.)"""
+    a = attn_inputs(case, 22)
+    a["q"][0, 0] = (a["q"][0, 0].float() * 2.0 ** power).to(BF)
+    a["q"][-1, -1, 0] = (a["q"][-1, -1, 0].float() * 2.0 ** power).to(BF)
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) == 0
+    r, T = reference(a)
+    check_attn(r, o, lse, T)
