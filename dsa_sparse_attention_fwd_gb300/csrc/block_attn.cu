@@ -502,6 +502,10 @@ __global__ void __launch_bounds__(kFwdThreads, 2)
                        lane);
     }
     odd |= some && !(chk.x + chk.y == 0.f);
+    // m is a rounded product, the weights' exponents are multiply-adds of its
+    // factors: above 2^25 they are a whole power of two apart, and a row may
+    // lose all its weights
+    odd |= m > neg_inf && fabsf(m) > 33554432.f;
     odd &= live;
     if (live) {
       const float lse2 = some ? m + log2f(l) : neg_inf;
