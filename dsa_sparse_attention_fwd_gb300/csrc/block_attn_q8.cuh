@@ -29,21 +29,29 @@ int run_attn_q8_tile(const BlockAttnQ8 &p, void *workspace, int num_sms,
                      cudaStream_t st);
 
 // One row by one warp in fp32 on the CUDA cores: a running maximum and sum
-// over its keys, 32 at a time, lane l holding one.  Rows whose fast result is
-// not finite are computed again by it: a key that only other rows of a tile
-// see may hold anything.  qs: the query times 2^-eq as fp32 in shared memory,
-// this warp's own copy; lane l returns o[l + 32 i] in acc[i].
+// over its keys, 32 at a time, lane l holding one.  Rows of a tile whose fast
+// result is not finite are computed again by it where a key that only other rows
+// see may be the reason.  qs: the query times 2^-eq as fp32 in shared memory,
+// this warp's own copy; lane l returns o[l D / 32 + i] in acc[i].
+//
+// A chain of loads, those of 32 keys and their values on the way together: 3
+// to 5 ms for 131072 keys, 125 ms for 2^21 (a key at a time it was 19 and 450),
+// so that the four rows that a warp may have end well within the limit of the
+// waits for it, four seconds.
+template <int D>
 __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
                                             int s, int hk, const float *qs,
                                             int eq, int lane, bool &bad,
-                                            float (&acc)[4], float &lse) {
+                                            float (&acc)[D / 32], float &lse) {
+  constexpr int C = D / 32;  // columns of a lane
   const float neg_inf = -__int_as_float(0x7f800000);
   const long long pos = row_pos(p.q_pos, b, s);
   const int32_t *ids = row_ids(p, b, s, hk);
   const int n_cand = p.topk + p.local;
   float m = neg_inf, l = 0.f;
-  for (int i = 0; i < 4; ++i) acc[i] = 0.f;
-  for (int i = 0; i < n_cand; ++i) {
+  for (int i = 0; i < C; ++i) acc[i] = 0.f;
+  // (a sum that is not a number stays one, and o with it)
+  for (int i = 0; i < n_cand && l == l; ++i) {
     if (i >= p.topk && pos < (long long)(i - p.topk) << p.lb) break;
     const int n = candidate(p, ids, pos, i, bad);
     if (n < 0) continue;
@@ -59,30 +67,46 @@ __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
       const int jj = c + lane;
       const long long j = (long long)n * p.blk + jj;
       const bool has = jj < p.blk && j <= pos && j < p.T;
+      const unsigned any = __ballot_sync(0xffffffffu, has);
+      if (!any) continue;
       const int off = off0 + min(jj, p.blk - 1);
       const int ek = q8_exp(__ldg(p.c.ks + q8_scale_at(p.c, page, off, hk)));
       const float sv = q8_pow2(q8_exp(__ldg(p.c.vs + q8_scale_at(p.c, page, off, hk))));
-      const uint8_t *kr =
-          p.c.k + page * p.c.k_p + off * p.c.k_t + hk * p.c.k_h;
+      // (keys that the row does not see lie in the page, too: read, not used)
+      const uint4 *kr = reinterpret_cast<const uint4 *>(
+          p.c.k + page * p.c.k_p + off * p.c.k_t + hk * p.c.k_h);
       const long long vo = page * p.c.v_p + off * p.c.v_t + hk * p.c.v_h;
-      float x = 0.f;
-      if (has) {
-        for (int d = 0; d < p.D; d += 4) {
-          const uint32_t w = *reinterpret_cast<const uint32_t *>(kr + d);
-          const float2 lo = q8_float2(w & 0xffffu), hi = q8_float2(w >> 16);
-          x = fmaf(qs[d], lo.x, x);
-          x = fmaf(qs[d + 1], lo.y, x);
-          x = fmaf(qs[d + 2], hi.x, x);
-          x = fmaf(qs[d + 3], hi.y, x);
-        }
-        x = scalbnf(x * p.scale, ek + eq);  // (the factor may pass fp32)
+      uint4 kw[D / 16];
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) kw[u] = __ldg(kr + u);
+      uint32_t v[32];
+#pragma unroll
+      for (int u = 0; u < 32; ++u) {
+        const uint8_t *at = p.c.v + __shfl_sync(0xffffffffu, vo, u) + lane * C;
+        if constexpr (C == 4)
+          v[u] = __ldg(reinterpret_cast<const uint32_t *>(at));
+        else
+          v[u] = __ldg(reinterpret_cast<const uint16_t *>(at));
       }
+      float x = 0.f;
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) {
+        const uint32_t w[4] = {kw[u].x, kw[u].y, kw[u].z, kw[u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float *qd = qs + 16 * u + 4 * k;
+          const float2 lo = q8_float2(w[k] & 0xffffu), hi = q8_float2(w[k] >> 16);
+          x = fmaf(qd[0], lo.x, x);
+          x = fmaf(qd[1], lo.y, x);
+          x = fmaf(qd[2], hi.x, x);
+          x = fmaf(qd[3], hi.y, x);
+        }
+      }
+      x = scalbnf(x * p.scale, ek + eq);  // (the factor may pass fp32)
       float t = has ? x : neg_inf;
       for (int o = 16; o; o >>= 1)
         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
       const float mn = fmaxf(m, t);
-      const unsigned any = __ballot_sync(0xffffffffu, has);
-      if (!any) continue;
       // a finite stand-in while every score so far is -inf
       const float mu = mn > neg_inf ? mn : 0.f;
       const float f = m > neg_inf ? expf(m - mu) : 0.f;
@@ -90,21 +114,24 @@ __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
       float es = e;
       for (int o = 16; o; o >>= 1) es += __shfl_xor_sync(0xffffffffu, es, o);
       l = l * f + es;
-      for (int k = 0; k < 4; ++k) acc[k] *= f;
+      if (l != l) break;
+      for (int k = 0; k < C; ++k) acc[k] *= f;
       m = mn;
-      for (int t2 = 0; t2 < 32; ++t2) {
-        const long long at = __shfl_sync(0xffffffffu, vo, t2);
-        const float w = __shfl_sync(0xffffffffu, e * sv, t2);
-        if (!(any >> t2 & 1u)) continue;
-        for (int k = 0; k * 32 < p.D; ++k) {
-          const float2 v = q8_float2(p.c.v[at + lane + 32 * k]);
-          acc[k] = fmaf(w, v.x, acc[k]);
+#pragma unroll
+      for (int u = 0; u < 32; ++u) {
+        const float w = __shfl_sync(0xffffffffu, e * sv, u);
+        const uint32_t y = any >> u & 1u ? v[u] : 0u;
+#pragma unroll
+        for (int k = 0; k < C; k += 2) {
+          const float2 t2 = q8_float2(k ? y >> 16 : y & 0xffffu);
+          acc[k] = fmaf(w, t2.x, acc[k]);
+          acc[k + 1] = fmaf(w, t2.y, acc[k + 1]);
         }
       }
     }
   }
   const bool some = l > 0.f || l != l;
-  for (int k = 0; k < 4; ++k) acc[k] = some ? acc[k] / l : 0.f;
+  for (int k = 0; k < C; ++k) acc[k] = some ? acc[k] / l : 0.f;
   lse = some ? m + logf(l) : neg_inf;
 }
 
@@ -112,24 +139,29 @@ __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
 // is brought to [1, 2) first, so that its products stay within fp32 whatever
 // finite values it has.  (Inlined, rare as it is: kernels with setmaxnreg make
 // no calls.)
+template <int D>
 __device__ __forceinline__ void redo_row_q8(const BlockAttnQ8 &p, int b, int s,
                                             int h, float *qs, int lane) {
   const size_t at = ((size_t)s * p.B + b) * p.H + h;
   float top = 0.f;
-  for (int d = lane; d < p.D; d += 32)
-    top = fmaxf(top, fabsf(__bfloat162float(p.q[at * p.D + d])));
+  for (int d = lane; d < D; d += 32)
+    top = fmaxf(top, fabsf(__bfloat162float(p.q[at * D + d])));
   top = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(top)));
   const int eq = min(max((__float_as_int(top) >> 23) - 127, -100), 120);
   const float f = q8_pow2(-eq);
   __syncwarp();
-  for (int d = lane; d < p.D; d += 32)
-    qs[d] = __bfloat162float(p.q[at * p.D + d]) * f;
+  for (int d = lane; d < D; d += 32)
+    qs[d] = __bfloat162float(p.q[at * D + d]) * f;
   __syncwarp();
   bool bad = false;
-  float acc[4], lse;
-  attn_row_q8(p, b, s, h / p.G, qs, eq, lane, bad, acc, lse);
-  for (int i = 0; i * 32 < p.D; ++i)
-    p.o[at * p.D + lane + 32 * i] = __float2bfloat16(acc[i]);
+  float acc[D / 32], lse;
+  attn_row_q8<D>(p, b, s, h / p.G, qs, eq, lane, bad, acc, lse);
+  if constexpr (D == 128)
+    reinterpret_cast<uint2 *>(p.o + at * D)[lane] = make_uint2(
+        pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+  else
+    reinterpret_cast<uint32_t *>(p.o + at * D)[lane] =
+        pack_bf16x2(acc[0], acc[1]);
   if (lane == 0) p.lse[at] = lse;
 }
 

@@ -30,9 +30,11 @@
 // t) reads 16 neighbours of a key, and for the output product 16 neighbours of
 // the keys 2t and (2t + 1) ^ 4.
 //
-// Values that are not finite: masked scores are replaced before use, value
-// rows that no row of the tile sees are zeroed in registers, and rows whose
-// result is not finite are computed again on their own (block_attn_q8.cuh).
+// Values that are not finite: masked scores are replaced before use, and value
+// rows that no row of the tile sees are zeroed in registers.  What is not finite
+// then comes from a key that some row sees.  A row's own it keeps.  Where rows of
+// a tile see different keys (several queries over all keys), or a row's factor
+// may have left fp32, the row is computed again on its own (block_attn_q8.cuh).
 //
 // Measured on one GB300 (copies 6767 GB/s), on the device: 64 single tokens over
 // all of 2048 to 32767 keys, 4 heads of 128, 1.09 GB: 186 us, 5.8 TB/s; the loop
@@ -83,6 +85,13 @@ struct StepPlan {
 struct Maps8 {
   CUtensorMap k, v;
 };
+
+// In place of a part's log-sum: the row is to be computed again.  (A NaN that no
+// arithmetic gives.)
+constexpr int kAgain = 0x7fc0a9a1;
+// c times the query's power of two up to which scores are right whatever the
+// keys' scales (2^40 at most) and codes are.
+constexpr float kMostFactor = 1208925819614629174706176.f;  // 2^80
 
 // What the producer says of an item's part.
 struct Entry {
@@ -595,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float mx = M;
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            again |= ls[u] != ls[u];
+            again |= __float_as_int(ls[u]) == kAgain;
             mx = fmaxf(mx, ls[u]);
           }
           const float ref = mx > neg_inf ? mx : 0.f;
@@ -616,20 +625,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = e.s + rr / p.G, h = e.hk * p.G + rr % p.G;
         const long long to = ((long long)s * p.B + e.b) * p.H + h;
         if (mine) {
-          const float inv = sum > 0.f ? 1.f / sum : 0.f;
+          const bool some = sum > 0.f || sum != sum;
+          const float inv = some ? 1.f / sum : 0.f;
           reinterpret_cast<uint2 *>(p.o + to * D)[c] =
               make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
                          pack_bf16x2(acc.z * inv, acc.w * inv));
           if (c == 0)
-            p.lse[to] = sum > 0.f ? (M + log2f(sum)) * 0.69314718055994531f
-                                  : neg_inf;
+            p.lse[to] =
+                some ? (M + log2f(sum)) * 0.69314718055994531f : neg_inf;
         }
-        // rows with a part that is not finite
+        // rows with a part that says so
         unsigned odd = __ballot_sync(0xffffffffu, mine && again && c == 0);
         for (; odd; odd &= odd - 1) {
           const int src = __ffs(odd) - 1;
-          redo_row_q8(p, e.b, __shfl_sync(0xffffffffu, s, src),
-                      __shfl_sync(0xffffffffu, h, src), qs, lane);
+          redo_row_q8<D>(p, e.b, __shfl_sync(0xffffffffu, s, src),
+                         __shfl_sync(0xffffffffu, h, src), qs, lane);
         }
       }
     };
@@ -686,6 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int first = e.tile * kRows;
       const int live = min(pl.rows - first, kRows);
+      const bool mixed = pl.all && p.S > 1;  // rows that see different keys
       // the tile's rows see the same keys but where a step holds keys after
       // the first row's position or before the last row's first block
       int pos_lo = 0x7fffffff, lo_hi = 0;
@@ -945,6 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[k].w = fmaf(v.w, f[i], acc[k].w);
             }
             acc[k].x *= inv, acc[k].y *= inv, acc[k].z *= inv, acc[k].w *= inv;
+            if (!some) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             const float top = fmaxf(fmaxf(fabsf(acc[k].x), fabsf(acc[k].y)),
                                     fmaxf(fabsf(acc[k].z), fabsf(acc[k].w)));
             odd |= !(top <= 3e38f) || acc[k].x != acc[k].x ||
@@ -952,6 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    acc[k].w != acc[k].w;
           }
         }
+        odd &= mixed || rw.cr[r] > kMostFactor;
         const unsigned votes = __ballot_sync(0xffffffffu, mine && odd);
         odd = (votes >> (lane & 16) & 0xffffu) != 0u;  // any of the row's
         const float lse2 = some ? M + log2f(sum) : neg_inf;
@@ -972,16 +985,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < kPer; ++k)
             reinterpret_cast<float4 *>(pl.part_o + part * D)[j * kPer + k] =
                 acc[k];
-          // a NaN tells the joining CTA to compute the row again
           if (j == 0)
-            pl.part_l[part] = odd ? __int_as_float(0x7fffffff) : lse2;
+            pl.part_l[part] = __int_as_float(
+                odd            ? kAgain
+                : lse2 != lse2 ? 0x7fffffff
+                               : __float_as_int(lse2));
         }
         if (e.slot < 0) {
           unsigned again = __ballot_sync(0xffffffffu, mine && odd && j == 0);
           for (; again; again &= again - 1) {
             const int src = __ffs(again) - 1;
-            redo_row_q8(p, e.b, __shfl_sync(0xffffffffu, s, src),
-                        __shfl_sync(0xffffffffu, h, src), qs, lane);
+            redo_row_q8<D>(p, e.b, __shfl_sync(0xffffffffu, s, src),
+                           __shfl_sync(0xffffffffu, h, src), qs, lane);
           }
         }
       }

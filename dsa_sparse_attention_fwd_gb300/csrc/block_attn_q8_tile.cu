@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       float *qs = reinterpret_cast<float *>(smem + L::kOffQ) + warp * 1024;
       for (; todo; todo &= todo - 1) {
         const int r = warp * 32 + __ffs(todo) - 1;
-        redo_row_q8(p, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
+        redo_row_q8<D>(p, b, s0 + r / p.G, hk * p.G + r % p.G, qs, lane);
       }
     }
   }
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(256)
     }
     const int h = hk * p.G + row % p.G;
     if (odd) {  // (all lanes of the warp)
-      redo_row_q8(p, b, s, h, qs[warp], lane);
+      redo_row_q8<D>(p, b, s, h, qs[warp], lane);
       continue;
     }
     const size_t at = ((size_t)s * p.B + b) * p.H + h;

@@ -772,7 +772,11 @@ DSA_API int dsa_paged_read_q8(const void *k_cache, const void *v_cache,
  * below 2^-31 of the row's largest such product count as nothing in o).
  * Envelope: that of dsa_block_attn_paged_fwd() and of the cache, D in {64, 128}.
  * What a masked key's or value's code or scale holds (NaN too) does not reach a
- * row.  Counts in the workspace's first 256 bytes are zero between calls; after
+ * row.  To tell, rows of drafts over all keys and of chunks that share a tile
+ * with a NaN are computed again by a warp each, 3 to 5 ms for every 131072 keys;
+ * so are rows of infinite queries and, in chunks, of scores above 2^25.  Scores
+ * beyond fp32's range give NaN.
+ * Counts in the workspace's first 256 bytes are zero between calls; after
  * DSA_ERR_DEVICE_TIMEOUT zero them again.
  *   workspace: dsa_block_attn_q8_workspace_size() bytes (T = max_pages *
  *   page_size), 256-byte aligned (0 for invalid sizes).
