@@ -8,9 +8,12 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests.cache_q8_ref import E4M3
+from tests.block_ref import row_keys
+from tests.cache_q8_ref import E4M3, dense
 from tests.test_cache_q8 import (ATTN, BF, attn_inputs, call, check_attn,
-                                 dsa, raw, reference)  # noqa: F401
+                                 dsa, raw, reference, test_append as append_as,
+                                 test_append_of_unaligned_rows as
+                                 append_unaligned_as)  # noqa: F401
 
 gpu = pytest.mark.gpu
 
@@ -192,3 +195,143 @@ def test_a_nan_in_a_selection(dsa, S, B, H, Hk, D):
         assert torch.equal(torch.isnan(lse2),
                            sees if which == "kc" else torch.zeros_like(sees))
         assert bool(((o2.double() - o.double()).abs() <= tol)[~bad].all())
+
+
+# ---- appends of every width --------------------------------------------------
+
+# head size, rotated part and its start, pairs of neighbours
+WIDTHS = [(64, 64, 0, False), (48, 16, 16, True), (128, 64, 64, False),
+          (96, 96, 0, True), (192, 64, 0, False), (256, 256, 0, True)]
+
+
+@gpu
+@pytest.mark.parametrize("S", [1, 2, 3, 4, 8, 9, 40, 150])
+@pytest.mark.parametrize("width,group", [
+    (w, n) for w in WIDTHS for n in (16, 32, 64, 128) if w[0] * n <= 16384])
+def test_append_of_every_width(dsa, width, group, S):
+    """As many new rows as a warp, two passes of a warp or a CTA take, in groups
+    of every size, normed and rotated, beginning inside groups."""
+    D, R, r0, inter = width
+    append_as(dsa, (S, 4, 6, 2, D, R, r0, inter, 128, 4, group, S % 2 == 0,
+                    S > 4), True)
+
+
+@gpu
+@pytest.mark.parametrize("S", [1, 2, 3, 100])
+@pytest.mark.parametrize("D,R,group", [
+    (64, 24, 128), (128, 36, 128), (112, 64, 16), (192, 64, 64), (256, 256, 16)])
+def test_append_of_unaligned_rows_of_every_width(dsa, S, D, R, group):
+    append_unaligned_as(dsa, S, D, R, group, True)
+
+
+# ---- every key once -------------------------------------------------------------
+
+@gpu
+@pytest.mark.parametrize("S,H,D", [(3, 4, 64), (2, 8, 128), (2, 16, 64),
+                                   (2, 24, 64), (40, 2, 128)])
+def test_every_key_of_the_longest_cache_counts_once(dsa, S, H, D):
+    """64 keys of 2^21 share the softmax, each with a value of its own: the
+    first and the last ones that rows see, those at the borders of what a CTA
+    takes, of pages and of groups.  A key that is lost or counts twice changes
+    its column by all of it.  (The other scores are 0, these 40: 2^21 e^-40 of
+    the weight is nothing.)"""
+    page, group, block = 4096, 128, 128
+    T = 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(D + H)
+    kc, vc = (torch.zeros((T // page, page, 1, D), dtype=torch.uint8,
+                          device="cuda") for _ in "kv")
+    ones = torch.ones((T // page, page // group, 1), device="cuda")
+    table = torch.randperm(T // page, generator=g, device="cuda")
+    q = torch.ones((S, 1, H, D), dtype=BF, device="cuda")
+    pos = T - S - 3
+    # borders of the slices and of the parts that tiles are cut into
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    at = [0, 1, pos - 1, pos] + list(range(pos + 1, pos + S + 1))
+    steps = (pos + S - 1) // 32 + 1
+    share, more = steps // sms, steps % sms
+    at += [32 * (c * share + c * more // sms) + d for c in range(1, sms)
+           for d in (-1, 0)]
+    for parts in (255, 2 * sms // max(1, S * H // 128), 152, 304):
+        at += [64 * (T // 64 * c // parts) + d
+               for c in torch.randint(1, parts, (24,)).tolist() for d in (-1, 0)]
+    at += torch.randint(0, T, (64,)).tolist()
+    at += [page * i + d for i in (1, 2, T // page - 1) for d in (-1, 0)]
+    at += [group * i + d for i in (1, 77, T // group - 1) for d in (-1, 0)]
+    at = sorted(set(at))
+    one = int(torch.ones(1).to(E4M3).view(torch.uint8))
+    for i in range(0, len(at), 64):
+        js = torch.tensor(at[i:i + 64], device="cuda")
+        pg, off = table[js // page], js % page
+        kc[pg, off] = one
+        vc[pg, off, 0, torch.arange(len(js), device="cuda")] = one
+        o, lse, ws = dsa.dsa_block_attn_paged_q8_fwd(
+            q, kc.view(E4M3), vc.view(E4M3), ones, ones,
+            table.to(torch.int32)[None], None, block, 40.0 / D,
+            q_pos=torch.tensor([pos], dtype=torch.int32, device="cuda"),
+            local_blocks=T // block)
+        assert dsa.dsa_indexer_check(ws) == 0
+        kc[pg, off] = 0
+        vc[pg, off] = 0
+        for s in range(S):
+            seen = (js <= pos + s).double()
+            n = float(seen.sum())
+            want = torch.zeros(D, dtype=torch.float64, device="cuda")
+            want[:len(js)] = seen / max(n, 1)
+            err = (o[s, 0].double() - want).abs().max()
+            # (weights as fp16, the result as bf16)
+            assert n == 0 or float(err) <= (2.0 ** -11 + 2.0 ** -8) / n, (i, s)
+            if n:
+                z = 40 + torch.tensor(n).double().log()
+                assert bool((lse[s, 0].double() - z.cuda()).abs().max() <=
+                            2.0 ** -15 * 41)
+
+
+# ---- pages that the table names wrongly ----------------------------------------
+
+def ref_without(a, hidden):
+    """The attention with the keys hidden[b] left out, in 64 bits."""
+    k, v = (torch.stack(dense(c, s, a["good"], a["group"]), 1)
+            for c, s in ((a["kc"], a["ks"]), (a["vc"], a["vs"])))
+    S, B, H, D = a["q"].shape
+    T, _, Hk, _ = k.shape
+    r = {n: torch.zeros((S, B, H, D)).double() for n in ("o", "A_o")}
+    r["lse"] = torch.full((S, B, H), -float("inf")).double()
+    r["X"] = torch.zeros((S, B, H)).double()
+    for b in range(B):
+        for s in range(S):
+            for hk in range(Hk):
+                js = [j for j in row_keys(a["ids"], b, s, hk,
+                                          int(a["q_pos"][b]) + s, a["block"],
+                                          a["local"], T) if j not in hidden[b]]
+                if not js:
+                    continue
+                hs = slice(hk * (H // Hk), (hk + 1) * (H // Hk))
+                qq = a["q"][s, b, hs].double()
+                x = a["scale"] * qq @ k[js, b, hk].T
+                p = torch.softmax(x, 1)
+                r["o"][s, b, hs] = p @ v[js, b, hk]
+                r["A_o"][s, b, hs] = p @ v[js, b, hk].abs()
+                r["lse"][s, b, hs] = torch.logsumexp(x, 1)
+                r["X"][s, b, hs] = (a["scale"] * qq.abs()
+                                    @ k[js, b, hk].abs().T).amax(1)
+    r["w_top"] = float(a["vs"].max())
+    return r, T
+
+
+@gpu
+@pytest.mark.parametrize("case", [ATTN[1], ATTN[8], ATTN[9], ATTN[12],
+                                  ATTN[15], ATTN[21]])
+def test_rows_without_a_bad_page(dsa, case):
+    """All rows of all sequences, with another wrong page in each."""
+    a = attn_inputs(case, 24)
+    B, pages, page = a["q"].shape[1], a["table"].shape[1], a["kc"].shape[1]
+    a["good"] = a["table"].clone()
+    hidden = []
+    for b in range(B):
+        bad = b % pages
+        a["table"][b, bad] = (-1, a["kc"].shape[0], 2 ** 31 - 1)[b % 3]
+        hidden.append(range(bad * page, (bad + 1) * page))
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) in (0, 6)
+    r, T = ref_without(a, hidden)
+    check_attn(r, o, lse, T)
