@@ -73,6 +73,12 @@ constexpr int fwd_stages(int D, bool few) {
   return D == 64 ? (few ? 5 : 4) : (few ? 3 : 2);
 }
 constexpr float kSlack = 8.f;
+// The counts of written parts, a byte for each item that is split, in the 256
+// bytes that every entry point leaves to the status word: no other use of a
+// workspace touches them.  Zero between calls.
+constexpr int kDoneOffset = 64;
+static_assert(kDoneOffset + kSplitItems / 2 <= 256,
+              "a byte for each item that is split");
 
 template <int D, bool FEW>
 struct FwdSmem {
@@ -111,14 +117,77 @@ __device__ __noinline__ void redo_row(const BlockAttn &p, const FwdPlan &pl,
   if (lane == 0) pl.lse[at] = lse;
 }
 
+// Joins the parts of a split tile, o = sum_i w_i o_i / sum_i w_i with w_i =
+// 2^(l_i - max), in the order of the splits; the CTA that finished last.  A
+// thread takes four columns of a row and has kJoin parts in flight: the join
+// is a chain of loads from L2.  qs: 128 floats of shared memory a warp.
+constexpr int kJoin = 8;
 template <int D>
-__device__ __noinline__ void join_tile(const BlockAttn &p, const FwdPlan &pl,
-                                       size_t part0, int b, int s0, int nq,
-                                       int hk, float *qs, int tid) {
-  join_parts<D, kFwdThreads>(p, pl, part0, b, s0, nq, hk, qs, tid,
-                             [&](int b1, int s1, int h1, float *qs1, int l) {
-                               redo_row(p, pl, b1, s1, h1, qs1, l);
-                             });
+__device__ __noinline__ void join_parts(const BlockAttn &p, const FwdPlan &pl,
+                                        size_t part0, int b, int s0, int nq,
+                                        int hk, float *qs, int tid) {
+  constexpr int kLanes = D / 4;  // threads of a row: half a warp or a warp
+  const float neg_inf = -__int_as_float(0x7f800000);
+  const int rows = pl.qt * p.G, lane = tid & 31, c = tid % kLanes;
+  const int todo = nq * p.G;
+  // (whole warps stay in the loop: they vote)
+  for (int r0 = tid / 32 * (32 / kLanes); r0 < todo;
+       r0 += kFwdThreads / kLanes) {
+    const int r = r0 + lane / kLanes;
+    const bool mine = r < todo;
+    const size_t part = part0 + (mine ? r : 0);
+    float m = neg_inf, sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool odd = false;
+    for (int i0 = 0; i0 < pl.splits; i0 += kJoin) {
+      float l[kJoin];
+      float4 v[kJoin];
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const size_t at = part + (size_t)min(i0 + u, pl.splits - 1) * rows;
+        l[u] = __ldcg(pl.part_l + at);
+        v[u] = __ldcg(reinterpret_cast<const float4 *>(pl.part_o + at * D) + c);
+        if (i0 + u >= pl.splits) l[u] = neg_inf;
+      }
+      float mx = m;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        odd |= l[u] != l[u];
+        mx = fmaxf(mx, l[u]);
+      }
+      const float ref = mx > neg_inf ? mx : 0.f;
+      const float f = ex2(m - ref);
+      sum *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll
+      for (int u = 0; u < kJoin; ++u) {
+        const float w = ex2(l[u] - ref);
+        sum += w;
+        acc.x = fmaf(w, v[u].x, acc.x);
+        acc.y = fmaf(w, v[u].y, acc.y);
+        acc.z = fmaf(w, v[u].z, acc.z);
+        acc.w = fmaf(w, v[u].w, acc.w);
+      }
+      m = mx;
+    }
+    const int s = s0 + r / p.G, h = hk * p.G + r % p.G;
+    if (mine) {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const size_t at = ((size_t)s * p.B + b) * p.H + h;
+      reinterpret_cast<uint2 *>(pl.o + at * D)[c] =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv),
+                     pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (c == 0)
+        pl.lse[at] =
+            sum > 0.f ? (m + log2f(sum)) * 0.69314718055994531f : neg_inf;
+    }
+    // rows with a part that is not finite
+    unsigned again = __ballot_sync(0xffffffffu, mine && odd && c == 0);
+    for (; again; again &= again - 1) {
+      const int ra = r0 + (__ffs(again) - 1) / kLanes;
+      redo_row(p, pl, b, s0 + ra / p.G, hk * p.G + ra % p.G,
+               qs + tid / 32 * 128, lane);
+    }
+  }
 }
 
 template <int D, bool FEW>
@@ -533,7 +602,8 @@ done:
     const int item = blockIdx.x / pl.splits;
     if (tid == 0) {
       const int sh = 8 * (item & 3);
-      uint32_t *word = pl.done + (item >> 2);
+      uint32_t *word = reinterpret_cast<uint32_t *>(p.status) +
+                       (kDoneOffset + item) / 4;
       const uint32_t before = atomicAdd(word, 1u << sh) >> sh & 0xffu;
       const bool last = before + 1 == (uint32_t)pl.splits;
       if (last) atomicAnd(word, ~(0xffu << sh));  // for the next call
@@ -542,8 +612,8 @@ done:
     }
     __syncthreads();
     if (*sCount)
-      join_tile<D>(p, pl, (size_t)item * pl.splits * (pl.qt * p.G), b, s0, nq,
-                   hk, reinterpret_cast<float *>(smem + L::kOffK), tid);
+      join_parts<D>(p, pl, (size_t)item * pl.splits * (pl.qt * p.G), b, s0, nq,
+                    hk, reinterpret_cast<float *>(smem + L::kOffK), tid);
     __syncthreads();
   }
   if (warp == kMmaWarp) {

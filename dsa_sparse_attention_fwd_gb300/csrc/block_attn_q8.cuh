@@ -28,6 +28,17 @@ int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
 int run_attn_q8_tile(const BlockAttnQ8 &p, void *workspace, int num_sms,
                      cudaStream_t st);
 
+// Registers of a thread move between the warpgroups of a CTA: never more than
+// the launch gave to all of them.
+template <int R>
+__device__ __forceinline__ void regs_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_fewer() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 // One row by one warp in fp32 on the CUDA cores: a running maximum and sum
 // over its keys, 32 at a time, lane l holding one.  Rows of a tile whose fast
 // result is not finite are computed again by it where a key that only other rows

@@ -73,7 +73,6 @@ constexpr int kMaxCtas = 256 - kDoneOffset;
 struct StepPlan {
   bool all;     // no selection: all keys of the local blocks
   int rows;     // that share keys: S * G, of one query of a selection G
-  int tiles;    // items that these are cut into
   int items_b;  // items of a sequence
   int box;      // tokens of a TMA box: 16 or 32
   int stages;   // of a warp's ring
@@ -95,10 +94,10 @@ constexpr float kMostFactor = 1208925819614629174706176.f;  // 2^80
 
 // What the producer says of an item's part.
 struct Entry {
-  int n, g0;           // its steps, and the CTA's steps before it
-  int b, hk, tile, s;  // s: the query, of a selection
-  int c0, c1;          // CTAs that share it
-  int slot;            // where this one's part goes: 0, 1 or -1 (whole)
+  int n, g0;     // its steps, and the CTA's steps before it
+  int b, hk, s;  // s: the query, of a selection
+  int c0, c1;    // CTAs that share it
+  int slot;      // where this one's part goes: 0, 1 or -1 (whole)
 };
 
 // Of 16 keys of a step: exponents of the scales, the first key, and how many
@@ -135,15 +134,6 @@ struct StepSmem {
 template <int D>
 __device__ __forceinline__ int run_at(int q, int k) {
   return D == 128 ? 4 * q + (k ^ (q >> 1)) : 2 * q + (k ^ (q >> 2));
-}
-
-template <int R>
-__device__ __forceinline__ void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_fewer() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4],
@@ -326,15 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const unsigned w_i = w_b + idx * U;
       const unsigned x0 = w - w_i, x1 = min(U, x0 + (u1 - w));
       w += x1 - x0;
-      const int tile = idx % pl.tiles;
-      const int hk = idx / pl.tiles % p.Hk;
-      const int s = idx / pl.tiles / p.Hk;  // (0 without a selection)
+      const int hk = idx % p.Hk;
+      const int s = idx / p.Hk;  // (0 without a selection)
       // the item's keys: units of `box` keys
       Span sp;
       int units;
       if (pl.all) {
-        sp = span_of(p, b, tile * kRows / p.G,
-                     (min(pl.rows, (tile + 1) * kRows) - 1) / p.G);
+        sp = span_of(p, b, 0, p.S - 1);
         units = max(0, sp.hi - sp.lo + pl.box) / pl.box;
       } else {
         // (the list of the item before has been read by all)
@@ -380,10 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int gq = lane >> 2, tq = lane & 3;
       uint4 raw[2][D / 32];
       auto row_of = [&](int r, int &rs, int &rh) {
-        const int rr = tile * kRows + r;
-        rh = hk * p.G + rr % p.G;
-        rs = s + rr / p.G;
-        return rr < pl.rows;
+        rh = hk * p.G + r % p.G;
+        rs = s + r / p.G;
+        return r < pl.rows;
       };
       auto fetch = [&](int mt) {
 #pragma unroll
@@ -454,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Entry &e = entries[entry & 1];
           e.n = t1 - t0;
           e.g0 = g0;
-          e.b = b, e.hk = hk, e.tile = tile, e.s = s;
+          e.b = b, e.hk = hk, e.s = s;
           e.slot = x0 == 0 && x1 == U ? -1 : x0 == 0 ? 1 : 0;
           e.c0 = e.c1 = (int)cta;
           if (e.slot >= 0) {
@@ -577,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // last, o = sum_i w_i o_i / sum_i w_i with w_i = 2^(l_i - max).
     auto join_item = [&](const Entry &e) {
       const int parts = e.c1 - e.c0 + 1;
-      const int first = e.tile * kRows, live = min(pl.rows - first, kRows);
+      const int live = pl.rows;
       constexpr int kLanes = D / 4;  // threads of a row: a warp or half of one
       const int c = tid % kLanes;
       // (whole warps stay in the loop: they vote)
@@ -621,8 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           M = mx;
         }
-        const int rr = first + r;
-        const int s = e.s + rr / p.G, h = e.hk * p.G + rr % p.G;
+        const int s = e.s + r / p.G, h = e.hk * p.G + r % p.G;
         const long long to = ((long long)s * p.B + e.b) * p.H + h;
         if (mine) {
           const bool some = sum > 0.f || sum != sum;
@@ -694,8 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           qr[ks][0] = v.x, qr[ks][1] = v.y, qr[ks][2] = v.z, qr[ks][3] = v.w;
         }
       }
-      const int first = e.tile * kRows;
-      const int live = min(pl.rows - first, kRows);
+      const int live = pl.rows;
       const bool mixed = pl.all && p.S > 1;  // rows that see different keys
       // the tile's rows see the same keys but where a step holds keys after
       // the first row's position or before the last row's first block
@@ -968,8 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned votes = __ballot_sync(0xffffffffu, mine && odd);
         odd = (votes >> (lane & 16) & 0xffffu) != 0u;  // any of the row's
         const float lse2 = some ? M + log2f(sum) : neg_inf;
-        const int rr = first + r;
-        const int s = e.s + rr / p.G, h = e.hk * p.G + rr % p.G;
+        const int s = e.s + r / p.G, h = e.hk * p.G + r % p.G;
         const long long to = ((long long)s * p.B + e.b) * p.H + h;
         if (mine && e.slot < 0) {
 #pragma unroll
@@ -1040,8 +1024,7 @@ int run_attn_q8_step(const BlockAttnQ8 &p, void *workspace, int num_sms,
   pl.all = p.topk == 0;
   pl.rows = pl.all ? p.S * p.G : p.G;
   const int mt = pl.rows > 16 ? 2 : 1;
-  pl.tiles = (pl.rows + 16 * mt - 1) / (16 * mt);
-  const long long items = (long long)pl.tiles * p.Hk * (pl.all ? 1 : p.S);
+  const long long items = (long long)p.Hk * (pl.all ? 1 : p.S);
   if (items * p.B >= (1ll << 31)) return DSA_ERR_UNSUPPORTED;
   pl.items_b = (int)items;
   pl.box = p.blk >= 32 ? 32 : 16;

@@ -103,15 +103,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc,
       : "memory");
 }
 
-template <int R>
-__device__ __forceinline__ void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
-}
-template <int R>
-__device__ __forceinline__ void regs_fewer() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
-}
-
 // wait_bar_rest() without the call: kernels that move registers between warps
 // (setmaxnreg) may not make one.
 __device__ __forceinline__ bool wait_bar_rest_inl(uint32_t bar, uint32_t parity,
