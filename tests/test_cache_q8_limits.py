@@ -8,10 +8,12 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests.block_ref import row_keys
+from tests.block_ref import norm_rope_ref, row_keys
 from tests.cache_q8_ref import E4M3, dense
-from tests.test_cache_q8 import (ATTN, BF, attn_inputs, call, check_attn,
-                                 dsa, raw, reference, test_append as append_as,
+from tests.test_cache_q8 import (ATTN, BF, EPS, attn_inputs, call,
+                                 check_append, check_attn, dsa, inv,
+                                 make_cache, raw, reference, weights,
+                                 test_append as append_as,
                                  test_append_of_unaligned_rows as
                                  append_unaligned_as)  # noqa: F401
 
@@ -335,3 +337,144 @@ def test_rows_without_a_bad_page(dsa, case):
     assert dsa.dsa_indexer_check(ws) in (0, 6)
     r, T = ref_without(a, hidden)
     check_attn(r, o, lse, T)
+
+
+# ---- other calls that the documentation allows ---------------------------------
+
+@gpu
+@pytest.mark.parametrize("shift", [0, 1])          # of the rows: 16-byte pieces
+@pytest.mark.parametrize("S,D,R,group", [(1, 128, 128, 64), (3, 64, 32, 16),
+                                         (90, 96, 64, 32)])
+def test_append_far_away_with_a_rotation_scale(dsa, S, D, R, group, shift):
+    """Positions near 2^30, scaled rotations, a batch that is broadcast; read
+    back from there."""
+    B, H, Hk, page = 2, 3, 2, 128
+    far = 1 << 23                                  # pages of a sequence
+    g = torch.Generator().manual_seed(5)
+    n = (H + 2 * Hk) * D
+    buf = torch.randn((S, 1, n + 8), generator=g).to(BF)
+    cut = lambda t: t[..., shift:shift + n].unflatten(-1, (H + 2 * Hk, D)
+                                                      ).expand(-1, B, -1, -1)
+    q, k, v = cut(buf).split([H, Hk, Hk], 2)
+    gq, gk, gv = cut(buf.cuda()).split([H, Hk, Hk], 2)
+    kc, vc, ks, vs = make_cache(8, page, Hk, D, group, 8)
+    start = torch.tensor([far * page - S - 3, far * page - 200])
+    dev = [t.cuda() for t in (kc, vc, ks, vs)]
+    table = torch.full((B, far), 99, dtype=torch.int32, device="cuda")
+    table[:, -3:] = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32)
+    wq, wk = weights(D, 3)
+    m = 1.375
+    st = start.to(torch.int32).cuda()
+    out_q, ws = dsa.dsa_paged_append_q8(
+        gk, gv, *dev, table, st, inv_freq=inv(R).cuda(), wk=wk.cuda(), eps=EPS,
+        q=gq, wq=wq.cuda(), rot_scale=m)
+    assert dsa.dsa_indexer_check(ws) == 0
+    pos = start[None, :] + torch.arange(S)[:, None]
+    want, mag = norm_rope_ref(k, wk, pos, inv(R), 0, False, EPS, m)
+    base = (far - 3) * page                        # what the table's end names
+    small, at = table[:, -3:].cpu(), (start - base).tolist()
+    # 2^-19 of the pair for the norm and rotation, and the angle.  A turn's
+    # fraction f / (2 pi) < 0.16 comes out of two roundings in 64 bits, 2^-53.5 of
+    # it each at most: 2^30 positions later 2^-25 turns, 2^-22.3; the
+    # definition's pos f is off by half a step at 2^30, 2^-24.  Both: below 2^-21.
+    slack = 2.0 ** -19 * mag + 2.0 ** -21 * mag
+    check_append(want, slack, kc, ks, dev[0].cpu(), dev[2].cpu(), small, at,
+                 [S] * B, group)
+    check_append(v.double(), 0.0, vc, vs, dev[1].cpu(), dev[3].cpu(), small, at,
+                 [S] * B, group)
+    want, mag = norm_rope_ref(q, wq, pos, inv(R), 0, False, EPS, m)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -19 + 2.0 ** -21) * mag + 1e-38
+    assert bool(((out_q.double().cpu() - want).abs() <= tol).all())
+    _, got, ws = dsa.dsa_paged_read_q8(*dev, table, S, first=st)
+    assert dsa.dsa_indexer_check(ws) == 0
+    full = dense(dev[1].cpu(), dev[3].cpu(), small, group)
+    for b in range(B):
+        assert torch.equal(got[:, b].double().cpu(), full[b][at[b]:at[b] + S])
+
+
+@gpu
+@pytest.mark.parametrize("case", [ATTN[1], ATTN[5], ATTN[8], ATTN[12],
+                                  ATTN[15], ATTN[17]])
+def test_attention_of_a_selection_alone(dsa, case):
+    """No local blocks: a row's own block counts where it is named."""
+    a = attn_inputs(case, 25)
+    a["local"] = 0
+    own = int(a["q_pos"][0]) // a["block"]
+    a["ids"][0, ..., -1] = own
+    o, lse, ws = call(dsa, a)
+    assert dsa.dsa_indexer_check(ws) == 0
+    r, T = reference(a)
+    check_attn(r, o, lse, T)
+
+
+@gpu
+@pytest.mark.parametrize("topk", [0, 12])
+@pytest.mark.parametrize("S,B,H,Hk,D,block", [(2100, 1, 6, 2, 64, 32),
+                                              (1030, 2, 8, 1, 128, 128)])
+def test_attention_of_long_chunks(dsa, S, B, H, Hk, D, block, topk):
+    page, group, T = 256, 64, 4096
+    a = long_cache(S, B, H, Hk, D, T, page, group, 26)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    a["q_pos"] = torch.randint(0, T - S, (B,), generator=g, device="cuda"
+                               ).to(torch.int32)
+    ids = None
+    if topk:
+        ids = torch.randint(-1, T // block, (B, S, Hk, topk), generator=g,
+                            device="cuda").to(torch.int32)
+    o, lse = attend(dsa, a, ids, block)
+    order = a["table"][0].long()
+    k, v = ((a[c].double() * a[s].double().repeat_interleave(group, 1)[..., None]
+             )[order].flatten(0, 1) for c, s in (("kc", "ks"), ("vc", "vs")))
+    j = torch.arange(T, device="cuda")
+    top = float(a["vs"].max())
+    for b in range(B):
+        pos = int(a["q_pos"][b]) + torch.arange(S, device="cuda")
+        own = pos // block
+        for h in range(H):
+            hk = h // (H // Hk)
+            sees = j[None] <= pos[:, None]
+            if topk:
+                held = torch.zeros((S, T // block + 1), dtype=torch.bool,
+                                   device="cuda")
+                i = ids[b, :, hk].long()
+                held.scatter_(1, torch.where(i < 0, T // block, i), True)
+                held[torch.arange(S), own] = True
+                sees &= held[:, :-1].repeat_interleave(block, 1)
+            x = 0.11 * a["q"][:, b, h].double() @ k[:, hk].T
+            x = x.masked_fill(~sees, -float("inf"))
+            z = torch.logsumexp(x, 1)
+            p = torch.exp(x - z[:, None])
+            want, A = p @ v[:, hk], p @ v[:, hk].abs()
+            tol = ((2.0 ** -11 + 2.0 ** -12) * A + 2.0 ** -8 * want.abs()
+                   + T * 2.0 ** -22 * top + 1e-30)
+            assert bool(((o[:, b, h].double() - want).abs() <= tol).all())
+            X = (0.11 * a["q"][:, b, h].double().abs() @ k[:, hk].abs().T).amax(1)
+            assert bool(((lse[:, b, h].double() - z).abs()
+                         <= 2.0 ** -15 * (1 + X)).all())
+
+
+@gpu
+def test_more_than_2_to_the_31_steps(dsa):
+    """Single tokens whose selections could have 2^31 steps of 32 keys between
+    them: slices are counted in units of several.  Against the same blocks as
+    short lists; a row's order of summation is another."""
+    B, D, block, page, T = 33000, 64, 128, 4096, 1 << 21
+    a = long_cache(1, 1, 1, 1, D, T, page, 128, 27)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    a["q"] = torch.randn((1, B, 1, D), generator=g, device="cuda").to(BF)
+    a["table"] = a["table"].repeat(B, 1)
+    a["q_pos"] = torch.full((B,), T - 1, dtype=torch.int32, device="cuda")
+    few = torch.randint(0, T // block - 1, (B, 1, 3), generator=g,
+                        device="cuda").to(torch.int32)
+    o, lse = attend(dsa, a, few, block)
+    most = 16380
+    assert B * (most + 1) * block // 32 > 2 ** 31
+    ids = torch.full((B, 1, most), -1, dtype=torch.int32, device="cuda")
+    ids[..., 7], ids[..., 9000], ids[..., -1] = few.unbind(-1)
+    o2, lse2 = attend(dsa, a, ids, block)
+    A, _ = attend(dsa, a, few, block, vc=(raw(a["vc"]) & 0x7f).view(E4M3))
+    tol = (2 * (2.0 ** -11 + 2.0 ** -12) * A.double() * (1 + 2.0 ** -7)
+           + 2 * 2.0 ** -8 * o.double().abs()
+           + 2 * 4 * block * 2.0 ** -22 * float(a["vs"].max()))
+    assert bool(((o2.double() - o.double()).abs() <= tol).all())
+    assert bool(((lse2 - lse).abs() <= 2.0 ** -14 * (1 + lse.abs() + 40)).all())
