@@ -151,7 +151,9 @@ __device__ __forceinline__ void store_group(
 
 // Rows that cannot be read in 16-byte pieces (odd strides or pointers, halves
 // that do not fall on them): element loads, the partners of the rotation through
-// shared memory.  CTAs 0 .. kv - 1 take keys and values, the others queries as
+// shared memory.  A thread holds up to 16 rows as they came, which spills 252 to
+// 276 bytes of it: one token of 64 sequences takes 12.7 us instead of 4.9, the
+// ragged chunk above 234 instead of 27.  It is there for layouts that are rare.  CTAs 0 .. kv - 1 take keys and values, the others queries as
 // norm_rope_kernel() does.  Keys and values: an item is a group that a
 // sequence's rows can reach and one head (by a warp, where a group gets few new
 // rows) or several (by a CTA, the angles of the group's tokens in shared

@@ -20,7 +20,10 @@ namespace {
 //     252.  At 64 dimensions, 32 rows: few 20 / 51 / 155, many 18 / 65 / 217;
 //     64 rows: few 19 / 84 / 288, many 19 / 74 / 244.
 //   a selection, one token, 16 rows: few 21 / 21 / 21 / 42 for 1 / 4 / 16 / 64
-//     sequences, many 16 / 18 / 22 / 46 (two launches up to 16).
+//     sequences, many 16 / 18 / 22 / 46 (two launches up to 16).  Up to 4
+//     sequences the rule goes by the host's time, 21 us a call with one launch
+//     and 27 with two; in a captured graph, which has none, the kernel for many
+//     rows would be the faster one there.
 //   a selection, four tokens of 8 heads: few 18 / 20 / 37 / 116, many 24 / 19 /
 //     28 / 67, where tokens that share blocks read them once.
 bool few_rows(int S, int B, int Hk, int G, int D, int topk) {

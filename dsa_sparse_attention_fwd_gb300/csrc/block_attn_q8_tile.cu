@@ -30,9 +30,17 @@
 // so were tiles cut in parts where there are one to three a CTA slot (268 ->
 // 287): two CTAs at work fill an SM, the parts only add their ends.
 //
+// Two CTAs an SM need half of its shared memory each: at 128 dimensions there are
+// 7.4 KB for 4 bytes a block that the table can name and 2 a block of a list, at
+// 64 dimensions 56 KB.  Over all keys that is up to 1236 blocks (79104 tokens of
+// 64); with a table of more one CTA an SM remains, whatever the sequences'
+// lengths: 2 x 512 tokens over up to 15500 keys 256 us with a table of 15872
+// tokens, 259 with 65536, 408 with 131072, 417 with 1048576.
+//
 // Warps: 0 .. 3 softmax (thread = row = tensor-memory lane), 4 .. 7 convert the
 // values, 8 TMA producer, 9 MMA issuer and tensor-memory allocator; two CTAs an
-// SM.  Masks and rows that are not finite: as in block_attn.cu.
+// SM.  Masks and rows that are not finite, or whose scores are above 2^25: as in
+// block_attn.cu, the row path in block_attn_q8.cuh.
 #include "block_attn_host.cuh"
 #include "block_attn_q8.cuh"
 #include "block_attn_split.cuh"

@@ -11,8 +11,10 @@ tokens through a paged cache, a prompt in one chunk and then one token at a
 time, and returns the layer's outputs, which are those of the training forward
 up to roundings.  `serve(.., bits=8)` keeps the cache in 8 bits
 (dsa_paged_append_q8, dsa_paged_read_q8 for the block means,
-dsa_block_attn_paged_q8_fwd): half the memory and, for single tokens, half the
-time; its outputs are those of keys and values rounded to e4m3.
+dsa_block_attn_paged_q8_fwd): half the memory; attention of one token of 64
+sequences takes 43 us instead of 51 over 34 blocks of 64, 190 instead of 446 over
+all keys, of one sequence over its blocks 15 instead of 12.  Its outputs are those
+of keys and values rounded to e4m3.
 
     python examples/block_sparse_layer.py
 """
