@@ -46,9 +46,10 @@ __device__ __forceinline__ void regs_fewer() {
 // this warp's own copy; lane l returns o[l D / 32 + i] in acc[i].
 //
 // A chain of loads, those of 32 keys and their values on the way together: 3
-// to 5 ms for 131072 keys, 125 ms for 2^21 (a key at a time it was 19 and 450),
-// so that the four rows that a warp may have end well within the limit of the
-// waits for it, four seconds.
+// to 5 ms for 131072 keys, 125 ms for 2^21, so that the four rows that a warp may
+// have end well within the limit of the waits for it, four seconds.  (A value at a
+// time it took 28 to 57 ms for 131072 keys, which is 0.9 s for 2^21; 16 at a time
+// behind branches 9 to 19 ms.)
 template <int D>
 __device__ __forceinline__ void attn_row_q8(const BlockAttnQ8 &p, int b,
                                             int s, int hk, const float *qs,
